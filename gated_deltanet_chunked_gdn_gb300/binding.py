@@ -26,13 +26,19 @@ EXPORTED = ["gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_stag
             "gdn_get_device_status", "gdn_resolve_path", "gdn_status_string", "gdn_version", "gdn_recurrent_fwd",
             "gdn_causal_conv1d_fwd", "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_chunk_bwd_get_device_status", "gdn_chunk_fwd_host_workspace_size", "gdn_chunk_fwd_host",
-            "gdn_chunk_fwd_host_get_device_status"]
+            "gdn_chunk_fwd_host_get_device_status", "gdn_selective_scan_fwd_workspace_size",
+            "gdn_selective_scan_fwd", "gdn_selective_scan_get_device_status", "gdn_selective_scan_step"]
 
 
 class Problem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("N", ctypes.c_int), ("Hqk", ctypes.c_int),
                 ("Hv", ctypes.c_int), ("K", ctypes.c_int), ("V", ctypes.c_int), ("C", ctypes.c_int),
                 ("dt", ctypes.c_int), ("varlen", ctypes.c_int)]
+
+
+class ScanProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "N", "D", "S", "G", "dt", "varlen", "softplus")] + \
+        [(n, ctypes.c_int64) for n in ("ld_x", "ld_delta", "ld_z", "ld_b", "ld_c")]
 
 
 class StagedLayout(ctypes.Structure):
@@ -105,6 +111,15 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdn_chunk_fwd_host.restype = ctypes.c_int
         lib.gdn_chunk_fwd_host_get_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int)]
         lib.gdn_chunk_fwd_host_get_device_status.restype = ctypes.c_int
+        SP = ctypes.POINTER(ScanProblem)
+        lib.gdn_selective_scan_fwd_workspace_size.argtypes = [SP]
+        lib.gdn_selective_scan_fwd_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_selective_scan_fwd.argtypes = [SP] + [vp] * 13 + [ctypes.c_size_t, vp]
+        lib.gdn_selective_scan_fwd.restype = ctypes.c_int
+        lib.gdn_selective_scan_get_device_status.argtypes = [SP, vp, vp, ctypes.POINTER(ctypes.c_int)]
+        lib.gdn_selective_scan_get_device_status.restype = ctypes.c_int
+        lib.gdn_selective_scan_step.argtypes = [SP] + [vp] * 10 + [ctypes.c_int, vp, vp, vp]
+        lib.gdn_selective_scan_step.restype = ctypes.c_int
         lib.gdn_version.argtypes = []
         lib.gdn_version.restype = ctypes.c_char_p
         _lib = lib
@@ -444,3 +459,124 @@ def gdn_chunk_bwd_get_device_status(workspace, stream=None) -> int:
     if st:
         raise GDNError(st, "gdn_chunk_bwd_get_device_status")
     return int(v.value)
+
+
+def _address(t: Optional[torch.Tensor]) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+def _row_stride(name: str, t: torch.Tensor, row: int) -> int:
+    """Elements from one token's row of t [B, T, ...] to the next; the rows themselves contiguous, the
+    sequences of a batch one after the other at the same stride."""
+    if t.is_contiguous():
+        return row
+    B, T = t.shape[:2]
+    ld = t.stride(1) if T > 1 else t.stride(0) if B > 1 else row
+    inner, ok = 1, True
+    for i in range(t.dim() - 1, 1, -1):
+        ok = ok and (t.shape[i] == 1 or t.stride(i) == inner)
+        inner *= t.shape[i]
+    if not ok or ld < row or (B > 1 and T > 1 and t.stride(0) != T * ld):
+        raise ValueError(f"{name} must have contiguous rows, one token after the other at one stride")
+    return ld
+
+
+def _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32, others=()):
+    """Checks of a scan's tensors and its problem.  fp32: (name, tensor, shape) that must be contiguous float32;
+    others: (name, tensor) that must be like x and contiguous."""
+    dtype, shape = x.dtype, x.shape
+    if dtype not in DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    if len(shape) != 3 or B.dim() != 4:
+        raise ValueError("x must be [B, T, D] and B [B, T, G, S]")
+    nb, T, d = shape
+    G, S = B.shape[2], B.shape[3]
+    if delta.shape != shape or (z is not None and z.shape != shape):
+        raise ValueError("delta and z must have the shape of x")
+    if C.shape != B.shape or B.shape[:2] != shape[:2] or A.shape != (d, S):
+        raise ValueError("B and C must be [B, T, G, S] and A [D, S]")
+    for name, t in (("x", x), ("delta", delta), ("B", B), ("C", C), ("z", z), *others):
+        if t is not None and (t.dtype != dtype or not t.is_cuda):
+            raise ValueError(f"{name} must be a CUDA tensor with the dtype of x")
+    for name, t in others:
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with the shape of x")
+    for name, t, want in (("A", A, (d, S)), ("D", D, (d,)), ("dt_bias", dt_bias, (d,)), *fp32):
+        if t is not None and (t.dtype != torch.float32 or t.shape != want or not t.is_cuda or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {tuple(want)}")
+    N = nb
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor")
+        N = cu_seqlens.numel() - 1
+    gs = G * S
+    return ScanProblem(nb, T, N, d, S, G, DTYPES[dtype], int(cu_seqlens is not None), int(bool(softplus)),
+                       _row_stride("x", x, d), _row_stride("delta", delta, d),
+                       _row_stride("z", z, d) if z is not None else 0, _row_stride("B", B, gs),
+                       _row_stride("C", C, gs))
+
+
+def _scan_sequences(x, cu_seqlens) -> int:
+    return cu_seqlens.numel() - 1 if cu_seqlens is not None else x.shape[0]
+
+
+def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, h0=None,
+                           cu_seqlens=None, y=None, ht=None, output_final_state: bool = True, workspace=None,
+                           stream=None):
+    """Selective state space scan.  x, delta, z [B, T, D], B and C [B, T, G, S] (one dtype, bf16 or fp32; rows
+    may be slices of wider rows), A [D, S], D and dt_bias [D], h0 [N, D, S] fp32.  Returns (y, ht); ht is None
+    when ``output_final_state`` is False."""
+    lib = load()
+    state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
+    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (("h0", h0, state), ("ht", ht, state)),
+                      (("y", y),) if y is not None else ())
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if ht is None and output_final_state:
+        ht = torch.empty(state, dtype=torch.float32, device=x.device)
+    if workspace is None:
+        need = lib.gdn_selective_scan_fwd_workspace_size(p)
+        if need == 0:
+            raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_selective_scan_fwd_workspace_size")
+        workspace = _alloc_ws(need, x.device)
+    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    st = lib.gdn_selective_scan_fwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                    _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
+                                    y.data_ptr(), _address(ht), workspace.data_ptr(), workspace.numel(), s)
+    if st:
+        raise GDNError(st, "gdn_selective_scan_fwd")
+    return y, ht
+
+
+def gdn_selective_scan_fwd_workspace_size(p: ScanProblem) -> int:
+    return int(load().gdn_selective_scan_fwd_workspace_size(ctypes.byref(p)))
+
+
+def gdn_selective_scan_get_device_status(p: ScanProblem, workspace, stream=None) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream(workspace.device).cuda_stream
+    v = ctypes.c_int(0)
+    st = load().gdn_selective_scan_get_device_status(ctypes.byref(p), workspace.data_ptr(), s, ctypes.byref(v))
+    if st:
+        raise GDNError(st, "gdn_selective_scan_get_device_status")
+    return int(v.value)
+
+
+def gdn_selective_scan_step(x, delta, A, B, C, state, D=None, z=None, dt_bias=None, softplus: bool = True,
+                            state_indices=None, cu_seqlens=None, y=None, stream=None):
+    """The scan's tokens on a state pool (decode).  ``state`` [slots, D, S] fp32 is updated in place; returns y."""
+    lib = load()
+    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
+                      (("state", state, (state.shape[0], x.shape[-1], A.shape[-1])),),
+                      (("y", y),) if y is not None else ())
+    if state_indices is not None and (state_indices.dtype != torch.int32 or not state_indices.is_cuda
+                                      or not state_indices.is_contiguous() or state_indices.numel() != p.N):
+        raise ValueError("state_indices must be a contiguous int32 CUDA tensor, one slot a sequence")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    st = lib.gdn_selective_scan_step(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                     _address(D), _address(z), _address(dt_bias), state.data_ptr(),
+                                     _address(state_indices), state.shape[0], _address(cu_seqlens), y.data_ptr(), s)
+    if st:
+        raise GDNError(st, "gdn_selective_scan_step")
+    return y

@@ -33,6 +33,39 @@ bool problem_ok(const gdn_problem* pp, gdn_problem* out) {
   return true;
 }
 
+// Shape checks of a scan problem; normalises N for equal lengths and the flag.
+gdn_status scan_problem_ok(const gdn_scan_problem* pp, gdn_scan_problem* out) {
+  if (!pp) return GDN_ERR_INVALID_ARG;
+  gdn_scan_problem p = *pp;
+  if (p.dt != GDN_F32 && p.dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (p.D <= 0 || p.S <= 0 || p.G <= 0 || p.D % p.G != 0) return GDN_ERR_INVALID_ARG;
+  if (p.varlen) {
+    if (p.B != 1 || p.N <= 0 || p.T < 0) return GDN_ERR_INVALID_ARG;
+  } else {
+    if (p.B <= 0 || p.T <= 0) return GDN_ERR_INVALID_ARG;
+    p.N = p.B;
+  }
+  if ((int64_t)p.B * p.T >= ((int64_t)1 << 31) - 1024) return GDN_ERR_INVALID_ARG;
+  const int64_t gs = (int64_t)p.G * p.S;
+  const int64_t ld[5] = {p.ld_x, p.ld_delta, p.ld_z, p.ld_b, p.ld_c}, row[5] = {p.D, p.D, p.D, gs, gs};
+  for (int i = 0; i < 5; ++i)
+    if (ld[i] != 0 && ld[i] < row[i]) return GDN_ERR_INVALID_ARG;
+  if (p.S > kScanMaxS || p.D > kScanMaxD) return GDN_ERR_UNSUPPORTED;
+  p.softplus = p.softplus != 0;
+  *out = p;
+  return GDN_OK;
+}
+
+// Pointers of a scan's inputs.
+bool scan_inputs_ok(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* Bm,
+                    const void* Cm, const float* Dskip, const void* z, const float* dt_bias, const int32_t* cu) {
+  if (!A || (p.varlen ? !cu : cu != nullptr)) return false;
+  if ((int64_t)p.B * p.T > 0 && (!x || !delta || !Bm || !Cm)) return false;
+  const size_t es = p.dt == GDN_F32 ? 4 : 2;
+  if (!aligned(x, es) || !aligned(delta, es) || !aligned(z, es) || !aligned(Bm, es) || !aligned(Cm, es)) return false;
+  return aligned(A, p.S % 4 == 0 ? 16 : 4) && aligned(Dskip, 4) && aligned(dt_bias, 4) && aligned(cu, 4);
+}
+
 gdn_path resolve(const gdn_problem& p, gdn_path path) {
   if (path == GDN_PATH_AUTO) {
     if (!fused_supported(p) && !fused1_supported(p)) return GDN_PATH_STAGED;
@@ -277,6 +310,55 @@ gdn_status gdn_chunk_bwd_get_device_status(void* workspace, void* stream, int* d
   if (cudaMemset(word, 0, sizeof(int32_t)) != cudaSuccess) return GDN_ERR_CUDA;
   *dev_status = host;
   return GDN_OK;
+}
+
+size_t gdn_selective_scan_fwd_workspace_size(const gdn_scan_problem* pp) {
+  gdn_scan_problem p;
+  return scan_problem_ok(pp, &p) == GDN_OK ? scan_fwd_workspace_bytes(p) : 0;
+}
+
+gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A,
+                                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                  const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
+                                  float* ht, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_scan_problem p;
+  const gdn_status ok = scan_problem_ok(pp, &p);
+  if (ok != GDN_OK) return ok;
+  if (!scan_inputs_ok(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, cu_seqlens)) return GDN_ERR_INVALID_ARG;
+  const size_t sa = p.S % 4 == 0 ? 16 : 4, es = p.dt == GDN_F32 ? 4 : 2;
+  if (!aligned(h0, sa) || !aligned(ht, sa) || !aligned(y, es)) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)p.B * p.T > 0 && !y) return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < scan_fwd_workspace_bytes(p))
+    return GDN_ERR_INVALID_ARG;
+  return run_scan_fwd(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, h0, cu_seqlens, y, ht, workspace,
+                      static_cast<cudaStream_t>(stream));
+}
+
+gdn_status gdn_selective_scan_get_device_status(const gdn_scan_problem* pp, void* workspace, void* stream,
+                                                int* dev_status) {
+  gdn_scan_problem p;
+  if (!dev_status || scan_problem_ok(pp, &p) != GDN_OK) return GDN_ERR_INVALID_ARG;
+  if (p.varlen) return gdn_chunk_bwd_get_device_status(workspace, stream, dev_status);   // the word is at the front
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GDN_ERR_CUDA;
+  *dev_status = GDN_DEV_OK;
+  return GDN_OK;
+}
+
+gdn_status gdn_selective_scan_step(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A,
+                                   const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                   const float* dt_bias, float* state, const int32_t* state_indices,
+                                   int state_slots, const int32_t* cu_seqlens, void* y, void* stream) {
+  gdn_scan_problem p;
+  const gdn_status ok = scan_problem_ok(pp, &p);
+  if (ok != GDN_OK) return ok;
+  if (!scan_inputs_ok(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, cu_seqlens)) return GDN_ERR_INVALID_ARG;
+  const size_t sa = p.S % 4 == 0 ? 16 : 4, es = p.dt == GDN_F32 ? 4 : 2;
+  if (!state || state_slots <= 0 || !aligned(state, sa) || !aligned(state_indices, 4) || !aligned(y, es))
+    return GDN_ERR_INVALID_ARG;
+  if (!state_indices && state_slots < p.N) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)p.B * p.T > 0 && !y) return GDN_ERR_INVALID_ARG;
+  return run_scan_step(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, state, state_indices, state_slots, cu_seqlens, y,
+                       static_cast<cudaStream_t>(stream));
 }
 
 const char* gdn_status_string(gdn_status s) {

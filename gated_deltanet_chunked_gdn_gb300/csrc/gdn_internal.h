@@ -142,6 +142,17 @@ gdn_status run_bwdc(const gdn_problem& p, const void* q, const void* k, const vo
                     const float* dht, float* dq, float* dk, float* dv, float* dg, float* dbeta, float* dh0, void* ws,
                     cudaStream_t s);
 
+// Selective state space scan (gdn_scan.cu).
+constexpr int kScanMaxS = 64;      // states a channel
+constexpr int kScanMaxD = 131072;  // channels (at most 32768 CTAs a line of tokens, in the grid's second dimension)
+size_t scan_fwd_workspace_bytes(const gdn_scan_problem& p);
+gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
+                        const void* C, const float* Dp, const void* z, const float* dt_bias, const float* h0,
+                        const int32_t* cu, void* y, float* ht, void* ws, cudaStream_t s);
+gdn_status run_scan_step(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
+                         const void* C, const float* Dp, const void* z, const float* dt_bias, float* state,
+                         const int32_t* state_indices, int state_slots, const int32_t* cu, void* y, cudaStream_t s);
+
 // Chunk-parallel path (gdn_cp.cu): sequences cut into segments run in parallel.
 size_t cp_workspace_bytes(const gdn_problem& p);
 gdn_status run_cp(const gdn_problem& p, const void* q, const void* k, const void* v, const float* g,

@@ -1,0 +1,280 @@
+// gdn_scan.cuh -- pieces shared by the selective state space scan's forward
+// (gdn_scan.cu) and backward (gdn_scan_bwd.cu): arguments, the cut of the
+// sequences into segments, the layout of a warp's channels and states, and the
+// scalar functions.
+//
+// The scan, for a channel d of group g(d) and a state n:
+//     dt_t   = softplus(delta_t + dt_bias)     (or delta_t + dt_bias)
+//     h_t[n] = e^{dt_t A[n]} h_{t-1}[n] + dt_t x_t B_t[n]
+//     y_t    = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)
+//
+// Layout.  A warp owns kCpw(RL) = 2 * 32 / RL channels of one group and all of
+// their states: RL lanes stand side by side over the states of a channel pair
+// (four states each, S <= 4 RL), the 32 / RL lanes of one state quarter over the
+// channel pairs, so a lane keeps 2 x 4 states in registers.  Two channels a
+// lane: B_t and C_t are read from shared memory as one 16-byte vector each
+// (two cycles of the SM's shared-memory port a warp, measured) and serve eight
+// state updates, which cost eight cycles of the ex2 unit and of the FMA pipe;
+// with one channel a lane the reads would take as long as the arithmetic.  The
+// lanes of a state quarter are adjacent: a 16-byte read costs two cycles when
+// neighbouring lanes read one address and four when they do not.
+#pragma once
+
+#include <type_traits>
+
+#include "gdn_internal.h"
+#include "gdn_sm100.cuh"
+
+namespace gdn {
+namespace scan {
+
+constexpr int kTileMax = 16;   // tokens a tile
+
+struct Args {
+  const void *x, *dl, *z, *B, *C;
+  const float *A, *Dp, *bias, *h0;
+  const int32_t* cu;
+  int64_t ldx, ldd, ldz, ldb, ldc;   // elements from one token to the next
+  int64_t T;                         // tokens of a sequence, or of the packed batch
+  int N, D, S, G, Dg;                // Dg = D / G channels a group
+  int cbg;                           // warp channel blocks a group
+  int softplus;
+  bool vx, vd, vz, vb, vc;           // pairs of neighbours can be loaded at once
+  // segments
+  int nseg;                 // of a sequence (equal lengths)
+  int seglen;               // tokens, a multiple of kTileMax
+  const int32_t* seg0;      // packed: [N] first segment of every sequence, the number of segments (< 0:
+                            // malformed), the number of sequences with several, and which they are
+  float* hseg;              // [segments][D][S]: local end states, then the states the segments start from
+  float* dtsum;             // [segments][D]: sum of dt over the segment
+  // forward outputs
+  void* y;
+  float* ht;
+  bool vy;
+};
+
+struct Unit {
+  int n;
+  int64_t tok0;
+  int len;
+  bool first, last;   // of its sequence
+};
+
+// Segment u of the batch; false past the last one (or for malformed cu_seqlens).
+__device__ __forceinline__ bool unit_of(const Args& a, int64_t u, Unit& r) {
+  int64_t s, e, j;
+  if (a.cu) {
+    if (u >= a.seg0[a.N]) return false;
+    int lo = 0, hi = a.N - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seg0[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    r.n = lo;
+    j = u - a.seg0[lo];
+    s = a.cu[lo];
+    e = a.cu[lo + 1];
+  } else {
+    r.n = (int)(u / a.nseg);
+    j = u % a.nseg;
+    s = (int64_t)r.n * a.T;
+    e = s + a.T;
+  }
+  r.tok0 = s + j * a.seglen;
+  const int64_t left = e - r.tok0;
+  r.len = (int)(left < a.seglen ? left : a.seglen);
+  r.first = j == 0;
+  r.last = left <= a.seglen;
+  return true;
+}
+
+// Two neighbouring elements as loaded (converted when they are used, so that
+// the loads of the next tile stay in flight).
+template <typename T> struct Raw2;
+template <> struct Raw2<__nv_bfloat16> {
+  uint32_t v;
+  __device__ __forceinline__ void zero() { v = 0u; }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec, bool ok0, bool ok1) {
+    if (vec && ok1) {
+      v = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      const uint32_t lo = ok0 ? __ldg(reinterpret_cast<const uint16_t*>(p)) : 0u;
+      const uint32_t hi = ok1 ? __ldg(reinterpret_cast<const uint16_t*>(p) + 1) : 0u;
+      v = lo | (hi << 16);
+    }
+  }
+  __device__ __forceinline__ float2 f() const {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+};
+template <> struct Raw2<float> {
+  float2 v;
+  __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p, bool vec, bool ok0, bool ok1) {
+    if (vec && ok1) {
+      v = __ldg(reinterpret_cast<const float2*>(p));
+    } else {
+      v.x = ok0 ? __ldg(p) : 0.f;
+      v.y = ok1 ? __ldg(p + 1) : 0.f;
+    }
+  }
+  __device__ __forceinline__ float2 f() const { return v; }
+};
+
+template <typename T>
+__device__ __forceinline__ void store2(T* p, float2 v, bool vec, bool ok0, bool ok1) {
+  if constexpr (std::is_same<T, float>::value) {
+    if (vec && ok1) {
+      *reinterpret_cast<float2*>(p) = v;
+      return;
+    }
+  } else {
+    if (vec && ok1) {
+      *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+      return;
+    }
+  }
+  if (ok0) p[0] = from_f<T>(v.x);
+  if (ok1) p[1] = from_f<T>(v.y);
+}
+
+// Up to four consecutive floats, entries at or past `n` read as 0 / not written.
+__device__ __forceinline__ void load4(const float* p, int n, bool vec, float (&v)[4]) {
+  if (vec && n >= 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+__device__ __forceinline__ void store4(float* p, int n, bool vec, const float (&v)[4]) {
+  if (vec && n >= 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+__device__ __forceinline__ float rcp_approx(float y) {   // about 1 ulp; 1 / inf = 0
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+
+// softplus(v) = max(v, 0) + log(1 + e^{-|v|}).  log(1 + e) / e on [0, 1] is a
+// polynomial of degree 8, fitted here by Remez's exchange for least relative
+// error (3e-8; 1.7e-7 with the rounding of its fp32 steps), so that tiny steps
+// (v << 0) keep their relative accuracy.  e_out = e^{-|v|}.
+__device__ __forceinline__ float softplus(float v, float& e_out) {
+  const float e = sm100::ex2_fast(-sm100::kLog2e * fabsf(v));
+  float p = 0.00523269409f;
+  p = fmaf(p, e, -0.0295052379f);
+  p = fmaf(p, e, 0.0782259554f);
+  p = fmaf(p, e, -0.136632457f);
+  p = fmaf(p, e, 0.191060066f);
+  p = fmaf(p, e, -0.24842982f);
+  p = fmaf(p, e, 0.333190978f);
+  p = fmaf(p, e, -0.499994934f);
+  p = fmaf(p, e, 0.99999994f);
+  e_out = e;
+  return fmaxf(v, 0.f) + p * e;
+}
+
+// sigmoid(v)
+__device__ __forceinline__ float sigmoid(float v) {
+  return rcp_approx(1.f + sm100::ex2_fast(-sm100::kLog2e * v));
+}
+
+__host__ __device__ constexpr int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v / 2); }
+
+// A warp's lanes over channel pairs and states, and which tokens of a group of
+// four a lane finishes (converts on the way in, writes on the way out).
+template <int RL>
+struct Lanes {
+  static constexpr int CL = 32 / RL;              // lanes over channel pairs
+  static constexpr int LR = log2i(RL);
+  static constexpr int SP = 4 * RL;               // states with padding
+  static constexpr int CPW = 2 * CL;              // channels a warp
+  static constexpr int TPL = RL >= 4 ? 1 : 4 / RL;    // tokens of a group a lane finishes
+  static constexpr int TT = RL >= 4 ? 16 : 4 * RL;    // tokens a tile: four a lane
+  static constexpr int NG = TT / 4;
+  static constexpr int NPB = (TT * SP + 63) / 64;     // pairs of B (or C) a lane stages
+  int lane, chl, sl, own;
+  bool dup;   // another lane finishes the same tokens
+  __device__ __forceinline__ Lanes() {
+    lane = threadIdx.x & 31;
+    chl = lane & (CL - 1);
+    sl = lane / CL;
+    own = RL >= 4 ? sl >> (LR >= 2 ? LR - 2 : 0) : sl;
+    dup = RL > 4 && (sl & (RL / 4 - 1)) != 0;
+  }
+  // token (within a tile) of this lane's slot k
+  __device__ __forceinline__ int token(int k) const { return (k / TPL) * 4 + own * TPL + k % TPL; }
+};
+
+// Sums over the state lanes of four tokens' values v[tok * NV + i]: lane `own`
+// ends with its tokens' sums in v[0 .. TPL * NV).
+template <int RL, int NV>
+__device__ __forceinline__ void reduce_states(float (&v)[4 * NV], int lane) {
+  if constexpr (RL >= 2) {
+    const bool up = lane & 16;
+#pragma unroll
+    for (int i = 0; i < 2 * NV; ++i) {
+      const float send = up ? v[i] : v[i + 2 * NV];
+      const float keep = up ? v[i + 2 * NV] : v[i];
+      v[i] = keep + __shfl_xor_sync(~0u, send, 16);
+    }
+  }
+  if constexpr (RL >= 4) {
+    const bool up = lane & 8;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float send = up ? v[i] : v[i + NV];
+      const float keep = up ? v[i + NV] : v[i];
+      v[i] = keep + __shfl_xor_sync(~0u, send, 8);
+    }
+  }
+#pragma unroll
+  for (int m = 4; m >= 32 / RL && RL >= 8; m >>= 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(~0u, v[i], m);
+  }
+}
+
+// Host side ---------------------------------------------------------------
+
+inline int lanes_for(int S) { return S <= 4 ? 1 : S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16; }
+
+// How a problem's sequences are cut: segments of seglen tokens, at most
+// max_units of them in all.
+struct Plan {
+  int RL, cpw, cbg;
+  int nseg, seglen;
+  int64_t max_units;
+  bool cut;   // some sequence may have several segments
+};
+
+// Packed sequences longer than a segment: fewer than this.
+inline int64_t max_cut(int64_t N, int64_t T, int64_t seglen) {
+  const int64_t m = T / seglen;
+  return m < 1 ? 1 : m < N ? m : N;
+}
+inline size_t seg0_bytes(int64_t N, int64_t T, int64_t seglen) {
+  return sizeof(int32_t) * (size_t)(N + 2 + max_cut(N, T, seglen));
+}
+
+Plan make_plan(const gdn_scan_problem& p);
+Args base_args(const gdn_scan_problem& p, const Plan& pl, const void* x, const void* delta, const float* A,
+               const void* B, const void* C, const float* Dp, const void* z, const float* dt_bias, const float* h0,
+               const int32_t* cu);
+// Packed batches: validates cu_seqlens into *status and writes seg0.
+cudaError_t launch_prepare_segments(const int32_t* cu, int N, int64_t T, int seglen, int32_t* seg0, int32_t* status,
+                                    cudaStream_t s);
+// Start states of every segment into hseg (two launches); dtsum is kept.
+cudaError_t launch_segment_states(const Args& a, const Plan& pl, gdn_dtype dt, cudaStream_t s);
+
+}  // namespace scan
+}  // namespace gdn

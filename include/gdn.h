@@ -400,6 +400,84 @@ gdn_status gdn_causal_conv1d_fwd(const void* x, const float* weight, const float
                                  void* stream);
 
 /*
+ * Selective state space scan (a diagonal linear recurrence whose steps, input
+ * and output maps depend on the token): the mixer that hybrid stacks put next
+ * to the gated delta rule, behind the same short causal convolution.  For
+ * channel d of group g = d / (D / G) and state n < S,
+ *     dt_t   = softplus(delta_t[d] + dt_bias[d])      (without softplus: the sum itself)
+ *     h_t[n] = e^{dt_t A[d][n]} h_{t-1}[n] + dt_t x_t[d] B_t[g][n]
+ *     y_t[d] = (sum_n C_t[g][n] h_t[n] + Dskip[d] x_t[d]) * silu(z_t[d])
+ * States, steps and sums are fp32; y is rounded once to p->dt.
+ *
+ * Problem description.
+ *   B, T, N, varlen : as for gdn_problem (N = B for equal lengths)
+ *   D, S, G  : channels (at most 131072), states a channel (at most 64) and
+ *              groups of channels that share B and C; D % G == 0
+ *   dt       : dtype of x, delta, z, B, C, y and of their gradients
+ *   softplus : 0 or 1, as above
+ *   ld_*     : elements from one token's row to the next (0: rows are
+ *              contiguous), at least a row; a sequence's rows and the
+ *              sequences of a batch follow one another at this stride, so a
+ *              column slice of a wider matrix can be passed as it is.  ld_x,
+ *              ld_delta, ld_z: rows of D elements; ld_b, ld_c: rows of G * S.
+ * y, gradients and everything else are contiguous.  Pointers need the
+ * alignment of their elements only, except A, h0, ht, state, dA, dht and dh0:
+ * 16 bytes when S % 4 == 0.
+ */
+typedef struct {
+  int B, T, N, D, S, G;
+  gdn_dtype dt;
+  int varlen;
+  int softplus;
+  int64_t ld_x, ld_delta, ld_z, ld_b, ld_c;
+} gdn_scan_problem;
+
+/*
+ * The scan over prompts or training sequences.
+ *   x, delta    : [B, T, D];  A : [D, S] fp32;  Bm, Cm : [B, T, G, S]
+ *   Dskip       : [D] fp32 or NULL (= 0);  z : [B, T, D] or NULL (no gate)
+ *   dt_bias     : [D] fp32 or NULL (= 0)
+ *   h0          : [N, D, S] fp32 or NULL (= 0);  cu_seqlens as for gdn_chunk_fwd
+ *   y           : out [B, T, D];  ht : out [N, D, S] fp32 or NULL
+ *   workspace   : gdn_selective_scan_fwd_workspace_size(p) bytes (0: invalid
+ *                 problem), 256-byte aligned.  Sequences are cut into segments
+ *                 that run side by side when the channels of all sequences do
+ *                 not fill the device: query the size with the device current
+ *                 that will run the call.
+ * Malformed cu_seqlens set the status word (GDN_DEV_BAD_CU_SEQLENS, read with
+ * gdn_selective_scan_get_device_status) and leave y and ht unwritten.
+ * Asynchronous on `stream`; results do not depend on the run.
+ */
+size_t gdn_selective_scan_fwd_workspace_size(const gdn_scan_problem* p);
+gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* p, const void* x, const void* delta, const float* A,
+                                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                  const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
+                                  float* ht, void* workspace, size_t workspace_bytes, void* stream);
+/* Status word that the last scan call on `workspace` left (forward or
+ * backward; synchronises `stream`, then clears the word).  Equal-length calls
+ * write none: GDN_DEV_OK. */
+gdn_status gdn_selective_scan_get_device_status(const gdn_scan_problem* p, void* workspace, void* stream,
+                                                int* dev_status);
+
+/*
+ * The scan on a pool of states, for single tokens (decode); several tokens of
+ * a sequence run one after the other.
+ *   state       : [state_slots, D, S] fp32 pool, read and updated in place
+ *   state_indices : [N] int32 slot of each sequence, or NULL (slot n; then
+ *                 state_slots >= N).  A sequence whose slot is outside
+ *                 [0, state_slots) gets zero outputs and no state update;
+ *                 distinct sequences must use distinct slots.
+ *   cu_seqlens  : as for gdn_chunk_fwd; a sequence whose offsets fall outside
+ *                 [0, T] or decrease is skipped
+ *   other arguments as for gdn_selective_scan_fwd
+ * One launch, no workspace; asynchronous on `stream`.
+ */
+gdn_status gdn_selective_scan_step(const gdn_scan_problem* p, const void* x, const void* delta, const float* A,
+                                   const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                   const float* dt_bias, float* state, const int32_t* state_indices,
+                                   int state_slots, const int32_t* cu_seqlens, void* y, void* stream);
+
+/*
  * Test hook (no counterpart on the pages): y[i] = e^{x[i]} computed the way
  * the fused kernel computes its decay factors (2^{x log2 e} on the MUFU ex2
  * unit), so tests can bound its error against CUDA's expf.  x, y device

@@ -27,7 +27,9 @@ EXPORTED = ["gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_stag
             "gdn_causal_conv1d_fwd", "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_chunk_bwd_get_device_status", "gdn_chunk_fwd_host_workspace_size", "gdn_chunk_fwd_host",
             "gdn_chunk_fwd_host_get_device_status", "gdn_selective_scan_fwd_workspace_size",
-            "gdn_selective_scan_fwd", "gdn_selective_scan_get_device_status", "gdn_selective_scan_step"]
+            "gdn_selective_scan_fwd", "gdn_selective_scan_get_device_status", "gdn_selective_scan_step",
+            "gdn_selective_scan_bwd_workspace_size", "gdn_selective_scan_bwd",
+            "gdn_causal_conv1d_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_q4_matvec"]
 
 
 class Problem(ctypes.Structure):
@@ -120,6 +122,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdn_selective_scan_get_device_status.restype = ctypes.c_int
         lib.gdn_selective_scan_step.argtypes = [SP] + [vp] * 10 + [ctypes.c_int, vp, vp, vp]
         lib.gdn_selective_scan_step.restype = ctypes.c_int
+        lib.gdn_selective_scan_bwd_workspace_size.argtypes = [SP]
+        lib.gdn_selective_scan_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_selective_scan_bwd.argtypes = [SP] + [vp] * 22 + [ctypes.c_size_t, vp]
+        lib.gdn_selective_scan_bwd.restype = ctypes.c_int
+        lib.gdn_causal_conv1d_bwd_workspace_size.argtypes = [ctypes.c_int] * 4
+        lib.gdn_causal_conv1d_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_causal_conv1d_bwd.argtypes = [vp, fp, fp, ctypes.c_int, vp, i32p] + [ctypes.c_int] * 6 + \
+            [vp] * 7 + [ctypes.c_size_t, vp]
+        lib.gdn_causal_conv1d_bwd.restype = ctypes.c_int
+        lib.gdn_q4_matvec.argtypes = [vp, ctypes.c_int64, vp, vp, ctypes.c_int, vp, fp] + [ctypes.c_int] * 5 + [vp, vp]
+        lib.gdn_q4_matvec.restype = ctypes.c_int
         lib.gdn_version.argtypes = []
         lib.gdn_version.restype = ctypes.c_char_p
         _lib = lib
@@ -579,4 +592,125 @@ def gdn_selective_scan_step(x, delta, A, B, C, state, D=None, z=None, dt_bias=No
                                      _address(state_indices), state.shape[0], _address(cu_seqlens), y.data_ptr(), s)
     if st:
         raise GDNError(st, "gdn_selective_scan_step")
+    return y
+
+
+def gdn_selective_scan_bwd_workspace_size(p: ScanProblem) -> int:
+    return int(load().gdn_selective_scan_bwd_workspace_size(ctypes.byref(p)))
+
+
+def gdn_selective_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None, softplus: bool = True, h0=None,
+                           dht=None, cu_seqlens=None, want_dh0: Optional[bool] = None, workspace=None,
+                           stream=None) -> dict:
+    """Backward of gdn_selective_scan_fwd for upstream gradients ``dout`` (dL/dy, dtype of x) and ``dht`` (dL/dht,
+    fp32 or None).  Returns dx, ddelta, dB, dC, dz (dtype of x), dA, dD, ddt_bias, dh0 (fp32) and the workspace
+    under "workspace"; dD, dz and ddt_bias are None where the input is, dh0 unless ``want_dh0`` (by default: h0 is
+    given)."""
+    lib = load()
+    state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
+    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
+                      (("h0", h0, state), ("dht", dht, state)), (("dout", dout),))
+    if workspace is None:
+        need = lib.gdn_selective_scan_bwd_workspace_size(p)
+        if need == 0:
+            raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_selective_scan_bwd_workspace_size")
+        workspace = _alloc_ws(need, x.device)
+    like = dict(dtype=x.dtype, device=x.device)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    if want_dh0 is None:
+        want_dh0 = h0 is not None
+    out = {"dx": torch.empty(x.shape, **like), "ddelta": torch.empty(x.shape, **like),
+           "dA": torch.empty(A.shape, **f32), "dB": torch.empty(B.shape, **like), "dC": torch.empty(C.shape, **like),
+           "dD": torch.empty(D.shape, **f32) if D is not None else None,
+           "dz": torch.empty(x.shape, **like) if z is not None else None,
+           "ddt_bias": torch.empty(dt_bias.shape, **f32) if dt_bias is not None else None,
+           "dh0": torch.empty(state, **f32) if want_dh0 else None}
+    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    st = lib.gdn_selective_scan_bwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                    _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
+                                    dout.data_ptr(), _address(dht), *(_address(t) for t in out.values()),
+                                    workspace.data_ptr(), workspace.numel(), s)
+    if st:
+        raise GDNError(st, "gdn_selective_scan_bwd")
+    out["workspace"] = workspace
+    return out
+
+
+def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial_state=None, dfinal_state=None,
+                          cu_seqlens=None, want_dinitial_state: Optional[bool] = None, workspace=None,
+                          stream=None) -> dict:
+    """Backward of gdn_causal_conv1d_fwd for ``dout`` (dL/dy) and ``dfinal_state`` (dL/d new state, [N, W-1, D], or
+    None).  x, dout [B, T, D] and initial_state [N, W-1, D] share a dtype; weight [D, W], bias [D] fp32.  Returns
+    dx, dweight, dbias, dinitial_state and the workspace under "workspace"; dbias is None without bias,
+    dinitial_state unless ``want_dinitial_state`` (by default: initial_state is given)."""
+    lib = load()
+    if x.dtype not in DTYPES or x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
+        raise ValueError("x must be float32 or bfloat16 [B, T, D] and weight [D, W]")
+    B, T, D = x.shape
+    W = weight.shape[1]
+    if cu_seqlens is not None and cu_seqlens.dtype != torch.int32:
+        raise ValueError("cu_seqlens must be int32")
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
+    state = (N, W - 1, D)
+    for name, t, dtype, shape in (("x", x, x.dtype, x.shape), ("dout", dout, x.dtype, x.shape),
+                                  ("weight", weight, torch.float32, (D, W)), ("bias", bias, torch.float32, (D,)),
+                                  ("initial_state", initial_state, x.dtype, state),
+                                  ("dfinal_state", dfinal_state, x.dtype, state),
+                                  ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))):
+        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.shape != shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    if workspace is None:
+        need = lib.gdn_causal_conv1d_bwd_workspace_size(B, T, D, W)
+        if need == 0:
+            raise GDNError(GDN_ERR_INVALID_ARG, "gdn_causal_conv1d_bwd_workspace_size")
+        workspace = _alloc_ws(need, x.device)
+    if want_dinitial_state is None:
+        want_dinitial_state = initial_state is not None
+    f32 = dict(dtype=torch.float32, device=x.device)
+    out = {"dx": torch.empty_like(x), "dweight": torch.empty((D, W), **f32),
+           "dbias": torch.empty((D,), **f32) if bias is not None else None,
+           "dinitial_state": torch.empty(state, dtype=x.dtype, device=x.device) if want_dinitial_state else None}
+    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    st = lib.gdn_causal_conv1d_bwd(x.data_ptr(), weight.data_ptr(), _address(bias), W, _address(initial_state),
+                                   _address(cu_seqlens), N, B, T, D, DTYPES[x.dtype], ACTIVATIONS[activation],
+                                   dout.data_ptr(), _address(dfinal_state), *(_address(t) for t in out.values()),
+                                   workspace.data_ptr(), workspace.numel(), s)
+    if st:
+        raise GDNError(st, "gdn_causal_conv1d_bwd")
+    out["workspace"] = workspace
+    return out
+
+
+def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None):
+    """y = x W^T + bias for 4-bit weights W [N, K] = (code - zero) * scale.  x [..., K] (bf16 or fp32; two
+    dimensions may have any row stride), qweight [N, K / 2] uint8 (code 2j in byte j's low half), scales
+    [N, K / group] (bf16 or fp32), zeros [N, K / group] uint8 or None (8), bias [N] fp32.  Returns y [..., N]."""
+    lib = load()
+    N, half = qweight.shape
+    K, groups = 2 * half, scales.shape[1]
+    if x.dtype not in DTYPES or scales.dtype not in DTYPES:
+        raise ValueError("x and scales must be float32 or bfloat16")
+    if x.shape[-1] != K or not x.is_cuda or groups == 0 or K % groups != 0:
+        raise ValueError("x must be a CUDA tensor of shape [..., K] and scales [N, K / group]")
+    for name, t, dtype, shape in (("qweight", qweight, torch.uint8, (N, half)),
+                                  ("scales", scales, scales.dtype, (N, groups)),
+                                  ("zeros", zeros, torch.uint8, (N, groups)), ("bias", bias, torch.float32, (N,))):
+        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.shape != shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}")
+    if x.is_contiguous():
+        M, ld = x.numel() // K, K
+    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K:
+        M, ld = x.shape[0], x.stride(0)
+    else:
+        raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
+    want = (*x.shape[:-1], N)
+    if y is None:
+        y = torch.empty(want, dtype=x.dtype, device=x.device)
+    elif y.shape != want or y.dtype != x.dtype or not y.is_cuda or not y.is_contiguous():
+        raise ValueError("y must be a contiguous CUDA tensor [..., N] with the dtype of x")
+    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    st = lib.gdn_q4_matvec(x.data_ptr(), ld, qweight.data_ptr(), scales.data_ptr(), DTYPES[scales.dtype],
+                           _address(zeros), _address(bias), M, N, K, K // groups, DTYPES[x.dtype], y.data_ptr(), s)
+    if st:
+        raise GDNError(st, "gdn_q4_matvec")
     return y

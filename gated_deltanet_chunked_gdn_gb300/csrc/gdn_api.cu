@@ -361,6 +361,83 @@ gdn_status gdn_selective_scan_step(const gdn_scan_problem* pp, const void* x, co
                        static_cast<cudaStream_t>(stream));
 }
 
+size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_problem* pp) {
+  gdn_scan_problem p;
+  return scan_problem_ok(pp, &p) == GDN_OK && p.G <= kScanBwdMaxG ? scan_bwd_workspace_bytes(p) : 0;
+}
+
+gdn_status gdn_selective_scan_bwd(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A,
+                                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                  const float* dt_bias, const float* h0, const int32_t* cu_seqlens,
+                                  const void* dout, const float* dht, void* dx, void* ddelta, float* dA, void* dB,
+                                  void* dC, float* dD, void* dz, float* ddt_bias, float* dh0, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  gdn_scan_problem p;
+  const gdn_status ok = scan_problem_ok(pp, &p);
+  if (ok != GDN_OK) return ok;
+  if (p.G > kScanBwdMaxG) return GDN_ERR_UNSUPPORTED;
+  if (!scan_inputs_ok(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, cu_seqlens)) return GDN_ERR_INVALID_ARG;
+  const size_t sa = p.S % 4 == 0 ? 16 : 4, es = p.dt == GDN_F32 ? 4 : 2;
+  const void* states[] = {h0, dht, dA, dh0};
+  for (const void* q : states)
+    if (!aligned(q, sa)) return GDN_ERR_INVALID_ARG;
+  const void* rows[] = {dout, dx, ddelta, dB, dC, dz};
+  for (const void* q : rows)
+    if (!aligned(q, es)) return GDN_ERR_INVALID_ARG;
+  if (!dA || !aligned(dD, 4) || !aligned(ddt_bias, 4) || !z != !dz) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)p.B * p.T > 0 && (!dout || !dx || !ddelta || !dB || !dC)) return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < scan_bwd_workspace_bytes(p))
+    return GDN_ERR_INVALID_ARG;
+  return run_scan_bwd(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, h0, cu_seqlens, dout, dht, dx, ddelta, dA, dB, dC,
+                      dD, dz, ddt_bias, dh0, workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_causal_conv1d_bwd_workspace_size(int B, int T, int D, int W) {
+  if (W < 1 || W > 4 || D <= 0 || D % 8 != 0 || B < 0 || T < 0) return 0;
+  return conv1d_bwd_workspace_bytes((int64_t)B * T, D, W);
+}
+
+gdn_status gdn_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, int W,
+                                 const void* initial_state, const int32_t* cu_seqlens, int N, int B, int T, int D,
+                                 gdn_dtype dt, gdn_activation act, const void* dout, const void* dfinal_state,
+                                 void* dx, float* dweight, float* dbias, void* dinitial_state, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (W < 1 || W > 4 || D <= 0 || D % 8 != 0 || B < 0 || T < 0 || N < 0) return GDN_ERR_INVALID_ARG;
+  if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (act != GDN_ACT_NONE && act != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
+  if (cu_seqlens ? B != 1 : N != B) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)B * T > 0 && (!x || !dout || !dx)) return GDN_ERR_INVALID_ARG;
+  if (!weight || !dweight) return GDN_ERR_INVALID_ARG;
+  const void* a16[] = {x, dout, dx, initial_state, dfinal_state, dinitial_state};
+  for (const void* p : a16)
+    if (!aligned(p, 16)) return GDN_ERR_INVALID_ARG;
+  const void* a4[] = {weight, bias, cu_seqlens, dweight, dbias};
+  for (const void* p : a4)
+    if (!aligned(p, 4)) return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) ||
+      workspace_bytes < conv1d_bwd_workspace_bytes((int64_t)B * T, D, W))
+    return GDN_ERR_INVALID_ARG;
+  return run_causal_conv1d_bwd(x, weight, bias, W, initial_state, cu_seqlens, N, B, T, D, dt, act == GDN_ACT_SILU,
+                               dout, dfinal_state, dx, dweight, dbias, dinitial_state, workspace,
+                               static_cast<cudaStream_t>(stream));
+}
+
+gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, const void* scales, gdn_dtype sdt,
+                         const uint8_t* zeros, const float* bias, int M, int N, int K, int group, gdn_dtype dt,
+                         void* y, void* stream) {
+  if ((dt != GDN_F32 && dt != GDN_BF16) || (sdt != GDN_F32 && sdt != GDN_BF16)) return GDN_ERR_INVALID_ARG;
+  if (M < 0 || N <= 0 || K <= 0 || group <= 0 || group % 32 != 0 || K % group != 0) return GDN_ERR_INVALID_ARG;
+  if (ld_x == 0) ld_x = K;
+  if (ld_x < K || !qweight || !aligned(qweight, 16) || !scales) return GDN_ERR_INVALID_ARG;
+  const size_t es = dt == GDN_F32 ? 4 : 2;
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(scales, sdt == GDN_F32 ? 4 : 2) || !aligned(bias, 4))
+    return GDN_ERR_INVALID_ARG;
+  if (M == 0) return GDN_OK;
+  if (!x || !y) return GDN_ERR_INVALID_ARG;
+  return run_q4_matvec(x, ld_x, qweight, scales, sdt, zeros, bias, M, N, K, group, dt, y,
+                       static_cast<cudaStream_t>(stream));
+}
+
 const char* gdn_status_string(gdn_status s) {
   switch (s) {
     case GDN_OK: return "ok";

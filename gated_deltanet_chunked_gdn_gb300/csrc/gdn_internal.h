@@ -153,6 +153,27 @@ gdn_status run_scan_step(const gdn_scan_problem& p, const void* x, const void* d
                          const void* C, const float* Dp, const void* z, const float* dt_bias, float* state,
                          const int32_t* state_indices, int state_slots, const int32_t* cu, void* y, cudaStream_t s);
 
+// Its backward (gdn_scan_bwd.cu).
+constexpr int kScanBwdMaxG = 32768;
+size_t scan_bwd_workspace_bytes(const gdn_scan_problem& p);
+gdn_status run_scan_bwd(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
+                        const void* C, const float* Dp, const void* z, const float* dt_bias, const float* h0,
+                        const int32_t* cu, const void* dout, const float* dht, void* dx, void* ddelta, float* dA,
+                        void* dB, void* dC, float* dD, void* dz, float* ddt_bias, float* dh0, void* ws,
+                        cudaStream_t s);
+
+// Backward of the causal convolution (gdn_conv1d_bwd.cu).
+size_t conv1d_bwd_workspace_bytes(int64_t tokens, int D, int W);
+gdn_status run_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, int W,
+                                 const void* initial_state, const int32_t* cu, int N, int B, int T, int D,
+                                 gdn_dtype dt, bool silu_act, const void* dout, const void* dfinal_state, void* dx,
+                                 float* dweight, float* dbias, void* dinitial_state, void* ws, cudaStream_t s);
+
+// Rows times 4-bit weights (gdn_q4.cu).
+gdn_status run_q4_matvec(const void* x, int64_t ldx, const uint8_t* qweight, const void* scales, gdn_dtype sdt,
+                         const uint8_t* zeros, const float* bias, int M, int N, int K, int group, gdn_dtype dt,
+                         void* y, cudaStream_t s);
+
 // Chunk-parallel path (gdn_cp.cu): sequences cut into segments run in parallel.
 size_t cp_workspace_bytes(const gdn_problem& p);
 gdn_status run_cp(const gdn_problem& p, const void* q, const void* k, const void* v, const float* g,

@@ -400,6 +400,50 @@ gdn_status gdn_causal_conv1d_fwd(const void* x, const float* weight, const float
                                  void* stream);
 
 /*
+ * Backward of gdn_causal_conv1d_fwd, with the initial inputs given per sequence
+ * (the forward call overwrites its state pool): for upstream gradients dout =
+ * dL/dy and dfinal_state = dL/d(new state), the gradients of L with respect to
+ * x, weight, bias and the initial inputs.
+ *   x, dout, dx : [B, T, D] of dtype dt, 16-byte aligned, D % 8 == 0
+ *   weight, bias, W, act, cu_seqlens, N, B, T : as for gdn_causal_conv1d_fwd
+ *   initial_state : [N, W-1, D] of dtype dt or NULL (= 0);  dfinal_state : the
+ *                 same shape or NULL (= 0).  16-byte aligned; ignored when W == 1.
+ *   dweight     : out [D, W] fp32;  dbias : out [D] fp32 or NULL
+ *   dinitial_state : out [N, W-1, D] of dtype dt or NULL
+ *   workspace   : gdn_causal_conv1d_bwd_workspace_size(B, T, D, W) bytes (0:
+ *                 invalid), 256-byte aligned (partial sums of dweight and dbias)
+ * A sequence with malformed offsets is skipped as in the forward (no gradient of
+ * it is written or added).  Sums are added in a fixed order: results do not
+ * depend on the run.  Asynchronous on `stream`.
+ */
+size_t gdn_causal_conv1d_bwd_workspace_size(int B, int T, int D, int W);
+gdn_status gdn_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, int W,
+                                 const void* initial_state, const int32_t* cu_seqlens, int N, int B, int T, int D,
+                                 gdn_dtype dt, gdn_activation act, const void* dout, const void* dfinal_state,
+                                 void* dx, float* dweight, float* dbias, void* dinitial_state, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * A few rows times a matrix of 4-bit weights with group scales (the projections
+ * of a decode step; any number of rows is computed, 32 of bf16 or 10 of fp32 a
+ * pass over the weights):
+ *     y[m][n] = sum_k x[m][k] (code[n][k] - zero[n][k / group]) scale[n][k / group] + bias[n]
+ *   x           : [M, K] of dtype dt, rows ld_x elements apart (0: K)
+ *   qweight     : [N, K / 2] bytes, 16-byte aligned; byte j of a row holds code 2j
+ *                 in its low four bits and code 2j + 1 in its high four
+ *   scales      : [N, K / group] of dtype sdt
+ *   zeros       : [N, K / group] bytes, 0 .. 127, or NULL (8 everywhere)
+ *   bias        : [N] fp32 or NULL
+ *   K           : a multiple of group;  group : a multiple of 32
+ *   y           : out [M, N] of dtype dt, contiguous
+ * Products and sums are exact to fp32 (no weight and, in fp32, no x is rounded);
+ * y is rounded once.  No workspace; asynchronous on `stream`.
+ */
+gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, const void* scales, gdn_dtype sdt,
+                         const uint8_t* zeros, const float* bias, int M, int N, int K, int group, gdn_dtype dt,
+                         void* y, void* stream);
+
+/*
  * Selective state space scan (a diagonal linear recurrence whose steps, input
  * and output maps depend on the token): the mixer that hybrid stacks put next
  * to the gated delta rule, behind the same short causal convolution.  For
@@ -458,6 +502,33 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* p, const void* x, cons
  * write none: GDN_DEV_OK. */
 gdn_status gdn_selective_scan_get_device_status(const gdn_scan_problem* p, void* workspace, void* stream,
                                                 int* dev_status);
+
+/*
+ * Backward of gdn_selective_scan_fwd: for upstream gradients dout = dL/dy and
+ * dht = dL/dht, the gradients of L with respect to every input, by the adjoint
+ * recurrence q_t = C_t dout_t silu(z_t) + e^{dt_{t+1} A} q_{t+1}.
+ *   inputs      : as for gdn_selective_scan_fwd (G at most 32768)
+ *   dout        : [B, T, D] dtype p->dt, contiguous;  dht : [N, D, S] fp32 or NULL (= 0)
+ *   dx, ddelta  : out [B, T, D] dtype p->dt;  dB, dC : out [B, T, G, S] dtype p->dt
+ *                 (fp32 sums over the channels of a group, rounded once)
+ *   dz          : out [B, T, D] dtype p->dt, required with z, else NULL
+ *   dA          : out [D, S] fp32;  dD, ddt_bias : out [D] fp32 or NULL to skip them
+ *                 (sums over all tokens of the batch; given whether or not
+ *                 Dskip and dt_bias are)
+ *   dh0         : out [N, D, S] fp32 or NULL
+ *   workspace   : gdn_selective_scan_bwd_workspace_size(p) bytes, 256-byte
+ *                 aligned (states before the tiles of tokens, and partial sums)
+ * Sums are added in a fixed order (no atomics): results do not depend on the
+ * run.  Malformed cu_seqlens set the status word and leave the gradients
+ * unwritten.  Asynchronous on `stream`.
+ */
+size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_problem* p);
+gdn_status gdn_selective_scan_bwd(const gdn_scan_problem* p, const void* x, const void* delta, const float* A,
+                                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                  const float* dt_bias, const float* h0, const int32_t* cu_seqlens,
+                                  const void* dout, const float* dht, void* dx, void* ddelta, float* dA, void* dB,
+                                  void* dC, float* dD, void* dz, float* ddt_bias, float* dh0, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * The scan on a pool of states, for single tokens (decode); several tokens of

@@ -50,7 +50,9 @@ gdn_status scan_problem_ok(const gdn_scan_problem* pp, gdn_scan_problem* out) {
   const int64_t ld[5] = {p.ld_x, p.ld_delta, p.ld_z, p.ld_b, p.ld_c}, row[5] = {p.D, p.D, p.D, gs, gs};
   for (int i = 0; i < 5; ++i)
     if (ld[i] != 0 && ld[i] < row[i]) return GDN_ERR_INVALID_ARG;
-  if (p.S > kScanMaxS || p.D > kScanMaxD) return GDN_ERR_UNSUPPORTED;
+  for (int64_t l : ld)
+    if (l > (1 << 28)) return GDN_ERR_UNSUPPORTED;   // the kernels keep row strides as 32-bit byte counts
+  if (p.S > kScanMaxS || p.D > kScanMaxD || gs > (1 << 28)) return GDN_ERR_UNSUPPORTED;
   p.softplus = p.softplus != 0;
   *out = p;
   return GDN_OK;

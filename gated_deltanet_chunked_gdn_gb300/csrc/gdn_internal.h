@@ -144,7 +144,7 @@ gdn_status run_bwdc(const gdn_problem& p, const void* q, const void* k, const vo
 
 // Selective state space scan (gdn_scan.cu).
 constexpr int kScanMaxS = 64;      // states a channel
-constexpr int kScanMaxD = 131072;  // channels (at most 32768 CTAs a line of tokens, in the grid's second dimension)
+constexpr int kScanMaxD = 65536;   // channels (at most 32768 CTAs a line of tokens, in the grid's second dimension)
 size_t scan_fwd_workspace_bytes(const gdn_scan_problem& p);
 gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
                         const void* C, const float* Dp, const void* z, const float* dt_bias, const float* h0,

@@ -25,24 +25,47 @@ namespace gdn {
 namespace scan {
 namespace {
 
-constexpr int kWarps = 4;   // warps a CTA
+// Warps a CTA (they share nothing; the widest layout's tiles need the room).
+constexpr int warps_of(int RL) { return RL == 16 ? 2 : 4; }
+constexpr int kRing = 3;   // tiles as loaded: one in use, two on their way
 
+// Shared memory of a warp: the tile being run as fp32, and tiles as loaded.
 template <typename T, int RL, bool STATES>
-__global__ void __launch_bounds__(32 * kWarps) scan_kernel(const Args a) {
+struct Tiles {
   using L = Lanes<RL>;
-  __shared__ __align__(16) float sB[kWarps][L::TT][L::SP];
-  __shared__ __align__(16) float sC[STATES ? 1 : kWarps][STATES ? 1 : L::TT][STATES ? 4 : L::SP];
-  __shared__ __align__(16) float4 sdt[kWarps][L::TT][L::CL];
+  static constexpr int NZ = STATES ? 1 : L::TT;
+  float4 dt[L::TT][L::CL];   // dt, dt x of a channel pair
+  float B[L::TT][L::SP], C[NZ][L::SP];
+  alignas(16) T rx[kRing][L::TT][L::CPW];
+  alignas(16) T rd[kRing][L::TT][L::CPW];
+  alignas(16) T rz[STATES ? 1 : kRing][NZ][L::CPW];
+  alignas(16) T rB[kRing][L::TT][L::SP];
+  alignas(16) T rC[STATES ? 1 : kRing][NZ][L::SP];
+};
+
+// ASYNC: rows arrive by asynchronous copies, otherwise through registers.
+template <typename T, int RL, bool STATES, bool GATE, bool ASYNC>
+__global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a) {
+  using L = Lanes<RL>;
+  using CK = Chunks<T, RL>;
+  constexpr int W = warps_of(RL);
+  constexpr int VE = RowVec<T, RL>::VE, NV = RowVec<T, RL>::NV, NPV = (NV + 31) / 32;
+  extern __shared__ __align__(16) char raw_smem[];
   const L ln;
   const int w = threadIdx.x >> 5;
-  const int cb = blockIdx.y * kWarps + w;
+  Tiles<T, RL, STATES>& sm = reinterpret_cast<Tiles<T, RL, STATES>*>(raw_smem)[w];
+  const int cb = blockIdx.y * W + w;
   const int g = cb / a.cbg;
   if (g >= a.G) return;
   Unit u;
-  if (!unit_of(a, blockIdx.x, u)) return;
-  if (STATES && u.last) return;   // nobody starts from its end
+  // (the states pass leaves out every sequence's last segment, from whose end nobody
+  // starts; equal lengths do not even launch it, or the CTAs that do run would share
+  // half of the SMs)
+  const int64_t un = STATES && !a.cu ? blockIdx.x / (a.nseg - 1) * a.nseg + blockIdx.x % (a.nseg - 1) : blockIdx.x;
+  if (!unit_of(a, un, u)) return;
+  if (STATES && u.last) return;
 
-  const int d = g * a.Dg + (cb - g * a.cbg) * L::CPW + 2 * ln.chl;   // this lane's channel pair
+  const int dw = g * a.Dg + (cb - g * a.cbg) * L::CPW, d = dw + 2 * ln.chl;   // the warp's and this lane's channels
   const int dend = (g + 1) * a.Dg;
   const bool ok0 = d < dend, ok1 = d + 1 < dend;
   const int n0 = 4 * ln.sl, nn = a.S - n0;   // this lane's states
@@ -57,7 +80,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_kernel(const Args a) {
       load4(a.A + (int64_t)(d + c) * a.S + n0, nn, v4, r);
       if (!STATES) {
         const float* from = nullptr;
-        if (!u.first) from = a.hseg + ((int64_t)blockIdx.x * a.D + d + c) * a.S;
+        if (!u.first) from = a.hseg + (un * a.D + d + c) * a.S;
         else if (a.h0) from = a.h0 + ((int64_t)u.n * a.D + d + c) * a.S;
         if (from) load4(from + n0, nn, v4, s);
       }
@@ -70,86 +93,146 @@ __global__ void __launch_bounds__(32 * kWarps) scan_kernel(const Args a) {
   const float2 bias = make_float2(a.bias && ok0 ? a.bias[d] : 0.f, a.bias && ok1 ? a.bias[d + 1] : 0.f);
   const float2 skip = make_float2(a.Dp && ok0 ? a.Dp[d] : 0.f, a.Dp && ok1 ? a.Dp[d + 1] : 0.f);
 
-  const T* px = static_cast<const T*>(a.x) + u.tok0 * a.ldx + d;
-  const T* pd = static_cast<const T*>(a.dl) + u.tok0 * a.ldd + d;
-  const T* pz = a.z ? static_cast<const T*>(a.z) + u.tok0 * a.ldz + d : nullptr;
-  const T* pB = static_cast<const T*>(a.B) + u.tok0 * a.ldb + g * a.S;
-  const T* pC = static_cast<const T*>(a.C) + u.tok0 * a.ldc + g * a.S;
+  // the warp's first row of every tensor
+  const char* px = static_cast<const char*>(a.x) + u.tok0 * a.bx + dw * (int64_t)sizeof(T);
+  const char* pd = static_cast<const char*>(a.dl) + u.tok0 * a.bd + dw * (int64_t)sizeof(T);
+  const char* pz = static_cast<const char*>(a.z) + u.tok0 * a.bz + dw * (int64_t)sizeof(T);
+  const char* pB = static_cast<const char*>(a.B) + u.tok0 * a.bb + g * a.S * (int64_t)sizeof(T);
+  const char* pC = static_cast<const char*>(a.C) + u.tok0 * a.bc + g * a.S * (int64_t)sizeof(T);
+  T* py = static_cast<T*>(a.y) + u.tok0 * a.D + d;
 
-  Raw2<T> rx[4], rd[4], rz[4], rB[L::NPB], rC[L::NPB];
-  auto load_tile = [&](int t0) {
+  // A tile's rows into ring slot r: by copies, or in two steps through registers.
+  Raw2<T> gx[4], gd[4], gz[4];
+  uint4 gB[NPV], gC[NPV];
+  auto fetch = [&](int t0, int r) {
+    if constexpr (ASYNC) {
+      const int vx = (dend - dw) * (int)sizeof(T), vs = a.S * (int)sizeof(T);
+      copy_rows<L::TT, CK::ROW, CK::X>((char*)&sm.rx[r][0][0], px, a.bx, t0, u.len, vx, ln.lane);
+      copy_rows<L::TT, CK::ROW, CK::X>((char*)&sm.rd[r][0][0], pd, a.bd, t0, u.len, vx, ln.lane);
+      copy_rows<L::TT, CK::SROW, CK::B>((char*)&sm.rB[r][0][0], pB, a.bb, t0, u.len, vs, ln.lane);
+      if constexpr (!STATES) {
+        copy_rows<L::TT, CK::SROW, CK::B>((char*)&sm.rC[r][0][0], pC, a.bc, t0, u.len, vs, ln.lane);
+        if (GATE) copy_rows<L::TT, CK::ROW, CK::X>((char*)&sm.rz[r][0][0], pz, a.bz, t0, u.len, vx, ln.lane);
+      }
+      copies_commit();
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = t0 + ln.token(k);
-      rx[k].zero(), rd[k].zero(), rz[k].zero();
-      if (t < u.len && ok0) {
-        rx[k].load(px + t * a.ldx, a.vx, ok0, ok1);
-        rd[k].load(pd + t * a.ldd, a.vd, ok0, ok1);
-        if (!STATES && pz) rz[k].load(pz + t * a.ldz, a.vz, ok0, ok1);
+      for (int k = 0; k < 4; ++k) {
+        const int t = t0 + ln.token(k);
+        gx[k].zero(), gd[k].zero(), gz[k].zero();
+        if (t < u.len && ok0) {
+          gx[k].load(row((const T*)px, t, a.bx) + 2 * ln.chl, a.vin, ok0, ok1);
+          gd[k].load(row((const T*)pd, t, a.bd) + 2 * ln.chl, a.vin, ok0, ok1);
+          if (!STATES && GATE) gz[k].load(row((const T*)pz, t, a.bz) + 2 * ln.chl, a.vin, ok0, ok1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NPV; ++i) {
+        const int p = (ln.lane + 32 * i) * VE, t = t0 + p / L::SP, n = p % L::SP;
+        gB[i] = gC[i] = make_uint4(0u, 0u, 0u, 0u);
+        if ((NV % 32 == 0 || ln.lane + 32 * i < NV) && t < u.len) {
+          gB[i] = load_row16<T, VE>(row((const T*)pB, t, a.bb), n, a.S, a.vbc);
+          if (!STATES) gC[i] = load_row16<T, VE>(row((const T*)pC, t, a.bc), n, a.S, a.vbc);
+        }
       }
     }
+  };
+  auto fetched = [&](int r) {   // the registers' tile into slot r
+    if constexpr (!ASYNC) {
 #pragma unroll
-    for (int i = 0; i < L::NPB; ++i) {
-      const int p = ln.lane + 32 * i, t = t0 + p / (L::SP / 2), n = 2 * (p % (L::SP / 2));
-      rB[i].zero(), rC[i].zero();
-      if (p < L::TT * L::SP / 2 && t < u.len && n < a.S) {
-        rB[i].load(pB + t * a.ldb + n, a.vb, true, n + 1 < a.S);
-        if (!STATES) rC[i].load(pC + t * a.ldc + n, a.vc, true, n + 1 < a.S);
+      for (int k = 0; k < 4; ++k) {
+        const int t = ln.token(k), c = 2 * ln.chl;
+        gx[k].store(&sm.rx[r][t][c]), gd[k].store(&sm.rd[r][t][c]);
+        if constexpr (!STATES && GATE) gz[k].store(&sm.rz[r][t][c]);
+      }
+#pragma unroll
+      for (int i = 0; i < NPV; ++i) {
+        if (NV % 32 == 0 || ln.lane + 32 * i < NV) {
+          const int p = (ln.lane + 32 * i) * VE;
+          copy_vec<VE * sizeof(T)>(&sm.rB[r][0][0] + p, gB[i]);
+          if constexpr (!STATES) copy_vec<VE * sizeof(T)>(&sm.rC[r][0][0] + p, gC[i]);
+        }
       }
     }
   };
 
+  float2 xs[4], zs[4];                  // x and z of this lane's tokens of the tile being run
   float2 dts = make_float2(0.f, 0.f);   // STATES: sum of this lane's steps
-  load_tile(0);
-  for (int t0 = 0; t0 < u.len; t0 += L::TT) {
-    // this tile to shared memory, the next one's loads behind it
-    float2 xs[4], zs[4];
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = rx[k].f();
-      float2 dt = rd[k].f();
-      dt.x += bias.x, dt.y += bias.y;
-      if (a.softplus) {
-        float e;
-        dt.x = softplus(dt.x, e), dt.y = softplus(dt.y, e);
-      }
-      if (t0 + ln.token(k) >= u.len) dt = make_float2(0.f, 0.f);   // past the end: the state stays
-      xs[k] = x;
-      if (!STATES) zs[k] = rz[k].f();
-      if (STATES) dts.x += dt.x, dts.y += dt.y;
-      if (!ln.dup) sdt[w][ln.token(k)][ln.chl] = make_float4(dt.x, dt.x * x.x, dt.y, dt.y * x.y);
+  // One of this lane's tokens of ring slot r's tile (first token t0) as fp32; past the sequence's end steps and inputs are zero: the state stays.
+  auto stage = [&](int k, int t0, int r) {
+    const int t = ln.token(k), c = 2 * ln.chl;
+    Raw2<T> x, e;
+    x.load_shared(&sm.rx[r][t][c]), e.load_shared(&sm.rd[r][t][c]);
+    float2 dt = __fadd2_rn(e.f(), bias);
+    if (a.softplus) {
+      float2 ex;
+      dt = softplus2(dt, ex);
     }
+    xs[k] = x.f();
+    if constexpr (!STATES && GATE) {
+      Raw2<T> z;
+      z.load_shared(&sm.rz[r][t][c]);
+      zs[k] = z.f();
+    }
+    const float2 dx = __fmul2_rn(dt, xs[k]);   // x is zero past the end
+    if (t0 + t >= u.len) dt = make_float2(0.f, 0.f);
+    if (STATES) dts = __fadd2_rn(dts, dt);
+    if (!ln.dup) sm.dt[t][ln.chl] = make_float4(dt.x, dt.y, dx.x, dx.y);
+  };
+  auto stage_rows = [&](int r) {
 #pragma unroll
-    for (int i = 0; i < L::NPB; ++i) {
-      const int p = ln.lane + 32 * i, t = p / (L::SP / 2), n = 2 * (p % (L::SP / 2));
-      if (p < L::TT * L::SP / 2) {
-        *reinterpret_cast<float2*>(&sB[w][t][n]) = rB[i].f();
-        if constexpr (!STATES) *reinterpret_cast<float2*>(&sC[w][t][n]) = rC[i].f();
+    for (int i = 0; i < NPV; ++i) {
+      if (NV % 32 == 0 || ln.lane + 32 * i < NV) {
+        const int p = (ln.lane + 32 * i) * VE;
+        put_row16<T, VE>(&sm.B[0][0] + p, get_vec<VE * sizeof(T)>(&sm.rB[r][0][0] + p));
+        if constexpr (!STATES) put_row16<T, VE>(&sm.C[0][0] + p, get_vec<VE * sizeof(T)>(&sm.rC[r][0][0] + p));
       }
     }
-    __syncwarp();
-    if (t0 + L::TT < u.len) load_tile(t0 + L::TT);
+  };
 
+  const int ntile = (u.len + L::TT - 1) / L::TT;
+  if (ntile > 0) {
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(i * L::TT, i), fetched(i);
+  }
+  for (int i = 0, r = 0; i < ntile; ++i) {
+    const int t0 = i * L::TT;
+    const int rn = r == 0 ? kRing - 1 : r - 1;   // the slot that tile i - 1 has left
+    if (ASYNC) copies_wait<kRing - 2>();
+    __syncwarp();
+    fetch(t0 + (kRing - 1) * L::TT, rn);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) stage(k, t0, r);
+    stage_rows(r);
+    __syncwarp();
 #pragma unroll
     for (int gr = 0; gr < L::NG; ++gr) {
+      // four tokens' decays and inputs, then the recurrence over them
       float v[8];
+      float2 aa[4][2][2], uu[4][2][2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = 4 * gr + j;
-        const float4 q = sdt[w][t][ln.chl];
-        const float4 b = *reinterpret_cast<const float4*>(&sB[w][t][n0]);
-        float4 cc;
-        if constexpr (!STATES) cc = *reinterpret_cast<const float4*>(&sC[w][t][n0]);
+        const float4 q = sm.dt[4 * gr + j][ln.chl];
+        const float4 bb = *reinterpret_cast<const float4*>(&sm.B[4 * gr + j][n0]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float dt = c ? q.z : q.x, ux = c ? q.w : q.y;
-          const float2 dt2 = make_float2(dt, dt), ux2 = make_float2(ux, ux);
+          const float dc = c ? q.y : q.x, ux = c ? q.w : q.z;
+          const float2 dt2 = make_float2(dc, dc), ux2 = make_float2(ux, ux);
           const float2 e0 = __fmul2_rn(dt2, A2[c][0]), e1 = __fmul2_rn(dt2, A2[c][1]);
-          const float2 a0 = make_float2(sm100::ex2_fast(e0.x), sm100::ex2_fast(e0.y));
-          const float2 a1 = make_float2(sm100::ex2_fast(e1.x), sm100::ex2_fast(e1.y));
-          h[c][0] = __ffma2_rn(a0, h[c][0], __fmul2_rn(ux2, make_float2(b.x, b.y)));
-          h[c][1] = __ffma2_rn(a1, h[c][1], __fmul2_rn(ux2, make_float2(b.z, b.w)));
+          aa[j][c][0] = make_float2(sm100::ex2_fast(e0.x), sm100::ex2_fast(e0.y));
+          aa[j][c][1] = make_float2(sm100::ex2_fast(e1.x), sm100::ex2_fast(e1.y));
+          uu[j][c][0] = __fmul2_rn(ux2, make_float2(bb.x, bb.y));
+          uu[j][c][1] = __fmul2_rn(ux2, make_float2(bb.z, bb.w));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float4 cc;
+        if constexpr (!STATES) cc = *reinterpret_cast<const float4*>(&sm.C[4 * gr + j][n0]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          h[c][0] = __ffma2_rn(aa[j][c][0], h[c][0], uu[j][c][0]);
+          h[c][1] = __ffma2_rn(aa[j][c][1], h[c][1], uu[j][c][1]);
           if constexpr (!STATES) {
             float2 y2 = __fmul2_rn(h[c][0], make_float2(cc.x, cc.y));
             y2 = __ffma2_rn(h[c][1], make_float2(cc.z, cc.w), y2);
@@ -162,14 +245,24 @@ __global__ void __launch_bounds__(32 * kWarps) scan_kernel(const Args a) {
 #pragma unroll
         for (int j = 0; j < L::TPL; ++j) {
           const int k = gr * L::TPL + j, t = t0 + ln.token(k);
-          float2 o = make_float2(fmaf(skip.x, xs[k].x, v[2 * j]), fmaf(skip.y, xs[k].y, v[2 * j + 1]));
-          if (pz) o.x *= zs[k].x * sigmoid(zs[k].x), o.y *= zs[k].y * sigmoid(zs[k].y);
-          if (t < u.len && ok0 && !ln.dup)
-            store2(static_cast<T*>(a.y) + (u.tok0 + t) * a.D + d, o, a.vy, ok0, ok1);
+          float2 o = __ffma2_rn(skip, xs[k], make_float2(v[2 * j], v[2 * j + 1]));
+          if constexpr (GATE) {
+            const float2 nl = __fmul2_rn(zs[k], make_float2(-sm100::kLog2e, -sm100::kLog2e));
+            const float2 den = __fadd2_rn(make_float2(sm100::ex2_fast(nl.x), sm100::ex2_fast(nl.y)), make_float2(1.f, 1.f));
+            o = __fmul2_rn(__fmul2_rn(o, zs[k]), make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+          }
+          if constexpr (ASYNC) {   // the rows are even: both channels or none
+            if (t < u.len && ok1 && !ln.dup) store2(py + (int64_t)t * a.D, o);
+          } else if (t < u.len && ok0 && !ln.dup) {
+            store2(py + (int64_t)t * a.D, o, a.vy, ok0, ok1);
+          }
         }
       }
     }
+    if (!ASYNC) fetched(rn);
+    r = r + 1 == kRing ? 0 : r + 1;
   }
+  if (ASYNC) copies_wait<0>();
 
   // end states
   if constexpr (STATES) {
@@ -180,12 +273,12 @@ __global__ void __launch_bounds__(32 * kWarps) scan_kernel(const Args a) {
       dts.y += __shfl_xor_sync(~0u, dts.y, m);
     }
     if (ln.sl == 0) {
-      if (ok0) a.dtsum[(int64_t)blockIdx.x * a.D + d] = dts.x;
-      if (ok1) a.dtsum[(int64_t)blockIdx.x * a.D + d + 1] = dts.y;
+      if (ok0) a.dtsum[un * a.D + d] = dts.x;
+      if (ok1) a.dtsum[un * a.D + d + 1] = dts.y;
     }
   }
   float* to = nullptr;
-  if (STATES) to = a.hseg + (int64_t)blockIdx.x * a.D * a.S;
+  if (STATES) to = a.hseg + un * a.D * a.S;
   else if (a.ht && u.last) to = a.ht + (int64_t)u.n * a.D * a.S;
   if (to) {
 #pragma unroll
@@ -209,12 +302,23 @@ __global__ void __launch_bounds__(256) chain_kernel(const Args a) {
   const int64_t u1 = a.cu ? a.seg0[n + 1] : u0 + a.nseg;
   const float r = a.A[i] * sm100::kLog2e;
   float h = a.h0 ? a.h0[n * DS + i] : 0.f;
-  for (int64_t u = u0; u + 1 < u1; ++u) {
-    const float end = a.hseg[u * DS + i], dt = a.dtsum[u * a.D + d];
-    if (u > u0) a.hseg[u * DS + i] = h;
-    h = fmaf(sm100::ex2_fast(r * dt), h, end);
+  // eight segments' loads at a time
+  for (int64_t u = u0; u + 1 < u1; u += 8) {
+    float end[8], dt[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = u + k + 1 < u1;
+      end[k] = in ? a.hseg[(u + k) * DS + i] : 0.f;
+      dt[k] = in ? a.dtsum[(u + k) * a.D + d] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (u + k + 1 >= u1) break;
+      a.hseg[(u + k) * DS + i] = h;
+      h = fmaf(sm100::ex2_fast(r * dt[k]), h, end[k]);
+    }
   }
-  if (u1 > u0 + 1) a.hseg[(u1 - 1) * DS + i] = h;
+  a.hseg[(u1 - 1) * DS + i] = h;
 }
 
 // One CTA: checks cu_seqlens, writes every sequence's first segment and lists
@@ -322,31 +426,28 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const StepArgs p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) A2[i] *= sm100::kLog2e;
   const float bias = a.bias ? a.bias[dd] : 0.f, skip = a.Dp ? a.Dp[dd] : 0.f;
-  const T* px = static_cast<const T*>(a.x) + s0 * a.ldx + dd;
-  const T* pd = static_cast<const T*>(a.dl) + s0 * a.ldd + dd;
-  const T* pz = a.z ? static_cast<const T*>(a.z) + s0 * a.ldz + dd : nullptr;
-  const T* pB = static_cast<const T*>(a.B) + s0 * a.ldb + g * a.S + n0;
-  const T* pC = static_cast<const T*>(a.C) + s0 * a.ldc + g * a.S + n0;
-  for (int64_t t = 0; t < len; ++t) {
-    const float x = to_f(px[t * a.ldx]);
-    float dt = to_f(pd[t * a.ldd]) + bias;
-    const float z = pz ? to_f(pz[t * a.ldz]) : 0.f;
+  const T* px = reinterpret_cast<const T*>(static_cast<const char*>(a.x) + s0 * a.bx) + dd;
+  const T* pd = reinterpret_cast<const T*>(static_cast<const char*>(a.dl) + s0 * a.bd) + dd;
+  const T* pz = reinterpret_cast<const T*>(static_cast<const char*>(a.z) + s0 * a.bz) + dd;
+  const T* pB = reinterpret_cast<const T*>(static_cast<const char*>(a.B) + s0 * a.bb) + g * a.S + n0;
+  const T* pC = reinterpret_cast<const T*>(static_cast<const char*>(a.C) + s0 * a.bc) + g * a.S + n0;
+  for (int t = 0; t < len; ++t) {
+    const float x = to_f(*row(px, t, a.bx));
+    float dt = to_f(*row(pd, t, a.bd)) + bias;
+    const float z = a.z ? to_f(*row(pz, t, a.bz)) : 0.f;
     float b[4], c[4];
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       Raw2<T> rb, rc;
       rb.zero(), rc.zero();
       if (i < nn) {
-        rb.load(pB + t * a.ldb + i, a.vb, true, i + 1 < nn);
-        rc.load(pC + t * a.ldc + i, a.vc, true, i + 1 < nn);
+        rb.load(row(pB, t, a.bb) + i, a.vbc, true, i + 1 < nn);
+        rc.load(row(pC, t, a.bc) + i, a.vbc, true, i + 1 < nn);
       }
       const float2 fb = rb.f(), fc = rc.f();
       b[i] = fb.x, b[i + 1] = fb.y, c[i] = fc.x, c[i + 1] = fc.y;
     }
-    if (a.softplus) {
-      float e;
-      dt = softplus(dt, e);
-    }
+    if (a.softplus) dt = softplus(dt);
     const float ux = dt * x;
     float o = 0.f;
 #pragma unroll
@@ -357,7 +458,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const StepArgs p) {
 #pragma unroll
     for (int m = 1; m < RL; m <<= 1) o += __shfl_xor_sync(~0u, o, m);
     o = fmaf(skip, x, o);
-    if (pz) o *= z * sigmoid(z);
+    if (a.z) o *= z * sigmoid(z);
     if (ok && sl == 0) y[(s0 + t) * a.D + d] = from_f<T>(o);
   }
   if (!ok) return;
@@ -383,12 +484,21 @@ void by_lanes(int RL, F&& f) {
 
 template <typename T, bool STATES>
 void launch_scan(const Args& a, const Plan& pl, cudaStream_t s) {
-  const dim3 grid((unsigned)pl.max_units, (unsigned)ceil_div((int64_t)a.G * a.cbg, kWarps));
-  by_lanes(pl.RL, [&](auto rl) { scan_kernel<T, decltype(rl)::value, STATES><<<grid, 32 * kWarps, 0, s>>>(a); });
-}
-
-bool pairs(const void* p, size_t es, int64_t ld, bool rows_even) {
-  return rows_even && ld % 2 == 0 && reinterpret_cast<uintptr_t>(p) % (2 * es) == 0;
+  by_lanes(pl.RL, [&](auto rl) {
+    constexpr int R = decltype(rl)::value, W = warps_of(R);
+    const int64_t units = STATES && !a.cu ? pl.max_units - a.N : pl.max_units;
+    const dim3 grid((unsigned)units, (unsigned)ceil_div((int64_t)a.G * a.cbg, W));
+    const size_t bytes = W * sizeof(Tiles<T, R, STATES>);
+    auto go = [&](auto gate) {
+      constexpr bool Z = decltype(gate)::value;
+      auto* k = a.async ? scan_kernel<T, R, STATES, Z, true> : scan_kernel<T, R, STATES, Z, false>;
+      if (bytes > 48 * 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+      k<<<grid, 32 * W, bytes, s>>>(a);
+    };
+    if constexpr (STATES) go(std::false_type());
+    else if (a.z) go(std::true_type());
+    else go(std::false_type());
+  });
 }
 
 struct Layout {
@@ -413,18 +523,25 @@ Plan make_plan(const gdn_scan_problem& p) {
   pl.RL = lanes_for(p.S);
   pl.cpw = 64 / pl.RL;
   pl.cbg = (int)ceil_div(p.D / p.G, pl.cpw);
-  const int64_t cw = (int64_t)p.G * pl.cbg;         // warps a line of tokens
-  const int64_t slots = (int64_t)sm_count() * 8;    // warps that fill the SMs
+  const int64_t cw = (int64_t)p.G * pl.cbg;              // warps a line of tokens
+  const int64_t fill = (int64_t)sm_count() * 27 / 2;     // warps that keep the SMs busy
+  // A cut costs a second run over all tokens but the last segments'.  Equal lengths
+  // are cut when fewer than three warps an SM would run, into enough segments for
+  // 13.5 (one GB300, 4096 channels, 16 states: 1 x 4096 tokens, 256 warps, 291 us
+  // uncut, 185 / 164 / 162 in 4 / 8 / 16 segments; 4 x 8192 tokens, 1024 warps, 811 us
+  // uncut, 1051 in two).  Packed sequences, whose lengths the host does not know, are
+  // cut so that the longest ones do not outlast the rest (64 sequences of up to 2048
+  // tokens, 2048 channels: 160 / 181 / 206 / 300 us with segments of 128 / 256 / 512 /
+  // 1024 tokens).
   if (p.varlen) {
-    int64_t len = align_up((size_t)(p.T * cw / slots), kTileMax);
+    int64_t len = (int64_t)align_up((size_t)(p.T * cw / (4 * fill)), kTileMax);
     if (len < 128) len = 128;
     pl.seglen = (int)len;
     pl.nseg = 1;
     pl.max_units = p.T / len + p.N;
     pl.cut = p.T > len;
   } else {
-    int64_t n = 1;
-    if (p.B * cw < slots) n = ceil_div(slots, p.B * cw);
+    int64_t n = p.B * cw < 3 * sm_count() ? ceil_div(fill, p.B * cw) : 1;
     if (n > p.T / 128) n = p.T / 128 > 1 ? p.T / 128 : 1;
     pl.seglen = (int)align_up((size_t)ceil_div(p.T, n), kTileMax);
     pl.nseg = (int)ceil_div(p.T, pl.seglen);
@@ -444,20 +561,22 @@ Args base_args(const gdn_scan_problem& p, const Plan& pl, const void* x, const v
   a.cu = p.varlen ? cu : nullptr;
   a.D = p.D, a.S = p.S, a.G = p.G, a.Dg = p.D / p.G;
   const int64_t gs = (int64_t)p.G * p.S;
-  a.ldx = p.ld_x ? p.ld_x : p.D;
-  a.ldd = p.ld_delta ? p.ld_delta : p.D;
-  a.ldz = p.ld_z ? p.ld_z : p.D;
-  a.ldb = p.ld_b ? p.ld_b : gs;
-  a.ldc = p.ld_c ? p.ld_c : gs;
+  a.bx = (int)((p.ld_x ? p.ld_x : p.D) * es);
+  a.bd = (int)((p.ld_delta ? p.ld_delta : p.D) * es);
+  a.bz = (int)((p.ld_z ? p.ld_z : p.D) * es);
+  a.bb = (int)((p.ld_b ? p.ld_b : gs) * es);
+  a.bc = (int)((p.ld_c ? p.ld_c : gs) * es);
   a.T = p.T, a.N = p.N;
   a.cbg = pl.cbg, a.nseg = pl.nseg, a.seglen = pl.seglen;
   a.softplus = p.softplus;
-  const bool even = a.Dg % 2 == 0;
-  a.vx = pairs(x, es, a.ldx, even);
-  a.vd = pairs(delta, es, a.ldd, even);
-  a.vz = pairs(z, es, a.ldz, even);
-  a.vb = pairs(B, es, a.ldb, a.S % 2 == 0);
-  a.vc = pairs(C, es, a.ldc, a.S % 2 == 0);
+  a.vin = a.Dg % 2 == 0 && aligned_rows(x, a.bx, 2 * es) && aligned_rows(delta, a.bd, 2 * es) &&
+          (!z || aligned_rows(z, a.bz, 2 * es));
+  const int ve = 16 / (int)es < 4 * pl.RL ? 16 / (int)es : 4 * pl.RL;   // RowVec::VE
+  a.vbc = ve * es == 16 && a.S == 4 * pl.RL && aligned_rows(B, a.bb, 16) && aligned_rows(C, a.bc, 16);
+  const int cx = chunk_x(pl.RL, (int)es), cb = chunk_b(pl.RL, (int)es);
+  a.async = a.Dg % 2 == 0 && aligned_rows(x, a.bx, cx) && aligned_rows(delta, a.bd, cx) &&
+            (!z || aligned_rows(z, a.bz, cx)) && aligned_rows(B, a.bb, cb) && aligned_rows(C, a.bc, cb) &&
+            (a.G == 1 || (a.Dg * es % cx == 0 && a.S * es % cb == 0));
   return a;
 }
 
@@ -491,7 +610,9 @@ gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* de
   Args a = base_args(p, pl, x, delta, A, B, C, Dp, z, dt_bias, h0, cu);
   char* w = static_cast<char*>(ws);
   a.y = y, a.ht = ht;
-  a.vy = pairs(y, p.dt == GDN_F32 ? 4 : 2, p.D, a.Dg % 2 == 0);
+  const int es = p.dt == GDN_F32 ? 4 : 2;
+  a.vy = a.Dg % 2 == 0 && aligned_rows(y, p.D * es, 2 * es);
+  a.async = a.async && a.vy;
   if (p.varlen) {
     a.seg0 = reinterpret_cast<int32_t*>(w + l.seg0);
     if (launch_prepare_segments(cu, p.N, p.T, pl.seglen, reinterpret_cast<int32_t*>(w + l.seg0),

@@ -34,12 +34,14 @@ struct Args {
   const void *x, *dl, *z, *B, *C;
   const float *A, *Dp, *bias, *h0;
   const int32_t* cu;
-  int64_t ldx, ldd, ldz, ldb, ldc;   // elements from one token to the next
+  int bx, bd, bz, bb, bc;            // bytes from one token's row to the next
   int64_t T;                         // tokens of a sequence, or of the packed batch
   int N, D, S, G, Dg;                // Dg = D / G channels a group
   int cbg;                           // warp channel blocks a group
   int softplus;
-  bool vx, vd, vz, vb, vc;           // pairs of neighbours can be loaded at once
+  bool vin;     // pairs of neighbouring channels of x, delta and z can be loaded at once
+  bool vbc;     // vectors of B and C (RowVec) can be loaded at once
+  bool async;   // every row can be copied in chunks (Chunks)
   // segments
   int nseg;                 // of a sequence (equal lengths)
   int seglen;               // tokens, a multiple of kTileMax
@@ -88,12 +90,20 @@ __device__ __forceinline__ bool unit_of(const Args& a, int64_t u, Unit& r) {
   return true;
 }
 
+// Row t of a tensor whose rows are `stride` bytes apart (one multiply-add).
+template <typename T>
+__device__ __forceinline__ const T* row(const T* p, int t, int stride) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + (int64_t)t * stride);
+}
+
 // Two neighbouring elements as loaded (converted when they are used, so that
 // the loads of the next tile stay in flight).
 template <typename T> struct Raw2;
 template <> struct Raw2<__nv_bfloat16> {
   uint32_t v;
   __device__ __forceinline__ void zero() { v = 0u; }
+  __device__ __forceinline__ void load_shared(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint32_t*>(p) = v; }
   __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec, bool ok0, bool ok1) {
     if (vec && ok1) {
       v = __ldg(reinterpret_cast<const uint32_t*>(p));
@@ -110,6 +120,8 @@ template <> struct Raw2<__nv_bfloat16> {
 template <> struct Raw2<float> {
   float2 v;
   __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
+  __device__ __forceinline__ void load_shared(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float2*>(p) = v; }
   __device__ __forceinline__ void load(const float* p, bool vec, bool ok0, bool ok1) {
     if (vec && ok1) {
       v = __ldg(reinterpret_cast<const float2*>(p));
@@ -121,6 +133,72 @@ template <> struct Raw2<float> {
   __device__ __forceinline__ float2 f() const { return v; }
 };
 
+// A tile's rows of B (or C, padded to SP states) move in vectors of VE elements,
+// 16 bytes where a row has as many; NV of them.
+template <typename T, int RL>
+struct RowVec {
+  static constexpr int SP = 4 * RL, VE = 16 / (int)sizeof(T) < SP ? 16 / (int)sizeof(T) : SP;
+  static constexpr int NV = (RL >= 4 ? 16 : 4 * RL) * SP / VE;
+};
+// VE elements of a row from element n on (of `len`), one by one when they cannot be
+// loaded at once.
+template <typename T, int VE>
+__device__ __forceinline__ uint4 load_row16(const T* p, int n, int len, bool vec) {
+  if (VE * sizeof(T) == 16 && vec) return __ldg(reinterpret_cast<const uint4*>(p + n));
+  uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < VE; ++i)
+    if (n + i < len) {
+      if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(__ldg(p + n + i));
+      else v[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + n + i) << (16 * (i % 2));
+    }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// .. to shared memory as floats.
+template <typename T, int VE>
+__device__ __forceinline__ void put_row16(float* o, uint4 q) {
+  float4* p = reinterpret_cast<float4*>(o);
+  if constexpr (sizeof(T) == 4) {
+    p[0] = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
+  } else {
+    p[0] = make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                       __uint_as_float(q.y & 0xffff0000u));
+    if (VE == 8) p[1] = make_float4(__uint_as_float(q.z << 16), __uint_as_float(q.z & 0xffff0000u), __uint_as_float(q.w << 16),
+                       __uint_as_float(q.w & 0xffff0000u));
+  }
+}
+
+// BYTES (8 or 16) of a register vector to and from shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_vec(void* p, uint4 q) {
+  if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = q;
+  else *reinterpret_cast<uint2*>(p) = make_uint2(q.x, q.y);
+}
+template <int BYTES>
+__device__ __forceinline__ uint4 get_vec(const void* p) {
+  if constexpr (BYTES == 16) return *reinterpret_cast<const uint4*>(p);
+  const uint2 q = *reinterpret_cast<const uint2*>(p);
+  return make_uint4(q.x, q.y, 0u, 0u);
+}
+
+// Asynchronous copy of CH (8 or 16) bytes to shared memory; only the first `bytes`
+// of them are read, the rest become zero.
+template <int CH>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  if constexpr (CH == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+template <typename T>
+__device__ __forceinline__ void store2(T* p, float2 v) {
+  if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float2*>(p) = v;
+  else *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
 template <typename T>
 __device__ __forceinline__ void store2(T* p, float2 v, bool vec, bool ok0, bool ok1) {
   if constexpr (std::is_same<T, float>::value) {
@@ -168,19 +246,19 @@ __device__ __forceinline__ float rcp_approx(float y) {   // about 1 ulp; 1 / inf
 // polynomial of degree 8, fitted here by Remez's exchange for least relative
 // error (3e-8; 1.7e-7 with the rounding of its fp32 steps), so that tiny steps
 // (v << 0) keep their relative accuracy.  e_out = e^{-|v|}.
-__device__ __forceinline__ float softplus(float v, float& e_out) {
-  const float e = sm100::ex2_fast(-sm100::kLog2e * fabsf(v));
-  float p = 0.00523269409f;
-  p = fmaf(p, e, -0.0295052379f);
-  p = fmaf(p, e, 0.0782259554f);
-  p = fmaf(p, e, -0.136632457f);
-  p = fmaf(p, e, 0.191060066f);
-  p = fmaf(p, e, -0.24842982f);
-  p = fmaf(p, e, 0.333190978f);
-  p = fmaf(p, e, -0.499994934f);
-  p = fmaf(p, e, 0.99999994f);
+__device__ __forceinline__ float2 softplus2(float2 v, float2& e_out) {
+  const float2 e = make_float2(sm100::ex2_fast(-sm100::kLog2e * fabsf(v.x)), sm100::ex2_fast(-sm100::kLog2e * fabsf(v.y)));
+  constexpr float k[9] = {0.00523269409f, -0.0295052379f, 0.0782259554f, -0.136632457f, 0.191060066f,
+                          -0.24842982f, 0.333190978f, -0.499994934f, 0.99999994f};
+  float2 p = make_float2(k[0], k[0]);
+#pragma unroll
+  for (int i = 1; i < 9; ++i) p = __ffma2_rn(p, e, make_float2(k[i], k[i]));
   e_out = e;
-  return fmaxf(v, 0.f) + p * e;
+  return __ffma2_rn(p, e, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+__device__ __forceinline__ float softplus(float v) {
+  float2 e;
+  return softplus2(make_float2(v, v), e).x;
 }
 
 // sigmoid(v)
@@ -201,7 +279,6 @@ struct Lanes {
   static constexpr int TPL = RL >= 4 ? 1 : 4 / RL;    // tokens of a group a lane finishes
   static constexpr int TT = RL >= 4 ? 16 : 4 * RL;    // tokens a tile: four a lane
   static constexpr int NG = TT / 4;
-  static constexpr int NPB = (TT * SP + 63) / 64;     // pairs of B (or C) a lane stages
   int lane, chl, sl, own;
   bool dup;   // another lane finishes the same tokens
   __device__ __forceinline__ Lanes() {
@@ -244,7 +321,36 @@ __device__ __forceinline__ void reduce_states(float (&v)[4 * NV], int lane) {
   }
 }
 
+// Bytes of an asynchronous copy of a row of a warp's channels, and of a group's states.
+template <typename T, int RL>
+struct Chunks {
+  static constexpr int ROW = 64 / RL * (int)sizeof(T), X = ROW < 16 ? ROW : 16;
+  static constexpr int SROW = 4 * RL * (int)sizeof(T), B = SROW < 16 ? SROW : 16;
+};
+inline int chunk_x(int RL, int es) { return 64 / RL * es < 16 ? 64 / RL * es : 16; }
+inline int chunk_b(int RL, int es) { return 4 * RL * es < 16 ? 4 * RL * es : 16; }
+
+// Rows t0 .. of a tile from a tensor (`first` its row 0, `stride` bytes a row) to
+// dst[TT][ROW bytes]: `valid` bytes of a row exist, rows from `len` on become zero.
+template <int TT, int ROW, int CH>
+__device__ __forceinline__ void copy_rows(char* dst, const char* first, int stride, int t0, int len, int valid, int lane) {
+  constexpr int PER = ROW / CH, N = TT * PER;
+#pragma unroll
+  for (int i = 0; i < (N + 31) / 32; ++i) {
+    const int q = lane + 32 * i, t = q / PER, o = q % PER * CH;
+    if (N % 32 == 0 || q < N) {
+      int bytes = t0 + t < len ? min(valid - o, CH) : 0;
+      if (bytes < 0) bytes = 0;
+      copy_async<CH>(dst + q * CH, bytes > 0 ? first + (int64_t)(t0 + t) * stride + o : first, bytes);
+    }
+  }
+}
+
 // Host side ---------------------------------------------------------------
+
+inline bool aligned_rows(const void* p, int64_t stride, size_t to) {
+  return reinterpret_cast<uintptr_t>(p) % to == 0 && stride % (int64_t)to == 0;
+}
 
 inline int lanes_for(int S) { return S <= 4 ? 1 : S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16; }
 

@@ -81,27 +81,29 @@ __global__ void __launch_bounds__(128) scan_rev_kernel(const BwdArgs b) {
     q[c][0] = q[c][1] = make_float2(0.f, 0.f);
   }
   const float2 bias = make_float2(a.bias && ok0 ? a.bias[d] : 0.f, a.bias && ok1 ? a.bias[d + 1] : 0.f);
-  const T* pd = static_cast<const T*>(a.dl) + u.tok0 * a.ldd + d;
-  const T* pz = a.z ? static_cast<const T*>(a.z) + u.tok0 * a.ldz + d : nullptr;
+  const T* pd = reinterpret_cast<const T*>(static_cast<const char*>(a.dl) + u.tok0 * a.bd) + d;
+  const T* pz = a.z ? reinterpret_cast<const T*>(static_cast<const char*>(a.z) + u.tok0 * a.bz) + d : nullptr;
   const T* pg = static_cast<const T*>(b.dout) + u.tok0 * a.D + d;
-  const T* pC = static_cast<const T*>(a.C) + u.tok0 * a.ldc + g * a.S;
-  Raw2<T> rd[4], rz[4], rg[4], rC[L::NPB];
+  const T* pC = reinterpret_cast<const T*>(static_cast<const char*>(a.C) + u.tok0 * a.bc) + g * a.S;
+  constexpr int VE = RowVec<T, RL>::VE, NV = RowVec<T, RL>::NV, NPV = (NV + 31) / 32;
+  Raw2<T> rd[4], rz[4], rg[4];
+  uint4 rC[NPV];
   auto load_tile = [&](int t0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int t = t0 + ln.token(k);
       rd[k].zero(), rz[k].zero(), rg[k].zero();
       if (t < u.len && ok0) {
-        rd[k].load(pd + t * a.ldd, a.vd, ok0, ok1);
+        rd[k].load(row(pd, t, a.bd), a.vin, ok0, ok1);
         rg[k].load(pg + (int64_t)t * a.D, b.vg, ok0, ok1);
-        if (pz) rz[k].load(pz + t * a.ldz, a.vz, ok0, ok1);
+        if (pz) rz[k].load(row(pz, t, a.bz), a.vin, ok0, ok1);
       }
     }
 #pragma unroll
-    for (int i = 0; i < L::NPB; ++i) {
-      const int p = ln.lane + 32 * i, t = t0 + p / (L::SP / 2), n = 2 * (p % (L::SP / 2));
-      rC[i].zero();
-      if (p < L::TT * L::SP / 2 && t < u.len && n < a.S) rC[i].load(pC + t * a.ldc + n, a.vc, true, n + 1 < a.S);
+    for (int i = 0; i < NPV; ++i) {
+      const int p = (ln.lane + 32 * i) * VE, t = t0 + p / L::SP, n = p % L::SP;
+      rC[i] = make_uint4(0u, 0u, 0u, 0u);
+      if ((NV % 32 == 0 || ln.lane + 32 * i < NV) && t < u.len) rC[i] = load_row16<T, VE>(row(pC, t, a.bc), n, a.S, a.vbc);
     }
   };
   float2 dts = make_float2(0.f, 0.f);
@@ -114,8 +116,8 @@ __global__ void __launch_bounds__(128) scan_rev_kernel(const BwdArgs b) {
       float2 dt = rd[k].f();
       dt.x += bias.x, dt.y += bias.y;
       if (a.softplus) {
-        float e;
-        dt.x = softplus(dt.x, e), dt.y = softplus(dt.y, e);
+        float2 e;
+        dt = softplus2(dt, e);
       }
       if (t0 + ln.token(k) >= u.len) dt = make_float2(0.f, 0.f);
       dts.x += dt.x, dts.y += dt.y;
@@ -123,10 +125,8 @@ __global__ void __launch_bounds__(128) scan_rev_kernel(const BwdArgs b) {
       if (!ln.dup) sdt[w][ln.token(k)][ln.chl] = make_float4(dt.x, dy.x, dt.y, dy.y);
     }
 #pragma unroll
-    for (int i = 0; i < L::NPB; ++i) {
-      const int p = ln.lane + 32 * i, t = p / (L::SP / 2), n = 2 * (p % (L::SP / 2));
-      if (p < L::TT * L::SP / 2) *reinterpret_cast<float2*>(&sC[w][t][n]) = rC[i].f();
-    }
+    for (int i = 0; i < NPV; ++i)
+      if (NV % 32 == 0 || ln.lane + 32 * i < NV) put_row16<T, VE>(&sC[w][0][0] + (ln.lane + 32 * i) * VE, rC[i]);
     __syncwarp();
     if (t0 > 0) load_tile(t0 - L::TT);
 #pragma unroll 4
@@ -175,10 +175,20 @@ __global__ void __launch_bounds__(256) rev_chain_kernel(const BwdArgs b) {
   const int64_t u1 = a.cu ? a.seg0[n + 1] : u0 + a.nseg;
   const float r = a.A[i] * sm100::kLog2e;
   float q = b.dht ? b.dht[n * DS + i] : 0.f;
-  for (int64_t u = u1 - 1; u > u0; --u) {
-    const float loc = b.qseg[u * DS + i], dt = b.qdt[u * a.D + d];
-    b.qseg[u * DS + i] = q;
-    q = fmaf(sm100::ex2_fast(r * dt), q, loc);
+  for (int64_t u = u1 - 1; u > u0; u -= 8) {   // eight segments' loads at a time
+    float loc[8], dt[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = u - k > u0;
+      loc[k] = in ? b.qseg[(u - k) * DS + i] : 0.f;
+      dt[k] = in ? b.qdt[(u - k) * a.D + d] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (u - k <= u0) break;
+      b.qseg[(u - k) * DS + i] = q;
+      q = fmaf(sm100::ex2_fast(r * dt[k]), q, loc[k]);
+    }
   }
   b.qseg[u0 * DS + i] = q;
 }
@@ -252,12 +262,12 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
 
   Unit u;
   for (int64_t un = blockIdx.x; un < b.units && unit_of(a, un, u); un += b.slots) {
-    const T* px = static_cast<const T*>(a.x) + u.tok0 * a.ldx + d;
-    const T* pd = static_cast<const T*>(a.dl) + u.tok0 * a.ldd + d;
-    const T* pz = gate ? static_cast<const T*>(a.z) + u.tok0 * a.ldz + d : nullptr;
+    const T* px = reinterpret_cast<const T*>(static_cast<const char*>(a.x) + u.tok0 * a.bx) + d;
+    const T* pd = reinterpret_cast<const T*>(static_cast<const char*>(a.dl) + u.tok0 * a.bd) + d;
+    const T* pz = gate ? reinterpret_cast<const T*>(static_cast<const char*>(a.z) + u.tok0 * a.bz) + d : nullptr;
     const T* pg = static_cast<const T*>(b.dout) + u.tok0 * a.D + d;
-    const T* pB = static_cast<const T*>(a.B) + u.tok0 * a.ldb + g * a.S;
-    const T* pC = static_cast<const T*>(a.C) + u.tok0 * a.ldc + g * a.S;
+    const T* pB = reinterpret_cast<const T*>(static_cast<const char*>(a.B) + u.tok0 * a.bb) + g * a.S;
+    const T* pC = reinterpret_cast<const T*>(static_cast<const char*>(a.C) + u.tok0 * a.bc) + g * a.S;
 
     float2 h[2][2], q[2][2];   // state; a q from the right
 #pragma unroll
@@ -285,23 +295,23 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
         rx.zero(), rd.zero(), rz.zero(), rg.zero();
         const bool in = t < u.len && ok0;
         if (in) {
-          rx.load(px + t * a.ldx, a.vx, ok0, ok1);
-          rd.load(pd + t * a.ldd, a.vd, ok0, ok1);
+          rx.load(row(px, t, a.bx), a.vin, ok0, ok1);
+          rd.load(row(pd, t, a.bd), a.vin, ok0, ok1);
           if (back) {
             rg.load(pg + (int64_t)t * a.D, b.vg, ok0, ok1);
-            if (pz) rz.load(pz + t * a.ldz, a.vz, ok0, ok1);
+            if (pz) rz.load(row(pz, t, a.bz), a.vin, ok0, ok1);
           }
         }
         const float2 x = rx.f();
         float2 dt = rd.f();
         dt.x += bias.x, dt.y += bias.y;
         if (a.softplus) {
-          float ex, ey;
+          float2 e;
           const float2 v = dt;
-          dt.x = softplus(v.x, ex), dt.y = softplus(v.y, ey);
+          dt = softplus2(v, e);
           // sigmoid(v), from e^{-|v|}
-          if (back) sp[k] = make_float2((v.x >= 0.f ? 1.f : ex) * rcp_approx(1.f + ex),
-                                        (v.y >= 0.f ? 1.f : ey) * rcp_approx(1.f + ey));
+          if (back) sp[k] = make_float2((v.x >= 0.f ? 1.f : e.x) * rcp_approx(1.f + e.x),
+                                        (v.y >= 0.f ? 1.f : e.y) * rcp_approx(1.f + e.y));
         } else if (back) {
           sp[k] = make_float2(1.f, 1.f);
         }
@@ -313,16 +323,16 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
         }
       }
       // B (and C) of the CTA's group
-      for (int p = threadIdx.x; p < L::TT * L::SP / 2; p += NT) {
-        const int tk = p / (L::SP / 2), n = 2 * (p % (L::SP / 2)), t = t0 + tk;
-        Raw2<T> rb, rc;
-        rb.zero(), rc.zero();
-        if (t < u.len && n < a.S) {
-          rb.load(pB + t * a.ldb + n, a.vb, true, n + 1 < a.S);
-          if (back) rc.load(pC + t * a.ldc + n, a.vc, true, n + 1 < a.S);
+      constexpr int VE = RowVec<T, RL>::VE;
+      for (int i = threadIdx.x; i < RowVec<T, RL>::NV; i += NT) {
+        const int p = i * VE, t = t0 + p / L::SP, n = p % L::SP;
+        uint4 rb = make_uint4(0u, 0u, 0u, 0u), rc = rb;
+        if (t < u.len) {
+          rb = load_row16<T, VE>(row(pB, t, a.bb), n, a.S, a.vbc);
+          if (back) rc = load_row16<T, VE>(row(pC, t, a.bc), n, a.S, a.vbc);
         }
-        *reinterpret_cast<float2*>(&sm.B[tk][n]) = rb.f();
-        if (back) *reinterpret_cast<float2*>(&sm.C[tk][n]) = rc.f();
+        put_row16<T, VE>(&sm.B[0][0] + p, rb);
+        if (back) put_row16<T, VE>(&sm.C[0][0] + p, rc);
       }
     };
     // one token of the recurrence
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
             dbias.x += dd.x, dbias.y += dd.y;
             if (gate) {
               Raw2<T> rz, rg;
-              rz.load(pz + t * a.ldz, a.vz, ok0, ok1);
+              rz.load(row(pz, t, a.bz), a.vin, ok0, ok1);
               rg.load(pg + (int64_t)t * a.D, b.vg, ok0, ok1);
               const float2 z = rz.f(), gr2 = rg.f();
               const float s0 = sigmoid(z.x), s1 = sigmoid(z.y);

@@ -455,7 +455,7 @@ gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, co
  *
  * Problem description.
  *   B, T, N, varlen : as for gdn_problem (N = B for equal lengths)
- *   D, S, G  : channels (at most 131072), states a channel (at most 64) and
+ *   D, S, G  : channels (at most 65536), states a channel (at most 64) and
  *              groups of channels that share B and C; D % G == 0
  *   dt       : dtype of x, delta, z, B, C, y and of their gradients
  *   softplus : 0 or 1, as above

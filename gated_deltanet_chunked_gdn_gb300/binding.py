@@ -478,6 +478,13 @@ def _address(t: Optional[torch.Tensor]) -> int:
     return t.data_ptr() if t is not None else 0
 
 
+try:   # the current stream's handle without a Stream object around it
+    _current_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _current_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _row_stride(name: str, t: torch.Tensor, row: int) -> int:
     """Elements from one token's row of t [B, T, ...] to the next; the rows themselves contiguous, the
     sequences of a batch one after the other at the same stride."""
@@ -494,9 +501,35 @@ def _row_stride(name: str, t: torch.Tensor, row: int) -> int:
     return ld
 
 
-def _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32, others=()):
+def _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32=(), others=()):
     """Checks of a scan's tensors and its problem.  fp32: (name, tensor, shape) that must be contiguous float32;
     others: (name, tensor) that must be like x and contiguous."""
+    # the usual call, all rows contiguous, in one expression: a decode step's launch is shorter than its checks
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    if len(shape) == 3 and B.dim() == 4 and x.is_cuda and dtype in DTYPES:
+        nb, T, d = shape
+        _, _, G, S = bshape = B.shape
+        f32 = torch.float32
+        if (x.is_contiguous() and delta.is_contiguous() and B.is_contiguous() and C.is_contiguous()
+                and A.is_contiguous() and delta.shape == shape and C.shape == bshape and bshape[0] == nb
+                and bshape[1] == T and A.shape == (d, S) and delta.dtype is dtype and B.dtype is dtype
+                and C.dtype is dtype and A.dtype is f32 and delta.device == dev and B.device == dev
+                and C.device == dev and A.device == dev
+                and (z is None or (z.shape == shape and z.dtype is dtype and z.device == dev and z.is_contiguous()))
+                and (D is None or (D.shape == (d,) and D.dtype is f32 and D.device == dev and D.is_contiguous()))
+                and (dt_bias is None or (dt_bias.shape == (d,) and dt_bias.dtype is f32 and dt_bias.device == dev
+                                         and dt_bias.is_contiguous()))):
+            for _, t, want in fp32:
+                if t is not None and (t.dtype is not f32 or t.device != dev or t.shape != want
+                                      or not t.is_contiguous()):
+                    break
+            else:
+                if cu_seqlens is None and not others:
+                    return ScanProblem(nb, T, nb, d, S, G, DTYPES[dtype], 0, 1 if softplus else 0)
+    return _scan_problem_checked(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32, others)
+
+
+def _scan_problem_checked(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32, others):
     dtype, shape = x.dtype, x.shape
     if dtype not in DTYPES:
         raise ValueError("x must be float32 or bfloat16")
@@ -509,17 +542,18 @@ def _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32, 
     if C.shape != B.shape or B.shape[:2] != shape[:2] or A.shape != (d, S):
         raise ValueError("B and C must be [B, T, G, S] and A [D, S]")
     for name, t in (("x", x), ("delta", delta), ("B", B), ("C", C), ("z", z), *others):
-        if t is not None and (t.dtype != dtype or not t.is_cuda):
-            raise ValueError(f"{name} must be a CUDA tensor with the dtype of x")
+        if t is not None and (t.dtype != dtype or not t.is_cuda or t.device != x.device):
+            raise ValueError(f"{name} must be a CUDA tensor with the dtype and device of x")
     for name, t in others:
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous with the shape of x")
     for name, t, want in (("A", A, (d, S)), ("D", D, (d,)), ("dt_bias", dt_bias, (d,)), *fp32):
-        if t is not None and (t.dtype != torch.float32 or t.shape != want or not t.is_cuda or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.float32 or t.shape != want or t.device != x.device
+                              or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {tuple(want)}")
     N = nb
     if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous():
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device or not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor")
         N = cu_seqlens.numel() - 1
     gs = G * S
@@ -539,12 +573,12 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
     """Selective state space scan.  x, delta, z [B, T, D], B and C [B, T, G, S] (one dtype, bf16 or fp32; rows
     may be slices of wider rows), A [D, S], D and dt_bias [D], h0 [N, D, S] fp32.  Returns (y, ht); ht is None
     when ``output_final_state`` is False."""
-    lib = load()
+    lib = _lib or load()
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (("h0", h0, state), ("ht", ht, state)),
                       (("y", y),) if y is not None else ())
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if ht is None and output_final_state:
         ht = torch.empty(state, dtype=torch.float32, device=x.device)
     if workspace is None:
@@ -552,7 +586,7 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
         if need == 0:
             raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_selective_scan_fwd_workspace_size")
         workspace = _alloc_ws(need, x.device)
-    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_selective_scan_fwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                     _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
                                     y.data_ptr(), _address(ht), workspace.data_ptr(), workspace.numel(), s)
@@ -577,16 +611,16 @@ def gdn_selective_scan_get_device_status(p: ScanProblem, workspace, stream=None)
 def gdn_selective_scan_step(x, delta, A, B, C, state, D=None, z=None, dt_bias=None, softplus: bool = True,
                             state_indices=None, cu_seqlens=None, y=None, stream=None):
     """The scan's tokens on a state pool (decode).  ``state`` [slots, D, S] fp32 is updated in place; returns y."""
-    lib = load()
+    lib = _lib or load()
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
                       (("state", state, (state.shape[0], x.shape[-1], A.shape[-1])),),
                       (("y", y),) if y is not None else ())
-    if state_indices is not None and (state_indices.dtype != torch.int32 or not state_indices.is_cuda
+    if state_indices is not None and (state_indices.dtype is not torch.int32 or state_indices.device != x.device
                                       or not state_indices.is_contiguous() or state_indices.numel() != p.N):
         raise ValueError("state_indices must be a contiguous int32 CUDA tensor, one slot a sequence")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_selective_scan_step(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                      _address(D), _address(z), _address(dt_bias), state.data_ptr(),
                                      _address(state_indices), state.shape[0], _address(cu_seqlens), y.data_ptr(), s)
@@ -606,7 +640,7 @@ def gdn_selective_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None
     fp32 or None).  Returns dx, ddelta, dB, dC, dz (dtype of x), dA, dD, ddt_bias, dh0 (fp32) and the workspace
     under "workspace"; dD, dz and ddt_bias are None where the input is, dh0 unless ``want_dh0`` (by default: h0 is
     given)."""
-    lib = load()
+    lib = _lib or load()
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
                       (("h0", h0, state), ("dht", dht, state)), (("dout", dout),))
@@ -625,7 +659,7 @@ def gdn_selective_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None
            "dz": torch.empty(x.shape, **like) if z is not None else None,
            "ddt_bias": torch.empty(dt_bias.shape, **f32) if dt_bias is not None else None,
            "dh0": torch.empty(state, **f32) if want_dh0 else None}
-    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_selective_scan_bwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                     _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
                                     dout.data_ptr(), _address(dht), *(_address(t) for t in out.values()),
@@ -643,7 +677,7 @@ def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial
     None).  x, dout [B, T, D] and initial_state [N, W-1, D] share a dtype; weight [D, W], bias [D] fp32.  Returns
     dx, dweight, dbias, dinitial_state and the workspace under "workspace"; dbias is None without bias,
     dinitial_state unless ``want_dinitial_state`` (by default: initial_state is given)."""
-    lib = load()
+    lib = _lib or load()
     if x.dtype not in DTYPES or x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
         raise ValueError("x must be float32 or bfloat16 [B, T, D] and weight [D, W]")
     B, T, D = x.shape
@@ -670,7 +704,7 @@ def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial
     out = {"dx": torch.empty_like(x), "dweight": torch.empty((D, W), **f32),
            "dbias": torch.empty((D,), **f32) if bias is not None else None,
            "dinitial_state": torch.empty(state, dtype=x.dtype, device=x.device) if want_dinitial_state else None}
-    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_causal_conv1d_bwd(x.data_ptr(), weight.data_ptr(), _address(bias), W, _address(initial_state),
                                    _address(cu_seqlens), N, B, T, D, DTYPES[x.dtype], ACTIVATIONS[activation],
                                    dout.data_ptr(), _address(dfinal_state), *(_address(t) for t in out.values()),
@@ -685,30 +719,33 @@ def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None
     """y = x W^T + bias for 4-bit weights W [N, K] = (code - zero) * scale.  x [..., K] (bf16 or fp32; two
     dimensions may have any row stride), qweight [N, K / 2] uint8 (code 2j in byte j's low half), scales
     [N, K / group] (bf16 or fp32), zeros [N, K / group] uint8 or None (8), bias [N] fp32.  Returns y [..., N]."""
-    lib = load()
-    N, half = qweight.shape
+    lib = _lib or load()
+    N, half = qshape = qweight.shape
     K, groups = 2 * half, scales.shape[1]
-    if x.dtype not in DTYPES or scales.dtype not in DTYPES:
+    dtype, sdt, dev = x.dtype, scales.dtype, x.device
+    if dtype not in DTYPES or sdt not in DTYPES:
         raise ValueError("x and scales must be float32 or bfloat16")
     if x.shape[-1] != K or not x.is_cuda or groups == 0 or K % groups != 0:
         raise ValueError("x must be a CUDA tensor of shape [..., K] and scales [N, K / group]")
-    for name, t, dtype, shape in (("qweight", qweight, torch.uint8, (N, half)),
-                                  ("scales", scales, scales.dtype, (N, groups)),
-                                  ("zeros", zeros, torch.uint8, (N, groups)), ("bias", bias, torch.float32, (N,))):
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.shape != shape):
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}")
+    if not (qweight.dtype is torch.uint8 and qweight.device == dev and qweight.is_contiguous()
+            and scales.shape[0] == N and scales.device == dev and scales.is_contiguous()
+            and (zeros is None or (zeros.dtype is torch.uint8 and zeros.shape == scales.shape and zeros.device == dev
+                                   and zeros.is_contiguous()))
+            and (bias is None or (bias.dtype is torch.float32 and bias.shape == (N,) and bias.device == dev
+                                  and bias.is_contiguous()))):
+        raise ValueError(f"qweight (uint8 {tuple(qshape)}), scales and zeros (uint8) [N, K / group] and bias (float32 "
+                         "[N]) must be contiguous and on the device of x")
     if x.is_contiguous():
         M, ld = x.numel() // K, K
     elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K:
         M, ld = x.shape[0], x.stride(0)
     else:
         raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
-    want = (*x.shape[:-1], N)
     if y is None:
-        y = torch.empty(want, dtype=x.dtype, device=x.device)
-    elif y.shape != want or y.dtype != x.dtype or not y.is_cuda or not y.is_contiguous():
+        y = x.new_empty((*x.shape[:-1], N))
+    elif y.shape != (*x.shape[:-1], N) or y.dtype != dtype or y.device != dev or not y.is_contiguous():
         raise ValueError("y must be a contiguous CUDA tensor [..., N] with the dtype of x")
-    s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
+    s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_q4_matvec(x.data_ptr(), ld, qweight.data_ptr(), scales.data_ptr(), DTYPES[scales.dtype],
                            _address(zeros), _address(bias), M, N, K, K // groups, DTYPES[x.dtype], y.data_ptr(), s)
     if st:

@@ -429,6 +429,7 @@ gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, co
                          void* y, void* stream) {
   if ((dt != GDN_F32 && dt != GDN_BF16) || (sdt != GDN_F32 && sdt != GDN_BF16)) return GDN_ERR_INVALID_ARG;
   if (M < 0 || N <= 0 || K <= 0 || group <= 0 || group % 32 != 0 || K % group != 0) return GDN_ERR_INVALID_ARG;
+  if (K > (1 << 20)) return GDN_ERR_UNSUPPORTED;
   if (ld_x == 0) ld_x = K;
   if (ld_x < K || !qweight || !aligned(qweight, 16) || !scales) return GDN_ERR_INVALID_ARG;
   const size_t es = dt == GDN_F32 ? 4 : 2;

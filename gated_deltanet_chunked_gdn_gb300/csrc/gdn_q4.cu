@@ -4,27 +4,34 @@
 //
 // Codes are read as they are stored (rows of K nibbles) and become tensor-core
 // operands in registers: a nibble j in the low bits of a bf16's mantissa on top of
-// 1/2 is 1/2 + j/256, exactly, so two codes take one AND-OR (and a shift), and one
-// packed subtraction of 1/2 + zero/256 leaves (code - zero)/256, again exactly.
-// mma.sync m16n8k16 then multiplies 16 weight rows by 8 columns of x with fp32 sums;
-// 256 times the group's scale multiplies the fp32 sum, so no weight is ever rounded
-// (and codes below 1 keep large fp32 x from overflowing before the scale).  mma.sync
-// and not tcgen05: the weights are used once, and the way through shared memory
-// and the accumulators' way through tensor memory would cost more than the
-// products, which are far below the tensor units' rate; what bounds the loop beside
-// HBM is turning codes into operands.
+// 1/2 is 1/2 + j/256, exactly, so two neighbouring codes take a byte permutation and
+// one AND-OR, and one packed subtraction of 1/2 + zero/256 leaves (code - zero)/256,
+// again exactly.  mma.sync m16n8k16 then multiplies 16 weight rows by 8 columns of x
+// with fp32 sums; 256 times the group's scale multiplies the fp32 sum, so no weight is
+// ever rounded (and codes below 1 keep large fp32 x from overflowing before the scale).
+// mma.sync and not tcgen05: for a few rows the weights are used once, and their way as
+// bf16 through shared memory would cost more than the products; what bounds the loop
+// beside HBM is turning codes into operands (about 13 instructions for eight).  From 16
+// rows on mma.sync's own rate does.
 //
-// The k order inside an mma is free as long as both operands share it: lane c of a
-// row's four takes WL consecutive words (8 WL codes), 16 bytes a load when the
-// group size allows (all lanes of an mma have to be in one group), and the four
-// code pairs that a word's shifts yield are (0,4), (1,5), (2,6), (3,7), so x's words
-// are permuted to match.
+// The k order inside an mma is free as long as both operands share it, but all its
+// products have to be of one group.  A lane loads 16 bytes (32 codes) of a row, the
+// four lanes of a row 128 codes (a block).  Groups of 64 or 32 are smaller than that:
+// the four lanes exchange words (2 or 4 shuffles a 16 bytes) so that each mma's words
+// come from one group, which costs less than narrower loads, whose requests touch a
+// row's line for 16 bytes only.
 //
-// fp32 x: each value is split into three bf16 (24 bits in all), which take three of
-// the mma's columns; the three sums are added at the end, so fp32 accuracy is kept.
+// Weights and x come by asynchronous copies into rings of blocks; every lane
+// copies the weights that it reads itself.  x stands in pieces of eight values,
+// swizzled so that the operands' reads meet no bank twice.  fp32 x (and rows that are
+// not aligned) go through registers: each fp32 value is cut into three bf16 (24 bits
+// in all), which take three of the mma's columns; the three sums are added at the end,
+// so fp32 accuracy is kept.
 //
-// A CTA computes 16 rows; its eight warps split K and add up through shared
-// memory in a fixed order.
+// A CTA's eight warps are RW rows of warps over 16 MT weight rows each times 8 / RW
+// shares of K, which add up through shared memory in a fixed order.  The warps of a
+// share use one copy of x: many columns of x would otherwise be brought and read once a
+// 16 weight rows, at four times their bytes.
 #include <type_traits>
 
 #include "gdn_internal.h"
@@ -33,7 +40,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kBlock = 128;   // codes of a row that its four lanes load at once
 
 struct Q4Args {
   const void* x;
@@ -43,7 +50,9 @@ struct Q4Args {
   const float* bias;
   void* y;
   int64_t ldx;
-  int M, N, K, group;
+  int M, N, K, groups;   // groups a row
+  unsigned gmagic;       // 2^32 / (group / 32), rounded up (0 for 1): a code's group by a multiplication
+  bool vec;              // rows of x in whole 16-byte pieces
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -54,195 +63,380 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four code pairs of a word, less their zero point, over 256 (off: 1/2 + zero/256).
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The codes of a word as four pairs of neighbours, less their zero point, over 256
+// (off: 1/2 + zero/256).
 __device__ __forceinline__ void decode(uint32_t w, __nv_bfloat162 off, uint32_t (&p)[4]) {
+  const uint32_t h = w >> 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | 0x3f003f00u;
+    // byte j of w (its low nibble is the first code) and of h (the second)
+    uint32_t v = (__byte_perm(w, h, 0x0400 + 0x1111 * j) & 0x000f000fu) | 0x3f003f00u;
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
     p[j] = *reinterpret_cast<const uint32_t*>(&d);
   }
 }
 
-template <int WL> struct Words;
-template <> struct Words<4> {
-  uint4 v;
-  __device__ __forceinline__ void load(const uint8_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ uint32_t at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-};
-template <> struct Words<2> {
-  uint2 v;
-  __device__ __forceinline__ void load(const uint8_t* p) { v = __ldcs(reinterpret_cast<const uint2*>(p)); }
-  __device__ __forceinline__ uint32_t at(int i) const { return i == 0 ? v.x : v.y; }
-};
-template <> struct Words<1> {
-  uint32_t v;
-  __device__ __forceinline__ void load(const uint8_t* p) { v = __ldcs(reinterpret_cast<const uint32_t*>(p)); }
-  __device__ __forceinline__ uint32_t at(int) const { return v; }
-};
-
 // Columns of the mma that a row of x takes.
 template <typename T> constexpr int kParts = std::is_same<T, float>::value ? 3 : 1;
 
-// The x operand of a word's eight codes, for one column: pairs (0,4), (1,5), (2,6), (3,7).
-__device__ __forceinline__ void load_x(const __nv_bfloat16* p, bool vec, int, uint32_t (&b)[4]) {
-  uint32_t v[4];
-  if (vec) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-  } else {
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+// Eight values of x for one column, as loaded.
+template <typename T> struct X8;
+template <> struct X8<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec) {
+    if (vec) {
+      q = __ldg(reinterpret_cast<const uint4*>(p));
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      uint32_t v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldg(h + 2 * i) | ((uint32_t)__ldg(h + 2 * i + 1) << 16);
+      for (int i = 0; i < 4; ++i) v[i] = __ldg(h + 2 * i) | ((uint32_t)__ldg(h + 2 * i + 1) << 16);
+      q = make_uint4(v[0], v[1], v[2], v[3]);
+    }
   }
-  b[0] = __byte_perm(v[0], v[2], 0x5410), b[1] = __byte_perm(v[0], v[2], 0x7632);
-  b[2] = __byte_perm(v[1], v[3], 0x5410), b[3] = __byte_perm(v[1], v[3], 0x7632);
-}
-__device__ __forceinline__ void load_x(const float* p, bool vec, int part, uint32_t (&b)[4]) {
+  __device__ __forceinline__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint4 operand(int) const { return q; }
+};
+template <> struct X8<float> {
   float f[8];
-  if (vec) {
-    const float4 q = __ldg(reinterpret_cast<const float4*>(p)), r = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w, f[4] = r.x, f[5] = r.y, f[6] = r.z, f[7] = r.w;
-  } else {
+  __device__ __forceinline__ void load(const float* p, bool vec) {
+    if (vec) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(p)), r = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w, f[4] = r.x, f[5] = r.y, f[6] = r.z, f[7] = r.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __ldg(p + i);
+      for (int i = 0; i < 8; ++i) f[i] = __ldg(p + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
   }
   // the first, second or third 8 bits (cut, not rounded, so that none overflows; an
   // infinity has no rest)
+  __device__ __forceinline__ uint4 operand(int part) const {
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float hi = __uint_as_float(__float_as_uint(f[i]) & 0xffff0000u);
-    const float r1 = hi == f[i] ? 0.f : f[i] - hi;
-    const float mid = __uint_as_float(__float_as_uint(r1) & 0xffff0000u);
-    f[i] = part == 0 ? hi : part == 1 ? mid : r1 - mid;
+    for (int i = 0; i < 8; ++i) {
+      const float hi = __uint_as_float(__float_as_uint(f[i]) & 0xffff0000u);
+      const float r1 = hi == f[i] ? 0.f : f[i] - hi;
+      const float mid = __uint_as_float(__float_as_uint(r1) & 0xffff0000u);
+      v[i] = part == 0 ? hi : part == 1 ? mid : r1 - mid;
+    }
+    return make_uint4(sm100::pack_bf16(v[0], v[1]), sm100::pack_bf16(v[2], v[3]), sm100::pack_bf16(v[4], v[5]),
+                      sm100::pack_bf16(v[6], v[7]));
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = sm100::pack_bf16(f[i], f[i + 4]);
-}
+};
 
-// NT: column tiles of 8.  WL: words a lane reads at once.
-template <typename T, typename ST, int NT, int WL>
-__global__ void __launch_bounds__(32 * kWarps) q4_matvec_kernel(const Q4Args a, int m0) {
-  constexpr int KB = 32 * WL;   // codes of a row a step covers
-  constexpr int P = kParts<T>;
-  __shared__ float red[kWarps][16][NT * 8 + 1];
+// NT: column tiles of 8.  MT: tiles of 16 weight rows a warp.  RW: rows of warps, of
+// NW in all.  R: blocks in a ring, one in use, the others on their way.
+template <int NT_, int MT_, int RW_, int NW_, int R_>
+struct Conf {
+  static constexpr int NT = NT_, MT = MT_, RW = RW_, NW = NW_, R = R_;
+  static constexpr int KW = NW / RW, COLS = 8 * NT, ROWS = 16 * MT * RW;
+  static constexpr size_t W = sizeof(uint4) * NW * R * MT * 64;             // rings of weights
+  static constexpr size_t SUM = sizeof(float) * KW * ROWS * (COLS + 1);     // the shares' sums
+  // .. and of x, NCP columns to a piece
+  static constexpr size_t bytes(int ncp) {
+    const size_t b = W + sizeof(uint4) * KW * R * 16 * ncp;
+    return b > SUM ? b : SUM;
+  }
+};
+
+// GM: group size a multiple of 128 (0), 64 (1), 32 (2).  NCP: ncol, the columns there
+// are, rounded up to a power of two (what a piece's columns take in shared memory; the
+// other lanes of an mma read one of these, for columns of the result that nobody
+// stores).  ASYNC: bf16 x in rows of whole 16-byte pieces.
+template <typename T, typename ST, typename F, int GM, int NCP, bool ASYNC>
+__global__ void __launch_bounds__(32 * F::NW) q4_matvec_kernel(const Q4Args a, int m0, int ncol) {
+  constexpr int NT = F::NT, MT = F::MT, RW = F::RW, kRing = F::R;
+  constexpr int P = kParts<T>, KW = F::KW, COLS = F::COLS;
+  constexpr int SLOTS = GM == 0 ? 1 : GM == 1 ? 2 : 4;   // groups a block can meet
+  constexpr int QB = 4 / SLOTS;                          // blocks whose groups a row's four lanes hold
+  extern __shared__ __align__(16) char raw_smem[];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int rw = wp % RW, kw = wp / RW;
   const int r = lane >> 2, c = lane & 3;
-  const int row0 = 16 * blockIdx.x;
-  const int ra = min(row0 + r, a.N - 1), rb = min(row0 + r + 8, a.N - 1);   // past the end: not stored
-  const int64_t rowbytes = a.K / 2, groups = a.K / a.group;
-  const uint8_t* wa = a.w + ra * rowbytes + 4 * WL * c;
-  const uint8_t* wb = a.w + rb * rowbytes + 4 * WL * c;
-  const ST* scale = static_cast<const ST*>(a.scale);
-  const ST* sa = scale + ra * groups;
-  const ST* sb = scale + rb * groups;
-  const uint8_t* za = a.zero ? a.zero + ra * groups : nullptr;
-  const uint8_t* zb = a.zero ? a.zero + rb * groups : nullptr;
-  // this lane's columns of x (the b operand): column lane / 4 of each tile
-  const T* xp[NT];
-  int part[NT];
-  bool has[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int col = 8 * t + r;
-    part[t] = col % P;
-    has[t] = m0 + col / P < a.M;
-    xp[t] = static_cast<const T*>(a.x) + (has[t] ? (int64_t)(m0 + col / P) * a.ldx : 0) + 8 * WL * c;
-  }
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) % 16 == 0) && (a.ldx * sizeof(T)) % 16 == 0;
+  uint4* ring = reinterpret_cast<uint4*>(raw_smem) + wp * (kRing * MT * 64) + lane;   // [kRing][MT][2][32 lanes]
+  uint4* xring = reinterpret_cast<uint4*>(raw_smem + F::W) + kw * (kRing * 16 * NCP);   // [kRing][16 words][NCP]
 
-  const int nb = a.K / KB;
-  const int b0 = (int)((int64_t)nb * wp / kWarps), b1 = (int)((int64_t)nb * (wp + 1) / kWarps);
-  float total[NT][4], acc[NT][4];
+  const int nb = (a.K + kBlock - 1) / kBlock;   // the last block may be short (groups of 32 or 64)
+  const int b0 = (int)((int64_t)nb * kw / KW), b1 = (int)((int64_t)nb * (kw + 1) / KW);
+  const int row0 = 16 * MT * (RW * blockIdx.x + rw);
+  const uint8_t* wsrc[MT][2];   // the next block to fetch
+  int64_t srow[MT][2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) total[t][i] = acc[t][i] = 0.f;
-  const int per = a.group / KB;   // steps a group
-  constexpr int U = NT >= 4 ? 2 : 4;
-  for (int b = b0; b < b1; b += U) {
-    Words<WL> qa[U], qb[U];
-    float fa[U], fb[U];
-    __nv_bfloat162 oa[U], ob[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = min(b + u, b1 - 1);
-      qa[u].load(wa + (int64_t)s * (KB / 2));
-      qb[u].load(wb + (int64_t)s * (KB / 2));
-      const int g = s / per;
-      fa[u] = 256.f * to_f(sa[g]), fb[u] = 256.f * to_f(sb[g]);
-      oa[u] = __float2bfloat162_rn(0.53125f), ob[u] = oa[u];
-      if (za) {
-        oa[u] = __float2bfloat162_rn(fmaf((float)za[g], 0.00390625f, 0.5f));
-        ob[u] = __float2bfloat162_rn(fmaf((float)zb[g], 0.00390625f, 0.5f));
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int row = min(row0 + 16 * t + r + 8 * h, a.N - 1);   // past the end: not stored
+      wsrc[t][h] = a.w + row * (int64_t)(a.K / 2) + (int64_t)b0 * (kBlock / 2) + 16 * c;
+      srow[t][h] = row * (int64_t)a.groups;
     }
+  const ST* scale = static_cast<const ST*>(a.scale);
+
+  // word kc's pieces stand in the order col ^ swz(kc): the reads below take two
+  // neighbouring columns of four words at a time
+  auto swz = [](int kc) { return GM == 0 ? (kc / 4 & 3) * 2 : GM == 1 ? ((kc / 4 & 1) + 2 * (kc / 2 & 1)) * 2 : (kc & 3) * 2; };
+  // x of a block: this lane brings word kcol of columns col0, col0 + 2 RW, ..
+  const int kcol = lane % 16, col0 = 2 * rw + lane / 16, sw = swz(kcol) & (NCP - 1);
+  const T* xsrc = static_cast<const T*>(a.x) + (m0 + col0 / P) * a.ldx + b0 * (int64_t)kBlock + 8 * kcol;
+  auto fetch = [&](int b, int slot) {
+    // (what stands behind the last codes of a short block meets zeros of x)
+    if (b < b1 && b * kBlock + 32 * c < a.K) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b + u >= b1) break;
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int i = 0; i < WL; ++i) {
-        uint32_t pa[4], pb[4];
-        decode(qa[u].at(i), oa[u], pa);
-        decode(qb[u].at(i), ob[u], pb);
+        for (int h = 0; h < 2; ++h) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           sm100::smem_u32(ring + (slot * MT * 2 + t * 2 + h) * 32)),
+                       "l"(wsrc[t][h])
+                       : "memory");
+          wsrc[t][h] += kBlock / 2;
+        }
+    }
+    if (b < b1) {
+      const bool have = b * kBlock + 8 * kcol < a.K;
+      uint4* dst = xring + (slot * 16 + kcol) * NCP;
+      const T* src = xsrc;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          uint32_t xb[4] = {0u, 0u, 0u, 0u};
-          if (has[t]) load_x(xp[t] + (int64_t)(b + u) * KB + 8 * i, vec, part[t], xb);
-          mma_bf16(acc[t], pa[0], pb[0], pa[1], pb[1], xb[0], xb[1]);
-          mma_bf16(acc[t], pa[2], pb[2], pa[3], pb[3], xb[2], xb[3]);
+      for (int j = 0; j < (NCP + 2 * RW - 1) / (2 * RW); ++j) {
+        const int col = col0 + j * 2 * RW;
+        if (col >= ncol) break;
+        if constexpr (ASYNC) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst + (col ^ sw))),
+                       "l"(have ? src : static_cast<const T*>(a.x)), "r"(have ? 16 : 0)
+                       : "memory");
+          src += 2 * RW * a.ldx;
+        } else {
+          X8<T> x;
+          x.zero();
+          if (have) x.load(xsrc + (col / P - col0 / P) * a.ldx, a.vec);
+          dst[col ^ sw] = x.operand(col % P);
         }
       }
-      if ((b + u + 1) % per == 0 || b + u + 1 == b1) {   // the group (or this warp's share of it) ends
+      xsrc += kBlock;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < kRing - 1; ++i) fetch(b0 + i, i);
+
+  // scales (and zero points) of QB blocks from b on: lane c has the c-th group's.  Two
+  // such steps are on their way, as loaded: a conversion would wait for them.
+  float s0[MT][2];      // 256 times the scale
+  uint32_t o0[MT][2];   // 1/2 + zero/256, twice
+  ST s1[MT][2], s2[MT][2];
+  uint8_t z1[MT][2], z2[MT][2];
+  auto load_scales = [&](int b, ST (&sc)[MT][2], uint8_t (&ze)[MT][2]) {
+    // past the end (an empty share's too) some group of the row: x is zero there
+    const int k = max(0, min(b * kBlock + c * (kBlock / SLOTS), a.K - 32));
+    const unsigned g = a.gmagic ? __umulhi((unsigned)k / 32, a.gmagic) : (unsigned)k / 32;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          total[t][0] = fmaf(fa[u], acc[t][0], total[t][0]);
-          total[t][1] = fmaf(fa[u], acc[t][1], total[t][1]);
-          total[t][2] = fmaf(fb[u], acc[t][2], total[t][2]);
-          total[t][3] = fmaf(fb[u], acc[t][3], total[t][3]);
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        sc[t][h] = scale[srow[t][h] + g];
+        ze[t][h] = a.zero ? a.zero[srow[t][h] + g] : 8;
+      }
+  };
+  load_scales(b0, s1, z1);
+  load_scales(b0 + QB, s2, z2);
+
+  // this lane's column of x among a word's pieces, and its first word (see below)
+  const int xlane = ((r ^ (2 * c)) & (NCP - 1)) + NCP * (GM == 0 ? 4 * c : GM == 1 ? 4 * (c & 1) + 2 * (c >> 1) : c);
+
+  float total[MT][NT][4];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[t][n][i] = 0.f;
+
+  int slot = 0, q = 0;   // ring slot; the block's place among those whose scales are here
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    if constexpr (RW == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(32 * RW) : "memory");
+    fetch(b + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);   // into the slot of the block before
+    if (q == 0) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s0[t][h] = 256.f * to_f(s1[t][h]);
+          o0[t][h] = 0x3f003f00u + 0x10001u * z1[t][h];
+          s1[t][h] = s2[t][h], z1[t][h] = z2[t][h];
+        }
+      load_scales(b + 2 * QB, s2, z2);
+    }
+    uint32_t wd[MT][2][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 v = ring[(slot * MT * 2 + t * 2 + h) * 32];
+        uint32_t w0 = v.x, w1 = v.y, w2 = v.z, w3 = v.w;
+        if constexpr (GM >= 1) {   // lanes 0, 1 hand their upper two words to lanes 2, 3 for the lower two
+          const bool up = c & 2;
+          const uint32_t e0 = __shfl_xor_sync(~0u, up ? w0 : w2, 2), e1 = __shfl_xor_sync(~0u, up ? w1 : w3, 2);
+          if (up) w0 = e0, w1 = e1; else w2 = e0, w3 = e1;
+        }
+        if constexpr (GM == 2) {   // .. and the lanes of a pair one word of each two
+          const bool up = c & 1;
+          const uint32_t e0 = __shfl_xor_sync(~0u, up ? w0 : w1, 1), e1 = __shfl_xor_sync(~0u, up ? w2 : w3, 1);
+          if (up) w0 = e0, w2 = e1; else w1 = e0, w3 = e1;
+        }
+        wd[t][h][0] = w0, wd[t][h][1] = w1, wd[t][h][2] = w2, wd[t][h][3] = w3;
+      }
+    const uint4* xrow = xring + slot * 16 * NCP + xlane;
+#pragma unroll
+    for (int g = 0; g < SLOTS; ++g) {   // the words of one group
+      constexpr int CH = NT == 1 ? 2 : 1;   // independent sums: an mma waits for its accumulator
+      float acc[CH][MT][NT][4], f[MT][2];
+      __nv_bfloat162 o[MT][2];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f[t][h] = __shfl_sync(~0u, s0[t][h], q * SLOTS + g, 4);
+          const uint32_t os = a.zero ? __shfl_sync(~0u, o0[t][h], q * SLOTS + g, 4) : 0x3f083f08u;
+          o[t][h] = *reinterpret_cast<const __nv_bfloat162*>(&os);
         }
       }
-    }
-  }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    red[wp][r][8 * t + 2 * c] = total[t][0], red[wp][r][8 * t + 2 * c + 1] = total[t][1];
-    red[wp][r + 8][8 * t + 2 * c] = total[t][2], red[wp][r + 8][8 * t + 2 * c + 1] = total[t][3];
+      for (int i = g * (4 / SLOTS); i < (g + 1) * (4 / SLOTS); ++i) {
+        // this lane's word i is the block's word 4 c + i (GM 0), 8 (i / 2) + 4 (c % 2) +
+        // 2 (c / 2) + i % 2 (1) or 4 i + c (2); its swizzle is 2 c
+        const int word = GM == 0 ? i : GM == 1 ? 8 * (i / 2) + (i & 1) : 4 * i;
+        uint4 xb[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xb[n] = xrow[word * NCP + (8 * n & (NCP - 1))];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t pa[4], pb[4];
+          decode(wd[t][0][i], o[t][0], pa);
+          decode(wd[t][1][i], o[t][1], pb);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const bool first = i == g * (4 / SLOTS);
+            if (first) mma_bf16_zero(acc[0][t][n], pa[0], pb[0], pa[1], pb[1], xb[n].x, xb[n].y);
+            else mma_bf16(acc[0][t][n], pa[0], pb[0], pa[1], pb[1], xb[n].x, xb[n].y);
+            if (first && CH == 2) mma_bf16_zero(acc[CH - 1][t][n], pa[2], pb[2], pa[3], pb[3], xb[n].z, xb[n].w);
+            else mma_bf16(acc[CH - 1][t][n], pa[2], pb[2], pa[3], pb[3], xb[n].z, xb[n].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[0][t][n][i];
+            if (CH == 2) v += acc[CH - 1][t][n][i];
+            total[t][n][i] = fmaf(f[t][i / 2], v, total[t][n][i]);
+          }
+    }
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    q = q + 1 == QB ? 0 : q + 1;
   }
+
+  // the shares' sums, in order
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  const int rows = min(NT * 8 / P, a.M - m0);
-  for (int i = threadIdx.x; i < 16 * rows; i += 32 * kWarps) {
-    const int n = i % 16, m = i / 16;
-    if (row0 + n >= a.N) continue;
+  float* red = reinterpret_cast<float*>(raw_smem);   // [KW][ROWS][COLS + 1]
+  constexpr int ROWS = F::ROWS, LD = COLS + 1;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[(kw * ROWS + 16 * (MT * rw + t) + r + 8 * (i / 2)) * LD + 8 * n + 2 * c + i % 2] = total[t][n][i];
+  __syncthreads();
+  const int rows = ncol / P, n0 = ROWS * blockIdx.x;
+  for (int i = threadIdx.x; i < ROWS * rows; i += 32 * F::NW) {
+    const int n = i % ROWS, m = i / ROWS;
+    if (n0 + n >= a.N) continue;
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k)
+    for (int k = 0; k < KW; ++k)
 #pragma unroll
-      for (int q = P - 1; q >= 0; --q) s += red[k][n][m * P + q];
-    if (a.bias) s += a.bias[row0 + n];
-    static_cast<T*>(a.y)[(int64_t)(m0 + m) * a.N + row0 + n] = from_f<T>(s);
+      for (int e = P - 1; e >= 0; --e) s += red[(k * ROWS + n) * LD + m * P + e];
+    if (a.bias) s += a.bias[n0 + n];
+    static_cast<T*>(a.y)[(int64_t)(m0 + m) * a.N + n0 + n] = from_f<T>(s);
   }
 }
 
-template <typename T, typename ST, int NT>
-void launch_q4(const Q4Args& a, int m0, cudaStream_t s) {
-  const unsigned grid = (unsigned)ceil_div(a.N, 16);
-  if (a.group % 128 == 0) q4_matvec_kernel<T, ST, NT, 4><<<grid, 32 * kWarps, 0, s>>>(a, m0);
-  else if (a.group % 64 == 0) q4_matvec_kernel<T, ST, NT, 2><<<grid, 32 * kWarps, 0, s>>>(a, m0);
-  else q4_matvec_kernel<T, ST, NT, 1><<<grid, 32 * kWarps, 0, s>>>(a, m0);
+template <typename T, typename ST, typename F, int NCP>
+cudaError_t launch_q4(const Q4Args& a, int m0, int ncol, cudaStream_t s) {
+  constexpr size_t bytes = F::bytes(NCP);
+  auto go = [&](auto* k) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)ceil_div(a.N, F::ROWS), 32 * F::NW, bytes, s>>>(a, m0, ncol);
+    return cudaGetLastError();
+  };
+  auto by_vec = [&](auto gm) {
+    constexpr int GM = decltype(gm)::value;
+    if constexpr (kParts<T> == 1) {
+      if (a.vec) return go(q4_matvec_kernel<T, ST, F, GM, NCP, true>);
+    }
+    return go(q4_matvec_kernel<T, ST, F, GM, NCP, false>);
+  };
+  const int group = a.K / a.groups;
+  if (group % 128 == 0) return by_vec(std::integral_constant<int, 0>());
+  if (group % 64 == 0) return by_vec(std::integral_constant<int, 1>());
+  return by_vec(std::integral_constant<int, 2>());
 }
 
+// Which configuration (one GB300, us a call, bf16).  One row of x: 16 weight rows a
+// warp and short rings, so that three CTAs share an SM (16384 x 8192 codes 26.6; 32
+// rows a warp and rings of six 28.8).  Up to 4 columns, warps in pairs on one copy of
+// x (2 rows, 4096 x 4096: 8.5; alone 9.3).  Up to 8: 32 rows a warp once they fill the
+// SMs (8 rows, 16384 x 8192: 40 against 46; 5 rows, 12288 x 4096: 26 against 23).  Up
+// to 16: 32 rows a warp, four warps on one x (40; 59 with 16 rows and two).  fp32 x,
+// cut by the warps that bring it: fewer warps to a share (4 rows, 4096 x 4096: 22; 37).
+// 17 to 32: the mma are what counts, at about 24 cycles each a sub-partition (two
+// thirds of the 60 us of 32 rows, 16384 x 8192).
 template <typename T, typename ST>
-void run_rows(const Q4Args& a, cudaStream_t s) {
+cudaError_t run_rows(const Q4Args& a, cudaStream_t s) {
   constexpr int P = kParts<T>;
   for (int m0 = 0; m0 < a.M;) {   // 32 columns at a time: the weights come from HBM or L2 again for each
-    const int cols = (a.M - m0) * P;
-    if (cols <= 8) launch_q4<T, ST, 1>(a, m0, s), m0 += 8 / P;
-    else if (cols <= 16) launch_q4<T, ST, 2>(a, m0, s), m0 += 16 / P;
-    else launch_q4<T, ST, 4>(a, m0, s), m0 += 32 / P;
+    const int left = (a.M - m0) * P;
+    cudaError_t e;
+    int rows = a.M - m0;
+    if (left <= 1) {
+      e = launch_q4<T, ST, Conf<1, 1, 1, 8, 4>, 1>(a, m0, left, s);
+    } else if (left <= 4) {
+      e = launch_q4<T, ST, Conf<1, 1, 2, 8, 4>, 4>(a, m0, left, s);
+    } else if (left <= 8 && a.N < 96 * sm_count()) {
+      e = launch_q4<T, ST, Conf<1, 1, 2, 8, 4>, 8>(a, m0, left, s);
+    } else if (left <= 8) {
+      e = launch_q4<T, ST, Conf<1, 2, 2, 8, 4>, 8>(a, m0, left, s);
+    } else if (left <= 16 && P > 1) {
+      e = launch_q4<T, ST, Conf<2, 1, 2, 8, 4>, 16>(a, m0, left, s);
+    } else if (left <= 16) {
+      e = launch_q4<T, ST, Conf<2, 2, 4, 8, 4>, 16>(a, m0, left, s);
+    } else {
+      if (rows > 32 / P) rows = 32 / P;
+      e = launch_q4<T, ST, Conf<4, 2, 4, 8, 4>, 32>(a, m0, rows * P, s);
+    }
+    if (e != cudaSuccess) return e;
+    m0 += rows;
   }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -250,11 +444,15 @@ void run_rows(const Q4Args& a, cudaStream_t s) {
 gdn_status run_q4_matvec(const void* x, int64_t ldx, const uint8_t* qweight, const void* scales, gdn_dtype sdt,
                          const uint8_t* zeros, const float* bias, int M, int N, int K, int group, gdn_dtype dt,
                          void* y, cudaStream_t s) {
-  Q4Args a = {x, qweight, scales, zeros, bias, y, ldx, M, N, K, group};
+  const int es = dt == GDN_F32 ? 4 : 2, g32 = group / 32;
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ldx * es) % 16 == 0;
+  const Q4Args a = {x, qweight, scales, zeros, bias, y, ldx, M, N, K, K / group,
+                    g32 == 1 ? 0u : (unsigned)(((1ull << 32) + g32 - 1) / g32), vec};
   using B = __nv_bfloat16;
-  if (dt == GDN_F32) sdt == GDN_F32 ? run_rows<float, float>(a, s) : run_rows<float, B>(a, s);
-  else sdt == GDN_F32 ? run_rows<B, float>(a, s) : run_rows<B, B>(a, s);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  cudaError_t e;
+  if (dt == GDN_F32) e = sdt == GDN_F32 ? run_rows<float, float>(a, s) : run_rows<float, B>(a, s);
+  else e = sdt == GDN_F32 ? run_rows<B, float>(a, s) : run_rows<B, B>(a, s);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace gdn

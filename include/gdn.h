@@ -434,7 +434,7 @@ gdn_status gdn_causal_conv1d_bwd(const void* x, const float* weight, const float
  *   scales      : [N, K / group] of dtype sdt
  *   zeros       : [N, K / group] bytes, 0 .. 127, or NULL (8 everywhere)
  *   bias        : [N] fp32 or NULL
- *   K           : a multiple of group;  group : a multiple of 32
+ *   K           : a multiple of group, at most 2^20;  group : a multiple of 32
  *   y           : out [M, N] of dtype dt, contiguous
  * Products and sums are exact to fp32 (no weight and, in fp32, no x is rounded);
  * y is rounded once.  No workspace; asynchronous on `stream`.

@@ -61,6 +61,13 @@ def test_q4_lengths(gdn, K, group):
     check(gdn, make(2, 50, K, group, "f32", "f32", True, False, seed=K + 1))
 
 
+def test_q4_many_rows_of_weights(gdn):
+    """Enough of them for 32 a warp, and a last tile that is not full."""
+    check(gdn, make(6, 14700, 192, 64, "bf16", "bf16", True, True, seed=2))
+    check(gdn, make(14, 14603, 160, 32, "bf16", "f32", True, False, seed=4))
+    check(gdn, make(2, 14700, 256, 128, "f32", "f32", False, True, seed=6))
+
+
 @pytest.mark.parametrize("N,K", [(4096, 4096), (1000, 11008), (12288, 2048)])
 def test_q4_large(gdn, N, K):
     check(gdn, make(4, N, K, 32, "bf16", "bf16", False, True, seed=5))

@@ -90,6 +90,37 @@ __device__ __forceinline__ bool unit_of(const Args& a, int64_t u, Unit& r) {
   return true;
 }
 
+// Four consecutive elements as loaded, entries at or past n as 0.
+template <typename T> struct Raw4;
+template <> struct Raw4<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool vec) {
+    if (vec) {
+      v = __ldg(reinterpret_cast<const uint2*>(p));
+    } else {
+      uint32_t e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + i) : 0u;
+      v = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    }
+  }
+  __device__ __forceinline__ float2 lo() const { return make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)); }
+  __device__ __forceinline__ float2 hi() const { return make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)); }
+};
+template <> struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p, int n, bool vec) {
+    if (vec) {
+      v = __ldg(reinterpret_cast<const float4*>(p));
+    } else {
+      v.x = 0 < n ? __ldg(p) : 0.f, v.y = 1 < n ? __ldg(p + 1) : 0.f;
+      v.z = 2 < n ? __ldg(p + 2) : 0.f, v.w = 3 < n ? __ldg(p + 3) : 0.f;
+    }
+  }
+  __device__ __forceinline__ float2 lo() const { return make_float2(v.x, v.y); }
+  __device__ __forceinline__ float2 hi() const { return make_float2(v.z, v.w); }
+};
+
 // Row t of a tensor whose rows are `stride` bytes apart (one multiply-add).
 template <typename T>
 __device__ __forceinline__ const T* row(const T* p, int t, int stride) {

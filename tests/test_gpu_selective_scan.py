@@ -196,6 +196,30 @@ def test_step_state_pool(gdn, dtype, D, S, G):
     assert torch.equal(state.cpu()[untouched], pool[untouched])
 
 
+@pytest.mark.parametrize("dtype,D,S", [("bf16", 70, 16), ("f32", 33, 5), ("bf16", 40, 32), ("f32", 20, 64), ("bf16", 9, 3)])
+def test_step_many_sequences(gdn, dtype, D, S):
+    """Enough sequences that threads take several, their number not a multiple of that."""
+    n = 101
+    inp = R.make_scan(n, 1, D, S, 1, dtype, seed=D)
+    del inp["h0"]
+    pool = torch.randn(n + 20, D, S, generator=torch.Generator().manual_seed(2))
+    slots = torch.randperm(n + 20, generator=torch.Generator().manual_seed(3))[:n]
+    slots[[0, 7, 50, 100]] = torch.tensor([-1, n + 20, -2, -5])
+    state = pool.cuda()
+    y = gdn.gdn_selective_scan_step(**cuda(inp), state=state, state_indices=slots.int().cuda())
+    torch.cuda.synchronize()
+    has = (slots >= 0) & (slots < n + 20)
+    h0 = torch.zeros(n, D, S)
+    h0[has] = pool[slots[has]]
+    y_ref, ht_ref = R.scan(**inp, h0=h0)
+    y_ref[~has] = 0
+    want = pool.double().clone()
+    want[slots[has]] = ht_ref[has]
+    assert torch.all(y[~has.cuda()] == 0)
+    assert rel_fro(y.double().cpu(), y_ref) <= TOL[dtype]
+    assert rel_fro(state.cpu(), want) <= F32
+
+
 def test_step_several_tokens_packed(gdn):
     lens = [3, 0, 5, 1]
     inp = R.make_scan(1, 0, 50, 16, 1, "bf16", init=True, lens=lens, seed=12)

@@ -196,13 +196,19 @@ __global__ void __launch_bounds__(256) rev_chain_kernel(const BwdArgs b) {
 // ------------------------------------------------------------ the gradients
 
 // Warps of a CTA (one group's channels), and its shared memory.
-template <int RL>
+constexpr int kBwdRing = 3;   // tiles as loaded: one in use, two on their way
+constexpr int bwd_warps(int RL) { return RL >= 8 ? 4 : 8; }
+
+template <typename T, int RL>
 struct Smem {
   using L = Lanes<RL>;
-  static constexpr int W = RL >= 8 ? 4 : 8;
+  static constexpr int W = bwd_warps(RL);
   static constexpr int NS = L::NG > 1 ? L::NG - 1 : 1;
+  // rows as loaded: x, delta, dout and z of the warps' channels, B and C
+  alignas(16) T rx[kBwdRing][4][W][L::TT][L::CPW];
+  alignas(16) T rbc[kBwdRing][2][L::TT][L::SP];
   float B[L::TT][L::SP], C[L::TT][L::SP];
-  float4 dt[W][L::TT][L::CL];     // dt, dt x of a channel pair
+  float4 dt[W][L::TT][L::CL];     // dt of a channel pair, dt x
   float2 dy[W][L::TT][L::CL];
   float4 sub[W][NS][2][32];       // states before the tile's second, third, .. four tokens
   float red[W][L::TT][2][L::SP];  // dB and dC of a warp's channels
@@ -227,10 +233,11 @@ __device__ __forceinline__ void reduce_channels(float (&v)[32], int lane) {
   }
 }
 
-template <typename T, int RL>
-__global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArgs b) {
+// ASYNC: rows arrive by asynchronous copies, otherwise by loads as they are needed.
+template <typename T, int RL, bool ASYNC>
+__global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdArgs b) {
   using L = Lanes<RL>;
-  using SM = Smem<RL>;
+  using SM = Smem<T, RL>;
   constexpr int W = SM::W, NT = 32 * W;
   extern __shared__ __align__(16) char raw_smem[];
   SM& sm = *reinterpret_cast<SM*>(raw_smem);
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
   const int w = threadIdx.x >> 5;
   const int g = blockIdx.y / b.cgrp, jb = blockIdx.y - g * b.cgrp;
   const int wb = jb * W + w;   // warp block of the group; past the group's end: nothing to do but the barriers
-  const int d = g * a.Dg + wb * L::CPW + 2 * ln.chl, dend = (g + 1) * a.Dg;
+  const int dw = g * a.Dg + wb * L::CPW, d = dw + 2 * ln.chl, dend = (g + 1) * a.Dg;
   const bool ok0 = d < dend, ok1 = d + 1 < dend;
   const int n0 = 4 * ln.sl, nn = a.S - n0;
   const bool v4 = a.S % 4 == 0;
@@ -285,30 +292,51 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
       q[c][0] = make_float2(r[0], r[1]), q[c][1] = make_float2(r[2], r[3]);
     }
 
+    // tile i's rows into ring slot r (those that the walk back needs too)
+    auto fetch = [&](int i, int r, bool back) {
+      if constexpr (ASYNC) {
+        constexpr int XROW = L::CPW * sizeof(T), SROW = L::SP * sizeof(T);
+        constexpr int CX = XROW < 16 ? XROW : 16, CB = SROW < 16 ? SROW : 16;
+        if (i >= 0) {
+          const int t0 = i * L::TT, vx = (dend - dw) * (int)sizeof(T), vs = a.S * (int)sizeof(T);
+          auto rows = [&](int k, const T* p, int stride) {
+            copy_rows<L::TT, XROW, CX>((char*)&sm.rx[r][k][w][0][0], (const char*)(p - 2 * ln.chl), stride, t0, u.len, vx,
+                                       ln.lane);
+          };
+          rows(0, px, a.bx);
+          rows(1, pd, a.bd);
+          if (back) {
+            rows(2, pg, a.D * (int)sizeof(T));
+            if (gate) rows(3, pz, a.bz);
+          }
+          if (w == 0)
+            copy_rows<L::TT, SROW, CB>((char*)&sm.rbc[r][0][0][0], (const char*)pB, a.bb, t0, u.len, vs, ln.lane);
+          if (w == 1 && back)
+            copy_rows<L::TT, SROW, CB>((char*)&sm.rbc[r][1][0][0], (const char*)pC, a.bc, t0, u.len, vs, ln.lane);
+        }
+        copies_commit();
+      }
+    };
+    // a pair of this lane's channels of row kind k (x, delta, dout, z) at token tk of slot r's tile
+    auto pair = [&](int k, int r, int tk, int t, const T* p, int stride, bool vec) {
+      Raw2<T> v;
+      v.zero();
+      if constexpr (ASYNC) v.load_shared(&sm.rx[r][k][w][tk][2 * ln.chl]);
+      else if (t < u.len && ok0) v.load(row(p, t, stride), vec, ok0, ok1);
+      return v.f();
+    };
     // a tile's steps and inputs into shared memory; x and softplus' stay
     float2 xs[4], sp[4];
-    auto stage = [&](int t0, bool back) {
+    auto stage = [&](int t0, int r, bool back) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int tk = ln.token(k), t = t0 + tk;
-        Raw2<T> rx, rd, rz, rg;
-        rx.zero(), rd.zero(), rz.zero(), rg.zero();
-        const bool in = t < u.len && ok0;
-        if (in) {
-          rx.load(row(px, t, a.bx), a.vin, ok0, ok1);
-          rd.load(row(pd, t, a.bd), a.vin, ok0, ok1);
-          if (back) {
-            rg.load(pg + (int64_t)t * a.D, b.vg, ok0, ok1);
-            if (pz) rz.load(row(pz, t, a.bz), a.vin, ok0, ok1);
-          }
-        }
-        const float2 x = rx.f();
-        float2 dt = rd.f();
-        dt.x += bias.x, dt.y += bias.y;
+        const float2 x = pair(0, r, tk, t, px, a.bx, a.vin);
+        float2 dt = __fadd2_rn(pair(1, r, tk, t, pd, a.bd, a.vin), bias);
         if (a.softplus) {
           float2 e;
           const float2 v = dt;
-          dt = softplus2(v, e);
+          dt = softplus2(dt, e);
           // sigmoid(v), from e^{-|v|}
           if (back) sp[k] = make_float2((v.x >= 0.f ? 1.f : e.x) * rcp_approx(1.f + e.x),
                                         (v.y >= 0.f ? 1.f : e.y) * rcp_approx(1.f + e.y));
@@ -317,17 +345,26 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
         }
         if (t >= u.len) dt = make_float2(0.f, 0.f);
         xs[k] = x;
+        const float2 dx = __fmul2_rn(dt, x);   // x is zero past the end
+        float2 dy;
+        if (back) {
+          dy = pair(2, r, tk, t, pg, a.D * (int)sizeof(T), b.vg);
+          if (gate) dy = gated<T>(dy, pair(3, r, tk, t, pz, a.bz, a.vin), true);
+        }
         if (!ln.dup) {
-          sm.dt[w][tk][ln.chl] = make_float4(dt.x, dt.x * x.x, dt.y, dt.y * x.y);
-          if (back) sm.dy[w][tk][ln.chl] = gated<T>(rg.f(), rz.f(), gate);
+          sm.dt[w][tk][ln.chl] = make_float4(dt.x, dt.y, dx.x, dx.y);
+          if (back) sm.dy[w][tk][ln.chl] = dy;
         }
       }
       // B (and C) of the CTA's group
-      constexpr int VE = RowVec<T, RL>::VE;
-      for (int i = threadIdx.x; i < RowVec<T, RL>::NV; i += NT) {
+      constexpr int VE = RowVec<T, RL>::VE, NV = RowVec<T, RL>::NV;
+      for (int i = threadIdx.x; i < NV; i += NT) {
         const int p = i * VE, t = t0 + p / L::SP, n = p % L::SP;
         uint4 rb = make_uint4(0u, 0u, 0u, 0u), rc = rb;
-        if (t < u.len) {
+        if constexpr (ASYNC) {
+          rb = get_vec<VE * sizeof(T)>(&sm.rbc[r][0][0][0] + p);
+          if (back) rc = get_vec<VE * sizeof(T)>(&sm.rbc[r][1][0][0] + p);
+        } else if (t < u.len) {
           rb = load_row16<T, VE>(row(pB, t, a.bb), n, a.S, a.vbc);
           if (back) rc = load_row16<T, VE>(row(pC, t, a.bc), n, a.S, a.vbc);
         }
@@ -341,7 +378,7 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
       const float4 bb = *reinterpret_cast<const float4*>(&sm.B[t][n0]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float dt = c ? s.z : s.x, ux = c ? s.w : s.y;
+        const float dt = c ? s.y : s.x, ux = c ? s.w : s.z;
         const float2 dt2 = make_float2(dt, dt), ux2 = make_float2(ux, ux);
         const float2 e0 = __fmul2_rn(dt2, A2[c][0]), e1 = __fmul2_rn(dt2, A2[c][1]);
         aa[c][0] = make_float2(sm100::ex2_fast(e0.x), sm100::ex2_fast(e0.y));
@@ -353,31 +390,41 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
 
     // forward: the state before every tile
     const int ntile = (u.len + L::TT - 1) / L::TT;
-    for (int i = 0; i < ntile; ++i) {
+#pragma unroll
+    for (int k = 0; k < kBwdRing - 1; ++k) fetch(k < ntile - 1 ? k : -1, k, false);
+    for (int i = 0, r = 0; i < ntile; ++i) {
+      if (i + 1 == ntile) break;   // the last tile's is in h
       float4* o = ck + (int64_t)i * (W * 64);
       o[0] = make_float4(h[0][0].x, h[0][0].y, h[0][1].x, h[0][1].y);
       o[32] = make_float4(h[1][0].x, h[1][0].y, h[1][1].x, h[1][1].y);
-      if (i + 1 == ntile) break;
-      __syncthreads();
-      stage(i * L::TT, false);
+      if (ASYNC) copies_wait<kBwdRing - 2>();
+      __syncthreads();   // copies are here; the tile before has been used
+      fetch(i + kBwdRing - 1 < ntile - 1 ? i + kBwdRing - 1 : -1, r == 0 ? kBwdRing - 1 : r - 1, false);
+      stage(i * L::TT, r, false);
       __syncthreads();
       float2 aa[2][2];
 #pragma unroll 4
       for (int t = 0; t < L::TT; ++t) advance(t, h, aa);
+      r = r + 1 == kBwdRing ? 0 : r + 1;
     }
 
-    // backward
-    for (int i = ntile - 1; i >= 0; --i) {
+    // backward, the state before the next tile loaded ahead
+    float4 c0, c1;
+    if (ASYNC) copies_wait<0>();
+#pragma unroll
+    for (int k = 0; k < kBwdRing - 1; ++k) fetch(ntile - 1 - k, k, true);
+    for (int i = ntile - 1, r = 0; i >= 0; --i) {
       const int t0 = i * L::TT;
-      __syncthreads();
-      stage(t0, true);
-      __syncthreads();
-      {
-        const float4* o = ck + (int64_t)i * (W * 64);
-        const float4 s0 = o[0], s1 = o[32];
-        h[0][0] = make_float2(s0.x, s0.y), h[0][1] = make_float2(s0.z, s0.w);
-        h[1][0] = make_float2(s1.x, s1.y), h[1][1] = make_float2(s1.z, s1.w);
+      if (i + 1 < ntile) {
+        h[0][0] = make_float2(c0.x, c0.y), h[0][1] = make_float2(c0.z, c0.w);
+        h[1][0] = make_float2(c1.x, c1.y), h[1][1] = make_float2(c1.z, c1.w);
       }
+      if (ASYNC) copies_wait<kBwdRing - 2>();
+      __syncthreads();
+      if (i > 0) c0 = ck[(int64_t)(i - 1) * (W * 64)], c1 = ck[(int64_t)(i - 1) * (W * 64) + 32];
+      fetch(i - (kBwdRing - 1), r == 0 ? kBwdRing - 1 : r - 1, true);
+      stage(t0, r, true);
+      __syncthreads();
       // states before each four tokens
       if (L::NG > 1) {
         const float2 k00 = h[0][0], k01 = h[0][1], k10 = h[1][0], k11 = h[1][1];
@@ -425,7 +472,7 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
           float2 dB2[2], dC2[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float dt = c ? s.z : s.x, ux = c ? s.w : s.y, gy = c ? dy.y : dy.x;
+            const float dt = c ? s.y : s.x, ux = c ? s.w : s.z, gy = c ? dy.y : dy.x;
             const float2 dt2 = make_float2(dt, dt), ux2 = make_float2(ux, ux), gy2 = make_float2(gy, gy);
             float2 gB = make_float2(0.f, 0.f), wA = gB, y2 = gB;
 #pragma unroll
@@ -464,7 +511,7 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
           const float2 dy = sm.dy[w][tk][ln.chl], x = xs[k];
           const float2 gB = make_float2(v[6 * j], v[6 * j + 1]);
           const float2 wA = make_float2(v[6 * j + 2], v[6 * j + 3]);
-          const float2 dx = make_float2(fmaf(gB.x, s.x, skip.x * dy.x), fmaf(gB.y, s.z, skip.y * dy.y));
+          const float2 dx = make_float2(fmaf(gB.x, s.x, skip.x * dy.x), fmaf(gB.y, s.y, skip.y * dy.y));
           const float2 dd = make_float2(fmaf(gB.x, x.x, wA.x * kLn2) * sp[k].x, fmaf(gB.y, x.y, wA.y * kLn2) * sp[k].y);
           if (t < u.len && ok0 && !ln.dup) {
             const int64_t o = (u.tok0 + t) * a.D + d;
@@ -473,10 +520,8 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
             dD.x = fmaf(dy.x, x.x, dD.x), dD.y = fmaf(dy.y, x.y, dD.y);
             dbias.x += dd.x, dbias.y += dd.y;
             if (gate) {
-              Raw2<T> rz, rg;
-              rz.load(row(pz, t, a.bz), a.vin, ok0, ok1);
-              rg.load(pg + (int64_t)t * a.D, b.vg, ok0, ok1);
-              const float2 z = rz.f(), gr2 = rg.f();
+              const float2 z = pair(3, r, tk, t, pz, a.bz, a.vin);
+              const float2 gr2 = pair(2, r, tk, t, pg, a.D * (int)sizeof(T), b.vg);
               const float s0 = sigmoid(z.x), s1 = sigmoid(z.y);
               const float2 dz = make_float2(
                   gr2.x * fmaf(skip.x, x.x, v[6 * j + 4]) * (s0 * fmaf(z.x, 1.f - s0, 1.f)),
@@ -489,14 +534,16 @@ __global__ void __launch_bounds__(32 * Smem<RL>::W) scan_bwd_kernel(const BwdArg
       // dB and dC of the CTA's channels
       __syncthreads();
       for (int p = threadIdx.x; p < L::TT * 2 * L::SP; p += NT) {
-        const int tk = p / (2 * L::SP), r = p % (2 * L::SP), n = r % L::SP, t = t0 + tk;
+        const int tk = p / (2 * L::SP), m = p % (2 * L::SP), n = m % L::SP, t = t0 + tk;
         if (n >= a.S || t >= u.len) continue;
         float sum = 0.f;
 #pragma unroll
-        for (int ww = 0; ww < W; ++ww) sum += sm.red[ww][tk][r / L::SP][n];
-        b.pbc[((((int64_t)jb * b.Ttot + u.tok0 + t) * a.G + g) * 2 + r / L::SP) * a.S + n] = sum;
+        for (int ww = 0; ww < W; ++ww) sum += sm.red[ww][tk][m / L::SP][n];
+        b.pbc[((((int64_t)jb * b.Ttot + u.tok0 + t) * a.G + g) * 2 + m / L::SP) * a.S + n] = sum;
       }
+      r = r + 1 == kBwdRing ? 0 : r + 1;
     }
+    if (ASYNC) copies_wait<0>();
     if (b.dh0 && u.first) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -581,7 +628,7 @@ Plan bwd_plan(const gdn_scan_problem& p) {
 
 BwdLayout bwd_layout(const gdn_scan_problem& p, const Plan& pl) {
   BwdLayout l;
-  l.warps = pl.RL >= 8 ? 4 : 8;
+  l.warps = bwd_warps(pl.RL);
   l.cgrp = (int)ceil_div(pl.cbg, l.warps);
   const int tt = pl.RL >= 4 ? 16 : 4 * pl.RL;
   const int64_t most = p.T < pl.seglen ? p.T : pl.seglen;
@@ -619,11 +666,16 @@ cudaError_t launch_bwd(const BwdArgs& b, const Plan& pl, cudaStream_t s) {
     rev_chain_kernel<<<dim3((unsigned)ceil_div((int64_t)a.D * a.S, 256), (unsigned)ny, (unsigned)ceil_div(ncut, ny)),
                        256, 0, s>>>(b);
   }
-  const size_t bytes = sizeof(Smem<RL>);
-  const cudaError_t e =
-      cudaFuncSetAttribute(scan_bwd_kernel<T, RL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  constexpr size_t bytes = sizeof(Smem<T, RL>);
+  const int es = sizeof(T), xrow = Lanes<RL>::CPW * es, srow = 4 * RL * es;
+  const int cx = xrow < 16 ? xrow : 16, cb = srow < 16 ? srow : 16;
+  const bool async = aligned_rows(a.x, a.bx, cx) && aligned_rows(a.dl, a.bd, cx) && (!a.z || aligned_rows(a.z, a.bz, cx)) &&
+                     aligned_rows(b.dout, (int64_t)a.D * es, cx) && aligned_rows(a.B, a.bb, cb) &&
+                     aligned_rows(a.C, a.bc, cb) && (a.G == 1 || (a.Dg * es % cx == 0 && a.S * es % cb == 0));
+  auto* k = async ? scan_bwd_kernel<T, RL, true> : scan_bwd_kernel<T, RL, false>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  scan_bwd_kernel<T, RL><<<dim3(b.slots, a.G * b.cgrp), 32 * Smem<RL>::W, bytes, s>>>(b);
+  k<<<dim3(b.slots, a.G * b.cgrp), 32 * bwd_warps(RL), bytes, s>>>(b);
   if (b.Ttot > 0)
     scan_bwd_bc_kernel<T><<<(unsigned)ceil_div(b.Ttot * a.G * 2 * a.S, 256), 256, 0, s>>>(b);
   scan_bwd_params_kernel<<<(unsigned)ceil_div((int64_t)a.D * a.S + 2 * a.D, 256), 256, 0, s>>>(b);

@@ -43,11 +43,11 @@ struct Tiles {
   alignas(16) T rC[STATES ? 1 : kRing][NZ][L::SP];
 };
 
-// ASYNC: rows arrive by asynchronous copies, otherwise through registers.
-template <typename T, int RL, bool STATES, bool GATE, bool ASYNC>
+template <typename T, int RL, bool STATES, bool GATE, int ROWS>
 __global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a) {
   using L = Lanes<RL>;
-  using CK = Chunks<T, RL>;
+  constexpr bool ASYNC = ROWS != kRegs;
+  constexpr int XROW = L::CPW * sizeof(T), SROW = L::SP * sizeof(T), CX = chunk<ROWS, XROW>(), CB = chunk<ROWS, SROW>();
   constexpr int W = warps_of(RL);
   constexpr int VE = RowVec<T, RL>::VE, NV = RowVec<T, RL>::NV, NPV = (NV + 31) / 32;
   extern __shared__ __align__(16) char raw_smem[];
@@ -107,12 +107,12 @@ __global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a
   auto fetch = [&](int t0, int r) {
     if constexpr (ASYNC) {
       const int vx = (dend - dw) * (int)sizeof(T), vs = a.S * (int)sizeof(T);
-      copy_rows<L::TT, CK::ROW, CK::X>((char*)&sm.rx[r][0][0], px, a.bx, t0, u.len, vx, ln.lane);
-      copy_rows<L::TT, CK::ROW, CK::X>((char*)&sm.rd[r][0][0], pd, a.bd, t0, u.len, vx, ln.lane);
-      copy_rows<L::TT, CK::SROW, CK::B>((char*)&sm.rB[r][0][0], pB, a.bb, t0, u.len, vs, ln.lane);
+      copy_rows<L::TT, XROW, CX>((char*)&sm.rx[r][0][0], px, a.bx, t0, u.len, vx, ln.lane);
+      copy_rows<L::TT, XROW, CX>((char*)&sm.rd[r][0][0], pd, a.bd, t0, u.len, vx, ln.lane);
+      copy_rows<L::TT, SROW, CB>((char*)&sm.rB[r][0][0], pB, a.bb, t0, u.len, vs, ln.lane);
       if constexpr (!STATES) {
-        copy_rows<L::TT, CK::SROW, CK::B>((char*)&sm.rC[r][0][0], pC, a.bc, t0, u.len, vs, ln.lane);
-        if (GATE) copy_rows<L::TT, CK::ROW, CK::X>((char*)&sm.rz[r][0][0], pz, a.bz, t0, u.len, vx, ln.lane);
+        copy_rows<L::TT, SROW, CB>((char*)&sm.rC[r][0][0], pC, a.bc, t0, u.len, vs, ln.lane);
+        if (GATE) copy_rows<L::TT, XROW, CX>((char*)&sm.rz[r][0][0], pz, a.bz, t0, u.len, vx, ln.lane);
       }
       copies_commit();
     } else {
@@ -599,7 +599,9 @@ void launch_scan(const Args& a, const Plan& pl, cudaStream_t s) {
     const size_t bytes = W * sizeof(Tiles<T, R, STATES>);
     auto go = [&](auto gate) {
       constexpr bool Z = decltype(gate)::value;
-      auto* k = a.async ? scan_kernel<T, R, STATES, Z, true> : scan_kernel<T, R, STATES, Z, false>;
+      auto* k = a.rows == kWide     ? scan_kernel<T, R, STATES, Z, kWide>
+                : a.rows == kNarrow ? scan_kernel<T, R, STATES, Z, kNarrow>
+                                    : scan_kernel<T, R, STATES, Z, kRegs>;
       if (bytes > 48 * 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
       k<<<grid, 32 * W, bytes, s>>>(a);
     };
@@ -681,10 +683,9 @@ Args base_args(const gdn_scan_problem& p, const Plan& pl, const void* x, const v
           (!z || aligned_rows(z, a.bz, 2 * es));
   const int ve = 16 / (int)es < 4 * pl.RL ? 16 / (int)es : 4 * pl.RL;   // RowVec::VE
   a.vbc = ve * es == 16 && a.S == 4 * pl.RL && aligned_rows(B, a.bb, 16) && aligned_rows(C, a.bc, 16);
-  const int cx = chunk_x(pl.RL, (int)es), cb = chunk_b(pl.RL, (int)es);
-  a.async = a.Dg % 2 == 0 && aligned_rows(x, a.bx, cx) && aligned_rows(delta, a.bd, cx) &&
-            (!z || aligned_rows(z, a.bz, cx)) && aligned_rows(B, a.bb, cb) && aligned_rows(C, a.bc, cb) &&
-            (a.G == 1 || (a.Dg * es % cx == 0 && a.S * es % cb == 0));
+  RowsOf r = {64 / pl.RL * (int)es, 4 * pl.RL * (int)es, a.G > 1, a.Dg * (int64_t)es, a.S * (int64_t)es};
+  r.x(x, a.bx), r.x(delta, a.bd), r.x(z, a.bz), r.s(B, a.bb), r.s(C, a.bc);
+  a.rows = a.Dg % 2 == 0 ? r.rows : kRegs;
   return a;
 }
 
@@ -720,7 +721,7 @@ gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* de
   a.y = y, a.ht = ht;
   const int es = p.dt == GDN_F32 ? 4 : 2;
   a.vy = a.Dg % 2 == 0 && aligned_rows(y, p.D * es, 2 * es);
-  a.async = a.async && a.vy;
+  if (!a.vy) a.rows = kRegs;
   if (p.varlen) {
     a.seg0 = reinterpret_cast<int32_t*>(w + l.seg0);
     if (launch_prepare_segments(cu, p.N, p.T, pl.seglen, reinterpret_cast<int32_t*>(w + l.seg0),

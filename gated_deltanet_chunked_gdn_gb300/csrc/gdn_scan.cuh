@@ -41,7 +41,7 @@ struct Args {
   int softplus;
   bool vin;     // pairs of neighbouring channels of x, delta and z can be loaded at once
   bool vbc;     // vectors of B and C (RowVec) can be loaded at once
-  bool async;   // every row can be copied in chunks (Chunks)
+  int rows;     // Rows
   // segments
   int nseg;                 // of a sequence (equal lengths)
   int seglen;               // tokens, a multiple of kTileMax
@@ -212,15 +212,22 @@ __device__ __forceinline__ uint4 get_vec(const void* p) {
   return make_uint4(q.x, q.y, 0u, 0u);
 }
 
-// Asynchronous copy of CH (8 or 16) bytes to shared memory; only the first `bytes`
+// Asynchronous copy of CH (4, 8 or 16) bytes to shared memory; only the first `bytes`
 // of them are read, the rest become zero.
 template <int CH>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
   if constexpr (CH == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes), "n"(CH)
+                 : "memory");
 }
+
+// How rows come to shared memory: copies of 16 bytes (or a shorter row), of 4 bytes,
+// or loads through registers where not even pairs of bf16 are aligned.
+enum Rows { kRegs = 0, kWide = 1, kNarrow = 2 };
+template <int ROWS, int ROW>
+constexpr int chunk() { return ROWS == kNarrow ? 4 : ROW < 16 ? ROW : 16; }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
@@ -352,15 +359,6 @@ __device__ __forceinline__ void reduce_states(float (&v)[4 * NV], int lane) {
   }
 }
 
-// Bytes of an asynchronous copy of a row of a warp's channels, and of a group's states.
-template <typename T, int RL>
-struct Chunks {
-  static constexpr int ROW = 64 / RL * (int)sizeof(T), X = ROW < 16 ? ROW : 16;
-  static constexpr int SROW = 4 * RL * (int)sizeof(T), B = SROW < 16 ? SROW : 16;
-};
-inline int chunk_x(int RL, int es) { return 64 / RL * es < 16 ? 64 / RL * es : 16; }
-inline int chunk_b(int RL, int es) { return 4 * RL * es < 16 ? 4 * RL * es : 16; }
-
 // Rows t0 .. of a tile from a tensor (`first` its row 0, `stride` bytes a row) to
 // dst[TT][ROW bytes]: `valid` bytes of a row exist, rows from `len` on become zero.
 template <int TT, int ROW, int CH>
@@ -382,6 +380,23 @@ __device__ __forceinline__ void copy_rows(char* dst, const char* first, int stri
 inline bool aligned_rows(const void* p, int64_t stride, size_t to) {
   return reinterpret_cast<uintptr_t>(p) % to == 0 && stride % (int64_t)to == 0;
 }
+
+// The widest copies that rows allow: x-like rows of xrow bytes a warp at px (stride bytes
+// apart), B and C rows of srow bytes.
+struct RowsOf {
+  int xrow, srow;
+  bool groups;   // several groups: chunks may not leave a group's channels or states
+  int64_t xg, sg;   // bytes of a group's channels, states
+  int rows = kWide;
+  void use(const void* p, int64_t stride, int row, int64_t group) {
+    if (!p) return;
+    const int wide = row < 16 ? row : 16;
+    if (rows == kWide && !(aligned_rows(p, stride, wide) && (!groups || group % wide == 0))) rows = kNarrow;
+    if (rows == kNarrow && !(aligned_rows(p, stride, 4) && (!groups || group % 4 == 0))) rows = kRegs;
+  }
+  void x(const void* p, int64_t stride) { use(p, stride, xrow, xg); }
+  void s(const void* p, int64_t stride) { use(p, stride, srow, sg); }
+};
 
 inline int lanes_for(int S) { return S <= 4 ? 1 : S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16; }
 

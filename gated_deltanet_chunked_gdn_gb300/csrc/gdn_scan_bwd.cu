@@ -233,11 +233,11 @@ __device__ __forceinline__ void reduce_channels(float (&v)[32], int lane) {
   }
 }
 
-// ASYNC: rows arrive by asynchronous copies, otherwise by loads as they are needed.
-template <typename T, int RL, bool ASYNC>
+template <typename T, int RL, int ROWS>
 __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdArgs b) {
   using L = Lanes<RL>;
   using SM = Smem<T, RL>;
+  constexpr bool ASYNC = ROWS != kRegs;
   constexpr int W = SM::W, NT = 32 * W;
   extern __shared__ __align__(16) char raw_smem[];
   SM& sm = *reinterpret_cast<SM*>(raw_smem);
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
     auto fetch = [&](int i, int r, bool back) {
       if constexpr (ASYNC) {
         constexpr int XROW = L::CPW * sizeof(T), SROW = L::SP * sizeof(T);
-        constexpr int CX = XROW < 16 ? XROW : 16, CB = SROW < 16 ? SROW : 16;
+        constexpr int CX = chunk<ROWS, XROW>(), CB = chunk<ROWS, SROW>();
         if (i >= 0) {
           const int t0 = i * L::TT, vx = (dend - dw) * (int)sizeof(T), vs = a.S * (int)sizeof(T);
           auto rows = [&](int k, const T* p, int stride) {
@@ -667,12 +667,10 @@ cudaError_t launch_bwd(const BwdArgs& b, const Plan& pl, cudaStream_t s) {
                        256, 0, s>>>(b);
   }
   constexpr size_t bytes = sizeof(Smem<T, RL>);
-  const int es = sizeof(T), xrow = Lanes<RL>::CPW * es, srow = 4 * RL * es;
-  const int cx = xrow < 16 ? xrow : 16, cb = srow < 16 ? srow : 16;
-  const bool async = aligned_rows(a.x, a.bx, cx) && aligned_rows(a.dl, a.bd, cx) && (!a.z || aligned_rows(a.z, a.bz, cx)) &&
-                     aligned_rows(b.dout, (int64_t)a.D * es, cx) && aligned_rows(a.B, a.bb, cb) &&
-                     aligned_rows(a.C, a.bc, cb) && (a.G == 1 || (a.Dg * es % cx == 0 && a.S * es % cb == 0));
-  auto* k = async ? scan_bwd_kernel<T, RL, true> : scan_bwd_kernel<T, RL, false>;
+  const int64_t es = sizeof(T);
+  RowsOf r = {Lanes<RL>::CPW * (int)es, 4 * RL * (int)es, a.G > 1, a.Dg * es, a.S * es};
+  r.x(a.x, a.bx), r.x(a.dl, a.bd), r.x(a.z, a.bz), r.x(b.dout, a.D * es), r.s(a.B, a.bb), r.s(a.C, a.bc);
+  auto* k = r.rows == kWide ? scan_bwd_kernel<T, RL, kWide> : r.rows == kNarrow ? scan_bwd_kernel<T, RL, kNarrow> : scan_bwd_kernel<T, RL, kRegs>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   k<<<dim3(b.slots, a.G * b.cgrp), 32 * bwd_warps(RL), bytes, s>>>(b);

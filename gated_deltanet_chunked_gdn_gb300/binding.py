@@ -505,22 +505,24 @@ def _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, fp32=(
     """Checks of a scan's tensors and its problem.  fp32: (name, tensor, shape) that must be contiguous float32;
     others: (name, tensor) that must be like x and contiguous."""
     # the usual call, all rows contiguous, in one expression: a decode step's launch is shorter than its checks
-    dtype, shape, dev = x.dtype, x.shape, x.device
-    if len(shape) == 3 and B.dim() == 4 and x.is_cuda and dtype in DTYPES:
+    dtype, shape, dev = x.dtype, x.shape, x.get_device()
+    if len(shape) == 3 and B.dim() == 4 and dev >= 0 and dtype in DTYPES:
         nb, T, d = shape
         _, _, G, S = bshape = B.shape
         f32 = torch.float32
         if (x.is_contiguous() and delta.is_contiguous() and B.is_contiguous() and C.is_contiguous()
                 and A.is_contiguous() and delta.shape == shape and C.shape == bshape and bshape[0] == nb
                 and bshape[1] == T and A.shape == (d, S) and delta.dtype is dtype and B.dtype is dtype
-                and C.dtype is dtype and A.dtype is f32 and delta.device == dev and B.device == dev
-                and C.device == dev and A.device == dev
-                and (z is None or (z.shape == shape and z.dtype is dtype and z.device == dev and z.is_contiguous()))
-                and (D is None or (D.shape == (d,) and D.dtype is f32 and D.device == dev and D.is_contiguous()))
-                and (dt_bias is None or (dt_bias.shape == (d,) and dt_bias.dtype is f32 and dt_bias.device == dev
-                                         and dt_bias.is_contiguous()))):
+                and C.dtype is dtype and A.dtype is f32 and delta.get_device() == dev and B.get_device() == dev
+                and C.get_device() == dev and A.get_device() == dev
+                and (z is None or (z.shape == shape and z.dtype is dtype and z.get_device() == dev
+                                   and z.is_contiguous()))
+                and (D is None or (D.shape == (d,) and D.dtype is f32 and D.get_device() == dev
+                                   and D.is_contiguous()))
+                and (dt_bias is None or (dt_bias.shape == (d,) and dt_bias.dtype is f32
+                                         and dt_bias.get_device() == dev and dt_bias.is_contiguous()))):
             for _, t, want in fp32:
-                if t is not None and (t.dtype is not f32 or t.device != dev or t.shape != want
+                if t is not None and (t.dtype is not f32 or t.get_device() != dev or t.shape != want
                                       or not t.is_contiguous()):
                     break
             else:
@@ -612,18 +614,26 @@ def gdn_selective_scan_step(x, delta, A, B, C, state, D=None, z=None, dt_bias=No
                             state_indices=None, cu_seqlens=None, y=None, stream=None):
     """The scan's tokens on a state pool (decode).  ``state`` [slots, D, S] fp32 is updated in place; returns y."""
     lib = _lib or load()
-    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
-                      (("state", state, (state.shape[0], x.shape[-1], A.shape[-1])),),
+    slots, d, S = state.shape
+    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (),
                       (("y", y),) if y is not None else ())
-    if state_indices is not None and (state_indices.dtype is not torch.int32 or state_indices.device != x.device
-                                      or not state_indices.is_contiguous() or state_indices.numel() != p.N):
-        raise ValueError("state_indices must be a contiguous int32 CUDA tensor, one slot a sequence")
+    dev = x.get_device()
+    if (state.dtype is not torch.float32 or d != x.shape[-1] or S != A.shape[-1] or state.get_device() != dev
+            or not state.is_contiguous()):
+        raise ValueError("state must be a contiguous float32 CUDA tensor [slots, D, S]")
+    idx = 0
+    if state_indices is not None:
+        if (state_indices.dtype is not torch.int32 or state_indices.get_device() != dev
+                or not state_indices.is_contiguous() or state_indices.numel() != p.N):
+            raise ValueError("state_indices must be a contiguous int32 CUDA tensor, one slot a sequence")
+        idx = state_indices.data_ptr()
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    s = stream if stream is not None else _current_stream(x.get_device())
+        y = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     st = lib.gdn_selective_scan_step(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                                     _address(D), _address(z), _address(dt_bias), state.data_ptr(),
-                                     _address(state_indices), state.shape[0], _address(cu_seqlens), y.data_ptr(), s)
+                                     0 if D is None else D.data_ptr(), 0 if z is None else z.data_ptr(),
+                                     0 if dt_bias is None else dt_bias.data_ptr(), state.data_ptr(), idx, slots,
+                                     0 if cu_seqlens is None else cu_seqlens.data_ptr(), y.data_ptr(),
+                                     _current_stream(dev) if stream is None else stream)
     if st:
         raise GDNError(st, "gdn_selective_scan_step")
     return y
@@ -722,16 +732,16 @@ def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None
     lib = _lib or load()
     N, half = qshape = qweight.shape
     K, groups = 2 * half, scales.shape[1]
-    dtype, sdt, dev = x.dtype, scales.dtype, x.device
+    dtype, sdt, dev = x.dtype, scales.dtype, x.get_device()
     if dtype not in DTYPES or sdt not in DTYPES:
         raise ValueError("x and scales must be float32 or bfloat16")
-    if x.shape[-1] != K or not x.is_cuda or groups == 0 or K % groups != 0:
+    if x.shape[-1] != K or dev < 0 or groups == 0 or K % groups != 0:
         raise ValueError("x must be a CUDA tensor of shape [..., K] and scales [N, K / group]")
-    if not (qweight.dtype is torch.uint8 and qweight.device == dev and qweight.is_contiguous()
-            and scales.shape[0] == N and scales.device == dev and scales.is_contiguous()
-            and (zeros is None or (zeros.dtype is torch.uint8 and zeros.shape == scales.shape and zeros.device == dev
-                                   and zeros.is_contiguous()))
-            and (bias is None or (bias.dtype is torch.float32 and bias.shape == (N,) and bias.device == dev
+    if not (qweight.dtype is torch.uint8 and qweight.get_device() == dev and qweight.is_contiguous()
+            and scales.shape[0] == N and scales.get_device() == dev and scales.is_contiguous()
+            and (zeros is None or (zeros.dtype is torch.uint8 and zeros.shape == scales.shape
+                                   and zeros.get_device() == dev and zeros.is_contiguous()))
+            and (bias is None or (bias.dtype is torch.float32 and bias.shape == (N,) and bias.get_device() == dev
                                   and bias.is_contiguous()))):
         raise ValueError(f"qweight (uint8 {tuple(qshape)}), scales and zeros (uint8) [N, K / group] and bias (float32 "
                          "[N]) must be contiguous and on the device of x")
@@ -742,10 +752,10 @@ def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None
     else:
         raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
     if y is None:
-        y = x.new_empty((*x.shape[:-1], N))
-    elif y.shape != (*x.shape[:-1], N) or y.dtype != dtype or y.device != dev or not y.is_contiguous():
+        y = torch.empty((*x.shape[:-1], N), dtype=dtype, device=x.device)
+    elif y.shape != (*x.shape[:-1], N) or y.dtype != dtype or y.get_device() != dev or not y.is_contiguous():
         raise ValueError("y must be a contiguous CUDA tensor [..., N] with the dtype of x")
-    s = stream if stream is not None else _current_stream(x.get_device())
+    s = stream if stream is not None else _current_stream(dev)
     st = lib.gdn_q4_matvec(x.data_ptr(), ld, qweight.data_ptr(), scales.data_ptr(), DTYPES[scales.dtype],
                            _address(zeros), _address(bias), M, N, K, K // groups, DTYPES[x.dtype], y.data_ptr(), s)
     if st:

@@ -440,6 +440,10 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
         h[0][0] = k00, h[0][1] = k01, h[1][0] = k10, h[1][1] = k11;
       }
       const float2 first00 = h[0][0], first01 = h[0][1], first10 = h[1][0], first11 = h[1][1];
+      // dA of the tile first: a sum over all tokens in one place would lose small terms
+      float2 tA[2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tA[c][0] = tA[c][1] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int gr = L::NG - 1; gr >= 0; --gr) {
         float2 hs[2][2];   // state before the four tokens
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
               y2 = __ffma2_rn(hh[j][c][e], C2[e], y2);
               const float2 aq = __fmul2_rn(aa[j][c][e], qq);
               const float2 wq = __fmul2_rn(aq, j ? hh[j - 1][c][e] : hs[c][e]);
-              dA[c][e] = __ffma2_rn(wq, dt2, dA[c][e]);
+              tA[c][e] = __ffma2_rn(wq, dt2, tA[c][e]);
               wA = __ffma2_rn(wq, A2[c][e], wA);
               q[c][e] = aq;
             }
@@ -531,6 +535,10 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
           }
         }
       }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) dA[c][e] = __fadd2_rn(dA[c][e], tA[c][e]);
       // dB and dC of the CTA's channels
       __syncthreads();
       for (int p = threadIdx.x; p < L::TT * 2 * L::SP; p += NT) {

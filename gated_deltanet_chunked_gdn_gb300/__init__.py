@@ -5,7 +5,7 @@ Python binding (``binding``), the build step (``build``) and the seeded
 synthetic input recipes (``inputs``).  Submodules are imported lazily so that
 ``inputs`` can be used without loading the CUDA library.
 """
-__all__ = ["binding", "build", "inputs"]
+__all__ = ["binding", "build", "inputs", "selective_layer"]
 
 
 def __getattr__(name):

@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kVec = 4;      // channels a thread, as packed pairs
 constexpr int kPairs = kVec / 2;
-constexpr int kRun = 256;    // tokens a run
+constexpr int kRun = 256;    // most tokens of a run
 constexpr int kU = 4;        // tokens a batch (the next batch loaded ahead)
 
 struct ConvBwdArgs {
@@ -41,7 +41,7 @@ struct ConvBwdArgs {
   float *part;   // [runs][D][W + 1]
   float *dweight, *dbias;
   int64_t Ttot, runs;
-  int N, Tseq, D;
+  int N, Tseq, D, run;   // tokens a run
 };
 
 // kVec values of a row, as loaded and as pairs.
@@ -91,8 +91,8 @@ template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, 4) conv1d_bwd_kernel(const ConvBwdArgs a) {
   const int c0 = kVec * (blockIdx.y * kThreads + threadIdx.x);
   if (c0 >= a.D) return;
-  const int64_t t0 = (int64_t)blockIdx.x * kRun;
-  const int64_t t1 = t0 + kRun < a.Ttot ? t0 + kRun : a.Ttot;
+  const int64_t t0 = (int64_t)blockIdx.x * a.run;
+  const int64_t t1 = t0 + a.run < a.Ttot ? t0 + a.run : a.Ttot;
   const int64_t D = a.D;
   const T* __restrict__ x = static_cast<const T*>(a.x);
   const T* __restrict__ dy = static_cast<const T*>(a.dout);
@@ -359,8 +359,18 @@ void by_width(const ConvBwdArgs& a, int W, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+// Long runs spread their start and the W-1 tokens behind them over more tokens;
+// shorter ones (down to 32) while fewer than eight CTAs an SM would run.
+int run_length(int64_t tokens, int D) {
+  int run = kRun;
+  while (run > 32 && ceil_div(tokens, run) * ceil_div(D, kVec * kThreads) < 8 * sm_count()) run /= 2;
+  return run;
+}
+}  // namespace
+
 size_t conv1d_bwd_workspace_bytes(int64_t tokens, int D, int W) {
-  return align_up(sizeof(float) * (size_t)ceil_div(tokens, kRun) * D * (W + 1)) + kAlign;
+  return align_up(sizeof(float) * (size_t)ceil_div(tokens, run_length(tokens, D)) * D * (W + 1)) + kAlign;
 }
 
 gdn_status run_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, int W,
@@ -376,7 +386,8 @@ gdn_status run_causal_conv1d_bwd(const void* x, const float* weight, const float
   a.dx = dx, a.dweight = dweight, a.dbias = dbias;
   a.part = static_cast<float*>(ws);
   a.Ttot = (int64_t)B * T;
-  a.runs = ceil_div(a.Ttot, kRun);
+  a.run = run_length(a.Ttot, D);
+  a.runs = ceil_div(a.Ttot, a.run);
   a.N = N, a.Tseq = T, a.D = D;
   if (dt == GDN_F32) silu_act ? by_width<float, true>(a, W, s) : by_width<float, false>(a, W, s);
   else silu_act ? by_width<__nv_bfloat16, true>(a, W, s) : by_width<__nv_bfloat16, false>(a, W, s);

@@ -411,7 +411,8 @@ gdn_status gdn_causal_conv1d_fwd(const void* x, const float* weight, const float
  *   dweight     : out [D, W] fp32;  dbias : out [D] fp32 or NULL
  *   dinitial_state : out [N, W-1, D] of dtype dt or NULL
  *   workspace   : gdn_causal_conv1d_bwd_workspace_size(B, T, D, W) bytes (0:
- *                 invalid), 256-byte aligned (partial sums of dweight and dbias)
+ *                 invalid; query it with the device current that will run the
+ *                 call), 256-byte aligned (partial sums of dweight and dbias)
  * A sequence with malformed offsets is skipped as in the forward (no gradient of
  * it is written or added).  Sums are added in a fixed order: results do not
  * depend on the run.  Asynchronous on `stream`.

@@ -383,8 +383,10 @@ template <typename T, typename ST, typename F, int NCP>
 cudaError_t launch_q4(const Q4Args& a, int m0, int ncol, cudaStream_t s) {
   constexpr size_t bytes = F::bytes(NCP);
   auto go = [&](auto* k) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
+    if constexpr (bytes > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+      if (e != cudaSuccess) return e;
+    }
     k<<<(unsigned)ceil_div(a.N, F::ROWS), 32 * F::NW, bytes, s>>>(a, m0, ncol);
     return cudaGetLastError();
   };

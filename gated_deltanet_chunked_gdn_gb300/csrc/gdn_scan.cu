@@ -634,12 +634,12 @@ Plan make_plan(const gdn_scan_problem& p) {
   pl.cpw = 64 / pl.RL;
   pl.cbg = (int)ceil_div(p.D / p.G, pl.cpw);
   const int64_t cw = (int64_t)p.G * pl.cbg;              // warps a line of tokens
-  const int64_t fill = (int64_t)sm_count() * 27 / 2;     // warps that keep the SMs busy
+  const int64_t fill = (int64_t)sm_count() * 12;         // warps that the SMs hold (three CTAs of four each)
   // A cut costs a second run over all tokens but the last segments'.  Equal lengths
-  // are cut when fewer than three warps an SM would run, into enough segments for
-  // 13.5 (one GB300, 4096 channels, 16 states: 1 x 4096 tokens, 256 warps, 291 us
-  // uncut, 185 / 164 / 162 in 4 / 8 / 16 segments; 4 x 8192 tokens, 1024 warps, 811 us
-  // uncut, 1051 in two).  Packed sequences, whose lengths the host does not know, are
+  // are cut when fewer than three warps an SM would run, into as many segments as run
+  // at once (one GB300, 4096 channels, 16 states: 1 x 4096 tokens, 256 warps, 291 us
+  // uncut, 185 / 170 / 150 / 161 / 179 in 4 / 6 / 7 / 8 / 9 segments; 4 x 8192 tokens,
+  // 1024 warps, 811 us uncut, 1051 in two).  Packed sequences, whose lengths the host does not know, are
   // cut so that the longest ones do not outlast the rest (64 sequences of up to 2048
   // tokens, 2048 channels: 160 / 181 / 206 / 300 us with segments of 128 / 256 / 512 /
   // 1024 tokens).
@@ -651,7 +651,7 @@ Plan make_plan(const gdn_scan_problem& p) {
     pl.max_units = p.T / len + p.N;
     pl.cut = p.T > len;
   } else {
-    int64_t n = p.B * cw < 3 * sm_count() ? ceil_div(fill, p.B * cw) : 1;
+    int64_t n = p.B * cw < 3 * sm_count() ? fill / (p.B * cw) : 1;
     if (n > p.T / 128) n = p.T / 128 > 1 ? p.T / 128 : 1;
     pl.seglen = (int)align_up((size_t)ceil_div(p.T, n), kTileMax);
     pl.nseg = (int)ceil_div(p.T, pl.seglen);

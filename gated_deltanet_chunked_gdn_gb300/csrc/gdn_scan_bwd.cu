@@ -618,18 +618,34 @@ struct BwdLayout {
 
 constexpr int kMaxSeg = 8192;   // tokens a segment: bounds the states kept before the tiles
 
+// CTAs that the device holds at once (eight warps an SM, by their registers), and a
+// problem's channel blocks.
+int64_t bwd_capacity(const Plan& pl) { return (int64_t)sm_count() * (8 / bwd_warps(pl.RL)); }
+int64_t bwd_blocks(const gdn_scan_problem& p, const Plan& pl) { return p.G * ceil_div(pl.cbg, bwd_warps(pl.RL)); }
+
+// A CTA holds its place for a whole segment, so segments are made for one round of
+// CTAs: equal lengths are cut when that lets twice as many run, packed sequences into
+// halves of a CTA's share of the tokens (at least 64).
 Plan bwd_plan(const gdn_scan_problem& p) {
   Plan pl = make_plan(p);
-  if (pl.seglen > kMaxSeg) {
-    pl.seglen = kMaxSeg;
-    if (p.varlen) {
-      pl.max_units = p.T / kMaxSeg + p.N;
-      pl.cut = p.T > kMaxSeg;
-    } else {
-      pl.nseg = (int)ceil_div(p.T, kMaxSeg);
-      pl.max_units = (int64_t)p.B * pl.nseg;
-      pl.cut = pl.nseg > 1;
-    }
+  const int64_t cap = bwd_capacity(pl), cbs = bwd_blocks(p, pl);
+  int64_t len;
+  if (p.varlen) {
+    len = (int64_t)align_up((size_t)(p.T * cbs / (2 * cap)), kTileMax);
+    if (len < 64) len = 64;
+    if (len > kMaxSeg) len = kMaxSeg;
+    pl.seglen = (int)len;
+    pl.max_units = p.T / len + p.N;
+    pl.cut = p.T > len;
+  } else {
+    int64_t n = 2 * p.B * cbs <= cap ? cap / (p.B * cbs) : 1;
+    if (n > p.T / 64) n = p.T / 64 > 1 ? p.T / 64 : 1;
+    len = (int64_t)align_up((size_t)ceil_div(p.T, n), kTileMax);
+    if (len > kMaxSeg) len = kMaxSeg;
+    pl.seglen = (int)len;
+    pl.nseg = (int)ceil_div(p.T, len);
+    pl.max_units = (int64_t)p.B * pl.nseg;
+    pl.cut = pl.nseg > 1;
   }
   return pl;
 }
@@ -641,7 +657,7 @@ BwdLayout bwd_layout(const gdn_scan_problem& p, const Plan& pl) {
   const int tt = pl.RL >= 4 ? 16 : 4 * pl.RL;
   const int64_t most = p.T < pl.seglen ? p.T : pl.seglen;
   l.tiles = (int)ceil_div(most > 0 ? most : 1, tt);
-  const int64_t cbs = (int64_t)p.G * l.cgrp, want = ceil_div((int64_t)sm_count() * 2, cbs);
+  const int64_t cbs = bwd_blocks(p, pl), cap = bwd_capacity(pl), want = cap / cbs > 1 ? cap / cbs : 1;
   l.slots = (int)(pl.max_units < want ? pl.max_units : want);
   const size_t DS = (size_t)p.D * p.S, f = sizeof(float);
   size_t o = 0;

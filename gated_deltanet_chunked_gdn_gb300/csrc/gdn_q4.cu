@@ -78,7 +78,10 @@ __device__ __forceinline__ void decode(uint32_t w, __nv_bfloat162 off, uint32_t 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     // byte j of w (its low nibble is the first code) and of h (the second)
-    uint32_t v = (__byte_perm(w, h, 0x0400 + 0x1111 * j) & 0x000f000fu) | 0x3f003f00u;
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"   // (a & b) | c
+        : "=r"(v)
+        : "r"(__byte_perm(w, h, 0x0400 + 0x1111 * j)), "r"(0x000f000fu), "r"(0x3f003f00u));
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
     p[j] = *reinterpret_cast<const uint32_t*>(&d);
   }
@@ -170,18 +173,22 @@ __global__ void __launch_bounds__(32 * F::NW) q4_matvec_kernel(const Q4Args a, i
 
   const int nb = (a.K + kBlock - 1) / kBlock;   // the last block may be short (groups of 32 or 64)
   const int b0 = (int)((int64_t)nb * kw / KW), b1 = (int)((int64_t)nb * (kw + 1) / KW);
-  const int row0 = 16 * MT * (RW * blockIdx.x + rw);
-  const uint8_t* wsrc[MT][2];   // the next block to fetch
-  int64_t srow[MT][2];
+  // 32-bit offsets from the CTA's first row (at most 128 rows of 2^20 codes): addresses
+  // and predicates would otherwise cost as much as the codes' conversion
+  const int first = F::ROWS * blockIdx.x;
+  const uint8_t* wbase = a.w + (int64_t)first * (a.K / 2);
+  const ST* sbase = static_cast<const ST*>(a.scale) + (int64_t)first * a.groups;
+  const uint8_t* zbase = a.zero ? a.zero + (int64_t)first * a.groups : nullptr;
+  uint32_t woff[MT][2], soff[MT][2];
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = min(row0 + 16 * t + r + 8 * h, a.N - 1);   // past the end: not stored
-      wsrc[t][h] = a.w + row * (int64_t)(a.K / 2) + (int64_t)b0 * (kBlock / 2) + 16 * c;
-      srow[t][h] = row * (int64_t)a.groups;
+      const int row = min(16 * (MT * rw + t) + r + 8 * h, a.N - 1 - first);   // past the end: not stored
+      woff[t][h] = row * (uint32_t)(a.K / 2) + 16 * c;
+      soff[t][h] = row * (uint32_t)a.groups;
     }
-  const ST* scale = static_cast<const ST*>(a.scale);
+  const int bw = min(b1, (a.K - 32 * c + kBlock - 1) / kBlock);   // blocks in which this lane's codes exist
 
   // word kc's pieces stand in the order col ^ swz(kc): the reads below take two
   // neighbouring columns of four words at a time
@@ -189,22 +196,21 @@ __global__ void __launch_bounds__(32 * F::NW) q4_matvec_kernel(const Q4Args a, i
   // x of a block: this lane brings word kcol of columns col0, col0 + 2 RW, ..
   const int kcol = lane % 16, col0 = 2 * rw + lane / 16, sw = swz(kcol) & (NCP - 1);
   const T* xsrc = static_cast<const T*>(a.x) + (m0 + col0 / P) * a.ldx + b0 * (int64_t)kBlock + 8 * kcol;
+  const int bx = (a.K - 8 * kcol + kBlock - 1) / kBlock;   // .. its words of x
   auto fetch = [&](int b, int slot) {
     // (what stands behind the last codes of a short block meets zeros of x)
-    if (b < b1 && b * kBlock + 32 * c < a.K) {
+    if (b < bw) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                            sm100::smem_u32(ring + (slot * MT * 2 + t * 2 + h) * 32)),
-                       "l"(wsrc[t][h])
+                       "l"(wbase + (woff[t][h] + (uint32_t)b * (kBlock / 2)))
                        : "memory");
-          wsrc[t][h] += kBlock / 2;
-        }
     }
     if (b < b1) {
-      const bool have = b * kBlock + 8 * kcol < a.K;
+      const bool have = b < bx;
       uint4* dst = xring + (slot * 16 + kcol) * NCP;
       const T* src = xsrc;
 #pragma unroll
@@ -244,8 +250,8 @@ __global__ void __launch_bounds__(32 * F::NW) q4_matvec_kernel(const Q4Args a, i
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        sc[t][h] = scale[srow[t][h] + g];
-        ze[t][h] = a.zero ? a.zero[srow[t][h] + g] : 8;
+        sc[t][h] = sbase[soff[t][h] + g];
+        ze[t][h] = zbase ? zbase[soff[t][h] + g] : 8;
       }
   };
   load_scales(b0, s1, z1);

@@ -741,7 +741,9 @@ gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* de
 gdn_status run_scan_step(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
                          const void* C, const float* Dp, const void* z, const float* dt_bias, float* state,
                          const int32_t* state_indices, int state_slots, const int32_t* cu, void* y, cudaStream_t s) {
-  const Plan pl = make_plan(p);
+  Plan pl = {};   // (no segments here)
+  pl.RL = lanes_for(p.S);
+  pl.nseg = 1;
   StepArgs sa;
   sa.a = base_args(p, pl, x, delta, A, B, C, Dp, z, dt_bias, nullptr, cu);
   sa.a.y = y;

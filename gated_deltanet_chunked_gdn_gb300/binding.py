@@ -588,6 +588,8 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
         if need == 0:
             raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_selective_scan_fwd_workspace_size")
         workspace = _alloc_ws(need, x.device)
+        if stream is not None:   # not handed out again before that stream is done with it
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=x.device))
     s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_selective_scan_fwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                     _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),

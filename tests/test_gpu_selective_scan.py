@@ -131,8 +131,26 @@ def test_scan_on_another_stream_and_twice(gdn):
     s.wait_stream(torch.cuda.current_stream())
     gdn.gdn_selective_scan_fwd(**inp, y=y2, ht=ht2, workspace=ws, stream=s.cuda_stream)
     s.synchronize()
+    y3, _ = gdn.gdn_selective_scan_fwd(**inp, stream=s.cuda_stream)   # its own workspace, on that stream
+    s.synchronize()
+    assert torch.equal(y, y3)
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(ht, ht2)
+
+
+def test_scan_all_sequences_empty(gdn):
+    inp = R.make_scan(1, 0, 20, 8, 1, "bf16", init=True, lens=[0, 0, 0], seed=15)
+    d = cuda(inp)
+    y, ht = gdn.gdn_selective_scan_fwd(**d, cu_seqlens=offsets([0, 0, 0]))
+    assert y.shape == (1, 0, 20) and torch.equal(ht, d["h0"])
+    dht = torch.randn_like(ht)
+    g = gdn.gdn_selective_scan_bwd(**d, dout=torch.empty_like(d["x"]), dht=dht, cu_seqlens=offsets([0, 0, 0]))
+    torch.cuda.synchronize()
+    assert torch.equal(g["dh0"], dht) and torch.all(g["dA"] == 0) and torch.all(g["dD"] == 0)
+    state = d.pop("h0").clone()
+    before = state.clone()
+    gdn.gdn_selective_scan_step(**d, state=state, cu_seqlens=offsets([0, 0, 0]))
+    assert torch.equal(state, before)
 
 
 def test_scan_offsets_past_32_bits(gdn):

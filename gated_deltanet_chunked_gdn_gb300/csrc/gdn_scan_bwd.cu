@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(256) rev_chain_kernel(const BwdArgs b) {
 
 // ------------------------------------------------------------ the gradients
 
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
+
 // Warps of a CTA (one group's channels), and its shared memory.
 constexpr int kBwdRing = 3;   // tiles as loaded: one in use, two on their way
 constexpr int bwd_warps(int RL) { return RL >= 8 ? 4 : 8; }
@@ -253,9 +255,10 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
   const bool gate = a.z != nullptr;
   constexpr float kLn2 = 0.6931471805599453f;
 
-  float2 A2[2][2], dA[2][2];
+  float2 A2[2][2], dA[2][2], lost[2][2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
+    lost[c][0] = lost[c][1] = make_float2(0.f, 0.f);
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     if (c ? ok1 : ok0) load4(a.A + (int64_t)(d + c) * a.S + n0, nn, v4, r);
     A2[c][0] = make_float2(r[0] * sm100::kLog2e, r[1] * sm100::kLog2e);
@@ -538,7 +541,11 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) dA[c][e] = __fadd2_rn(dA[c][e], tA[c][e]);
+        for (int e = 0; e < 2; ++e) {   // what each addition drops is put back into the next
+          const float2 y = sub2(tA[c][e], lost[c][e]), sum = __fadd2_rn(dA[c][e], y);
+          lost[c][e] = sub2(sub2(sum, dA[c][e]), y);
+          dA[c][e] = sum;
+        }
       // dB and dC of the CTA's channels
       __syncthreads();
       for (int p = threadIdx.x; p < L::TT * 2 * L::SP; p += NT) {

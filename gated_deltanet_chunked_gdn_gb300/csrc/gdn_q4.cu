@@ -1,6 +1,6 @@
 // gdn_q4.cu -- a few rows times a matrix of 4-bit weights with group scales:
 //     y[m][n] = sum_k x[m][k] (code[n][k] - zero[n][k / g]) scale[n][k / g] + bias[n]
-// (the projections of a decode step).  Bound by the weights' bytes, N K / 2.
+// (the projections of a decode step).  Its floor is the weights' bytes, N K / 2.
 //
 // Codes are read as they are stored (rows of K nibbles) and become tensor-core
 // operands in registers: a nibble j in the low bits of a bf16's mantissa on top of
@@ -9,17 +9,17 @@
 // again exactly.  mma.sync m16n8k16 then multiplies 16 weight rows by 8 columns of x
 // with fp32 sums; 256 times the group's scale multiplies the fp32 sum, so no weight is
 // ever rounded (and codes below 1 keep large fp32 x from overflowing before the scale).
-// mma.sync and not tcgen05: for a few rows the weights are used once, and their way as
-// bf16 through shared memory would cost more than the products; what bounds the loop
-// beside HBM is turning codes into operands (about 13 instructions for eight).  From 16
-// rows on mma.sync's own rate does.
+// mma.sync and not tcgen05: for a few rows the weights are used once, and they stay in
+// registers on their way to the products.  What bounds the loop at one row is turning
+// codes into operands (16384 x 8192, by ncu: ALU pipe 70 %, mma.sync pipe 15 %, DRAM
+// 31 %).  At 32 rows no unit is full (mma.sync 29 %, ALU 32 %, IPC 1.4 of 4): latency at
+// 8 warps an SM.
 //
 // The k order inside an mma is free as long as both operands share it, but all its
 // products have to be of one group.  A lane loads 16 bytes (32 codes) of a row, the
 // four lanes of a row 128 codes (a block).  Groups of 64 or 32 are smaller than that:
 // the four lanes exchange words (2 or 4 shuffles a 16 bytes) so that each mma's words
-// come from one group, which costs less than narrower loads, whose requests touch a
-// row's line for 16 bytes only.
+// come from one group, and keep the wide loads.
 //
 // Weights and x come by asynchronous copies into rings of blocks; every lane
 // copies the weights that it reads itself.  x stands in pieces of eight values,
@@ -409,15 +409,16 @@ cudaError_t launch_q4(const Q4Args& a, int m0, int ncol, cudaStream_t s) {
   return by_vec(std::integral_constant<int, 2>());
 }
 
-// Which configuration (one GB300, us a call, bf16).  One row of x: 16 weight rows a
+// Which configuration (one GB300, us a call, bf16; both sides of each choice as it was
+// taken: with 32-bit offsets the kept sides are 25.0 for one row, 36.1 for
+// eight and 36.8 for 16 of 16384 x 8192, 8.1 for two of 4096 x 4096, 22.6 for five).  One row of x: 16 weight rows a
 // warp and short rings, so that three CTAs share an SM (16384 x 8192 codes 26.6; 32
 // rows a warp and rings of six 28.8).  Up to 4 columns, warps in pairs on one copy of
 // x (2 rows, 4096 x 4096: 8.5; alone 9.3).  Up to 8: 32 rows a warp once they fill the
 // SMs (8 rows, 16384 x 8192: 40 against 46; 5 rows, 12288 x 4096: 26 against 23).  Up
 // to 16: 32 rows a warp, four warps on one x (40; 59 with 16 rows and two).  fp32 x,
 // cut by the warps that bring it: fewer warps to a share (4 rows, 4096 x 4096: 22; 37).
-// 17 to 32: the mma are what counts, at about 24 cycles each a sub-partition (two
-// thirds of the 60 us of 32 rows, 16384 x 8192).
+// 17 to 32: 58 us for 32 rows, 16384 x 8192.
 template <typename T, typename ST>
 cudaError_t run_rows(const Q4Args& a, cudaStream_t s) {
   constexpr int P = kParts<T>;

@@ -4,14 +4,22 @@
 // scalar functions are in gdn_scan.cuh.
 //
 // Forward.  Each warp runs its channels through a segment of a sequence on its
-// own (no block barrier): tiles of 16 tokens, whose x, delta, z, B and C are
-// loaded one tile ahead into registers; the tile's steps (softplus), dt x, B and
+// own (no block barrier): tiles of 16 tokens, whose x, delta, z, B and C come by
+// asynchronous copies two tiles ahead (rows that are not aligned: through
+// registers); the tile's steps (softplus), dt x, B and
 // C go through a few KB of shared memory as fp32, and every token is then
 //     a = 2^{dt A log2 e}, h = a h + (dt x) B, y = sum_n C h
 // on 2 x 4 states a lane, the products on packed fp32 pairs.  The sums over the
 // state lanes are reduce-scattered four tokens at a time, so that a lane ends
 // with the token whose x and z it loaded.  Per state: one ex2 and four FMA-pipe
 // operations, which both units (32 and 128 lanes a cycle) pass in the same time.
+//
+// What bounds it (one GB300): neither unit nor HBM, but issue and latency at the
+// few warps that the chains make.  57 instructions a token and warp (256 updates),
+// IPC 2.0 of 4, where a packed pair takes two issue slots; ex2 34 %, LSU wavefronts
+// 49 %, DRAM 14 % (by ncu).  4096 channels, 16 states, bf16, gated: 4 x 8192 tokens
+// 0.81 ms, 1 x 4096 tokens 0.148 ms in seven segments (states 56 us, chain 4,
+// outputs 86).
 //
 // Few chains.  When the channels of all sequences do not fill the SMs, sequences
 // are cut into segments: a states-only pass runs every segment but a sequence's

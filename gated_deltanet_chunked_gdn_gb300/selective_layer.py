@@ -68,6 +68,15 @@ def dequantize(qweight: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
     return (q * scales.float()[..., None]).view(qweight.shape[0], -1)
 
 
+def _pool_rows(slots, size):
+    """(src, rows, some): every sequence's final state goes to row ``rows[n]`` of a pool of ``size`` rows, taken from
+    sequence ``src[n]``.  A sequence whose slot is outside the pool has no state and repeats the first that has one
+    (the same value to the same row), so that the device decides and the host does not wait; ``some``: there is one."""
+    known = (slots >= 0) & (slots < size)
+    src = torch.where(known, torch.arange(slots.numel(), device=slots.device), known.int().argmax())
+    return src, slots[src].long().clamp(0, size - 1), known.any()
+
+
 class SelectiveLayer(torch.nn.Module):
     """width: the model's; channels D, states S a channel, groups G that share B and C, W taps, rank of the step."""
 
@@ -122,7 +131,9 @@ class SelectiveLayer(torch.nn.Module):
 
     @torch.no_grad()
     def prompt(self, u, states, slots, cu_seqlens=None):
-        """New sequences' prompts; their states go to the pools' rows ``slots`` (int32)."""
+        """New sequences' prompts; their states go to the pools' rows ``slots`` (int32).  A slot outside the pools
+        means "no state": the outputs are computed and nothing is kept.  Malformed cu_seqlens leave the scan's pool
+        as it is."""
         conv, scan = states
         n = cu_seqlens.numel() - 1 if cu_seqlens is not None else u.shape[0]
         x, z = (u @ self.in_proj.t()).chunk(2, dim=-1)
@@ -131,9 +142,11 @@ class SelectiveLayer(torch.nn.Module):
                                                                                          device=u.device),
                                       cu_seqlens=cu_seqlens)
         dt, B, C = self._split(x @ self.x_proj.t())
+        src, rows, some = _pool_rows(slots, scan.shape[0])
+        before = scan[rows]
         y, ht = gdn.gdn_selective_scan_fwd(x, dt @ self.dt_proj.t(), -torch.exp(self.A_log), B, C, D=self.Dskip, z=z,
-                                           dt_bias=self.dt_bias, cu_seqlens=cu_seqlens)
-        scan[slots.long()] = ht
+                                           dt_bias=self.dt_bias, cu_seqlens=cu_seqlens, ht=before.clone())
+        scan[rows] = torch.where(some, ht[src], before)
         return y @ self.out_proj.t()
 
     @torch.no_grad()

@@ -1,0 +1,79 @@
+"""The selective layer's own arithmetic on the CPU (no GPU): the operators that it
+calls are replaced by their definitions in 64 bits, with the library's rules for
+slots."""
+import pytest
+import torch
+
+import selective_reference as R
+from gated_deltanet_chunked_gdn_gb300 import selective_layer as mod
+
+
+def lens_of(cu):
+    return None if cu is None else (cu[1:] - cu[:-1]).tolist()
+
+
+def conv_fwd(x, weight, bias=None, activation="silu", conv_state=None, cache_indices=None, has_initial_state=None,
+             cu_seqlens=None):
+    """gdn_causal_conv1d_fwd from zero initial inputs; a slot outside the pool means that nothing is written."""
+    lens = lens_of(cu_seqlens)
+    if lens is not None and min(lens) < 0:
+        return torch.zeros_like(x)
+    y, final = R.conv(x, weight, bias, activation, lens=lens)
+    if conv_state is not None:
+        for n, slot in enumerate(cache_indices.tolist()):
+            if 0 <= slot < conv_state.shape[0]:
+                conv_state[slot] = final[n].to(conv_state.dtype)
+    return y.to(x.dtype)
+
+
+def scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, ht=None,
+             output_final_state=True):
+    """gdn_selective_scan_fwd; malformed offsets leave ht unwritten."""
+    lens = lens_of(cu_seqlens)
+    if ht is None:
+        ht = torch.full((len(lens or x), *A.shape), float("nan"))
+    if lens is not None and (min(lens) < 0 or sum(lens) != x.shape[1]):
+        return torch.zeros_like(x), ht
+    y, h = R.scan(x, delta, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=h0, lens=lens)
+    ht.copy_(h)
+    return y.to(x.dtype), ht
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    monkeypatch.setattr(mod.gdn, "gdn_causal_conv1d_fwd", conv_fwd)
+    monkeypatch.setattr(mod.gdn, "gdn_selective_scan_fwd", scan_fwd)
+    torch.manual_seed(0)
+    return mod.SelectiveLayer(8, 6, states=4, rank=32, device="cpu")
+
+
+def prompt(layer, slots, cu=None):
+    torch.manual_seed(1)
+    u = torch.randn(3, 5, 8).bfloat16() if cu is None else torch.randn(1, cu[-1], 8).bfloat16()
+    conv, scan = layer.new_states(5)
+    conv.fill_(3.0), scan.fill_(7.0)
+    out = layer.prompt(u, (conv, scan), torch.tensor(slots, dtype=torch.int32),
+                       None if cu is None else torch.tensor(cu, dtype=torch.int32))
+    return out, conv, scan
+
+
+@pytest.mark.parametrize("slots", [[-1, 2, 0], [1, 5, 4], [3, -7, 99], [4, 1, -1], [-1, -1, 5]])
+@pytest.mark.parametrize("cu", [None, [0, 4, 4, 11]])
+def test_prompt_slots_outside_the_pool(layer, slots, cu):
+    """A sequence whose slot is outside the pool has no state: both pools' other rows keep their values to the bit,
+    and the sequences with slots get the states that they get alone."""
+    out, conv, scan = prompt(layer, slots, cu)
+    ref, conv_ref, scan_ref = prompt(layer, [0, 1, 2], cu)
+    assert torch.equal(out, ref)
+    for row in range(5):
+        if row in slots:
+            assert torch.equal(scan[row], scan_ref[slots.index(row)])
+            assert torch.equal(conv[row], conv_ref[slots.index(row)])
+        else:
+            assert torch.all(scan[row] == 7.0) and torch.all(conv[row] == 3.0)
+
+
+def test_prompt_malformed_offsets_leave_the_scan_states(layer):
+    """The scan writes no final states then, so none may reach the pool."""
+    _, _, scan = prompt(layer, [3, 0, 1], [0, 8, 2, 11])
+    assert torch.all(scan == 7.0)

@@ -485,6 +485,20 @@ except AttributeError:
         return torch.cuda.current_stream(index).cuda_stream
 
 
+def _lend(stream: int, device, blocks) -> None:
+    """Hands blocks that a call has allocated (None among them) to the stream that it runs on.  They come from the
+    current stream's pool, where work queued earlier may still use their memory and where they return when they are
+    dropped: another stream waits for that work, and the memory is not given out again before it is done."""
+    blocks = [b for b in blocks if b is not None]
+    here = torch.cuda.current_stream(device)
+    if not blocks or stream == here.cuda_stream:
+        return
+    other = torch.cuda.ExternalStream(stream, device=device)
+    other.wait_stream(here)
+    for b in blocks:
+        b.record_stream(other)
+
+
 def _row_stride(name: str, t: torch.Tensor, row: int) -> int:
     """Elements from one token's row of t [B, T, ...] to the next; the rows themselves contiguous, the
     sequences of a batch one after the other at the same stride."""
@@ -579,6 +593,7 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (("h0", h0, state), ("ht", ht, state)),
                       (("y", y),) if y is not None else ())
+    given = y, ht, workspace
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if ht is None and output_final_state:
@@ -588,8 +603,8 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
         if need == 0:
             raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_selective_scan_fwd_workspace_size")
         workspace = _alloc_ws(need, x.device)
-        if stream is not None:   # not handed out again before that stream is done with it
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=x.device))
+    if stream is not None:
+        _lend(stream, x.device, [t for t, g in zip((y, ht, workspace), given) if g is None])
     s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_selective_scan_fwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                     _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
@@ -631,6 +646,8 @@ def gdn_selective_scan_step(x, delta, A, B, C, state, D=None, z=None, dt_bias=No
         idx = state_indices.data_ptr()
     if y is None:
         y = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if stream is not None:
+            _lend(stream, x.device, (y,))
     st = lib.gdn_selective_scan_step(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                      0 if D is None else D.data_ptr(), 0 if z is None else z.data_ptr(),
                                      0 if dt_bias is None else dt_bias.data_ptr(), state.data_ptr(), idx, slots,
@@ -656,6 +673,7 @@ def gdn_selective_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
                       (("h0", h0, state), ("dht", dht, state)), (("dout", dout),))
+    given = workspace
     if workspace is None:
         need = lib.gdn_selective_scan_bwd_workspace_size(p)
         if need == 0:
@@ -671,6 +689,8 @@ def gdn_selective_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None
            "dz": torch.empty(x.shape, **like) if z is not None else None,
            "ddt_bias": torch.empty(dt_bias.shape, **f32) if dt_bias is not None else None,
            "dh0": torch.empty(state, **f32) if want_dh0 else None}
+    if stream is not None:
+        _lend(stream, x.device, (*out.values(), workspace if given is None else None))
     s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_selective_scan_bwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                     _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
@@ -705,6 +725,7 @@ def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial
                                   ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))):
         if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.shape != shape):
             raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    given = workspace
     if workspace is None:
         need = lib.gdn_causal_conv1d_bwd_workspace_size(B, T, D, W)
         if need == 0:
@@ -716,6 +737,8 @@ def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial
     out = {"dx": torch.empty_like(x), "dweight": torch.empty((D, W), **f32),
            "dbias": torch.empty((D,), **f32) if bias is not None else None,
            "dinitial_state": torch.empty(state, dtype=x.dtype, device=x.device) if want_dinitial_state else None}
+    if stream is not None:
+        _lend(stream, x.device, (*out.values(), workspace if given is None else None))
     s = stream if stream is not None else _current_stream(x.get_device())
     st = lib.gdn_causal_conv1d_bwd(x.data_ptr(), weight.data_ptr(), _address(bias), W, _address(initial_state),
                                    _address(cu_seqlens), N, B, T, D, DTYPES[x.dtype], ACTIVATIONS[activation],
@@ -755,6 +778,8 @@ def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None
         raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
     if y is None:
         y = torch.empty((*x.shape[:-1], N), dtype=dtype, device=x.device)
+        if stream is not None:
+            _lend(stream, x.device, (y,))
     elif y.shape != (*x.shape[:-1], N) or y.dtype != dtype or y.get_device() != dev or not y.is_contiguous():
         raise ValueError("y must be a contiguous CUDA tensor [..., N] with the dtype of x")
     s = stream if stream is not None else _current_stream(dev)

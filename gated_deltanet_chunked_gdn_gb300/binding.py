@@ -229,6 +229,7 @@ def gdn_chunk_fwd(q, k, v, g, beta, scale: Optional[float] = None, h0=None, cu_s
     p = problem_of(q, v, C, cu_seqlens)
     if scale is None:
         scale = q.shape[-1] ** -0.5
+    given = o, ht, workspace
     if o is None:
         o = torch.empty_like(v)
     if ht is None and output_final_state:
@@ -238,6 +239,8 @@ def gdn_chunk_fwd(q, k, v, g, beta, scale: Optional[float] = None, h0=None, cu_s
         raise GDNError(GDN_ERR_UNSUPPORTED if path in ("fused", "cp", "fused1") else GDN_ERR_INVALID_ARG, "gdn_chunk_fwd_workspace_size")
     if workspace is None:
         workspace = _alloc_ws(need, q.device)
+    if stream is not None:
+        _lend(stream, q.device, [t for t, g in zip((o, ht, workspace), given) if g is None])
     s = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
     st = lib.gdn_chunk_fwd(ctypes.byref(p), PATHS[path], _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                            ctypes.c_float(scale), _ptr(h0), _ptr(cu_seqlens), _ptr(o), _ptr(ht), _ptr(workspace),
@@ -276,6 +279,8 @@ def gdn_chunk_fwd_host(q, k, v, g, beta, scale: Optional[float] = None, h0=None,
         raise GDNError(GDN_ERR_INVALID_ARG, "gdn_chunk_fwd_host_workspace_size")
     if workspace is None:
         workspace = _alloc_ws(need, dev)
+        if stream is not None:
+            _lend(stream, dev, (workspace,))
     s = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
     st = lib.gdn_chunk_fwd_host(ctypes.byref(p), PATHS[path], int(nsplit), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                                 _ptr(beta), ctypes.c_float(scale), _ptr(h0), _ptr(cu_seqlens), _ptr(o), _ptr(ht),
@@ -305,10 +310,13 @@ def gdn_chunk_fwd_staged(q, k, v, g, beta, scale: Optional[float] = None, h0=Non
         scale = q.shape[-1] ** -0.5
     stop = STAGES[stop_after] if isinstance(stop_after, str) else int(stop_after)
     layout = gdn_staged_layout(p)
+    given = workspace
     o = torch.zeros_like(v)
     ht = torch.zeros((p.N, p.Hv, p.K, p.V), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = _alloc_ws(layout.total, q.device)
+    if stream is not None:
+        _lend(stream, q.device, (o, ht, workspace if given is None else None))
     s = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
     st = lib.gdn_chunk_fwd_staged(ctypes.byref(p), stop, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                   ctypes.c_float(scale), _ptr(h0), _ptr(cu_seqlens), _ptr(o), _ptr(ht),
@@ -372,6 +380,8 @@ def gdn_recurrent_fwd(q, k, v, a, b, A_log, state, dt_bias=None, scale: Optional
         scale = q.shape[-1] ** -0.5
     if o is None:
         o = torch.empty_like(v)
+        if stream is not None:
+            _lend(stream, q.device, (o,))
     s = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
     st = lib.gdn_recurrent_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b), _ptr(A_log),
                                _ptr(dt_bias), ctypes.c_float(scale), _ptr(state), _ptr(state_indices),
@@ -413,6 +423,8 @@ def gdn_causal_conv1d_fwd(x, weight, bias=None, activation="silu", conv_state=No
     N = int(cu_seqlens.numel()) - 1 if cu_seqlens is not None else B
     if y is None:
         y = torch.empty_like(x)
+        if stream is not None:
+            _lend(stream, x.device, (y,))
     slots = int(conv_state.shape[0]) if conv_state is not None else 0
     s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
     st = lib.gdn_causal_conv1d_fwd(_ptr(x), _ptr(weight), _ptr(bias), W, _ptr(conv_state), slots,
@@ -448,12 +460,15 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale: Optional[float] = None, h0=None
     need = gdn_chunk_bwd_workspace_size(p)
     if need == 0:
         raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_chunk_bwd_workspace_size")
+    given = workspace
     if workspace is None:
         workspace = _alloc_ws(need, q.device)
     f32 = dict(dtype=torch.float32, device=q.device)
     out = {"dq": torch.empty(q.shape, **f32), "dk": torch.empty(k.shape, **f32), "dv": torch.empty(v.shape, **f32),
            "dg": torch.empty(g.shape, **f32), "dbeta": torch.empty(beta.shape, **f32),
            "dh0": torch.empty((p.N, p.Hv, p.K, p.V), **f32) if want_dh0 else None}
+    if stream is not None:
+        _lend(stream, q.device, (*out.values(), workspace if given is None else None))
     s = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
     st = lib.gdn_chunk_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.c_float(scale),
                            _ptr(h0), _ptr(cu_seqlens), _ptr(dout), _ptr(dht), _ptr(out["dq"]), _ptr(out["dk"]),

@@ -14,11 +14,45 @@ convolution and the scan's state.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
 
 from . import binding as gdn
+
+
+class _FirstOrder(torch.autograd.Function):
+    """Gradients as they are; differentiating them again raises."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return grads
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the selective layer's operators have first derivatives only: their gradients cannot be "
+                           "differentiated again")
+
+
+def _first_order(backward):
+    """For a backward that torch cannot differentiate.  Under create_graph its gradients would count as constants;
+    here they depend on something, so that a second derivative through them raises, whether or not the incoming
+    gradient needs one (the operator's inputs, which they depend on too, may)."""
+
+    @functools.wraps(backward)
+    def call(ctx, *dys):
+        with torch.no_grad():
+            grads = backward(ctx, *dys)
+        if not torch.is_grad_enabled():   # no graph of the gradients is wanted
+            return grads
+        some = [i for i, g in enumerate(grads) if g is not None]
+        anchor = torch.zeros((), device=grads[some[0]].device, requires_grad=True)
+        grads = list(grads)
+        for i, g in zip(some, _FirstOrder.apply(anchor, *(grads[i] for i in some))):
+            grads[i] = g
+        return tuple(grads)
+    return call
 
 
 class CausalConv1d(torch.autograd.Function):
@@ -30,6 +64,7 @@ class CausalConv1d(torch.autograd.Function):
         return gdn.gdn_causal_conv1d_fwd(x, weight, bias, "silu", cu_seqlens=cu_seqlens)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, weight, bias, cu = ctx.saved_tensors
         g = gdn.gdn_causal_conv1d_bwd(x, weight, dy.contiguous(), bias=bias, activation="silu", cu_seqlens=cu)
@@ -46,6 +81,7 @@ class SelectiveScan(torch.autograd.Function):
                                           output_final_state=False)[0]
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, delta, A, B, C, D, z, dt_bias, cu = ctx.saved_tensors
         g = gdn.gdn_selective_scan_bwd(x, delta, A, B, C, dy.contiguous(), D=D, z=z, dt_bias=dt_bias, cu_seqlens=cu)

@@ -77,3 +77,71 @@ def test_prompt_malformed_offsets_leave_the_scan_states(layer):
     """The scan writes no final states then, so none may reach the pool."""
     _, _, scan = prompt(layer, [3, 0, 1], [0, 8, 2, 11])
     assert torch.all(scan == 7.0)
+
+
+def conv_bwd(x, weight, dout, bias=None, activation="silu", cu_seqlens=None):
+    leaves = [t.double().requires_grad_() for t in (x, weight, bias)]
+    with torch.enable_grad():
+        y, _ = R.conv(*leaves, activation, lens=lens_of(cu_seqlens))
+    g = torch.autograd.grad(y, leaves, dout.double())
+    return {"dx": g[0].to(x.dtype), "dweight": g[1].float(), "dbias": g[2].float()}
+
+
+def scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None, cu_seqlens=None):
+    inp = {"x": x, "delta": delta, "A": A, "B": B, "C": C, "D": D, "z": z, "dt_bias": dt_bias}
+    with torch.enable_grad():
+        g = R.scan_grads(inp, dout, lens=lens_of(cu_seqlens))
+    return {"d" + k: g[k].to(v.dtype) for k, v in inp.items()}
+
+
+@pytest.fixture
+def training(layer, monkeypatch):
+    monkeypatch.setattr(mod.gdn, "gdn_causal_conv1d_bwd", conv_bwd)
+    monkeypatch.setattr(mod.gdn, "gdn_selective_scan_bwd", scan_bwd)
+    return layer
+
+
+def test_second_derivatives_are_refused(training):
+    """They are not built: a penalty on a gradient raises rather than leaving the operators' part of it out."""
+    u = torch.randn(2, 7, 8).bfloat16().requires_grad_()
+    (du,) = torch.autograd.grad(training(u).float().square().sum(), u, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        du.float().square().sum().backward()
+
+
+@pytest.mark.parametrize("op", ["conv", "scan"])
+def test_second_derivatives_are_refused_for_constant_upstream_gradients(training, op):
+    """The incoming gradient is a constant here, the operator's inputs are not."""
+    w = torch.randn(6, 6).requires_grad_()
+    v = torch.randn(1, 9, 6)
+    u = torch.randn(1, 9, 6).requires_grad_()
+    if op == "conv":
+        y = mod.CausalConv1d.apply(u @ w, torch.randn(6, 4), torch.randn(6), None)
+    else:
+        bc = torch.randn(1, 9, 1, 4)
+        y = mod.SelectiveScan.apply(u @ w, v, -torch.rand(6, 4), bc, bc, torch.randn(6), v, torch.randn(6), None)
+    (du,) = torch.autograd.grad(y.sum(), u, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        du.square().sum().backward()
+
+
+@pytest.mark.parametrize("cu", [None, [0, 4, 4, 11]])
+def test_first_derivatives(training, cu):
+    """Through torch's own operators the layer would have these (with and without a graph of them): bf16 roundings
+    on the way, once a tensor, on both sides alike; the recurrences themselves are the same numbers."""
+    u = torch.randn(*((2, 7) if cu is None else (1, 11)), 8).bfloat16()
+    cu = None if cu is None else torch.tensor(cu, dtype=torch.int32)
+    params = list(training.parameters())
+    plain = torch.autograd.grad(training(u, cu).float().square().sum(), params)
+    graph = torch.autograd.grad(training(u, cu).float().square().sum(), params, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(plain, graph))
+
+    x, z = (u @ training.in_proj.t()).chunk(2, dim=-1)
+    x, _ = R.conv(x, training.conv_weight, training.conv_bias, lens=lens_of(cu))
+    x = x.bfloat16()
+    dt, B, C = training._split(x @ training.x_proj.t())
+    y, _ = R.scan(x, dt @ training.dt_proj.t(), -torch.exp(training.A_log), B, C, D=training.Dskip, z=z,
+                  dt_bias=training.dt_bias, lens=lens_of(cu))
+    want = torch.autograd.grad((y.bfloat16() @ training.out_proj.t()).float().square().sum(), params)
+    for a, b in zip(plain, want):
+        assert (a.double() - b.double()).norm() <= 2e-2 * b.double().norm()

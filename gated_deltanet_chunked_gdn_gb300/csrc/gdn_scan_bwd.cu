@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
   }
   const float2 bias = make_float2(a.bias && ok0 ? a.bias[d] : 0.f, a.bias && ok1 ? a.bias[d + 1] : 0.f);
   const float2 skip = make_float2(a.Dp && ok0 ? a.Dp[d] : 0.f, a.Dp && ok1 ? a.Dp[d + 1] : 0.f);
-  float2 dD = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f);
+  float2 dD = make_float2(0.f, 0.f), dbias = dD, lostD = dD, lostb = dD;
   float4* ck = b.ck + ((int64_t)(blockIdx.y * b.slots + blockIdx.x) * b.tiles) * (W * 64) + w * 64 + ln.lane;
 
   Unit u;
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
         h[0][0] = k00, h[0][1] = k01, h[1][0] = k10, h[1][1] = k11;
       }
       const float2 first00 = h[0][0], first01 = h[0][1], first10 = h[1][0], first11 = h[1][1];
-      // dA of the tile first: a sum over all tokens in one place would lose small terms
-      float2 tA[2][2];
+      // dA, dD and ddt_bias of the tile first: a sum over all tokens in one place would lose small terms
+      float2 tA[2][2], tD = make_float2(0.f, 0.f), tb = tD;
 #pragma unroll
       for (int c = 0; c < 2; ++c) tA[c][0] = tA[c][1] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -541,8 +541,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
             const int64_t o = (u.tok0 + t) * a.D + d;
             store2(static_cast<T*>(b.dx) + o, dx, b.vo, ok0, ok1);
             store2(static_cast<T*>(b.ddelta) + o, dd, b.vo, ok0, ok1);
-            dD.x = fmaf(dy.x, x.x, dD.x), dD.y = fmaf(dy.y, x.y, dD.y);
-            dbias.x += dd.x, dbias.y += dd.y;
+            tD = __ffma2_rn(dy, x, tD);
+            tb = __fadd2_rn(tb, dd);
             if (gate) {
               const float2 z = pair(3, r, tk, t, pz, a.bz, a.vin);
               const float2 gr2 = pair(2, r, tk, t, pg, a.D * (int)sizeof(T), b.vg);
@@ -559,6 +559,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 2; ++e) add_kept(dA[c][e], lost[c][e], tA[c][e]);
+      add_kept(dD, lostD, tD);
+      add_kept(dbias, lostb, tb);
       // dB and dC of the CTA's channels
       __syncthreads();
       for (int p = threadIdx.x; p < L::TT * 2 * L::SP; p += NT) {

@@ -33,3 +33,46 @@ def test_bwd_infinite_rate_gradients(gdn, sign, state, adjoint):
     g = gdn.gdn_selective_scan_bwd(one, one, torch.zeros(D, S, device="cuda"), bc, bc, one, softplus=False,
                                    h0=full(sign * state), dht=full(adjoint))
     assert torch.all(g["dA"] == sign * float("inf"))
+
+
+@pytest.mark.parametrize("S,D", [(16, 9984), (64, 2560)])
+def test_bwd_parameter_sums_keep_small_terms(gdn, S, D):
+    """Sequences of 2048 tokens that one CTA walks from end to start, where the last four are 2^24 and the others 1:
+    with dout = 1, B = 1, C = 0, no decay and dht = 1 / S, dD and ddt_bias are the sum of x, every term exact.  A lane
+    adds up to four terms of a tile (three roundings), the tiles with compensation (two), the lanes of a channel
+    (four): 9 * 2^-24 of a sum of positive terms.  dA is the sum of dt / S times the state before the token: up to 16 terms
+    of a tile a lane (15), two for the tiles, four for the state's own sum of 2^24s: 21 * 2^-24."""
+    T, u = 2048, 2.0 ** -24
+    x = torch.ones(1, T, D, device="cuda")
+    x[:, -4:] = 2.0 ** 24
+    one, B = torch.ones_like(x), torch.ones(1, T, 1, S, device="cuda")
+    zero = torch.zeros(D, device="cuda")
+    g = gdn.gdn_selective_scan_bwd(x, 0.5 * one, torch.zeros(D, S, device="cuda"), B, torch.zeros_like(B), one,
+                                   softplus=False, D=zero, dt_bias=zero, dht=torch.full((1, D, S), 1 / S, device="cuda"))
+    want = x.double().sum((0, 1))
+    for k in ("dD", "ddt_bias"):
+        assert ((g[k].double() - want).abs() <= 9 * u * want).all(), k
+    before = 0.5 * (x[0].double().cumsum(0) - x[0].double())
+    want = (0.5 / S * before.sum(0))[:, None]
+    assert ((g["dA"].double() - want).abs() <= 21 * u * want).all()
+
+
+def test_bwd_infinite_skip_gradients(gdn):
+    """The sum of dD over the tiles stays an infinity, too."""
+    x = torch.full((1, 48, 4), 1e30, device="cuda")
+    bc = torch.ones(1, 48, 1, 4, device="cuda")
+    zero = torch.zeros(4, device="cuda")
+    g = gdn.gdn_selective_scan_bwd(x, torch.ones_like(x), torch.zeros(4, 4, device="cuda"), bc, torch.zeros_like(bc), x,
+                                   softplus=False, D=zero, dt_bias=zero, dht=torch.full((1, 4, 4), -1e30, device="cuda"))
+    assert torch.all(g["dD"] == float("inf"))
+
+
+def test_bwd_infinite_bias_gradients(gdn):
+    """.. and that of ddt_bias: steps so small that the states stay finite (else adjoint times state times a rate of
+    0 is a NaN of its own, in each token's ddelta)."""
+    x = torch.full((1, 48, 4), 1e30, device="cuda")
+    bc = torch.ones(1, 48, 1, 4, device="cuda")
+    g = gdn.gdn_selective_scan_bwd(x, torch.full_like(x, 1e-30), torch.zeros(4, 4, device="cuda"), bc,
+                                   torch.zeros_like(bc), x, softplus=False, dt_bias=torch.zeros(4, device="cuda"),
+                                   dht=torch.full((1, 4, 4), -1e30, device="cuda"))
+    assert torch.all(g["ddelta"] == -float("inf")) and torch.all(g["ddt_bias"] == -float("inf"))

@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a
         if (from) load4(from + n0, nn, v4, s);
       }
     }
-    A2[c][0] = make_float2(r[0] * sm100::kLog2e, r[1] * sm100::kLog2e);
-    A2[c][1] = make_float2(r[2] * sm100::kLog2e, r[3] * sm100::kLog2e);
+    A2[c][0] = make_float2(rate2(r[0]), rate2(r[1]));
+    A2[c][1] = make_float2(rate2(r[2]), rate2(r[3]));
     h[c][0] = make_float2(s[0], s[1]);
     h[c][1] = make_float2(s[2], s[3]);
   }
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256) chain_kernel(const Args a) {
   const int d = (int)(i / a.S);
   const int64_t u0 = a.cu ? a.seg0[n] : (int64_t)n * a.nseg;
   const int64_t u1 = a.cu ? a.seg0[n + 1] : u0 + a.nseg;
-  const float r = a.A[i] * sm100::kLog2e;
+  const float r = rate2(a.A[i]);
   float h = a.h0 ? a.h0[n * DS + i] : 0.f;
   // eight segments' loads at a time
   for (int64_t u = u0; u + 1 < u1; u += 8) {
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const StepArgs p) {
   }
   load4(a.A + (int64_t)dd * a.S + n0, nn, v4, A2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= sm100::kLog2e;
+  for (int i = 0; i < 4; ++i) A2[i] = rate2(A2[i]);
   const float bias = a.bias ? a.bias[dd] : 0.f, skip = a.Dp ? a.Dp[dd] : 0.f;
   const T* px = reinterpret_cast<const T*>(static_cast<const char*>(a.x) + s0 * a.bx) + dd;
   const T* pd = reinterpret_cast<const T*>(static_cast<const char*>(a.dl) + s0 * a.bd) + dd;
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(256, 4) scan_token_kernel(const StepArgs p) {
   for (int q = 0; q < NQ; ++q) {
     load4(a.A + (int64_t)dd * a.S + 4 * (sl + RL * q), a.S - 4 * (sl + RL * q), v4, A2[q]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[q][j] *= sm100::kLog2e;
+    for (int j = 0; j < 4; ++j) A2[q][j] = rate2(A2[q][j]);
   }
   const float bias = a.bias ? a.bias[dd] : 0.f, skip = a.Dp ? a.Dp[dd] : 0.f;
   T* y = static_cast<T*>(a.y);

@@ -20,6 +20,7 @@
 // neighbouring lanes read one address and four when they do not.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "gdn_internal.h"
@@ -272,6 +273,14 @@ __device__ __forceinline__ void store4(float* p, int n, bool vec, const float (&
     for (int i = 0; i < 4; ++i)
       if (i < n) p[i] = v[i];
   }
+}
+
+// A decay rate in base 2.  An infinite one (or one that overflows here) becomes the
+// largest: a step of zero, which pads the tiles, keeps the state (0 * -inf would be a
+// NaN), and any other still makes the decay 0.
+__device__ __forceinline__ float rate2(float a) {
+  const float r = a * sm100::kLog2e;
+  return r < -FLT_MAX ? -FLT_MAX : r;
 }
 
 __device__ __forceinline__ float rcp_approx(float y) {   // about 1 ulp; 1 / inf = 0

@@ -27,8 +27,6 @@
 // 225 instructions a token and warp of 256 updates, IPC 2.0 of 4, LSU wavefronts
 // 39 %, DRAM 8 % (by ncu, 236 registers).  4 x 4096 tokens, 4096 channels, 16
 // states, bf16, gated: 1.81 ms.
-#include <cfloat>
-
 #include "gdn_scan.cuh"
 
 namespace gdn {
@@ -83,8 +81,8 @@ __global__ void __launch_bounds__(128) scan_rev_kernel(const BwdArgs b) {
   for (int c = 0; c < 2; ++c) {
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     if (c ? ok1 : ok0) load4(a.A + (int64_t)(d + c) * a.S + n0, nn, v4, r);
-    A2[c][0] = make_float2(r[0] * sm100::kLog2e, r[1] * sm100::kLog2e);
-    A2[c][1] = make_float2(r[2] * sm100::kLog2e, r[3] * sm100::kLog2e);
+    A2[c][0] = make_float2(rate2(r[0]), rate2(r[1]));
+    A2[c][1] = make_float2(rate2(r[2]), rate2(r[3]));
     q[c][0] = q[c][1] = make_float2(0.f, 0.f);
   }
   const float2 bias = make_float2(a.bias && ok0 ? a.bias[d] : 0.f, a.bias && ok1 ? a.bias[d + 1] : 0.f);
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(256) rev_chain_kernel(const BwdArgs b) {
   const int d = (int)(i / a.S);
   const int64_t u0 = a.cu ? a.seg0[n] : (int64_t)n * a.nseg;
   const int64_t u1 = a.cu ? a.seg0[n + 1] : u0 + a.nseg;
-  const float r = a.A[i] * sm100::kLog2e;
+  const float r = rate2(a.A[i]);
   float q = b.dht ? b.dht[n * DS + i] : 0.f;
   for (int64_t u = u1 - 1; u > u0; u -= 8) {   // eight segments' loads at a time
     float loc[8], dt[8];
@@ -278,8 +276,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
     lost[c][0] = lost[c][1] = make_float2(0.f, 0.f);
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     if (c ? ok1 : ok0) load4(a.A + (int64_t)(d + c) * a.S + n0, nn, v4, r);
-    A2[c][0] = make_float2(r[0] * sm100::kLog2e, r[1] * sm100::kLog2e);
-    A2[c][1] = make_float2(r[2] * sm100::kLog2e, r[3] * sm100::kLog2e);
+    A2[c][0] = make_float2(rate2(r[0]), rate2(r[1]));
+    A2[c][1] = make_float2(rate2(r[2]), rate2(r[3]));
     dA[c][0] = dA[c][1] = make_float2(0.f, 0.f);
   }
   const float2 bias = make_float2(a.bias && ok0 ? a.bias[d] : 0.f, a.bias && ok1 ? a.bias[d + 1] : 0.f);

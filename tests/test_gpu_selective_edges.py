@@ -76,3 +76,50 @@ def test_bwd_infinite_bias_gradients(gdn):
                                    torch.zeros_like(bc), x, softplus=False, dt_bias=torch.zeros(4, device="cuda"),
                                    dht=torch.full((1, 4, 4), -1e30, device="cuda"))
     assert torch.all(g["ddelta"] == -float("inf")) and torch.all(g["ddt_bias"] == -float("inf"))
+
+
+def offsets(lens):
+    return torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+
+
+def infinite_rates(T, D, S, G, lens=None, seed=3):
+    """Some states forget everything at each token: a rate of -infinity, or one whose base-2 form overflows."""
+    inp = R.make_scan(2, T, D, S, G, "f32", init=True, lens=lens, seed=seed)
+    inp["A"][:, 1], inp["A"][::2, 2] = -float("inf"), -3e38
+    return inp
+
+
+@pytest.mark.parametrize("T,D,S,G,lens", [(21, 6, 4, 1, None), (16, 8, 8, 2, None), (1, 5, 16, 1, None),
+                                          (37, 40, 16, 2, None), (700, 6, 30, 1, None),
+                                          (0, 10, 16, 2, [300, 0, 5, 129])])
+def test_infinite_rates(gdn, T, D, S, G, lens):
+    """Outputs and states are those of the definition, whatever the last tile's padding; bar as for other rates."""
+    inp = infinite_rates(T, D, S, G, lens)
+    y, ht = gdn.gdn_selective_scan_fwd(**cuda(inp), cu_seqlens=None if lens is None else offsets(lens))
+    y_ref, ht_ref = R.scan(**inp, lens=lens)
+    assert rel_fro(y.cpu(), y_ref) <= 1e-5 and rel_fro(ht.cpu(), ht_ref) <= 1e-5
+
+
+@pytest.mark.parametrize("T,D,S,G,lens", [(21, 6, 4, 1, None), (37, 40, 16, 2, None), (200, 6, 30, 1, None),
+                                          (0, 10, 16, 2, [130, 0, 5, 70])])
+def test_bwd_infinite_rates(gdn, T, D, S, G, lens):
+    """The gradients that the definition has then: all but those of the steps, where it is 0 times infinity."""
+    inp = infinite_rates(T, D, S, G, lens)
+    g = torch.Generator().manual_seed(5)
+    dout, dht = torch.randn(inp["x"].shape, generator=g), torch.randn(inp["h0"].shape, generator=g)
+    got = gdn.gdn_selective_scan_bwd(**cuda(inp), dout=dout.cuda(), dht=dht.cuda(),
+                                     cu_seqlens=None if lens is None else offsets(lens))
+    want = R.scan_grads(inp, dout, dht, lens=lens)
+    for k in ("x", "A", "B", "C", "D", "z", "h0"):
+        assert rel_fro(got["d" + k].cpu(), want[k]) <= 5e-5, k
+
+
+@pytest.mark.parametrize("N,T", [(3, 1), (70, 1), (2, 5)])
+def test_step_infinite_rates(gdn, N, T):
+    inp = R.make_scan(N, T, 24, 16, 2, "f32", init=True, seed=6)
+    inp["A"][:, 1], inp["A"][::2, 2] = -float("inf"), -3e38
+    y_ref, ht_ref = R.scan(**inp)
+    d = cuda(inp)
+    state = d.pop("h0").clone()
+    y = gdn.gdn_selective_scan_step(**d, state=state)
+    assert rel_fro(y.cpu(), y_ref) <= 1e-5 and rel_fro(state.cpu(), ht_ref) <= 1e-5

@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a
       load4(a.A + (int64_t)(d + c) * a.S + n0, nn, v4, r);
       if (!STATES) {
         const float* from = nullptr;
-        if (!u.first) from = a.hseg + (un * a.D + d + c) * a.S;
+        // (a cut sequence's first segment too: ht, which its last one writes, may be h0)
+        if (!u.first || !u.last) from = a.hseg + (un * a.D + d + c) * a.S;
         else if (a.h0) from = a.h0 + ((int64_t)u.n * a.D + d + c) * a.S;
         if (from) load4(from + n0, nn, v4, s);
       }

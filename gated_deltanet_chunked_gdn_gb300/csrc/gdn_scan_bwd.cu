@@ -299,10 +299,12 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
     for (int c = 0; c < 2; ++c) {
       float s[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
       if (c ? ok1 : ok0) {
-        const float* from = !u.first ? a.hseg + (un * a.D + d + c) * a.S
-                            : a.h0   ? a.h0 + ((int64_t)u.n * a.D + d + c) * a.S : nullptr;
+        // (a cut sequence's first and last too: dh0, which its first one writes, may be h0 or dht)
+        const bool cut = !u.first || !u.last;
+        const float* from = cut    ? a.hseg + (un * a.D + d + c) * a.S
+                            : a.h0 ? a.h0 + ((int64_t)u.n * a.D + d + c) * a.S : nullptr;
         if (from) load4(from + n0, nn, v4, s);
-        const float* end = !u.last ? b.qseg + (un * a.D + d + c) * a.S
+        const float* end = cut     ? b.qseg + (un * a.D + d + c) * a.S
                            : b.dht ? b.dht + ((int64_t)u.n * a.D + d + c) * a.S : nullptr;
         if (end) load4(end + n0, nn, v4, r);
       }

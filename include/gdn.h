@@ -465,9 +465,11 @@ gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, co
  *              sequences of a batch follow one another at this stride, so a
  *              column slice of a wider matrix can be passed as it is.  ld_x,
  *              ld_delta, ld_z: rows of D elements; ld_b, ld_c: rows of G * S.
- * y, gradients and everything else are contiguous.  Pointers need the
- * alignment of their elements only, except A, h0, ht, state, dA, dht and dh0:
- * 16 bytes when S % 4 == 0.
+ * y, gradients and everything else are contiguous.  Outputs must not overlap
+ * inputs or one another, but ht may be h0 and dh0 may be h0 or dht (the same
+ * pointer: states updated in place).  Pointers need the alignment of their
+ * elements only, except A, h0, ht, state, dA, dht and dh0: 16 bytes when
+ * S % 4 == 0.
  */
 typedef struct {
   int B, T, N, D, S, G;

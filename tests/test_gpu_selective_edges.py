@@ -123,3 +123,41 @@ def test_step_infinite_rates(gdn, N, T):
     state = d.pop("h0").clone()
     y = gdn.gdn_selective_scan_step(**d, state=state)
     assert rel_fro(y.cpu(), y_ref) <= 1e-5 and rel_fro(state.cpu(), ht_ref) <= 1e-5
+
+
+CUT = [(3, 700, 6, 30, 1, None), (2, 3000, 64, 16, 1, None), (1, 0, 10, 16, 2, [300, 0, 700, 3, 128, 129]),
+       (200, 40, 32, 16, 1, None)]   # the last: whole sequences, several to a CTA
+
+
+@pytest.mark.parametrize("B,T,D,S,G,lens", CUT)
+def test_states_in_place(gdn, B, T, D, S, G, lens):
+    """ht given as h0: bit for bit the call with a tensor of its own, cut sequences too."""
+    inp = cuda(R.make_scan(B, T, D, S, G, "f32", init=True, lens=lens, seed=7))
+    cu = None if lens is None else offsets(lens)
+    y, ht = gdn.gdn_selective_scan_fwd(**inp, cu_seqlens=cu)
+    for _ in range(3):
+        state = inp["h0"].clone()
+        y2, _ = gdn.gdn_selective_scan_fwd(**(inp | {"h0": state}), ht=state, cu_seqlens=cu)
+        assert torch.equal(y, y2) and torch.equal(ht, state)
+
+
+@pytest.mark.parametrize("B,T,D,S,G,lens", CUT)
+@pytest.mark.parametrize("which", ["h0", "dht"])
+def test_bwd_states_in_place(gdn, B, T, D, S, G, lens, which):
+    """dh0 written over h0 or over dht (the C call; the binding allocates its own)."""
+    inp = cuda(R.make_scan(B, T, D, S, G, "f32", init=True, lens=lens, seed=8))
+    cu = None if lens is None else offsets(lens)
+    dout, dht = torch.randn_like(inp["x"]), torch.randn_like(inp["h0"])
+    want = gdn.gdn_selective_scan_bwd(**inp, dout=dout, dht=dht, cu_seqlens=cu)
+    p = gdn._scan_problem(inp["x"], inp["delta"], inp["A"], inp["B"], inp["C"], inp["D"], inp["z"], inp["dt_bias"], True,
+                          cu, ())
+    over = {"h0": inp["h0"].clone(), "dht": dht.clone()}
+    out = {k: torch.empty_like(v) for k, v in want.items() if k not in ("dh0", "workspace")}
+    ws = want["workspace"]
+    st = gdn.load().gdn_selective_scan_bwd(
+        p, *(inp[k].data_ptr() for k in ("x", "delta", "A", "B", "C", "D", "z", "dt_bias")), over["h0"].data_ptr(),
+        0 if cu is None else cu.data_ptr(), dout.data_ptr(), over["dht"].data_ptr(),
+        *(out[k].data_ptr() for k in ("dx", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddt_bias")),
+        over[which].data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == gdn.GDN_OK
+    assert torch.equal(over[which], want["dh0"]) and all(torch.equal(v, want[k]) for k, v in out.items())

@@ -738,8 +738,10 @@ def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial
                                   ("initial_state", initial_state, x.dtype, state),
                                   ("dfinal_state", dfinal_state, x.dtype, state),
                                   ("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))):
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or t.shape != shape):
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+        if t is not None and (not t.is_cuda or t.device != x.device or not t.is_contiguous() or t.dtype != dtype
+                              or t.shape != shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on the device "
+                             "of x")
     given = workspace
     if workspace is None:
         need = lib.gdn_causal_conv1d_bwd_workspace_size(B, T, D, W)

@@ -500,6 +500,11 @@ except AttributeError:
         return torch.cuda.current_stream(index).cuda_stream
 
 
+def _check_ws(workspace, x) -> None:
+    if workspace is not None and workspace.device != x.device:
+        raise ValueError("workspace must be on the device of x")
+
+
 def _lend(stream: int, device, blocks) -> None:
     """Hands blocks that a call has allocated (None among them) to the stream that it runs on.  They come from the
     current stream's pool, where work queued earlier may still use their memory and where they return when they are
@@ -605,6 +610,7 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
     may be slices of wider rows), A [D, S], D and dt_bias [D], h0 [N, D, S] fp32.  Returns (y, ht); ht is None
     when ``output_final_state`` is False."""
     lib = _lib or load()
+    _check_ws(workspace, x)
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (("h0", h0, state), ("ht", ht, state)),
                       (("y", y),) if y is not None else ())
@@ -685,6 +691,7 @@ def gdn_selective_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, dt_bias=None
     under "workspace"; dD, dz and ddt_bias are None where the input is, dh0 unless ``want_dh0`` (by default: h0 is
     given)."""
     lib = _lib or load()
+    _check_ws(workspace, x)
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
     p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens,
                       (("h0", h0, state), ("dht", dht, state)), (("dout", dout),))
@@ -727,6 +734,7 @@ def gdn_causal_conv1d_bwd(x, weight, dout, bias=None, activation="silu", initial
     lib = _lib or load()
     if x.dtype not in DTYPES or x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
         raise ValueError("x must be float32 or bfloat16 [B, T, D] and weight [D, W]")
+    _check_ws(workspace, x)
     B, T, D = x.shape
     W = weight.shape[1]
     if cu_seqlens is not None and cu_seqlens.dtype != torch.int32:

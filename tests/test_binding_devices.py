@@ -18,3 +18,24 @@ def test_conv_bwd_tensors_share_a_device(other):
                     cu_seqlens=at("cu_seqlens", 3, dtype=torch.int32))
         with pytest.raises(ValueError, match=other):
             gdn.gdn_causal_conv1d_bwd(**args)
+
+
+def scan(at):
+    return dict(x=at("x", 1, 16, 32), delta=at("delta", 1, 16, 32), A=at("A", 32, 4), B=at("B", 1, 16, 1, 4),
+                C=at("C", 1, 16, 1, 4))
+
+
+@pytest.mark.parametrize("device", ["cpu", "cuda:1"])
+@pytest.mark.parametrize("call", ["scan_fwd", "scan_bwd", "conv_bwd"])
+def test_workspaces_are_checked(call, device):
+    """The library writes to it, so it is on the device of x."""
+    with FakeTensorMode():
+        at = lambda name, *s: torch.empty(*s, device="cuda:0")
+        ws = torch.empty(1 << 24, dtype=torch.uint8, device=device)
+        with pytest.raises(ValueError, match="workspace"):
+            if call == "scan_fwd":
+                gdn.gdn_selective_scan_fwd(**scan(at), workspace=ws)
+            elif call == "scan_bwd":
+                gdn.gdn_selective_scan_bwd(**scan(at), dout=at("dout", 1, 16, 32), workspace=ws)
+            else:
+                gdn.gdn_causal_conv1d_bwd(at("x", 1, 16, 32), at("w", 32, 4), at("dout", 1, 16, 32), workspace=ws)

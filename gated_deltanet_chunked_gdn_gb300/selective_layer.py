@@ -113,6 +113,9 @@ def _pool_rows(slots, size):
     return src, slots[src].long().clamp(0, size - 1), known.any()
 
 
+PROJECTIONS = ("in_proj", "x_proj", "dt_proj", "out_proj")
+
+
 class SelectiveLayer(torch.nn.Module):
     """width: the model's; channels D, states S a channel, groups G that share B and C, W taps, rank of the step."""
 
@@ -135,7 +138,24 @@ class SelectiveLayer(torch.nn.Module):
         self.Dskip = torch.nn.Parameter(torch.ones(channels, device=device))
         step = torch.exp(torch.rand(channels, device=device) * math.log(100) + math.log(1e-3))   # in [1e-3, 1e-1]
         self.dt_bias = torch.nn.Parameter(torch.log(torch.expm1(step)))
-        self.q4 = None
+
+    @property
+    def q4(self):
+        """{projection: (codes, scales)} of step(), or None before quantize_()."""
+        b = self._buffers
+        return {k: (b[k + "_codes"], b[k + "_scales"]) for k in PROJECTIONS} if "A" in b else None
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        """A checkpoint of a quantized layer brings its 4-bit weights; those of a layer that gets other parameters
+        without any are dropped."""
+        names = [k + kind for k in PROJECTIONS for kind in ("_codes", "_scales")] + ["A"]
+        if all(prefix + k in state_dict for k in names):
+            for k in names:
+                self.register_buffer(k, torch.empty_like(state_dict[prefix + k], device=self.in_proj.device))
+        elif any(prefix + k in state_dict for k in (*PROJECTIONS, "A_log")):
+            for k in names:
+                self._buffers.pop(k, None)
+        super()._load_from_state_dict(state_dict, prefix, *args)
 
     def _split(self, dbc):
         dt, B, C = dbc.split([self.rank, self.G * self.S, self.G * self.S], dim=-1)
@@ -160,9 +180,13 @@ class SelectiveLayer(torch.nn.Module):
 
     @torch.no_grad()
     def quantize_(self, group=32):
-        """4-bit copies of the projections for step()."""
-        self.q4 = {k: quantize(getattr(self, k), group) for k in ("in_proj", "x_proj", "dt_proj", "out_proj")}
-        self.A = -torch.exp(self.A_log)
+        """4-bit copies of the projections (and the decay rates) for step(): buffers, which move and are saved with
+        the layer.  To be called again when the parameters have changed."""
+        for k in PROJECTIONS:
+            codes, scales = quantize(getattr(self, k), group)
+            self.register_buffer(k + "_codes", codes)
+            self.register_buffer(k + "_scales", scales)
+        self.register_buffer("A", -torch.exp(self.A_log))
         return self
 
     @torch.no_grad()
@@ -189,9 +213,12 @@ class SelectiveLayer(torch.nn.Module):
     def step(self, u, states, slots):
         """One token of every sequence: u [N, width] on the pools' rows ``slots``, with the 4-bit weights."""
         conv, scan = states
+        q4 = self.q4
+        if q4 is None:
+            raise RuntimeError("step() multiplies by 4-bit weights: call quantize_() first")
 
         def product(v, name):
-            return gdn.gdn_q4_matvec(v, *self.q4[name])
+            return gdn.gdn_q4_matvec(v, *q4[name])
 
         x, z = product(u, "in_proj").chunk(2, dim=-1)
         x = gdn.gdn_causal_conv1d_fwd(x.contiguous()[:, None], self.conv_weight, self.conv_bias, "silu",

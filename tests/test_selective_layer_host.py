@@ -145,3 +145,69 @@ def test_first_derivatives(training, cu):
     want = torch.autograd.grad((y.bfloat16() @ training.out_proj.t()).float().square().sum(), params)
     for a, b in zip(plain, want):
         assert (a.double() - b.double()).norm() <= 2e-2 * b.double().norm()
+
+
+def q4_matvec(x, qweight, scales):
+    return (x.double() @ R.q4_weights(qweight, scales).t()).to(x.dtype)
+
+
+def conv_step(x, weight, bias, activation, conv_state, cache_indices):
+    at = cache_indices.long()
+    y, final = R.conv(x, weight, bias, activation, conv_state[at])
+    conv_state[at] = final.to(conv_state.dtype)
+    return y.to(x.dtype)
+
+
+def scan_step(x, delta, A, B, C, state, D=None, z=None, dt_bias=None, state_indices=None):
+    at = state_indices.long()
+    y, h = R.scan(x, delta, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=state[at])
+    state[at] = h.float()
+    return y.to(x.dtype)
+
+
+@pytest.fixture
+def serving(layer, monkeypatch):
+    monkeypatch.setattr(mod.gdn, "gdn_causal_conv1d_fwd", conv_step)
+    monkeypatch.setattr(mod.gdn, "gdn_selective_scan_step", scan_step)
+    monkeypatch.setattr(mod.gdn, "gdn_q4_matvec", q4_matvec)
+    layer = mod.SelectiveLayer(32, 64, states=4, rank=32, device="cpu")
+    with torch.no_grad():
+        layer.A_log += 0.1
+    return layer
+
+
+def step(layer):
+    u = torch.randn(2, 32, generator=torch.Generator().manual_seed(2)).bfloat16()
+    return layer.step(u, layer.new_states(2), torch.tensor([1, 0], dtype=torch.int32))
+
+
+def test_step_wants_the_4_bit_weights(serving):
+    with pytest.raises(RuntimeError, match="quantize_"):
+        step(serving)
+
+
+def test_4_bit_weights_are_saved_and_loaded(serving):
+    """A checkpoint of a quantized layer gives a new one the same step, whose own weights need not be near the codes."""
+    want = step(serving.quantize_())
+    other = mod.SelectiveLayer(32, 64, states=4, rank=32, device="cpu")
+    other.load_state_dict(serving.state_dict())
+    assert torch.equal(step(other), want)
+    assert all(torch.equal(a, b) for k in serving.q4 for a, b in zip(serving.q4[k], other.q4[k]))
+    outer = torch.nn.Sequential(mod.SelectiveLayer(32, 64, states=4, rank=32, device="cpu"))   # within another module
+    outer.load_state_dict({"0." + k: v for k, v in serving.state_dict().items()})
+    assert torch.equal(step(outer[0]), want)
+
+
+def test_4_bit_weights_do_not_outlive_a_checkpoint_without_them(serving):
+    plain = mod.SelectiveLayer(32, 64, states=4, rank=32, device="cpu")
+    serving.quantize_().load_state_dict(plain.state_dict())
+    with pytest.raises(RuntimeError, match="quantize_"):
+        step(serving)
+    assert torch.equal(step(serving.quantize_()), step(plain.quantize_()))
+
+
+def test_4_bit_weights_move_with_the_layer(serving):
+    moved = serving.quantize_().to("meta")
+    tensors = [t for pair in moved.q4.values() for t in pair] + [moved.A]
+    assert len(tensors) == 9 and all(t.is_meta for t in tensors)
+    assert all(moved.q4[k][0].dtype == torch.uint8 for k in moved.q4)

@@ -510,11 +510,10 @@ def _lend(stream: int, device, blocks) -> None:
     current stream's pool, where work queued earlier may still use their memory and where they return when they are
     dropped: another stream waits for that work, and the memory is not given out again before it is done."""
     blocks = [b for b in blocks if b is not None]
-    here = torch.cuda.current_stream(device)
-    if not blocks or stream == here.cuda_stream:
+    if not blocks or stream == _current_stream(blocks[0].get_device()):
         return
     other = torch.cuda.ExternalStream(stream, device=device)
-    other.wait_stream(here)
+    other.wait_stream(torch.cuda.current_stream(device))
     for b in blocks:
         b.record_stream(other)
 

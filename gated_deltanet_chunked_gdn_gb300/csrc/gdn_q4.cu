@@ -409,16 +409,25 @@ cudaError_t launch_q4(const Q4Args& a, int m0, int ncol, cudaStream_t s) {
   return by_vec(std::integral_constant<int, 2>());
 }
 
-// Which configuration (one GB300, us a call, bf16; both sides of each choice as it was
-// taken: with 32-bit offsets the kept sides are 25.0 for one row, 36.1 for
-// eight and 36.8 for 16 of 16384 x 8192, 8.1 for two of 4096 x 4096, 22.6 for five).  One row of x: 16 weight rows a
-// warp and short rings, so that three CTAs share an SM (16384 x 8192 codes 26.6; 32
-// rows a warp and rings of six 28.8).  Up to 4 columns, warps in pairs on one copy of
-// x (2 rows, 4096 x 4096: 8.5; alone 9.3).  Up to 8: 32 rows a warp once they fill the
-// SMs (8 rows, 16384 x 8192: 40 against 46; 5 rows, 12288 x 4096: 26 against 23).  Up
-// to 16: 32 rows a warp, four warps on one x (40; 59 with 16 rows and two).  fp32 x,
-// cut by the warps that bring it: fewer warps to a share (4 rows, 4096 x 4096: 22; 37).
-// 17 to 32: 58 us for 32 rows, 16384 x 8192.
+// Which configuration.  One GB300, us a call in a graph, the kept side and the other
+// one in the same code; bf16 x, groups of 128, no zero points, unless said.
+//   One row of x: 16 weight rows a warp and short rings, so that three CTAs share an SM
+//     (the other: 32 rows and rings of six).  16384 x 8192 24.6 / 25.6, in groups of 32
+//     30.4 / 34.5; 4096 x 4096 6.1 / 6.1.
+//   Up to 4 columns: warps in pairs on one copy of x (alone).  2 rows of 4096 x 4096 8.1 /
+//     9.2; 4 rows of 16384 x 8192 30.6 / 37.3.
+//   Up to 8: 32 rows a warp (16) from 96 weight rows an SM on.  8 rows of 16384 x 8192 29.7 /
+//     38.7, 24576 x 8192 42.1 / 54.6; 5 rows of 16384 x 4096 in groups of 32 23.3 / 26.4;
+//     2 fp32 rows of 16384 x 8192 34.2 / 57.5.  16 rows a warp (32) below.  5 rows of 12288 x
+//     4096 in groups of 32 21.6 / 22.2; but of 8192 x 4096 15.9 / 14.9, and 8 rows of 12288 x
+//     8192 34.1 / 29.4, 14336 x 8192 36.2 / 29.5: the limit is too high for those.
+//   Up to 16: 32 rows a warp, four warps on one x (16 rows, two warps).  16 rows of 16384 x
+//     8192 36.6 / 57.1, 12288 x 4096 in groups of 32 26.2 / 34.2; but 4096 x 4096 18.7 / 12.6,
+//     9 rows 17.2 / 10.9: few weight rows leave SMs idle this way.
+//   Up to 16 columns of fp32 x, cut by the warps that bring it: fewer warps to a share (the
+//     bf16 choice).  4 rows of 4096 x 4096 21.8 / 35.0; but 5 rows of 16384 x 8192 102 / 72.
+//   17 to 32: 17 rows of 16384 x 8192 48.8, 32 rows 57.9; 32 of 12288 x 4096 in groups of 32
+//     38.2 (nothing else measured).
 template <typename T, typename ST>
 cudaError_t run_rows(const Q4Args& a, cudaStream_t s) {
   constexpr int P = kParts<T>;

@@ -643,7 +643,11 @@ Plan make_plan(const gdn_scan_problem& p) {
   pl.cpw = 64 / pl.RL;
   pl.cbg = (int)ceil_div(p.D / p.G, pl.cpw);
   const int64_t cw = (int64_t)p.G * pl.cbg;              // warps a line of tokens
-  const int64_t fill = (int64_t)sm_count() * 12;         // warps that the SMs hold (three CTAs of four each)
+  // Warps that the SMs hold in most layouts: three CTAs of four each.  (By their tiles'
+  // shared memory fp32 with 9 to 32 states holds 8, more than 32 states 10 in bf16 and 6
+  // in fp32; the rules below were measured in bf16 with 16 states, and cut those prompts
+  // into more segments than run at once.)
+  const int64_t fill = (int64_t)sm_count() * 12;
   // A cut costs a second run over all tokens but the last segments'.  Equal lengths
   // are cut when fewer than three warps an SM would run, into as many segments as run
   // at once (one GB300, 4096 channels, 16 states: 1 x 4096 tokens, 256 warps, 291 us

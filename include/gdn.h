@@ -437,8 +437,10 @@ gdn_status gdn_causal_conv1d_bwd(const void* x, const float* weight, const float
  *   bias        : [N] fp32 or NULL
  *   K           : a multiple of group, at most 2^20;  group : a multiple of 32
  *   y           : out [M, N] of dtype dt, contiguous
- * Products and sums are exact to fp32 (no weight and, in fp32, no x is rounded);
- * y is rounded once.  No workspace; asynchronous on `stream`.
+ * No weight and, in fp32, no x is rounded; products with codes less zero points are
+ * exact in fp32 and their sums, over a group and over the groups, round as fp32 sums do
+ * (by about 2e-6 of sum |x w| at most for K = 8192).  y is rounded once to dt.  No
+ * workspace; asynchronous on `stream`.
  */
 gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, const void* scales, gdn_dtype sdt,
                          const uint8_t* zeros, const float* bias, int M, int N, int K, int group, gdn_dtype dt,

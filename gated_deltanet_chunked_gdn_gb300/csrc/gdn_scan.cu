@@ -227,9 +227,8 @@ __global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a
         for (int c = 0; c < 2; ++c) {
           const float dc = c ? q.y : q.x, ux = c ? q.w : q.z;
           const float2 dt2 = make_float2(dc, dc), ux2 = make_float2(ux, ux);
-          const float2 e0 = __fmul2_rn(dt2, A2[c][0]), e1 = __fmul2_rn(dt2, A2[c][1]);
-          aa[j][c][0] = make_float2(sm100::ex2_fast(e0.x), sm100::ex2_fast(e0.y));
-          aa[j][c][1] = make_float2(sm100::ex2_fast(e1.x), sm100::ex2_fast(e1.y));
+          aa[j][c][0] = decay2(dt2, A2[c][0]);
+          aa[j][c][1] = decay2(dt2, A2[c][1]);
           uu[j][c][0] = __fmul2_rn(ux2, make_float2(bb.x, bb.y));
           uu[j][c][1] = __fmul2_rn(ux2, make_float2(bb.z, bb.w));
         }
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const StepArgs p) {
     float o = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      h[i] = fmaf(sm100::ex2_fast(dt * A2[i]), h[i], ux * b[i]);
+      h[i] = fmaf(decay(dt, A2[i]), h[i], ux * b[i]);
       o = fmaf(c[i], h[i], o);
     }
 #pragma unroll
@@ -559,8 +558,7 @@ __global__ void __launch_bounds__(256, 4) scan_token_kernel(const StepArgs p) {
     for (int q = 0; q < NQ; ++q) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float2 e = __fmul2_rn(dt2, make_float2(A2[q][2 * j], A2[q][2 * j + 1]));
-        const float2 hn = __ffma2_rn(make_float2(sm100::ex2_fast(e.x), sm100::ex2_fast(e.y)),
+        const float2 hn = __ffma2_rn(decay2(dt2, make_float2(A2[q][2 * j], A2[q][2 * j + 1])),
                                      make_float2(h[i][q][2 * j], h[i][q][2 * j + 1]), __fmul2_rn(ux2, j ? rB[i][q].hi() : rB[i][q].lo()));
         h[i][q][2 * j] = hn.x, h[i][q][2 * j + 1] = hn.y;
         o2 = __ffma2_rn(j ? rC[i][q].hi() : rC[i][q].lo(), hn, o2);

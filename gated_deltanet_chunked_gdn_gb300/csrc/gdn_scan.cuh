@@ -283,6 +283,20 @@ __device__ __forceinline__ float rate2(float a) {
   return r < -FLT_MAX ? -FLT_MAX : r;
 }
 
+// Decays e^{dt A}, from the rate in base 2.  ex2.approx of a negative argument is low on
+// average: by 5e-9 to 8e-9 for arguments of 2e-4 to 4e-3, by 1.6e-8 to 2.7e-8 for 4e-3
+// to 1/2 (relative, 2^20 arguments a range against 64 bits, one GB300; its largest error
+// is 1.4e-7).  A state is multiplied once a token, so this bias adds up over its memory,
+// and made most of the gradients' error (13 packed sequences in fp32: dA 1.1e-6, with
+// exact decays 2.4e-7).  The exponent's multiply-add puts 1.4e-8 of it back: 5.3e-7.
+// 2^kEx2Bias itself is 1, so that a step or a rate of zero still keeps the state.
+constexpr float kEx2Bias = 2e-8f;   // 1.4e-8 log2 e
+__device__ __forceinline__ float decay(float dt, float rate) { return sm100::ex2_fast(fmaf(dt, rate, kEx2Bias)); }
+__device__ __forceinline__ float2 decay2(float2 dt, float2 rate) {
+  const float2 e = __ffma2_rn(dt, rate, make_float2(kEx2Bias, kEx2Bias));
+  return make_float2(sm100::ex2_fast(e.x), sm100::ex2_fast(e.y));
+}
+
 __device__ __forceinline__ float rcp_approx(float y) {   // about 1 ulp; 1 / inf = 0
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));

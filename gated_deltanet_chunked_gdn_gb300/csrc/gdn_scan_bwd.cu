@@ -142,11 +142,8 @@ __global__ void __launch_bounds__(128) scan_rev_kernel(const BwdArgs b) {
       for (int c = 0; c < 2; ++c) {
         const float dt = c ? s.z : s.x, dy = c ? s.w : s.y;
         const float2 dt2 = make_float2(dt, dt), dy2 = make_float2(dy, dy);
-        const float2 e0 = __fmul2_rn(dt2, A2[c][0]), e1 = __fmul2_rn(dt2, A2[c][1]);
-        q[c][0] = __fmul2_rn(make_float2(sm100::ex2_fast(e0.x), sm100::ex2_fast(e0.y)),
-                             __ffma2_rn(dy2, make_float2(cc.x, cc.y), q[c][0]));
-        q[c][1] = __fmul2_rn(make_float2(sm100::ex2_fast(e1.x), sm100::ex2_fast(e1.y)),
-                             __ffma2_rn(dy2, make_float2(cc.z, cc.w), q[c][1]));
+        q[c][0] = __fmul2_rn(decay2(dt2, A2[c][0]), __ffma2_rn(dy2, make_float2(cc.x, cc.y), q[c][0]));
+        q[c][1] = __fmul2_rn(decay2(dt2, A2[c][1]), __ffma2_rn(dy2, make_float2(cc.z, cc.w), q[c][1]));
       }
     }
   }
@@ -400,9 +397,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(RL)) scan_bwd_kernel(const BwdA
       for (int c = 0; c < 2; ++c) {
         const float dt = c ? s.y : s.x, ux = c ? s.w : s.z;
         const float2 dt2 = make_float2(dt, dt), ux2 = make_float2(ux, ux);
-        const float2 e0 = __fmul2_rn(dt2, A2[c][0]), e1 = __fmul2_rn(dt2, A2[c][1]);
-        aa[c][0] = make_float2(sm100::ex2_fast(e0.x), sm100::ex2_fast(e0.y));
-        aa[c][1] = make_float2(sm100::ex2_fast(e1.x), sm100::ex2_fast(e1.y));
+        aa[c][0] = decay2(dt2, A2[c][0]);
+        aa[c][1] = decay2(dt2, A2[c][1]);
         hh[c][0] = __ffma2_rn(aa[c][0], hh[c][0], __fmul2_rn(ux2, make_float2(bb.x, bb.y)));
         hh[c][1] = __ffma2_rn(aa[c][1], hh[c][1], __fmul2_rn(ux2, make_float2(bb.z, bb.w)));
       }

@@ -24,9 +24,10 @@
 // segments' ends come from the same chaining backwards in time.
 //
 // What bounds it (one GB300): as the forward, issue and latency at 8 warps an SM.
-// 225 instructions a token and warp of 256 updates, IPC 2.0 of 4, LSU wavefronts
-// 39 %, DRAM 8 % (by ncu, 236 registers).  4 x 4096 tokens, 4096 channels, 16
-// states, bf16, gated: 1.83 ms.
+// 230 instructions a token and warp of 256 updates, IPC 2.0 of 4, LSU wavefronts
+// 38 %, DRAM 8 % (by ncu, 237 registers).  4 x 4096 tokens, 4096 channels, 16
+// states, bf16, gated: 1.82 ms, one hundredth of it for the compensated sums of dD
+// and ddt_bias and for infinite ones.
 #include "gdn_scan.cuh"
 
 namespace gdn {

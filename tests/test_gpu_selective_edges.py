@@ -161,3 +161,29 @@ def test_bwd_states_in_place(gdn, B, T, D, S, G, lens, which):
         over[which].data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
     assert st == gdn.GDN_OK
     assert torch.equal(over[which], want["dh0"]) and all(torch.equal(v, want[k]) for k, v in out.items())
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_steps(gdn, dtype, low):
+    """Tokens whose delta is -infinity or the type's lowest number make no step: they keep the state and get no
+    gradient of their step; a sequence of nothing else keeps its initial state."""
+    lens = [40, 17, 300]
+    inp = R.make_scan(1, 0, 32, 16, 2, dtype, init=True, lens=lens, seed=9)
+    inp["delta"][:, 5:60:3], inp["delta"][:, 40:57], inp["delta"][:, 100] = low, low, low
+    y, ht = gdn.gdn_selective_scan_fwd(**cuda(inp), cu_seqlens=offsets(lens))
+    y_ref, ht_ref = R.scan(**inp, lens=lens)
+    more = 2.0 ** -8 if dtype == "bf16" else 0.0
+    assert rel_fro(y.double().cpu(), y_ref) <= 1e-5 + more and rel_fro(ht.cpu(), ht_ref) <= 1e-5
+    assert torch.equal(ht[1].cpu(), inp["h0"][1])
+    state = inp["h0"].cuda()
+    rest = {k: v for k, v in cuda(inp).items() if k != "h0"}
+    ys = gdn.gdn_selective_scan_step(**rest, state=state, cu_seqlens=offsets(lens))
+    assert rel_fro(ys.double().cpu(), y_ref) <= 1e-5 + more and torch.equal(state[1].cpu(), inp["h0"][1])
+    g = torch.Generator().manual_seed(10)
+    dout, dht = torch.randn(y_ref.shape, generator=g).to(inp["x"].dtype), torch.randn(ht_ref.shape, generator=g)
+    got = gdn.gdn_selective_scan_bwd(**cuda(inp), dout=dout.cuda(), dht=dht.cuda(), cu_seqlens=offsets(lens))
+    want = R.scan_grads(inp, dout, dht, lens=lens)
+    for k, v in inp.items():
+        assert rel_fro(got["d" + k].double().cpu(), want[k]) <= 5e-5 + (more if v.dtype == torch.bfloat16 else 0.0), k
+    assert not got["ddelta"][:, 40:57].any()

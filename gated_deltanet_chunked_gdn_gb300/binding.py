@@ -27,7 +27,7 @@ EXPORTED = ["gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_stag
             "gdn_causal_conv1d_fwd", "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_chunk_bwd_get_device_status", "gdn_chunk_fwd_host_workspace_size", "gdn_chunk_fwd_host",
             "gdn_chunk_fwd_host_get_device_status", "gdn_selective_scan_fwd_workspace_size",
-            "gdn_selective_scan_fwd", "gdn_selective_scan_get_device_status", "gdn_selective_scan_step",
+            "gdn_selective_scan_fwd", "gdn_selective_scan_fwd_pool", "gdn_selective_scan_get_device_status", "gdn_selective_scan_step",
             "gdn_selective_scan_bwd_workspace_size", "gdn_selective_scan_bwd",
             "gdn_causal_conv1d_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_q4_matvec"]
 
@@ -118,6 +118,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdn_selective_scan_fwd_workspace_size.restype = ctypes.c_size_t
         lib.gdn_selective_scan_fwd.argtypes = [SP] + [vp] * 13 + [ctypes.c_size_t, vp]
         lib.gdn_selective_scan_fwd.restype = ctypes.c_int
+        lib.gdn_selective_scan_fwd_pool.argtypes = [SP] + [vp] * 13 + [ctypes.c_int, vp, ctypes.c_size_t, vp]
+        lib.gdn_selective_scan_fwd_pool.restype = ctypes.c_int
         lib.gdn_selective_scan_get_device_status.argtypes = [SP, vp, vp, ctypes.POINTER(ctypes.c_int)]
         lib.gdn_selective_scan_get_device_status.restype = ctypes.c_int
         lib.gdn_selective_scan_step.argtypes = [SP] + [vp] * 10 + [ctypes.c_int, vp, vp, vp]
@@ -604,14 +606,23 @@ def _scan_sequences(x, cu_seqlens) -> int:
 
 def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, h0=None,
                            cu_seqlens=None, y=None, ht=None, output_final_state: bool = True, workspace=None,
-                           stream=None):
+                           stream=None, state_indices=None):
     """Selective state space scan.  x, delta, z [B, T, D], B and C [B, T, G, S] (one dtype, bf16 or fp32; rows
     may be slices of wider rows), A [D, S], D and dt_bias [D], h0 [N, D, S] fp32.  Returns (y, ht); ht is None
-    when ``output_final_state`` is False."""
+    when ``output_final_state`` is False.  With ``state_indices`` [N] int32, ht is a pool [slots, D, S] whose rows
+    they are (outside the pool: the sequence keeps no state)."""
     lib = _lib or load()
     _check_ws(workspace, x)
     state = (_scan_sequences(x, cu_seqlens), x.shape[-1], A.shape[-1])
-    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (("h0", h0, state), ("ht", ht, state)),
+    rows = state
+    if state_indices is not None:
+        if (ht is None or ht.dim() != 3 or ht.shape[0] == 0 or state_indices.dtype is not torch.int32
+                or state_indices.device != x.device or not state_indices.is_contiguous()
+                or state_indices.numel() != state[0]):
+            raise ValueError("state_indices must be a contiguous int32 CUDA tensor, one row of the pool ht "
+                             "[slots, D, S] a sequence")
+        rows = (ht.shape[0], *state[1:])
+    p = _scan_problem(x, delta, A, B, C, D, z, dt_bias, softplus, cu_seqlens, (("h0", h0, state), ("ht", ht, rows)),
                       (("y", y),) if y is not None else ())
     given = y, ht, workspace
     if y is None:
@@ -626,9 +637,13 @@ def gdn_selective_scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, soft
     if stream is not None:
         _lend(stream, x.device, [t for t, g in zip((y, ht, workspace), given) if g is None])
     s = stream if stream is not None else _current_stream(x.get_device())
-    st = lib.gdn_selective_scan_fwd(p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                                    _address(D), _address(z), _address(dt_bias), _address(h0), _address(cu_seqlens),
-                                    y.data_ptr(), _address(ht), workspace.data_ptr(), workspace.numel(), s)
+    call = (p, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _address(D), _address(z),
+            _address(dt_bias), _address(h0), _address(cu_seqlens), y.data_ptr(), _address(ht))
+    if state_indices is None:
+        st = lib.gdn_selective_scan_fwd(*call, workspace.data_ptr(), workspace.numel(), s)
+    else:
+        st = lib.gdn_selective_scan_fwd_pool(*call, state_indices.data_ptr(), rows[0], workspace.data_ptr(),
+                                             workspace.numel(), s)
     if st:
         raise GDNError(st, "gdn_selective_scan_fwd")
     return y, ht

@@ -319,10 +319,12 @@ size_t gdn_selective_scan_fwd_workspace_size(const gdn_scan_problem* pp) {
   return scan_problem_ok(pp, &p) == GDN_OK ? scan_fwd_workspace_bytes(p) : 0;
 }
 
-gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A,
-                                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
-                                  const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
-                                  float* ht, void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+// The scan forward, its final states to rows of ht in order or by a slot map.
+gdn_status scan_fwd(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A, const void* Bm,
+                    const void* Cm, const float* Dskip, const void* z, const float* dt_bias, const float* h0,
+                    const int32_t* cu_seqlens, void* y, float* ht, const int32_t* state_indices, int state_slots,
+                    void* workspace, size_t workspace_bytes, void* stream) {
   gdn_scan_problem p;
   const gdn_status ok = scan_problem_ok(pp, &p);
   if (ok != GDN_OK) return ok;
@@ -332,8 +334,27 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* pp, const void* x, con
   if ((int64_t)p.B * p.T > 0 && !y) return GDN_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < scan_fwd_workspace_bytes(p))
     return GDN_ERR_INVALID_ARG;
-  return run_scan_fwd(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, h0, cu_seqlens, y, ht, workspace,
-                      static_cast<cudaStream_t>(stream));
+  return run_scan_fwd(p, x, delta, A, Bm, Cm, Dskip, z, dt_bias, h0, cu_seqlens, y, ht, state_indices, state_slots,
+                      workspace, static_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A,
+                                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                  const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
+                                  float* ht, void* workspace, size_t workspace_bytes, void* stream) {
+  return scan_fwd(pp, x, delta, A, Bm, Cm, Dskip, z, dt_bias, h0, cu_seqlens, y, ht, nullptr, 0, workspace,
+                  workspace_bytes, stream);
+}
+
+gdn_status gdn_selective_scan_fwd_pool(const gdn_scan_problem* pp, const void* x, const void* delta, const float* A,
+                                       const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                       const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
+                                       float* state, const int32_t* state_indices, int state_slots, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  if (!state || !state_indices || !aligned(state_indices, 4) || state_slots <= 0) return GDN_ERR_INVALID_ARG;
+  return scan_fwd(pp, x, delta, A, Bm, Cm, Dskip, z, dt_bias, h0, cu_seqlens, y, state, state_indices, state_slots,
+                  workspace, workspace_bytes, stream);
 }
 
 gdn_status gdn_selective_scan_get_device_status(const gdn_scan_problem* pp, void* workspace, void* stream,

@@ -148,7 +148,8 @@ constexpr int kScanMaxD = 65536;   // channels (at most 32768 CTAs a line of tok
 size_t scan_fwd_workspace_bytes(const gdn_scan_problem& p);
 gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
                         const void* C, const float* Dp, const void* z, const float* dt_bias, const float* h0,
-                        const int32_t* cu, void* y, float* ht, void* ws, cudaStream_t s);
+                        const int32_t* cu, void* y, float* ht, const int32_t* state_indices, int state_slots,
+                        void* ws, cudaStream_t s);
 gdn_status run_scan_step(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
                          const void* C, const float* Dp, const void* z, const float* dt_bias, float* state,
                          const int32_t* state_indices, int state_slots, const int32_t* cu, void* y, cudaStream_t s);

@@ -287,7 +287,10 @@ __global__ void __launch_bounds__(32 * warps_of(RL), 3) scan_kernel(const Args a
   }
   float* to = nullptr;
   if (STATES) to = a.hseg + un * a.D * a.S;
-  else if (a.ht && u.last) to = a.ht + (int64_t)u.n * a.D * a.S;
+  else if (a.ht && u.last) {
+    const int r = a.slot ? a.slot[u.n] : u.n;
+    if (!a.slot || (r >= 0 && r < a.slots)) to = a.ht + (int64_t)r * a.D * a.S;
+  }
   if (to) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -724,12 +727,13 @@ size_t scan_fwd_workspace_bytes(const gdn_scan_problem& p) { return layout_of(p,
 
 gdn_status run_scan_fwd(const gdn_scan_problem& p, const void* x, const void* delta, const float* A, const void* B,
                         const void* C, const float* Dp, const void* z, const float* dt_bias, const float* h0,
-                        const int32_t* cu, void* y, float* ht, void* ws, cudaStream_t s) {
+                        const int32_t* cu, void* y, float* ht, const int32_t* state_indices, int state_slots,
+                        void* ws, cudaStream_t s) {
   const Plan pl = make_plan(p);
   const Layout l = layout_of(p, pl);
   Args a = base_args(p, pl, x, delta, A, B, C, Dp, z, dt_bias, h0, cu);
   char* w = static_cast<char*>(ws);
-  a.y = y, a.ht = ht;
+  a.y = y, a.ht = ht, a.slot = state_indices, a.slots = state_slots;
   const int es = p.dt == GDN_F32 ? 4 : 2;
   a.vy = a.Dg % 2 == 0 && aligned_rows(y, p.D * es, 2 * es);
   if (!a.vy) a.rows = kRegs;

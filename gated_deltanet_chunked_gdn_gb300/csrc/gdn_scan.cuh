@@ -52,7 +52,9 @@ struct Args {
   float* dtsum;             // [segments][D]: sum of dt over the segment
   // forward outputs
   void* y;
-  float* ht;
+  float* ht;                // [N][D][S], or a pool of `slots` such rows
+  const int32_t* slot;      // row of every sequence's final state (outside the pool: not kept), or null (row n)
+  int slots;
   bool vy;
 };
 

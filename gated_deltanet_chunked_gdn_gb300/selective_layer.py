@@ -104,15 +104,6 @@ def dequantize(qweight: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
     return (q * scales.float()[..., None]).view(qweight.shape[0], -1)
 
 
-def _pool_rows(slots, size):
-    """(src, rows, some): every sequence's final state goes to row ``rows[n]`` of a pool of ``size`` rows, taken from
-    sequence ``src[n]``.  A sequence whose slot is outside the pool has no state and repeats the first that has one
-    (the same value to the same row), so that the device decides and the host does not wait; ``some``: there is one."""
-    known = (slots >= 0) & (slots < size)
-    src = torch.where(known, torch.arange(slots.numel(), device=slots.device), known.int().argmax())
-    return src, slots[src].long().clamp(0, size - 1), known.any()
-
-
 PROJECTIONS = ("in_proj", "x_proj", "dt_proj", "out_proj")
 
 
@@ -202,11 +193,8 @@ class SelectiveLayer(torch.nn.Module):
                                                                                          device=u.device),
                                       cu_seqlens=cu_seqlens)
         dt, B, C = self._split(x @ self.x_proj.t())
-        src, rows, some = _pool_rows(slots, scan.shape[0])
-        before = scan[rows]
-        y, ht = gdn.gdn_selective_scan_fwd(x, dt @ self.dt_proj.t(), -torch.exp(self.A_log), B, C, D=self.Dskip, z=z,
-                                           dt_bias=self.dt_bias, cu_seqlens=cu_seqlens, ht=before.clone())
-        scan[rows] = torch.where(some, ht[src], before)
+        y, _ = gdn.gdn_selective_scan_fwd(x, dt @ self.dt_proj.t(), -torch.exp(self.A_log), B, C, D=self.Dskip, z=z,
+                                          dt_bias=self.dt_bias, cu_seqlens=cu_seqlens, ht=scan, state_indices=slots)
         return y @ self.out_proj.t()
 
     @torch.no_grad()

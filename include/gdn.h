@@ -502,6 +502,20 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_problem* p, const void* x, cons
                                   const void* Bm, const void* Cm, const float* Dskip, const void* z,
                                   const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
                                   float* ht, void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * The same, with the final states written to rows of a pool, as
+ * gdn_selective_scan_step finds them: prompts of new sequences.
+ *   state       : [state_slots, D, S] fp32 pool;  state_indices : [N] int32, row
+ *                 of each sequence.  A sequence whose row is outside
+ *                 [0, state_slots) keeps no state (its outputs are computed);
+ *                 distinct sequences must use distinct rows.  The pool must not
+ *                 overlap h0.  Malformed cu_seqlens leave it as it is.
+ */
+gdn_status gdn_selective_scan_fwd_pool(const gdn_scan_problem* p, const void* x, const void* delta, const float* A,
+                                       const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                       const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* y,
+                                       float* state, const int32_t* state_indices, int state_slots, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 /* Status word that the last scan call on `workspace` left (forward or
  * backward; synchronises `stream`, then clears the word).  Equal-length calls
  * write none: GDN_DEV_OK. */

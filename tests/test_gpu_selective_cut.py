@@ -103,3 +103,29 @@ def test_layer_gradients_packed(gdn):
     for k, v in layer.named_parameters():
         assert rel_fro(v.grad.double().cpu(), p[k].grad) <= 5e-2, k
     assert rel_fro(u.grad.double().cpu(), u64.grad) <= 5e-2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,D,S,G,lens", [(5, 20, 50, 16, 1, None), (5, 700, 6, 30, 1, None),
+                                            (1, 0, 64, 16, 2, [300, 0, 700, 1, 129]), (1, 0, 7, 3, 1, [5, 0, 1, 40, 16])])
+def test_final_states_into_a_pool(gdn, dtype, B, T, D, S, G, lens):
+    """Rows of a pool as a map gives them, bit for bit the states in order; no state outside, no other row touched."""
+    inp = cuda(R.make_scan(B, T, D, S, G, dtype, init=True, lens=lens, seed=T))
+    y, ht = gdn.gdn_selective_scan_fwd(**inp, cu_seqlens=offsets(lens))
+    slots = [6, -1, 0, 9, 3]                                     # nine rows: the fourth is past them
+    pool = torch.full((9, D, S), 7.0, device="cuda")
+    y2, same = gdn.gdn_selective_scan_fwd(**inp, cu_seqlens=offsets(lens), ht=pool,
+                                          state_indices=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    assert same is pool and torch.equal(y, y2)
+    for row in range(9):
+        assert torch.equal(pool[row], ht[slots.index(row)]) if row in slots else torch.all(pool[row] == 7.0)
+
+
+def test_malformed_offsets_leave_the_pool(gdn):
+    inp = cuda(R.make_scan(1, 30, 16, 4, 1, "f32", seed=11))
+    inp.pop("h0")
+    pool = torch.full((4, 16, 4), 7.0, device="cuda")
+    for bad in ([0, 20, 10, 30], [0, 10, 20, 29], [0, 10, 40, 30]):
+        gdn.gdn_selective_scan_fwd(**inp, cu_seqlens=torch.tensor(bad, dtype=torch.int32, device="cuda"), ht=pool,
+                                   state_indices=torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda"))
+        assert torch.all(pool == 7.0)

@@ -27,15 +27,17 @@ def conv_fwd(x, weight, bias=None, activation="silu", conv_state=None, cache_ind
 
 
 def scan_fwd(x, delta, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, ht=None,
-             output_final_state=True):
-    """gdn_selective_scan_fwd; malformed offsets leave ht unwritten."""
+             output_final_state=True, state_indices=None):
+    """gdn_selective_scan_fwd; malformed offsets leave ht unwritten, and so does a row outside the pool."""
     lens = lens_of(cu_seqlens)
     if ht is None:
         ht = torch.full((len(lens or x), *A.shape), float("nan"))
     if lens is not None and (min(lens) < 0 or sum(lens) != x.shape[1]):
         return torch.zeros_like(x), ht
     y, h = R.scan(x, delta, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=h0, lens=lens)
-    ht.copy_(h)
+    for n, row in enumerate(range(len(h)) if state_indices is None else state_indices.tolist()):
+        if 0 <= row < len(ht):
+            ht[row] = h[n]
     return y.to(x.dtype), ht
 
 

@@ -29,7 +29,11 @@ EXPORTED = ["gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_stag
             "gdn_chunk_fwd_host_get_device_status", "gdn_selective_scan_fwd_workspace_size",
             "gdn_selective_scan_fwd", "gdn_selective_scan_fwd_pool", "gdn_selective_scan_get_device_status", "gdn_selective_scan_step",
             "gdn_selective_scan_bwd_workspace_size", "gdn_selective_scan_bwd",
-            "gdn_causal_conv1d_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_q4_matvec"]
+            "gdn_causal_conv1d_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_q4_matvec",
+            "gdn_linear_attn_fwd_workspace_size", "gdn_linear_attn_fwd", "gdn_linear_attn_bwd_workspace_size",
+            "gdn_linear_attn_bwd", "gdn_linear_attn_get_device_status", "gdn_linear_attn_step", "gdn_gated_norm_fwd",
+            "gdn_gated_norm_bwd_workspace_size", "gdn_gated_norm_bwd", "gdn_residual_norm_fwd",
+            "gdn_residual_norm_bwd_workspace_size", "gdn_residual_norm_bwd"]
 
 
 class Problem(ctypes.Structure):
@@ -41,6 +45,11 @@ class Problem(ctypes.Structure):
 class ScanProblem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "N", "D", "S", "G", "dt", "varlen", "softplus")] + \
         [(n, ctypes.c_int64) for n in ("ld_x", "ld_delta", "ld_z", "ld_b", "ld_c")]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "N", "Hqk", "Hv", "K", "V", "dt", "varlen", "g_per_head")] + \
+        [(n, ctypes.c_int64) for n in ("ld_q", "ld_k", "ld_v")]
 
 
 class StagedLayout(ctypes.Structure):
@@ -135,6 +144,22 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdn_causal_conv1d_bwd.restype = ctypes.c_int
         lib.gdn_q4_matvec.argtypes = [vp, ctypes.c_int64, vp, vp, ctypes.c_int, vp, fp] + [ctypes.c_int] * 5 + [vp, vp]
         lib.gdn_q4_matvec.restype = ctypes.c_int
+        LP, sz, i64, ci, cf = ctypes.POINTER(LinearProblem), ctypes.c_size_t, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+        for name, args in (("gdn_linear_attn_fwd", [LP, vp, vp, vp, vp, cf, vp, vp, vp, vp, vp, ci, vp, sz, vp]),
+                           ("gdn_linear_attn_bwd", [LP, vp, vp, vp, vp, cf] + [vp] * 10 + [sz, vp]),
+                           ("gdn_linear_attn_get_device_status", [vp, vp, ctypes.POINTER(ci)]),
+                           ("gdn_linear_attn_step", [LP, vp, vp, vp, vp, cf, vp, vp, ci, vp, vp, vp]),
+                           ("gdn_gated_norm_fwd", [vp, i64, vp, i64, vp, ci, ci, ci, ci, cf, vp, vp, vp]),
+                           ("gdn_gated_norm_bwd", [vp, i64, vp, i64, vp, vp, vp] + [ci] * 4 + [vp] * 4 + [sz, vp]),
+                           ("gdn_residual_norm_fwd", [vp, i64, vp, vp, vp, ci, cf, vp] + [ci] * 4 + [cf] + [vp] * 4),
+                           ("gdn_residual_norm_bwd", [vp, i64, vp, vp, vp, vp, vp, vp, ci, cf, vp] + [ci] * 4 +
+                            [vp] * 6 + [sz, vp])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ci
+        for name, args in (("gdn_linear_attn_fwd_workspace_size", [LP]), ("gdn_linear_attn_bwd_workspace_size", [LP]),
+                           ("gdn_gated_norm_bwd_workspace_size", [ci]), ("gdn_residual_norm_bwd_workspace_size", [ci])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = sz
         lib.gdn_version.argtypes = []
         lib.gdn_version.restype = ctypes.c_char_p
         _lib = lib
@@ -827,3 +852,351 @@ def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None
     if st:
         raise GDNError(st, "gdn_q4_matvec")
     return y
+
+
+def _linear_problem(q, k, v, g, cu_seqlens, fp32=(), others=()):
+    """Checks of a linear attention's tensors and its problem.  fp32: (name, tensor, shape) that must be contiguous
+    float32; others: (name, tensor) that must be like v and contiguous."""
+    dtype, dev = v.dtype, v.get_device()
+    if dtype not in DTYPES or dev < 0 or q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k [B, T, Hqk, K] and v [B, T, Hv, V] must be float32 or bfloat16 CUDA tensors")
+    B, T, Hqk, K = qshape = q.shape
+    _, _, Hv, V = vshape = v.shape
+    if k.shape != qshape or vshape[0] != B or vshape[1] != T:
+        raise ValueError("q and k must have one shape, and v their batch and tokens")
+    for name, t in (("q", q), ("k", k), *others):
+        if t.dtype is not dtype or t.get_device() != dev:
+            raise ValueError(f"{name} must have the dtype and device of v")
+    for name, t in others:
+        if t.shape != vshape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with the shape of v")
+    per_head = g.dim() == 1
+    if (g.dtype is not torch.float32 or g.get_device() != dev or not g.is_contiguous()
+            or g.shape != ((Hv,) if per_head else (B, T, Hv))):
+        raise ValueError("g must be a contiguous float32 CUDA tensor [B, T, Hv], or [Hv] for one decay a head")
+    for name, t, want in fp32:
+        if t is not None and (t.dtype is not torch.float32 or t.get_device() != dev or t.shape != want
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {tuple(want)}")
+    N = B
+    if cu_seqlens is not None:
+        if (cu_seqlens.dtype is not torch.int32 or cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous()
+                or cu_seqlens.dim() != 1):
+            raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor [N + 1]")
+        N = cu_seqlens.numel() - 1
+    return LinearProblem(B, T, N, Hqk, Hv, K, V, DTYPES[dtype], int(cu_seqlens is not None), int(per_head),
+                         _row_stride("q", q, Hqk * K), _row_stride("k", k, Hqk * K), _row_stride("v", v, Hv * V))
+
+
+def _linear_state(q, v, cu_seqlens):
+    return _scan_sequences(q, cu_seqlens), v.shape[-2], q.shape[-1], v.shape[-1]
+
+
+def _slot_map(state_indices, n, dev, what):
+    if (state_indices.dtype is not torch.int32 or state_indices.get_device() != dev
+            or not state_indices.is_contiguous() or state_indices.numel() != n):
+        raise ValueError(f"state_indices must be a contiguous int32 CUDA tensor, one {what} a sequence")
+    return state_indices.data_ptr()
+
+
+def gdn_linear_attn_fwd(q, k, v, g, scale: Optional[float] = None, h0=None, cu_seqlens=None, o=None, ht=None,
+                        output_final_state: bool = True, state_indices=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head: S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  q, k
+    [B, T, Hqk, K] and v [B, T, Hv, V] (one dtype, bf16 or fp32; rows may be slices of wider rows), g fp32 [B, T, Hv]
+    or [Hv], h0 [N, Hv, K, V] fp32.  Returns (o, ht); ht is None when ``output_final_state`` is False.  With
+    ``state_indices`` [N] int32, ht is a pool [slots, Hv, K, V] whose rows they are (outside the pool: the sequence
+    keeps no state).  ``scale`` defaults to K ** -0.5."""
+    lib = _lib or load()
+    _check_ws(workspace, q)
+    state = _linear_state(q, v, cu_seqlens)
+    rows, idx, dev = state, 0, v.get_device()
+    if state_indices is not None:
+        if ht is None or ht.dim() != 4 or ht.shape[0] == 0:
+            raise ValueError("state_indices needs a pool ht [slots, Hv, K, V]")
+        idx = _slot_map(state_indices, state[0], dev, "row of the pool")
+        rows = (ht.shape[0], *state[1:])
+    p = _linear_problem(q, k, v, g, cu_seqlens, (("h0", h0, state), ("ht", ht, rows)),
+                        (("o", o),) if o is not None else ())
+    given = o, ht, workspace
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    if ht is None and output_final_state:
+        ht = torch.empty(state, dtype=torch.float32, device=v.device)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = lib.gdn_linear_attn_fwd_workspace_size(p)
+        if need == 0:
+            raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_linear_attn_fwd_workspace_size")
+        workspace = _alloc_ws(need, v.device)
+    if stream is not None:
+        _lend(stream, v.device, [t for t, x in zip((o, ht, workspace), given) if x is None])
+    with torch.cuda.device(dev):
+        st = lib.gdn_linear_attn_fwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                     state[2] ** -0.5 if scale is None else scale, _address(h0), _address(cu_seqlens),
+                                     o.data_ptr(), _address(ht), idx, rows[0], workspace.data_ptr(), workspace.numel(),
+                                     stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_linear_attn_fwd")
+    return o, ht
+
+
+def gdn_linear_attn_fwd_workspace_size(p: LinearProblem) -> int:
+    return int(load().gdn_linear_attn_fwd_workspace_size(ctypes.byref(p)))
+
+
+def gdn_linear_attn_bwd_workspace_size(p: LinearProblem) -> int:
+    return int(load().gdn_linear_attn_bwd_workspace_size(ctypes.byref(p)))
+
+
+def gdn_linear_attn_get_device_status(workspace, stream=None) -> int:
+    s = stream if stream is not None else _current_stream(workspace.get_device())
+    v = ctypes.c_int(0)
+    st = load().gdn_linear_attn_get_device_status(workspace.data_ptr(), s, ctypes.byref(v))
+    if st:
+        raise GDNError(st, "gdn_linear_attn_get_device_status")
+    return int(v.value)
+
+
+def gdn_linear_attn_bwd(q, k, v, g, dout, scale: Optional[float] = None, h0=None, dht=None, cu_seqlens=None,
+                        want_dh0: Optional[bool] = None, workspace=None, stream=None) -> dict:
+    """Backward of gdn_linear_attn_fwd for upstream gradients ``dout`` (dL/do, like v) and ``dht`` (dL/dht, fp32 or
+    None).  Returns dq, dk, dv (dtype of v), dg, dh0 (fp32) and the workspace under "workspace"; dh0 is None unless
+    ``want_dh0`` (by default: h0 is given)."""
+    lib = _lib or load()
+    _check_ws(workspace, q)
+    state, dev = _linear_state(q, v, cu_seqlens), v.get_device()
+    p = _linear_problem(q, k, v, g, cu_seqlens, (("h0", h0, state), ("dht", dht, state)), (("dout", dout),))
+    given = workspace
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = lib.gdn_linear_attn_bwd_workspace_size(p)
+        if need == 0:
+            raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_linear_attn_bwd_workspace_size")
+        workspace = _alloc_ws(need, v.device)
+    if want_dh0 is None:
+        want_dh0 = h0 is not None
+    like, f32 = dict(dtype=v.dtype, device=v.device), dict(dtype=torch.float32, device=v.device)
+    out = {"dq": torch.empty(q.shape, **like), "dk": torch.empty(k.shape, **like), "dv": torch.empty(v.shape, **like),
+           "dg": torch.empty(g.shape, **f32), "dh0": torch.empty(state, **f32) if want_dh0 else None}
+    if stream is not None:
+        _lend(stream, v.device, (*out.values(), workspace if given is None else None))
+    with torch.cuda.device(dev):
+        st = lib.gdn_linear_attn_bwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                     state[2] ** -0.5 if scale is None else scale, _address(h0), _address(cu_seqlens),
+                                     dout.data_ptr(), _address(dht), *(_address(t) for t in out.values()),
+                                     workspace.data_ptr(), workspace.numel(),
+                                     stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_linear_attn_bwd")
+    out["workspace"] = workspace
+    return out
+
+
+def gdn_linear_attn_step(q, k, v, g, state, scale: Optional[float] = None, state_indices=None, cu_seqlens=None, o=None,
+                         stream=None):
+    """The recurrence's tokens on a state pool (decode).  ``state`` [slots, Hv, K, V] fp32 is updated in place;
+    returns o.  Other arguments as for gdn_linear_attn_fwd."""
+    lib = _lib or load()
+    dev = v.get_device()
+    slots = state.shape[0]
+    p = _linear_problem(q, k, v, g, cu_seqlens, (("state", state, (slots, v.shape[-2], q.shape[-1], v.shape[-1])),),
+                        (("o", o),) if o is not None else ())
+    idx = 0 if state_indices is None else _slot_map(state_indices, p.N, dev, "slot")
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        if stream is not None:
+            _lend(stream, v.device, (o,))
+    with torch.cuda.device(dev):
+        st = lib.gdn_linear_attn_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                      p.K ** -0.5 if scale is None else scale, state.data_ptr(), idx, slots,
+                                      _address(cu_seqlens), o.data_ptr(),
+                                      stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_linear_attn_step")
+    return o
+
+
+def _norm_rows(name: str, t, inner: int, width: int):
+    """(rows, elements from one row to the next) of t, whose last ``inner`` dimensions are a row of ``width``."""
+    if t.is_contiguous():
+        return t.numel() // width if width else 0, width
+    lead, want = t.dim() - inner, 1
+    for i in range(t.dim() - 1, lead - 1, -1):
+        if t.shape[i] != 1 and t.stride(i) != want:
+            raise ValueError(f"{name} must have contiguous rows, one after the other at one stride")
+        want *= t.shape[i]
+    rows, ld = 1, 0
+    for i in range(lead - 1, -1, -1):
+        if t.shape[i] != 1:
+            if ld == 0:
+                ld = t.stride(i)
+            elif t.stride(i) != ld * rows:
+                raise ValueError(f"{name} must have contiguous rows, one after the other at one stride")
+            rows *= t.shape[i]
+    if ld != 0 and ld < width:
+        raise ValueError(f"{name} must have contiguous rows, one after the other at one stride")
+    return rows, ld or width
+
+
+def _check_like(dev, *tensors):
+    """(name, tensor, dtype, shape): contiguous CUDA tensors of the device."""
+    for name, t, dtype, shape in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or t.shape != shape
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the device of x")
+
+
+def _gated_norm(x, z, weight, others):
+    dtype, dev = x.dtype, x.get_device()
+    if dtype not in DTYPES or dev < 0 or x.dim() < 2:
+        raise ValueError("x must be a float32 or bfloat16 CUDA tensor [..., H, V]")
+    H, V = x.shape[-2:]
+    if z is not None and (z.shape != x.shape or z.dtype is not dtype or z.get_device() != dev):
+        raise ValueError("z must have the shape, dtype and device of x")
+    _check_like(dev, ("weight", weight, torch.float32, (V,)), *others)
+    rows, ld_x = _norm_rows("x", x, 2, H * V)
+    return rows, H, V, ld_x, _norm_rows("z", z, 2, H * V)[1] if z is not None else 0, DTYPES[dtype], dev
+
+
+def gdn_gated_norm_fwd(x, z, weight, eps: float = 1e-6, y=None, save_rstd: bool = False, stream=None):
+    """y = silu(z) * weight * x / rms(x) for every head: x, z [..., H, V] (bf16 or fp32; rows of H * V may be slices of
+    wider rows; z None: no gate), weight [V] fp32.  Returns (y, rstd); rstd [..., H] fp32 is None unless
+    ``save_rstd`` (for the backward)."""
+    lib = _lib or load()
+    rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("y", y, x.dtype, x.shape),))
+    fresh = []
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        fresh.append(y)
+    rstd = None
+    if save_rstd:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        fresh.append(rstd)
+    if stream is not None:
+        _lend(stream, x.device, fresh)
+    with torch.cuda.device(dev):
+        st = lib.gdn_gated_norm_fwd(x.data_ptr(), ld_x, _address(z), ld_z, weight.data_ptr(), rows, H, V, dt, eps,
+                                    y.data_ptr(), _address(rstd),
+                                    stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_gated_norm_fwd")
+    return y, rstd
+
+
+def gdn_gated_norm_bwd(x, z, weight, rstd, dy, workspace=None, stream=None) -> dict:
+    """Backward of gdn_gated_norm_fwd for ``dy`` (like y), with the rstd that it saved.  Returns dx, dz (None without
+    z), dweight (fp32) and the workspace under "workspace"."""
+    lib = _lib or load()
+    _check_ws(workspace, x)
+    rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("dy", dy, x.dtype, x.shape),
+                                                                 ("rstd", rstd, torch.float32, x.shape[:-1])))
+    given = workspace
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = lib.gdn_gated_norm_bwd_workspace_size(V)
+            if need == 0:
+                raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_gated_norm_bwd_workspace_size")
+            workspace = _alloc_ws(need, x.device)
+        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
+               "dz": torch.empty(x.shape, dtype=x.dtype, device=x.device) if z is not None else None,
+               "dweight": torch.empty((V,), dtype=torch.float32, device=x.device)}
+        if stream is not None:
+            _lend(stream, x.device, (*out.values(), workspace if given is None else None))
+        st = lib.gdn_gated_norm_bwd(x.data_ptr(), ld_x, _address(z), ld_z, weight.data_ptr(), rstd.data_ptr(),
+                                    dy.data_ptr(), rows, H, V, dt, *(_address(t) for t in out.values()),
+                                    workspace.data_ptr(), workspace.numel(),
+                                    stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_gated_norm_bwd")
+    out["workspace"] = workspace
+    return out
+
+
+def _residual_norm(y, residual, post_weight, gate, weight, others):
+    dtype, dev = y.dtype, y.get_device()
+    if dtype not in DTYPES or dev < 0 or y.dim() < 1:
+        raise ValueError("y must be a float32 or bfloat16 CUDA tensor [..., D]")
+    shape, D = y.shape, y.shape[-1]
+    if residual.dtype not in (dtype, torch.float32):
+        raise ValueError("residual must have the dtype of y, or float32")
+    kind = 0 if gate is None else 1 if gate.dim() == 1 and gate.dtype is torch.float32 and shape != gate.shape else 2
+    f32 = torch.float32
+    _check_like(dev, ("residual", residual, residual.dtype, shape), ("post_weight", post_weight, f32, (D,)),
+                ("gate", gate, *((f32, (D,)) if kind == 1 else (dtype, shape))), ("weight", weight, f32, (D,)),
+                *others)
+    rows, ld = _norm_rows("y", y, 1, D)
+    return rows, D, ld, kind, DTYPES[dtype], DTYPES[residual.dtype], dev
+
+
+def gdn_residual_norm_fwd(y, residual, post_weight=None, gate=None, residual_scale: float = 1.0, weight=None,
+                          eps: float = 1e-6, h=None, n=None, save_rstd: bool = False, stream=None):
+    """Between two blocks: h = residual + residual_scale * gate * (post_weight * y / rms(y)), n = weight * h / rms(h).
+    y [..., D] (bf16 or fp32; rows may be slices of wider rows), residual [..., D] (the dtype of y, or fp32), gate None,
+    [D] fp32 or [..., D] like y, post_weight (None: y as it is) and weight (None: no n) [D] fp32.  Returns
+    (h, n, rstd); h may be the residual itself, n is None without weight, rstd [..., 2] fp32 unless ``save_rstd``."""
+    lib = _lib or load()
+    rows, D, ld, kind, dt, rdt, dev = _residual_norm(y, residual, post_weight, gate, weight,
+                                                     (("h", h, residual.dtype, y.shape), ("n", n, y.dtype, y.shape)))
+    if n is not None and weight is None:
+        raise ValueError("n needs weight")
+    fresh = []
+    if h is None:
+        h = torch.empty(y.shape, dtype=residual.dtype, device=y.device)
+        fresh.append(h)
+    if n is None and weight is not None:
+        n = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        fresh.append(n)
+    rstd = None
+    if save_rstd:
+        rstd = torch.empty((*y.shape[:-1], 2), dtype=torch.float32, device=y.device)
+        fresh.append(rstd)
+    if stream is not None:
+        _lend(stream, y.device, fresh)
+    with torch.cuda.device(dev):
+        st = lib.gdn_residual_norm_fwd(y.data_ptr(), ld, residual.data_ptr(), _address(post_weight), _address(gate),
+                                       kind, residual_scale, _address(weight), rows, D, dt, rdt, eps, h.data_ptr(),
+                                       _address(n), _address(rstd),
+                                       stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_residual_norm_fwd")
+    return h, n, rstd
+
+
+def gdn_residual_norm_bwd(y, residual, rstd, dh, dn=None, post_weight=None, gate=None, residual_scale: float = 1.0,
+                          weight=None, workspace=None, stream=None) -> dict:
+    """Backward of gdn_residual_norm_fwd for ``dh`` (like h, or None) and ``dn`` (like n; with weight), from its inputs
+    (the residual as it was before the call) and the rstd that it saved.  Returns dy, dresidual, dpost_weight, dgate,
+    dweight (None where the input is) and the workspace under "workspace"."""
+    lib = _lib or load()
+    if workspace is not None and workspace.device != y.device:
+        raise ValueError("workspace must be on the device of y")
+    rows, D, ld, kind, dt, rdt, dev = _residual_norm(
+        y, residual, post_weight, gate, weight,
+        (("rstd", rstd, torch.float32, (*y.shape[:-1], 2)), ("dh", dh, residual.dtype, y.shape),
+         ("dn", dn, y.dtype, y.shape)))
+    if (dn is None) != (weight is None):
+        raise ValueError("dn and weight come together")
+    given = workspace
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = lib.gdn_residual_norm_bwd_workspace_size(D)
+            if need == 0:
+                raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_residual_norm_bwd_workspace_size")
+            workspace = _alloc_ws(need, y.device)
+        f32 = dict(dtype=torch.float32, device=y.device)
+        out = {"dy": torch.empty(y.shape, dtype=y.dtype, device=y.device),
+               "dresidual": torch.empty(y.shape, dtype=residual.dtype, device=y.device),
+               "dpost_weight": torch.empty((D,), **f32) if post_weight is not None else None,
+               "dgate": torch.empty(gate.shape, dtype=gate.dtype, device=y.device) if gate is not None else None,
+               "dweight": torch.empty((D,), **f32) if weight is not None else None}
+        if stream is not None:
+            _lend(stream, y.device, (*out.values(), workspace if given is None else None))
+        st = lib.gdn_residual_norm_bwd(y.data_ptr(), ld, residual.data_ptr(), rstd.data_ptr(), _address(dh),
+                                       _address(dn), _address(post_weight), _address(gate), kind, residual_scale,
+                                       _address(weight), rows, D, dt, rdt, *(_address(t) for t in out.values()),
+                                       workspace.data_ptr(), workspace.numel(),
+                                       stream if stream is not None else _current_stream(dev))
+    if st:
+        raise GDNError(st, "gdn_residual_norm_bwd")
+    out["workspace"] = workspace
+    return out

@@ -68,6 +68,44 @@ bool scan_inputs_ok(const gdn_scan_problem& p, const void* x, const void* delta,
   return aligned(A, p.S % 4 == 0 ? 16 : 4) && aligned(Dskip, 4) && aligned(dt_bias, 4) && aligned(cu, 4);
 }
 
+// Shape checks of a linear attention problem; fills in N, the row strides and the flags.
+gdn_status linear_problem_ok(const gdn_linear_problem* pp, gdn_linear_problem* out) {
+  if (!pp) return GDN_ERR_INVALID_ARG;
+  gdn_linear_problem p = *pp;
+  if (p.dt != GDN_F32 && p.dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (p.Hqk <= 0 || p.Hv <= 0 || p.Hv % p.Hqk != 0 || !dim_ok(p.K) || !dim_ok(p.V)) return GDN_ERR_INVALID_ARG;
+  if (p.varlen) {
+    if (p.B != 1 || p.N <= 0 || p.T < 0) return GDN_ERR_INVALID_ARG;
+  } else {
+    if (p.B <= 0 || p.T <= 0) return GDN_ERR_INVALID_ARG;
+    p.N = p.B;
+  }
+  if (p.Hv > 1024) return GDN_ERR_UNSUPPORTED;
+  // tokens are int32 in the kernels (room for the last chunk's end), element offsets int64; the grids are one-dimensional
+  const int64_t tokens = (int64_t)p.B * p.T, blocks = (int64_t)(p.K / 64) * (p.V / 64) * p.Hv;
+  if (tokens >= ((int64_t)1 << 31) - 1024) return GDN_ERR_INVALID_ARG;
+  const int64_t chunks = p.varlen ? tokens / 64 + p.N : p.B * ceil_div(p.T, 64);
+  if (chunks * blocks >= ((int64_t)1 << 31) || p.N * blocks * 4 >= ((int64_t)1 << 31)) return GDN_ERR_UNSUPPORTED;
+  int64_t* ld[3] = {&p.ld_q, &p.ld_k, &p.ld_v};
+  const int64_t row[3] = {(int64_t)p.Hqk * p.K, (int64_t)p.Hqk * p.K, (int64_t)p.Hv * p.V};
+  for (int i = 0; i < 3; ++i) {
+    if (*ld[i] == 0) *ld[i] = row[i];
+    if (*ld[i] < row[i] || *ld[i] % (p.dt == GDN_F32 ? 4 : 8) != 0) return GDN_ERR_INVALID_ARG;
+    if (*ld[i] > (1 << 28)) return GDN_ERR_UNSUPPORTED;
+  }
+  p.varlen = p.varlen != 0;
+  p.g_per_head = p.g_per_head != 0;
+  *out = p;
+  return GDN_OK;
+}
+
+bool linear_inputs_ok(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                      const int32_t* cu) {
+  if (p.varlen ? !cu : cu != nullptr) return false;
+  if ((int64_t)p.B * p.T > 0 && (!q || !k || !v || !g)) return false;
+  return aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(g, 4) && aligned(cu, 4);
+}
+
 gdn_path resolve(const gdn_problem& p, gdn_path path) {
   if (path == GDN_PATH_AUTO) {
     if (!fused_supported(p) && !fused1_supported(p)) return GDN_PATH_STAGED;
@@ -460,6 +498,188 @@ gdn_status gdn_q4_matvec(const void* x, int64_t ld_x, const uint8_t* qweight, co
   if (!x || !y) return GDN_ERR_INVALID_ARG;
   return run_q4_matvec(x, ld_x, qweight, scales, sdt, zeros, bias, M, N, K, group, dt, y,
                        static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_linear_attn_fwd_workspace_size(const gdn_linear_problem* pp) {
+  gdn_linear_problem p;
+  return linear_problem_ok(pp, &p) == GDN_OK ? linear_fwd_workspace_bytes(p) : 0;
+}
+
+gdn_status gdn_linear_attn_fwd(const gdn_linear_problem* pp, const void* q, const void* k, const void* v,
+                               const float* g, float scale, const float* h0, const int32_t* cu_seqlens, void* o,
+                               float* ht, const int32_t* state_indices, int state_slots, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  gdn_linear_problem p;
+  const gdn_status st = linear_problem_ok(pp, &p);
+  if (st != GDN_OK) return st;
+  if (!linear_inputs_ok(p, q, k, v, g, cu_seqlens) || !aligned(h0, 16) || !aligned(ht, 16) || !aligned(o, 16))
+    return GDN_ERR_INVALID_ARG;
+  if ((int64_t)p.B * p.T > 0 && !o) return GDN_ERR_INVALID_ARG;
+  if (state_indices && (!ht || state_slots <= 0 || !aligned(state_indices, 4))) return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < linear_fwd_workspace_bytes(p))
+    return GDN_ERR_INVALID_ARG;
+  return run_linear_fwd(p, q, k, v, g, scale, h0, cu_seqlens, o, ht, state_indices, state_slots, workspace,
+                        static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_problem* pp) {
+  gdn_linear_problem p;
+  return linear_problem_ok(pp, &p) == GDN_OK ? linear_bwd_workspace_bytes(p) : 0;
+}
+
+gdn_status gdn_linear_attn_bwd(const gdn_linear_problem* pp, const void* q, const void* k, const void* v,
+                               const float* g, float scale, const float* h0, const int32_t* cu_seqlens,
+                               const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
+                               float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_linear_problem p;
+  const gdn_status st = linear_problem_ok(pp, &p);
+  if (st != GDN_OK) return st;
+  if (!linear_inputs_ok(p, q, k, v, g, cu_seqlens)) return GDN_ERR_INVALID_ARG;
+  const void* a16[] = {h0, dht, dh0, dout, dq, dk, dv};
+  for (const void* x : a16)
+    if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)p.B * p.T > 0 && (!dout || !dq || !dk || !dv || !dg)) return GDN_ERR_INVALID_ARG;
+  if (p.g_per_head && !dg) return GDN_ERR_INVALID_ARG;
+  if (!aligned(dg, 4) || !workspace || !aligned(workspace, kAlign) ||
+      workspace_bytes < linear_bwd_workspace_bytes(p))
+    return GDN_ERR_INVALID_ARG;
+  return run_linear_bwd(p, q, k, v, g, scale, h0, cu_seqlens, dout, dht, dq, dk, dv, dg, dh0, workspace,
+                        static_cast<cudaStream_t>(stream));
+}
+
+gdn_status gdn_linear_attn_get_device_status(void* workspace, void* stream, int* dev_status) {
+  if (!workspace || !dev_status) return GDN_ERR_INVALID_ARG;
+  int32_t host = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaStreamSynchronize(s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (cudaMemcpy(&host, workspace, sizeof(host), cudaMemcpyDeviceToHost) != cudaSuccess) return GDN_ERR_CUDA;
+  if (cudaMemset(workspace, 0, sizeof(host)) != cudaSuccess) return GDN_ERR_CUDA;
+  *dev_status = host;
+  return GDN_OK;
+}
+
+gdn_status gdn_linear_attn_step(const gdn_linear_problem* pp, const void* q, const void* k, const void* v,
+                                const float* g, float scale, float* state, const int32_t* state_indices,
+                                int state_slots, const int32_t* cu_seqlens, void* o, void* stream) {
+  gdn_linear_problem p;
+  const gdn_status st = linear_problem_ok(pp, &p);
+  if (st != GDN_OK) return st;
+  if (!linear_inputs_ok(p, q, k, v, g, cu_seqlens) || !aligned(o, 16)) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)p.B * p.T > 0 && !o) return GDN_ERR_INVALID_ARG;
+  if (!state || !aligned(state, 16) || state_slots <= 0 || !aligned(state_indices, 4)) return GDN_ERR_INVALID_ARG;
+  if (!state_indices && state_slots < p.N) return GDN_ERR_INVALID_ARG;
+  return run_linear_step(p, q, k, v, g, scale, state, state_indices, state_slots, cu_seqlens, o,
+                         static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+bool dtype_ok(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
+size_t size_of(gdn_dtype d) { return d == GDN_F32 ? 4 : 2; }
+
+gdn_status gated_norm_ok(int64_t* ld_x, int64_t* ld_z, const void* x, const void* z, const float* weight, int rows,
+                         int H, int V, gdn_dtype dt) {
+  if (!dtype_ok(dt) || rows < 0 || H <= 0 || V <= 0) return GDN_ERR_INVALID_ARG;
+  if (V > kNormMaxWidth || (int64_t)H * V >= ((int64_t)1 << 31) || (int64_t)rows * H >= ((int64_t)1 << 31) - 1024)
+    return GDN_ERR_UNSUPPORTED;
+  if (*ld_x == 0) *ld_x = (int64_t)H * V;
+  if (*ld_z == 0) *ld_z = (int64_t)H * V;
+  if (*ld_x < (int64_t)H * V || *ld_z < (int64_t)H * V) return GDN_ERR_INVALID_ARG;
+  const size_t es = size_of(dt);
+  if (!aligned(x, es) || !aligned(z, es) || !weight || !aligned(weight, 4)) return GDN_ERR_INVALID_ARG;
+  return rows > 0 && !x ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+
+gdn_status residual_norm_ok(int64_t* ld_y, const void* y, const void* residual, const float* post_weight,
+                            const void* gate, gdn_gate kind, const float* weight, int rows, int D, gdn_dtype dt,
+                            gdn_dtype rdt) {
+  if (!dtype_ok(dt) || !dtype_ok(rdt) || rows < 0 || D <= 0) return GDN_ERR_INVALID_ARG;
+  if (dt == GDN_F32 && rdt != GDN_F32) return GDN_ERR_INVALID_ARG;
+  if (kind != GDN_GATE_NONE && kind != GDN_GATE_CHANNEL && kind != GDN_GATE_ELEMENT) return GDN_ERR_INVALID_ARG;
+  if (D > kNormMaxWidth || rows >= 0x7fffffff - 1024) return GDN_ERR_UNSUPPORTED;
+  if (*ld_y == 0) *ld_y = D;
+  if (*ld_y < D) return GDN_ERR_INVALID_ARG;
+  if ((kind == GDN_GATE_NONE) != (gate == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(y, size_of(dt)) || !aligned(residual, size_of(rdt)) || !aligned(post_weight, 4) ||
+      !aligned(weight, 4) || !aligned(gate, kind == GDN_GATE_CHANNEL ? 4 : size_of(dt)))
+    return GDN_ERR_INVALID_ARG;
+  return rows > 0 && (!y || !residual) ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+
+}  // namespace
+
+gdn_status gdn_gated_norm_fwd(const void* x, int64_t ld_x, const void* z, int64_t ld_z, const float* weight, int rows,
+                              int H, int V, gdn_dtype dt, float eps, void* y, float* rstd, void* stream) {
+  const gdn_status st = gated_norm_ok(&ld_x, &ld_z, x, z, weight, rows, H, V, dt);
+  if (st != GDN_OK) return st;
+  if ((rows > 0 && !y) || !aligned(y, size_of(dt)) || !aligned(rstd, 4)) return GDN_ERR_INVALID_ARG;
+  if (rows == 0) return GDN_OK;
+  return run_gated_norm_fwd(x, ld_x, z, ld_z, weight, rows, H, V, dt, eps, y, rstd, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_gated_norm_bwd_workspace_size(int V) {
+  return V > 0 && V <= kNormMaxWidth ? gated_norm_bwd_workspace_bytes(V) : 0;
+}
+
+gdn_status gdn_gated_norm_bwd(const void* x, int64_t ld_x, const void* z, int64_t ld_z, const float* weight,
+                              const float* rstd, const void* dy, int rows, int H, int V, gdn_dtype dt, void* dx,
+                              void* dz, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  const gdn_status st = gated_norm_ok(&ld_x, &ld_z, x, z, weight, rows, H, V, dt);
+  if (st != GDN_OK) return st;
+  const size_t es = size_of(dt);
+  if ((z == nullptr) != (dz == nullptr) || (rows > 0 && (!rstd || !dy || !dx)) || !dweight) return GDN_ERR_INVALID_ARG;
+  if (!aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dy, es) || !aligned(dx, es) || !aligned(dz, es))
+    return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < gated_norm_bwd_workspace_bytes(V))
+    return GDN_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return cudaMemsetAsync(dweight, 0, sizeof(float) * V, s) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return run_gated_norm_bwd(x, ld_x, z, ld_z, weight, rstd, dy, rows, H, V, dt, dx, dz, dweight, workspace, s);
+}
+
+gdn_status gdn_residual_norm_fwd(const void* y, int64_t ld_y, const void* residual, const float* post_weight,
+                                 const void* gate, gdn_gate gate_kind, float residual_scale, const float* weight,
+                                 int rows, int D, gdn_dtype dt, gdn_dtype rdt, float eps, void* h, void* n,
+                                 float* rstd, void* stream) {
+  const gdn_status st = residual_norm_ok(&ld_y, y, residual, post_weight, gate, gate_kind, weight, rows, D, dt, rdt);
+  if (st != GDN_OK) return st;
+  if (rows == 0) return GDN_OK;
+  if (!h || (weight == nullptr) != (n == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(h, size_of(rdt)) || !aligned(n, size_of(dt)) || !aligned(rstd, 4)) return GDN_ERR_INVALID_ARG;
+  return run_residual_norm_fwd(y, ld_y, residual, post_weight, gate, gate_kind, residual_scale, weight, rows, D, dt, rdt,
+                               eps, h, n, rstd, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_residual_norm_bwd_workspace_size(int D) {
+  return D > 0 && D <= kNormMaxWidth ? residual_norm_bwd_workspace_bytes(D) : 0;
+}
+
+gdn_status gdn_residual_norm_bwd(const void* y, int64_t ld_y, const void* residual, const float* rstd, const void* dh,
+                                 const void* dn, const float* post_weight, const void* gate, gdn_gate gate_kind,
+                                 float residual_scale, const float* weight, int rows, int D, gdn_dtype dt,
+                                 gdn_dtype rdt, void* dy, void* dresidual, float* dpost_weight, void* dgate,
+                                 float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  const gdn_status st = residual_norm_ok(&ld_y, y, residual, post_weight, gate, gate_kind, weight, rows, D, dt, rdt);
+  if (st != GDN_OK) return st;
+  const size_t es = size_of(dt), er = size_of(rdt);
+  if ((post_weight == nullptr) != (dpost_weight == nullptr) || (weight == nullptr) != (dweight == nullptr))
+    return GDN_ERR_INVALID_ARG;
+  if (!aligned(rstd, 4) || !aligned(dh, er) || !aligned(dn, es) || !aligned(dy, es) || !aligned(dresidual, er) ||
+      !aligned(dpost_weight, 4) || !aligned(dweight, 4) || !aligned(dgate, gate_kind == GDN_GATE_CHANNEL ? 4 : es))
+    return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < residual_norm_bwd_workspace_bytes(D))
+    return GDN_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {   // the sums over no rows
+    float* sums[3] = {dpost_weight, dweight, gate_kind == GDN_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr};
+    for (float* x : sums)
+      if (x && cudaMemsetAsync(x, 0, sizeof(float) * D, s) != cudaSuccess) return GDN_ERR_CUDA;
+    return GDN_OK;
+  }
+  if (!rstd || !dy || !dresidual || (weight == nullptr) != (dn == nullptr) || (gate == nullptr) != (dgate == nullptr))
+    return GDN_ERR_INVALID_ARG;
+  return run_residual_norm_bwd(y, ld_y, residual, rstd, dh, dn, post_weight, gate, gate_kind, residual_scale, weight,
+                               rows, D, dt, rdt, dy, dresidual, dpost_weight, dgate, dweight, workspace, s);
 }
 
 const char* gdn_status_string(gdn_status s) {

@@ -175,6 +175,37 @@ gdn_status run_q4_matvec(const void* x, int64_t ldx, const uint8_t* qweight, con
                          const uint8_t* zeros, const float* bias, int M, int N, int K, int group, gdn_dtype dt,
                          void* y, cudaStream_t s);
 
+// Decayed linear attention (gdn_linear.cu, gdn_linear_bwd.cu): problems with
+// their row strides filled in.
+size_t linear_fwd_workspace_bytes(const gdn_linear_problem& p);
+gdn_status run_linear_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                          float scale, const float* h0, const int32_t* cu, void* o, float* ht,
+                          const int32_t* state_indices, int state_slots, void* ws, cudaStream_t s);
+gdn_status run_linear_step(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                           float scale, float* state, const int32_t* state_indices, int state_slots,
+                           const int32_t* cu, void* o, cudaStream_t s);
+size_t linear_bwd_workspace_bytes(const gdn_linear_problem& p);
+gdn_status run_linear_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                          float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht,
+                          void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s);
+
+// Norms (gdn_norms.cu); gmode as gdn_gate.
+constexpr int kNormMaxWidth = 16384;
+size_t gated_norm_bwd_workspace_bytes(int V);
+size_t residual_norm_bwd_workspace_bytes(int D);
+gdn_status run_gated_norm_fwd(const void* x, int64_t ldx, const void* z, int64_t ldz, const float* w, int tokens, int H,
+                              int V, gdn_dtype dt, float eps, void* y, float* rstd, cudaStream_t s);
+gdn_status run_gated_norm_bwd(const void* x, int64_t ldx, const void* z, int64_t ldz, const float* w, const float* rstd,
+                              const void* dy, int tokens, int H, int V, gdn_dtype dt, void* dx, void* dz, float* dw,
+                              void* ws, cudaStream_t s);
+gdn_status run_residual_norm_fwd(const void* y, int64_t ldy, const void* res, const float* pw, const void* gate,
+                                 int gmode, float scale, const float* w, int rows, int D, gdn_dtype dt, gdn_dtype rdt,
+                                 float eps, void* h, void* n, float* rstd, cudaStream_t s);
+gdn_status run_residual_norm_bwd(const void* y, int64_t ldy, const void* res, const float* rstd, const void* dh,
+                                 const void* dn, const float* pw, const void* gate, int gmode, float scale,
+                                 const float* w, int rows, int D, gdn_dtype dt, gdn_dtype rdt, void* dy, void* dres,
+                                 float* dpw, void* dgate, float* dw, void* ws, cudaStream_t s);
+
 // Chunk-parallel path (gdn_cp.cu): sequences cut into segments run in parallel.
 size_t cp_workspace_bytes(const gdn_problem& p);
 gdn_status run_cp(const gdn_problem& p, const void* q, const void* k, const void* v, const float* g,

@@ -1,0 +1,359 @@
+// gdn_linear.cu -- decayed linear attention: the forward pass in fp32 arithmetic for every type and head dim (three
+// launches over 64-token chunks: the chunks' own states, the sums along each sequence, the outputs), and the step on a
+// state pool.  bf16 prompts and training run the tensor-core kernel of gdn_linear_tc.cu instead where it applies.
+#include "gdn_linear_simt.cuh"
+
+namespace gdn {
+namespace lin {
+
+// ------------------------------------------------- pieces of packed batches
+namespace {
+
+// One CTA: first piece of every sequence (a running sum over tiles of 1024 sequences), then every piece by a search
+// for its sequence.
+__global__ void __launch_bounds__(1024) pieces_kernel(const int32_t* __restrict__ cu, int N, int T, int size, int most,
+                                                      int32_t* __restrict__ seq, int32_t* __restrict__ tok0,
+                                                      int32_t* __restrict__ len, int32_t* __restrict__ first,
+                                                      int32_t* __restrict__ nc, int32_t* __restrict__ status) {
+  __shared__ int warp_sum[32];
+  __shared__ int carry, bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) carry = 0, bad = cu[0] != 0 || cu[N] != T;
+  __syncthreads();
+  for (int base = 0; base < N; base += 1024) {
+    const int n = base + tid;
+    int64_t L = 0;
+    if (n < N) {
+      const int64_t a = cu[n], b = cu[n + 1];
+      L = b - a;
+      if (L < 0 || a < 0 || b > T) bad = 1, L = 0;
+    }
+    const int mine = (int)((L + size - 1) / size);
+    int s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += t;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+      int w = warp_sum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += t;
+      }
+      warp_sum[lane] = w;
+    }
+    __syncthreads();
+    const int before = carry + (warp ? warp_sum[warp - 1] : 0) + s - mine;
+    if (n < N) first[n] = before;
+    __syncthreads();
+    if (tid == 1023) carry = before + mine;
+    __syncthreads();
+  }
+  const int total = carry;
+  if (tid == 0) {
+    if (total > most) bad = 1;
+    first[N] = total;
+    *nc = bad ? -1 : total;
+    if (bad) atomicExch(status, GDN_DEV_BAD_CU_SEQLENS);
+  }
+  __syncthreads();
+  if (bad) return;
+  for (int c = tid; c < total; c += 1024) {
+    int lo = 0, hi = N - 1;   // the last sequence with first <= c and pieces of its own
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= c) lo = mid;
+      else hi = mid - 1;
+    }
+    const int at = (c - first[lo]) * size, L = cu[lo + 1] - cu[lo];
+    seq[c] = lo;
+    tok0[c] = cu[lo] + at;
+    len[c] = L - at < size ? L - at : size;
+  }
+}
+
+}  // namespace
+
+int pieces_max(const gdn_linear_problem& p, int size) {
+  return (int)(p.varlen ? p.T / size + (int64_t)p.N : p.B * ceil_div(p.T, size));
+}
+
+size_t pieces_bytes(const gdn_linear_problem& p, int size) {
+  return p.varlen ? align_up(sizeof(int32_t) * (3 * (size_t)pieces_max(p, size) + p.N + 2)) : 0;
+}
+
+Pieces pieces_at(const gdn_linear_problem& p, int size, void* tables) {
+  Pieces t;
+  memset(&t, 0, sizeof(t));
+  t.T = p.T;
+  t.size = size;
+  t.per = (int)ceil_div(p.T, size);
+  if (p.varlen) {
+    const int most = pieces_max(p, size);
+    int32_t* at = static_cast<int32_t*>(tables);
+    t.seq = at;
+    t.tok0 = at + most;
+    t.len = at + 2 * (int64_t)most;
+    t.first = at + 3 * (int64_t)most;
+    t.nc = t.first + p.N + 1;
+  }
+  return t;
+}
+
+cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* cu, void* tables, int32_t* status,
+                          cudaStream_t s) {
+  if (!p.varlen) return cudaSuccess;
+  const Pieces t = pieces_at(p, size, tables);
+  pieces_kernel<<<1, 1024, 0, s>>>(cu, p.N, p.T, size, pieces_max(p, size), const_cast<int32_t*>(t.seq),
+                                   const_cast<int32_t*>(t.tok0), const_cast<int32_t*>(t.len),
+                                   const_cast<int32_t*>(t.first), const_cast<int32_t*>(t.nc), status);
+  return cudaGetLastError();
+}
+
+// -------------------------------------------------------------- the step
+namespace {
+
+// One CTA per (sequence, value head, COLS columns of V): the state's slice lives in registers for all of the
+// sequence's tokens (COLS / 4 column groups of float4, the other threads' groups along K) and is read and written
+// once.  Bound by the state's traffic, 8 K V bytes a head; streaming hints, since a pool larger than L2 is touched
+// once a step.
+template <typename T, int K, int COLS>
+__global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                       const T* __restrict__ v, int64_t ldq, int64_t ldk, int64_t ldv,
+                                                       const float* __restrict__ g, int g_per_head, float scale,
+                                                       float* __restrict__ state,
+                                                       const int32_t* __restrict__ state_indices, int slots,
+                                                       const int32_t* __restrict__ cu, int Tseq, int64_t Ttot, int Hqk,
+                                                       int Hv, int V, T* __restrict__ o) {
+  constexpr int CG = COLS / 4, RG = 256 / CG, RPG = K / RG;
+  static_assert(RPG >= 1 && RPG * RG == K, "every thread holds rows");
+  __shared__ float ks[K], qs[K];
+  __shared__ float part[8][COLS];
+  const int e0 = COLS * blockIdx.x, h = blockIdx.y % Hv;
+  const int n = blockIdx.y / Hv;
+  const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG, lane = tid & 31, warp = tid >> 5;
+  const int hq = h / (Hv / Hqk);
+  const int64_t tok0 = cu ? cu[n] : (int64_t)n * Tseq;
+  const int64_t L = cu ? (int64_t)cu[n + 1] - cu[n] : Tseq;
+  if (L <= 0 || tok0 < 0 || tok0 + L > Ttot) return;   // malformed offsets: touch nothing
+  const int slot = state_indices ? state_indices[n] : n;
+  if (slot < 0 || slot >= slots) {
+    for (int64_t t = 0; t < L; ++t)
+      if (tid < COLS) o[((tok0 + t) * Hv + h) * (int64_t)V + e0 + tid] = from_f<T>(0.f);
+    return;
+  }
+  float* S = state + (((int64_t)slot * Hv + h) * K) * (int64_t)V + e0 + 4 * cg;
+  float s[RPG][4];
+#pragma unroll
+  for (int r = 0; r < RPG; ++r) {
+    const float4 x = __ldcs(reinterpret_cast<const float4*>(S + (int64_t)(rg * RPG + r) * V));
+    s[r][0] = x.x, s[r][1] = x.y, s[r][2] = x.z, s[r][3] = x.w;
+  }
+  for (int64_t t = 0; t < L; ++t) {
+    const int64_t tok = tok0 + t;
+    if (tid < K) {
+      ks[tid] = to_f(k[tok * ldk + hq * K + tid]);
+      qs[tid] = to_f(q[tok * ldq + hq * K + tid]);
+    }
+    const float a = expf(g_per_head ? g[h] : g[tok * Hv + h]);
+    const float4 v4 = load4(v + tok * ldv + (int64_t)h * V + e0 + 4 * cg);
+    const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+    __syncthreads();
+    float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < RPG; ++r) {
+      const float kd = ks[rg * RPG + r], qd = qs[rg * RPG + r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[r][j] = fmaf(a, s[r][j], kd * vv[j]);
+        p[j] = fmaf(qd, s[r][j], p[j]);
+      }
+    }
+    // over the row groups of a warp by shuffles, over the warps through shared memory
+#pragma unroll
+    for (int off = CG; off < 32; off <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] += __shfl_xor_sync(0xffffffffu, p[j], off);
+    if (lane < CG) *reinterpret_cast<float4*>(&part[warp][4 * cg]) = make_float4(p[0], p[1], p[2], p[3]);
+    __syncthreads();
+    if (tid < COLS) {
+      float acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) acc += part[w][tid];
+      o[(tok * Hv + h) * (int64_t)V + e0 + tid] = from_f<T>(scale * acc);
+    }
+    // part is written again only after the next token's first barrier, which the readers above pass after reading
+  }
+#pragma unroll
+  for (int r = 0; r < RPG; ++r)
+    __stcs(reinterpret_cast<float4*>(S + (int64_t)(rg * RPG + r) * V), make_float4(s[r][0], s[r][1], s[r][2], s[r][3]));
+}
+
+template <typename T, int COLS>
+gdn_status launch_step(const gdn_linear_problem& p, const T* q, const T* k, const T* v, const float* g, float scale,
+                       float* state, const int32_t* idx, int slots, const int32_t* cu, T* o, cudaStream_t s) {
+  const int64_t y = (int64_t)p.N * p.Hv;
+  if (y > 65535) {   // sequences in several launches: the grid's second dimension ends there
+    const int per = 65535 / p.Hv;
+    for (int n = 0; n < p.N; n += per) {
+      gdn_linear_problem c = p;
+      c.N = p.N - n < per ? p.N - n : per;
+      const int64_t t = p.varlen ? 0 : (int64_t)n * p.T;
+      const gdn_status st = launch_step<T, COLS>(c, q + t * p.ld_q, k + t * p.ld_k, v + t * p.ld_v,
+                                                 p.g_per_head ? g : g + t * p.Hv, scale, idx ? state : state + (int64_t)n * p.Hv * p.K * p.V,
+                                                 idx ? idx + n : nullptr, idx ? slots : slots - n, p.varlen ? cu + n : nullptr,
+                                                 o + t * p.Hv * p.V, s);
+      if (st != GDN_OK) return st;
+    }
+    return GDN_OK;
+  }
+  const dim3 grid(p.V / COLS, (unsigned)y);
+  const int64_t Ttot = (int64_t)p.B * p.T;
+#define GDN_STEP(K)                                                                                                   \
+  lin_step_kernel<T, K, COLS><<<grid, 256, 0, s>>>(q, k, v, p.ld_q, p.ld_k, p.ld_v, g, p.g_per_head, scale, state,    \
+                                                   idx, slots, p.varlen ? cu : nullptr, p.T, Ttot, p.Hqk, p.Hv, p.V, o)
+  if (p.K == 64) GDN_STEP(64);
+  else if (p.K == 128) GDN_STEP(128);
+  else GDN_STEP(256);
+#undef GDN_STEP
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <typename T>
+gdn_status step_t(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                  float scale, float* state, const int32_t* idx, int slots, const int32_t* cu, void* o,
+                  cudaStream_t s) {
+  // few heads: narrower slices, so that every SM has some
+  if ((int64_t)p.N * p.Hv * (p.V / 64) < 2 * sm_count())
+    return launch_step<T, 16>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, state, idx, slots, cu, (T*)o, s);
+  return launch_step<T, 64>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, state, idx, slots, cu, (T*)o, s);
+}
+
+}  // namespace
+}  // namespace lin
+
+gdn_status run_linear_step(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                           float scale, float* state, const int32_t* idx, int slots, const int32_t* cu, void* o,
+                           cudaStream_t s) {
+  if ((int64_t)p.B * p.T == 0) return GDN_OK;
+  if (p.dt == GDN_F32) return lin::step_t<float>(p, q, k, v, g, scale, state, idx, slots, cu, o, s);
+  return lin::step_t<__nv_bfloat16>(p, q, k, v, g, scale, state, idx, slots, cu, o, s);
+}
+
+// --------------------------------------------------- forward, fp32 arithmetic
+namespace lin {
+namespace {
+
+// Outputs of one chunk of one value head: P = e^{b_i - b_j} q_i . k_j, then 64 columns of o at a time.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) outputs_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                           const T* __restrict__ v, Shape d, const float* __restrict__ g,
+                                                           Pieces pc, float scale, const float* __restrict__ S0,
+                                                           T* __restrict__ o) {
+  __shared__ __align__(16) float As[kC * kLd], Bs[kC * kLd], Ps[kC * kLd];
+  __shared__ float hi[kC], lo[kC], up[kC];
+  const int c = blockIdx.x / d.Hv, h = blockIdx.x % d.Hv, hq = h / (d.Hv / d.Hqk);
+  const Piece p = piece_of(pc, c);
+  if (!p.ok) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  if (tid < 32) chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, tid, hi, lo);
+  __syncthreads();
+  if (tid < kC) up[tid] = scale * expf(hi[tid] + lo[tid]);
+  const T* qp = q + p.tok0 * d.ldq + (int64_t)hq * d.K;
+  const T* kp = k + p.tok0 * d.ldk + (int64_t)hq * d.K;
+  const T* vp = v + p.tok0 * d.ldv + (int64_t)h * d.V;
+  float acc[4][4];
+  zero(acc);
+  for (int d0 = 0; d0 < d.K; d0 += kC) {
+    __syncthreads();
+    load_t(As, qp + d0, d.ldq, p.len, nullptr);
+    load_t(Bs, kp + d0, d.ldk, p.len, nullptr);
+    __syncthreads();
+    fma_tile(acc, As, Bs, ty, tx);
+  }
+  // P^T [j][i]
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = 4 * ty + r, j = 4 * tx + u;
+      const float e = expf((hi[i] - hi[j]) + (lo[i] - lo[j]));
+      Ps[j * kLd + i] = j <= i ? scale * e * acc[r][u] : 0.f;
+    }
+  const float* S = S0 + ((int64_t)c * d.Hv + h) * d.K * d.V;
+  for (int e0 = 0; e0 < d.V; e0 += kC) {
+    zero(acc);
+    for (int d0 = 0; d0 < d.K; d0 += kC) {
+      __syncthreads();
+      load_t(As, qp + d0, d.ldq, p.len, up);
+      load_n(Bs, S + (int64_t)d0 * d.V + e0, d.V, kC, nullptr);
+      __syncthreads();
+      fma_tile(acc, As, Bs, ty, tx);
+    }
+    __syncthreads();
+    load_n(Bs, vp + e0, d.ldv, p.len, nullptr);
+    __syncthreads();
+    fma_tile(acc, Ps, Bs, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 4 * ty + r;
+      if (i < p.len) store4(o + ((p.tok0 + i) * d.Hv + h) * (int64_t)d.V + e0 + 4 * tx, acc[r]);
+    }
+  }
+}
+
+template <typename T>
+gdn_status fwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v, const float* g, float scale,
+                 const float* h0, const Pieces& pc, T* o, float* ht, const int32_t* idx, int slots, float* states,
+                 float* total, cudaStream_t s) {
+  const Shape d = shape_of(p);
+  const int most = pieces_max(p, kC);
+  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, states, total, s);
+  if (st != GDN_OK) return st;
+  st = launch_sums<false>(d, pc, p.N, total, h0, states, ht, idx, slots, s);
+  if (st != GDN_OK || most == 0) return st;
+  outputs_kernel<T><<<(unsigned)((int64_t)most * p.Hv), kThreads, 0, s>>>(q, k, v, d, g, pc, scale, states, o);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+// [status][tables][total: chunks x Hv][states: chunks x Hv x K x V]
+size_t simt_fwd_bytes(const gdn_linear_problem& p) {
+  const size_t cells = (size_t)pieces_max(p, kC) * p.Hv;
+  return kAlign + pieces_bytes(p, kC) + align_up(4 * cells) + 4 * cells * p.K * p.V;
+}
+
+gdn_status simt_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                    float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx, int slots,
+                    void* ws, cudaStream_t s) {
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  int32_t* status = reinterpret_cast<int32_t*>(at);
+  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
+  void* tables = at + kAlign;
+  if (launch_pieces(p, kC, cu, tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
+  const Pieces pc = pieces_at(p, kC, tables);
+  float* total = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, kC));
+  float* states = total + align_up(4 * (size_t)pieces_max(p, kC) * p.Hv) / 4;
+  if (p.dt == GDN_F32)
+    return fwd_t<float>(p, (const float*)q, (const float*)k, (const float*)v, g, scale, h0, pc, (float*)o, ht, idx,
+                        slots, states, total, s);
+  using T = __nv_bfloat16;
+  return fwd_t<T>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, h0, pc, (T*)o, ht, idx, slots, states, total, s);
+}
+
+}  // namespace lin
+
+size_t linear_fwd_workspace_bytes(const gdn_linear_problem& p) { return lin::simt_fwd_bytes(p); }
+
+gdn_status run_linear_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                          float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx,
+                          int slots, void* ws, cudaStream_t s) {
+  return lin::simt_fwd(p, q, k, v, g, scale, h0, cu, o, ht, idx, slots, ws, s);
+}
+
+}  // namespace gdn

@@ -1,0 +1,85 @@
+// gdn_linear.cuh -- pieces shared by the kernels of decayed linear attention
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t            (S is [K][V], one per value head)
+//
+// in chunks of 64 tokens.  With b_i the sum of g over the chunk's tokens up to i, and S0 the state before the chunk,
+//
+//   o_i  = scale (e^{b_i} S0^T q_i + sum_{j <= i} e^{b_i - b_j} (q_i . k_j) v_j)
+//   S_64 = e^{b_last} S0 + sum_j e^{b_last - b_j} k_j v_j^T
+#pragma once
+
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace lin {
+
+constexpr int kC = 64;   // tokens a chunk
+
+// Chunks (or segments of chunks) of a batch.  Packed batches: tables that a launch before builds from cu_seqlens
+// (nc < 0: malformed); equal lengths: arithmetic.
+struct Pieces {
+  const int32_t* seq;    // null: equal lengths
+  const int32_t* tok0;
+  const int32_t* len;
+  const int32_t* first;  // [N + 1] first piece of each sequence
+  const int32_t* nc;
+  int T, per;            // equal lengths: tokens a sequence, pieces a sequence
+  int size;              // tokens a piece
+};
+
+struct Piece {
+  int seq, len;
+  int64_t tok0;
+  bool ok;
+};
+
+__device__ __forceinline__ Piece piece_of(const Pieces& t, int c) {
+  Piece p;
+  if (t.seq) {
+    p.ok = c < *t.nc;
+    p.seq = p.ok ? t.seq[c] : 0;
+    p.tok0 = p.ok ? t.tok0[c] : 0;
+    p.len = p.ok ? t.len[c] : 0;
+  } else {
+    p.ok = true;
+    p.seq = c / t.per;
+    const int at = (c - p.seq * t.per) * t.size;
+    p.tok0 = (int64_t)p.seq * t.T + at;
+    p.len = t.T - at < t.size ? t.T - at : t.size;
+  }
+  return p;
+}
+
+// Decays below e^-700 are 0 in fp32 (and -infinity among the sums would make differences of them NaN); NaN passes.
+__device__ __forceinline__ double log_decay(float g) { return g < -700.f ? -700.0 : (double)g; }
+
+// One warp: sums of the log decays of a chunk, as pairs of floats (hi + lo has the double's first 48 bits: the
+// difference of two sums keeps its precision behind a strong decay).  Rows past len add nothing.
+__device__ __forceinline__ void chunk_sums(const float* g, int64_t stride, int len, int lane, float* hi, float* lo) {
+  const int r = 2 * lane;
+  const double a = r < len ? log_decay(g[r * stride]) : 0.0;
+  const double b = r + 1 < len ? log_decay(g[(r + 1) * stride]) : 0.0;
+  double s = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+  const double s0 = s - b;
+  hi[r] = (float)s0, lo[r] = (float)(s0 - (double)(float)s0);
+  hi[r + 1] = (float)s, lo[r + 1] = (float)(s - (double)(float)s);
+}
+
+}  // namespace lin
+
+// Workspace layout and launches shared by the forward and the backward pass (gdn_linear.cu).
+namespace lin {
+size_t pieces_bytes(const gdn_linear_problem& p, int size);   // 0 for equal lengths
+int pieces_max(const gdn_linear_problem& p, int size);
+// Status word, then (packed batches) the tables of pieces of `size` tokens.
+Pieces pieces_at(const gdn_linear_problem& p, int size, void* tables);
+cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* cu, void* tables, int32_t* status,
+                          cudaStream_t s);
+}  // namespace lin
+
+}  // namespace gdn

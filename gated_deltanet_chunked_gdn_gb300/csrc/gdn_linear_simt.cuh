@@ -1,0 +1,194 @@
+// gdn_linear_simt.cuh -- fp32 tiles of decayed linear attention: 64 x 64 x 64 products by 256 threads (4 x 4 results a
+// thread, operands in shared memory with the summed dimension outermost), the chunks' own states, and the sums along a
+// sequence.
+#pragma once
+
+#include <string.h>
+
+#include "gdn_linear.cuh"
+
+namespace gdn {
+namespace lin {
+
+constexpr int kThreads = 256;
+constexpr int kLd = 68;   // row length of a tile in shared memory: 16-byte rows, transposed stores without conflicts
+
+// Head dims and row strides of a problem.
+struct Shape {
+  int Hqk, Hv, K, V, g_per_head;
+  int64_t ldq, ldk, ldv;
+};
+
+inline Shape shape_of(const gdn_linear_problem& p) {
+  return {p.Hqk, p.Hv, p.K, p.V, p.g_per_head, p.ld_q, p.ld_k, p.ld_v};
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                     __uint_as_float(x.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+__device__ __forceinline__ void zero(float (&a)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[i][j] = 0.f;
+}
+
+// dst[row][col] = src[row][col] * w[row] for 64 x 64 elements; rows past `rows` are zeros.
+template <typename T>
+__device__ __forceinline__ void load_n(float* dst, const T* src, int64_t ld, int rows, const float* w) {
+  const int c = 4 * (threadIdx.x & 15);
+#pragma unroll
+  for (int r = threadIdx.x >> 4; r < kC; r += kThreads / 16) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      x = load4(src + r * ld + c);
+      if (w) {
+        const float f = w[r];
+        x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+      }
+    }
+    *reinterpret_cast<float4*>(dst + r * kLd + c) = x;
+  }
+}
+
+// dst[col][row] = src[row][col] * w[row].
+template <typename T>
+__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t ld, int rows, const float* w) {
+  const int r = threadIdx.x & 63;
+  const float f = w ? w[r] : 1.f;
+#pragma unroll
+  for (int c = 4 * (threadIdx.x >> 6); c < kC; c += 16) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      x = load4(src + r * ld + c);
+      if (w) x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+    }
+    dst[c * kLd + r] = x.x, dst[(c + 1) * kLd + r] = x.y, dst[(c + 2) * kLd + r] = x.z, dst[(c + 3) * kLd + r] = x.w;
+  }
+}
+
+// acc[r][u] += sum_kk A[kk][4 ty + r] B[kk][4 tx + u] over 64 kk
+__device__ __forceinline__ void fma_tile(float (&acc)[4][4], const float* A, const float* B, int ty, int tx) {
+#pragma unroll 16
+  for (int kk = 0; kk < kC; ++kk) {
+    const float4 a = *reinterpret_cast<const float4*>(A + kk * kLd + 4 * ty);
+    const float4 b = *reinterpret_cast<const float4*>(B + kk * kLd + 4 * tx);
+    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) acc[r][u] = fmaf(av[r], bv[u], acc[r][u]);
+  }
+}
+
+// What a chunk adds to the state behind it, sum_j e^{b_last - b_j} x_j y_j^T (x = k, y = v), or, for the adjoint, to
+// the one before it, factor sum_i e^{b_i} x_i y_i^T (x = q, y = do): one 64 x 64 block of [K][V] a CTA.
+template <typename T, bool ADJ>
+__global__ void __launch_bounds__(kThreads) states_kernel(const T* __restrict__ x, int64_t ldx,
+                                                          const T* __restrict__ y, int64_t ldy, Shape d,
+                                                          const float* __restrict__ g, Pieces pc, float factor,
+                                                          float* __restrict__ S, float* __restrict__ total) {
+  __shared__ __align__(16) float Xs[kC * kLd], Ys[kC * kLd];
+  __shared__ float hi[kC], lo[kC], w[kC];
+  const int nb = (d.K / kC) * (d.V / kC);
+  const int blk = blockIdx.x % nb, ch = blockIdx.x / nb;
+  const int c = ch / d.Hv, h = ch % d.Hv, hq = h / (d.Hv / d.Hqk);
+  const int d0 = blk / (d.V / kC) * kC, e0 = blk % (d.V / kC) * kC;
+  const Piece p = piece_of(pc, c);
+  if (!p.ok) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  if (tid < 32) chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, tid, hi, lo);
+  __syncthreads();
+  if (tid < kC) {
+    w[tid] = ADJ ? factor * expf(hi[tid] + lo[tid]) : expf((hi[kC - 1] - hi[tid]) + (lo[kC - 1] - lo[tid]));
+    if (tid == kC - 1 && blk == 0) total[ch] = expf(hi[tid] + lo[tid]);
+  }
+  __syncthreads();
+  load_n(Xs, x + p.tok0 * ldx + (int64_t)hq * d.K + d0, ldx, p.len, w);
+  load_n(Ys, y + p.tok0 * ldy + (int64_t)h * d.V + e0, ldy, p.len, nullptr);
+  __syncthreads();
+  float acc[4][4];
+  zero(acc);
+  fma_tile(acc, Xs, Ys, ty, tx);
+  float* out = S + ((int64_t)ch * d.K + d0) * d.V + e0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) store4(out + (int64_t)(4 * ty + r) * d.V + 4 * tx, acc[r]);
+}
+
+// Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (REV: the adjoint of the
+// state behind it); four elements of a state a thread, the next chunks' loads in flight.
+template <bool REV>
+__global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const float* __restrict__ total,
+                                                   const float* __restrict__ init, float* __restrict__ S,
+                                                   float* __restrict__ fin, const int32_t* __restrict__ idx,
+                                                   int slots) {
+  const int64_t kv = (int64_t)d.K * d.V;
+  const int per = (int)(kv / 1024);   // CTAs a state
+  const int nh = blockIdx.x / per, n = nh / d.Hv, h = nh % d.Hv;
+  const int64_t at = ((int64_t)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
+  if (pc.seq && *pc.nc < 0) return;
+  const int c0 = pc.seq ? pc.first[n] : n * pc.per, c1 = pc.seq ? pc.first[n + 1] : c0 + pc.per;
+  float4 run = init ? load4(init + nh * kv + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int AHEAD = 4;
+  for (int base = 0; base < c1 - c0; base += AHEAD) {
+    float4 x[AHEAD];
+    float a[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int c = REV ? c1 - 1 - base - i : c0 + base + i;
+      if (base + i < c1 - c0) {
+        x[i] = __ldcs(reinterpret_cast<const float4*>(S + ((int64_t)c * d.Hv + h) * kv + at));
+        a[i] = total[(int64_t)c * d.Hv + h];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int c = REV ? c1 - 1 - base - i : c0 + base + i;
+      if (base + i < c1 - c0) {
+        *reinterpret_cast<float4*>(S + ((int64_t)c * d.Hv + h) * kv + at) = run;
+        run.x = fmaf(a[i], run.x, x[i].x), run.y = fmaf(a[i], run.y, x[i].y);
+        run.z = fmaf(a[i], run.z, x[i].z), run.w = fmaf(a[i], run.w, x[i].w);
+      }
+    }
+  }
+  if (fin) {
+    int64_t row = n;
+    if (idx) {
+      row = idx[n];
+      if (row < 0 || row >= slots) return;
+    }
+    *reinterpret_cast<float4*>(fin + (row * d.Hv + h) * kv + at) = run;
+  }
+}
+
+template <typename T, bool ADJ>
+gdn_status launch_states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g,
+                         const Pieces& pc, int most, float factor, float* S, float* total, cudaStream_t s) {
+  if (most == 0) return GDN_OK;
+  const int64_t grid = (int64_t)most * d.Hv * (d.K / kC) * (d.V / kC);
+  states_kernel<T, ADJ><<<(unsigned)grid, kThreads, 0, s>>>(x, ldx, y, ldy, d, g, pc, factor, S, total);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <bool REV>
+gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const float* init, float* S,
+                       float* fin, const int32_t* idx, int slots, cudaStream_t s) {
+  const int64_t grid = (int64_t)N * d.Hv * ((int64_t)d.K * d.V / 1024);
+  sums_kernel<REV><<<(unsigned)grid, 256, 0, s>>>(d, pc, total, init, S, fin, idx, slots);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace lin
+}  // namespace gdn

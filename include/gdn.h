@@ -568,6 +568,147 @@ gdn_status gdn_selective_scan_step(const gdn_scan_problem* p, const void* x, con
                                    int state_slots, const int32_t* cu_seqlens, void* y, void* stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrence without the delta
+ * rule's correction (a fixed decay a head, or one that depends on the token).
+ * For value head h, reading q/k head h / (Hv / Hqk),
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * States and sums are fp32; o is rounded once to p->dt (bf16: products of bf16
+ * operands, the weights between tokens and the copy of the state that o is
+ * formed from rounded to bf16; final states keep fp32 accuracy).
+ *
+ * Problem description.
+ *   B, T, N, Hqk, Hv, K, V, varlen : as for gdn_problem (Hv at most 1024)
+ *   dt         : dtype of q, k, v, o and of their gradients
+ *   g_per_head : 1: g is [Hv] fp32, one decay a head; 0: g is [B, T, Hv] fp32
+ *   ld_q, ld_k, ld_v : elements from one token's row (of Hqk * K or Hv * V) to
+ *                the next (0: contiguous); a sequence's tokens and the
+ *                sequences of a batch follow one another at this stride, so a
+ *                column slice of a wider matrix can be passed as it is.
+ * q, k, v, o, their gradients, states: 16-byte aligned, and row strides a
+ * multiple of 16 bytes.  g is a log decay, used as given (at most 0 in use; a
+ * growing head works as long as e^{sum of g over 64 tokens} stays in fp32;
+ * -infinity, or anything below -700, starts the state anew).  Outputs must not
+ * overlap inputs or one another, but ht may be h0 and dh0 may be h0 or dht (the
+ * same pointer).
+ */
+typedef struct {
+  int B, T, N, Hqk, Hv, K, V;
+  gdn_dtype dt;
+  int varlen;
+  int g_per_head;
+  int64_t ld_q, ld_k, ld_v;
+} gdn_linear_problem;
+
+/*
+ * Prompts or training sequences.
+ *   q, k    : [B, T, Hqk, K];  v : [B, T, Hv, V];  o : out [B, T, Hv, V], contiguous
+ *   h0      : [N, Hv, K, V] fp32 or NULL (= 0);  cu_seqlens as for gdn_chunk_fwd
+ *   ht      : out [N, Hv, K, V] fp32 or NULL; with state_indices ([N] int32) a
+ *             pool [state_slots, Hv, K, V], the final state of sequence n going
+ *             to row state_indices[n] (outside [0, state_slots): the sequence
+ *             keeps none; distinct sequences use distinct rows; the pool must
+ *             not overlap h0)
+ *   workspace : gdn_linear_attn_fwd_workspace_size(p) bytes (0: invalid
+ *             problem; query it with the device current that will run the
+ *             call), 256-byte aligned
+ * Malformed cu_seqlens set the status word (GDN_DEV_BAD_CU_SEQLENS, read with
+ * gdn_linear_attn_get_device_status) and leave o and ht unwritten.
+ * Asynchronous on `stream`; results do not depend on the run.
+ */
+size_t gdn_linear_attn_fwd_workspace_size(const gdn_linear_problem* p);
+gdn_status gdn_linear_attn_fwd(const gdn_linear_problem* p, const void* q, const void* k, const void* v,
+                               const float* g, float scale, const float* h0, const int32_t* cu_seqlens, void* o,
+                               float* ht, const int32_t* state_indices, int state_slots, void* workspace,
+                               size_t workspace_bytes, void* stream);
+/*
+ * Backward: for upstream gradients dout = dL/do and dht = dL/dht, the gradients
+ * of L with respect to every input.
+ *   dout        : [B, T, Hv, V] dtype p->dt, contiguous;  dht : [N, Hv, K, V] fp32 or NULL (= 0)
+ *   dq, dk      : out [B, T, Hqk, K] (summed over the value heads of a q/k head);
+ *                 dv : out [B, T, Hv, V]; dtype p->dt, rounded once, contiguous
+ *   dg          : out fp32, the shape of g
+ *   dh0         : out [N, Hv, K, V] fp32 or NULL
+ *   workspace   : gdn_linear_attn_bwd_workspace_size(p) bytes, 256-byte aligned
+ * No atomics: results do not depend on the run.  Malformed cu_seqlens as above.
+ */
+size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_problem* p);
+gdn_status gdn_linear_attn_bwd(const gdn_linear_problem* p, const void* q, const void* k, const void* v,
+                               const float* g, float scale, const float* h0, const int32_t* cu_seqlens,
+                               const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
+                               float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+/* Status word that the last call on `workspace` left (forward or backward;
+ * synchronises `stream`, then clears the word). */
+gdn_status gdn_linear_attn_get_device_status(void* workspace, void* stream, int* dev_status);
+/*
+ * Single tokens on a pool of states (decode); several tokens of a sequence run
+ * one after the other.
+ *   state       : [state_slots, Hv, K, V] fp32 pool, read and updated in place
+ *   state_indices, cu_seqlens : as for gdn_selective_scan_step
+ * No workspace; asynchronous on `stream`.
+ */
+gdn_status gdn_linear_attn_step(const gdn_linear_problem* p, const void* q, const void* k, const void* v,
+                                const float* g, float scale, float* state, const int32_t* state_indices,
+                                int state_slots, const int32_t* cu_seqlens, void* o, void* stream);
+
+/*
+ * Norm of a mixer's output with its gate, for every head of V elements:
+ *     y = silu(z) * weight * x / sqrt(mean(x^2) + eps)
+ *   x, z   : [rows, H, V] of dtype dt, rows ld_x, ld_z elements apart (0: H * V);
+ *            z NULL: no gate
+ *   weight : [V] fp32;  y : out [rows, H, V] dtype dt, contiguous
+ *   rstd   : out [rows, H] fp32, 1 / sqrt(mean(x^2) + eps), for the backward, or NULL
+ * V at most 16384, rows * H below 2^31.  Pointers need the alignment of their
+ * elements only (16-byte aligned rows are faster).  fp32 sums, one rounding.
+ */
+gdn_status gdn_gated_norm_fwd(const void* x, int64_t ld_x, const void* z, int64_t ld_z, const float* weight, int rows,
+                              int H, int V, gdn_dtype dt, float eps, void* y, float* rstd, void* stream);
+/*
+ * Its backward for dy (as y).  dx, dz : out, contiguous, dtype dt (dz NULL
+ * without z);  dweight : out [V] fp32, summed in a fixed order.  workspace:
+ * gdn_gated_norm_bwd_workspace_size(V) bytes (0: invalid; query it with the
+ * device current that will run the call), 256-byte aligned.
+ */
+size_t gdn_gated_norm_bwd_workspace_size(int V);
+gdn_status gdn_gated_norm_bwd(const void* x, int64_t ld_x, const void* z, int64_t ld_z, const float* weight,
+                              const float* rstd, const void* dy, int rows, int H, int V, gdn_dtype dt, void* dx,
+                              void* dz, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum { GDN_GATE_NONE = 0, GDN_GATE_CHANNEL = 1, GDN_GATE_ELEMENT = 2 } gdn_gate;
+
+/*
+ * Between two blocks: the norm after the one, its gate, the scaled residual sum
+ * and the norm before the next, in one pass:
+ *     u = post_weight * y / sqrt(mean(y^2) + eps)     (post_weight NULL: u = y)
+ *     h = residual + residual_scale * gate * u
+ *     n = weight * h / sqrt(mean(h^2) + eps)          (from h before its rounding)
+ *   y        : [rows, D] of dtype dt, rows ld_y elements apart (0: D)
+ *   residual, h : [rows, D] of dtype rdt (dt, or fp32), contiguous; h may be residual
+ *   gate     : NULL (GDN_GATE_NONE), [D] fp32 (GDN_GATE_CHANNEL) or [rows, D] of dtype dt (GDN_GATE_ELEMENT)
+ *   post_weight, weight : [D] fp32 or NULL;  n : out [rows, D] dtype dt, with weight, else NULL
+ *   rstd     : out [rows, 2] fp32 (of y, 1 without post_weight; of h, 1 without weight) or NULL
+ * D at most 16384.  Pointers need the alignment of their elements only.
+ */
+gdn_status gdn_residual_norm_fwd(const void* y, int64_t ld_y, const void* residual, const float* post_weight,
+                                 const void* gate, gdn_gate gate_kind, float residual_scale, const float* weight,
+                                 int rows, int D, gdn_dtype dt, gdn_dtype rdt, float eps, void* h, void* n,
+                                 float* rstd, void* stream);
+/*
+ * Its backward for dh (dtype rdt, NULL = 0) and dn (dtype dt; with weight, else
+ * NULL), from the forward's inputs (the residual as it was before) and rstd.
+ *   dy : out [rows, D] dtype dt;  dresidual : out [rows, D] dtype rdt (may be dh)
+ *   dpost_weight, dweight : out [D] fp32, with the weights, else NULL
+ *   dgate : out as gate, NULL without
+ *   workspace : gdn_residual_norm_bwd_workspace_size(D) bytes, 256-byte aligned
+ * Sums over rows are added in a fixed order.
+ */
+size_t gdn_residual_norm_bwd_workspace_size(int D);
+gdn_status gdn_residual_norm_bwd(const void* y, int64_t ld_y, const void* residual, const float* rstd, const void* dh,
+                                 const void* dn, const float* post_weight, const void* gate, gdn_gate gate_kind,
+                                 float residual_scale, const float* weight, int rows, int D, gdn_dtype dt,
+                                 gdn_dtype rdt, void* dy, void* dresidual, float* dpost_weight, void* dgate,
+                                 float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Test hook (no counterpart on the pages): y[i] = e^{x[i]} computed the way
  * the fused kernel computes its decay factors (2^{x log2 e} on the MUFU ex2
  * unit), so tests can bound its error against CUDA's expf.  x, y device

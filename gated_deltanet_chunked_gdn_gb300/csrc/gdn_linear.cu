@@ -348,12 +348,14 @@ gdn_status simt_fwd(const gdn_linear_problem& p, const void* q, const void* k, c
 
 }  // namespace lin
 
-size_t linear_fwd_workspace_bytes(const gdn_linear_problem& p) { return lin::simt_fwd_bytes(p); }
+size_t linear_fwd_workspace_bytes(const gdn_linear_problem& p) {
+  return lin::tc_supported(p) ? lin::tc_fwd_bytes(p) : lin::simt_fwd_bytes(p);
+}
 
 gdn_status run_linear_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                           float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx,
                           int slots, void* ws, cudaStream_t s) {
-  return lin::simt_fwd(p, q, k, v, g, scale, h0, cu, o, ht, idx, slots, ws, s);
+  return (lin::tc_supported(p) ? lin::tc_fwd : lin::simt_fwd)(p, q, k, v, g, scale, h0, cu, o, ht, idx, slots, ws, s);
 }
 
 }  // namespace gdn

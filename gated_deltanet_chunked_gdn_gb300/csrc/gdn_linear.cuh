@@ -80,6 +80,13 @@ int pieces_max(const gdn_linear_problem& p, int size);
 Pieces pieces_at(const gdn_linear_problem& p, int size, void* tables);
 cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* cu, void* tables, int32_t* status,
                           cudaStream_t s);
+
+// The tensor-core forward pass (gdn_linear_tc.cu).
+bool tc_supported(const gdn_linear_problem& p);
+size_t tc_fwd_bytes(const gdn_linear_problem& p);
+gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                  float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx, int slots,
+                  void* ws, cudaStream_t s);
 }  // namespace lin
 
 }  // namespace gdn

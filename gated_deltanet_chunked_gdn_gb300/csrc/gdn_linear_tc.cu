@@ -1,0 +1,593 @@
+// gdn_linear_tc.cu -- decayed linear attention of bf16 prompts and training batches on the tensor cores.
+//
+// A CTA walks a segment of a (sequence, value head, 128 columns of V) chain in chunks of 64 tokens.  Everything is
+// transposed so that every tcgen05.mma has M = 128 (TMEM lane = value column e, or token):
+//
+//   [K;Q] K^T                -> lanes 64..127: Q K^T                              (M128 N64)
+//   OQ^T = S^T Q^T           S^T: bf16 copy of the state before the chunk         (M128 N64)
+//   OP^T = V^T P^T           P = lower(scale e^{b_i - b_j} Q K^T), bf16           (M128 N64)
+//   U^T  = V''^T K           V'' = diag(e^{b_last - b_j}) V in two bf16 terms     (M128 N K)
+//   o_i  = scale e^{b_i} OQ_i + OP_i,   S^T <- e^{b_last} S^T + U^T
+//
+// The state itself stays in fp32 registers (a thread holds K / 2 columns of one row of S^T), and what a chunk adds to
+// it comes out of the tensor cores complete: V'' keeps 16 bits of the weighted values (2^-17 of each), so the final
+// state has fp32 accuracy although its inputs are bf16, and no sum longer than a chunk is left to the tensor cores'
+// accumulation.  o reads a bf16 copy of the state and bf16 weights: one rounding of each term, like o's own.
+// Two CTAs share an SM: one's loads and SIMT phases run under the other's products.
+//
+// Chains that do not fill the device are cut into segments of whole chunks: a launch before forms every segment's own
+// contribution and decay (no q, no outputs), and the sums along the sequence give the states the segments start from.
+//
+// Rows past a sequence's end are zeroed in the K and V tiles (they may hold another sequence's values, NaN among them)
+// and their weights are selected to zero; their outputs are not stored.
+#include <string.h>
+
+#include "gdn_linear_simt.cuh"
+#include "gdn_solve64.cuh"
+
+namespace gdn {
+namespace lin {
+namespace {
+
+using namespace sm100;
+using solve64::dsw;
+
+constexpr int kTcThreads = 256;
+
+struct TcParams {
+  const float* g;
+  const float* h0;       // [N][Hv][K][V]
+  const float* start;    // [segments][Hv][K][V] states before the segments, or null (one segment a sequence)
+  float* ht;             // final states (or a pool), or null
+  const int32_t* idx;
+  float* own;            // STATES: the segments' own contributions
+  float* total;          // STATES: their decays
+  __nv_bfloat16* o;
+  int32_t* status;
+  Pieces pc;
+  const int32_t* cu;
+  int slots, Hqk, Hv, V, g_per_head, varlen, T;
+  float scale;
+};
+
+// Shared memory, byte offsets from a 1024-byte aligned base.
+template <int KD, int VD>
+struct Map {
+  static constexpr uint32_t KQ = 0;                               // k rows 0..63, q rows 64..127; 64 columns an atom column
+  static constexpr uint32_t V = KQ + KD / 64 * 16384;
+  static constexpr uint32_t P = V + VD / 64 * 8192;
+  static constexpr uint32_t X = P + 8192;                         // S^T bf16 [e][d], then V'' [j][e] hi and lo
+  static constexpr uint32_t kS = (uint32_t)VD * KD * 2, kW = (uint32_t)VD * 64 * 2 * 2;
+  static constexpr uint32_t OS = X + (kS > kW ? kS : kW);         // o staging
+  static constexpr uint32_t Tail = OS + VD / 64 * 8192;
+  // rows 64..127 of a 64-row A tile are read (and ignored): they stay inside
+  static constexpr uint32_t Misc = Tail < X + 32768 ? X + 32768 : Tail;
+  static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512, Raw = Misc + 768;   // Raw: float[2][64]
+  static constexpr uint32_t Bar = Misc + 1280, Flags = Misc + 1344;
+  static constexpr uint32_t Used = Misc + 1408;
+  static constexpr uint32_t Bytes = Used + 1024;
+  static constexpr int Cols = KD + 128 <= 256 ? 256 : 512;        // TMEM: U^T, Q K^T / OP^T, OQ^T
+  static constexpr int Ctas = KD == 256 ? 1 : 2;
+};
+
+// a and b as sums of two bf16 values each, packed.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+
+// Decays of a chunk, by one warp: gam_i = log2(e) b_i, down_j = e^{b_last - b_j} (0 past the end), up_i = scale e^{b_i};
+// sums in 64 bits, so that down keeps fp32 accuracy behind a strong decay.
+__device__ __forceinline__ void tc_decays(const float* raw, int len, float scale, int lane, float* gam, float* down,
+                                          float* up) {
+  const int r = 2 * lane;
+  // e^-150 is 0 in fp32: stronger decays are cut there, and -infinity never meets itself in a difference
+  const float ga = raw[r] < -150.f ? -150.f : raw[r], gb = raw[r + 1] < -150.f ? -150.f : raw[r + 1];
+  const double a = r < len ? (double)ga : 0.0, b = r + 1 < len ? (double)gb : 0.0;
+  double s = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+  const double last = __shfl_sync(0xffffffffu, s, 31), s0 = s - b;
+  constexpr double kL = 1.4426950408889634;
+  gam[r] = (float)(s0 * kL), gam[r + 1] = (float)(s * kL);
+  down[r] = r < len ? expf((float)(last - s0)) : 0.f;
+  down[r + 1] = r + 1 < len ? expf((float)(last - s)) : 0.f;
+  up[r] = scale * expf((float)s0), up[r + 1] = scale * expf((float)s);
+}
+
+// V'' = diag(down) V: `n` threads (thread t of them), 8 columns of a row at a time; zeros where down is 0.
+template <int VD>
+__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, const float* down, int t, int n) {
+#pragma unroll 4
+  for (int u = t; u < 64 * (VD / 8); u += n) {
+    const int j = u / (VD / 8), c = u % (VD / 8);
+    const uint32_t off = (c >> 3) * 8192 + sw128_chunk(j, c & 7);
+    const uint4 w = *reinterpret_cast<const uint4*>(sm + v + off);
+    const float f = down[j];
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      split2(f * __uint_as_float(in[i] << 16), f * __uint_as_float(in[i] & 0xffff0000u), hi[i], lo[i]);
+    *reinterpret_cast<uint4*>(sm + x + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(sm + x + VD / 64 * 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+// Zeros in rows [from, 64) of a tile of 64-column atom columns `stride` bytes apart.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int columns, uint32_t stride, int from, int tid) {
+  const int n = (64 - from) * columns * 8;
+  for (int u = tid; u < n; u += kTcThreads) {
+    const int c = u % (columns * 8), r = from + u / (columns * 8);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * stride + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// FULL: outputs and final states.  Otherwise the segments' own contributions and decays.
+template <int KD, int VD, bool FULL>
+__global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
+    lin_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                  const TcParams prm) {
+  using M = Map<KD, VD>;
+  constexpr int KH = KD / 2;   // columns of S^T a thread holds
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
+  float* gam = reinterpret_cast<float*>(sm + M::Gam);
+  float* down = reinterpret_cast<float*>(sm + M::Down);
+  float* up = reinterpret_cast<float*>(sm + M::Up);
+  float* raw = reinterpret_cast<float*>(sm + M::Raw);
+  // every barrier completes one phase a chunk, and every thread that waits for it does so once a chunk, in order
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::Bar);
+  uint64_t *bar_kq = bars, *bar_v = bars + 1, *bar_qk = bars + 2, *bar_qs = bars + 3, *bar_pv = bars + 4,
+           *bar_u = bars + 5;
+  volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(sm + M::Flags);   // [0] TMEM base
+  volatile uint32_t* count = flags + 1;   // thread 0: phases begun on each barrier (what an abort has to wait for)
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qd = warp & 3, hf = warp >> 2;   // TMEM lane quadrant, half of the columns
+  const int row = 32 * qd + lane;
+  const int slices = prm.V / VD;
+  const int slice = blockIdx.x % slices, ch = blockIdx.x / slices;
+  const int c = ch / prm.Hv, h = ch % prm.Hv, hq = h / (prm.Hv / prm.Hqk), e0 = slice * VD;
+  const Piece p = piece_of(prm.pc, c);
+  if (!p.ok) return;
+  // first and last segment of its sequence
+  const int64_t seq0 = prm.varlen ? prm.cu[p.seq] : (int64_t)p.seq * prm.T;
+  const int64_t seq1 = prm.varlen ? prm.cu[p.seq + 1] : seq0 + prm.T;
+  const bool is_first = p.tok0 == seq0, is_last = p.tok0 + p.len == seq1;
+  if (!FULL && is_last) return;   // nobody starts behind it
+  const int nchunks = (p.len + 63) / 64;
+
+  if (tid == 0) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) mbar_init(bars + i, 1);
+    mbar_fence_init();
+#pragma unroll
+    for (int i = 0; i < 6; ++i) count[i] = 0;
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    if (FULL) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_o);
+    }
+  }
+  if (warp == 0) tmem_alloc(const_cast<uint32_t*>(flags), M::Cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = flags[0];
+  const uint32_t R_U = tmem, R_a = tmem + KD, R_b = tmem + KD + 64;
+  const uint32_t lane_off = static_cast<uint32_t>(32 * qd) << 16;
+
+  bool bad = false;   // one of this thread's waits ran out
+  auto issue_kq = [&](int i) {
+    const int t = (int)(p.tok0 + 64 * i);
+    count[0] = i + 1;
+    mbar_arrive_expect_tx(bar_kq, (FULL ? 2 : 1) * KD / 64 * 8192);
+#pragma unroll
+    for (int a = 0; a < KD / 64; ++a) {
+      tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_kq, 64 * a, hq, t);
+      if (FULL) tma_load_3d(sm + M::KQ + a * 16384 + 8192, &tm_q, bar_kq, 64 * a, hq, t);
+    }
+  };
+  auto issue_v = [&](int i) {
+    const int t = (int)(p.tok0 + 64 * i);
+    count[1] = i + 1;
+    mbar_arrive_expect_tx(bar_v, VD / 64 * 8192);
+#pragma unroll
+    for (int a = 0; a < VD / 64; ++a) tma_load_3d(sm + M::V + a * 8192, &tm_v, bar_v, e0 + 64 * a, h, t);
+  };
+  auto wait = [&](uint64_t* bar, int i) {
+    if (!bad) bad = !mbar_wait(bar, i & 1, prm.status);
+  };
+  auto commit = [&](int b, int i) {
+    mma_commit(bars + b);
+    count[b] = i + 1;
+  };
+  // warp 1 copies chunk i's log decays one chunk ahead (lane l: rows 2 l, 2 l + 1)
+  auto fetch_g = [&](int i) {
+    float* dst = raw + (i & 1) * 64;
+#pragma unroll
+    for (int r = 2 * lane; r < 2 * lane + 2; ++r) {
+      const int64_t t = 64 * (int64_t)i + r;
+      if (t < p.len) cp_async4(dst + r, prm.g + (prm.g_per_head ? h : (p.tok0 + t) * prm.Hv + h));
+    }
+    cp_async_commit();
+  };
+  if (tid == 0) {
+    issue_kq(0);
+    issue_v(0);
+  }
+  if (warp == 1) fetch_g(0);
+
+  // S^T[e = row][d = hf KH + i]
+  float S[KH];
+  {
+    const int64_t kv = (int64_t)KD * prm.V;
+    const float* from = nullptr;
+    if (FULL) {
+      if (!is_first && prm.start) from = prm.start + (int64_t)ch * kv;
+      else if (prm.h0) from = prm.h0 + ((int64_t)p.seq * prm.Hv + h) * kv;
+    }
+    if (from && row < VD) {
+      from += (int64_t)hf * KH * prm.V + e0 + row;
+#pragma unroll
+      for (int i = 0; i < KH; ++i) S[i] = from[(int64_t)i * prm.V];
+    } else {
+#pragma unroll
+      for (int i = 0; i < KH; ++i) S[i] = 0.f;
+    }
+  }
+  float dec = 1.f, total = 1.f;
+
+#pragma unroll 1
+  for (int i = 0; i < nchunks; ++i) {
+    const int len = p.len - 64 * i < 64 ? p.len - 64 * i : 64;
+    // ---- the chunk's decays (warp 1); the state: what the chunk before added, and its bf16 copy
+    if (warp == 1) {
+      cp_async_wait_all();
+      __syncwarp();
+      tc_decays(raw + (i & 1) * 64, len, prm.scale, lane, gam, down, up);
+      if (i + 1 < nchunks) fetch_g(i + 1);
+    }
+    if (tid == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
+      const int t = (int)(p.tok0 + 64 * (i + 1));
+#pragma unroll
+      for (int a = 0; a < KD / 64; ++a) {
+        tma_prefetch_3d(&tm_k, 64 * a, hq, t);
+        if (FULL) tma_prefetch_3d(&tm_q, 64 * a, hq, t);
+      }
+#pragma unroll
+      for (int a = 0; a < VD / 64; ++a) tma_prefetch_3d(&tm_v, e0 + 64 * a, h, t);
+    }
+    if (i > 0) {
+      wait(bar_u, i - 1);
+      tc_fence_after();
+      if (tid == 0 && !bad) {
+        issue_kq(i);        // K and Q of the chunk before have been read
+        if (!FULL) issue_v(i);
+      }
+#pragma unroll
+      for (int b = 0; b < KH; b += 32) {
+        float u[32];
+        tmem_ld32(R_U + lane_off + hf * KH + b, u);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[b + j] = fmaf(dec, S[b + j], u[j]);
+      }
+    }
+    if (FULL && row < VD) {
+#pragma unroll
+      for (int b = 0; b < KH; b += 8) {
+        const int d = hf * KH + b;
+        *reinterpret_cast<uint4*>(sm + M::X + (d >> 6) * (VD * 128) + sw128_chunk(row, (d & 63) >> 3)) =
+            make_uint4(pack_bf16(S[b], S[b + 1]), pack_bf16(S[b + 2], S[b + 3]), pack_bf16(S[b + 4], S[b + 5]),
+                       pack_bf16(S[b + 6], S[b + 7]));
+      }
+    }
+    if (len < 64) {
+      wait(bar_kq, i);
+      wait(bar_v, i);
+      zero_rows(sm + M::KQ, KD / 64, 16384, len, tid);
+      zero_rows(sm + M::V, VD / 64, 8192, len, tid);
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    if (__syncthreads_or(bad)) break;
+    tc_fence_after();
+
+    if (FULL) {
+      if (tid == 0) {
+        wait(bar_kq, i);
+        bulk_wait_read();   // the o staging has been read
+        if (!bad) {
+          tc_fence_after();
+          const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
+#pragma unroll
+          for (int s = 0; s < KD / 16; ++s) {
+            const uint32_t a = M::KQ + (s >> 2) * 16384 + (s & 3) * 32;
+            mma_bf16(R_a, dsw(s4, a, 16), dsw(s4, a, 16), id, s > 0);
+          }
+          commit(2, i);
+#pragma unroll
+          for (int s = 0; s < KD / 16; ++s) {
+            const uint32_t a = M::X + (s >> 2) * (VD * 128) + (s & 3) * 32;
+            const uint32_t b = M::KQ + 8192 + (s >> 2) * 16384 + (s & 3) * 32;
+            mma_bf16(R_b, dsw(s4, a, 16), dsw(s4, b, 16), id, s > 0);
+          }
+          commit(3, i);
+        }
+      }
+      __syncwarp();
+      if (qd >= 2) {
+        // P row i2, columns 32 hf ..
+        wait(bar_qk, i);
+        tc_fence_after();
+        float v[32];
+        const int i2 = row - 64;
+        if (qd == 2 && hf == 1) {   // above the diagonal
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        } else {
+          tmem_ld32(R_a + lane_off + 32 * hf, v);
+          const float gi = gam[i2];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = 32 * hf + j <= i2 ? prm.scale * ex2_fast(gi - gam[32 * hf + j]) * v[j] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) solve64::store8_bf16(sm + M::P + sw128_chunk(i2, 4 * hf + q), v + 8 * q);
+        wait(bar_qs, i);
+      } else {
+        wait(bar_v, i);
+        wait(bar_qs, i);   // the state's copy has been read: its place takes V''
+        weigh_values<VD>(sm, M::V, M::X, down, 64 * hf + row, 128);
+      }
+    } else {
+      wait(bar_v, i);
+      weigh_values<VD>(sm, M::V, M::X, down, tid, kTcThreads);
+    }
+    dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may be written
+    total *= dec;
+    if (!FULL && tid == 0) wait(bar_kq, i);
+    fence_proxy_async();
+    tc_fence_before();
+    if (__syncthreads_or(bad)) break;
+    tc_fence_after();
+    if (tid == 0) {
+      if (FULL) {
+        const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(R_a, dsw(s4, M::V + s * 2048, 8192), dsw(s4, M::P + s * 32, 16), id, s > 0);
+        commit(4, i);
+      }
+      const uint32_t id = idesc_bf16(128, KD, 1, 1, 0);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        mma_bf16(R_U, dsw(s4, M::X + (s >> 2) * (VD / 64 * 8192) + (s & 3) * 2048, 8192),
+                 dsw(s4, M::KQ + (s & 3) * 2048, 16384), id, s > 0);
+      commit(5, i);
+    }
+    __syncwarp();
+    if (FULL) {
+      // o_i = up_i OQ_i + OP_i: this thread has column e0 + row of o for 32 rows; neighbouring lanes exchange values
+      // so that each writes bf16 pairs
+      const int ecol = (row & 63) & ~1;
+      const bool odd = lane & 1;
+      uint8_t* lbase = sm + M::OS + (row >> 6) * 8192 + (odd ? 128 : 0) + (ecol & 7) * 2;
+      const uint32_t xsw = (static_cast<uint32_t>((ecol >> 3) ^ (odd ? 1 : 0))) << 4;
+      float oq[32];
+      tmem_ld32(R_b + lane_off + 32 * hf, oq);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) oq[j] *= up[32 * hf + j];
+      wait(bar_pv, i);
+      tc_fence_after();
+      if (tid == 0 && i + 1 < nchunks && !bad) issue_v(i + 1);
+      if (row < VD) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float b[16];
+          const uint32_t col = 32 * hf + 16 * q;
+          tmem_ld16(R_a + lane_off + col, b);
+          uint8_t* qb = lbase + col * 128;
+#pragma unroll
+          for (int pp = 0; pp < 8; ++pp) {
+            const float v0 = oq[16 * q + 2 * pp] + b[2 * pp], v1 = oq[16 * q + 2 * pp + 1] + b[2 * pp + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            const uint32_t word = odd ? pack_bf16(other, v1) : pack_bf16(v0, other);
+            const uint32_t off = (2 * pp) * 128 + (xsw ^ (static_cast<uint32_t>((2 * pp) & 7) << 4));
+            *reinterpret_cast<uint32_t*>(qb + off) = word;
+          }
+        }
+      }
+      fence_proxy_async();
+      tc_fence_before();
+      __syncthreads();
+      const int64_t t0 = p.tok0 + 64 * (int64_t)i;
+      if (len == 64) {
+        if (tid == 0) {
+#pragma unroll
+          for (int a = 0; a < VD / 64; ++a) tma_store_3d(&tm_o, sm + M::OS + a * 8192, e0 + 64 * a, h, (int)t0);
+          bulk_commit();
+        }
+      } else {
+        for (int u = tid; u < len * (VD / 8); u += kTcThreads) {
+          const int r = u / (VD / 8), q = u % (VD / 8);
+          const uint4 val = *reinterpret_cast<const uint4*>(sm + M::OS + (q >> 3) * 8192 + sw128_chunk(r, q & 7));
+          *reinterpret_cast<uint4*>(prm.o + ((t0 + r) * prm.Hv + h) * (int64_t)prm.V + e0 + q * 8) = val;
+        }
+      }
+    }
+  }
+
+  // what the last chunk added; after an abort (every thread left the loop at the same barrier) nothing is written
+  if (!__syncthreads_or(bad)) {
+    wait(bar_u, nchunks - 1);
+    tc_fence_after();
+#pragma unroll
+    for (int b = 0; b < KH; b += 32) {
+      float u[32];
+      tmem_ld32(R_U + lane_off + hf * KH + b, u);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) S[b + j] = fmaf(dec, S[b + j], u[j]);
+    }
+    float* to = nullptr;
+    const int64_t kv = (int64_t)KD * prm.V;
+    if (!FULL) {
+      to = prm.own + (int64_t)ch * kv;
+      if (tid == 0 && slice == 0) prm.total[ch] = total;
+    } else if (is_last && prm.ht) {
+      int64_t at = p.seq;
+      if (prm.idx) {
+        at = prm.idx[p.seq];
+        if (at < 0 || at >= prm.slots) at = -1;
+      }
+      if (at >= 0) to = prm.ht + (at * prm.Hv + h) * kv;
+    }
+    if (to && row < VD && !bad) {
+      to += (int64_t)hf * KH * prm.V + e0 + row;
+#pragma unroll
+      for (int i = 0; i < KH; ++i) to[(int64_t)i * prm.V] = S[i];
+    }
+  }
+  if (tid == 0) bulk_wait_read();
+  if (warp == 1) cp_async_wait_all();
+  if (__syncthreads_or(bad) && tid == 0) {
+    // abort: loads and products in flight finish (bounded) before their memory is released
+    for (int b = 0; b < 6; ++b)
+      if (count[b] > 0) mbar_wait(bars + b, (count[b] - 1) & 1, prm.status, 100000000ull);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, M::Cols);
+}
+
+// Final states of sequences without tokens: the initial ones.
+__global__ void __launch_bounds__(256) empty_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ nc,
+                                                    int Hv, int64_t kv, const float* __restrict__ h0,
+                                                    float* __restrict__ ht, const int32_t* __restrict__ idx,
+                                                    int slots) {
+  const int n = blockIdx.x;
+  if (*nc < 0 || cu[n] != cu[n + 1]) return;
+  int64_t to = n;
+  if (idx) {
+    to = idx[n];
+    if (to < 0 || to >= slots) return;
+  }
+  const int64_t size = Hv * kv;
+  for (int64_t i = 4 * (int64_t)threadIdx.x; i < size; i += 1024)
+    *reinterpret_cast<float4*>(ht + to * size + i) =
+        h0 ? load4(h0 + n * size + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+int slice_width(const gdn_linear_problem& p) { return p.V >= 128 ? 128 : 64; }
+
+// Tokens a segment: whole sequences when their chains fill the device, else about a twelfth of an even share (whole
+// chunks), at least four chunks.
+int segment_tokens(const gdn_linear_problem& p) {
+  const int64_t slots = (p.K == 256 ? 1 : 2) * (int64_t)sm_count();
+  const int64_t heads = (int64_t)p.Hv * (p.V / slice_width(p));
+  const int64_t chunks = p.varlen ? p.T / 64 + p.N : p.B * ceil_div(p.T, 64);
+  const int64_t whole = ceil_div(p.T > 0 ? p.T : 1, 64);
+  int64_t m = whole;
+  if (p.varlen || p.N * heads < 2 * slots) m = ceil_div(chunks * heads, 4 * slots);
+  if (m < 4) m = 4;
+  if (m > whole) m = whole;
+  return (int)(64 * m);
+}
+
+template <int KD, int VD>
+gdn_status launch_tc(const gdn_linear_problem& p, bool full, unsigned grid, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, const CUtensorMap& to, const TcParams& prm, cudaStream_t s) {
+  auto kern = full ? lin_tc_kernel<KD, VD, true> : lin_tc_kernel<KD, VD, false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Map<KD, VD>::Bytes) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<grid, kTcThreads, Map<KD, VD>::Bytes, s>>>(tq, tk, tv, to, prm);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status launch_tc(const gdn_linear_problem& p, bool full, unsigned grid, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, const CUtensorMap& to, const TcParams& prm, cudaStream_t s) {
+  if (p.V == 64) {
+    if (p.K == 64) return launch_tc<64, 64>(p, full, grid, tq, tk, tv, to, prm, s);
+    if (p.K == 128) return launch_tc<128, 64>(p, full, grid, tq, tk, tv, to, prm, s);
+    return launch_tc<256, 64>(p, full, grid, tq, tk, tv, to, prm, s);
+  }
+  if (p.K == 64) return launch_tc<64, 128>(p, full, grid, tq, tk, tv, to, prm, s);
+  if (p.K == 128) return launch_tc<128, 128>(p, full, grid, tq, tk, tv, to, prm, s);
+  return launch_tc<256, 128>(p, full, grid, tq, tk, tv, to, prm, s);
+}
+
+}  // namespace
+
+bool tc_supported(const gdn_linear_problem& p) { return p.dt == GDN_BF16; }
+
+// [status][tables][decays: segments x Hv][states: segments x Hv x K x V]
+size_t tc_fwd_bytes(const gdn_linear_problem& p) {
+  const int seg = segment_tokens(p);
+  const size_t cells = seg < p.T ? (size_t)pieces_max(p, seg) * p.Hv : 0;
+  return kAlign + pieces_bytes(p, seg) + align_up(4 * cells) + 4 * cells * p.K * p.V;
+}
+
+gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                  float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx, int slots,
+                  void* ws, cudaStream_t s) {
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  int32_t* status = reinterpret_cast<int32_t*>(at);
+  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
+  const int seg = segment_tokens(p), most = pieces_max(p, seg);
+  void* tables = at + kAlign;
+  if (launch_pieces(p, seg, cu, tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
+  TcParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.pc = pieces_at(p, seg, tables);
+  if (p.varlen && ht) {
+    empty_kernel<<<p.N, 256, 0, s>>>(cu, prm.pc.nc, p.Hv, (int64_t)p.K * p.V, h0, ht, idx, slots);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  }
+  const int64_t tokens = (int64_t)p.B * p.T;
+  if (tokens == 0) return GDN_OK;
+  CUtensorMap tq, tk, tv, to;
+  const uint32_t box[3] = {64, 1, 64};
+  const uint64_t kd[3] = {(uint64_t)p.K, (uint64_t)p.Hqk, (uint64_t)tokens};
+  const uint64_t vd[3] = {(uint64_t)p.V, (uint64_t)p.Hv, (uint64_t)tokens};
+  const uint64_t sq[2] = {(uint64_t)p.K * 2, (uint64_t)p.ld_q * 2}, sk[2] = {(uint64_t)p.K * 2, (uint64_t)p.ld_k * 2};
+  const uint64_t sv[2] = {(uint64_t)p.V * 2, (uint64_t)p.ld_v * 2};
+  const uint64_t so[2] = {(uint64_t)p.V * 2, (uint64_t)p.Hv * p.V * 2};
+  if (!make_tmap_bf16(&tq, q, 3, kd, sq, box) || !make_tmap_bf16(&tk, k, 3, kd, sk, box) ||
+      !make_tmap_bf16(&tv, v, 3, vd, sv, box) || !make_tmap_bf16(&to, o, 3, vd, so, box))
+    return GDN_ERR_CUDA;
+  prm.g = g;
+  prm.h0 = h0;
+  prm.ht = ht;
+  prm.idx = idx;
+  prm.slots = slots;
+  prm.o = static_cast<__nv_bfloat16*>(o);
+  prm.status = status;
+  prm.cu = cu;
+  prm.Hqk = p.Hqk;
+  prm.Hv = p.Hv;
+  prm.V = p.V;
+  prm.g_per_head = p.g_per_head;
+  prm.varlen = p.varlen;
+  prm.T = p.T;
+  prm.scale = scale;
+  const unsigned grid = (unsigned)((int64_t)most * p.Hv * (p.V / slice_width(p)));
+  if (seg < p.T) {
+    prm.total = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, seg));
+    prm.own = prm.total + align_up(4 * (size_t)most * p.Hv) / 4;
+    gdn_status st = launch_tc(p, false, grid, tq, tk, tv, to, prm, s);
+    if (st == GDN_OK) st = launch_sums<false>(shape_of(p), prm.pc, p.N, prm.total, h0, prm.own, nullptr, nullptr, 0, s);
+    if (st != GDN_OK) return st;
+    prm.start = prm.own;
+  }
+  return launch_tc(p, true, grid, tq, tk, tv, to, prm, s);
+}
+
+}  // namespace lin
+}  // namespace gdn

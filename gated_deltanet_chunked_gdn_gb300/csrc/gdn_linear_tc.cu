@@ -35,7 +35,7 @@ using solve64::dsw;
 constexpr int kTcThreads = 256;
 
 struct TcParams {
-  const float* g;
+  const float* decays;   // [slots of chunks][Hv][3][64], decays_kernel
   const float* h0;       // [N][Hv][K][V]
   const float* start;    // [segments][Hv][K][V] states before the segments, or null (one segment a sequence)
   float* ht;             // final states (or a pool), or null
@@ -46,7 +46,7 @@ struct TcParams {
   int32_t* status;
   Pieces pc;
   const int32_t* cu;
-  int slots, Hqk, Hv, V, g_per_head, varlen, T;
+  int slots, Hqk, Hv, V, varlen, T;
   float scale;
 };
 
@@ -62,9 +62,9 @@ struct Map {
   static constexpr uint32_t Tail = OS + VD / 64 * 8192;
   // rows 64..127 of a 64-row A tile are read (and ignored): they stay inside
   static constexpr uint32_t Misc = Tail < X + 32768 ? X + 32768 : Tail;
-  static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512, Raw = Misc + 768;   // Raw: float[2][64]
-  static constexpr uint32_t Bar = Misc + 1280, Flags = Misc + 1344;
-  static constexpr uint32_t Used = Misc + 1408;
+  static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512;   // a chunk's decays, as they lie in memory
+  static constexpr uint32_t Bar = Misc + 768, Flags = Misc + 832;
+  static constexpr uint32_t Used = Misc + 896;
   static constexpr uint32_t Bytes = Used + 1024;
   static constexpr int Cols = KD + 128 <= 256 ? 256 : 512;        // TMEM: U^T, Q K^T / OP^T, OQ^T
   static constexpr int Ctas = KD == 256 ? 1 : 2;
@@ -76,26 +76,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
 
-// Decays of a chunk, by one warp: gam_i = log2(e) b_i, down_j = e^{b_last - b_j} (0 past the end), up_i = scale e^{b_i};
-// sums in 64 bits, so that down keeps fp32 accuracy behind a strong decay.
-__device__ __forceinline__ void tc_decays(const float* raw, int len, float scale, int lane, float* gam, float* down,
-                                          float* up) {
-  const int r = 2 * lane;
-  // e^-150 is 0 in fp32: stronger decays are cut there, and -infinity never meets itself in a difference
-  const float ga = raw[r] < -150.f ? -150.f : raw[r], gb = raw[r + 1] < -150.f ? -150.f : raw[r + 1];
-  const double a = r < len ? (double)ga : 0.0, b = r + 1 < len ? (double)gb : 0.0;
-  double s = a + b;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double t = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += t;
-  }
-  const double last = __shfl_sync(0xffffffffu, s, 31), s0 = s - b;
-  constexpr double kL = 1.4426950408889634;
-  gam[r] = (float)(s0 * kL), gam[r + 1] = (float)(s * kL);
-  down[r] = r < len ? expf((float)(last - s0)) : 0.f;
-  down[r + 1] = r + 1 < len ? expf((float)(last - s)) : 0.f;
-  up[r] = scale * expf((float)s0), up[r + 1] = scale * expf((float)s);
+// 16-byte aligned block of a multiple of 16 bytes, global -> shared.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // V'' = diag(down) V: `n` threads (thread t of them), 8 columns of a row at a time; zeros where down is 0.
@@ -126,6 +112,39 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int columns, uint32_t s
   }
 }
 
+// Slot of a piece's first chunk among all chunks' decays: one more for every sequence before, whose last chunk may be
+// short, so that no two chunks share one.
+__device__ __forceinline__ int64_t chunk_slot(const Piece& p) { return p.tok0 / 64 + p.seq; }
+
+// Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end) and scale e^{b_i}, the sums in 64 bits
+// (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay).  A warp takes a chunk and head at a time.  Done by the kernels below, one warp would take 2000 cycles of a chunk's 5000 while the others wait.
+__global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
+                                                     float scale, float* __restrict__ out) {
+  const Piece p = piece_of(pc, blockIdx.x);
+  if (!p.ok) return;
+  const int lane = threadIdx.x & 31, r = 2 * lane, chunks = (p.len + 63) / 64;
+  for (int64_t w = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); w < (int64_t)chunks * Hv; w += 8 * gridDim.y) {
+    const int i = (int)(w / Hv), h = (int)(w % Hv), len = p.len - 64 * i;
+    const float* gp = g + (g_per_head ? h : (p.tok0 + 64 * i + r) * Hv + h);
+    const float ga = r < len ? gp[0] : 0.f, gb = r + 1 < len ? gp[g_per_head ? 0 : Hv] : 0.f;
+    // e^-150 is 0 in fp32: stronger decays are cut there, and -infinity never meets itself in a difference
+    const double a = ga < -150.f ? -150.0 : (double)ga, b = gb < -150.f ? -150.0 : (double)gb;
+    double s = a + b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += t;
+    }
+    const double last = __shfl_sync(0xffffffffu, s, 31), s0 = s - b;
+    constexpr double kL = 1.4426950408889634;
+    float* to = out + ((chunk_slot(p) + i) * Hv + h) * 192 + r;
+    *reinterpret_cast<float2*>(to) = make_float2((float)(s0 * kL), (float)(s * kL));
+    *reinterpret_cast<float2*>(to + 64) =
+        make_float2(r < len ? expf((float)(last - s0)) : 0.f, r + 1 < len ? expf((float)(last - s)) : 0.f);
+    *reinterpret_cast<float2*>(to + 128) = make_float2(scale * expf((float)s0), scale * expf((float)s));
+  }
+}
+
 // FULL: outputs and final states.  Otherwise the segments' own contributions and decays.
 template <int KD, int VD, bool FULL>
 __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
@@ -137,10 +156,9 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
-  float* gam = reinterpret_cast<float*>(sm + M::Gam);
-  float* down = reinterpret_cast<float*>(sm + M::Down);
-  float* up = reinterpret_cast<float*>(sm + M::Up);
-  float* raw = reinterpret_cast<float*>(sm + M::Raw);
+  const float* gam = reinterpret_cast<const float*>(sm + M::Gam);
+  const float* down = reinterpret_cast<const float*>(sm + M::Down);
+  const float* up = reinterpret_cast<const float*>(sm + M::Up);
   // every barrier completes one phase a chunk, and every thread that waits for it does so once a chunk, in order
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::Bar);
   uint64_t *bar_kq = bars, *bar_v = bars + 1, *bar_qk = bars + 2, *bar_qs = bars + 3, *bar_pv = bars + 4,
@@ -188,7 +206,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   auto issue_kq = [&](int i) {
     const int t = (int)(p.tok0 + 64 * i);
     count[0] = i + 1;
-    mbar_arrive_expect_tx(bar_kq, (FULL ? 2 : 1) * KD / 64 * 8192);
+    mbar_arrive_expect_tx(bar_kq, (FULL ? 2 : 1) * KD / 64 * 8192 + 768);
+    bulk_load(sm + M::Gam, prm.decays + ((chunk_slot(p) + i) * prm.Hv + h) * 192, 768, bar_kq);
 #pragma unroll
     for (int a = 0; a < KD / 64; ++a) {
       tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_kq, 64 * a, hq, t);
@@ -209,21 +228,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     mma_commit(bars + b);
     count[b] = i + 1;
   };
-  // warp 1 copies chunk i's log decays one chunk ahead (lane l: rows 2 l, 2 l + 1)
-  auto fetch_g = [&](int i) {
-    float* dst = raw + (i & 1) * 64;
-#pragma unroll
-    for (int r = 2 * lane; r < 2 * lane + 2; ++r) {
-      const int64_t t = 64 * (int64_t)i + r;
-      if (t < p.len) cp_async4(dst + r, prm.g + (prm.g_per_head ? h : (p.tok0 + t) * prm.Hv + h));
-    }
-    cp_async_commit();
-  };
   if (tid == 0) {
     issue_kq(0);
     issue_v(0);
   }
-  if (warp == 1) fetch_g(0);
 
   // S^T[e = row][d = hf KH + i]
   float S[KH];
@@ -248,13 +256,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
 #pragma unroll 1
   for (int i = 0; i < nchunks; ++i) {
     const int len = p.len - 64 * i < 64 ? p.len - 64 * i : 64;
-    // ---- the chunk's decays (warp 1); the state: what the chunk before added, and its bf16 copy
-    if (warp == 1) {
-      cp_async_wait_all();
-      __syncwarp();
-      tc_decays(raw + (i & 1) * 64, len, prm.scale, lane, gam, down, up);
-      if (i + 1 < nchunks) fetch_g(i + 1);
-    }
+    // ---- the state: what the chunk before added, and its bf16 copy
     if (tid == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
       const int t = (int)(p.tok0 + 64 * (i + 1));
 #pragma unroll
@@ -301,8 +303,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     tc_fence_after();
 
     if (FULL) {
+      wait(bar_kq, i);   // every thread reads the decays
       if (tid == 0) {
-        wait(bar_kq, i);
         bulk_wait_read();   // the o staging has been read
         if (!bad) {
           tc_fence_after();
@@ -336,8 +338,17 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
           tmem_ld32(R_a + lane_off + 32 * hf, v);
           const float gi = gam[i2];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = 32 * hf + j <= i2 ? prm.scale * ex2_fast(gi - gam[32 * hf + j]) * v[j] : 0.f;
+          for (int j4 = 0; j4 < 8; ++j4) {
+            const float4 g4 = *reinterpret_cast<const float4*>(gam + 32 * hf + 4 * j4);
+            const float gj[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int j = 4 * j4 + u;
+              // above the diagonal cleared by its bits: a branch an element would cost ten times the products
+              const uint32_t keep = 32 * hf + j <= i2 ? 0xffffffffu : 0u;
+              v[j] = __uint_as_float(__float_as_uint(prm.scale * ex2_fast(gi - gj[u]) * v[j]) & keep);
+            }
+          }
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) solve64::store8_bf16(sm + M::P + sw128_chunk(i2, 4 * hf + q), v + 8 * q);
@@ -348,12 +359,12 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         weigh_values<VD>(sm, M::V, M::X, down, 64 * hf + row, 128);
       }
     } else {
+      wait(bar_kq, i);
       wait(bar_v, i);
       weigh_values<VD>(sm, M::V, M::X, down, tid, kTcThreads);
     }
-    dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may be written
+    dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may come in
     total *= dec;
-    if (!FULL && tid == 0) wait(bar_kq, i);
     fence_proxy_async();
     tc_fence_before();
     if (__syncthreads_or(bad)) break;
@@ -456,7 +467,6 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     }
   }
   if (tid == 0) bulk_wait_read();
-  if (warp == 1) cp_async_wait_all();
   if (__syncthreads_or(bad) && tid == 0) {
     // abort: loads and products in flight finish (bounded) before their memory is released
     for (int b = 0; b < 6; ++b)
@@ -527,11 +537,16 @@ gdn_status launch_tc(const gdn_linear_problem& p, bool full, unsigned grid, cons
 
 bool tc_supported(const gdn_linear_problem& p) { return p.dt == GDN_BF16; }
 
-// [status][tables][decays: segments x Hv][states: segments x Hv x K x V]
+// [slots of chunks][Hv][3][64] fp32
+size_t decays_bytes(const gdn_linear_problem& p) {
+  return 768 * (size_t)((int64_t)p.B * p.T / 64 + p.N + 1) * p.Hv;
+}
+
+// [status][tables][decays][the segments' own: segments x Hv][states: segments x Hv x K x V]
 size_t tc_fwd_bytes(const gdn_linear_problem& p) {
   const int seg = segment_tokens(p);
   const size_t cells = seg < p.T ? (size_t)pieces_max(p, seg) * p.Hv : 0;
-  return kAlign + pieces_bytes(p, seg) + align_up(4 * cells) + 4 * cells * p.K * p.V;
+  return kAlign + pieces_bytes(p, seg) + decays_bytes(p) + align_up(4 * cells) + 4 * cells * p.K * p.V;
 }
 
 gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
@@ -562,7 +577,12 @@ gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, con
   if (!make_tmap_bf16(&tq, q, 3, kd, sq, box) || !make_tmap_bf16(&tk, k, 3, kd, sk, box) ||
       !make_tmap_bf16(&tv, v, 3, vd, sv, box) || !make_tmap_bf16(&to, o, 3, vd, so, box))
     return GDN_ERR_CUDA;
-  prm.g = g;
+  float* decays = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, seg));
+  const int64_t share = ceil_div((int64_t)(seg / 64) * p.Hv, 8);   // CTAs a piece
+  decays_kernel<<<dim3(most, (unsigned)(share < 64 ? share : 64)), 256, 0, s>>>(g, p.g_per_head, p.Hv, prm.pc, scale,
+                                                                               decays);
+  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  prm.decays = decays;
   prm.h0 = h0;
   prm.ht = ht;
   prm.idx = idx;
@@ -573,13 +593,12 @@ gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, con
   prm.Hqk = p.Hqk;
   prm.Hv = p.Hv;
   prm.V = p.V;
-  prm.g_per_head = p.g_per_head;
   prm.varlen = p.varlen;
   prm.T = p.T;
   prm.scale = scale;
   const unsigned grid = (unsigned)((int64_t)most * p.Hv * (p.V / slice_width(p)));
   if (seg < p.T) {
-    prm.total = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, seg));
+    prm.total = decays + decays_bytes(p) / 4;
     prm.own = prm.total + align_up(4 * (size_t)most * p.Hv) / 4;
     gdn_status st = launch_tc(p, false, grid, tq, tk, tv, to, prm, s);
     if (st == GDN_OK) st = launch_sums<false>(shape_of(p), prm.pc, p.N, prm.total, h0, prm.own, nullptr, nullptr, 0, s);

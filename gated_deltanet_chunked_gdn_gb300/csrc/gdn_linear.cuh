@@ -81,6 +81,13 @@ Pieces pieces_at(const gdn_linear_problem& p, int size, void* tables);
 cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* cu, void* tables, int32_t* status,
                           cudaStream_t s);
 
+// The tensor-core backward pass (gdn_linear_tc_bwd.cu).
+bool tc_bwd_supported(const gdn_linear_problem& p);
+size_t tc_bwd_bytes(const gdn_linear_problem& p);
+gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g, float scale,
+                  const float* h0, const int32_t* cu, const void* dout, const float* dht, void* dq, void* dk, void* dv,
+                  float* dg, float* dh0, void* ws, cudaStream_t s);
+
 // The tensor-core forward pass (gdn_linear_tc.cu).
 bool tc_supported(const gdn_linear_problem& p);
 size_t tc_fwd_bytes(const gdn_linear_problem& p);

@@ -232,24 +232,6 @@ __global__ void __launch_bounds__(kThreads) grads_kernel(
   }
 }
 
-// dst[row][hq][:] = sum over the R value heads of a q/k head, in their order (row: a token)
-template <typename T>
-__global__ void __launch_bounds__(256) heads_kernel(const float* __restrict__ src, int64_t quads, int R, int K4,
-                                                    const int32_t* __restrict__ nc, T* __restrict__ dst) {
-  if (nc && *nc < 0) return;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= quads) return;
-  const int64_t head = at / K4;
-  const float* p = src + ((head * R) * K4 + (at - head * K4)) * 4;
-  float4 s = load4(p);
-  for (int r = 1; r < R; ++r) {
-    const float4 x = load4(p + (int64_t)r * K4 * 4);
-    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-  }
-  const float v[4] = {s.x, s.y, s.z, s.w};
-  store4(dst + at * 4, v);
-}
-
 // dg of fixed decays: the chunks' sums of one head, in a fixed order
 __global__ void __launch_bounds__(256) head_decays_kernel(const float* __restrict__ part, int Hv, int most,
                                                           const int32_t* __restrict__ nc, float* __restrict__ dg) {
@@ -320,17 +302,20 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
     if (st != GDN_OK) return st;
   }
   if (shared && most > 0) {
-    const int64_t quads = (int64_t)p.B * p.T * p.Hqk * (p.K / 4);
-    const unsigned grid = (unsigned)ceil_div(quads, 256);
-    for (int i = 0; i < 2; ++i)
-      heads_kernel<T><<<grid, 256, 0, s>>>(reinterpret_cast<const float*>(ws + (i ? L.dk : L.dq)), quads, p.Hv / p.Hqk,
-                                           p.K / 4, pc.nc, i ? dk : dq);
+    st = launch_heads<T>(p, reinterpret_cast<const float*>(ws + L.dq), pc.nc, dq, s);
+    if (st == GDN_OK) st = launch_heads<T>(p, reinterpret_cast<const float*>(ws + L.dk), pc.nc, dk, s);
+    if (st != GDN_OK) return st;
   }
-  if (p.g_per_head) head_decays_kernel<<<p.Hv, 256, 0, s>>>(part, p.Hv, most, pc.nc, dg);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return p.g_per_head ? launch_head_decays(p, part, pc.nc, dg, s) : GDN_OK;
 }
 
 }  // namespace
+
+gdn_status launch_head_decays(const gdn_linear_problem& p, const float* part, const int32_t* nc, float* dg,
+                              cudaStream_t s) {
+  head_decays_kernel<<<p.Hv, 256, 0, s>>>(part, p.Hv, pieces_max(p, kC), nc, dg);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
 
 size_t simt_bwd_bytes(const gdn_linear_problem& p) { return layout_of(p).end; }
 
@@ -353,12 +338,14 @@ gdn_status simt_bwd(const gdn_linear_problem& p, const void* q, const void* k, c
 
 }  // namespace lin
 
-size_t linear_bwd_workspace_bytes(const gdn_linear_problem& p) { return lin::simt_bwd_bytes(p); }
+size_t linear_bwd_workspace_bytes(const gdn_linear_problem& p) {
+  return lin::tc_bwd_supported(p) ? lin::tc_bwd_bytes(p) : lin::simt_bwd_bytes(p);
+}
 
 gdn_status run_linear_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                           float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht,
                           void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s) {
-  return lin::simt_bwd(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, s);
+  return (lin::tc_bwd_supported(p) ? lin::tc_bwd : lin::simt_bwd)(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, s);
 }
 
 }  // namespace gdn

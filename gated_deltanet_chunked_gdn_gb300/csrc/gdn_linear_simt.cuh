@@ -190,5 +190,35 @@ gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* tot
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// dst[row][hq][:] = sum over the R value heads of a q/k head, in their order (row: a token)
+template <typename T>
+__global__ void __launch_bounds__(256) heads_kernel(const float* __restrict__ src, int64_t quads, int R, int K4,
+                                                    const int32_t* __restrict__ nc, T* __restrict__ dst) {
+  if (nc && *nc < 0) return;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= quads) return;
+  const int64_t head = at / K4;
+  const float* p = src + ((head * R) * K4 + (at - head * K4)) * 4;
+  float4 s = load4(p);
+  for (int r = 1; r < R; ++r) {
+    const float4 x = load4(p + (int64_t)r * K4 * 4);
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  store4(dst + at * 4, v);
+}
+
+// src: fp32 [B, T, Hv, K]; dst [B, T, Hqk, K].
+template <typename T>
+gdn_status launch_heads(const gdn_linear_problem& p, const float* src, const int32_t* nc, T* dst, cudaStream_t s) {
+  const int64_t quads = (int64_t)p.B * p.T * p.Hqk * (p.K / 4);
+  heads_kernel<T><<<(unsigned)ceil_div(quads, 256), 256, 0, s>>>(src, quads, p.Hv / p.Hqk, p.K / 4, nc, dst);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// dg of fixed decays from the chunks' sums [chunks][Hv] (gdn_linear_bwd.cu).
+gdn_status launch_head_decays(const gdn_linear_problem& p, const float* part, const int32_t* nc, float* dg,
+                              cudaStream_t s);
+
 }  // namespace lin
 }  // namespace gdn

@@ -6,12 +6,12 @@
 //   [K;Q] K^T                -> lanes 64..127: Q K^T                              (M128 N64)
 //   OQ^T = S^T Q^T           S^T: bf16 copy of the state before the chunk         (M128 N64)
 //   OP^T = V^T P^T           P = lower(scale e^{b_i - b_j} Q K^T), bf16           (M128 N64)
-//   U^T  = V''^T K           V'' = diag(e^{b_last - b_j}) V in two bf16 terms     (M128 N K)
+//   U^T  = V''^T K           V'' = diag(e^{b_last - b_j}) V in three bf16 terms   (M128 N K)
 //   o_i  = scale e^{b_i} OQ_i + OP_i,   S^T <- e^{b_last} S^T + U^T
 //
 // The state itself stays in fp32 registers (a thread holds K / 2 columns of one row of S^T), and what a chunk adds to
-// it comes out of the tensor cores complete: V'' keeps 16 bits of the weighted values (2^-17 of each), so the final
-// state has fp32 accuracy although its inputs are bf16, and no sum longer than a chunk is left to the tensor cores'
+// it comes out of the tensor cores complete: V'' keeps all 24 bits of the weighted values (with two terms the final
+// state was off by 2.4e-6, with three by 1e-7), and no sum longer than a chunk is left to the tensor cores'
 // accumulation.  o reads a bf16 copy of the state and bf16 weights: one rounding of each term, like o's own.
 // Two CTAs share an SM: one's loads and SIMT phases run under the other's products.
 //
@@ -20,35 +20,13 @@
 //
 // Rows past a sequence's end are zeroed in the K and V tiles (they may hold another sequence's values, NaN among them)
 // and their weights are selected to zero; their outputs are not stored.
-#include <string.h>
-
-#include "gdn_linear_simt.cuh"
-#include "gdn_solve64.cuh"
+#include "gdn_linear_tc.cuh"
 
 namespace gdn {
 namespace lin {
 namespace {
 
-using namespace sm100;
-using solve64::dsw;
-
 constexpr int kTcThreads = 256;
-
-struct TcParams {
-  const float* decays;   // [slots of chunks][Hv][3][64], decays_kernel
-  const float* h0;       // [N][Hv][K][V]
-  const float* start;    // [segments][Hv][K][V] states before the segments, or null (one segment a sequence)
-  float* ht;             // final states (or a pool), or null
-  const int32_t* idx;
-  float* own;            // STATES: the segments' own contributions
-  float* total;          // STATES: their decays
-  __nv_bfloat16* o;
-  int32_t* status;
-  Pieces pc;
-  const int32_t* cu;
-  int slots, Hqk, Hv, V, varlen, T;
-  float scale;
-};
 
 // Shared memory, byte offsets from a 1024-byte aligned base.
 template <int KD, int VD>
@@ -56,12 +34,13 @@ struct Map {
   static constexpr uint32_t KQ = 0;                               // k rows 0..63, q rows 64..127; 64 columns an atom column
   static constexpr uint32_t V = KQ + KD / 64 * 16384;
   static constexpr uint32_t P = V + VD / 64 * 8192;
-  static constexpr uint32_t X = P + 8192;                         // S^T bf16 [e][d], then V'' [j][e] hi and lo
+  static constexpr uint32_t X = P + 8192;                         // S^T bf16 [e][d], then the first two terms of V'' [j][e]
   static constexpr uint32_t kS = (uint32_t)VD * KD * 2, kW = (uint32_t)VD * 64 * 2 * 2;
-  static constexpr uint32_t OS = X + (kS > kW ? kS : kW);         // o staging
+  static constexpr uint32_t OS = X + (kS > kW ? kS : kW);         // the third term of V'', then o
   static constexpr uint32_t Tail = OS + VD / 64 * 8192;
   // rows 64..127 of a 64-row A tile are read (and ignored): they stay inside
-  static constexpr uint32_t Misc = Tail < X + 32768 ? X + 32768 : Tail;
+  static constexpr uint32_t kEnd = X + 32768 > OS + 16384 ? X + 32768 : OS + 16384;
+  static constexpr uint32_t Misc = Tail < kEnd ? kEnd : Tail;
   static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512;   // a chunk's decays, as they lie in memory
   static constexpr uint32_t Bar = Misc + 768, Flags = Misc + 832;
   static constexpr uint32_t Used = Misc + 896;
@@ -70,23 +49,17 @@ struct Map {
   static constexpr int Ctas = KD == 256 ? 1 : 2;
 };
 
-// a and b as sums of two bf16 values each, packed.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(a, b);
-  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
-}
-
-// 16-byte aligned block of a multiple of 16 bytes, global -> shared.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+// A whole 32-byte sector a thread: rows of S^T lie one a lane.
+__device__ __forceinline__ void store32(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
 
 // V'' = diag(down) V: `n` threads (thread t of them), 8 columns of a row at a time; zeros where down is 0.
 template <int VD>
-__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, const float* down, int t, int n) {
+__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, uint32_t x3, const float* down, int t,
+                                             int n) {
 #pragma unroll 4
   for (int u = t; u < 64 * (VD / 8); u += n) {
     const int j = u / (VD / 8), c = u % (VD / 8);
@@ -94,30 +67,23 @@ __device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x
     const uint4 w = *reinterpret_cast<const uint4*>(sm + v + off);
     const float f = down[j];
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t hi[4], lo[4];
+    uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      split2(f * __uint_as_float(in[i] << 16), f * __uint_as_float(in[i] & 0xffff0000u), hi[i], lo[i]);
+    for (int i = 0; i < 4; ++i) {
+      float a = f * __uint_as_float(in[i] << 16), b = f * __uint_as_float(in[i] & 0xffff0000u);
+      hi[i] = pack_bf16(a, b);
+      a -= __uint_as_float(hi[i] << 16), b -= __uint_as_float(hi[i] & 0xffff0000u);
+      split2(a, b, lo[i], rest[i]);
+    }
     *reinterpret_cast<uint4*>(sm + x + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(sm + x + VD / 64 * 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(sm + x3 + off) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
   }
 }
 
-// Zeros in rows [from, 64) of a tile of 64-column atom columns `stride` bytes apart.
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int columns, uint32_t stride, int from, int tid) {
-  const int n = (64 - from) * columns * 8;
-  for (int u = tid; u < n; u += kTcThreads) {
-    const int c = u % (columns * 8), r = from + u / (columns * 8);
-    *reinterpret_cast<uint4*>(tile + (c >> 3) * stride + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-}
-
-// Slot of a piece's first chunk among all chunks' decays: one more for every sequence before, whose last chunk may be
-// short, so that no two chunks share one.
-__device__ __forceinline__ int64_t chunk_slot(const Piece& p) { return p.tok0 / 64 + p.seq; }
-
-// Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end) and scale e^{b_i}, the sums in 64 bits
-// (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay).  A warp takes a chunk and head at a time.  Done by the kernels below, one warp would take 2000 cycles of a chunk's 5000 while the others wait.
+// Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i} and what the first lacks
+// to 48 bits; the sums in 64 bits (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and differences
+// of the sums do).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A warp takes a chunk and head at a time.  Done by the kernels below, one warp would take 2000 cycles of a chunk's 5000 while the others wait.
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
                                                      float scale, float* __restrict__ out) {
   const Piece p = piece_of(pc, blockIdx.x);
@@ -137,21 +103,24 @@ __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g
     }
     const double last = __shfl_sync(0xffffffffu, s, 31), s0 = s - b;
     constexpr double kL = 1.4426950408889634;
-    float* to = out + ((chunk_slot(p) + i) * Hv + h) * 192 + r;
-    *reinterpret_cast<float2*>(to) = make_float2((float)(s0 * kL), (float)(s * kL));
+    float* to = out + ((chunk_slot(p) + i) * Hv + h) * 256 + r;
+    const float h0 = (float)(s0 * kL), h1 = (float)(s * kL);
+    *reinterpret_cast<float2*>(to) = make_float2(h0, h1);
+    *reinterpret_cast<float2*>(to + 192) = make_float2((float)(s0 * kL - h0), (float)(s * kL - h1));
     *reinterpret_cast<float2*>(to + 64) =
         make_float2(r < len ? expf((float)(last - s0)) : 0.f, r + 1 < len ? expf((float)(last - s)) : 0.f);
     *reinterpret_cast<float2*>(to + 128) = make_float2(scale * expf((float)s0), scale * expf((float)s));
   }
 }
 
-// FULL: outputs and final states.  Otherwise the segments' own contributions and decays.
-template <int KD, int VD, bool FULL>
+// The walk over a segment's chunks.  ADJ: backwards, x = q, y = do, weights scale e^{b_i}: the adjoint of the state.
+template <int KD, int VD, int MODE, bool ADJ>
 __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     lin_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const TcParams prm) {
   using M = Map<KD, VD>;
+  constexpr bool FULL = MODE == kFull;
   constexpr int KH = KD / 2;   // columns of S^T a thread holds
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -174,12 +143,12 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   const int c = ch / prm.Hv, h = ch % prm.Hv, hq = h / (prm.Hv / prm.Hqk), e0 = slice * VD;
   const Piece p = piece_of(prm.pc, c);
   if (!p.ok) return;
-  // first and last segment of its sequence
   const int64_t seq0 = prm.varlen ? prm.cu[p.seq] : (int64_t)p.seq * prm.T;
   const int64_t seq1 = prm.varlen ? prm.cu[p.seq + 1] : seq0 + prm.T;
-  const bool is_first = p.tok0 == seq0, is_last = p.tok0 + p.len == seq1;
-  if (!FULL && is_last) return;   // nobody starts behind it
+  const bool ends = ADJ ? p.tok0 == seq0 : p.tok0 + p.len == seq1;   // the walk's last segment of its sequence
+  if (MODE == kOwn && ends) return;   // nobody starts behind it
   const int nchunks = (p.len + 63) / 64;
+  auto chunk_at = [&](int i) { return ADJ ? nchunks - 1 - i : i; };
 
   if (tid == 0) {
 #pragma unroll
@@ -204,10 +173,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
 
   bool bad = false;   // one of this thread's waits ran out
   auto issue_kq = [&](int i) {
-    const int t = (int)(p.tok0 + 64 * i);
+    const int at = chunk_at(i), t = (int)(p.tok0 + 64 * at);
     count[0] = i + 1;
     mbar_arrive_expect_tx(bar_kq, (FULL ? 2 : 1) * KD / 64 * 8192 + 768);
-    bulk_load(sm + M::Gam, prm.decays + ((chunk_slot(p) + i) * prm.Hv + h) * 192, 768, bar_kq);
+    bulk_load(sm + M::Gam, prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * 256, 768, bar_kq);
 #pragma unroll
     for (int a = 0; a < KD / 64; ++a) {
       tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_kq, 64 * a, hq, t);
@@ -215,7 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     }
   };
   auto issue_v = [&](int i) {
-    const int t = (int)(p.tok0 + 64 * i);
+    const int t = (int)(p.tok0 + 64 * chunk_at(i));
     count[1] = i + 1;
     mbar_arrive_expect_tx(bar_v, VD / 64 * 8192);
 #pragma unroll
@@ -238,8 +207,9 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   {
     const int64_t kv = (int64_t)KD * prm.V;
     const float* from = nullptr;
-    if (FULL) {
-      if (!is_first && prm.start) from = prm.start + (int64_t)ch * kv;
+    if (MODE != kOwn) {
+      // cut sequences start from a copy of h0, which another segment's CTA may be overwriting with the final state
+      if (prm.start) from = prm.start + (int64_t)ch * kv;
       else if (prm.h0) from = prm.h0 + ((int64_t)p.seq * prm.Hv + h) * kv;
     }
     if (from && row < VD) {
@@ -255,10 +225,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
 
 #pragma unroll 1
   for (int i = 0; i < nchunks; ++i) {
-    const int len = p.len - 64 * i < 64 ? p.len - 64 * i : 64;
+    const int at = chunk_at(i), len = p.len - 64 * at < 64 ? p.len - 64 * at : 64;
     // ---- the state: what the chunk before added, and its bf16 copy
     if (tid == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
-      const int t = (int)(p.tok0 + 64 * (i + 1));
+      const int t = (int)(p.tok0 + 64 * chunk_at(i + 1));
 #pragma unroll
       for (int a = 0; a < KD / 64; ++a) {
         tma_prefetch_3d(&tm_k, 64 * a, hq, t);
@@ -291,11 +261,16 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
                        pack_bf16(S[b + 6], S[b + 7]));
       }
     }
+    if (MODE == kEmit && row < VD) {
+      float* to = prm.emit + ((chunk_slot(p) + at) * prm.Hv + h) * (int64_t)(KD * VD) + row * KD + hf * KH;
+#pragma unroll
+      for (int b = 0; b < KH; b += 8) store32(to + b, S + b);
+    }
     if (len < 64) {
       wait(bar_kq, i);
       wait(bar_v, i);
-      zero_rows(sm + M::KQ, KD / 64, 16384, len, tid);
-      zero_rows(sm + M::V, VD / 64, 8192, len, tid);
+      zero_rows(sm + M::KQ, KD / 64, 16384, len, tid, kTcThreads);
+      zero_rows(sm + M::V, VD / 64, 8192, len, tid, kTcThreads);
     }
     fence_proxy_async();
     tc_fence_before();
@@ -356,12 +331,12 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       } else {
         wait(bar_v, i);
         wait(bar_qs, i);   // the state's copy has been read: its place takes V''
-        weigh_values<VD>(sm, M::V, M::X, down, 64 * hf + row, 128);
+        weigh_values<VD>(sm, M::V, M::X, M::OS, down, 64 * hf + row, 128);
       }
     } else {
       wait(bar_kq, i);
       wait(bar_v, i);
-      weigh_values<VD>(sm, M::V, M::X, down, tid, kTcThreads);
+      weigh_values<VD>(sm, M::V, M::X, M::OS, ADJ ? up : down, tid, kTcThreads);
     }
     dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may come in
     total *= dec;
@@ -370,6 +345,11 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     if (__syncthreads_or(bad)) break;
     tc_fence_after();
     if (tid == 0) {
+      const uint32_t idu = idesc_bf16(128, KD, 1, 1, 0);
+      // the third term first: its place takes o, which is written once V^T P^T, issued behind it, is complete
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mma_bf16(R_U, dsw(s4, M::OS + s * 2048, 8192), dsw(s4, M::KQ + s * 2048, 16384), idu, s > 0);
       if (FULL) {
         const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
 #pragma unroll
@@ -377,11 +357,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
           mma_bf16(R_a, dsw(s4, M::V + s * 2048, 8192), dsw(s4, M::P + s * 32, 16), id, s > 0);
         commit(4, i);
       }
-      const uint32_t id = idesc_bf16(128, KD, 1, 1, 0);
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         mma_bf16(R_U, dsw(s4, M::X + (s >> 2) * (VD / 64 * 8192) + (s & 3) * 2048, 8192),
-                 dsw(s4, M::KQ + (s & 3) * 2048, 16384), id, s > 0);
+                 dsw(s4, M::KQ + (s & 3) * 2048, 16384), idu, 1);
       commit(5, i);
     }
     __syncwarp();
@@ -419,7 +398,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       fence_proxy_async();
       tc_fence_before();
       __syncthreads();
-      const int64_t t0 = p.tok0 + 64 * (int64_t)i;
+      const int64_t t0 = p.tok0 + 64 * (int64_t)at;
       if (len == 64) {
         if (tid == 0) {
 #pragma unroll
@@ -449,10 +428,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     }
     float* to = nullptr;
     const int64_t kv = (int64_t)KD * prm.V;
-    if (!FULL) {
+    if (MODE == kOwn) {
       to = prm.own + (int64_t)ch * kv;
       if (tid == 0 && slice == 0) prm.total[ch] = total;
-    } else if (is_last && prm.ht) {
+    } else if (ends && prm.ht) {
       int64_t at = p.seq;
       if (prm.idx) {
         at = prm.idx[p.seq];
@@ -497,7 +476,34 @@ __global__ void __launch_bounds__(256) empty_kernel(const int32_t* __restrict__ 
 
 int slice_width(const gdn_linear_problem& p) { return p.V >= 128 ? 128 : 64; }
 
-// Tokens a segment: whole sequences when their chains fill the device, else about a twelfth of an even share (whole
+struct Maps {
+  CUtensorMap q, x, y, o;
+};
+
+template <int KD, int VD, int MODE, bool ADJ>
+gdn_status launch_one(unsigned grid, const Maps& m, const TcParams& prm, cudaStream_t s) {
+  auto kern = lin_tc_kernel<KD, VD, MODE, ADJ>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Map<KD, VD>::Bytes) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<grid, kTcThreads, Map<KD, VD>::Bytes, s>>>(m.q, m.x, m.y, m.o, prm);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <int KD, int VD>
+gdn_status launch_dims(int mode, bool adj, unsigned grid, const Maps& m, const TcParams& prm, cudaStream_t s) {
+  if (mode == kFull) return launch_one<KD, VD, kFull, false>(grid, m, prm, s);
+  if (mode == kOwn && !adj) return launch_one<KD, VD, kOwn, false>(grid, m, prm, s);
+  if constexpr (KD <= 128) {   // the head dims of the tensor-core backward pass
+    if (mode == kOwn) return launch_one<KD, VD, kOwn, true>(grid, m, prm, s);
+    if (adj) return launch_one<KD, VD, kEmit, true>(grid, m, prm, s);
+    return launch_one<KD, VD, kEmit, false>(grid, m, prm, s);
+  }
+  return GDN_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+// Tokens a segment: whole sequences when their chains fill the device, else about a quarter of an even share (whole
 // chunks), at least four chunks.
 int segment_tokens(const gdn_linear_problem& p) {
   const int64_t slots = (p.K == 256 ? 1 : 2) * (int64_t)sm_count();
@@ -511,36 +517,70 @@ int segment_tokens(const gdn_linear_problem& p) {
   return (int)(64 * m);
 }
 
-template <int KD, int VD>
-gdn_status launch_tc(const gdn_linear_problem& p, bool full, unsigned grid, const CUtensorMap& tq, const CUtensorMap& tk,
-                     const CUtensorMap& tv, const CUtensorMap& to, const TcParams& prm, cudaStream_t s) {
-  auto kern = full ? lin_tc_kernel<KD, VD, true> : lin_tc_kernel<KD, VD, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Map<KD, VD>::Bytes) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  kern<<<grid, kTcThreads, Map<KD, VD>::Bytes, s>>>(tq, tk, tv, to, prm);
+size_t decays_bytes(const gdn_linear_problem& p) {
+  return 1024 * (size_t)((int64_t)p.B * p.T / 64 + p.N + 1) * p.Hv;
+}
+
+gdn_status launch_decays(const gdn_linear_problem& p, const Pieces& pc, int size, const float* g, float scale,
+                         float* decays, cudaStream_t s) {
+  const int64_t share = ceil_div((int64_t)(size / 64) * p.Hv, 8);   // CTAs a piece
+  decays_kernel<<<dim3(pieces_max(p, size), (unsigned)(share < 64 ? share : 64)), 256, 0, s>>>(g, p.g_per_head, p.Hv,
+                                                                                              pc, scale, decays);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-gdn_status launch_tc(const gdn_linear_problem& p, bool full, unsigned grid, const CUtensorMap& tq, const CUtensorMap& tk,
-                     const CUtensorMap& tv, const CUtensorMap& to, const TcParams& prm, cudaStream_t s) {
-  if (p.V == 64) {
-    if (p.K == 64) return launch_tc<64, 64>(p, full, grid, tq, tk, tv, to, prm, s);
-    if (p.K == 128) return launch_tc<128, 64>(p, full, grid, tq, tk, tv, to, prm, s);
-    return launch_tc<256, 64>(p, full, grid, tq, tk, tv, to, prm, s);
-  }
-  if (p.K == 64) return launch_tc<64, 128>(p, full, grid, tq, tk, tv, to, prm, s);
-  if (p.K == 128) return launch_tc<128, 128>(p, full, grid, tq, tk, tv, to, prm, s);
-  return launch_tc<256, 128>(p, full, grid, tq, tk, tv, to, prm, s);
+gdn_status launch_empty(const gdn_linear_problem& p, const Pieces& pc, const int32_t* cu, const float* h0, float* ht,
+                        const int32_t* idx, int slots, cudaStream_t s) {
+  if (!p.varlen || !ht) return GDN_OK;
+  empty_kernel<<<p.N, 256, 0, s>>>(cu, pc.nc, p.Hv, (int64_t)p.K * p.V, h0, ht, idx, slots);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-}  // namespace
+TcParams tc_params(const gdn_linear_problem& p, const Pieces& pc, const int32_t* cu, float scale, const float* decays,
+                   int32_t* status) {
+  TcParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.pc = pc;
+  prm.decays = decays;
+  prm.status = status;
+  prm.cu = cu;
+  prm.Hqk = p.Hqk;
+  prm.Hv = p.Hv;
+  prm.V = p.V;
+  prm.varlen = p.varlen;
+  prm.T = p.T;
+  prm.scale = scale;
+  return prm;
+}
+
+gdn_status launch_walk(const gdn_linear_problem& p, int mode, bool adj, const void* q, const void* x, int64_t ld_x,
+                       const void* y, int64_t ld_y, void* o, TcParams prm, int size, cudaStream_t s) {
+  const int64_t tokens = (int64_t)p.B * p.T;
+  Maps m;
+  memset(&m, 0, sizeof(m));
+  const uint32_t box[3] = {64, 1, 64};
+  const uint64_t kd[3] = {(uint64_t)p.K, (uint64_t)p.Hqk, (uint64_t)tokens};
+  const uint64_t vd[3] = {(uint64_t)p.V, (uint64_t)p.Hv, (uint64_t)tokens};
+  const uint64_t sx[2] = {(uint64_t)p.K * 2, (uint64_t)ld_x * 2}, sy[2] = {(uint64_t)p.V * 2, (uint64_t)ld_y * 2};
+  if (!make_tmap_bf16(&m.x, x, 3, kd, sx, box) || !make_tmap_bf16(&m.y, y, 3, vd, sy, box)) return GDN_ERR_CUDA;
+  if (mode == kFull) {
+    const uint64_t sq[2] = {(uint64_t)p.K * 2, (uint64_t)p.ld_q * 2};
+    const uint64_t so[2] = {(uint64_t)p.V * 2, (uint64_t)p.Hv * p.V * 2};
+    if (!make_tmap_bf16(&m.q, q, 3, kd, sq, box) || !make_tmap_bf16(&m.o, o, 3, vd, so, box)) return GDN_ERR_CUDA;
+    prm.o = static_cast<__nv_bfloat16*>(o);
+  }
+  const unsigned grid = (unsigned)((int64_t)pieces_max(p, size) * p.Hv * (p.V / slice_width(p)));
+  if (p.V == 64) {
+    if (p.K == 64) return launch_dims<64, 64>(mode, adj, grid, m, prm, s);
+    if (p.K == 128) return launch_dims<128, 64>(mode, adj, grid, m, prm, s);
+    return launch_dims<256, 64>(mode, adj, grid, m, prm, s);
+  }
+  if (p.K == 64) return launch_dims<64, 128>(mode, adj, grid, m, prm, s);
+  if (p.K == 128) return launch_dims<128, 128>(mode, adj, grid, m, prm, s);
+  return launch_dims<256, 128>(mode, adj, grid, m, prm, s);
+}
 
 bool tc_supported(const gdn_linear_problem& p) { return p.dt == GDN_BF16; }
-
-// [slots of chunks][Hv][3][64] fp32
-size_t decays_bytes(const gdn_linear_problem& p) {
-  return 768 * (size_t)((int64_t)p.B * p.T / 64 + p.N + 1) * p.Hv;
-}
 
 // [status][tables][decays][the segments' own: segments x Hv][states: segments x Hv x K x V]
 size_t tc_fwd_bytes(const gdn_linear_problem& p) {
@@ -555,57 +595,28 @@ gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, con
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
   if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
-  const int seg = segment_tokens(p), most = pieces_max(p, seg);
+  const int seg = segment_tokens(p);
   void* tables = at + kAlign;
   if (launch_pieces(p, seg, cu, tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
-  TcParams prm;
-  memset(&prm, 0, sizeof(prm));
-  prm.pc = pieces_at(p, seg, tables);
-  if (p.varlen && ht) {
-    empty_kernel<<<p.N, 256, 0, s>>>(cu, prm.pc.nc, p.Hv, (int64_t)p.K * p.V, h0, ht, idx, slots);
-    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
-  }
-  const int64_t tokens = (int64_t)p.B * p.T;
-  if (tokens == 0) return GDN_OK;
-  CUtensorMap tq, tk, tv, to;
-  const uint32_t box[3] = {64, 1, 64};
-  const uint64_t kd[3] = {(uint64_t)p.K, (uint64_t)p.Hqk, (uint64_t)tokens};
-  const uint64_t vd[3] = {(uint64_t)p.V, (uint64_t)p.Hv, (uint64_t)tokens};
-  const uint64_t sq[2] = {(uint64_t)p.K * 2, (uint64_t)p.ld_q * 2}, sk[2] = {(uint64_t)p.K * 2, (uint64_t)p.ld_k * 2};
-  const uint64_t sv[2] = {(uint64_t)p.V * 2, (uint64_t)p.ld_v * 2};
-  const uint64_t so[2] = {(uint64_t)p.V * 2, (uint64_t)p.Hv * p.V * 2};
-  if (!make_tmap_bf16(&tq, q, 3, kd, sq, box) || !make_tmap_bf16(&tk, k, 3, kd, sk, box) ||
-      !make_tmap_bf16(&tv, v, 3, vd, sv, box) || !make_tmap_bf16(&to, o, 3, vd, so, box))
-    return GDN_ERR_CUDA;
+  const Pieces pc = pieces_at(p, seg, tables);
+  gdn_status st = launch_empty(p, pc, cu, h0, ht, idx, slots, s);
+  if (st != GDN_OK || (int64_t)p.B * p.T == 0) return st;
   float* decays = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, seg));
-  const int64_t share = ceil_div((int64_t)(seg / 64) * p.Hv, 8);   // CTAs a piece
-  decays_kernel<<<dim3(most, (unsigned)(share < 64 ? share : 64)), 256, 0, s>>>(g, p.g_per_head, p.Hv, prm.pc, scale,
-                                                                               decays);
-  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
-  prm.decays = decays;
+  st = launch_decays(p, pc, seg, g, scale, decays, s);
+  TcParams prm = tc_params(p, pc, cu, scale, decays, status);
   prm.h0 = h0;
+  if (st == GDN_OK && seg < p.T) {
+    prm.total = decays + decays_bytes(p) / 4;
+    prm.own = prm.total + align_up(4 * (size_t)pieces_max(p, seg) * p.Hv) / 4;
+    st = launch_walk(p, kOwn, false, nullptr, k, p.ld_k, v, p.ld_v, nullptr, prm, seg, s);
+    if (st == GDN_OK) st = launch_sums<false>(shape_of(p), pc, p.N, prm.total, h0, prm.own, nullptr, nullptr, 0, s);
+    prm.start = prm.own;
+  }
+  if (st != GDN_OK) return st;
   prm.ht = ht;
   prm.idx = idx;
   prm.slots = slots;
-  prm.o = static_cast<__nv_bfloat16*>(o);
-  prm.status = status;
-  prm.cu = cu;
-  prm.Hqk = p.Hqk;
-  prm.Hv = p.Hv;
-  prm.V = p.V;
-  prm.varlen = p.varlen;
-  prm.T = p.T;
-  prm.scale = scale;
-  const unsigned grid = (unsigned)((int64_t)most * p.Hv * (p.V / slice_width(p)));
-  if (seg < p.T) {
-    prm.total = decays + decays_bytes(p) / 4;
-    prm.own = prm.total + align_up(4 * (size_t)most * p.Hv) / 4;
-    gdn_status st = launch_tc(p, false, grid, tq, tk, tv, to, prm, s);
-    if (st == GDN_OK) st = launch_sums<false>(shape_of(p), prm.pc, p.N, prm.total, h0, prm.own, nullptr, nullptr, 0, s);
-    if (st != GDN_OK) return st;
-    prm.start = prm.own;
-  }
-  return launch_tc(p, true, grid, tq, tk, tv, to, prm, s);
+  return launch_walk(p, kFull, false, q, k, p.ld_k, v, p.ld_v, o, prm, seg, s);
 }
 
 }  // namespace lin

@@ -179,6 +179,22 @@ def test_pool_rows_and_states_in_place(gdn, dtype):
     assert gdn.gdn_linear_attn_fwd(x["q"], x["k"], x["v"], x["g"], output_final_state=False)[1] is None
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_long_sequences_states_in_place(gdn, dtype):
+    """Sequences cut into segments: the final state may take the initial one's place, dh0 that of dht."""
+    x = make(2, 3000, 1, 2, 128, 128, dtype, strong=0)
+    args = (x["q"], x["k"], x["v"], x["g"])
+    o, ht = gdn.gdn_linear_attn_fwd(*args, h0=x["h0"])
+    g = gdn.gdn_linear_attn_bwd(*args, x["do"], h0=x["h0"], dht=x["dht"])
+    for _ in range(5):
+        h = x["h0"].clone()
+        o2, _ = gdn.gdn_linear_attn_fwd(*args, h0=h, ht=h)
+        assert torch.equal(o, o2) and torch.equal(h, ht)
+    check_fwd(gdn, x)
+    check_bwd(gdn, x)
+    assert torch.equal(g["dh0"], gdn.gdn_linear_attn_bwd(*args, x["do"], h0=x["h0"], dht=x["dht"])["dh0"])
+
+
 def test_malformed_offsets_write_nothing(gdn):
     for bad in ([0, 50, 40, 100], [1, 50, 60, 100], [0, 50, 60, 99], [0, -3, 60, 100], [0, 200, 60, 100]):
         for dtype in (F32, BF):

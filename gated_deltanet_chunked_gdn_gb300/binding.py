@@ -527,6 +527,21 @@ except AttributeError:
         return torch.cuda.current_stream(index).cuda_stream
 
 
+try:
+    _current_device = torch._C._cuda_getDevice
+except AttributeError:
+    def _current_device() -> int:
+        return torch.cuda.current_device()
+
+
+def _call(dev: int, fn, *args):
+    """fn(*args) with the device current that it launches on."""
+    if _current_device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _check_ws(workspace, x) -> None:
     if workspace is not None and workspace.device != x.device:
         raise ValueError("workspace must be on the device of x")
@@ -858,6 +873,26 @@ def _linear_problem(q, k, v, g, cu_seqlens, fp32=(), others=()):
     """Checks of a linear attention's tensors and its problem.  fp32: (name, tensor, shape) that must be contiguous
     float32; others: (name, tensor) that must be like v and contiguous."""
     dtype, dev = v.dtype, v.get_device()
+    # the usual call, all rows contiguous, in one expression: a decode step's launch is shorter than its checks
+    if cu_seqlens is None and not others and dtype in DTYPES and dev >= 0 and q.dim() == 4 and v.dim() == 4:
+        B, T, Hqk, K = qshape = q.shape
+        b, t, Hv, V = v.shape
+        f32 = torch.float32
+        if (k.shape == qshape and b == B and t == T and q.dtype is dtype and k.dtype is dtype and g.dtype is f32
+                and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous()
+                and q.get_device() == dev and k.get_device() == dev and g.get_device() == dev
+                and (g.shape == (B, T, Hv) or g.shape == (Hv,))):
+            for _, x, want in fp32:
+                if x is not None and (x.dtype is not f32 or x.get_device() != dev or x.shape != want
+                                      or not x.is_contiguous()):
+                    break
+            else:
+                return LinearProblem(B, T, B, Hqk, Hv, K, V, DTYPES[dtype], 0, 1 if g.dim() == 1 else 0)
+    return _linear_problem_checked(q, k, v, g, cu_seqlens, fp32, others)
+
+
+def _linear_problem_checked(q, k, v, g, cu_seqlens, fp32, others):
+    dtype, dev = v.dtype, v.get_device()
     if dtype not in DTYPES or dev < 0 or q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k [B, T, Hqk, K] and v [B, T, Hv, V] must be float32 or bfloat16 CUDA tensors")
     B, T, Hqk, K = qshape = q.shape
@@ -923,18 +958,16 @@ def gdn_linear_attn_fwd(q, k, v, g, scale: Optional[float] = None, h0=None, cu_s
     if ht is None and output_final_state:
         ht = torch.empty(state, dtype=torch.float32, device=v.device)
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = lib.gdn_linear_attn_fwd_workspace_size(p)
+        need = _call(dev, lib.gdn_linear_attn_fwd_workspace_size, p)
         if need == 0:
             raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_linear_attn_fwd_workspace_size")
         workspace = _alloc_ws(need, v.device)
     if stream is not None:
         _lend(stream, v.device, [t for t, x in zip((o, ht, workspace), given) if x is None])
-    with torch.cuda.device(dev):
-        st = lib.gdn_linear_attn_fwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                     state[2] ** -0.5 if scale is None else scale, _address(h0), _address(cu_seqlens),
-                                     o.data_ptr(), _address(ht), idx, rows[0], workspace.data_ptr(), workspace.numel(),
-                                     stream if stream is not None else _current_stream(dev))
+    st = _call(dev, lib.gdn_linear_attn_fwd, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+               state[2] ** -0.5 if scale is None else scale, _address(h0), _address(cu_seqlens), o.data_ptr(),
+               _address(ht), idx, rows[0], workspace.data_ptr(), workspace.numel(),
+               stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_linear_attn_fwd")
     return o, ht
@@ -968,8 +1001,7 @@ def gdn_linear_attn_bwd(q, k, v, g, dout, scale: Optional[float] = None, h0=None
     p = _linear_problem(q, k, v, g, cu_seqlens, (("h0", h0, state), ("dht", dht, state)), (("dout", dout),))
     given = workspace
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = lib.gdn_linear_attn_bwd_workspace_size(p)
+        need = _call(dev, lib.gdn_linear_attn_bwd_workspace_size, p)
         if need == 0:
             raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_linear_attn_bwd_workspace_size")
         workspace = _alloc_ws(need, v.device)
@@ -980,12 +1012,10 @@ def gdn_linear_attn_bwd(q, k, v, g, dout, scale: Optional[float] = None, h0=None
            "dg": torch.empty(g.shape, **f32), "dh0": torch.empty(state, **f32) if want_dh0 else None}
     if stream is not None:
         _lend(stream, v.device, (*out.values(), workspace if given is None else None))
-    with torch.cuda.device(dev):
-        st = lib.gdn_linear_attn_bwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                     state[2] ** -0.5 if scale is None else scale, _address(h0), _address(cu_seqlens),
-                                     dout.data_ptr(), _address(dht), *(_address(t) for t in out.values()),
-                                     workspace.data_ptr(), workspace.numel(),
-                                     stream if stream is not None else _current_stream(dev))
+    st = _call(dev, lib.gdn_linear_attn_bwd, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+               state[2] ** -0.5 if scale is None else scale, _address(h0), _address(cu_seqlens), dout.data_ptr(),
+               _address(dht), *(_address(t) for t in out.values()), workspace.data_ptr(), workspace.numel(),
+               stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_linear_attn_bwd")
     out["workspace"] = workspace
@@ -1006,11 +1036,9 @@ def gdn_linear_attn_step(q, k, v, g, state, scale: Optional[float] = None, state
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         if stream is not None:
             _lend(stream, v.device, (o,))
-    with torch.cuda.device(dev):
-        st = lib.gdn_linear_attn_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                      p.K ** -0.5 if scale is None else scale, state.data_ptr(), idx, slots,
-                                      _address(cu_seqlens), o.data_ptr(),
-                                      stream if stream is not None else _current_stream(dev))
+    st = _call(dev, lib.gdn_linear_attn_step, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+               p.K ** -0.5 if scale is None else scale, state.data_ptr(), idx, slots, _address(cu_seqlens),
+               o.data_ptr(), stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_linear_attn_step")
     return o
@@ -1046,8 +1074,14 @@ def _check_like(dev, *tensors):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the device of x")
 
 
-def _gated_norm(x, z, weight, others):
-    dtype, dev = x.dtype, x.get_device()
+def _gated_norm(x, z, weight, others=()):
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
+    if (not others and dtype in DTYPES and dev >= 0 and len(shape) >= 2 and x.is_contiguous()
+            and weight.dtype is torch.float32 and weight.shape == shape[-1:] and weight.get_device() == dev
+            and weight.is_contiguous()
+            and (z is None or (z.shape == shape and z.dtype is dtype and z.get_device() == dev and z.is_contiguous()))):
+        H, V = shape[-2:]   # the usual call
+        return x.numel() // (H * V) if H * V else 0, H, V, 0, 0, DTYPES[dtype], dev
     if dtype not in DTYPES or dev < 0 or x.dim() < 2:
         raise ValueError("x must be a float32 or bfloat16 CUDA tensor [..., H, V]")
     H, V = x.shape[-2:]
@@ -1063,7 +1097,7 @@ def gdn_gated_norm_fwd(x, z, weight, eps: float = 1e-6, y=None, save_rstd: bool 
     wider rows; z None: no gate), weight [V] fp32.  Returns (y, rstd); rstd [..., H] fp32 is None unless
     ``save_rstd`` (for the backward)."""
     lib = _lib or load()
-    rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("y", y, x.dtype, x.shape),))
+    rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("y", y, x.dtype, x.shape),) if y is not None else ())
     fresh = []
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -1074,10 +1108,8 @@ def gdn_gated_norm_fwd(x, z, weight, eps: float = 1e-6, y=None, save_rstd: bool 
         fresh.append(rstd)
     if stream is not None:
         _lend(stream, x.device, fresh)
-    with torch.cuda.device(dev):
-        st = lib.gdn_gated_norm_fwd(x.data_ptr(), ld_x, _address(z), ld_z, weight.data_ptr(), rows, H, V, dt, eps,
-                                    y.data_ptr(), _address(rstd),
-                                    stream if stream is not None else _current_stream(dev))
+    st = _call(dev, lib.gdn_gated_norm_fwd, x.data_ptr(), ld_x, _address(z), ld_z, weight.data_ptr(), rows, H, V, dt,
+               eps, y.data_ptr(), _address(rstd), stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_gated_norm_fwd")
     return y, rstd
@@ -1091,21 +1123,19 @@ def gdn_gated_norm_bwd(x, z, weight, rstd, dy, workspace=None, stream=None) -> d
     rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("dy", dy, x.dtype, x.shape),
                                                                  ("rstd", rstd, torch.float32, x.shape[:-1])))
     given = workspace
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = lib.gdn_gated_norm_bwd_workspace_size(V)
-            if need == 0:
-                raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_gated_norm_bwd_workspace_size")
-            workspace = _alloc_ws(need, x.device)
-        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
-               "dz": torch.empty(x.shape, dtype=x.dtype, device=x.device) if z is not None else None,
-               "dweight": torch.empty((V,), dtype=torch.float32, device=x.device)}
-        if stream is not None:
-            _lend(stream, x.device, (*out.values(), workspace if given is None else None))
-        st = lib.gdn_gated_norm_bwd(x.data_ptr(), ld_x, _address(z), ld_z, weight.data_ptr(), rstd.data_ptr(),
-                                    dy.data_ptr(), rows, H, V, dt, *(_address(t) for t in out.values()),
-                                    workspace.data_ptr(), workspace.numel(),
-                                    stream if stream is not None else _current_stream(dev))
+    if workspace is None:
+        need = _call(dev, lib.gdn_gated_norm_bwd_workspace_size, V)
+        if need == 0:
+            raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_gated_norm_bwd_workspace_size")
+        workspace = _alloc_ws(need, x.device)
+    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
+           "dz": torch.empty(x.shape, dtype=x.dtype, device=x.device) if z is not None else None,
+           "dweight": torch.empty((V,), dtype=torch.float32, device=x.device)}
+    if stream is not None:
+        _lend(stream, x.device, (*out.values(), workspace if given is None else None))
+    st = _call(dev, lib.gdn_gated_norm_bwd, x.data_ptr(), ld_x, _address(z), ld_z, weight.data_ptr(), rstd.data_ptr(),
+               dy.data_ptr(), rows, H, V, dt, *(_address(t) for t in out.values()), workspace.data_ptr(),
+               workspace.numel(), stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_gated_norm_bwd")
     out["workspace"] = workspace
@@ -1117,10 +1147,22 @@ def _residual_norm(y, residual, post_weight, gate, weight, others):
     if dtype not in DTYPES or dev < 0 or y.dim() < 1:
         raise ValueError("y must be a float32 or bfloat16 CUDA tensor [..., D]")
     shape, D = y.shape, y.shape[-1]
+    f32 = torch.float32
+    if (not others and y.is_contiguous() and residual.is_contiguous() and residual.shape == shape
+            and residual.get_device() == dev and (residual.dtype is dtype or residual.dtype is f32)):
+        vec, kind = shape[-1:], 0
+        if gate is not None:   # 1: a vector, 2: like y
+            kind = 2 if gate.shape == shape and gate.dtype is dtype else 1
+        for t in (post_weight, weight, gate if kind == 1 else None):
+            if t is not None and (t.dtype is not f32 or t.shape != vec or t.get_device() != dev
+                                  or not t.is_contiguous()):
+                break
+        else:   # the usual call
+            if kind < 2 or (gate.get_device() == dev and gate.is_contiguous()):
+                return y.numel() // D if D else 0, D, 0, kind, DTYPES[dtype], DTYPES[residual.dtype], dev
     if residual.dtype not in (dtype, torch.float32):
         raise ValueError("residual must have the dtype of y, or float32")
     kind = 0 if gate is None else 1 if gate.dim() == 1 and gate.dtype is torch.float32 and shape != gate.shape else 2
-    f32 = torch.float32
     _check_like(dev, ("residual", residual, residual.dtype, shape), ("post_weight", post_weight, f32, (D,)),
                 ("gate", gate, *((f32, (D,)) if kind == 1 else (dtype, shape))), ("weight", weight, f32, (D,)),
                 *others)
@@ -1135,8 +1177,8 @@ def gdn_residual_norm_fwd(y, residual, post_weight=None, gate=None, residual_sca
     [D] fp32 or [..., D] like y, post_weight (None: y as it is) and weight (None: no n) [D] fp32.  Returns
     (h, n, rstd); h may be the residual itself, n is None without weight, rstd [..., 2] fp32 unless ``save_rstd``."""
     lib = _lib or load()
-    rows, D, ld, kind, dt, rdt, dev = _residual_norm(y, residual, post_weight, gate, weight,
-                                                     (("h", h, residual.dtype, y.shape), ("n", n, y.dtype, y.shape)))
+    given = (("h", h, residual.dtype, y.shape), ("n", n, y.dtype, y.shape)) if h is not None or n is not None else ()
+    rows, D, ld, kind, dt, rdt, dev = _residual_norm(y, residual, post_weight, gate, weight, given)
     if n is not None and weight is None:
         raise ValueError("n needs weight")
     fresh = []
@@ -1152,11 +1194,9 @@ def gdn_residual_norm_fwd(y, residual, post_weight=None, gate=None, residual_sca
         fresh.append(rstd)
     if stream is not None:
         _lend(stream, y.device, fresh)
-    with torch.cuda.device(dev):
-        st = lib.gdn_residual_norm_fwd(y.data_ptr(), ld, residual.data_ptr(), _address(post_weight), _address(gate),
-                                       kind, residual_scale, _address(weight), rows, D, dt, rdt, eps, h.data_ptr(),
-                                       _address(n), _address(rstd),
-                                       stream if stream is not None else _current_stream(dev))
+    st = _call(dev, lib.gdn_residual_norm_fwd, y.data_ptr(), ld, residual.data_ptr(), _address(post_weight),
+               _address(gate), kind, residual_scale, _address(weight), rows, D, dt, rdt, eps, h.data_ptr(),
+               _address(n), _address(rstd), stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_residual_norm_fwd")
     return h, n, rstd
@@ -1177,25 +1217,23 @@ def gdn_residual_norm_bwd(y, residual, rstd, dh, dn=None, post_weight=None, gate
     if (dn is None) != (weight is None):
         raise ValueError("dn and weight come together")
     given = workspace
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = lib.gdn_residual_norm_bwd_workspace_size(D)
-            if need == 0:
-                raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_residual_norm_bwd_workspace_size")
-            workspace = _alloc_ws(need, y.device)
-        f32 = dict(dtype=torch.float32, device=y.device)
-        out = {"dy": torch.empty(y.shape, dtype=y.dtype, device=y.device),
-               "dresidual": torch.empty(y.shape, dtype=residual.dtype, device=y.device),
-               "dpost_weight": torch.empty((D,), **f32) if post_weight is not None else None,
-               "dgate": torch.empty(gate.shape, dtype=gate.dtype, device=y.device) if gate is not None else None,
-               "dweight": torch.empty((D,), **f32) if weight is not None else None}
-        if stream is not None:
-            _lend(stream, y.device, (*out.values(), workspace if given is None else None))
-        st = lib.gdn_residual_norm_bwd(y.data_ptr(), ld, residual.data_ptr(), rstd.data_ptr(), _address(dh),
-                                       _address(dn), _address(post_weight), _address(gate), kind, residual_scale,
-                                       _address(weight), rows, D, dt, rdt, *(_address(t) for t in out.values()),
-                                       workspace.data_ptr(), workspace.numel(),
-                                       stream if stream is not None else _current_stream(dev))
+    if workspace is None:
+        need = _call(dev, lib.gdn_residual_norm_bwd_workspace_size, D)
+        if need == 0:
+            raise GDNError(GDN_ERR_UNSUPPORTED, "gdn_residual_norm_bwd_workspace_size")
+        workspace = _alloc_ws(need, y.device)
+    f32 = dict(dtype=torch.float32, device=y.device)
+    out = {"dy": torch.empty(y.shape, dtype=y.dtype, device=y.device),
+           "dresidual": torch.empty(y.shape, dtype=residual.dtype, device=y.device),
+           "dpost_weight": torch.empty((D,), **f32) if post_weight is not None else None,
+           "dgate": torch.empty(gate.shape, dtype=gate.dtype, device=y.device) if gate is not None else None,
+           "dweight": torch.empty((D,), **f32) if weight is not None else None}
+    if stream is not None:
+        _lend(stream, y.device, (*out.values(), workspace if given is None else None))
+    st = _call(dev, lib.gdn_residual_norm_bwd, y.data_ptr(), ld, residual.data_ptr(), rstd.data_ptr(), _address(dh),
+               _address(dn), _address(post_weight), _address(gate), kind, residual_scale, _address(weight), rows, D,
+               dt, rdt, *(_address(t) for t in out.values()), workspace.data_ptr(), workspace.numel(),
+               stream if stream is not None else _current_stream(dev))
     if st:
         raise GDNError(st, "gdn_residual_norm_bwd")
     out["workspace"] = workspace

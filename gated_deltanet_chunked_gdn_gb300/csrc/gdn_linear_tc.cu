@@ -56,24 +56,28 @@ __device__ __forceinline__ void store32(float* p, const float* v) {
                : "memory");
 }
 
-// V'' = diag(down) V: `n` threads (thread t of them), 8 columns of a row at a time; zeros where down is 0.
+// V'' = diag(down) V in three terms (packed pairs throughout: a chunk's instructions bound the kernel): a thread takes
+// 8 columns of a row at a time, units [u, end) in steps of n; zeros where down is 0.
 template <int VD>
-__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, uint32_t x3, const float* down, int t,
-                                             int n) {
-#pragma unroll 4
-  for (int u = t; u < 64 * (VD / 8); u += n) {
+__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, uint32_t x3, const float* down, int u,
+                                             int end, int n) {
+  const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll 2
+  for (; u < end; u += n) {
     const int j = u / (VD / 8), c = u % (VD / 8);
     const uint32_t off = (c >> 3) * 8192 + sw128_chunk(j, c & 7);
     const uint4 w = *reinterpret_cast<const uint4*>(sm + v + off);
-    const float f = down[j];
+    const float2 f = make_float2(down[j], down[j]);
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float a = f * __uint_as_float(in[i] << 16), b = f * __uint_as_float(in[i] & 0xffff0000u);
-      hi[i] = pack_bf16(a, b);
-      a -= __uint_as_float(hi[i] << 16), b -= __uint_as_float(hi[i] & 0xffff0000u);
-      split2(a, b, lo[i], rest[i]);
+      float2 a = __fmul2_rn(f, halves(in[i]));
+      hi[i] = pack_bf16(a.x, a.y);
+      a = __ffma2_rn(halves(hi[i]), minus, a);
+      lo[i] = pack_bf16(a.x, a.y);
+      a = __ffma2_rn(halves(lo[i]), minus, a);
+      rest[i] = pack_bf16(a.x, a.y);
     }
     *reinterpret_cast<uint4*>(sm + x + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(sm + x + VD / 64 * 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -81,9 +85,24 @@ __device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x
   }
 }
 
+// A sum of two floats that holds twice a float's bits.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two add(Two a, float bh, float bl) {
+  const float s = a.h + bh, v = s - a.h, e = ((a.h - (s - v)) + (bh - v)) + (a.l + bl);
+  const float h = s + e;
+  return {h, e - (h - s)};
+}
+__device__ __forceinline__ Two log2_units(Two a) {
+  constexpr float kLow = (float)(1.4426950408889634 - (double)kLog2e);   // log2(e) = kLog2e + kLow
+  const float h = a.h * kLog2e;
+  return {h, fmaf(a.h, kLog2e, -h) + fmaf(a.l, kLog2e, a.h * kLow)};
+}
+
 // Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i} and what the first lacks
-// to 48 bits; the sums in 64 bits (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and differences
-// of the sums do).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A warp takes a chunk and head at a time.  Done by the kernels below, one warp would take 2000 cycles of a chunk's 5000 while the others wait.
+// to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
+// differences of the sums do; sums in double take seven times as long, fp64 being scarce here).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A warp takes a chunk and head at a time.  Done by the kernels below, one warp would take 2000 cycles of a chunk's 5000 while the others wait.
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
                                                      float scale, float* __restrict__ out) {
   const Piece p = piece_of(pc, blockIdx.x);
@@ -94,22 +113,21 @@ __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g
     const float* gp = g + (g_per_head ? h : (p.tok0 + 64 * i + r) * Hv + h);
     const float ga = r < len ? gp[0] : 0.f, gb = r + 1 < len ? gp[g_per_head ? 0 : Hv] : 0.f;
     // e^-150 is 0 in fp32: stronger decays are cut there, and -infinity never meets itself in a difference
-    const double a = ga < -150.f ? -150.0 : (double)ga, b = gb < -150.f ? -150.0 : (double)gb;
-    double s = a + b;
+    const float a = ga < -150.f ? -150.f : ga, b = gb < -150.f ? -150.f : gb;
+    Two s = add({a, 0.f}, b, 0.f);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double t = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += t;
+      const float th = __shfl_up_sync(0xffffffffu, s.h, o), tl = __shfl_up_sync(0xffffffffu, s.l, o);
+      if (lane >= o) s = add(s, th, tl);
     }
-    const double last = __shfl_sync(0xffffffffu, s, 31), s0 = s - b;
-    constexpr double kL = 1.4426950408889634;
+    const float lh = __shfl_sync(0xffffffffu, s.h, 31), ll = __shfl_sync(0xffffffffu, s.l, 31);
+    const Two s0 = add(s, -b, 0.f), x0 = log2_units(s0), x1 = log2_units(s);
     float* to = out + ((chunk_slot(p) + i) * Hv + h) * 256 + r;
-    const float h0 = (float)(s0 * kL), h1 = (float)(s * kL);
-    *reinterpret_cast<float2*>(to) = make_float2(h0, h1);
-    *reinterpret_cast<float2*>(to + 192) = make_float2((float)(s0 * kL - h0), (float)(s * kL - h1));
-    *reinterpret_cast<float2*>(to + 64) =
-        make_float2(r < len ? expf((float)(last - s0)) : 0.f, r + 1 < len ? expf((float)(last - s)) : 0.f);
-    *reinterpret_cast<float2*>(to + 128) = make_float2(scale * expf((float)s0), scale * expf((float)s));
+    *reinterpret_cast<float2*>(to) = make_float2(x0.h, x1.h);
+    *reinterpret_cast<float2*>(to + 192) = make_float2(x0.l, x1.l);
+    *reinterpret_cast<float2*>(to + 64) = make_float2(r < len ? expf((lh - s0.h) + (ll - s0.l)) : 0.f,
+                                                      r + 1 < len ? expf((lh - s.h) + (ll - s.l)) : 0.f);
+    *reinterpret_cast<float2*>(to + 128) = make_float2(scale * expf(s0.h + s0.l), scale * expf(s.h + s.l));
   }
 }
 
@@ -130,8 +148,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   const float* up = reinterpret_cast<const float*>(sm + M::Up);
   // every barrier completes one phase a chunk, and every thread that waits for it does so once a chunk, in order
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::Bar);
-  uint64_t *bar_kq = bars, *bar_v = bars + 1, *bar_qk = bars + 2, *bar_qs = bars + 3, *bar_pv = bars + 4,
-           *bar_u = bars + 5;
+  uint64_t *bar_k = bars, *bar_v = bars + 1, *bar_qk = bars + 2, *bar_qs = bars + 3, *bar_pv = bars + 4,
+           *bar_u = bars + 5, *bar_q = bars + 6;
   volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(sm + M::Flags);   // [0] TMEM base
   volatile uint32_t* count = flags + 1;   // thread 0: phases begun on each barrier (what an abort has to wait for)
 
@@ -152,10 +170,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
 
   if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 7; ++i) mbar_init(bars + i, 1);
     mbar_fence_init();
 #pragma unroll
-    for (int i = 0; i < 6; ++i) count[i] = 0;
+    for (int i = 0; i < 7; ++i) count[i] = 0;
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
     if (FULL) {
@@ -172,16 +190,20 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   const uint32_t lane_off = static_cast<uint32_t>(32 * qd) << 16;
 
   bool bad = false;   // one of this thread's waits ran out
-  auto issue_kq = [&](int i) {
+  auto issue_k = [&](int i) {
     const int at = chunk_at(i), t = (int)(p.tok0 + 64 * at);
     count[0] = i + 1;
-    mbar_arrive_expect_tx(bar_kq, (FULL ? 2 : 1) * KD / 64 * 8192 + 768);
-    bulk_load(sm + M::Gam, prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * 256, 768, bar_kq);
+    mbar_arrive_expect_tx(bar_k, KD / 64 * 8192 + 768);
+    bulk_load(sm + M::Gam, prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * 256, 768, bar_k);
 #pragma unroll
-    for (int a = 0; a < KD / 64; ++a) {
-      tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_kq, 64 * a, hq, t);
-      if (FULL) tma_load_3d(sm + M::KQ + a * 16384 + 8192, &tm_q, bar_kq, 64 * a, hq, t);
-    }
+    for (int a = 0; a < KD / 64; ++a) tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_k, 64 * a, hq, t);
+  };
+  auto issue_q = [&](int i) {
+    const int t = (int)(p.tok0 + 64 * chunk_at(i));
+    count[6] = i + 1;
+    mbar_arrive_expect_tx(bar_q, KD / 64 * 8192);
+#pragma unroll
+    for (int a = 0; a < KD / 64; ++a) tma_load_3d(sm + M::KQ + a * 16384 + 8192, &tm_q, bar_q, 64 * a, hq, t);
   };
   auto issue_v = [&](int i) {
     const int t = (int)(p.tok0 + 64 * chunk_at(i));
@@ -198,7 +220,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     count[b] = i + 1;
   };
   if (tid == 0) {
-    issue_kq(0);
+    if (FULL) issue_q(0);
+    issue_k(0);
     issue_v(0);
   }
 
@@ -227,21 +250,11 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   for (int i = 0; i < nchunks; ++i) {
     const int at = chunk_at(i), len = p.len - 64 * at < 64 ? p.len - 64 * at : 64;
     // ---- the state: what the chunk before added, and its bf16 copy
-    if (tid == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
-      const int t = (int)(p.tok0 + 64 * chunk_at(i + 1));
-#pragma unroll
-      for (int a = 0; a < KD / 64; ++a) {
-        tma_prefetch_3d(&tm_k, 64 * a, hq, t);
-        if (FULL) tma_prefetch_3d(&tm_q, 64 * a, hq, t);
-      }
-#pragma unroll
-      for (int a = 0; a < VD / 64; ++a) tma_prefetch_3d(&tm_v, e0 + 64 * a, h, t);
-    }
     if (i > 0) {
       wait(bar_u, i - 1);
       tc_fence_after();
       if (tid == 0 && !bad) {
-        issue_kq(i);        // K and Q of the chunk before have been read
+        issue_k(i);         // K of the chunk before has been read
         if (!FULL) issue_v(i);
       }
 #pragma unroll
@@ -249,7 +262,11 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         float u[32];
         tmem_ld32(R_U + lane_off + hf * KH + b, u);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[b + j] = fmaf(dec, S[b + j], u[j]);
+        for (int j = 0; j < 32; j += 2) {
+          const float2 x = __ffma2_rn(make_float2(dec, dec), make_float2(S[b + j], S[b + j + 1]),
+                                      make_float2(u[j], u[j + 1]));
+          S[b + j] = x.x, S[b + j + 1] = x.y;
+        }
       }
     }
     if (FULL && row < VD) {
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       for (int b = 0; b < KH; b += 8) store32(to + b, S + b);
     }
     if (len < 64) {
-      wait(bar_kq, i);
+      wait(bar_k, i);
       wait(bar_v, i);
       zero_rows(sm + M::KQ, KD / 64, 16384, len, tid, kTcThreads);
       zero_rows(sm + M::V, VD / 64, 8192, len, tid, kTcThreads);
@@ -277,19 +294,20 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     if (__syncthreads_or(bad)) break;
     tc_fence_after();
 
+    if (warp == 6 && lane == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
+      const int t = (int)(p.tok0 + 64 * chunk_at(i + 1));
+#pragma unroll
+      for (int a = 0; a < KD / 64; ++a) tma_prefetch_3d(&tm_k, 64 * a, hq, t);
+#pragma unroll
+      for (int a = 0; a < VD / 64; ++a) tma_prefetch_3d(&tm_v, e0 + 64 * a, h, t);
+    }
     if (FULL) {
-      wait(bar_kq, i);   // every thread reads the decays
       if (tid == 0) {
         bulk_wait_read();   // the o staging has been read
+        const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
+        wait(bar_q, i);
         if (!bad) {
           tc_fence_after();
-          const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
-#pragma unroll
-          for (int s = 0; s < KD / 16; ++s) {
-            const uint32_t a = M::KQ + (s >> 2) * 16384 + (s & 3) * 32;
-            mma_bf16(R_a, dsw(s4, a, 16), dsw(s4, a, 16), id, s > 0);
-          }
-          commit(2, i);
 #pragma unroll
           for (int s = 0; s < KD / 16; ++s) {
             const uint32_t a = M::X + (s >> 2) * (VD * 128) + (s & 3) * 32;
@@ -298,10 +316,21 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
           }
           commit(3, i);
         }
+        wait(bar_k, i);
+        if (!bad) {
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < KD / 16; ++s) {
+            const uint32_t a = M::KQ + (s >> 2) * 16384 + (s & 3) * 32;
+            mma_bf16(R_a, dsw(s4, a, 16), dsw(s4, a, 16), id, s > 0);
+          }
+          commit(2, i);
+        }
       }
       __syncwarp();
       if (qd >= 2) {
         // P row i2, columns 32 hf ..
+        wait(bar_k, i);   // every thread that reads the decays waits for them
         wait(bar_qk, i);
         tc_fence_after();
         float v[32];
@@ -327,16 +356,20 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) solve64::store8_bf16(sm + M::P + sw128_chunk(i2, 4 * hf + q), v + 8 * q);
-        wait(bar_qs, i);
-      } else {
-        wait(bar_v, i);
-        wait(bar_qs, i);   // the state's copy has been read: its place takes V''
-        weigh_values<VD>(sm, M::V, M::X, M::OS, down, 64 * hf + row, 128);
       }
-    } else {
-      wait(bar_kq, i);
+      // V'': the warps without weights begin with five eighths of it, the one whose weights are all zero takes as
+      // much as the three others behind theirs
+      wait(bar_k, i);
       wait(bar_v, i);
-      weigh_values<VD>(sm, M::V, M::X, M::OS, ADJ ? up : down, tid, kTcThreads);
+      wait(bar_qs, i);   // the state's copy has been read: its place takes V''
+      constexpr int n = 64 * (VD / 8);
+      if (qd < 2) weigh_values<VD>(sm, M::V, M::X, M::OS, down, 64 * hf + row, n * 5 / 8, 128);
+      else if (warp == 6) weigh_values<VD>(sm, M::V, M::X, M::OS, down, n * 13 / 16 + lane, n, 32);
+      else weigh_values<VD>(sm, M::V, M::X, M::OS, down, n * 5 / 8 + 32 * (warp == 7 ? 2 : warp - 2) + lane, n * 13 / 16, 96);
+    } else {
+      wait(bar_k, i);
+      wait(bar_v, i);
+      weigh_values<VD>(sm, M::V, M::X, M::OS, ADJ ? up : down, tid, 64 * (VD / 8), kTcThreads);
     }
     dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may come in
     total *= dec;
@@ -362,6 +395,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         mma_bf16(R_U, dsw(s4, M::X + (s >> 2) * (VD / 64 * 8192) + (s & 3) * 2048, 8192),
                  dsw(s4, M::KQ + (s & 3) * 2048, 16384), idu, 1);
       commit(5, i);
+      if (FULL && i + 1 < nchunks) {
+        wait(bar_qk, i);   // Q has been read (QS before it)
+        if (!bad) issue_q(i + 1);
+      }
     }
     __syncwarp();
     if (FULL) {
@@ -373,8 +410,6 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       const uint32_t xsw = (static_cast<uint32_t>((ecol >> 3) ^ (odd ? 1 : 0))) << 4;
       float oq[32];
       tmem_ld32(R_b + lane_off + 32 * hf, oq);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) oq[j] *= up[32 * hf + j];
       wait(bar_pv, i);
       tc_fence_after();
       if (tid == 0 && i + 1 < nchunks && !bad) issue_v(i + 1);
@@ -387,9 +422,11 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
           uint8_t* qb = lbase + col * 128;
 #pragma unroll
           for (int pp = 0; pp < 8; ++pp) {
-            const float v0 = oq[16 * q + 2 * pp] + b[2 * pp], v1 = oq[16 * q + 2 * pp + 1] + b[2 * pp + 1];
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-            const uint32_t word = odd ? pack_bf16(other, v1) : pack_bf16(v0, other);
+            const float2 f = *reinterpret_cast<const float2*>(up + col + 2 * pp);
+            const float2 v = __ffma2_rn(f, make_float2(oq[16 * q + 2 * pp], oq[16 * q + 2 * pp + 1]),
+                                        make_float2(b[2 * pp], b[2 * pp + 1]));
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
+            const uint32_t word = odd ? pack_bf16(other, v.y) : pack_bf16(v.x, other);
             const uint32_t off = (2 * pp) * 128 + (xsw ^ (static_cast<uint32_t>((2 * pp) & 7) << 4));
             *reinterpret_cast<uint32_t*>(qb + off) = word;
           }
@@ -448,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   if (tid == 0) bulk_wait_read();
   if (__syncthreads_or(bad) && tid == 0) {
     // abort: loads and products in flight finish (bounded) before their memory is released
-    for (int b = 0; b < 6; ++b)
+    for (int b = 0; b < 7; ++b)
       if (count[b] > 0) mbar_wait(bars + b, (count[b] - 1) & 1, prm.status, 100000000ull);
   }
   tc_fence_before();
@@ -503,18 +540,26 @@ gdn_status launch_dims(int mode, bool adj, unsigned grid, const Maps& m, const T
 
 }  // namespace
 
-// Tokens a segment: whole sequences when their chains fill the device, else about a quarter of an even share (whole
-// chunks), at least four chunks.
+// Tokens a segment.  Equal lengths: the number of segments a sequence that costs least in chunks on the busiest CTA
+// slot: full walks in rounds of the slots' segments (and half as much for the segments' own contributions, where there
+// is more than one), about two chunks for a segment's start and end.  32 heads, K = V = 128: 8192 tokens take 9
+// segments, 4 x 8192 take 7.  Packed batches, whose lengths the host does not know: half of a slot's even share.
 int segment_tokens(const gdn_linear_problem& p) {
   const int64_t slots = (p.K == 256 ? 1 : 2) * (int64_t)sm_count();
   const int64_t heads = (int64_t)p.Hv * (p.V / slice_width(p));
-  const int64_t chunks = p.varlen ? p.T / 64 + p.N : p.B * ceil_div(p.T, 64);
   const int64_t whole = ceil_div(p.T > 0 ? p.T : 1, 64);
-  int64_t m = whole;
-  if (p.varlen || p.N * heads < 2 * slots) m = ceil_div(chunks * heads, 4 * slots);
-  if (m < 4) m = 4;
-  if (m > whole) m = whole;
-  return (int)(64 * m);
+  if (p.varlen) {
+    const int64_t m = ceil_div((p.T / 64 + p.N) * heads, 2 * slots);
+    return (int)(64 * (m < 4 ? (whole < 4 ? whole : 4) : (m > whole ? whole : m)));
+  }
+  const int64_t chains = p.N * heads;
+  int64_t best = whole, least = ceil_div(chains, slots) * (whole + 2) * 2;
+  for (int64_t n = 2; n <= 64 && 4 * n <= whole + 3; ++n) {
+    const int64_t m = ceil_div(whole, n), cut = ceil_div(whole, m);
+    const int64_t cost = (m + 2) * (2 * ceil_div(chains * cut, slots) + ceil_div(chains * (cut - 1), slots));
+    if (cost < least) least = cost, best = m;
+  }
+  return (int)(64 * best);
 }
 
 size_t decays_bytes(const gdn_linear_problem& p) {

@@ -31,6 +31,11 @@ struct TcParams {
   float scale;
 };
 
+// The two bf16 values of a word.
+__device__ __forceinline__ float2 halves(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 // a and b as sums of two bf16 values each, packed.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16(a, b);

@@ -41,9 +41,9 @@ struct Map {
   // rows 64..127 of a 64-row A tile are read (and ignored): they stay inside
   static constexpr uint32_t kEnd = X + 32768 > OS + 16384 ? X + 32768 : OS + 16384;
   static constexpr uint32_t Misc = Tail < kEnd ? kEnd : Tail;
-  static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512;   // a chunk's decays, as they lie in memory
-  static constexpr uint32_t Bar = Misc + 768, Flags = Misc + 832;
-  static constexpr uint32_t Used = Misc + 896;
+  static constexpr uint32_t Gam = Misc;   // a chunk's decays, as they lie in memory: gam, down, up; two chunks'
+  static constexpr uint32_t Bar = Misc + 1536, Flags = Misc + 1600;
+  static constexpr uint32_t Used = Misc + 1664;
   static constexpr uint32_t Bytes = Used + 1024;
   static constexpr int Cols = KD + 128 <= 256 ? 256 : 512;        // TMEM: U^T, Q K^T / OP^T, OQ^T
   static constexpr int Ctas = KD == 256 ? 1 : 2;
@@ -59,8 +59,8 @@ __device__ __forceinline__ void store32(float* p, const float* v) {
 // V'' = diag(down) V in three terms (packed pairs throughout: a chunk's instructions bound the kernel): a thread takes
 // 8 columns of a row at a time, units [u, end) in steps of n; zeros where down is 0.
 template <int VD>
-__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, uint32_t x3, const float* down, int u,
-                                             int end, int n) {
+__device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x, uint32_t x2, uint32_t x3,
+                                             const float* down, int u, int end, int n) {
   const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll 2
   for (; u < end; u += n) {
@@ -80,7 +80,7 @@ __device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x
       rest[i] = pack_bf16(a.x, a.y);
     }
     *reinterpret_cast<uint4*>(sm + x + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(sm + x + VD / 64 * 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(sm + x2 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     *reinterpret_cast<uint4*>(sm + x3 + off) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
   }
 }
@@ -143,10 +143,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
-  const float* gam = reinterpret_cast<const float*>(sm + M::Gam);
-  const float* down = reinterpret_cast<const float*>(sm + M::Down);
-  const float* up = reinterpret_cast<const float*>(sm + M::Up);
-  // every barrier completes one phase a chunk, and every thread that waits for it does so once a chunk, in order
+  // Every barrier completes one phase a chunk, and every thread that waits for it does so once a chunk, in order.
+  // Without outputs there is room for two chunks' loads, each with barriers of its own (bars 0, 1 and 2, 3).
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::Bar);
   uint64_t *bar_k = bars, *bar_v = bars + 1, *bar_qk = bars + 2, *bar_qs = bars + 3, *bar_pv = bars + 4,
            *bar_u = bars + 5, *bar_q = bars + 6;
@@ -190,13 +188,21 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   const uint32_t lane_off = static_cast<uint32_t>(32 * qd) << 16;
 
   bool bad = false;   // one of this thread's waits ran out
+  constexpr bool TWO = !FULL;
+  auto buffer = [&](int i) { return TWO ? i & 1 : 0; };
+  auto k_tile = [&](int i) { return M::KQ + 8192u * buffer(i); };   // the second in the place of Q
+  auto v_tile = [&](int i) { return buffer(i) ? M::X : M::V; };     // the second in the place of the state's copy
+  auto load_bar = [&](int which, int i) { return bars + which + 2 * buffer(i); };
+  auto load_no = [&](int i) { return TWO ? i >> 1 : i; };
+  auto decays_of = [&](int i) { return reinterpret_cast<const float*>(sm + M::Gam + 768 * buffer(i)); };
   auto issue_k = [&](int i) {
     const int at = chunk_at(i), t = (int)(p.tok0 + 64 * at);
-    count[0] = i + 1;
-    mbar_arrive_expect_tx(bar_k, KD / 64 * 8192 + 768);
-    bulk_load(sm + M::Gam, prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * 256, 768, bar_k);
+    uint64_t* bar = load_bar(0, i);
+    count[2 * buffer(i)] = load_no(i) + 1;
+    mbar_arrive_expect_tx(bar, KD / 64 * 8192 + 768);
+    bulk_load(sm + M::Gam + 768 * buffer(i), prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * 256, 768, bar);
 #pragma unroll
-    for (int a = 0; a < KD / 64; ++a) tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_k, 64 * a, hq, t);
+    for (int a = 0; a < KD / 64; ++a) tma_load_3d(sm + k_tile(i) + a * 16384, &tm_k, bar, 64 * a, hq, t);
   };
   auto issue_q = [&](int i) {
     const int t = (int)(p.tok0 + 64 * chunk_at(i));
@@ -207,10 +213,11 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   };
   auto issue_v = [&](int i) {
     const int t = (int)(p.tok0 + 64 * chunk_at(i));
-    count[1] = i + 1;
-    mbar_arrive_expect_tx(bar_v, VD / 64 * 8192);
+    uint64_t* bar = load_bar(1, i);
+    count[1 + 2 * buffer(i)] = load_no(i) + 1;
+    mbar_arrive_expect_tx(bar, VD / 64 * 8192);
 #pragma unroll
-    for (int a = 0; a < VD / 64; ++a) tma_load_3d(sm + M::V + a * 8192, &tm_v, bar_v, e0 + 64 * a, h, t);
+    for (int a = 0; a < VD / 64; ++a) tma_load_3d(sm + v_tile(i) + a * 8192, &tm_v, bar, e0 + 64 * a, h, t);
   };
   auto wait = [&](uint64_t* bar, int i) {
     if (!bad) bad = !mbar_wait(bar, i & 1, prm.status);
@@ -223,6 +230,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     if (FULL) issue_q(0);
     issue_k(0);
     issue_v(0);
+    if (TWO && nchunks > 1) {
+      issue_k(1);
+      issue_v(1);
+    }
   }
 
   // S^T[e = row][d = hf KH + i]
@@ -253,9 +264,12 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     if (i > 0) {
       wait(bar_u, i - 1);
       tc_fence_after();
-      if (tid == 0 && !bad) {
-        issue_k(i);         // K of the chunk before has been read
-        if (!FULL) issue_v(i);
+      if (tid == 0 && !bad) {   // the tiles of the chunk before have been read
+        if (FULL) issue_k(i);
+        if (TWO && i + 1 < nchunks) {
+          issue_k(i + 1);
+          issue_v(i + 1);
+        }
       }
 #pragma unroll
       for (int b = 0; b < KH; b += 32) {
@@ -284,17 +298,20 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       for (int b = 0; b < KH; b += 8) store32(to + b, S + b);
     }
     if (len < 64) {
-      wait(bar_k, i);
-      wait(bar_v, i);
-      zero_rows(sm + M::KQ, KD / 64, 16384, len, tid, kTcThreads);
-      zero_rows(sm + M::V, VD / 64, 8192, len, tid, kTcThreads);
+      wait(load_bar(0, i), load_no(i));
+      wait(load_bar(1, i), load_no(i));
+      zero_rows(sm + k_tile(i), KD / 64, 16384, len, tid, kTcThreads);
+      zero_rows(sm + v_tile(i), VD / 64, 8192, len, tid, kTcThreads);
     }
-    fence_proxy_async();
-    tc_fence_before();
-    if (__syncthreads_or(bad)) break;
-    tc_fence_after();
+    if (FULL || len < 64) {
+      fence_proxy_async();
+      tc_fence_before();
+      if (__syncthreads_or(bad)) break;
+      tc_fence_after();
+    }
+    const float *gam = decays_of(i), *down = gam + 64, *up = gam + 128;
 
-    if (warp == 6 && lane == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
+    if (FULL && warp == 6 && lane == 0 && i + 1 < nchunks) {   // the next chunk's tiles on their way to L2
       const int t = (int)(p.tok0 + 64 * chunk_at(i + 1));
 #pragma unroll
       for (int a = 0; a < KD / 64; ++a) tma_prefetch_3d(&tm_k, 64 * a, hq, t);
@@ -363,13 +380,18 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       wait(bar_v, i);
       wait(bar_qs, i);   // the state's copy has been read: its place takes V''
       constexpr int n = 64 * (VD / 8);
-      if (qd < 2) weigh_values<VD>(sm, M::V, M::X, M::OS, down, 64 * hf + row, n * 5 / 8, 128);
-      else if (warp == 6) weigh_values<VD>(sm, M::V, M::X, M::OS, down, n * 13 / 16 + lane, n, 32);
-      else weigh_values<VD>(sm, M::V, M::X, M::OS, down, n * 5 / 8 + 32 * (warp == 7 ? 2 : warp - 2) + lane, n * 13 / 16, 96);
+      constexpr uint32_t x2 = M::X + VD / 64 * 8192;
+      if (qd < 2) weigh_values<VD>(sm, M::V, M::X, x2, M::OS, down, 64 * hf + row, n * 5 / 8, 128);
+      else if (warp == 6) weigh_values<VD>(sm, M::V, M::X, x2, M::OS, down, n * 13 / 16 + lane, n, 32);
+      else
+        weigh_values<VD>(sm, M::V, M::X, x2, M::OS, down, n * 5 / 8 + 32 * (warp == 7 ? 2 : warp - 2) + lane, n * 13 / 16,
+                         96);
     } else {
-      wait(bar_k, i);
-      wait(bar_v, i);
-      weigh_values<VD>(sm, M::V, M::X, M::OS, ADJ ? up : down, tid, 64 * (VD / 8), kTcThreads);
+      wait(load_bar(0, i), load_no(i));
+      wait(load_bar(1, i), load_no(i));
+      // the first term in the place of V
+      weigh_values<VD>(sm, v_tile(i), v_tile(i), M::X + VD / 64 * 8192, M::OS, ADJ ? up : down, tid, 64 * (VD / 8),
+                       kTcThreads);
     }
     dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may come in
     total *= dec;
@@ -382,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       // the third term first: its place takes o, which is written once V^T P^T, issued behind it, is complete
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        mma_bf16(R_U, dsw(s4, M::OS + s * 2048, 8192), dsw(s4, M::KQ + s * 2048, 16384), idu, s > 0);
+        mma_bf16(R_U, dsw(s4, M::OS + s * 2048, 8192), dsw(s4, k_tile(i) + s * 2048, 16384), idu, s > 0);
       if (FULL) {
         const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
 #pragma unroll
@@ -391,9 +413,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         commit(4, i);
       }
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        mma_bf16(R_U, dsw(s4, M::X + (s >> 2) * (VD / 64 * 8192) + (s & 3) * 2048, 8192),
-                 dsw(s4, M::KQ + (s & 3) * 2048, 16384), idu, 1);
+      for (int s = 0; s < 8; ++s) {
+        const uint32_t term = s >> 2 ? M::X + VD / 64 * 8192 : (FULL ? M::X : v_tile(i));
+        mma_bf16(R_U, dsw(s4, term + (s & 3) * 2048, 8192), dsw(s4, k_tile(i) + (s & 3) * 2048, 16384), idu, 1);
+      }
       commit(5, i);
       if (FULL && i + 1 < nchunks) {
         wait(bar_qk, i);   // Q has been read (QS before it)

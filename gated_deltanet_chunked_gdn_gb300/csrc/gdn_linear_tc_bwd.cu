@@ -58,12 +58,20 @@ struct GradMap {
 
 // Four values as sums of three bf16 values each, packed.
 __device__ __forceinline__ void split3(const float4& v, uint32_t (&a)[2], uint32_t (&b)[2], uint32_t (&c)[2]) {
-  const float x[4] = {v.x, v.y, v.z, v.w};
+  const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    a[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-    split2(x[2 * i] - __uint_as_float(a[i] << 16), x[2 * i + 1] - __uint_as_float(a[i] & 0xffff0000u), b[i], c[i]);
+    float2 x = i ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+    a[i] = pack_bf16(x.x, x.y);
+    x = __ffma2_rn(halves(a[i]), minus, x);
+    b[i] = pack_bf16(x.x, x.y);
+    x = __ffma2_rn(halves(b[i]), minus, x);
+    c[i] = pack_bf16(x.x, x.y);
   }
+}
+
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 template <int KD, int VD, bool SHARED>
@@ -187,6 +195,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       zero_rows(sm + M::VO + 8192, VD / 64, 16384, len, tid, kGradThreads);
       fence_proxy_async();
       if (__syncthreads_or(bad)) break;
+    }
+    if (warp == 8 && lane == 0 && more) {
+      // the next chunk's tiles and its G, whose places stay taken until this one's end, on their way to L2
+      const int next = item + gridDim.x, h1 = next % prm.Hv, hq1 = h1 / (prm.Hv / prm.Hqk);
+      const Piece p1 = piece_of(prm.pc, next / prm.Hv);
+      const int t = (int)p1.tok0;
+      bulk_prefetch(prm.decays + cell(p1, h1) * 256, 1024);
+#pragma unroll
+      for (int a = 0; a < KD / 64; ++a) {
+        tma_prefetch_3d(&tm_k, 64 * a, hq1, t);
+        tma_prefetch_3d(&tm_q, 64 * a, hq1, t);
+      }
+#pragma unroll
+      for (int a = 0; a < VD / 64; ++a) {
+        tma_prefetch_3d(&tm_v, 64 * a, h1, t);
+        tma_prefetch_3d(&tm_do, 64 * a, h1, t);
+      }
+      bulk_prefetch(prm.states + cell(p1, h1) * (KD * VD), 2 * M::kTile);
+      bulk_prefetch(prm.adjoints + cell(p1, h1) * (KD * VD), 2 * M::kTile);
     }
     // ---- products that need the loads alone
     if (tid == 0 && !bad) {
@@ -323,7 +350,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const int d0 = part * COLS;
       const float f = query ? up[tok] : down[tok];
       const uint32_t ri = (query ? I1 : I2) + lane_off + d0, rd = (query ? D1 : D2) + lane_off + d0;
-      float x = 0.f;
+      float2 x2 = make_float2(0.f, 0.f);
       const int64_t t = p.tok0 + tok;
       const int64_t to = SHARED ? (t * prm.Hv + h) * KD + d0 : (t * prm.Hqk + hq) * KD + d0;
 #pragma unroll
@@ -338,13 +365,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                                                             sw128_chunk(row, ((col & 63) >> 3) + q));
           const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x = fmaf(__uint_as_float(rw[i] << 16), vi[8 * q + 2 * i], x);
-            x = fmaf(__uint_as_float(rw[i] & 0xffff0000u), vi[8 * q + 2 * i + 1], x);
-          }
+          for (int i = 0; i < 4; ++i)
+            x2 = __ffma2_rn(halves(rw[i]), make_float2(vi[8 * q + 2 * i], vi[8 * q + 2 * i + 1]), x2);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) vd[j] = fmaf(f, vi[j], vd[j]);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 y = __ffma2_rn(make_float2(f, f), make_float2(vi[j], vi[j + 1]), make_float2(vd[j], vd[j + 1]));
+          vd[j] = y.x, vd[j + 1] = y.y;
+        }
         if (tok < len) {
           if (SHARED) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(query ? prm.dq : prm.dk) + to + b);
@@ -359,7 +387,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           }
         }
       }
-      sumx[part * 128 + row] = x * f;
+      sumx[part * 128 + row] = (x2.x + x2.y) * f;
     }
     tc_fence_before();
     if (__syncthreads_or(bad)) break;

@@ -7,35 +7,53 @@
 // forms h again from its inputs in fp32 (reading y and the residual costs what reading h would, and h may have been
 // rounded to bf16).  Statistics and sums are fp32; every output is rounded once.
 //
-// All of it is bound by HBM traffic.  A row is held in registers by TPR threads (16 or 32: several rows a CTA, sums by
-// shuffles; 128 or 512: a CTA a row), in 16-byte vectors where rows are 16-byte aligned, in single elements otherwise.
-// The gradients of the weights are summed by column: every CTA takes rows at a fixed stride, adds each into fp32
-// columns of its own (registers or shared memory), and a second launch adds the CTAs' columns in a fixed order.
+// All of it is bound by HBM traffic.  A row is held in registers by 16 or 32 lanes (several rows a CTA, sums by
+// shuffles) or by the threads of a CTA, in 16-byte vectors where rows are 16-byte aligned, in single elements
+// otherwise.  The gradients of the weights are summed by column: every CTA takes rows at a fixed stride, adds each into
+// fp32 columns of its own (registers or shared memory), and a second launch adds the CTAs' columns in a fixed order.
 #include "gdn_internal.h"
 
 namespace gdn {
 namespace {
 
+// VEC elements as they lie in memory: 16 bytes or a multiple, or one element.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f(*p);
-  } else if constexpr (sizeof(T) == 4) {
+struct Raw {
+  uint4 v[VEC * sizeof(T) / 16];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p + i);
-      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-    }
-  } else if constexpr (VEC == 4) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
-    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < (int)(VEC * sizeof(T) / 16); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x), f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z), f[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[8 * i + 2 * j] = __uint_as_float(w[j] << 16), f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f(v); }
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[VEC]) {
+  Raw<T, VEC> r;
+  r.load(p);
+  r.get(f);
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -50,148 +68,171 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-  } else if constexpr (VEC == 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
   } else {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
   }
 }
 
-// Sum over the TPR threads of a row.  Rows of more than a warp: one barrier, the warps' sums in alternating halves of
-// sm[2][32] (a half is written again only after the next sum's barrier, which every reader of it has passed).
-template <int TPR>
+// A row's threads: GROUP lanes of a warp (16 or 32), or all of a CTA (GROUP 0).
+constexpr int kGroupThreads = 256;
+
+template <int GROUP>
+__device__ __forceinline__ int row_threads() {
+  return GROUP ? GROUP : (int)blockDim.x;
+}
+
+// Sum over a row's threads.  A CTA's: one barrier, the warps' sums in alternating halves of sm[2][32] (a half is
+// written again only after the next sum's barrier, which every reader of it has passed), added in one order.
+template <int GROUP>
 __device__ __forceinline__ float row_sum(float v, float* sm, int& phase) {
 #pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (TPR > 32) {
+  for (int o = (GROUP == 16 ? 16 : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (GROUP == 0) {
     float* s = sm + 32 * phase;
     phase ^= 1;
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.f;
+    v = lane < (int)(blockDim.x >> 5) ? s[lane] : 0.f;
 #pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) v += s[i];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
   return v;
 }
 
-constexpr int kBlock(int TPR) { return TPR <= 32 ? 256 : TPR; }
-
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
+// 1 / (1 + e^-z) by the exponential and reciprocal units: within 2^-21 + |z| 2^-24 of it, relatively; far out it is 0
+// or 1.  (expf and a division take three times the instructions and would bound the gated norm.)
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 // ------------------------------------------------------------- gated norm
-template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(kBlock(TPR)) gated_fwd_kernel(const T* __restrict__ x, int64_t ldx,
-                                                                const T* __restrict__ z, int64_t ldz,
-                                                                const float* __restrict__ w, int rows, int H, int V,
-                                                                float eps, T* __restrict__ y,
-                                                                float* __restrict__ rstd) {
+template <typename T, int VEC, int NV, int GROUP>
+__global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) gated_fwd_kernel(
+    const T* __restrict__ x, int64_t ldx, const T* __restrict__ z, int64_t ldz, const float* __restrict__ w, int rows,
+    int H, int V, float eps, T* __restrict__ y, float* __restrict__ rstd) {
   __shared__ float sm[64];
   int phase = 0;
-  constexpr int RPB = kBlock(TPR) / TPR;
-  const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const int tpr = row_threads<GROUP>(), rpb = GROUP ? kGroupThreads / GROUP : 1;
+  const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * rpb + (GROUP ? threadIdx.x / GROUP : 0);
   const bool live = row < rows;
   const int64_t token = live ? (int)row / H : 0, head = live ? (int)row - token * H : 0;
   const T* xp = x + token * ldx + head * V;
   const T* zp = z ? z + token * ldz + head * V : nullptr;
-  float a[NV][VEC], b[NV][VEC], c[NV][VEC];
+  float a[NV][VEC];
+  Raw<T, VEC> b[NV];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
+    const int e = (i * tpr + t) * VEC;
     const bool in = live && e < V;
     if (in) {
       load_vec<T, VEC>(xp + e, a[i]);
-      load_vec<float, VEC>(w + e, c[i]);
-      if (zp) load_vec<T, VEC>(zp + e, b[i]);
+      if (zp) b[i].load(zp + e);
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) ss += in ? a[i][j] * a[i][j] : 0.f;
   }
-  const float r = rsqrtf(row_sum<TPR>(ss, sm, phase) / V + eps);
+  const float r = rsqrtf(row_sum<GROUP>(ss, sm, phase) / V + eps);
   if (!live) return;
   if (rstd && t == 0) rstd[row] = r;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
+    const int e = (i * tpr + t) * VEC;
     if (e >= V) continue;
+    float c[VEC], g[VEC];
+    load_vec<float, VEC>(w + e, c);
+    if (zp) b[i].get(g);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float u = a[i][j] * r * c[i][j];
-      a[i][j] = zp ? u * (b[i][j] * sigmoid_f(b[i][j])) : u;
+      const float u = a[i][j] * r * c[j];
+      a[i][j] = zp ? u * (g[j] * sigmoid_f(g[j])) : u;
     }
     store_vec<T, VEC>(y + row * V + e, a[i]);
   }
 }
 
-template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(kBlock(TPR)) gated_bwd_kernel(const T* __restrict__ x, int64_t ldx,
-                                                                const T* __restrict__ z, int64_t ldz,
-                                                                const float* __restrict__ w,
-                                                                const float* __restrict__ rstd,
-                                                                const T* __restrict__ dy, int rows, int H, int V,
-                                                                T* __restrict__ dx, T* __restrict__ dz,
-                                                                float* __restrict__ part) {
+template <typename T, int VEC, int NV, int GROUP>
+__global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) gated_bwd_kernel(
+    const T* __restrict__ x, int64_t ldx, const T* __restrict__ z, int64_t ldz, const float* __restrict__ w,
+    const float* __restrict__ rstd, const T* __restrict__ dy, int rows, int H, int V, T* __restrict__ dx,
+    T* __restrict__ dz, float* __restrict__ part) {
   __shared__ float sm[64];
   extern __shared__ float cols[];   // [RPB][V]
   int phase = 0;
-  constexpr int RPB = kBlock(TPR) / TPR;
-  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int tpr = row_threads<GROUP>();
+  constexpr int RPB = GROUP ? kGroupThreads / GROUP : 1;
+  const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x, grp = GROUP ? threadIdx.x / GROUP : 0;
   float dw[NV][VEC], wv[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
+    const int e = (i * tpr + t) * VEC;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[i][j] = 0.f, wv[i][j] = 0.f;
     if (e < V) load_vec<float, VEC>(w + e, wv[i]);
   }
-  // whole groups of RPB rows: every thread of a row's warp takes part in its sums
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += (int64_t)gridDim.x * RPB) {
-    const int64_t row = base + grp;
-    const bool live = row < rows;
-    const int64_t token = live ? (int)row / H : 0, head = live ? (int)row - token * H : 0;
-    const T* xp = x + token * ldx + head * V;
-    const T* zp = z ? z + token * ldz + head * V : nullptr;
-    const float r = live ? rstd[row] : 0.f;
-    float xh[NV][VEC], d[NV][VEC], zz[NV][VEC];
-    float s = 0.f;
+  constexpr bool AHEAD = NV * VEC <= 8;   // rows that leave registers for the next one's loads
+  Raw<T, VEC> nx[NV], nd[NV], nz[NV];
+  float nr = 0.f;
+  auto fetch = [&](int64_t row) {
+    const int64_t token = (int)row / H, head = (int)row - token * H;
+    nr = rstd[row];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
+      if (e < V) {
+        nx[i].load(x + token * ldx + head * V + e);
+        nd[i].load(dy + row * V + e);
+        if (z) nz[i].load(z + token * ldz + head * V + e);
+      }
+    }
+  };
+  if (AHEAD && (int64_t)blockIdx.x * RPB + grp < rows) fetch((int64_t)blockIdx.x * RPB + grp);
+  // whole groups of RPB rows: every thread of a row's warp takes part in its sums
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step) {
+    const int64_t row = base + grp;
+    const bool live = row < rows;
+    if (!AHEAD && live) fetch(row);
+    const float r = live ? nr : 0.f;
+    float xh[NV][VEC], d[NV][VEC], zz[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
       if (live && e < V) {
-        load_vec<T, VEC>(xp + e, xh[i]);
-        load_vec<T, VEC>(dy + row * V + e, d[i]);
-        if (zp) load_vec<T, VEC>(zp + e, zz[i]);
+        nx[i].get(xh[i]);
+        nd[i].get(d[i]);
+        if (z) nz[i].get(zz[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) xh[i][j] = 0.f, d[i][j] = 0.f, zz[i][j] = 0.f;
       }
     }
+    if (AHEAD && row + step < rows) fetch(row + step);
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float h = xh[i][j] * r;
         xh[i][j] = h;
         float du = d[i][j];
-        if (zp) {
+        if (z) {
           const float zv = zz[i][j], sg = sigmoid_f(zv);
-          zz[i][j] = du * h * wv[i][j] * (sg * (1.f + zv * (1.f - sg)));
+          zz[i][j] = du * h * wv[i][j] * (sg * fmaf(zv, 1.f - sg, 1.f));
           du *= zv * sg;
         }
-        dw[i][j] += du * h;
+        dw[i][j] = fmaf(du, h, dw[i][j]);
         d[i][j] = du * wv[i][j];
-        s += d[i][j] * h;
+        s = fmaf(d[i][j], h, s);
       }
-      if (zp && live && e < V) store_vec<T, VEC>(dz + row * V + e, zz[i]);
+      if (z && live && e < V) store_vec<T, VEC>(dz + row * V + e, zz[i]);
     }
-    const float m = row_sum<TPR>(s, sm, phase) / V;
+    const float m = row_sum<GROUP>(s, sm, phase) / V;
     if (live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = (i * TPR + t) * VEC;
+        const int e = (i * tpr + t) * VEC;
         if (e >= V) continue;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) d[i][j] = r * (d[i][j] - xh[i][j] * m);
@@ -199,118 +240,197 @@ __global__ void __launch_bounds__(kBlock(TPR)) gated_bwd_kernel(const T* __restr
       }
     }
   }
+  if constexpr (GROUP == 0) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
-    if (e < V) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) cols[grp * V + e + j] = dw[i][j];
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e < V) store_vec<float, VEC>(part + (int64_t)blockIdx.x * V + e, dw[i]);
     }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < V; e += kBlock(TPR)) {
-    float s = 0.f;
+  } else {
 #pragma unroll
-    for (int g = 0; g < RPB; ++g) s += cols[g * V + e];
-    part[(int64_t)blockIdx.x * V + e] = s;
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e < V) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) cols[grp * V + e + j] = dw[i][j];
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < V; e += kGroupThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < RPB; ++g) s += cols[g * V + e];
+      part[(int64_t)blockIdx.x * V + e] = s;
+    }
   }
 }
 
 // ---------------------------------------------------------- residual norm
-// gate: 0 none, 1 a vector of D fp32, 2 a value of type T for every element
-template <typename T, typename R, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(kBlock(TPR)) residual_fwd_kernel(
+// gate: 0 none, 1 a vector of D fp32, 2 a value of type T for every element.  Rows of up to 8 elements a thread keep
+// the weights in registers and the next row's loads in flight.
+template <typename T, typename R, int VEC, int NV, int GROUP>
+__global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ pw,
     const void* __restrict__ gate, int gmode, float scale, const float* __restrict__ w, int rows, int D, float eps,
     R* __restrict__ hout, T* __restrict__ nout, float* __restrict__ rstd) {
   __shared__ float sm[64];
   int phase = 0;
-  constexpr int RPB = kBlock(TPR) / TPR;
-  const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool live = row < rows;
-  float a[NV][VEC], b[NV][VEC];
-  float ss = 0.f;
+  constexpr bool KEEP = NV * VEC <= 8;
+  constexpr int KV = KEEP ? NV : 1;
+  const int tpr = row_threads<GROUP>();
+  constexpr int RPB = GROUP ? kGroupThreads / GROUP : 1;
+  const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x, grp = GROUP ? threadIdx.x / GROUP : 0;
+  float kp[KV][VEC], kg[KV][VEC], kw[KV][VEC];
+  if constexpr (KEEP) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
-    const bool in = live && e < D;
-    if (in) {
-      load_vec<T, VEC>(y + row * ldy + e, a[i]);
-      load_vec<R, VEC>(res + row * D + e, b[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e >= D) continue;
+      if (pw) load_vec<float, VEC>(pw + e, kp[i]);
+      if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, kg[i]);
+      if (w) load_vec<float, VEC>(w + e, kw[i]);
     }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) ss += in ? a[i][j] * a[i][j] : 0.f;
   }
-  float r1 = 1.f;
-  if (pw) r1 = rsqrtf(row_sum<TPR>(ss, sm, phase) / D + eps);
-  ss = 0.f;
+  Raw<T, VEC> ny[NV], ng[NV];
+  Raw<R, VEC> nr[NV];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
-    if (!live || e >= D) continue;
-    float f[VEC];
-    if (pw) {
-      load_vec<float, VEC>(pw + e, f);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r1 * f[j];
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e < D) {
+        ny[i].load(y + row * ldy + e);
+        nr[i].load(res + row * D + e);
+        if (gmode == 2) ng[i].load(static_cast<const T*>(gate) + row * D + e);
+      }
     }
-    if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
-    if (gmode == 2) load_vec<T, VEC>(static_cast<const T*>(gate) + row * D + e, f);
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  if (KEEP && (int64_t)blockIdx.x * RPB + grp < rows) fetch((int64_t)blockIdx.x * RPB + grp);
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step) {
+    const int64_t row = base + grp;
+    const bool live = row < rows;
+    if (!KEEP && live) fetch(row);
+    float a[NV][VEC];
+    Raw<R, VEC> cr[NV];
+    Raw<T, VEC> cg[NV];
+    float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float u = gmode ? a[i][j] * f[j] : a[i][j];
-      a[i][j] = fmaf(scale, u, b[i][j]);
-      ss += a[i][j] * a[i][j];
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      const bool in = live && e < D;
+      ny[i].get(a[i]);
+      cr[i] = nr[i];
+      cg[i] = ng[i];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) ss += in ? a[i][j] * a[i][j] : 0.f;
     }
-    store_vec<R, VEC>(hout + row * D + e, a[i]);
-  }
-  float r2 = 1.f;
-  if (w) {
-    r2 = rsqrtf(row_sum<TPR>(ss, sm, phase) / D + eps);
-    if (live) {
+    if (KEEP && row + step < rows) fetch(row + step);
+    float r1 = 1.f;
+    if (pw) r1 = rsqrtf(row_sum<GROUP>(ss, sm, phase) / D + eps);
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (!live || e >= D) continue;
+      float f[VEC], b[VEC];
+      if (pw) {
+        if constexpr (!KEEP) load_vec<float, VEC>(pw + e, f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r1 * (KEEP ? kp[KEEP ? i : 0][j] : f[j]);
+      }
+      if (gmode == 1) {
+        if constexpr (!KEEP) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[i][j] *= KEEP ? kg[KEEP ? i : 0][j] : f[j];
+      }
+      if (gmode == 2) {
+        cg[i].get(f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[i][j] *= f[j];
+      }
+      cr[i].get(b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        a[i][j] = fmaf(scale, a[i][j], b[j]);
+        ss += a[i][j] * a[i][j];
+      }
+      store_vec<R, VEC>(hout + row * D + e, a[i]);
+    }
+    float r2 = 1.f;
+    if (w) {
+      r2 = rsqrtf(row_sum<GROUP>(ss, sm, phase) / D + eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = (i * TPR + t) * VEC;
-        if (e >= D) continue;
+        const int e = (i * tpr + t) * VEC;
+        if (!live || e >= D) continue;
         float f[VEC];
-        load_vec<float, VEC>(w + e, f);
+        if constexpr (!KEEP) load_vec<float, VEC>(w + e, f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r2 * f[j];
+        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r2 * (KEEP ? kw[KEEP ? i : 0][j] : f[j]);
         store_vec<T, VEC>(nout + row * D + e, a[i]);
       }
     }
+    if (rstd && live && t == 0) rstd[2 * row] = r1, rstd[2 * row + 1] = r2;
   }
-  if (rstd && live && t == 0) rstd[2 * row] = r1, rstd[2 * row + 1] = r2;
 }
 
-// cols (shared): [RPB][3][D] sums of dweight, dpost_weight, dgate; a thread adds to columns that no other thread of
-// its row touches
-template <typename T, typename R, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(kBlock(TPR)) residual_bwd_kernel(
+// Column sums of dweight, dpost_weight and dgate: in registers for rows of up to 8 elements a thread, else in shared
+// memory ([RPB][3][D]; a thread adds to columns that no other thread of its row touches).
+template <typename T, typename R, int VEC, int NV, int GROUP>
+__global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ rstd,
     const R* __restrict__ dh, const T* __restrict__ dn, const float* __restrict__ pw, const void* __restrict__ gate,
     int gmode, float scale, const float* __restrict__ w, int rows, int D, T* __restrict__ dy, R* __restrict__ dres,
     T* __restrict__ dgate, float* __restrict__ part) {
   __shared__ float sm[64];
-  extern __shared__ float cols[];
+  extern __shared__ __align__(16) float cols[];
   int phase = 0;
-  constexpr int RPB = kBlock(TPR) / TPR;
-  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  constexpr bool KEEP = NV * VEC <= 8;
+  constexpr int KV = KEEP ? NV : 1;
+  const int tpr = row_threads<GROUP>();
+  constexpr int RPB = GROUP ? kGroupThreads / GROUP : 1;
+  const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x, grp = GROUP ? threadIdx.x / GROUP : 0;
   float* cw = cols + (int64_t)grp * 3 * D;
   float* cp = cw + D;
   float* cg = cp + D;
-  for (int e = threadIdx.x; e < RPB * 3 * D; e += kBlock(TPR)) cols[e] = 0.f;
-  __syncthreads();
+  float aw[KV][VEC], ap[KV][VEC], ag[KV][VEC];   // KEEP: the sums
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) aw[i][j] = ap[i][j] = ag[i][j] = 0.f;
+  } else {
+    for (int e = threadIdx.x; e < RPB * 3 * D; e += blockDim.x) cols[e] = 0.f;
+    __syncthreads();
+  }
+  auto add = [&](float* to, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+      *to += v[0];
+    } else if ((D & 3) == 0) {   // 16-byte aligned columns
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4) {
+        float4 x = *reinterpret_cast<float4*>(to + j);
+        x.x += v[j], x.y += v[j + 1], x.z += v[j + 2], x.w += v[j + 3];
+        *reinterpret_cast<float4*>(to + j) = x;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) to[j] += v[j];
+    }
+  };
+  auto gate_of = [&](int64_t row, int e, float (&f)[VEC]) {
+    if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
+    if (gmode == 2) load_vec<T, VEC>(static_cast<const T*>(gate) + row * D + e, f);
+  };
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += (int64_t)gridDim.x * RPB) {
     const int64_t row = base + grp;
     const bool live = row < rows;
     const float r1 = live ? rstd[2 * row] : 0.f, r2 = live ? rstd[2 * row + 1] : 0.f;
-    float yh[NV][VEC], d[NV][VEC], hh[NV][VEC], aa[NV][VEC];
+    float yh[NV][VEC], d[NV][VEC], hh[NV][VEC], aa[NV][VEC], gt[KV][VEC];
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (!live || e >= D) continue;
       load_vec<T, VEC>(y + row * ldy + e, yh[i]);
       if (dh) {
@@ -319,38 +439,44 @@ __global__ void __launch_bounds__(kBlock(TPR)) residual_bwd_kernel(
 #pragma unroll
         for (int j = 0; j < VEC; ++j) d[i][j] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) yh[i][j] *= r1;
       if (w) {
         load_vec<R, VEC>(res + row * D + e, hh[i]);
         load_vec<T, VEC>(dn + row * D + e, aa[i]);
       }
+      if constexpr (KEEP) gate_of(row, e, gt[i]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) yh[i][j] *= r1;
     }
     if (w) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = (i * TPR + t) * VEC;
+        const int e = (i * tpr + t) * VEC;
         if (!live || e >= D) continue;
         float p[VEC], f[VEC], wv[VEC];
         if (pw) load_vec<float, VEC>(pw + e, p);
-        if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
-        if (gmode == 2) load_vec<T, VEC>(static_cast<const T*>(gate) + row * D + e, f);
+        if constexpr (!KEEP) gate_of(row, e, f);
         load_vec<float, VEC>(w + e, wv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           float u = pw ? yh[i][j] * p[j] : yh[i][j];
-          if (gmode) u *= f[j];
+          if (gmode) u *= KEEP ? gt[KEEP ? i : 0][j] : f[j];
           const float h = fmaf(scale, u, hh[i][j]) * r2;
           hh[i][j] = h;
-          cw[e + j] += aa[i][j] * h;
+          p[j] = aa[i][j] * h;
           aa[i][j] *= wv[j];
-          s += aa[i][j] * h;
+          s = fmaf(aa[i][j], h, s);
+        }
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) aw[i][j] += p[j];
+        } else {
+          add(cw + e, p);
         }
       }
-      const float m = row_sum<TPR>(s, sm, phase) / D;
+      const float m = row_sum<GROUP>(s, sm, phase) / D;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = (i * TPR + t) * VEC;
+        const int e = (i * tpr + t) * VEC;
         if (!live || e >= D) continue;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) d[i][j] += r2 * (aa[i][j] - hh[i][j] * m);
@@ -359,33 +485,38 @@ __global__ void __launch_bounds__(kBlock(TPR)) residual_bwd_kernel(
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (!live || e >= D) continue;
       store_vec<R, VEC>(dres + row * D + e, d[i]);
-      float p[VEC], f[VEC], dg[VEC];
+      float p[VEC], f[VEC], dg[VEC], dp[VEC];
       if (pw) load_vec<float, VEC>(pw + e, p);
-      if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
-      if (gmode == 2) load_vec<T, VEC>(static_cast<const T*>(gate) + row * D + e, f);
+      if constexpr (!KEEP) gate_of(row, e, f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         float du = scale * d[i][j];
         dg[j] = du * (pw ? yh[i][j] * p[j] : yh[i][j]);
-        if (gmode == 1) cg[e + j] += dg[j];
-        if (gmode) du *= f[j];
+        if (gmode) du *= KEEP ? gt[KEEP ? i : 0][j] : f[j];
+        dp[j] = du * yh[i][j];
         if (pw) {
-          cp[e + j] += du * yh[i][j];
           du *= p[j];
-          s += du * yh[i][j];
+          s = fmaf(du, yh[i][j], s);
         }
         d[i][j] = du;
       }
       if (gmode == 2) store_vec<T, VEC>(dgate + row * D + e, dg);
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) ag[i][j] += dg[j], ap[i][j] += dp[j];
+      } else {
+        if (gmode == 1) add(cg + e, dg);
+        if (pw) add(cp + e, dp);
+      }
     }
     float m = 0.f;
-    if (pw) m = row_sum<TPR>(s, sm, phase) / D;
+    if (pw) m = row_sum<GROUP>(s, sm, phase) / D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (!live || e >= D) continue;
       if (pw) {
 #pragma unroll
@@ -394,8 +525,20 @@ __global__ void __launch_bounds__(kBlock(TPR)) residual_bwd_kernel(
       store_vec<T, VEC>(dy + row * D + e, d[i]);
     }
   }
+  if constexpr (KEEP) {
+    // through shared memory where rows share a CTA; a CTA of one row writes its sums as they are
+    float* to = GROUP ? cw : part + (int64_t)blockIdx.x * 3 * D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e >= D) continue;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) to[e + j] = aw[i][j], to[D + e + j] = ap[i][j], to[2 * D + e + j] = ag[i][j];
+    }
+    if constexpr (GROUP == 0) return;
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < 3 * D; e += kBlock(TPR)) {
+  for (int e = threadIdx.x; e < 3 * D; e += blockDim.x) {
     float s = 0.f;
 #pragma unroll
     for (int g = 0; g < RPB; ++g) s += cols[(int64_t)g * 3 * D + e];
@@ -423,26 +566,40 @@ __global__ void __launch_bounds__(256) columns_kernel(const float* __restrict__ 
   }
 }
 
-// Threads a row and vectors a thread: the fewest threads whose registers hold the row at up to 16 elements a thread
-// (32 in the widest rows).
+// How a row of D elements is held: vectors of `vec` elements, nv of them a thread; its threads are `group` lanes (16 or
+// 32) or, for group 0, the `threads` of a CTA: as few vectors a thread as 512 threads can hold.
 struct Shape {
-  int vec, tpr, nv;
+  int vec, group, nv, threads;
+  int rpb() const { return group ? kGroupThreads / group : 1; }
 };
 
 Shape shape_of(int D, int vec) {
-  Shape s{vec, 0, 0};
-  const int per = vec == 1 ? 8 : 16;
-  s.tpr = D <= 16 * vec && vec > 1 ? 16 : (D <= 32 * per ? 32 : (D <= 128 * per ? 128 : 512));
-  const int need = (int)ceil_div(D, (int64_t)s.tpr * vec);
-  s.nv = 1;
-  while (s.nv < need) s.nv *= 2;
+  const int vectors = (int)ceil_div(D, vec), most = vec == 1 ? 8 : 16 / vec;   // vectors a lane
+  Shape s{vec, 0, 1, kGroupThreads};
+  if (vec > 1 && vectors <= 16) {
+    s.group = 16;
+  } else if (vectors <= 32 * most) {
+    s.group = 32;
+    while (32 * s.nv < vectors) s.nv *= 2;
+  } else {
+    while (512 * s.nv < vectors) s.nv *= 2;
+    s.threads = 32 * (int)ceil_div(vectors, 32 * s.nv);
+  }
   return s;
 }
 
-// CTAs of a backward pass: enough to fill the device, each with its own columns
-int bwd_blocks(int64_t rows, int rpb, int64_t smem) {
-  const int64_t per = smem > 100 * 1024 ? 1 : (smem > 50 * 1024 ? 2 : 4);
-  const int64_t need = ceil_div(rows, rpb), most = per * sm_count();
+// CTAs of a pass whose CTAs take rows at a fixed stride: what the device holds at once, each of the backward's with
+// columns of its own (kMostCtas an SM at most).
+constexpr int kMostCtas = 8;
+
+template <typename K>
+int resident_ctas(K kernel, int threads, size_t smem, int64_t rows, int rpb) {
+  const int64_t need = ceil_div(rows, rpb);
+  if (need <= sm_count()) return (int)need;
+  int per = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess || per < 1) per = 1;
+  if (per > kMostCtas) per = kMostCtas;
+  const int64_t most = (int64_t)per * sm_count();
   return (int)(need < most ? need : most);
 }
 
@@ -454,25 +611,24 @@ bool allow_smem(K kernel, size_t bytes) {
 }
 
 // The shapes that shape_of gives, and no others.
-#define GDN_NORM_CASE(VEC, NV, TPR, F)                                                                  \
-  case NV:                                                                                              \
-    if constexpr ((NV) * (VEC) <= ((TPR) == 512 ? 32 : ((VEC) == 1 ? 8 : 16))) F(VEC, NV, TPR);         \
+#define GDN_NORM_CASE(VEC, NV, GROUP, F)                                                                       \
+  case NV:                                                                                                     \
+    if constexpr ((NV) * (VEC) <= ((GROUP) == 0 ? 32 : ((VEC) == 1 ? 8 : 16))) F(VEC, NV, GROUP);              \
     break;
-#define GDN_NORM_NV(VEC, TPR, F)                                                                        \
-  switch (s.nv) {                                                                                       \
-    GDN_NORM_CASE(VEC, 1, TPR, F)                                                                       \
-    GDN_NORM_CASE(VEC, 2, TPR, F)                                                                       \
-    GDN_NORM_CASE(VEC, 4, TPR, F)                                                                       \
-    GDN_NORM_CASE(VEC, 8, TPR, F)                                                                       \
-    GDN_NORM_CASE(VEC, 16, TPR, F)                                                                      \
-    GDN_NORM_CASE(VEC, 32, TPR, F)                                                                      \
+#define GDN_NORM_NV(VEC, GROUP, F)                                                                             \
+  switch (s.nv) {                                                                                              \
+    GDN_NORM_CASE(VEC, 1, GROUP, F)                                                                            \
+    GDN_NORM_CASE(VEC, 2, GROUP, F)                                                                            \
+    GDN_NORM_CASE(VEC, 4, GROUP, F)                                                                            \
+    GDN_NORM_CASE(VEC, 8, GROUP, F)                                                                            \
+    GDN_NORM_CASE(VEC, 16, GROUP, F)                                                                           \
+    GDN_NORM_CASE(VEC, 32, GROUP, F)                                                                           \
   }
-#define GDN_NORM_TPR(VEC, F)                                                                            \
-  switch (s.tpr) {                                                                                      \
-    case 16: if constexpr (VEC > 1) F(VEC, 1, 16); break;                                               \
-    case 32: GDN_NORM_NV(VEC, 32, F) break;                                                             \
-    case 128: GDN_NORM_NV(VEC, 128, F) break;                                                           \
-    case 512: GDN_NORM_NV(VEC, 512, F) break;                                                           \
+#define GDN_NORM_SHAPE(VEC, F)                                                                                 \
+  switch (s.group) {                                                                                           \
+    case 16: if constexpr (VEC > 1) F(VEC, 1, 16); break;                                                      \
+    case 32: GDN_NORM_NV(VEC, 32, F) break;                                                                    \
+    default: GDN_NORM_NV(VEC, 0, F)                                                                            \
   }
 
 bool rows16(const void* p, int64_t row_bytes) {
@@ -486,14 +642,13 @@ gdn_status gated_fwd_t(const T* x, int64_t ldx, const T* z, int64_t ldz, const f
   const int es = sizeof(T), rows = tokens * H;
   const bool wide = rows16(x, ldx * es) && rows16(z, ldz * es) && rows16(w, 0) && rows16(y, (int64_t)V * es);
   const Shape s = shape_of(V, wide ? VW : 1);
-  const int rpb = s.tpr <= 32 ? 256 / s.tpr : 1;
-  const unsigned grid = (unsigned)ceil_div(rows, rpb);
-#define GDN_F(VEC, NV, TPR)                                                                                          \
-  gated_fwd_kernel<T, VEC, NV, TPR><<<grid, kBlock(TPR), 0, st>>>(x, ldx, z, ldz, w, rows, H, V, eps, y, rstd)
+  const unsigned grid = (unsigned)ceil_div(rows, s.rpb());
+#define GDN_F(VEC, NV, GROUP)                                                                                         \
+  gated_fwd_kernel<T, VEC, NV, GROUP><<<grid, s.threads, 0, st>>>(x, ldx, z, ldz, w, rows, H, V, eps, y, rstd)
   if (wide) {
-    GDN_NORM_TPR(VW, GDN_F)
+    GDN_NORM_SHAPE(VW, GDN_F)
   } else {
-    GDN_NORM_TPR(1, GDN_F)
+    GDN_NORM_SHAPE(1, GDN_F)
   }
 #undef GDN_F
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -507,23 +662,21 @@ gdn_status gated_bwd_t(const T* x, int64_t ldx, const T* z, int64_t ldz, const f
   const bool wide = rows16(x, ldx * es) && rows16(z, ldz * es) && rows16(w, 0) && rows16(dy, (int64_t)V * es) &&
                     rows16(dx, 0) && rows16(dz, 0);
   const Shape s = shape_of(V, wide ? VW : 1);
-  const int rpb = s.tpr <= 32 ? 256 / s.tpr : 1;
-  const size_t smem = sizeof(float) * rpb * V;
-  const int grid = bwd_blocks(rows, rpb, smem);
-  bool ok = true;
-#define GDN_F(VEC, NV, TPR)                                                                                         \
+  const size_t smem = s.group ? sizeof(float) * s.rpb() * V : 0;
+  int grid = 0;
+#define GDN_F(VEC, NV, GROUP)                                                                                       \
   {                                                                                                                 \
-    auto kern = gated_bwd_kernel<T, VEC, NV, TPR>;                                                                  \
-    ok = allow_smem(kern, smem);                                                                                    \
-    if (ok) kern<<<grid, kBlock(TPR), smem, st>>>(x, ldx, z, ldz, w, rstd, dy, rows, H, V, dx, dz, part);           \
+    auto kern = gated_bwd_kernel<T, VEC, NV, GROUP>;                                                                \
+    grid = resident_ctas(kern, s.threads, smem, rows, s.rpb());                                                     \
+    kern<<<grid, s.threads, smem, st>>>(x, ldx, z, ldz, w, rstd, dy, rows, H, V, dx, dz, part);                     \
   }
   if (wide) {
-    GDN_NORM_TPR(VW, GDN_F)
+    GDN_NORM_SHAPE(VW, GDN_F)
   } else {
-    GDN_NORM_TPR(1, GDN_F)
+    GDN_NORM_SHAPE(1, GDN_F)
   }
 #undef GDN_F
-  if (!ok || cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   columns_kernel<<<(unsigned)ceil_div(V, 8), 256, 0, st>>>(part, grid, V, 1, dw, nullptr, nullptr);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -537,15 +690,16 @@ gdn_status residual_fwd_t(const T* y, int64_t ldy, const R* res, const float* pw
   const bool wide = rows16(y, ldy * (int)sizeof(T)) && rows16(res, rr) && rows16(pw, 0) && rows16(w, 0) &&
                     rows16(gate, gmode == 2 ? rt : 0) && rows16(h, rr) && rows16(n, rt) && rt % 16 == 0;
   const Shape s = shape_of(D, wide ? VW : 1);
-  const int rpb = s.tpr <= 32 ? 256 / s.tpr : 1;
-  const unsigned grid = (unsigned)ceil_div(rows, rpb);
-#define GDN_F(VEC, NV, TPR)                                                                                    \
-  residual_fwd_kernel<T, R, VEC, NV, TPR><<<grid, kBlock(TPR), 0, st>>>(y, ldy, res, pw, gate, gmode, scale, w, rows, \
-                                                                        D, eps, h, n, rstd)
+#define GDN_F(VEC, NV, GROUP)                                                                                     \
+  {                                                                                                                 \
+    auto kern = residual_fwd_kernel<T, R, VEC, NV, GROUP>;                                                          \
+    kern<<<resident_ctas(kern, s.threads, 0, rows, s.rpb()), s.threads, 0, st>>>(                                   \
+        y, ldy, res, pw, gate, gmode, scale, w, rows, D, eps, h, n, rstd);                                          \
+  }
   if (wide) {
-    GDN_NORM_TPR(VW, GDN_F)
+    GDN_NORM_SHAPE(VW, GDN_F)
   } else {
-    GDN_NORM_TPR(1, GDN_F)
+    GDN_NORM_SHAPE(1, GDN_F)
   }
 #undef GDN_F
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -561,22 +715,22 @@ gdn_status residual_bwd_t(const T* y, int64_t ldy, const R* res, const float* rs
                     rows16(pw, 0) && rows16(w, 0) && rows16(gate, gmode == 2 ? rt : 0) && rows16(dy, rt) &&
                     rows16(dres, rr) && rows16(gmode == 2 ? dgate : nullptr, rt) && rt % 16 == 0;
   const Shape s = shape_of(D, wide ? VW : 1);
-  const int rpb = s.tpr <= 32 ? 256 / s.tpr : 1;
-  const size_t smem = sizeof(float) * rpb * 3 * D;
-  const int grid = bwd_blocks(rows, rpb, smem);
+  const size_t smem = s.group || s.nv * s.vec > 8 ? sizeof(float) * s.rpb() * 3 * D : 0;
+  int grid = 0;
   bool ok = true;
-#define GDN_F(VEC, NV, TPR)                                                                                        \
-  {                                                                                                                \
-    auto kern = residual_bwd_kernel<T, R, VEC, NV, TPR>;                                                           \
-    ok = allow_smem(kern, smem);                                                                                   \
-    if (ok)                                                                                                        \
-      kern<<<grid, kBlock(TPR), smem, st>>>(y, ldy, res, rstd, dh, dn, pw, gate, gmode, scale, w, rows, D, dy,     \
-                                            dres, gmode == 2 ? static_cast<T*>(dgate) : nullptr, part);            \
+#define GDN_F(VEC, NV, GROUP)                                                                                       \
+  {                                                                                                                 \
+    auto kern = residual_bwd_kernel<T, R, VEC, NV, GROUP>;                                                          \
+    ok = allow_smem(kern, smem);                                                                                    \
+    grid = resident_ctas(kern, s.threads, smem, rows, s.rpb());                                                     \
+    if (ok)                                                                                                         \
+      kern<<<grid, s.threads, smem, st>>>(y, ldy, res, rstd, dh, dn, pw, gate, gmode, scale, w, rows, D, dy, dres,  \
+                                          gmode == 2 ? static_cast<T*>(dgate) : nullptr, part);                     \
   }
   if (wide) {
-    GDN_NORM_TPR(VW, GDN_F)
+    GDN_NORM_SHAPE(VW, GDN_F)
   } else {
-    GDN_NORM_TPR(1, GDN_F)
+    GDN_NORM_SHAPE(1, GDN_F)
   }
 #undef GDN_F
   if (!ok || cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
@@ -589,8 +743,10 @@ gdn_status residual_bwd_t(const T* y, int64_t ldy, const R* res, const float* rs
 }  // namespace
 
 // Rows of columns that the largest grid of a backward pass writes.
-size_t gated_norm_bwd_workspace_bytes(int V) { return align_up(sizeof(float) * 4 * (size_t)sm_count() * V); }
-size_t residual_norm_bwd_workspace_bytes(int D) { return align_up(sizeof(float) * 4 * (size_t)sm_count() * 3 * D); }
+size_t gated_norm_bwd_workspace_bytes(int V) { return align_up(sizeof(float) * kMostCtas * (size_t)sm_count() * V); }
+size_t residual_norm_bwd_workspace_bytes(int D) {
+  return align_up(sizeof(float) * kMostCtas * (size_t)sm_count() * 3 * D);
+}
 
 gdn_status run_gated_norm_fwd(const void* x, int64_t ldx, const void* z, int64_t ldz, const float* w, int tokens, int H,
                               int V, gdn_dtype dt, float eps, void* y, float* rstd, cudaStream_t s) {

@@ -111,43 +111,58 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) gated_fwd_kernel(
     int H, int V, float eps, T* __restrict__ y, float* __restrict__ rstd) {
   __shared__ float sm[64];
   int phase = 0;
-  const int tpr = row_threads<GROUP>(), rpb = GROUP ? kGroupThreads / GROUP : 1;
-  const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x;
-  const int64_t row = (int64_t)blockIdx.x * rpb + (GROUP ? threadIdx.x / GROUP : 0);
-  const bool live = row < rows;
-  const int64_t token = live ? (int)row / H : 0, head = live ? (int)row - token * H : 0;
-  const T* xp = x + token * ldx + head * V;
-  const T* zp = z ? z + token * ldz + head * V : nullptr;
-  float a[NV][VEC];
-  Raw<T, VEC> b[NV];
-  float ss = 0.f;
+  constexpr bool AHEAD = NV * VEC <= 8;   // rows that leave registers for the next one's loads
+  const int tpr = row_threads<GROUP>();
+  constexpr int RPB = GROUP ? kGroupThreads / GROUP : 1;
+  const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x, grp = GROUP ? threadIdx.x / GROUP : 0;
+  Raw<T, VEC> nx[NV], nz[NV];
+  auto fetch = [&](int64_t row) {
+    const int64_t token = (int)row / H, head = (int)row - token * H;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (i * tpr + t) * VEC;
-    const bool in = live && e < V;
-    if (in) {
-      load_vec<T, VEC>(xp + e, a[i]);
-      if (zp) b[i].load(zp + e);
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e < V) {
+        nx[i].load(x + token * ldx + head * V + e);
+        if (z) nz[i].load(z + token * ldz + head * V + e);
+      }
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  if (AHEAD && (int64_t)blockIdx.x * RPB + grp < rows) fetch((int64_t)blockIdx.x * RPB + grp);
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step) {
+    const int64_t row = base + grp;
+    const bool live = row < rows;
+    if (!AHEAD && live) fetch(row);
+    float a[NV][VEC];
+    Raw<T, VEC> cz[NV];
+    float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) ss += in ? a[i][j] * a[i][j] : 0.f;
-  }
-  const float r = rsqrtf(row_sum<GROUP>(ss, sm, phase) / V + eps);
-  if (!live) return;
-  if (rstd && t == 0) rstd[row] = r;
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      const bool in = live && e < V;
+      nx[i].get(a[i]);
+      cz[i] = nz[i];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (i * tpr + t) * VEC;
-    if (e >= V) continue;
-    float c[VEC], g[VEC];
-    load_vec<float, VEC>(w + e, c);
-    if (zp) b[i].get(g);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float u = a[i][j] * r * c[j];
-      a[i][j] = zp ? u * (g[j] * sigmoid_f(g[j])) : u;
+      for (int j = 0; j < VEC; ++j) ss += in ? a[i][j] * a[i][j] : 0.f;
     }
-    store_vec<T, VEC>(y + row * V + e, a[i]);
+    if (AHEAD && row + step < rows) fetch(row + step);
+    const float r = rsqrtf(row_sum<GROUP>(ss, sm, phase) / V + eps);
+    if (!live) continue;
+    if (rstd && t == 0) rstd[row] = r;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e >= V) continue;
+      float c[VEC], g[VEC];
+      load_vec<float, VEC>(w + e, c);
+      if (z) cz[i].get(g);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float u = a[i][j] * r * c[j];
+        a[i][j] = z ? u * (g[j] * sigmoid_f(g[j])) : u;
+      }
+      store_vec<T, VEC>(y + row * V + e, a[i]);
+    }
   }
 }
 
@@ -266,32 +281,20 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) gated_bwd_kernel(
 }
 
 // ---------------------------------------------------------- residual norm
-// gate: 0 none, 1 a vector of D fp32, 2 a value of type T for every element.  Rows of up to 8 elements a thread keep
-// the weights in registers and the next row's loads in flight.
+// gate: 0 none, 1 a vector of D fp32, 2 a value of type T for every element.  Rows of up to 8 elements a thread have the
+// next row's loads in flight, and registers for two CTAs an SM.
 template <typename T, typename R, int VEC, int NV, int GROUP>
-__global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kernel(
+__global__ void __launch_bounds__(GROUP ? kGroupThreads : 512, NV * VEC <= 8 ? (GROUP ? 4 : 2) : 1) residual_fwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ pw,
     const void* __restrict__ gate, int gmode, float scale, const float* __restrict__ w, int rows, int D, float eps,
     R* __restrict__ hout, T* __restrict__ nout, float* __restrict__ rstd) {
   __shared__ float sm[64];
   int phase = 0;
-  constexpr bool KEEP = NV * VEC <= 8;
-  constexpr int KV = KEEP ? NV : 1;
+  constexpr bool AHEAD = NV * VEC <= 8;
   const int tpr = row_threads<GROUP>();
   constexpr int RPB = GROUP ? kGroupThreads / GROUP : 1;
   const int t = GROUP ? threadIdx.x % GROUP : threadIdx.x, grp = GROUP ? threadIdx.x / GROUP : 0;
-  float kp[KV][VEC], kg[KV][VEC], kw[KV][VEC];
-  if constexpr (KEEP) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = (i * tpr + t) * VEC;
-      if (e >= D) continue;
-      if (pw) load_vec<float, VEC>(pw + e, kp[i]);
-      if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, kg[i]);
-      if (w) load_vec<float, VEC>(w + e, kw[i]);
-    }
-  }
-  Raw<T, VEC> ny[NV], ng[NV];
+  Raw<T, VEC> ny[NV];
   Raw<R, VEC> nr[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -300,19 +303,17 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kern
       if (e < D) {
         ny[i].load(y + row * ldy + e);
         nr[i].load(res + row * D + e);
-        if (gmode == 2) ng[i].load(static_cast<const T*>(gate) + row * D + e);
       }
     }
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
-  if (KEEP && (int64_t)blockIdx.x * RPB + grp < rows) fetch((int64_t)blockIdx.x * RPB + grp);
+  if (AHEAD && (int64_t)blockIdx.x * RPB + grp < rows) fetch((int64_t)blockIdx.x * RPB + grp);
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step) {
     const int64_t row = base + grp;
     const bool live = row < rows;
-    if (!KEEP && live) fetch(row);
+    if (!AHEAD && live) fetch(row);
     float a[NV][VEC];
     Raw<R, VEC> cr[NV];
-    Raw<T, VEC> cg[NV];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -320,11 +321,10 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kern
       const bool in = live && e < D;
       ny[i].get(a[i]);
       cr[i] = nr[i];
-      cg[i] = ng[i];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss += in ? a[i][j] * a[i][j] : 0.f;
     }
-    if (KEEP && row + step < rows) fetch(row + step);
+    if (AHEAD && row + step < rows) fetch(row + step);
     float r1 = 1.f;
     if (pw) r1 = rsqrtf(row_sum<GROUP>(ss, sm, phase) / D + eps);
     ss = 0.f;
@@ -332,26 +332,22 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kern
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + t) * VEC;
       if (!live || e >= D) continue;
-      float f[VEC], b[VEC];
+      float f[VEC];
       if (pw) {
-        if constexpr (!KEEP) load_vec<float, VEC>(pw + e, f);
+        load_vec<float, VEC>(pw + e, f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r1 * (KEEP ? kp[KEEP ? i : 0][j] : f[j]);
+        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r1 * f[j];
       }
-      if (gmode == 1) {
-        if constexpr (!KEEP) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] *= KEEP ? kg[KEEP ? i : 0][j] : f[j];
-      }
-      if (gmode == 2) {
-        cg[i].get(f);
+      if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
+      if (gmode == 2) load_vec<T, VEC>(static_cast<const T*>(gate) + row * D + e, f);
+      if (gmode) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) a[i][j] *= f[j];
       }
-      cr[i].get(b);
+      cr[i].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        a[i][j] = fmaf(scale, a[i][j], b[j]);
+        a[i][j] = fmaf(scale, a[i][j], f[j]);
         ss += a[i][j] * a[i][j];
       }
       store_vec<R, VEC>(hout + row * D + e, a[i]);
@@ -364,9 +360,9 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kern
         const int e = (i * tpr + t) * VEC;
         if (!live || e >= D) continue;
         float f[VEC];
-        if constexpr (!KEEP) load_vec<float, VEC>(w + e, f);
+        load_vec<float, VEC>(w + e, f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r2 * (KEEP ? kw[KEEP ? i : 0][j] : f[j]);
+        for (int j = 0; j < VEC; ++j) a[i][j] = a[i][j] * r2 * f[j];
         store_vec<T, VEC>(nout + row * D + e, a[i]);
       }
     }
@@ -375,7 +371,8 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_fwd_kern
 }
 
 // Column sums of dweight, dpost_weight and dgate: in registers for rows of up to 8 elements a thread, else in shared
-// memory ([RPB][3][D]; a thread adds to columns that no other thread of its row touches).
+// memory ([RPB][3][D]; a thread adds to columns that no other thread of its row touches).  Where registers are left, the
+// next row's loads are in flight.
 template <typename T, typename R, int VEC, int NV, int GROUP>
 __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ rstd,
@@ -386,6 +383,7 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kern
   extern __shared__ __align__(16) float cols[];
   int phase = 0;
   constexpr bool KEEP = NV * VEC <= 8;
+  constexpr bool AHEAD = NV * VEC * (int)sizeof(R) <= 16;
   constexpr int KV = KEEP ? NV : 1;
   const int tpr = row_threads<GROUP>();
   constexpr int RPB = GROUP ? kGroupThreads / GROUP : 1;
@@ -422,31 +420,56 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kern
     if (gmode == 1) load_vec<float, VEC>(static_cast<const float*>(gate) + e, f);
     if (gmode == 2) load_vec<T, VEC>(static_cast<const T*>(gate) + row * D + e, f);
   };
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += (int64_t)gridDim.x * RPB) {
+  Raw<T, VEC> ny[NV], nn[NV], ng[NV];
+  Raw<R, VEC> nh[NV], ns[NV];
+  float n1 = 0.f, n2 = 0.f;
+  auto fetch = [&](int64_t row) {
+    n1 = rstd[2 * row], n2 = rstd[2 * row + 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + t) * VEC;
+      if (e >= D) continue;
+      ny[i].load(y + row * ldy + e);
+      if (dh) nh[i].load(dh + row * D + e);
+      if (w) {
+        ns[i].load(res + row * D + e);
+        nn[i].load(dn + row * D + e);
+      }
+      if (KEEP && gmode == 2) ng[i].load(static_cast<const T*>(gate) + row * D + e);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  if (AHEAD && (int64_t)blockIdx.x * RPB + grp < rows) fetch((int64_t)blockIdx.x * RPB + grp);
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step) {
     const int64_t row = base + grp;
     const bool live = row < rows;
-    const float r1 = live ? rstd[2 * row] : 0.f, r2 = live ? rstd[2 * row + 1] : 0.f;
+    if (!AHEAD && live) fetch(row);
+    const float r1 = live ? n1 : 0.f, r2 = live ? n2 : 0.f;
     float yh[NV][VEC], d[NV][VEC], hh[NV][VEC], aa[NV][VEC], gt[KV][VEC];
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + t) * VEC;
       if (!live || e >= D) continue;
-      load_vec<T, VEC>(y + row * ldy + e, yh[i]);
+      ny[i].get(yh[i]);
       if (dh) {
-        load_vec<R, VEC>(dh + row * D + e, d[i]);
+        nh[i].get(d[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) d[i][j] = 0.f;
       }
       if (w) {
-        load_vec<R, VEC>(res + row * D + e, hh[i]);
-        load_vec<T, VEC>(dn + row * D + e, aa[i]);
+        ns[i].get(hh[i]);
+        nn[i].get(aa[i]);
       }
-      if constexpr (KEEP) gate_of(row, e, gt[i]);
+      if constexpr (KEEP) {
+        if (gmode == 2) ng[i].get(gt[i]);
+        else gate_of(row, e, gt[i]);
+      }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) yh[i][j] *= r1;
     }
+    if (AHEAD && row + step < rows) fetch(row + step);
     if (w) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -526,16 +549,13 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kern
     }
   }
   if constexpr (KEEP) {
-    // through shared memory where rows share a CTA; a CTA of one row writes its sums as they are
-    float* to = GROUP ? cw : part + (int64_t)blockIdx.x * 3 * D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + t) * VEC;
       if (e >= D) continue;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) to[e + j] = aw[i][j], to[D + e + j] = ap[i][j], to[2 * D + e + j] = ag[i][j];
+      for (int j = 0; j < VEC; ++j) cw[e + j] = aw[i][j], cp[e + j] = ap[i][j], cg[e + j] = ag[i][j];
     }
-    if constexpr (GROUP == 0) return;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 3 * D; e += blockDim.x) {
@@ -642,9 +662,12 @@ gdn_status gated_fwd_t(const T* x, int64_t ldx, const T* z, int64_t ldz, const f
   const int es = sizeof(T), rows = tokens * H;
   const bool wide = rows16(x, ldx * es) && rows16(z, ldz * es) && rows16(w, 0) && rows16(y, (int64_t)V * es);
   const Shape s = shape_of(V, wide ? VW : 1);
-  const unsigned grid = (unsigned)ceil_div(rows, s.rpb());
-#define GDN_F(VEC, NV, GROUP)                                                                                         \
-  gated_fwd_kernel<T, VEC, NV, GROUP><<<grid, s.threads, 0, st>>>(x, ldx, z, ldz, w, rows, H, V, eps, y, rstd)
+#define GDN_F(VEC, NV, GROUP)                                                                                       \
+  {                                                                                                                 \
+    auto kern = gated_fwd_kernel<T, VEC, NV, GROUP>;                                                                \
+    kern<<<resident_ctas(kern, s.threads, 0, rows, s.rpb()), s.threads, 0, st>>>(x, ldx, z, ldz, w, rows, H, V, eps, \
+                                                                                 y, rstd);                          \
+  }
   if (wide) {
     GDN_NORM_SHAPE(VW, GDN_F)
   } else {
@@ -715,7 +738,7 @@ gdn_status residual_bwd_t(const T* y, int64_t ldy, const R* res, const float* rs
                     rows16(pw, 0) && rows16(w, 0) && rows16(gate, gmode == 2 ? rt : 0) && rows16(dy, rt) &&
                     rows16(dres, rr) && rows16(gmode == 2 ? dgate : nullptr, rt) && rt % 16 == 0;
   const Shape s = shape_of(D, wide ? VW : 1);
-  const size_t smem = s.group || s.nv * s.vec > 8 ? sizeof(float) * s.rpb() * 3 * D : 0;
+  const size_t smem = sizeof(float) * s.rpb() * 3 * D;
   int grid = 0;
   bool ok = true;
 #define GDN_F(VEC, NV, GROUP)                                                                                       \

@@ -79,18 +79,26 @@ __device__ __forceinline__ void load_t(float* dst, const T* src, int64_t ld, int
   }
 }
 
-// acc[r][u] += sum_kk A[kk][4 ty + r] B[kk][4 tx + u] over 64 kk
+// acc[r][u] += sum_kk A[kk][4 ty + r] B[kk][4 tx + u] over 64 kk, two columns an instruction
 __device__ __forceinline__ void fma_tile(float (&acc)[4][4], const float* A, const float* B, int ty, int tx) {
+  float2 c[4][2];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) c[r][0] = make_float2(acc[r][0], acc[r][1]), c[r][1] = make_float2(acc[r][2], acc[r][3]);
 #pragma unroll 16
   for (int kk = 0; kk < kC; ++kk) {
     const float4 a = *reinterpret_cast<const float4*>(A + kk * kLd + 4 * ty);
     const float4 b = *reinterpret_cast<const float4*>(B + kk * kLd + 4 * tx);
-    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    const float av[4] = {a.x, a.y, a.z, a.w};
+    const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) acc[r][u] = fmaf(av[r], bv[u], acc[r][u]);
+    for (int r = 0; r < 4; ++r) {
+      const float2 ar = make_float2(av[r], av[r]);
+      c[r][0] = __ffma2_rn(ar, b0, c[r][0]);
+      c[r][1] = __ffma2_rn(ar, b1, c[r][1]);
+    }
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc[r][0] = c[r][0].x, acc[r][1] = c[r][0].y, acc[r][2] = c[r][1].x, acc[r][3] = c[r][1].y;
 }
 
 // What a chunk adds to the state behind it, sum_j e^{b_last - b_j} x_j y_j^T (x = k, y = v), or, for the adjoint, to

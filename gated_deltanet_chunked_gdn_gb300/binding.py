@@ -1053,17 +1053,17 @@ def _norm_rows(name: str, t, inner: int, width: int):
         if t.shape[i] != 1 and t.stride(i) != want:
             raise ValueError(f"{name} must have contiguous rows, one after the other at one stride")
         want *= t.shape[i]
-    rows, ld = 1, 0
+    rows, ld = 1, None
     for i in range(lead - 1, -1, -1):
         if t.shape[i] != 1:
-            if ld == 0:
+            if ld is None:
                 ld = t.stride(i)
             elif t.stride(i) != ld * rows:
                 raise ValueError(f"{name} must have contiguous rows, one after the other at one stride")
             rows *= t.shape[i]
-    if ld != 0 and ld < width:
+    if ld is not None and ld < width:
         raise ValueError(f"{name} must have contiguous rows, one after the other at one stride")
-    return rows, ld or width
+    return rows, width if ld is None else ld
 
 
 def _check_like(dev, *tensors):

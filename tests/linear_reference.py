@@ -115,7 +115,7 @@ def residual_norm(y, res, pw, gate, scale, w, eps, dh=None, dn=None):
 
 def rel(x, ref):
     """Relative Frobenius error; inputs of any type."""
-    x, ref = x.double(), ref.double()
+    x, ref = x.detach().double(), ref.detach().double()
     n = float(torch.linalg.vector_norm(ref))
     d = float(torch.linalg.vector_norm(x - ref))
     return d / n if n else d

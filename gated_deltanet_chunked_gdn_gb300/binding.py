@@ -1162,9 +1162,9 @@ def _residual_norm(y, residual, post_weight, gate, weight, others):
                 return y.numel() // D if D else 0, D, 0, kind, DTYPES[dtype], DTYPES[residual.dtype], dev
     if residual.dtype not in (dtype, torch.float32):
         raise ValueError("residual must have the dtype of y, or float32")
-    kind = 0 if gate is None else 1 if gate.dim() == 1 and gate.dtype is torch.float32 and shape != gate.shape else 2
+    kind = 0 if gate is None else 2 if gate.shape == shape and gate.dtype is dtype else 1
     _check_like(dev, ("residual", residual, residual.dtype, shape), ("post_weight", post_weight, f32, (D,)),
-                ("gate", gate, *((f32, (D,)) if kind == 1 else (dtype, shape))), ("weight", weight, f32, (D,)),
+                ("gate", gate, *((f32, (D,)) if kind < 2 else (dtype, shape))), ("weight", weight, f32, (D,)),
                 *others)
     rows, ld = _norm_rows("y", y, 1, D)
     return rows, D, ld, kind, DTYPES[dtype], DTYPES[residual.dtype], dev

@@ -102,7 +102,10 @@ __device__ __forceinline__ Two log2_units(Two a) {
 
 // Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i} and what the first lacks
 // to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
-// differences of the sums do; sums in double take seven times as long, fp64 being scarce here).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A warp takes a chunk and head at a time.  Done by the kernels below, one warp would take 2000 cycles of a chunk's 5000 while the others wait.
+// differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads take 28 us, as
+// they are 8).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A
+// warp takes a chunk and head at a time.  (Within the kernels below it was one warp's work for 2000 cycles a chunk, while
+// the others waited.)
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
                                                      float scale, float* __restrict__ out) {
   const Piece p = piece_of(pc, blockIdx.x);
@@ -577,7 +580,7 @@ int segment_tokens(const gdn_linear_problem& p) {
   }
   const int64_t chains = p.N * heads;
   int64_t best = whole, least = ceil_div(chains, slots) * (whole + 2) * 2;
-  for (int64_t n = 2; n <= 64 && 4 * n <= whole + 3; ++n) {
+  for (int64_t n = 2; n <= 2 * slots && 4 * n <= whole + 3; n += 1 + n / 16) {
     const int64_t m = ceil_div(whole, n), cut = ceil_div(whole, m);
     const int64_t cost = (m + 2) * (2 * ceil_div(chains * cut, slots) + ceil_div(chains * (cut - 1), slots));
     if (cost < least) least = cost, best = m;

@@ -954,7 +954,7 @@ def gdn_linear_attn_fwd(q, k, v, g, scale: Optional[float] = None, h0=None, cu_s
                         (("o", o),) if o is not None else ())
     given = o, ht, workspace
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
     if ht is None and output_final_state:
         ht = torch.empty(state, dtype=torch.float32, device=v.device)
     if workspace is None:
@@ -1033,7 +1033,7 @@ def gdn_linear_attn_step(q, k, v, g, state, scale: Optional[float] = None, state
                         (("o", o),) if o is not None else ())
     idx = 0 if state_indices is None else _slot_map(state_indices, p.N, dev, "slot")
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
         if stream is not None:
             _lend(stream, v.device, (o,))
     st = _call(dev, lib.gdn_linear_attn_step, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
@@ -1100,7 +1100,7 @@ def gdn_gated_norm_fwd(x, z, weight, eps: float = 1e-6, y=None, save_rstd: bool 
     rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("y", y, x.dtype, x.shape),) if y is not None else ())
     fresh = []
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
         fresh.append(y)
     rstd = None
     if save_rstd:
@@ -1183,10 +1183,10 @@ def gdn_residual_norm_fwd(y, residual, post_weight=None, gate=None, residual_sca
         raise ValueError("n needs weight")
     fresh = []
     if h is None:
-        h = torch.empty(y.shape, dtype=residual.dtype, device=y.device)
+        h = torch.empty_like(residual)
         fresh.append(h)
     if n is None and weight is not None:
-        n = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        n = torch.empty_like(y, memory_format=torch.contiguous_format)
         fresh.append(n)
     rstd = None
     if save_rstd:

@@ -5,14 +5,14 @@
 //
 //   [K;Q] K^T                -> lanes 64..127: Q K^T                              (M128 N64)
 //   OQ^T = S^T Q^T           S^T: bf16 copy of the state before the chunk         (M128 N64)
-//   OP^T = V^T P^T           P = lower(scale e^{b_i - b_j} Q K^T), bf16           (M128 N64)
+//   OP^T = V^T P^T           P = lower(scale e^{b_i - b_j} Q K^T), two bf16 terms (M128 N64)
 //   U^T  = V''^T K           V'' = diag(e^{b_last - b_j}) V in three bf16 terms   (M128 N K)
 //   o_i  = scale e^{b_i} OQ_i + OP_i,   S^T <- e^{b_last} S^T + U^T
 //
 // The state itself stays in fp32 registers (a thread holds K / 2 columns of one row of S^T), and what a chunk adds to
 // it comes out of the tensor cores complete: V'' keeps all 24 bits of the weighted values (with two terms the final
 // state was off by 2.4e-6, with three by 1e-7), and no sum longer than a chunk is left to the tensor cores'
-// accumulation.  o reads a bf16 copy of the state and bf16 weights: one rounding of each term, like o's own.
+// accumulation.  o reads a bf16 copy of the state: one rounding of its terms, like o's own.
 // Two CTAs share an SM: one's loads and SIMT phases run under the other's products.
 //
 // Chains that do not fill the device are cut into segments of whole chunks: a launch before forms every segment's own
@@ -374,8 +374,16 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
             }
           }
         }
+        // the second term in the place of Q, which both of its products have read
 #pragma unroll
-        for (int q = 0; q < 4; ++q) solve64::store8_bf16(sm + M::P + sw128_chunk(i2, 4 * hf + q), v + 8 * q);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) split2(v[8 * q + 2 * u], v[8 * q + 2 * u + 1], hi[u], lo[u]);
+          const uint32_t off = sw128_chunk(i2, 4 * hf + q);
+          *reinterpret_cast<uint4*>(sm + M::P + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(sm + M::KQ + 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       // V'': the warps without weights begin with five eighths of it, the one whose weights are all zero takes as
       // much as the three others behind theirs
@@ -411,8 +419,9 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       if (FULL) {
         const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          mma_bf16(R_a, dsw(s4, M::V + s * 2048, 8192), dsw(s4, M::P + s * 32, 16), id, s > 0);
+        for (int s = 0; s < 8; ++s)
+          mma_bf16(R_a, dsw(s4, M::V + (s & 3) * 2048, 8192),
+                   dsw(s4, (s >> 2 ? M::KQ + 8192 : M::P) + (s & 3) * 32, 16), id, s > 0);
         commit(4, i);
       }
 #pragma unroll
@@ -421,10 +430,6 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         mma_bf16(R_U, dsw(s4, term + (s & 3) * 2048, 8192), dsw(s4, k_tile(i) + (s & 3) * 2048, 16384), idu, 1);
       }
       commit(5, i);
-      if (FULL && i + 1 < nchunks) {
-        wait(bar_qk, i);   // Q has been read (QS before it)
-        if (!bad) issue_q(i + 1);
-      }
     }
     __syncwarp();
     if (FULL) {
@@ -438,7 +443,10 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       tmem_ld32(R_b + lane_off + 32 * hf, oq);
       wait(bar_pv, i);
       tc_fence_after();
-      if (tid == 0 && i + 1 < nchunks && !bad) issue_v(i + 1);
+      if (tid == 0 && i + 1 < nchunks && !bad) {
+        issue_q(i + 1);
+        issue_v(i + 1);
+      }
       if (row < VD) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {

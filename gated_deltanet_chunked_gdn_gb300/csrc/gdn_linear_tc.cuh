@@ -39,7 +39,8 @@ __device__ __forceinline__ float2 halves(uint32_t w) {
 // a and b as sums of two bf16 values each, packed.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16(a, b);
-  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+  const float2 r = __ffma2_rn(halves(hi), make_float2(-1.f, -1.f), make_float2(a, b));
+  lo = pack_bf16(r.x, r.y);
 }
 
 // 16-byte aligned block of a multiple of 16 bytes, global -> shared.

@@ -399,9 +399,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int s = 0; s < 4; ++s)
         mma_bf16(I1, dsw(s4, M::VO + 8192 + s * 2048, 16384), dsw(s4, M::P + s * 32, 16), ida, s > 0);
 #pragma unroll
-      for (int s = 0; s < KD / 16; ++s)
-        mma_bf16(I1 + 64, dsw(s4, M::G + (s >> 2) * (VD * 128) + (s & 3) * 32, 16),
-                 dsw(s4, M::KQ + (s >> 2) * 16384 + (s & 3) * 32, 16), idb, s > 0);
+      for (int s = 0; s < 2 * (KD / 16); ++s) {   // two of G's terms
+        const int k = s % (KD / 16);
+        mma_bf16(I1 + 64, dsw(s4, M::G + s / (KD / 16) * M::kTile + (k >> 2) * (VD * 128) + (k & 3) * 32, 16),
+                 dsw(s4, M::KQ + (k >> 2) * 16384 + (k & 3) * 32, 16), idb, s > 0);
+      }
       commit(6, n);
     }
     __syncwarp();

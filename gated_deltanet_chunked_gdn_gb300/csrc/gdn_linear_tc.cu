@@ -49,7 +49,7 @@ struct Map {
   static constexpr int Ctas = KD == 256 ? 1 : 2;
 };
 
-// A whole 32-byte sector a thread: rows of S^T lie one a lane.
+// A whole 32-byte sector a thread; a warp's lanes write 1 KB side by side.
 __device__ __forceinline__ void store32(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       }
     }
     if (MODE == kEmit && row < VD) {
-      float* to = prm.emit + ((chunk_slot(p) + at) * prm.Hv + h) * (int64_t)(KD * VD) + row * KD + hf * KH;
+      float* to = prm.emit + ((chunk_slot(p) + at) * prm.Hv + h) * (int64_t)(KD * VD) + hf * KH * VD + row * 8;
 #pragma unroll
-      for (int b = 0; b < KH; b += 8) store32(to + b, S + b);
+      for (int b = 0; b < KH; b += 8) store32(to + b * VD, S + b);
     }
     if (len < 64) {
       wait(load_bar(0, i), load_no(i));

@@ -26,7 +26,7 @@ struct TcParams {
   int32_t* status;
   Pieces pc;
   const int32_t* cu;
-  float* emit;           // kEmit: [slots of chunks][Hv][V][K]
+  float* emit;           // kEmit: [slots of chunks][Hv][K / 8][V][8]
   int slots, Hqk, Hv, V, varlen, T;
   float scale;
 };

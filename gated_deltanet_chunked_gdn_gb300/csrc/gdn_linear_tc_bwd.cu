@@ -25,7 +25,7 @@ constexpr int kGradThreads = 512;
 
 struct GradParams {
   const float* decays;   // [slots][Hv][4][64]
-  const float* states;   // [slots][Hv][V][K]
+  const float* states;   // [slots][Hv][K / 8][V][8]
   const float* adjoints;
   void* dq;              // bf16 [B, T, Hqk, K], or fp32 [B, T, Hv, K] (SHARED)
   void* dk;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
   constexpr int NV = KD * VD / 4 / kGradThreads;   // quads of a state a thread holds
   auto tile_at = [&](int u) {   // place of this thread's quad u in a bf16 tile
-    const int quad = tid + u * kGradThreads, e = quad / (KD / 4), d = quad % (KD / 4) * 4;
+    const int quad = tid + u * kGradThreads, e = (quad >> 1) % VD, d = (quad >> 1) / VD * 8 + (quad & 1) * 4;
     return (uint32_t)((d >> 6) * (VD * 128)) + sw128_chunk(e, (d & 63) >> 3) + (d & 4) * 2;
   };
 
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       commit(3, n);
     }
     __syncwarp();
-    // ---- S0 and G: <G, S0>, and their terms in their own places (a warp a row of [e][d] at a time, four d a lane)
+    // ---- S0 and G: <G, S0>, and their terms in their own places (two lanes eight d of an e)
     wait(bar_s, n);
     wait(bar_g, n);
     uint32_t third[NV][2];   // of G

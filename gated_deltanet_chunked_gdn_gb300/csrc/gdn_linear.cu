@@ -309,13 +309,16 @@ __global__ void __launch_bounds__(kThreads) outputs_kernel(const T* __restrict__
 template <typename T>
 gdn_status fwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v, const float* g, float scale,
                  const float* h0, const Pieces& pc, T* o, float* ht, const int32_t* idx, int slots, float* states,
-                 float* total, cudaStream_t s) {
+                 float* total, int32_t* status, cudaStream_t s) {
   const Shape d = shape_of(p);
   const int most = pieces_max(p, kC);
-  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, states, total, s);
+  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, states, total, status, s);
   if (st != GDN_OK) return st;
   st = launch_sums<false>(d, pc, p.N, total, h0, states, ht, idx, slots, s);
   if (st != GDN_OK || most == 0) return st;
+  if constexpr (sizeof(T) == 4) {
+    if (tc32_supported(d)) return launch_outputs32(d, q, k, v, g, pc, most, scale, states, o, status, s);
+  }
   outputs_kernel<T><<<(unsigned)((int64_t)most * p.Hv), kThreads, 0, s>>>(q, k, v, d, g, pc, scale, states, o);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -341,9 +344,10 @@ gdn_status simt_fwd(const gdn_linear_problem& p, const void* q, const void* k, c
   float* states = total + align_up(4 * (size_t)pieces_max(p, kC) * p.Hv) / 4;
   if (p.dt == GDN_F32)
     return fwd_t<float>(p, (const float*)q, (const float*)k, (const float*)v, g, scale, h0, pc, (float*)o, ht, idx,
-                        slots, states, total, s);
+                        slots, states, total, status, s);
   using T = __nv_bfloat16;
-  return fwd_t<T>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, h0, pc, (T*)o, ht, idx, slots, states, total, s);
+  return fwd_t<T>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, h0, pc, (T*)o, ht, idx, slots, states, total, status,
+                  s);
 }
 
 }  // namespace lin

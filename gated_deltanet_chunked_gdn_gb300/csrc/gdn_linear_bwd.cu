@@ -276,12 +276,14 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
                  const Pieces& pc, const Layout& L, uint8_t* ws, cudaStream_t s) {
   const Shape d = shape_of(p);
   const int most = pieces_max(p, kC);
+  int32_t* status = reinterpret_cast<int32_t*>(ws);
   float* total = reinterpret_cast<float*>(ws + L.total);
   float* S = reinterpret_cast<float*>(ws + L.states);
   float* G = reinterpret_cast<float*>(ws + L.adjoints);
-  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, S, total, s);
+  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, S, total, status, s);
   if (st == GDN_OK) st = launch_sums<false>(d, pc, p.N, total, h0, S, nullptr, nullptr, 0, s);
-  if (st == GDN_OK) st = launch_states<T, true>(d, q, p.ld_q, dout, (int64_t)p.Hv * p.V, g, pc, most, scale, G, total, s);
+  if (st == GDN_OK)
+    st = launch_states<T, true>(d, q, p.ld_q, dout, (int64_t)p.Hv * p.V, g, pc, most, scale, G, total, status, s);
   if (st == GDN_OK) st = launch_sums<true>(d, pc, p.N, total, dht, G, dh0, nullptr, 0, s);
   if (st != GDN_OK) return st;
   float* part = reinterpret_cast<float*>(ws + L.part);

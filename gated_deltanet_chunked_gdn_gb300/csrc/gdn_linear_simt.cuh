@@ -181,10 +181,24 @@ __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const flo
   }
 }
 
+// fp32 on the tensor cores, for K and V of 64 and 128 (gdn_linear_tc32.cu).
+inline bool tc32_supported(const Shape& d) { return d.K <= 128 && d.V <= 128; }
+gdn_status launch_states32(bool adj, const Shape& d, const float* x, int64_t ldx, const float* y, int64_t ldy,
+                           const float* g, const Pieces& pc, int most, float factor, float* S, float* total,
+                           int32_t* status, cudaStream_t s);
+gdn_status launch_outputs32(const Shape& d, const float* q, const float* k, const float* v, const float* g,
+                            const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
+                            cudaStream_t s);
+
 template <typename T, bool ADJ>
 gdn_status launch_states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g,
-                         const Pieces& pc, int most, float factor, float* S, float* total, cudaStream_t s) {
+                         const Pieces& pc, int most, float factor, float* S, float* total, int32_t* status,
+                         cudaStream_t s) {
   if (most == 0) return GDN_OK;
+  if constexpr (sizeof(T) == 4) {
+    if (tc32_supported(d))
+      return launch_states32(ADJ, d, x, ldx, y, ldy, g, pc, most, factor, S, total, status, s);
+  }
   const int64_t grid = (int64_t)most * d.Hv * (d.K / kC) * (d.V / kC);
   states_kernel<T, ADJ><<<(unsigned)grid, kThreads, 0, s>>>(x, ldx, y, ldy, d, g, pc, factor, S, total);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -43,6 +43,20 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack_bf16(r.x, r.y);
 }
 
+// Four values as sums of three bf16 values each, packed.
+__device__ __forceinline__ void split3(const float4& v, uint32_t (&a)[2], uint32_t (&b)[2], uint32_t (&c)[2]) {
+  const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float2 x = i ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+    a[i] = pack_bf16(x.x, x.y);
+    x = __ffma2_rn(halves(a[i]), minus, x);
+    b[i] = pack_bf16(x.x, x.y);
+    x = __ffma2_rn(halves(b[i]), minus, x);
+    c[i] = pack_bf16(x.x, x.y);
+  }
+}
+
 // 16-byte aligned block of a multiple of 16 bytes, global -> shared.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(

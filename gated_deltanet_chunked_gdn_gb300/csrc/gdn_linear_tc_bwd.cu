@@ -56,20 +56,6 @@ struct GradMap {
   static constexpr uint32_t Bytes = Flags + 64 + 1024;
 };
 
-// Four values as sums of three bf16 values each, packed.
-__device__ __forceinline__ void split3(const float4& v, uint32_t (&a)[2], uint32_t (&b)[2], uint32_t (&c)[2]) {
-  const float2 minus = make_float2(-1.f, -1.f);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float2 x = i ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
-    a[i] = pack_bf16(x.x, x.y);
-    x = __ffma2_rn(halves(a[i]), minus, x);
-    b[i] = pack_bf16(x.x, x.y);
-    x = __ffma2_rn(halves(b[i]), minus, x);
-    c[i] = pack_bf16(x.x, x.y);
-  }
-}
-
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }

@@ -1,6 +1,6 @@
-// gdn_linear.cu -- decayed linear attention: the forward pass in fp32 arithmetic for every type and head dim (three
-// launches over 64-token chunks: the chunks' own states, the sums along each sequence, the outputs), and the step on a
-// state pool.  bf16 prompts and training run the tensor-core kernel of gdn_linear_tc.cu instead where it applies.
+// gdn_linear.cu -- decayed linear attention: the forward pass's dispatch (bf16: the walk of gdn_linear_tc.cu; fp32:
+// three launches over 64-token chunks, the chunks' own states, the sums along each sequence, the outputs, with the
+// kernels of gdn_linear_tc32.cu), the tables of packed batches, and the step on a state pool.
 #include "gdn_linear_simt.cuh"
 
 namespace gdn {
@@ -244,122 +244,47 @@ gdn_status run_linear_step(const gdn_linear_problem& p, const void* q, const voi
   return lin::step_t<__nv_bfloat16>(p, q, k, v, g, scale, state, idx, slots, cu, o, s);
 }
 
-// --------------------------------------------------- forward, fp32 arithmetic
+// ------------------------------------------------------------- forward, fp32
 namespace lin {
 namespace {
 
-// Outputs of one chunk of one value head: P = e^{b_i - b_j} q_i . k_j, then 64 columns of o at a time.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) outputs_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                           const T* __restrict__ v, Shape d, const float* __restrict__ g,
-                                                           Pieces pc, float scale, const float* __restrict__ S0,
-                                                           T* __restrict__ o) {
-  __shared__ __align__(16) float As[kC * kLd], Bs[kC * kLd], Ps[kC * kLd];
-  __shared__ float hi[kC], lo[kC], up[kC];
-  const int c = blockIdx.x / d.Hv, h = blockIdx.x % d.Hv, hq = h / (d.Hv / d.Hqk);
-  const Piece p = piece_of(pc, c);
-  if (!p.ok) return;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  if (tid < 32) chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, tid, hi, lo);
-  __syncthreads();
-  if (tid < kC) up[tid] = scale * expf(hi[tid] + lo[tid]);
-  const T* qp = q + p.tok0 * d.ldq + (int64_t)hq * d.K;
-  const T* kp = k + p.tok0 * d.ldk + (int64_t)hq * d.K;
-  const T* vp = v + p.tok0 * d.ldv + (int64_t)h * d.V;
-  float acc[4][4];
-  zero(acc);
-  for (int d0 = 0; d0 < d.K; d0 += kC) {
-    __syncthreads();
-    load_t(As, qp + d0, d.ldq, p.len, nullptr);
-    load_t(Bs, kp + d0, d.ldk, p.len, nullptr);
-    __syncthreads();
-    fma_tile(acc, As, Bs, ty, tx);
-  }
-  // P^T [j][i]
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = 4 * ty + r, j = 4 * tx + u;
-      const float e = expf((hi[i] - hi[j]) + (lo[i] - lo[j]));
-      Ps[j * kLd + i] = j <= i ? scale * e * acc[r][u] : 0.f;
-    }
-  const float* S = S0 + ((int64_t)c * d.Hv + h) * d.K * d.V;
-  for (int e0 = 0; e0 < d.V; e0 += kC) {
-    zero(acc);
-    for (int d0 = 0; d0 < d.K; d0 += kC) {
-      __syncthreads();
-      load_t(As, qp + d0, d.ldq, p.len, up);
-      load_n(Bs, S + (int64_t)d0 * d.V + e0, d.V, kC, nullptr);
-      __syncthreads();
-      fma_tile(acc, As, Bs, ty, tx);
-    }
-    __syncthreads();
-    load_n(Bs, vp + e0, d.ldv, p.len, nullptr);
-    __syncthreads();
-    fma_tile(acc, Ps, Bs, ty, tx);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 4 * ty + r;
-      if (i < p.len) store4(o + ((p.tok0 + i) * d.Hv + h) * (int64_t)d.V + e0 + 4 * tx, acc[r]);
-    }
-  }
-}
-
-template <typename T>
-gdn_status fwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v, const float* g, float scale,
-                 const float* h0, const Pieces& pc, T* o, float* ht, const int32_t* idx, int slots, float* states,
-                 float* total, int32_t* status, cudaStream_t s) {
-  const Shape d = shape_of(p);
-  const int most = pieces_max(p, kC);
-  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, states, total, status, s);
-  if (st != GDN_OK) return st;
-  st = launch_sums<false>(d, pc, p.N, total, h0, states, ht, idx, slots, s);
-  if (st != GDN_OK || most == 0) return st;
-  if constexpr (sizeof(T) == 4) {
-    if (tc32_supported(d)) return launch_outputs32(d, q, k, v, g, pc, most, scale, states, o, status, s);
-  }
-  outputs_kernel<T><<<(unsigned)((int64_t)most * p.Hv), kThreads, 0, s>>>(q, k, v, d, g, pc, scale, states, o);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-}
-
-}  // namespace
-
 // [status][tables][total: chunks x Hv][states: chunks x Hv x K x V]
-size_t simt_fwd_bytes(const gdn_linear_problem& p) {
+size_t fwd32_bytes(const gdn_linear_problem& p) {
   const size_t cells = (size_t)pieces_max(p, kC) * p.Hv;
   return kAlign + pieces_bytes(p, kC) + align_up(4 * cells) + 4 * cells * p.K * p.V;
 }
 
-gdn_status simt_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
-                    float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx, int slots,
-                    void* ws, cudaStream_t s) {
+gdn_status fwd32(const gdn_linear_problem& p, const float* q, const float* k, const float* v, const float* g,
+                 float scale, const float* h0, const int32_t* cu, float* o, float* ht, const int32_t* idx, int slots,
+                 void* ws, cudaStream_t s) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
   if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
   void* tables = at + kAlign;
   if (launch_pieces(p, kC, cu, tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
   const Pieces pc = pieces_at(p, kC, tables);
+  const Shape d = shape_of(p);
+  const int most = pieces_max(p, kC);
   float* total = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, kC));
-  float* states = total + align_up(4 * (size_t)pieces_max(p, kC) * p.Hv) / 4;
-  if (p.dt == GDN_F32)
-    return fwd_t<float>(p, (const float*)q, (const float*)k, (const float*)v, g, scale, h0, pc, (float*)o, ht, idx,
-                        slots, states, total, status, s);
-  using T = __nv_bfloat16;
-  return fwd_t<T>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, h0, pc, (T*)o, ht, idx, slots, states, total, status,
-                  s);
+  float* states = total + align_up(4 * (size_t)most * p.Hv) / 4;
+  gdn_status st = launch_states<float, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, states, total, status, s);
+  if (st == GDN_OK) st = launch_sums<false>(d, pc, p.N, total, h0, states, ht, idx, slots, s);
+  return st == GDN_OK ? launch_outputs(d, q, k, v, g, pc, most, scale, states, o, status, s) : st;
 }
 
+}  // namespace
 }  // namespace lin
 
 size_t linear_fwd_workspace_bytes(const gdn_linear_problem& p) {
-  return lin::tc_supported(p) ? lin::tc_fwd_bytes(p) : lin::simt_fwd_bytes(p);
+  return p.dt == GDN_BF16 ? lin::tc_fwd_bytes(p) : lin::fwd32_bytes(p);
 }
 
 gdn_status run_linear_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                           float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx,
                           int slots, void* ws, cudaStream_t s) {
-  return (lin::tc_supported(p) ? lin::tc_fwd : lin::simt_fwd)(p, q, k, v, g, scale, h0, cu, o, ht, idx, slots, ws, s);
+  if (p.dt == GDN_BF16) return lin::tc_fwd(p, q, k, v, g, scale, h0, cu, o, ht, idx, slots, ws, s);
+  return lin::fwd32(p, (const float*)q, (const float*)k, (const float*)v, g, scale, h0, cu, (float*)o, ht, idx, slots,
+                    ws, s);
 }
 
 }  // namespace gdn

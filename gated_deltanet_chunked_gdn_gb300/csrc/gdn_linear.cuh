@@ -88,8 +88,7 @@ gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, con
                   const float* h0, const int32_t* cu, const void* dout, const float* dht, void* dq, void* dk, void* dv,
                   float* dg, float* dh0, void* ws, cudaStream_t s);
 
-// The tensor-core forward pass (gdn_linear_tc.cu).
-bool tc_supported(const gdn_linear_problem& p);
+// The forward pass in bf16 (gdn_linear_tc.cu).
 size_t tc_fwd_bytes(const gdn_linear_problem& p);
 gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                   float scale, const float* h0, const int32_t* cu, void* o, float* ht, const int32_t* idx, int slots,

@@ -1,6 +1,5 @@
 // gdn_linear_simt.cuh -- fp32 tiles of decayed linear attention: 64 x 64 x 64 products by 256 threads (4 x 4 results a
-// thread, operands in shared memory with the summed dimension outermost), the chunks' own states, and the sums along a
-// sequence.
+// thread, operands in shared memory with the summed dimension outermost), and the sums along a sequence.
 #pragma once
 
 #include <string.h>
@@ -101,40 +100,6 @@ __device__ __forceinline__ void fma_tile(float (&acc)[4][4], const float* A, con
   for (int r = 0; r < 4; ++r) acc[r][0] = c[r][0].x, acc[r][1] = c[r][0].y, acc[r][2] = c[r][1].x, acc[r][3] = c[r][1].y;
 }
 
-// What a chunk adds to the state behind it, sum_j e^{b_last - b_j} x_j y_j^T (x = k, y = v), or, for the adjoint, to
-// the one before it, factor sum_i e^{b_i} x_i y_i^T (x = q, y = do): one 64 x 64 block of [K][V] a CTA.
-template <typename T, bool ADJ>
-__global__ void __launch_bounds__(kThreads) states_kernel(const T* __restrict__ x, int64_t ldx,
-                                                          const T* __restrict__ y, int64_t ldy, Shape d,
-                                                          const float* __restrict__ g, Pieces pc, float factor,
-                                                          float* __restrict__ S, float* __restrict__ total) {
-  __shared__ __align__(16) float Xs[kC * kLd], Ys[kC * kLd];
-  __shared__ float hi[kC], lo[kC], w[kC];
-  const int nb = (d.K / kC) * (d.V / kC);
-  const int blk = blockIdx.x % nb, ch = blockIdx.x / nb;
-  const int c = ch / d.Hv, h = ch % d.Hv, hq = h / (d.Hv / d.Hqk);
-  const int d0 = blk / (d.V / kC) * kC, e0 = blk % (d.V / kC) * kC;
-  const Piece p = piece_of(pc, c);
-  if (!p.ok) return;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  if (tid < 32) chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, tid, hi, lo);
-  __syncthreads();
-  if (tid < kC) {
-    w[tid] = ADJ ? factor * expf(hi[tid] + lo[tid]) : expf((hi[kC - 1] - hi[tid]) + (lo[kC - 1] - lo[tid]));
-    if (tid == kC - 1 && blk == 0) total[ch] = expf(hi[tid] + lo[tid]);
-  }
-  __syncthreads();
-  load_n(Xs, x + p.tok0 * ldx + (int64_t)hq * d.K + d0, ldx, p.len, w);
-  load_n(Ys, y + p.tok0 * ldy + (int64_t)h * d.V + e0, ldy, p.len, nullptr);
-  __syncthreads();
-  float acc[4][4];
-  zero(acc);
-  fma_tile(acc, Xs, Ys, ty, tx);
-  float* out = S + ((int64_t)ch * d.K + d0) * d.V + e0;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) store4(out + (int64_t)(4 * ty + r) * d.V + 4 * tx, acc[r]);
-}
-
 // Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (REV: the adjoint of the
 // state behind it); four elements of a state a thread, the next chunks' loads in flight.
 template <bool REV>
@@ -149,27 +114,34 @@ __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const flo
   if (pc.seq && *pc.nc < 0) return;
   const int c0 = pc.seq ? pc.first[n] : n * pc.per, c1 = pc.seq ? pc.first[n + 1] : c0 + pc.per;
   float4 run = init ? load4(init + nh * kv + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  // the next four chunks' loads are under way while these are added up
   constexpr int AHEAD = 4;
-  for (int base = 0; base < c1 - c0; base += AHEAD) {
-    float4 x[AHEAD];
-    float a[AHEAD];
+  float4 x[2][AHEAD];
+  float a[2][AHEAD];
+  auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
+  auto fetch = [&](float4 (&y)[AHEAD], float (&f)[AHEAD], int base) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int c = REV ? c1 - 1 - base - i : c0 + base + i;
+    for (int i = 0; i < AHEAD; ++i)
       if (base + i < c1 - c0) {
-        x[i] = __ldcs(reinterpret_cast<const float4*>(S + ((int64_t)c * d.Hv + h) * kv + at));
-        a[i] = total[(int64_t)c * d.Hv + h];
+        y[i] = __ldcs(reinterpret_cast<const float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at));
+        f[i] = total[(int64_t)chunk(base + i) * d.Hv + h];
       }
-    }
+  };
+  auto add = [&](const float4 (&y)[AHEAD], const float (&f)[AHEAD], int base) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int c = REV ? c1 - 1 - base - i : c0 + base + i;
+    for (int i = 0; i < AHEAD; ++i)
       if (base + i < c1 - c0) {
-        *reinterpret_cast<float4*>(S + ((int64_t)c * d.Hv + h) * kv + at) = run;
-        run.x = fmaf(a[i], run.x, x[i].x), run.y = fmaf(a[i], run.y, x[i].y);
-        run.z = fmaf(a[i], run.z, x[i].z), run.w = fmaf(a[i], run.w, x[i].w);
+        *reinterpret_cast<float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at) = run;
+        run.x = fmaf(f[i], run.x, y[i].x), run.y = fmaf(f[i], run.y, y[i].y);
+        run.z = fmaf(f[i], run.z, y[i].z), run.w = fmaf(f[i], run.w, y[i].w);
       }
-    }
+  };
+  fetch(x[0], a[0], 0);
+  for (int base = 0; base < c1 - c0; base += 2 * AHEAD) {
+    fetch(x[1], a[1], base + AHEAD);
+    add(x[0], a[0], base);
+    fetch(x[0], a[0], base + 2 * AHEAD);
+    add(x[1], a[1], base + AHEAD);
   }
   if (fin) {
     int64_t row = n;
@@ -181,28 +153,16 @@ __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const flo
   }
 }
 
-// fp32 on the tensor cores, for K and V of 64 and 128 (gdn_linear_tc32.cu).
-inline bool tc32_supported(const Shape& d) { return d.K <= 128 && d.V <= 128; }
-gdn_status launch_states32(bool adj, const Shape& d, const float* x, int64_t ldx, const float* y, int64_t ldy,
-                           const float* g, const Pieces& pc, int most, float factor, float* S, float* total,
-                           int32_t* status, cudaStream_t s);
-gdn_status launch_outputs32(const Shape& d, const float* q, const float* k, const float* v, const float* g,
-                            const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
-                            cudaStream_t s);
-
+// What a chunk adds to the state behind it, sum_j e^{b_last - b_j} x_j y_j^T (x = k, y = v), or, for the adjoint, to
+// the one before it, factor sum_i e^{b_i} x_i y_i^T (x = q, y = do), and its whole decay; the outputs of every chunk
+// from the state before it (gdn_linear_tc32.cu).
 template <typename T, bool ADJ>
 gdn_status launch_states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g,
                          const Pieces& pc, int most, float factor, float* S, float* total, int32_t* status,
-                         cudaStream_t s) {
-  if (most == 0) return GDN_OK;
-  if constexpr (sizeof(T) == 4) {
-    if (tc32_supported(d))
-      return launch_states32(ADJ, d, x, ldx, y, ldy, g, pc, most, factor, S, total, status, s);
-  }
-  const int64_t grid = (int64_t)most * d.Hv * (d.K / kC) * (d.V / kC);
-  states_kernel<T, ADJ><<<(unsigned)grid, kThreads, 0, s>>>(x, ldx, y, ldy, d, g, pc, factor, S, total);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-}
+                         cudaStream_t s);
+gdn_status launch_outputs(const Shape& d, const float* q, const float* k, const float* v, const float* g,
+                          const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
+                          cudaStream_t s);
 
 template <bool REV>
 gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const float* init, float* S,

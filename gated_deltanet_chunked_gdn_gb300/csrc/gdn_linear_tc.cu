@@ -659,8 +659,6 @@ gdn_status launch_walk(const gdn_linear_problem& p, int mode, bool adj, const vo
   return launch_dims<256, 128>(mode, adj, grid, m, prm, s);
 }
 
-bool tc_supported(const gdn_linear_problem& p) { return p.dt == GDN_BF16; }
-
 // [status][tables][decays][the segments' own: segments x Hv][states: segments x Hv x K x V]
 size_t tc_fwd_bytes(const gdn_linear_problem& p) {
   const int seg = segment_tokens(p);

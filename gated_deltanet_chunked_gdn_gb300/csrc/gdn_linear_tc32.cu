@@ -1,9 +1,9 @@
-// gdn_linear_tc32.cu -- the chunks' own states and the outputs of decayed linear attention for fp32 and K, V in
-// {64, 128} on the tensor cores.
+// gdn_linear_tc32.cu -- the chunks' own states and the outputs of decayed linear attention on the tensor cores with fp32
+// precision throughout, for fp32 and for bf16 with head dims of 256.
 //
 // An fp32 value is the sum of three bf16 values to its last bit or so (8 bits each); a product of two such sums keeps
-// the six of its nine terms that reach 2^-24 of it, each exact in the fp32 accumulators.  Six bf16 products cost a
-// sixth of 1.89 PFLOP/s, against 74 TFLOP/s of fp32 FMAs.
+// the six of its nine terms that reach 2^-24 of it, each exact in the fp32 accumulators (bf16 inputs are their own first
+// term).  Six bf16 products cost a sixth of 1.89 PFLOP/s, against 74 TFLOP/s of fp32 FMAs.
 //
 //   states:   D[e][d] = V^T (w K)                                (w_j = e^{b_last - b_j}; the adjoint's: q, do)
 //   outputs:  P = scale M (Q K^T),   o^T[e][i] = scale e^{b_i} (S0^T Q^T) + V^T P^T
@@ -16,20 +16,22 @@ namespace gdn {
 namespace lin {
 namespace {
 
-// Threads of a CTA: four quads of a 64-row tile each, whatever K.
-template <int KD>
-constexpr int kThreads32 = KD == 64 ? 256 : 512;
+constexpr int N = 256;   // threads
 
-// Rows of `cols` fp32 -> three tiles `tile` bytes apart of 64-column atom columns, row r times w[r]; zeros past `rows`.
-template <int ROWS, int COLS, int N>
-__device__ __forceinline__ void fetch(float4 (&x)[ROWS * COLS / 4 / N], const float* src, int64_t ld, int rows) {
+template <typename T>
+constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
+
+// ROWS x COLS values, four neighbours a thread at a time -> `TERMS` tiles of 64-column atom columns, row r times w[r];
+// zeros past `rows`.
+template <int ROWS, int COLS, typename T>
+__device__ __forceinline__ void fetch(float4 (&x)[ROWS * COLS / 4 / N], const T* src, int64_t ld, int rows) {
 #pragma unroll
   for (int u = 0; u < ROWS * COLS / 4 / N; ++u) {
     const int quad = threadIdx.x + u * N, r = quad / (COLS / 4), c = quad % (COLS / 4) * 4;
-    x[u] = r < rows ? *reinterpret_cast<const float4*>(src + r * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[u] = r < rows ? load4(src + r * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
-template <int ROWS, int COLS, int N>
+template <int ROWS, int COLS, int TERMS>
 __device__ __forceinline__ void place(uint8_t* sm, const float4 (&x)[ROWS * COLS / 4 / N], const float* w) {
   constexpr uint32_t tile = ROWS * COLS * 2;
 #pragma unroll
@@ -40,38 +42,49 @@ __device__ __forceinline__ void place(uint8_t* sm, const float4 (&x)[ROWS * COLS
       const float f = w[r];
       y.x *= f, y.y *= f, y.z *= f, y.w *= f;
     }
-    uint32_t w0[2], w1[2], w2[2];
-    split3(y, w0, w1, w2);
     uint8_t* to = sm + (c >> 6) * (ROWS * 128) + sw128_chunk(r, (c & 63) >> 3) + (c & 4) * 2;
-    *reinterpret_cast<uint2*>(to) = make_uint2(w0[0], w0[1]);
-    *reinterpret_cast<uint2*>(to + tile) = make_uint2(w1[0], w1[1]);
-    *reinterpret_cast<uint2*>(to + 2 * tile) = make_uint2(w2[0], w2[1]);
+    if (TERMS == 1) {
+      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    } else {
+      uint32_t w0[2], w1[2], w2[2];
+      split3(y, w0, w1, w2);
+      *reinterpret_cast<uint2*>(to) = make_uint2(w0[0], w0[1]);
+      *reinterpret_cast<uint2*>(to + tile) = make_uint2(w1[0], w1[1]);
+      *reinterpret_cast<uint2*>(to + 2 * tile) = make_uint2(w2[0], w2[1]);
+    }
   }
 }
 
-// The six products of terms, the smallest first: f(term of A, term of B, first)
-template <typename F>
-__device__ __forceinline__ void six(F f) {
-  f(2, 0, 0u), f(1, 1, 1u), f(0, 2, 1u), f(1, 0, 1u), f(0, 1, 1u), f(0, 0, 1u);
+// The products of A's and B's terms, the smallest first: f(term of A, term of B, 0 for the first one of all).
+template <int A, int B, typename F>
+__device__ __forceinline__ void products(F f) {
+  uint32_t more = 0;
+#pragma unroll
+  for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+    for (int a = 2; a >= 0; --a)
+      if (a < A && a <= sum && sum - a < B) f(a, sum - a, more), more = 1;
 }
 
-template <int KD, int VD>
+template <typename T, int KD, int VD>
 struct StateMap32 {
   static constexpr uint32_t kK = KD * 128, kV = VD * 128;   // a term's tile
-  static constexpr uint32_t V = 0, K = 3 * kV;
+  static constexpr uint32_t V = 0, K = kTerms<T> * kV;
   static constexpr uint32_t Misc = K + 3 * kK, Hi = Misc, Lo = Misc + 256, Wt = Misc + 512;
   static constexpr uint32_t Bar = Misc + 768, Flags = Bar + 8, Bytes = Flags + 56 + 1024;
 };
 
-template <int KD, int VD, bool ADJ>
-__global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
-    states_tc32_kernel(const float* __restrict__ x, int64_t ldx, const float* __restrict__ y, int64_t ldy, Shape d,
+// One chunk of one value head a CTA, KD x VD of its state.
+template <typename T, int KD, int VD, bool ADJ>
+__global__ void __launch_bounds__(N, 2)
+    states_tc32_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ y, int64_t ldy, Shape d,
                        const float* __restrict__ g, Pieces pc, float factor, float* __restrict__ S,
                        float* __restrict__ total, int32_t* status) {
-  using M = StateMap32<KD, VD>;
-  constexpr int N = kThreads32<KD>;
+  using M = StateMap32<T, KD, VD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const int c = blockIdx.x / d.Hv, h = blockIdx.x % d.Hv, hq = h / (d.Hv / d.Hqk);
+  const int nv = d.V / VD, nb = d.K / KD * nv;
+  const int ch = blockIdx.x / nb, blk = blockIdx.x - ch * nb, d0 = blk / nv * KD, e0 = blk % nv * VD;
+  const int c = ch / d.Hv, h = ch % d.Hv, hq = h / (d.Hv / d.Hqk);
   const Piece p = piece_of(pc, c);
   if (!p.ok) return;
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -88,31 +101,31 @@ __global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
   }
   if (warp == 0) tmem_alloc(flags, KD);
   float4 xs[64 * KD / 4 / N], ys[64 * VD / 4 / N];
-  fetch<64, KD, N>(xs, x + p.tok0 * ldx + (int64_t)hq * KD, ldx, p.len);
-  fetch<64, VD, N>(ys, y + p.tok0 * ldy + (int64_t)h * VD, ldy, p.len);
+  fetch<64, KD>(xs, x + p.tok0 * ldx + (int64_t)hq * d.K + d0, ldx, p.len);
+  fetch<64, VD>(ys, y + p.tok0 * ldy + (int64_t)h * d.V + e0, ldy, p.len);
   if (warp == 1) {
     chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
     __syncwarp();
 #pragma unroll
     for (int r = lane; r < kC; r += 32)
       w[r] = ADJ ? factor * expf(hi[r] + lo[r]) : expf((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
-    if (lane == 0) total[blockIdx.x] = expf(hi[kC - 1] + lo[kC - 1]);
+    if (lane == 0 && blk == 0) total[ch] = expf(hi[kC - 1] + lo[kC - 1]);
   }
-  place<64, VD, N>(sm + M::V, ys, nullptr);
+  place<64, VD, kTerms<T>>(sm + M::V, ys, nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags);
-  place<64, KD, N>(sm + M::K, xs, w);
+  place<64, KD, 3>(sm + M::K, xs, w);
   fence_proxy_async();
   __syncthreads();
   if (tid == 0) {
     const uint32_t id = idesc_bf16(128, KD, 1, 1, 0);
-    six([&](int a, int b, uint32_t first) {
+    products<kTerms<T>, 3>([&](int a, int b, uint32_t more) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         mma_bf16(tmem, dsw(s4, M::V + a * M::kV + s * 2048, 8192), dsw(s4, M::K + b * M::kK + s * 2048, 8192), id,
-                 s > 0 ? 1u : first);
+                 s > 0 ? 1u : more);
     });
     mma_commit(bar);
   }
@@ -121,14 +134,13 @@ __global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
   tc_fence_after();
   const int qd = warp & 3, part = warp >> 2, row = 32 * qd + lane;
   if (good && row < VD) {
-    constexpr int COLS = KD / (N / 128);
-    float* to = S + ((int64_t)blockIdx.x * KD + part * COLS) * VD + row;
+    float* to = S + ((int64_t)ch * d.K + d0 + part * (KD / 2)) * d.V + e0 + row;
 #pragma unroll
-    for (int b = 0; b < COLS; b += 16) {
+    for (int b = 0; b < KD / 2; b += 16) {
       float v[16];
-      tmem_ld16(tmem + (static_cast<uint32_t>(32 * qd) << 16) + part * COLS + b, v);
+      tmem_ld16(tmem + (static_cast<uint32_t>(32 * qd) << 16) + part * (KD / 2) + b, v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) to[(b + j) * VD] = v[j];
+      for (int j = 0; j < 16; ++j) to[(int64_t)(b + j) * d.V] = v[j];
     }
   }
   tc_fence_before();
@@ -137,101 +149,137 @@ __global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
   if (warp == 0) tmem_dealloc(tmem, KD);
 }
 
-template <int KD, int VD>
+template <int VD>
 struct OutMap32 {
-  static constexpr uint32_t kQ = KD * 128, kS = KD * VD * 2, kV = VD * 128, kP = 8192;
-  static constexpr uint32_t S = 0, V = S;            // V where S0 was
+  static constexpr uint32_t kQ = 8192, kS = 64 * VD * 2, kV = kS, kP = 8192;   // a term's tile
+  static constexpr uint32_t S = 0, V = S;                     // V where S0 was
   static constexpr uint32_t Q = S + 3 * kS;
-  static constexpr uint32_t K = Q + 3 * kQ, P = K;   // P where K was
-  static constexpr uint32_t Misc = K + 3 * kQ, Hi = Misc, Lo = Misc + 256, Up = Misc + 512;
-  static constexpr uint32_t Bar = Misc + 768, Flags = Bar + 24, Bytes = Flags + 40 + 1024;
+  static constexpr uint32_t K = Q + 3 * kQ, P = K;             // P where K was
+  static constexpr uint32_t Misc = K + 3 * kP, Hi = Misc, Lo = Misc + 256, Up = Misc + 512;
+  static constexpr uint32_t Bar = Misc + 768, Flags = Bar + 16, Bytes = Flags + 48 + 1024;
 };
 
-// One chunk of one value head a CTA.
-template <int KD, int VD>
-__global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
+// VD of the V = NV VD columns of the outputs of one chunk of one value head a CTA, 64 of the summed K at a time (KB of
+// them).  The
+// accumulators drop bits that small products add to large sums (o's error 6e-7 instead of 1.5e-7): with more than one
+// 64 of K, the products of first terms and all others have a sum each.
+template <int VD, int NV, int KB>
+__global__ void __launch_bounds__(N, 2)
     outputs_tc32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, Shape d,
                         const float* __restrict__ g, Pieces pc, float scale, const float* __restrict__ S0,
                         float* __restrict__ o, int32_t* status) {
-  using M = OutMap32<KD, VD>;
-  constexpr int N = kThreads32<KD>;
+  using M = OutMap32<VD>;
+  constexpr uint32_t kCols = KB > 1 ? 256 : 128, kRest = KB > 1 ? 128 : 0;   // TMEM columns, place of the others' sums
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const int c = blockIdx.x / d.Hv, h = blockIdx.x % d.Hv, hq = h / (d.Hv / d.Hqk);
+  constexpr int K = 64 * KB, V = NV * VD;
+  const int ch = blockIdx.x / NV, e0 = (blockIdx.x - ch * NV) * VD;
+  const int c = ch / d.Hv, h = ch % d.Hv, hq = h / (d.Hv / d.Hqk);
   const Piece p = piece_of(pc, c);
   if (!p.ok) return;
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
   float *hi = reinterpret_cast<float*>(sm + M::Hi), *lo = reinterpret_cast<float*>(sm + M::Lo);
   float* up = reinterpret_cast<float*>(sm + M::Up);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::Bar);   // Q K^T, S0^T Q^T, V^T P^T: one phase each
+  // Q K^T and, with the last of them, V^T P^T; S0^T Q^T: a phase for every 64 of K
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::Bar);
   uint32_t* flags = reinterpret_cast<uint32_t*>(sm + M::Flags);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qd = warp & 3, part = warp >> 2, row = 32 * qd + lane;
-  constexpr int COLS = 64 / (N / 128);   // tokens of a thread
   const uint32_t lane_off = static_cast<uint32_t>(32 * qd) << 16;
 
   if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) mbar_init(bars + i, 1);
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
     mbar_fence_init();
   }
-  if (warp == 0) tmem_alloc(flags, 128);
-  {
-    float4 xq[64 * KD / 4 / N], xk[64 * KD / 4 / N], xs[KD * VD / 4 / N];
-    fetch<64, KD, N>(xq, q + p.tok0 * d.ldq + (int64_t)hq * KD, d.ldq, p.len);
-    fetch<64, KD, N>(xk, k + p.tok0 * d.ldk + (int64_t)hq * KD, d.ldk, p.len);
-    fetch<KD, VD, N>(xs, S0 + (int64_t)blockIdx.x * KD * VD, VD, KD);
-    if (warp == 1) {
-      chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
-      __syncwarp();
+  if (warp == 0) tmem_alloc(flags, kCols);
+  const float* qp = q + p.tok0 * d.ldq + (int64_t)hq * K;
+  const float* kp = k + p.tok0 * d.ldk + (int64_t)hq * K;
+  const float* sp = S0 + (int64_t)ch * K * V + e0;
+  constexpr int last = KB - 1;
+  float4 xv[64 * VD / 4 / N];   // S0's rows, then V's
+  bool good = true;
+  uint32_t tmem = 0;
+  int issued0 = 0, issued1 = 0;   // phases begun
+#pragma unroll 1
+  for (int kb = 0; kb < KB; ++kb) {
+    float4 xq[4], xk[4];
+    fetch<64, 64>(xq, qp + 64 * kb, d.ldq, p.len);
+    fetch<64, 64>(xk, kp + 64 * kb, d.ldk, p.len);
+    fetch<64, VD>(xv, sp + (int64_t)64 * kb * V, V, 64);
+    if (kb == 0) {
+      if (warp == 1) {
+        chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
+        __syncwarp();
 #pragma unroll
-      for (int r = lane; r < kC; r += 32) up[r] = scale * expf(hi[r] + lo[r]);
+        for (int r = lane; r < kC; r += 32) up[r] = scale * expf(hi[r] + lo[r]);
+      }
+    } else {   // the tiles before have been read
+      good = good && mbar_wait(bars, (kb - 1) & 1, status);
+      good = good && mbar_wait(bars + 1, (kb - 1) & 1, status);
     }
-    place<64, KD, N>(sm + M::Q, xq, nullptr);
-    place<64, KD, N>(sm + M::K, xk, nullptr);
+    if (good) {
+      place<64, 64, 3>(sm + M::Q, xq, nullptr);
+      place<64, 64, 3>(sm + M::K, xk, nullptr);
+    }
     fence_proxy_async();
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(!good)) {
+      good = false;
+      break;
+    }
     tc_fence_after();
+    tmem = *reinterpret_cast<volatile uint32_t*>(flags);
     if (tid == 0) {
-      const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags), id = idesc_bf16(128, 64, 0, 0, 0);
-      six([&](int a, int b, uint32_t first) {
+      const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
+      products<3, 3>([&](int a, int b, uint32_t more) {
+        const bool main = a + b == 0;
+        const uint32_t to = tmem + (main ? 0 : kRest), first = main && KB > 1 ? 0u : more;
 #pragma unroll
-        for (int s = 0; s < KD / 16; ++s) {
-          const uint32_t at = (s >> 2) * 8192 + (s & 3) * 32;
-          mma_bf16(tmem, dsw(s4, M::Q + a * M::kQ + at, 16), dsw(s4, M::K + b * M::kQ + at, 16), id,
-                   s > 0 ? 1u : first);
-        }
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(to, dsw(s4, M::Q + a * M::kQ + s * 32, 16), dsw(s4, M::K + b * M::kQ + s * 32, 16), id,
+                   s > 0 || kb > 0 ? 1u : first);
       });
       mma_commit(bars);
     }
+    issued0 = kb + 1;
     __syncwarp();
-    place<KD, VD, N>(sm + M::S, xs, nullptr);
-  }
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags);
-  fence_proxy_async();
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
-    six([&](int a, int b, uint32_t first) {
+    place<64, VD, 3>(sm + M::S, xv, nullptr);
+    fence_proxy_async();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
+      products<3, 3>([&](int a, int b, uint32_t more) {
+        const bool main = a + b == 0;
+        const uint32_t to = tmem + 64 + (main ? 0 : kRest), first = main && KB > 1 ? 0u : more;
 #pragma unroll
-      for (int s = 0; s < KD / 16; ++s)
-        mma_bf16(tmem + 64, dsw(s4, M::S + a * M::kS + s * 2048, KD * 128),
-                 dsw(s4, M::Q + b * M::kQ + (s >> 2) * 8192 + (s & 3) * 32, 16), id, s > 0 ? 1u : first);
-    });
-    mma_commit(bars + 1);
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(to, dsw(s4, M::S + a * M::kS + s * 2048, 8192), dsw(s4, M::Q + b * M::kQ + s * 32, 16), id,
+                   s > 0 || kb > 0 ? 1u : first);
+      });
+      mma_commit(bars + 1);
+    }
+    issued1 = kb + 1;
+    __syncwarp();
   }
-  __syncwarp();
-  float4 xv[64 * VD / 4 / N];
-  fetch<64, VD, N>(xv, v + p.tok0 * d.ldv + (int64_t)h * VD, d.ldv, p.len);
-  bool good = mbar_wait(bars, 0, status);
-  tc_fence_after();
-  if (row < 64 && good) {   // P[row][.] of COLS tokens
+  if (good) {
+    fetch<64, VD>(xv, v + p.tok0 * d.ldv + (int64_t)h * V + e0, d.ldv, p.len);
+    good = mbar_wait(bars, last & 1, status);
+    tc_fence_after();
+  }
+  constexpr int COLS = 32;   // tokens of a thread
+  if (row < 64 && good) {    // P[row][.]
 #pragma unroll
     for (int b = 0; b < COLS; b += 16) {
       float x[16];
       const int j0 = part * COLS + b;
       tmem_ld16(tmem + lane_off + j0, x);
+      if (KB > 1) {
+        float rest[16];
+        tmem_ld16(tmem + kRest + lane_off + j0, rest);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] += rest[j];
+      }
       const float mine = hi[row], rest = lo[row];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -250,8 +298,8 @@ __global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
       }
     }
   }
-  good = good && mbar_wait(bars + 1, 0, status);
-  if (good) place<64, VD, N>(sm + M::V, xv, nullptr);
+  good = good && mbar_wait(bars + 1, last & 1, status);
+  if (good) place<64, VD, 3>(sm + M::V, xv, nullptr);
   fence_proxy_async();
   tc_fence_before();
   const bool all = !__syncthreads_or(!good);
@@ -259,38 +307,46 @@ __global__ void __launch_bounds__(kThreads32<KD>, KD == 64 ? 2 : 1)
   if (all) {
     if (tid == 0) {
       const uint32_t id = idesc_bf16(128, 64, 1, 0, 0);
-      six([&](int a, int b, uint32_t first) {
+      products<3, 3>([&](int a, int b, uint32_t more) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           mma_bf16(tmem, dsw(s4, M::V + a * M::kV + s * 2048, 8192), dsw(s4, M::P + b * M::kP + s * 32, 16), id,
-                   s > 0 ? 1u : first);
+                   s > 0 ? 1u : more);
       });
-      mma_commit(bars + 2);
+      mma_commit(bars);
     }
+    issued0 = last + 2;
     __syncwarp();
-    good = mbar_wait(bars + 2, 0, status);
+    good = mbar_wait(bars, (last + 1) & 1, status);
     tc_fence_after();
     if (good && row < VD) {
-      float* to = o + ((p.tok0 + part * COLS) * d.Hv + h) * (int64_t)VD + row;
+      float* to = o + ((p.tok0 + part * COLS) * d.Hv + h) * (int64_t)V + e0 + row;
 #pragma unroll
       for (int b = 0; b < COLS; b += 16) {
         float x[16], y[16];
         tmem_ld16(tmem + lane_off + part * COLS + b, x);
         tmem_ld16(tmem + lane_off + 64 + part * COLS + b, y);
+        if (KB > 1) {
+          float rest[16];
+          tmem_ld16(tmem + kRest + lane_off + 64 + part * COLS + b, rest);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] += rest[j];
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int i = part * COLS + b + j;
-          if (i < p.len) to[(int64_t)(b + j) * d.Hv * VD] = fmaf(up[i], y[j], x[j]);
+          if (i < p.len) to[(int64_t)(b + j) * d.Hv * V] = fmaf(up[i], y[j], x[j]);
         }
       }
     }
   }
   tc_fence_before();
   if (__syncthreads_or(!good) && tid == 0) {   // products still under way end before their memory is given back
-    for (int b = 0; b < (all ? 3 : 2); ++b) mbar_wait(bars + b, 0, status, 100000000ull);
+    if (issued0) mbar_wait(bars, (issued0 - 1) & 1, status, 100000000ull);
+    if (issued1) mbar_wait(bars + 1, (issued1 - 1) & 1, status, 100000000ull);
   }
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 128);
+  if (warp == 0) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(flags), kCols);
 }
 
 template <typename F>
@@ -298,54 +354,65 @@ bool allow(F kern, uint32_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <int KD, int VD, bool ADJ>
-gdn_status states(const Shape& d, const float* x, int64_t ldx, const float* y, int64_t ldy, const float* g,
-                  const Pieces& pc, int most, float factor, float* S, float* total, int32_t* status, cudaStream_t s) {
-  auto kern = states_tc32_kernel<KD, VD, ADJ>;
-  constexpr uint32_t bytes = StateMap32<KD, VD>::Bytes;
+template <typename T, int KD, int VD, bool ADJ>
+gdn_status states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g, const Pieces& pc,
+                  int most, float factor, float* S, float* total, int32_t* status, cudaStream_t s) {
+  auto kern = states_tc32_kernel<T, KD, VD, ADJ>;
+  constexpr uint32_t bytes = StateMap32<T, KD, VD>::Bytes;
   if (!allow(kern, bytes)) return GDN_ERR_CUDA;
-  kern<<<(unsigned)((int64_t)most * d.Hv), kThreads32<KD>, bytes, s>>>(x, ldx, y, ldy, d, g, pc, factor, S, total,
-                                                                       status);
+  const int64_t grid = (int64_t)most * d.Hv * (d.K / KD) * (d.V / VD);
+  kern<<<(unsigned)grid, N, bytes, s>>>(x, ldx, y, ldy, d, g, pc, factor, S, total, status);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-template <int KD, int VD>
+template <int VD, int NV, int KB>
 gdn_status outputs(const Shape& d, const float* q, const float* k, const float* v, const float* g, const Pieces& pc,
                    int most, float scale, const float* S0, float* o, int32_t* status, cudaStream_t s) {
-  auto kern = outputs_tc32_kernel<KD, VD>;
-  constexpr uint32_t bytes = OutMap32<KD, VD>::Bytes;
-  static_assert(bytes <= 232448, "shared memory of one SM");
+  auto kern = outputs_tc32_kernel<VD, NV, KB>;
+  constexpr uint32_t bytes = OutMap32<VD>::Bytes;
   if (!allow(kern, bytes)) return GDN_ERR_CUDA;
-  kern<<<(unsigned)((int64_t)most * d.Hv), kThreads32<KD>, bytes, s>>>(q, k, v, d, g, pc, scale, S0, o, status);
+  const int64_t grid = (int64_t)most * d.Hv * NV;
+  kern<<<(unsigned)grid, N, bytes, s>>>(q, k, v, d, g, pc, scale, S0, o, status);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
 
-#define GDN_HEADS(CALL)                          \
-  if (d.K == 64 && d.V == 64) return CALL(64, 64); \
-  if (d.K == 64) return CALL(64, 128);           \
-  if (d.V == 64) return CALL(128, 64);           \
-  return CALL(128, 128)
-
-gdn_status launch_states32(bool adj, const Shape& d, const float* x, int64_t ldx, const float* y, int64_t ldy,
-                           const float* g, const Pieces& pc, int most, float factor, float* S, float* total,
-                           int32_t* status, cudaStream_t s) {
-#define GDN_CALL(K, V)                                                                          \
-  adj ? states<K, V, true>(d, x, ldx, y, ldy, g, pc, most, factor, S, total, status, s)         \
-      : states<K, V, false>(d, x, ldx, y, ldy, g, pc, most, factor, S, total, status, s)
-  GDN_HEADS(GDN_CALL);
-#undef GDN_CALL
+template <typename T, bool ADJ>
+gdn_status launch_states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g,
+                         const Pieces& pc, int most, float factor, float* S, float* total, int32_t* status,
+                         cudaStream_t s) {
+  if (most == 0) return GDN_OK;
+#define GDN_STATES(K, V) return states<T, K, V, ADJ>(d, x, ldx, y, ldy, g, pc, most, factor, S, total, status, s)
+  if (d.K == 64 && d.V != 64) GDN_STATES(64, 128);
+  if (d.K != 64 && d.V == 64) GDN_STATES(128, 64);
+  if constexpr (sizeof(T) == 4) {   // bf16 comes here with a head dim of 256 alone
+    if (d.K == 64) GDN_STATES(64, 64);
+  }
+  GDN_STATES(128, 128);
+#undef GDN_STATES
 }
 
-gdn_status launch_outputs32(const Shape& d, const float* q, const float* k, const float* v, const float* g,
-                            const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
-                            cudaStream_t s) {
-#define GDN_CALL(K, V) outputs<K, V>(d, q, k, v, g, pc, most, scale, S0, o, status, s)
-  GDN_HEADS(GDN_CALL);
-#undef GDN_CALL
+gdn_status launch_outputs(const Shape& d, const float* q, const float* k, const float* v, const float* g,
+                          const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
+                          cudaStream_t s) {
+  if (most == 0) return GDN_OK;
+#define GDN_OUTPUTS(KB)                                                                        \
+  (d.V == 64 ? outputs<64, 1, KB> : d.V == 128 ? outputs<128, 1, KB> : outputs<128, 2, KB>)(   \
+      d, q, k, v, g, pc, most, scale, S0, o, status, s)
+  if (d.K == 64) return GDN_OUTPUTS(1);
+  return d.K == 128 ? GDN_OUTPUTS(2) : GDN_OUTPUTS(4);
+#undef GDN_OUTPUTS
 }
-#undef GDN_HEADS
+
+#define GDN_INSTANCE(T)                                                                                              \
+  template gdn_status launch_states<T, false>(const Shape&, const T*, int64_t, const T*, int64_t, const float*,      \
+                                              const Pieces&, int, float, float*, float*, int32_t*, cudaStream_t);    \
+  template gdn_status launch_states<T, true>(const Shape&, const T*, int64_t, const T*, int64_t, const float*,       \
+                                             const Pieces&, int, float, float*, float*, int32_t*, cudaStream_t)
+GDN_INSTANCE(float);
+GDN_INSTANCE(__nv_bfloat16);
+#undef GDN_INSTANCE
 
 }  // namespace lin
 }  // namespace gdn

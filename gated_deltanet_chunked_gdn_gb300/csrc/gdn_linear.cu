@@ -1,7 +1,7 @@
 // gdn_linear.cu -- decayed linear attention: the forward pass's dispatch (bf16: the walk of gdn_linear_tc.cu; fp32:
 // three launches over 64-token chunks, the chunks' own states, the sums along each sequence, the outputs, with the
 // kernels of gdn_linear_tc32.cu), the tables of packed batches, and the step on a state pool.
-#include "gdn_linear_simt.cuh"
+#include "gdn_linear_sums.cuh"
 
 namespace gdn {
 namespace lin {

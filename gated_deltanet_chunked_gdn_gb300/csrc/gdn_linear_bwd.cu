@@ -1,4 +1,5 @@
-// gdn_linear_bwd.cu -- backward of decayed linear attention, in fp32 arithmetic for every type and head dim.
+// gdn_linear_bwd.cu -- backward of decayed linear attention with fp32 precision throughout, for fp32 and for bf16 with
+// a head dim of 256 (other bf16 problems: gdn_linear_tc_bwd.cu).
 //
 // With S0 the state before a chunk, G the adjoint of the state behind it, M_ij = e^{b_i - b_j} (j <= i), w_j =
 // e^{b_last - b_j}:
@@ -12,224 +13,422 @@
 // sums of k_j . (w_j G v_j), past it e^{b_last} <G, S0>.  Every chunk forms its own, so that no rounding is carried from
 // chunk to chunk.  Heads that share q and k write their dq and dk to the workspace in fp32; a launch behind adds them
 // in order.
-#include "gdn_linear_simt.cuh"
+#include "gdn_linear_tc32.cuh"
 
 namespace gdn {
 namespace lin {
 namespace {
 
-// Sum over the 16 threads of a row of the 16 x 16 grid (half a warp).
-__device__ __forceinline__ float row16(float v) {
+constexpr int kGradThreads = 512;
+
+// Over a warp: x[j] summed over the lanes, in lane sum_of16(lane) = j (and in the lane beside it).
+__device__ __forceinline__ int sum_of16(int lane) {
+  return (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
+}
+__device__ __forceinline__ float reduce16(float (&x)[16], int lane) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int n = 8; n >= 1; n >>= 1) {
+    const bool upper = lane & (2 * n);
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float give = upper ? x[j] : x[j + n], keep = upper ? x[j + n] : x[j];
+      x[j] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
+    }
+  }
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
 }
 
-// Gradients of one chunk of one value head.
-template <typename T, typename TG>
-__global__ void __launch_bounds__(kThreads) grads_kernel(
+// A term's tile of 64 rows of 64: 8 KB.  DB, EB: columns of K, of V a stage takes.
+template <typename T, int DB, int EB>
+struct GradMap32 {
+  static constexpr int TERMS = kTerms<T>;
+  static constexpr uint32_t kT = 8192;
+  // stages: Q | K;  dO | V | S0 [d][e] | G;  K | Q, DB columns each;  G [d][e] | K | dO
+  static constexpr uint32_t kKQ = 64 * DB * 2, kSG = DB * 128, kGE = 64 * EB * 2;
+  static constexpr uint32_t S = 2 * TERMS * kT, G = S + 3 * kSG;
+  static constexpr uint32_t KE = 3 * kGE, OE = KE + TERMS * kT;
+  static constexpr uint32_t kEnd1 = G + 3 * kSG, kEnd2 = 2 * TERMS * kKQ, kEnd3 = OE + TERMS * kGE;
+  static constexpr uint32_t W = kEnd1 > kEnd2 ? (kEnd1 > kEnd3 ? kEnd1 : kEnd3) : (kEnd2 > kEnd3 ? kEnd2 : kEnd3);
+  static constexpr uint32_t P = W + 3 * kT;
+  static constexpr uint32_t Misc = P + 3 * kT;
+  static constexpr uint32_t Hi = Misc, Lo = Misc + 256, Up = Misc + 512, Down = Misc + 768;
+  static constexpr uint32_t RowA = Misc + 1024, ColA = RowA + 1024;   // [4 parts][64], [2 warps' rows][64]
+  static constexpr uint32_t SumQ = ColA + 512, SumK = SumQ + 1024;    // [4 warps' rows][64] each
+  static constexpr uint32_t Red = SumK + 1024, Bar = Red + 64, Flags = Bar + 8;
+  static constexpr uint32_t Bytes = Flags + 56 + 1024;
+};
+
+// Gradients of one chunk of one value head.  TMEM lane = token (Q K^T, dO V^T) or column of K or V (all else, so that a
+// warp writes 32 neighbours of a row); one batch of products at a time, the next tiles' loads under it.
+template <typename T, typename TG, int DB, int EB>
+__global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ dout, Shape d,
     const float* __restrict__ g, Pieces pc, float scale, const float* __restrict__ S0, const float* __restrict__ G,
-    TG* __restrict__ dq, TG* __restrict__ dk, T* __restrict__ dv, float* __restrict__ dg) {
-  extern __shared__ __align__(16) float sm[];
-  float* As = sm;                      // operands of the running product
-  float* Bs = As + kC * kLd;
-  float* Pn = Bs + kC * kLd;           // P [i][j]
-  float* Wn = Pn + kC * kLd;           // W [i][j]
-  float* Wt = Wn + kC * kLd;           // W [j][i]
-  float* hi = Wt + kC * kLd;
-  float* lo = hi + kC;
-  float* up = lo + kC;                 // scale e^{b_i}
-  float* down = up + kC;               // e^{b_last - b_j}
-  float* row = down + kC;              // row sums of A, then with what comes into the chunk
-  float* out = row + kC;               // what leaves the chunk
-  float* colp = out + kC;              // [16][64] column sums of A, by row group
-  float* red = colp + 16 * kC;         // [8] warps' parts of <G, S0>
+    TG* __restrict__ dq, TG* __restrict__ dk, T* __restrict__ dv, float* __restrict__ dg, int32_t* status) {
+  using M = GradMap32<T, DB, EB>;
+  constexpr int TERMS = M::TERMS, N = kGradThreads;
+  constexpr uint32_t kT = M::kT;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int c = blockIdx.x / d.Hv, h = blockIdx.x % d.Hv, hq = h / (d.Hv / d.Hqk);
   const Piece p = piece_of(pc, c);
   if (!p.ok) return;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  if (tid < 32) chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, tid, hi, lo);
-  __syncthreads();
-  if (tid < kC) {
-    up[tid] = scale * expf(hi[tid] + lo[tid]);
-    down[tid] = expf((hi[kC - 1] - hi[tid]) + (lo[kC - 1] - lo[tid]));
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
+  float *hi = reinterpret_cast<float*>(sm + M::Hi), *lo = reinterpret_cast<float*>(sm + M::Lo);
+  float *up = reinterpret_cast<float*>(sm + M::Up), *down = reinterpret_cast<float*>(sm + M::Down);
+  float *rowa = reinterpret_cast<float*>(sm + M::RowA), *cola = reinterpret_cast<float*>(sm + M::ColA);
+  float *sumq = reinterpret_cast<float*>(sm + M::SumQ), *sumk = reinterpret_cast<float*>(sm + M::SumK);
+  float* red = reinterpret_cast<float*>(sm + M::Red);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::Bar);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(sm + M::Flags);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qd = warp & 3, part = warp >> 2, row = 32 * qd + lane, t0 = 16 * part;   // lane of TMEM, first of 16 columns
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_fence_init();
   }
+  if (warp == 0) tmem_alloc(flags, 512);
+  if (warp == 1) {
+    chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
+    __syncwarp();
+#pragma unroll
+    for (int r = lane; r < kC; r += 32) {
+      up[r] = scale * expf(hi[r] + lo[r]);
+      down[r] = expf((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags);
+  const uint32_t mine = tmem + (static_cast<uint32_t>(32 * qd) << 16) + t0;
+  // columns; a sum over several tiles has another accumulator 64 behind, for all but the products of first terms
+  constexpr uint32_t QK = 0, OV = 128, IQ = 256, IK = 384, WK = OV, WQ = OV + 64, IV = QK, PO = OV;
+
   const T* qp = q + p.tok0 * d.ldq + (int64_t)hq * d.K;
   const T* kp = k + p.tok0 * d.ldk + (int64_t)hq * d.K;
   const T* vp = v + p.tok0 * d.ldv + (int64_t)h * d.V;
-  const int64_t ldo = (int64_t)d.Hv * d.V;
+  const int64_t ldo = (int64_t)d.Hv * d.V, ldg = (int64_t)d.Hv * d.K;
   const T* op = dout + p.tok0 * ldo + (int64_t)h * d.V;
-  float acc[4][4], qk[4][4];
-  zero(qk);
-  for (int d0 = 0; d0 < d.K; d0 += kC) {
-    __syncthreads();
-    load_t(As, qp + d0, d.ldq, p.len, nullptr);
-    load_t(Bs, kp + d0, d.ldk, p.len, nullptr);
-    __syncthreads();
-    fma_tile(qk, As, Bs, ty, tx);
-  }
-  zero(acc);
-  for (int e0 = 0; e0 < d.V; e0 += kC) {
-    __syncthreads();
-    load_t(As, op + e0, ldo, p.len, nullptr);
-    load_t(Bs, vp + e0, d.ldv, p.len, nullptr);
-    __syncthreads();
-    fma_tile(acc, As, Bs, ty, tx);
-  }
-  {
-    float rs[4] = {0.f, 0.f, 0.f, 0.f}, cs[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* sp = S0 + ((int64_t)c * d.Hv + h) * d.K * d.V;
+  const float* gp = G + ((int64_t)c * d.Hv + h) * d.K * d.V;
+
+  int n = 0;          // batches of products issued
+  bool good = true;
+  auto drained = [&] {   // they have been read and summed
+    if (good && n > 0) good = warp_wait(bar, (n - 1) & 1, status);
+  };
+  auto ready = [&] {     // tiles are in place, TMEM has been read
+    fence_proxy_async();
+    tc_fence_before();
+    if (__syncthreads_or(!good)) good = false;
+    tc_fence_after();
+    return good;
+  };
+  // one step of 16 of a sum over tiles at column `at`: products of terms a and b, in products()'s order
+  auto tiles = [&](uint32_t at, uint64_t A, uint64_t B, uint32_t id, int a, int b, uint32_t more, bool begun) {
+    const bool first = a + b == 0;
+    mma_bf16(tmem + at + (first ? 0 : 64), A, B, id, begun ? 1u : (first ? 0u : more));
+  };
+  auto sum_ld = [&](uint32_t at, float (&x)[16], bool rest) {
+    tmem_ld16(mine + at, x);
+    if (rest) {
+      float y[16];
+      tmem_ld16(mine + at + 64, y);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = 4 * ty + r, j = 4 * tx + u;
-        const float m = j <= i ? scale * expf((hi[i] - hi[j]) + (lo[i] - lo[j])) : 0.f;
-        const float pv = j <= i ? m * qk[r][u] : 0.f, wv = j <= i ? m * acc[r][u] : 0.f;
-        const float a = j < i ? wv * qk[r][u] : 0.f;   // a token with itself has no decay between
-        Pn[i * kLd + j] = pv;
-        Wn[i * kLd + j] = wv;
-        Wt[j * kLd + i] = wv;
-        rs[r] += a;
-        cs[u] += a;
-      }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      rs[r] = row16(rs[r]);
-      if (tx == 0) row[4 * ty + r] = rs[r], out[4 * ty + r] = 0.f;
+      for (int j = 0; j < 16; ++j) x[j] += y[j];
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) colp[ty * kC + 4 * tx + u] = cs[u];
-  }
-  const float* S = S0 + ((int64_t)c * d.Hv + h) * d.K * d.V;
-  const float* A = G + ((int64_t)c * d.Hv + h) * d.K * d.V;
-  // dv = P^T do + w (k G)
-  for (int e0 = 0; e0 < d.V; e0 += kC) {
-    zero(acc);
-    __syncthreads();
-    load_n(Bs, op + e0, ldo, p.len, nullptr);
-    __syncthreads();
-    fma_tile(acc, Pn, Bs, ty, tx);
-    for (int d0 = 0; d0 < d.K; d0 += kC) {
-      __syncthreads();
-      load_t(As, kp + d0, d.ldk, p.len, down);
-      load_n(Bs, A + (int64_t)d0 * d.V + e0, d.V, kC, nullptr);
-      __syncthreads();
-      fma_tile(acc, As, Bs, ty, tx);
+  };
+
+  // ---- Q K^T
+#pragma unroll 1
+  for (int kb = 0; kb < d.K / 64 && good; ++kb) {
+    float4 xq[2], xk[2];
+    fetch<64, 64, N>(xq, qp + 64 * kb, d.ldq, p.len);
+    fetch<64, 64, N>(xk, kp + 64 * kb, d.ldk, p.len);
+    drained();
+    if (good) {
+      place<64, 64, TERMS, N>(sm, xq, nullptr);
+      place<64, 64, TERMS, N>(sm + TERMS * kT, xk, nullptr);
     }
+    if (!ready()) break;
+    if (tid == 0) {
+      const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
+      products<TERMS, TERMS>([&](int a, int b, uint32_t more) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = 4 * ty + r;
-      if (j < p.len) store4(dv + (p.tok0 + j) * ldo + (int64_t)h * d.V + e0 + 4 * tx, acc[r]);
+        for (int s = 0; s < 4; ++s)
+          tiles(QK, dsw(s4, a * kT + s * 32, 16), dsw(s4, (TERMS + b) * kT + s * 32, 16), id, a, b, more,
+                kb > 0 || s > 0);
+      });
+      mma_commit(bar);
     }
+    ++n;
+    __syncwarp();
   }
-  // dq = W k + scale e^b (do S0^T),  dk = W^T q + w (v G^T); TG rows: value heads, or the q/k heads themselves
-  const int64_t ldg = (int64_t)d.Hv * d.K;
+  // ---- DB columns of dq, dk at a time
   float gs = 0.f;   // <G, S0>
-  for (int d0 = 0; d0 < d.K; d0 += kC) {
-    zero(acc);
-    for (int e0 = 0; e0 < d.V; e0 += kC) {
-      __syncthreads();
-      load_t(As, op + e0, ldo, p.len, up);
-      load_t(Bs, S + (int64_t)d0 * d.V + e0, d.V, kC, nullptr);
-      __syncthreads();
-      fma_tile(acc, As, Bs, ty, tx);
+#pragma unroll 1
+  for (int db = 0; db < d.K / DB && good; ++db) {
+#pragma unroll 1
+    for (int vb = 0; vb < d.V / 64 && good; ++vb) {
+      float4 xo[2], xv[2], xs[DB / 32], xg[DB / 32];
+      fetch<64, 64, N>(xo, op + 64 * vb, ldo, p.len);
+      fetch<64, 64, N>(xv, vp + 64 * vb, d.ldv, p.len);
+      fetch<DB, 64, N>(xs, sp + (int64_t)db * DB * d.V + 64 * vb, d.V, DB);
+      fetch<DB, 64, N>(xg, gp + (int64_t)db * DB * d.V + 64 * vb, d.V, DB);
 #pragma unroll
-      for (int r = ty; r < kC; r += 16) {   // Bs is [e][d]
-        const float4 s4 = *reinterpret_cast<const float4*>(Bs + r * kLd + 4 * tx);
-        const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+      for (int u = 0; u < DB / 32; ++u)
+        gs = fmaf(xs[u].x, xg[u].x, fmaf(xs[u].y, xg[u].y, fmaf(xs[u].z, xg[u].z, fmaf(xs[u].w, xg[u].w, gs))));
+      drained();
+      if (good) {
+        place<64, 64, TERMS, N>(sm, xo, nullptr);
+        place<64, 64, TERMS, N>(sm + TERMS * kT, xv, nullptr);
+        place<DB, 64, 3, N>(sm + M::S, xs, nullptr);
+        place<DB, 64, 3, N>(sm + M::G, xg, nullptr);
+      }
+      if (!ready()) break;
+      if (tid == 0) {
+        const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
+        if (db == 0)
+          products<TERMS, TERMS>([&](int a, int b, uint32_t more) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) gs = fmaf(sv[u], A[(int64_t)(d0 + 4 * tx + u) * d.V + e0 + r], gs);
+            for (int s = 0; s < 4; ++s)
+              tiles(OV, dsw(s4, a * kT + s * 32, 16), dsw(s4, (TERMS + b) * kT + s * 32, 16), id, a, b, more,
+                    vb > 0 || s > 0);
+          });
+        products<3, TERMS>([&](int a, int b, uint32_t more) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            tiles(IQ, dsw(s4, M::S + a * M::kSG + s * 32, 16), dsw(s4, b * kT + s * 32, 16), id, a, b, more,
+                  vb > 0 || s > 0);
+        });
+        products<3, TERMS>([&](int a, int b, uint32_t more) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            tiles(IK, dsw(s4, M::G + a * M::kSG + s * 32, 16), dsw(s4, (TERMS + b) * kT + s * 32, 16), id, a, b, more,
+                  vb > 0 || s > 0);
+        });
+        mma_commit(bar);
+      }
+      ++n;
+      __syncwarp();
+    }
+    if (!good) break;
+    float4 xk[DB / 32], xq[DB / 32];
+    fetch<64, DB, N>(xk, kp + db * DB, d.ldk, p.len);
+    fetch<64, DB, N>(xq, qp + db * DB, d.ldq, p.len);
+    drained();
+    tc_fence_after();
+    if (db == 0 && qd < 2 && good) {   // W, P and the sums of A: 16 columns of row `row`
+      float qk[16], ov[16];
+      sum_ld(QK, qk, TERMS > 1);
+      sum_ld(OV, ov, TERMS > 1);
+      const float b0 = hi[row], b1 = lo[row];
+      float rs = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int col = t0 + j;
+        const float m = scale * expf((b0 - hi[col]) + (b1 - lo[col]));
+        const float w = col <= row ? m * ov[j] : 0.f, a = col < row ? w * qk[j] : 0.f;   // a token with itself has no
+        qk[j] = col <= row ? m * qk[j] : 0.f;                                            // decay between
+        rs += a;
+        ov[j] = w;
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float(&x)[16] = m ? qk : ov;
+        uint8_t* at = sm + (m ? M::P : M::W);
+#pragma unroll
+        for (int j = 0; j < 16; j += 8) {
+          uint32_t a0[2], a1[2], a2[2], c0[2], c1[2], c2[2];
+          split3(make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]), a0, a1, a2);
+          split3(make_float4(x[j + 4], x[j + 5], x[j + 6], x[j + 7]), c0, c1, c2);
+          uint8_t* to = at + sw128_chunk(row, (t0 + j) >> 3);
+          *reinterpret_cast<uint4*>(to) = make_uint4(a0[0], a0[1], c0[0], c0[1]);
+          *reinterpret_cast<uint4*>(to + kT) = make_uint4(a1[0], a1[1], c1[0], c1[1]);
+          *reinterpret_cast<uint4*>(to + 2 * kT) = make_uint4(a2[0], a2[1], c2[0], c2[1]);
+        }
+      }
+      // A's columns: w (q k) again, from the products
+      float x[16];
+      sum_ld(QK, x, TERMS > 1);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = t0 + j < row ? ov[j] * x[j] : 0.f;
+      rowa[part * 64 + row] = rs;
+      const float cs = reduce16(x, lane);
+      if (!(lane & 1)) cola[qd * 64 + t0 + sum_of16(lane)] = cs;
+    }
+    if (good) {
+      place<64, DB, TERMS, N>(sm, xk, nullptr);
+      place<64, DB, TERMS, N>(sm + TERMS * M::kKQ, xq, nullptr);
+    }
+    if (!ready()) break;
+    if (tid == 0) {
+      const uint32_t idn = idesc_bf16(128, 64, 1, 0, 0), idt = idesc_bf16(128, 64, 1, 1, 0);
+      products<TERMS, 3>([&](int a, int b, uint32_t more) {   // (W K)^T: lanes d, columns i
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(tmem + WK, dsw(s4, a * M::kKQ + s * 2048, kT), dsw(s4, M::W + b * kT + s * 32, 16), idn,
+                   s > 0 ? 1u : more);
+      });
+      products<TERMS, 3>([&](int a, int b, uint32_t more) {   // (W^T Q)^T: lanes d, columns j
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(tmem + WQ, dsw(s4, (TERMS + a) * M::kKQ + s * 2048, kT), dsw(s4, M::W + b * kT + s * 2048, kT), idt,
+                   s > 0 ? 1u : more);
+      });
+      mma_commit(bar);
+    }
+    ++n;
+    __syncwarp();
+    drained();
+    tc_fence_after();
+    if (good) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {   // dq, dk: column db DB + row of 16 tokens
+        const T* src = (m ? kp : qp) + db * DB + row;
+        const int64_t ld = m ? d.ldk : d.ldq;
+        TG* to = (m ? dk : dq) + p.tok0 * ldg + (int64_t)h * d.K + db * DB + row;
+        const float* f = m ? down : up;
+        float in[16], own[16];
+        sum_ld(m ? IK : IQ, in, true);
+        tmem_ld16(mine + (m ? WQ : WK), own);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int t = t0 + j;
+          const bool is = t < p.len && row < DB;
+          const float y = f[t] * in[j];
+          if (is) to[t * ldg] = from_f<TG>(own[j] + y);
+          in[j] = is ? to_f(src[t * ld]) * y : 0.f;
+        }
+        const float s = reduce16(in, lane);
+        float* at = (m ? sumk : sumq) + qd * 64 + t0 + sum_of16(lane);
+        if (!(lane & 1)) *at = db ? *at + s : s;
       }
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 4 * ty + r;
-      float s = 0.f;
-      if (i < p.len) {
-        const float4 x = load4(qp + i * d.ldq + d0 + 4 * tx);
-        s = x.x * acc[r][0] + x.y * acc[r][1] + x.z * acc[r][2] + x.w * acc[r][3];
+  }
+  // ---- EB columns of dv at a time
+#pragma unroll 1
+  for (int eb = 0; eb < d.V / EB && good; ++eb) {
+#pragma unroll 1
+    for (int kb = 0; kb < d.K / 64 && good; ++kb) {
+      float4 xg[EB / 32], xk[2], xo[EB / 32];
+      fetch<64, EB, N>(xg, gp + (int64_t)64 * kb * d.V + eb * EB, d.V, 64);
+      fetch<64, 64, N>(xk, kp + 64 * kb, d.ldk, p.len);
+      if (kb == 0) fetch<64, EB, N>(xo, op + eb * EB, ldo, p.len);
+      drained();
+      if (good) {
+        place<64, EB, 3, N>(sm, xg, nullptr);
+        place<64, 64, TERMS, N>(sm + M::KE, xk, nullptr);
+        if (kb == 0) place<64, EB, TERMS, N>(sm + M::OE, xo, nullptr);
       }
-      s = row16(s);
-      if (tx == 0) row[i] += s;
-    }
-    __syncthreads();
-    load_n(Bs, kp + d0, d.ldk, p.len, nullptr);
-    __syncthreads();
-    fma_tile(acc, Wt, Bs, ty, tx);
+      if (!ready()) break;
+      if (tid == 0) {
+        const uint32_t idn = idesc_bf16(128, 64, 1, 0, 0), idt = idesc_bf16(128, 64, 1, 1, 0);
+        products<3, TERMS>([&](int a, int b, uint32_t more) {   // (K G)^T: lanes e, columns j
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 4 * ty + r;
-      if (i < p.len) store4(dq + (p.tok0 + i) * ldg + (int64_t)h * d.K + d0 + 4 * tx, acc[r]);
-    }
-    zero(acc);
-    for (int e0 = 0; e0 < d.V; e0 += kC) {
-      __syncthreads();
-      load_t(As, vp + e0, d.ldv, p.len, down);
-      load_t(Bs, A + (int64_t)d0 * d.V + e0, d.V, kC, nullptr);
-      __syncthreads();
-      fma_tile(acc, As, Bs, ty, tx);
-    }
+          for (int s = 0; s < 4; ++s)
+            tiles(IV, dsw(s4, a * M::kGE + s * 2048, kT), dsw(s4, M::KE + b * kT + s * 32, 16), idn, a, b, more,
+                  kb > 0 || s > 0);
+        });
+        if (kb == 0)
+          products<TERMS, 3>([&](int a, int b, uint32_t more) {   // (P^T dO)^T
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = 4 * ty + r;
-      float s = 0.f;
-      if (j < p.len) {
-        const float4 x = load4(kp + j * d.ldk + d0 + 4 * tx);
-        s = x.x * acc[r][0] + x.y * acc[r][1] + x.z * acc[r][2] + x.w * acc[r][3];
+            for (int s = 0; s < 4; ++s)
+              mma_bf16(tmem + PO, dsw(s4, M::OE + a * M::kGE + s * 2048, kT), dsw(s4, M::P + b * kT + s * 2048, kT), idt,
+                       s > 0 ? 1u : more);
+          });
+        mma_commit(bar);
       }
-      s = row16(s);
-      if (tx == 0) out[j] += s;
+      ++n;
+      __syncwarp();
     }
-    __syncthreads();
-    load_n(Bs, qp + d0, d.ldq, p.len, nullptr);
-    __syncthreads();
-    fma_tile(acc, Wn, Bs, ty, tx);
+    drained();
+    tc_fence_after();
+    if (good) {
+      float in[16], own[16];
+      sum_ld(IV, in, true);
+      tmem_ld16(mine + PO, own);
+      T* to = dv + p.tok0 * ldo + (int64_t)h * d.V + eb * EB + row;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = 4 * ty + r;
-      if (j < p.len) store4(dk + (p.tok0 + j) * ldg + (int64_t)h * d.K + d0 + 4 * tx, acc[r]);
+      for (int j = 0; j < 16; ++j)
+        if (t0 + j < p.len && row < EB) to[(t0 + j) * ldo] = from_f<T>(fmaf(down[t0 + j], in[j], own[j]));
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
-  if ((tid & 31) == 0) red[tid >> 5] = gs;
-  __syncthreads();
-  if (tid < kC) {
-    float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s += colp[r * kC + tid];
-    row[tid] -= s;
-  }
-  __syncthreads();
-  if (tid < 32) {
+  if (lane == 0) red[warp] = gs;
+  tc_fence_before();
+  const bool stop = __syncthreads_or(!good);
+  if (stop && tid == 0 && n > 0) mbar_wait(bar, (n - 1) & 1, status, 100000000ull);   // products under way end first
+  if (!stop && warp == 1) {
     // dg_s = sum_{i >= s} row_i + sum_{j < s} out_j + e^{b_last} <G, S0>
     double past = 0.0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) past += red[w];
+    for (int w = 0; w < N / 32; ++w) past += red[w];
     past *= (double)expf(hi[kC - 1] + lo[kC - 1]);
-    const int r = 2 * tid;
-    const double ra = row[r], rb = row[r + 1], oa = out[r], ob = out[r + 1];
-    double suf = ra + rb, pre = oa + ob;
+    const int r = 2 * lane;
+    double rw[2], ot[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      rw[u] = -(double)cola[r + u] - cola[64 + r + u], ot[u] = 0.0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        rw[u] += (double)rowa[w * 64 + r + u];
+        if (32 * w < DB) rw[u] += (double)sumq[w * 64 + r + u], ot[u] += (double)sumk[w * 64 + r + u];
+      }
+    }
+    double suf = rw[0] + rw[1], pre = ot[0] + ot[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double a = __shfl_down_sync(0xffffffffu, suf, o), b = __shfl_up_sync(0xffffffffu, pre, o);
-      if (tid + o < 32) suf += a;
-      if (tid >= o) pre += b;
+      if (lane + o < 32) suf += a;
+      if (lane >= o) pre += b;
     }
-    pre -= oa + ob;
-    const double x0 = suf + pre + past, x1 = suf - ra + pre + oa + past;
+    pre -= ot[0] + ot[1];
+    const double x0 = suf + pre + past, x1 = suf - rw[0] + pre + ot[0] + past;
     if (d.g_per_head) {
       double s = (r < p.len ? x0 : 0.0) + (r + 1 < p.len ? x1 : 0.0);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (tid == 0) dg[(int64_t)c * d.Hv + h] = (float)s;
+      if (lane == 0) dg[(int64_t)c * d.Hv + h] = (float)s;
     } else {
-      float* gp = dg + p.tok0 * d.Hv + h;
-      if (r < p.len) gp[(int64_t)r * d.Hv] = (float)x0;
-      if (r + 1 < p.len) gp[(int64_t)(r + 1) * d.Hv] = (float)x1;
+      float* to = dg + p.tok0 * d.Hv + h;
+      if (r < p.len) to[(int64_t)r * d.Hv] = (float)x0;
+      if (r + 1 < p.len) to[(int64_t)(r + 1) * d.Hv] = (float)x1;
     }
   }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, typename TG, int DB, int EB>
+gdn_status launch_grads(int most, const T* q, const T* k, const T* v, const T* dout, const Shape& d, const float* g,
+                        const Pieces& pc, float scale, const float* S, const float* G, TG* dq, TG* dk, T* dv,
+                        float* dg, int32_t* status, cudaStream_t s) {
+  auto kern = grads_kernel<T, TG, DB, EB>;
+  constexpr int bytes = (int)GradMap32<T, DB, EB>::Bytes;
+  static_assert(bytes <= 232448, "shared memory of one SM");
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<(unsigned)((int64_t)most * d.Hv), kGradThreads, bytes, s>>>(q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv,
+                                                                     dg, status);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <typename T, typename TG>
+gdn_status run_grads(int most, const T* q, const T* k, const T* v, const T* dout, const Shape& d, const float* g,
+                     const Pieces& pc, float scale, const float* S, const float* G, TG* dq, TG* dk, T* dv, float* dg,
+                     int32_t* status, cudaStream_t s) {
+#define GDN_GRADS(DB, EB) \
+  return launch_grads<T, TG, DB, EB>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dg, status, s)
+  if (d.K == 64 && d.V != 64) GDN_GRADS(64, 128);
+  if (d.K != 64 && d.V == 64) GDN_GRADS(128, 64);
+  if constexpr (sizeof(T) == 4) {   // bf16 comes here with a head dim of 256 alone
+    if (d.K == 64) GDN_GRADS(64, 64);
+  }
+  GDN_GRADS(128, 128);
+#undef GDN_GRADS
 }
 
 // dg of fixed decays: the chunks' sums of one head, in a fixed order
@@ -248,8 +447,6 @@ __global__ void __launch_bounds__(256) head_decays_kernel(const float* __restric
   }
   if (threadIdx.x == 0) dg[h] = (float)sm[0];
 }
-
-constexpr size_t kGradSmem = sizeof(float) * (5 * kC * kLd + 6 * kC + 16 * kC + 8);
 
 struct Layout {
   size_t tables, total, part, states, adjoints, dq, dk, end;
@@ -289,18 +486,12 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
   float* part = reinterpret_cast<float*>(ws + L.part);
   const bool shared = p.Hv != p.Hqk;
   if (most > 0) {
-    const unsigned grid = (unsigned)((int64_t)most * p.Hv);
     float* dgp = p.g_per_head ? part : dg;
-    auto run = [&](auto kern, auto* a, auto* b) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem) != cudaSuccess)
-        return GDN_ERR_CUDA;
-      kern<<<grid, kThreads, kGradSmem, s>>>(q, k, v, dout, d, g, pc, scale, S, G, a, b, dv, dgp);
-      return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-    };
     if (shared)
-      st = run(grads_kernel<T, float>, reinterpret_cast<float*>(ws + L.dq), reinterpret_cast<float*>(ws + L.dk));
+      st = run_grads<T, float>(most, q, k, v, dout, d, g, pc, scale, S, G, reinterpret_cast<float*>(ws + L.dq),
+                               reinterpret_cast<float*>(ws + L.dk), dv, dgp, status, s);
     else
-      st = run(grads_kernel<T, T>, dq, dk);
+      st = run_grads<T, T>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dgp, status, s);
     if (st != GDN_OK) return st;
   }
   if (shared && most > 0) {
@@ -319,9 +510,9 @@ gdn_status launch_head_decays(const gdn_linear_problem& p, const float* part, co
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-size_t simt_bwd_bytes(const gdn_linear_problem& p) { return layout_of(p).end; }
+size_t bwd32_bytes(const gdn_linear_problem& p) { return layout_of(p).end; }
 
-gdn_status simt_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+gdn_status bwd32(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                     float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht, void* dq,
                     void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s) {
   uint8_t* at = static_cast<uint8_t*>(ws);
@@ -341,13 +532,13 @@ gdn_status simt_bwd(const gdn_linear_problem& p, const void* q, const void* k, c
 }  // namespace lin
 
 size_t linear_bwd_workspace_bytes(const gdn_linear_problem& p) {
-  return lin::tc_bwd_supported(p) ? lin::tc_bwd_bytes(p) : lin::simt_bwd_bytes(p);
+  return lin::tc_bwd_supported(p) ? lin::tc_bwd_bytes(p) : lin::bwd32_bytes(p);
 }
 
 gdn_status run_linear_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                           float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht,
                           void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s) {
-  return (lin::tc_bwd_supported(p) ? lin::tc_bwd : lin::simt_bwd)(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, s);
+  return (lin::tc_bwd_supported(p) ? lin::tc_bwd : lin::bwd32)(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, s);
 }
 
 }  // namespace gdn

@@ -1,5 +1,5 @@
-// gdn_linear_simt.cuh -- fp32 tiles of decayed linear attention: 64 x 64 x 64 products by 256 threads (4 x 4 results a
-// thread, operands in shared memory with the summed dimension outermost), and the sums along a sequence.
+// gdn_linear_sums.cuh -- sums along a sequence of what its chunks (or segments) add to the state, and over the value
+// heads of a q/k head.
 #pragma once
 
 #include <string.h>
@@ -8,9 +8,6 @@
 
 namespace gdn {
 namespace lin {
-
-constexpr int kThreads = 256;
-constexpr int kLd = 68;   // row length of a tile in shared memory: 16-byte rows, transposed stores without conflicts
 
 // Head dims and row strides of a problem.
 struct Shape {
@@ -35,69 +32,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
   *reinterpret_cast<uint2*>(p) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
-__device__ __forceinline__ void zero(float (&a)[4][4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a[i][j] = 0.f;
-}
-
-// dst[row][col] = src[row][col] * w[row] for 64 x 64 elements; rows past `rows` are zeros.
-template <typename T>
-__device__ __forceinline__ void load_n(float* dst, const T* src, int64_t ld, int rows, const float* w) {
-  const int c = 4 * (threadIdx.x & 15);
-#pragma unroll
-  for (int r = threadIdx.x >> 4; r < kC; r += kThreads / 16) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
-      x = load4(src + r * ld + c);
-      if (w) {
-        const float f = w[r];
-        x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-      }
-    }
-    *reinterpret_cast<float4*>(dst + r * kLd + c) = x;
-  }
-}
-
-// dst[col][row] = src[row][col] * w[row].
-template <typename T>
-__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t ld, int rows, const float* w) {
-  const int r = threadIdx.x & 63;
-  const float f = w ? w[r] : 1.f;
-#pragma unroll
-  for (int c = 4 * (threadIdx.x >> 6); c < kC; c += 16) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
-      x = load4(src + r * ld + c);
-      if (w) x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-    }
-    dst[c * kLd + r] = x.x, dst[(c + 1) * kLd + r] = x.y, dst[(c + 2) * kLd + r] = x.z, dst[(c + 3) * kLd + r] = x.w;
-  }
-}
-
-// acc[r][u] += sum_kk A[kk][4 ty + r] B[kk][4 tx + u] over 64 kk, two columns an instruction
-__device__ __forceinline__ void fma_tile(float (&acc)[4][4], const float* A, const float* B, int ty, int tx) {
-  float2 c[4][2];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) c[r][0] = make_float2(acc[r][0], acc[r][1]), c[r][1] = make_float2(acc[r][2], acc[r][3]);
-#pragma unroll 16
-  for (int kk = 0; kk < kC; ++kk) {
-    const float4 a = *reinterpret_cast<const float4*>(A + kk * kLd + 4 * ty);
-    const float4 b = *reinterpret_cast<const float4*>(B + kk * kLd + 4 * tx);
-    const float av[4] = {a.x, a.y, a.z, a.w};
-    const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float2 ar = make_float2(av[r], av[r]);
-      c[r][0] = __ffma2_rn(ar, b0, c[r][0]);
-      c[r][1] = __ffma2_rn(ar, b1, c[r][1]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) acc[r][0] = c[r][0].x, acc[r][1] = c[r][0].y, acc[r][2] = c[r][1].x, acc[r][3] = c[r][1].y;
 }
 
 // Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (REV: the adjoint of the

@@ -5,7 +5,7 @@
 
 #include <string.h>
 
-#include "gdn_linear_simt.cuh"
+#include "gdn_linear_sums.cuh"
 #include "gdn_solve64.cuh"
 
 namespace gdn {

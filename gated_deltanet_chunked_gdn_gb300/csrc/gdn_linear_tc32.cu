@@ -1,70 +1,17 @@
 // gdn_linear_tc32.cu -- the chunks' own states and the outputs of decayed linear attention on the tensor cores with fp32
-// precision throughout, for fp32 and for bf16 with head dims of 256.
-//
-// An fp32 value is the sum of three bf16 values to its last bit or so (8 bits each); a product of two such sums keeps
-// the six of its nine terms that reach 2^-24 of it, each exact in the fp32 accumulators (bf16 inputs are their own first
-// term).  Six bf16 products cost a sixth of 1.89 PFLOP/s, against 74 TFLOP/s of fp32 FMAs.
+// precision throughout (the backward pass also has the states of bf16 inputs with a head dim of 256 from here).
 //
 //   states:   D[e][d] = V^T (w K)                                (w_j = e^{b_last - b_j}; the adjoint's: q, do)
 //   outputs:  P = scale M (Q K^T),   o^T[e][i] = scale e^{b_i} (S0^T Q^T) + V^T P^T
 //
-// Lanes of the tensor memory are the value columns, so that a warp writes 32 neighbours of a row of S or o.  Tiles of
-// 64 rows or columns are read as 128 where they stand in A; the lanes behind them are ignored.
-#include "gdn_linear_tc.cuh"
+// Lanes of the tensor memory are the value columns, so that a warp writes 32 neighbours of a row of S or o.
+#include "gdn_linear_tc32.cuh"
 
 namespace gdn {
 namespace lin {
 namespace {
 
 constexpr int N = 256;   // threads
-
-template <typename T>
-constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
-
-// ROWS x COLS values, four neighbours a thread at a time -> `TERMS` tiles of 64-column atom columns, row r times w[r];
-// zeros past `rows`.
-template <int ROWS, int COLS, typename T>
-__device__ __forceinline__ void fetch(float4 (&x)[ROWS * COLS / 4 / N], const T* src, int64_t ld, int rows) {
-#pragma unroll
-  for (int u = 0; u < ROWS * COLS / 4 / N; ++u) {
-    const int quad = threadIdx.x + u * N, r = quad / (COLS / 4), c = quad % (COLS / 4) * 4;
-    x[u] = r < rows ? load4(src + r * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-}
-template <int ROWS, int COLS, int TERMS>
-__device__ __forceinline__ void place(uint8_t* sm, const float4 (&x)[ROWS * COLS / 4 / N], const float* w) {
-  constexpr uint32_t tile = ROWS * COLS * 2;
-#pragma unroll
-  for (int u = 0; u < ROWS * COLS / 4 / N; ++u) {
-    const int quad = threadIdx.x + u * N, r = quad / (COLS / 4), c = quad % (COLS / 4) * 4;
-    float4 y = x[u];
-    if (w) {
-      const float f = w[r];
-      y.x *= f, y.y *= f, y.z *= f, y.w *= f;
-    }
-    uint8_t* to = sm + (c >> 6) * (ROWS * 128) + sw128_chunk(r, (c & 63) >> 3) + (c & 4) * 2;
-    if (TERMS == 1) {
-      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-    } else {
-      uint32_t w0[2], w1[2], w2[2];
-      split3(y, w0, w1, w2);
-      *reinterpret_cast<uint2*>(to) = make_uint2(w0[0], w0[1]);
-      *reinterpret_cast<uint2*>(to + tile) = make_uint2(w1[0], w1[1]);
-      *reinterpret_cast<uint2*>(to + 2 * tile) = make_uint2(w2[0], w2[1]);
-    }
-  }
-}
-
-// The products of A's and B's terms, the smallest first: f(term of A, term of B, 0 for the first one of all).
-template <int A, int B, typename F>
-__device__ __forceinline__ void products(F f) {
-  uint32_t more = 0;
-#pragma unroll
-  for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-    for (int a = 2; a >= 0; --a)
-      if (a < A && a <= sum && sum - a < B) f(a, sum - a, more), more = 1;
-}
 
 template <typename T, int KD, int VD>
 struct StateMap32 {
@@ -101,8 +48,8 @@ __global__ void __launch_bounds__(N, 2)
   }
   if (warp == 0) tmem_alloc(flags, KD);
   float4 xs[64 * KD / 4 / N], ys[64 * VD / 4 / N];
-  fetch<64, KD>(xs, x + p.tok0 * ldx + (int64_t)hq * d.K + d0, ldx, p.len);
-  fetch<64, VD>(ys, y + p.tok0 * ldy + (int64_t)h * d.V + e0, ldy, p.len);
+  fetch<64, KD, N>(xs, x + p.tok0 * ldx + (int64_t)hq * d.K + d0, ldx, p.len);
+  fetch<64, VD, N>(ys, y + p.tok0 * ldy + (int64_t)h * d.V + e0, ldy, p.len);
   if (warp == 1) {
     chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
     __syncwarp();
@@ -111,12 +58,12 @@ __global__ void __launch_bounds__(N, 2)
       w[r] = ADJ ? factor * expf(hi[r] + lo[r]) : expf((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
     if (lane == 0 && blk == 0) total[ch] = expf(hi[kC - 1] + lo[kC - 1]);
   }
-  place<64, VD, kTerms<T>>(sm + M::V, ys, nullptr);
+  place<64, VD, kTerms<T>, N>(sm + M::V, ys, nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags);
-  place<64, KD, 3>(sm + M::K, xs, w);
+  place<64, KD, 3, N>(sm + M::K, xs, w);
   fence_proxy_async();
   __syncthreads();
   if (tid == 0) {
@@ -130,7 +77,7 @@ __global__ void __launch_bounds__(N, 2)
     mma_commit(bar);
   }
   __syncwarp();
-  const bool good = mbar_wait(bar, 0, status);
+  const bool good = warp_wait(bar, 0, status);
   tc_fence_after();
   const int qd = warp & 3, part = warp >> 2, row = 32 * qd + lane;
   if (good && row < VD) {
@@ -160,9 +107,8 @@ struct OutMap32 {
 };
 
 // VD of the V = NV VD columns of the outputs of one chunk of one value head a CTA, 64 of the summed K at a time (KB of
-// them).  The
-// accumulators drop bits that small products add to large sums (o's error 6e-7 instead of 1.5e-7): with more than one
-// 64 of K, the products of first terms and all others have a sum each.
+// them).  With
+// more than one 64 of K, the products of first terms and all others have a sum each.
 template <int VD, int NV, int KB>
 __global__ void __launch_bounds__(N, 2)
     outputs_tc32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, Shape d,
@@ -204,9 +150,9 @@ __global__ void __launch_bounds__(N, 2)
 #pragma unroll 1
   for (int kb = 0; kb < KB; ++kb) {
     float4 xq[4], xk[4];
-    fetch<64, 64>(xq, qp + 64 * kb, d.ldq, p.len);
-    fetch<64, 64>(xk, kp + 64 * kb, d.ldk, p.len);
-    fetch<64, VD>(xv, sp + (int64_t)64 * kb * V, V, 64);
+    fetch<64, 64, N>(xq, qp + 64 * kb, d.ldq, p.len);
+    fetch<64, 64, N>(xk, kp + 64 * kb, d.ldk, p.len);
+    fetch<64, VD, N>(xv, sp + (int64_t)64 * kb * V, V, 64);
     if (kb == 0) {
       if (warp == 1) {
         chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
@@ -215,12 +161,12 @@ __global__ void __launch_bounds__(N, 2)
         for (int r = lane; r < kC; r += 32) up[r] = scale * expf(hi[r] + lo[r]);
       }
     } else {   // the tiles before have been read
-      good = good && mbar_wait(bars, (kb - 1) & 1, status);
-      good = good && mbar_wait(bars + 1, (kb - 1) & 1, status);
+      good = good && warp_wait(bars, (kb - 1) & 1, status);
+      good = good && warp_wait(bars + 1, (kb - 1) & 1, status);
     }
     if (good) {
-      place<64, 64, 3>(sm + M::Q, xq, nullptr);
-      place<64, 64, 3>(sm + M::K, xk, nullptr);
+      place<64, 64, 3, N>(sm + M::Q, xq, nullptr);
+      place<64, 64, 3, N>(sm + M::K, xk, nullptr);
     }
     fence_proxy_async();
     tc_fence_before();
@@ -244,7 +190,7 @@ __global__ void __launch_bounds__(N, 2)
     }
     issued0 = kb + 1;
     __syncwarp();
-    place<64, VD, 3>(sm + M::S, xv, nullptr);
+    place<64, VD, 3, N>(sm + M::S, xv, nullptr);
     fence_proxy_async();
     __syncthreads();
     if (tid == 0) {
@@ -263,8 +209,8 @@ __global__ void __launch_bounds__(N, 2)
     __syncwarp();
   }
   if (good) {
-    fetch<64, VD>(xv, v + p.tok0 * d.ldv + (int64_t)h * V + e0, d.ldv, p.len);
-    good = mbar_wait(bars, last & 1, status);
+    fetch<64, VD, N>(xv, v + p.tok0 * d.ldv + (int64_t)h * V + e0, d.ldv, p.len);
+    good = warp_wait(bars, last & 1, status);
     tc_fence_after();
   }
   constexpr int COLS = 32;   // tokens of a thread
@@ -298,8 +244,8 @@ __global__ void __launch_bounds__(N, 2)
       }
     }
   }
-  good = good && mbar_wait(bars + 1, last & 1, status);
-  if (good) place<64, VD, 3>(sm + M::V, xv, nullptr);
+  good = good && warp_wait(bars + 1, last & 1, status);
+  if (good) place<64, VD, 3, N>(sm + M::V, xv, nullptr);
   fence_proxy_async();
   tc_fence_before();
   const bool all = !__syncthreads_or(!good);
@@ -317,7 +263,7 @@ __global__ void __launch_bounds__(N, 2)
     }
     issued0 = last + 2;
     __syncwarp();
-    good = mbar_wait(bars, (last + 1) & 1, status);
+    good = warp_wait(bars, (last + 1) & 1, status);
     tc_fence_after();
     if (good && row < VD) {
       float* to = o + ((p.tok0 + part * COLS) * d.Hv + h) * (int64_t)V + e0 + row;

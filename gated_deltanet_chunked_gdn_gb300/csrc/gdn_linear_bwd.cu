@@ -495,8 +495,8 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
     if (st != GDN_OK) return st;
   }
   if (shared && most > 0) {
-    st = launch_heads<T>(p, reinterpret_cast<const float*>(ws + L.dq), pc.nc, dq, s);
-    if (st == GDN_OK) st = launch_heads<T>(p, reinterpret_cast<const float*>(ws + L.dk), pc.nc, dk, s);
+    st = launch_heads<T>(p, reinterpret_cast<const float*>(ws + L.dq), reinterpret_cast<const float*>(ws + L.dk), pc.nc,
+                         dq, dk, s);
     if (st != GDN_OK) return st;
   }
   return p.g_per_head ? launch_head_decays(p, part, pc.nc, dg, s) : GDN_OK;

@@ -106,11 +106,14 @@ gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* tot
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// dst[row][hq][:] = sum over the R value heads of a q/k head, in their order (row: a token)
+// dst[row][hq][:] = sum over the R value heads of a q/k head, in their order (row: a token); dq and dk
 template <typename T>
-__global__ void __launch_bounds__(256) heads_kernel(const float* __restrict__ src, int64_t quads, int R, int K4,
-                                                    const int32_t* __restrict__ nc, T* __restrict__ dst) {
+__global__ void __launch_bounds__(256) heads_kernel(const float* __restrict__ src0, const float* __restrict__ src1,
+                                                    int64_t quads, int R, int K4, const int32_t* __restrict__ nc,
+                                                    T* __restrict__ dst0, T* __restrict__ dst1) {
   if (nc && *nc < 0) return;
+  const float* src = blockIdx.y ? src1 : src0;
+  T* dst = blockIdx.y ? dst1 : dst0;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= quads) return;
   const int64_t head = at / K4;
@@ -124,11 +127,13 @@ __global__ void __launch_bounds__(256) heads_kernel(const float* __restrict__ sr
   store4(dst + at * 4, v);
 }
 
-// src: fp32 [B, T, Hv, K]; dst [B, T, Hqk, K].
+// dq and dk: fp32 [B, T, Hv, K] -> [B, T, Hqk, K].
 template <typename T>
-gdn_status launch_heads(const gdn_linear_problem& p, const float* src, const int32_t* nc, T* dst, cudaStream_t s) {
+gdn_status launch_heads(const gdn_linear_problem& p, const float* own_dq, const float* own_dk, const int32_t* nc, T* dq,
+                        T* dk, cudaStream_t s) {
   const int64_t quads = (int64_t)p.B * p.T * p.Hqk * (p.K / 4);
-  heads_kernel<T><<<(unsigned)ceil_div(quads, 256), 256, 0, s>>>(src, quads, p.Hv / p.Hqk, p.K / 4, nc, dst);
+  const dim3 grid((unsigned)ceil_div(quads, 256), 2);
+  heads_kernel<T><<<grid, 256, 0, s>>>(own_dq, own_dk, quads, p.Hv / p.Hqk, p.K / 4, nc, dq, dk);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

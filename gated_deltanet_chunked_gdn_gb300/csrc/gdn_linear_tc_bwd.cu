@@ -588,11 +588,9 @@ gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, con
 #undef GDN_GRADS
     if (st != GDN_OK) return st;
     if (shared) {
-      st = launch_heads<__nv_bfloat16>(p, reinterpret_cast<const float*>(at + L.dq), chunks.nc,
-                                       static_cast<__nv_bfloat16*>(dq), s);
-      if (st == GDN_OK)
-        st = launch_heads<__nv_bfloat16>(p, reinterpret_cast<const float*>(at + L.dk), chunks.nc,
-                                         static_cast<__nv_bfloat16*>(dk), s);
+      st = launch_heads<__nv_bfloat16>(p, reinterpret_cast<const float*>(at + L.dq),
+                                       reinterpret_cast<const float*>(at + L.dk), chunks.nc,
+                                       static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), s);
       if (st != GDN_OK) return st;
     }
   }

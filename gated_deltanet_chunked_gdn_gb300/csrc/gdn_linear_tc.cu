@@ -104,8 +104,9 @@ __device__ __forceinline__ Two log2_units(Two a) {
 // to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
 // differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads take 28 us, as
 // they are 8).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A
-// warp takes a chunk and head at a time.  (Within the kernels below it was one warp's work for 2000 cycles a chunk, while
-// the others waited.)
+// warp takes a chunk and head at a time.  (Within the
+// kernels below it was one warp's work for 2000 cycles a chunk, while the others waited.)  4 MB read, 17 MB written: the
+// 8 us are latency.
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
                                                      float scale, float* __restrict__ out) {
   const Piece p = piece_of(pc, blockIdx.x);
@@ -135,6 +136,11 @@ __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g
 }
 
 // The walk over a segment's chunks.  ADJ: backwards, x = q, y = do, weights scale e^{b_i}: the adjoint of the state.
+// 32 heads of 128: with outputs (kFull), 300 us for 4 x 8192 tokens and 82 for 8192 (3.6 TB/s of q, k, v and o); the
+// segments' own (kOwn) before it 117 and 37; states for the backward pass (kEmit), 139 us for 4 x 4096 tokens (5.8 TB/s,
+// 537 MB of them written: rows of S^T a lane took 152).  All but the last are bound by the chain of a chunk's phases:
+// tensor pipe 28 to 33 %, HBM 30 %, the schedulers issue a third of the time with two CTAs an SM.  A third CTA has no
+// room.
 template <int KD, int VD, int MODE, bool ADJ>
 __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     lin_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

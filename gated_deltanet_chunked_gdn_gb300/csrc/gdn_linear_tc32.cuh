@@ -19,8 +19,8 @@ namespace lin {
 template <typename T>
 constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
 
-// N threads: ROWS x COLS values, four neighbours a thread at a time -> `TERMS` tiles of 64-column atom columns, row r times w[r];
-// zeros past `rows`.
+// N threads: ROWS x COLS values, four neighbours a thread at a time -> `TERMS` tiles of 64-column atom columns, row r
+// times w[r]; zeros past `rows`.
 template <int ROWS, int COLS, int N, typename T>
 __device__ __forceinline__ void fetch(float4 (&x)[ROWS * COLS / 4 / N], const T* src, int64_t ld, int rows) {
 #pragma unroll

@@ -11,6 +11,9 @@
 // shuffles) or by the threads of a CTA, in 16-byte vectors where rows are 16-byte aligned, in single elements
 // otherwise.  The gradients of the weights are summed by column: every CTA takes rows at a fixed stride, adds each into
 // fp32 columns of its own (registers or shared memory), and a second launch adds the CTAs' columns in a fixed order.
+// Measured, of the bytes that have to move: gated norm, 16384 x 32 rows of 128 in bf16: forward 71 us (5.7 TB/s),
+// backward 115 (5.8); residual norm, 8192 x 4096 in bf16: forward 57 us (4.7); 4099 x 2500 in fp32 with a gate of its own
+// for each element: forward 37 us (5.5), backward 99 (3.3).
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -372,7 +375,9 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512, NV * VEC <= 8 ? (
 
 // Column sums of dweight, dpost_weight and dgate: in registers for rows of up to 8 elements a thread, else in shared
 // memory ([RPB][3][D]; a thread adds to columns that no other thread of its row touches).  Where registers are left, the
-// next row's loads are in flight.
+// next row's loads are in flight.  The furthest of these kernels from the bytes' time: up to five inputs a row and two
+// sums over the CTA between them and the outputs leave registers for one CTA an SM, whose threads wait.  Fewer threads a
+// row (206 us for 8192 x 4096 in bf16; 123 as it is) or 64 registers and two CTAs (326, spills) were slower.
 template <typename T, typename R, int VEC, int NV, int GROUP>
 __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ rstd,

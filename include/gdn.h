@@ -588,8 +588,10 @@ gdn_status gdn_selective_scan_step(const gdn_scan_problem* p, const void* x, con
  * multiple of 16 bytes.  g is a log decay, used as given (at most 0 in use; a
  * growing head works as long as e^{sum of g over 64 tokens} stays in fp32;
  * -infinity, or anything below -700, starts the state anew).  A NaN or an
- * infinity in a token's v or dout may reach the other tokens of its chunk (64
- * tokens of its sequence), before it as well; never another sequence.  Outputs must not
+ * infinity in a token's q, k, v or dout may reach the other tokens of its chunk
+ * (64 tokens of its sequence), before it as well, never another sequence; an
+ * infinity may come out as NaN.  fp32 values are used as sums of three bf16
+ * values: all of their 24 bits from 2^-110 up to 3.38e38.  Outputs must not
  * overlap inputs or one another, but ht may be h0 and dh0 may be h0 or dht (the
  * same pointer).
  */

@@ -375,9 +375,10 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512, NV * VEC <= 8 ? (
 
 // Column sums of dweight, dpost_weight and dgate: in registers for rows of up to 8 elements a thread, else in shared
 // memory ([RPB][3][D]; a thread adds to columns that no other thread of its row touches).  Where registers are left, the
-// next row's loads are in flight.  The furthest of these kernels from the bytes' time: up to five inputs a row and two
-// sums over the CTA between them and the outputs leave registers for one CTA an SM, whose threads wait.  Fewer threads a
-// row (206 us for 8192 x 4096 in bf16; 123 as it is) or 64 registers and two CTAs (326, spills) were slower.
+// next row's loads are in flight.  The furthest of these kernels from the bytes' time: registers for one CTA an SM, whose
+// 16 warps issue a third of the time (790 instructions a row and warp of 4096 fp32, and two sums over the CTA).  Slower
+// were, for 8192 x 4096 in bf16 (123 us), fewer threads a row (206), 64 registers and two CTAs (326, spills), the next
+// three rows in a ring in shared memory (135); for 4099 x 2500 in fp32 (99), that ring (105) and twice the threads (116).
 template <typename T, typename R, int VEC, int NV, int GROUP>
 __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ rstd,

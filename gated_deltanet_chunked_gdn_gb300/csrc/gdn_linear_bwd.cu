@@ -497,7 +497,7 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
       st = run_grads<T, T>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dgp, status, s);
     if (st != GDN_OK) return st;
   }
-  if (shared && most > 0) {
+  if (shared && (int64_t)p.B * p.T > 0) {
     st = launch_heads<T>(p, reinterpret_cast<const float*>(ws + L.dq), reinterpret_cast<const float*>(ws + L.dk), pc.nc,
                          dq, dk, s);
     if (st != GDN_OK) return st;

@@ -315,3 +315,39 @@ def test_captured_and_replayed(gdn, dtype):
     assert torch.equal(o, wo) and torch.equal(ht, wh) and torch.equal(s, ws) and torch.equal(pool, p2)
     for n in ("dq", "dk", "dv", "dg", "dh0"):
         assert torch.equal(g[n], wg[n]), n
+
+
+@pytest.mark.parametrize("dtype,V", [(BF, 128), (BF, 256), (F32, 128)])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_no_tokens_at_all(gdn, per_head, dtype, V):
+    """Packed batches whose sequences are all empty: states pass through, the decays' gradients are zero."""
+    x = make(1, 0, 2, 4, 64, V, dtype, lens=[0, 0, 0], per_head=per_head)
+    o, ht = gdn.gdn_linear_attn_fwd(x["q"], x["k"], x["v"], x["g"], h0=x["h0"], cu_seqlens=x["cu"])
+    assert o.shape == x["v"].shape and torch.equal(ht, x["h0"])
+    got = gdn.gdn_linear_attn_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], h0=x["h0"], dht=x["dht"],
+                                  cu_seqlens=x["cu"])
+    assert torch.equal(got["dh0"], x["dht"]) and got["dg"].shape == x["g"].shape and not got["dg"].any()
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 256), (128, 64), (256, 128), (256, 256)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_wide_heads_and_ragged_chunks(gdn, dtype, K, V):
+    """Every head dim in packed batches whose chunks end inside a tile, decays that are strong now and then."""
+    x = make(1, 0, 2, 6, K, V, dtype, lens=[1, 63, 0, 65, 200, 17], seed=K + V, strong=30.0)
+    check_fwd(gdn, x)
+    check_bwd(gdn, x)
+
+
+@pytest.mark.parametrize("dtype,K,V", [(F32, 64, 128), (F32, 256, 64), (BF, 256, 128)])
+def test_large_values_keep_their_neighbours_bits(gdn, dtype, K, V):
+    """Channels of very different sizes: every term of a value has to arrive, the small ones under large ones too."""
+    x = make(1, 260, 1, 2, K, V, dtype, seed=3)
+    x["q"] = x["q"] * torch.logspace(-4, 4, K, device=DEV).to(dtype)
+    x["k"] = x["k"] * torch.logspace(4, -4, K, device=DEV).to(dtype)
+    x["v"] = x["v"] * torch.logspace(-5, 5, V, device=DEV).to(dtype)
+    x["h0"] = None   # (a state beside products of these sizes would only add to them)
+    o, ht = gdn.gdn_linear_attn_fwd(x["q"], x["k"], x["v"], x["g"], scale=1.0)
+    wo, wh = ref.forward(x["q"], x["k"], x["v"], x["g"], 1.0, None, None)
+    for e in range(0, V, 16):   # each band of columns against its own norm
+        assert ref.rel(o[..., e:e + 16], wo[..., e:e + 16]) < O_TOL[dtype]
+        assert ref.rel(ht[..., e:e + 16], wh[..., e:e + 16]) < S_TOL[dtype]

@@ -227,8 +227,9 @@ template <typename T>
 gdn_status step_t(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                   float scale, float* state, const int32_t* idx, int slots, const int32_t* cu, void* o,
                   cudaStream_t s) {
-  // few heads: narrower slices, so that every SM has some (1 sequence of 32 heads of 128: 2.5 us in slices of 16)
-  if ((int64_t)p.N * p.Hv * (p.V / 64) < 2 * sm_count())
+  // few heads: narrower slices, so that every SM has some (32 heads of 128, slices of 16 and of 64 columns: 1 sequence
+  // 2.57 and 2.70 us, 4 sequences 4.87 and 3.61)
+  if (2 * (int64_t)p.N * p.Hv * (p.V / 64) < sm_count())
     return launch_step<T, 16>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, state, idx, slots, cu, (T*)o, s);
   return launch_step<T, 64>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, state, idx, slots, cu, (T*)o, s);
 }

@@ -14,7 +14,8 @@ namespace {
 __global__ void __launch_bounds__(1024) pieces_kernel(const int32_t* __restrict__ cu, int N, int T, int size, int most,
                                                       int32_t* __restrict__ seq, int32_t* __restrict__ tok0,
                                                       int32_t* __restrict__ len, int32_t* __restrict__ first,
-                                                      int32_t* __restrict__ nc, int32_t* __restrict__ status) {
+                                                      int32_t* __restrict__ nc, int32_t* __restrict__ status,
+                                                      bool begin) {
   __shared__ int warp_sum[32];
   __shared__ int carry, bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(1024) pieces_kernel(const int32_t* __restrict_
     if (total > most) bad = 1;
     first[N] = total;
     *nc = bad ? -1 : total;
-    if (bad) atomicExch(status, GDN_DEV_BAD_CU_SEQLENS);
+    if (bad || begin) *status = bad ? GDN_DEV_BAD_CU_SEQLENS : 0;
   }
   __syncthreads();
   if (bad) return;
@@ -105,12 +106,12 @@ Pieces pieces_at(const gdn_linear_problem& p, int size, void* tables) {
 }
 
 cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* cu, void* tables, int32_t* status,
-                          cudaStream_t s) {
-  if (!p.varlen) return cudaSuccess;
+                          bool begin, cudaStream_t s) {
+  if (!p.varlen) return begin ? cudaMemsetAsync(status, 0, sizeof(int32_t), s) : cudaSuccess;
   const Pieces t = pieces_at(p, size, tables);
   pieces_kernel<<<1, 1024, 0, s>>>(cu, p.N, p.T, size, pieces_max(p, size), const_cast<int32_t*>(t.seq),
                                    const_cast<int32_t*>(t.tok0), const_cast<int32_t*>(t.len),
-                                   const_cast<int32_t*>(t.first), const_cast<int32_t*>(t.nc), status);
+                                   const_cast<int32_t*>(t.first), const_cast<int32_t*>(t.nc), status, begin);
   return cudaGetLastError();
 }
 
@@ -260,9 +261,8 @@ gdn_status fwd32(const gdn_linear_problem& p, const float* q, const float* k, co
                  void* ws, cudaStream_t s) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
-  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
   void* tables = at + kAlign;
-  if (launch_pieces(p, kC, cu, tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (launch_pieces(p, kC, cu, tables, status, true, s) != cudaSuccess) return GDN_ERR_CUDA;
   const Pieces pc = pieces_at(p, kC, tables);
   const Shape d = shape_of(p);
   const int most = pieces_max(p, kC);

@@ -78,8 +78,10 @@ size_t pieces_bytes(const gdn_linear_problem& p, int size);   // 0 for equal len
 int pieces_max(const gdn_linear_problem& p, int size);
 // Status word, then (packed batches) the tables of pieces of `size` tokens.
 Pieces pieces_at(const gdn_linear_problem& p, int size, void* tables);
+// Their launch (none for equal lengths); the one that begins a call clears the status word, with a launch less for packed
+// batches.
 cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* cu, void* tables, int32_t* status,
-                          cudaStream_t s);
+                          bool begin, cudaStream_t s);
 
 // The tensor-core backward pass (gdn_linear_tc_bwd.cu).
 bool tc_bwd_supported(const gdn_linear_problem& p);

@@ -520,9 +520,8 @@ gdn_status bwd32(const gdn_linear_problem& p, const void* q, const void* k, cons
                     void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
-  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
   const Layout L = layout_of(p);
-  if (launch_pieces(p, kC, cu, at + L.tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (launch_pieces(p, kC, cu, at + L.tables, status, true, s) != cudaSuccess) return GDN_ERR_CUDA;
   const Pieces pc = pieces_at(p, kC, at + L.tables);
   if (p.dt == GDN_F32)
     return bwd_t<float>(p, (const float*)q, (const float*)k, (const float*)v, g, scale, h0, (const float*)dout, dht,

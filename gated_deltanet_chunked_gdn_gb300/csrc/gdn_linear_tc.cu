@@ -677,10 +677,9 @@ gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, con
                   void* ws, cudaStream_t s) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
-  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
   const int seg = segment_tokens(p);
   void* tables = at + kAlign;
-  if (launch_pieces(p, seg, cu, tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (launch_pieces(p, seg, cu, tables, status, true, s) != cudaSuccess) return GDN_ERR_CUDA;
   const Pieces pc = pieces_at(p, seg, tables);
   gdn_status st = launch_empty(p, pc, cu, h0, ht, idx, slots, s);
   if (st != GDN_OK || (int64_t)p.B * p.T == 0) return st;

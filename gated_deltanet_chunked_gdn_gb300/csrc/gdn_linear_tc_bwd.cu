@@ -522,9 +522,8 @@ gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, con
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
   const Layout L = layout_of(p);
-  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return GDN_ERR_CUDA;
-  if (launch_pieces(p, L.seg, cu, at + L.seg_tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
-  if (launch_pieces(p, 64, cu, at + L.chunk_tables, status, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (launch_pieces(p, L.seg, cu, at + L.seg_tables, status, true, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (launch_pieces(p, 64, cu, at + L.chunk_tables, status, false, s) != cudaSuccess) return GDN_ERR_CUDA;
   const Pieces segs = pieces_at(p, L.seg, at + L.seg_tables), chunks = pieces_at(p, 64, at + L.chunk_tables);
   gdn_status st = launch_empty(p, segs, cu, dht, dh0, nullptr, 0, s);
   if (st != GDN_OK) return st;

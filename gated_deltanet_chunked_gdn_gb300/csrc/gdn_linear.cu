@@ -115,6 +115,72 @@ cudaError_t launch_pieces(const gdn_linear_problem& p, int size, const int32_t* 
   return cudaGetLastError();
 }
 
+// ------------------------------------------------------ sums along sequences
+namespace {
+
+// Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (rev: the adjoint of the
+// state behind it); four elements of a state a thread.  2 x 4096 tokens of 16 heads of 128 (64 chunks a sequence):
+// 55 us, 4.9 TB/s; with loads only after the sums before, 132.  blockIdx.y: the first or the second of two sums.
+__global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const float* __restrict__ total, Sum first,
+                                                   Sum second) {
+  const Sum m = blockIdx.y ? second : first;
+  const float* __restrict__ init = m.init;
+  float* __restrict__ S = m.S;
+  const int64_t kv = (int64_t)d.K * d.V;
+  const int per = (int)(kv / 1024);   // CTAs a state
+  const int nh = blockIdx.x / per, n = nh / d.Hv, h = nh % d.Hv;
+  const int64_t at = ((int64_t)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
+  if (pc.seq && *pc.nc < 0) return;
+  const int c0 = pc.seq ? pc.first[n] : n * pc.per, c1 = pc.seq ? pc.first[n + 1] : c0 + pc.per;
+  float4 run = init ? load4(init + nh * kv + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  // the next four chunks' loads are under way while these are added up
+  constexpr int AHEAD = 4;
+  float4 x[2][AHEAD];
+  float a[2][AHEAD];
+  auto chunk = [&](int i) { return m.rev ? c1 - 1 - i : c0 + i; };
+  auto fetch = [&](float4 (&y)[AHEAD], float (&f)[AHEAD], int base) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (base + i < c1 - c0) {
+        y[i] = __ldcs(reinterpret_cast<const float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at));
+        f[i] = total[(int64_t)chunk(base + i) * d.Hv + h];
+      }
+  };
+  auto add = [&](const float4 (&y)[AHEAD], const float (&f)[AHEAD], int base) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (base + i < c1 - c0) {
+        *reinterpret_cast<float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at) = run;
+        run.x = fmaf(f[i], run.x, y[i].x), run.y = fmaf(f[i], run.y, y[i].y);
+        run.z = fmaf(f[i], run.z, y[i].z), run.w = fmaf(f[i], run.w, y[i].w);
+      }
+  };
+  fetch(x[0], a[0], 0);
+  for (int base = 0; base < c1 - c0; base += 2 * AHEAD) {
+    fetch(x[1], a[1], base + AHEAD);
+    add(x[0], a[0], base);
+    fetch(x[0], a[0], base + 2 * AHEAD);
+    add(x[1], a[1], base + AHEAD);
+  }
+  if (m.fin) {
+    int64_t row = n;
+    if (m.idx) {
+      row = m.idx[n];
+      if (row < 0 || row >= m.slots) return;
+    }
+    *reinterpret_cast<float4*>(m.fin + (row * d.Hv + h) * kv + at) = run;
+  }
+}
+
+}  // namespace
+
+gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const Sum& first, const Sum& second,
+                       int sides, cudaStream_t s) {
+  const int64_t grid = (int64_t)N * d.Hv * ((int64_t)d.K * d.V / 1024);
+  sums_kernel<<<dim3((unsigned)grid, sides), 256, 0, s>>>(d, pc, total, first, second);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 // -------------------------------------------------------------- the step
 namespace {
 
@@ -268,8 +334,9 @@ gdn_status fwd32(const gdn_linear_problem& p, const float* q, const float* k, co
   const int most = pieces_max(p, kC);
   float* total = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, kC));
   float* states = total + align_up(4 * (size_t)most * p.Hv) / 4;
-  gdn_status st = launch_states<float, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, states, total, status, s);
-  if (st == GDN_OK) st = launch_sums<false>(d, pc, p.N, total, h0, states, ht, idx, slots, s);
+  const Side<float> side{k, v, p.ld_k, p.ld_v, 1.f, states, false};
+  gdn_status st = launch_states(d, side, side, 1, g, pc, most, total, status, s);
+  if (st == GDN_OK) st = launch_sums(d, pc, p.N, total, Sum{h0, states, ht, idx, slots, false}, s);
   return st == GDN_OK ? launch_outputs(d, q, k, v, g, pc, most, scale, states, o, status, s) : st;
 }
 

@@ -480,11 +480,16 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
   float* total = reinterpret_cast<float*>(ws + L.total);
   float* S = reinterpret_cast<float*>(ws + L.states);
   float* G = reinterpret_cast<float*>(ws + L.adjoints);
-  gdn_status st = launch_states<T, false>(d, k, p.ld_k, v, p.ld_v, g, pc, most, 1.f, S, total, status, s);
-  if (st == GDN_OK) st = launch_sums<false>(d, pc, p.N, total, h0, S, nullptr, nullptr, 0, s);
-  if (st == GDN_OK)
-    st = launch_states<T, true>(d, q, p.ld_q, dout, (int64_t)p.Hv * p.V, g, pc, most, scale, G, total, status, s);
-  if (st == GDN_OK) st = launch_sums<true>(d, pc, p.N, total, dht, G, dh0, nullptr, 0, s);
+  const Side<T> states{k, v, p.ld_k, p.ld_v, 1.f, S, false};
+  const Side<T> adjoints{q, dout, p.ld_q, (int64_t)p.Hv * p.V, scale, G, true};
+  gdn_status st = launch_states(d, states, adjoints, 2, g, pc, most, total, status, s);
+  const Sum forth{h0, S, nullptr, nullptr, 0, false}, back{dht, G, dh0, nullptr, 0, true};
+  if (dh0 && dh0 == h0) {   // read before it is written
+    if (st == GDN_OK) st = launch_sums(d, pc, p.N, total, forth, s);
+    if (st == GDN_OK) st = launch_sums(d, pc, p.N, total, back, s);
+  } else if (st == GDN_OK) {
+    st = launch_sums(d, pc, p.N, total, forth, back, 2, s);
+  }
   if (st != GDN_OK) return st;
   float* part = reinterpret_cast<float*>(ws + L.part);
   const bool shared = p.Hv != p.Hqk;

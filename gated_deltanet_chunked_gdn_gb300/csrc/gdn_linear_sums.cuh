@@ -34,77 +34,41 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (REV: the adjoint of the
-// state behind it); four elements of a state a thread.  2 x 4096 tokens of 16 heads of 128 (64 chunks a sequence):
-// 55 us, 4.9 TB/s; with loads only after the sums before, 132.
-template <bool REV>
-__global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const float* __restrict__ total,
-                                                   const float* __restrict__ init, float* __restrict__ S,
-                                                   float* __restrict__ fin, const int32_t* __restrict__ idx,
-                                                   int slots) {
-  const int64_t kv = (int64_t)d.K * d.V;
-  const int per = (int)(kv / 1024);   // CTAs a state
-  const int nh = blockIdx.x / per, n = nh / d.Hv, h = nh % d.Hv;
-  const int64_t at = ((int64_t)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
-  if (pc.seq && *pc.nc < 0) return;
-  const int c0 = pc.seq ? pc.first[n] : n * pc.per, c1 = pc.seq ? pc.first[n + 1] : c0 + pc.per;
-  float4 run = init ? load4(init + nh * kv + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-  // the next four chunks' loads are under way while these are added up
-  constexpr int AHEAD = 4;
-  float4 x[2][AHEAD];
-  float a[2][AHEAD];
-  auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
-  auto fetch = [&](float4 (&y)[AHEAD], float (&f)[AHEAD], int base) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (base + i < c1 - c0) {
-        y[i] = __ldcs(reinterpret_cast<const float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at));
-        f[i] = total[(int64_t)chunk(base + i) * d.Hv + h];
-      }
-  };
-  auto add = [&](const float4 (&y)[AHEAD], const float (&f)[AHEAD], int base) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (base + i < c1 - c0) {
-        *reinterpret_cast<float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at) = run;
-        run.x = fmaf(f[i], run.x, y[i].x), run.y = fmaf(f[i], run.y, y[i].y);
-        run.z = fmaf(f[i], run.z, y[i].z), run.w = fmaf(f[i], run.w, y[i].w);
-      }
-  };
-  fetch(x[0], a[0], 0);
-  for (int base = 0; base < c1 - c0; base += 2 * AHEAD) {
-    fetch(x[1], a[1], base + AHEAD);
-    add(x[0], a[0], base);
-    fetch(x[0], a[0], base + 2 * AHEAD);
-    add(x[1], a[1], base + AHEAD);
-  }
-  if (fin) {
-    int64_t row = n;
-    if (idx) {
-      row = idx[n];
-      if (row < 0 || row >= slots) return;
-    }
-    *reinterpret_cast<float4*>(fin + (row * d.Hv + h) * kv + at) = run;
-  }
-}
+// A sum along every sequence (sums_kernel, gdn_linear.cu).
+struct Sum {
+  const float* init;
+  float* S;
+  float* fin;
+  const int32_t* idx;
+  int slots;
+  bool rev;
+};
 
 // What a chunk adds to the state behind it, sum_j e^{b_last - b_j} x_j y_j^T (x = k, y = v), or, for the adjoint, to
 // the one before it, factor sum_i e^{b_i} x_i y_i^T (x = q, y = do), and its whole decay; the outputs of every chunk
 // from the state before it (gdn_linear_tc32.cu).
-template <typename T, bool ADJ>
-gdn_status launch_states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g,
-                         const Pieces& pc, int most, float factor, float* S, float* total, int32_t* status,
-                         cudaStream_t s);
+template <typename T>
+struct Side {
+  const T *x, *y;
+  int64_t ldx, ldy;
+  float factor;
+  float* S;
+  bool adj;
+};
+// One launch for the states, or for them and the adjoint's (sides 1 or 2).
+template <typename T>
+gdn_status launch_states(const Shape& d, const Side<T>& first, const Side<T>& second, int sides, const float* g,
+                         const Pieces& pc, int most, float* total, int32_t* status, cudaStream_t s);
 gdn_status launch_outputs(const Shape& d, const float* q, const float* k, const float* v, const float* g,
                           const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
                           cudaStream_t s);
 
-template <bool REV>
-gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const float* init, float* S,
-                       float* fin, const int32_t* idx, int slots, cudaStream_t s) {
-  const int64_t grid = (int64_t)N * d.Hv * ((int64_t)d.K * d.V / 1024);
-  sums_kernel<REV><<<(unsigned)grid, 256, 0, s>>>(d, pc, total, init, S, fin, idx, slots);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+// Final states (or a pool's rows by idx), or, with rev, the adjoints before the sequences, go to fin.
+gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const Sum& first, const Sum& second,
+                       int sides, cudaStream_t s);
+inline gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const Sum& one,
+                              cudaStream_t s) {
+  return launch_sums(d, pc, N, total, one, one, 1, s);
 }
 
 // dst[row][hq][:] = sum over the R value heads of a q/k head, in their order (row: a token); dq and dk

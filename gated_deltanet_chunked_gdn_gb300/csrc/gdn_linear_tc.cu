@@ -691,7 +691,7 @@ gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, con
     prm.total = decays + decays_bytes(p) / 4;
     prm.own = prm.total + align_up(4 * (size_t)pieces_max(p, seg) * p.Hv) / 4;
     st = launch_walk(p, kOwn, false, nullptr, k, p.ld_k, v, p.ld_v, nullptr, prm, seg, s);
-    if (st == GDN_OK) st = launch_sums<false>(shape_of(p), pc, p.N, prm.total, h0, prm.own, nullptr, nullptr, 0, s);
+    if (st == GDN_OK) st = launch_sums(shape_of(p), pc, p.N, prm.total, Sum{h0, prm.own, nullptr, nullptr, 0, false}, s);
     prm.start = prm.own;
   }
   if (st != GDN_OK) return st;

@@ -24,10 +24,9 @@ struct StateMap32 {
 // One chunk of one value head a CTA, KD x VD of its state.  2 x 4096 tokens of 16 fp32 heads of 128: 66 us (3.6 TB/s of
 // states and inputs); 37 packed sequences, 12 heads of 64 x 128: 28 (fp32 FMAs: 47).  Bound by the latency of one round
 // of loading, splitting and products: two CTAs an SM, tensor pipe 14 to 18 %.
-template <typename T, int KD, int VD, bool ADJ>
+template <typename T, int KD, int VD>
 __global__ void __launch_bounds__(N, 2)
-    states_tc32_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ y, int64_t ldy, Shape d,
-                       const float* __restrict__ g, Pieces pc, float factor, float* __restrict__ S,
+    states_tc32_kernel(Side<T> first, Side<T> second, Shape d, const float* __restrict__ g, Pieces pc,
                        float* __restrict__ total, int32_t* status) {
   using M = StateMap32<T, KD, VD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -36,6 +35,7 @@ __global__ void __launch_bounds__(N, 2)
   const int c = ch / d.Hv, h = ch % d.Hv, hq = h / (d.Hv / d.Hqk);
   const Piece p = piece_of(pc, c);
   if (!p.ok) return;
+  const Side<T> m = blockIdx.y ? second : first;
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
   float *hi = reinterpret_cast<float*>(sm + M::Hi), *lo = reinterpret_cast<float*>(sm + M::Lo);
@@ -50,15 +50,15 @@ __global__ void __launch_bounds__(N, 2)
   }
   if (warp == 0) tmem_alloc(flags, KD);
   float4 xs[64 * KD / 4 / N], ys[64 * VD / 4 / N];
-  fetch<64, KD, N>(xs, x + p.tok0 * ldx + (int64_t)hq * d.K + d0, ldx, p.len);
-  fetch<64, VD, N>(ys, y + p.tok0 * ldy + (int64_t)h * d.V + e0, ldy, p.len);
+  fetch<64, KD, N>(xs, m.x + p.tok0 * m.ldx + (int64_t)hq * d.K + d0, m.ldx, p.len);
+  fetch<64, VD, N>(ys, m.y + p.tok0 * m.ldy + (int64_t)h * d.V + e0, m.ldy, p.len);
   if (warp == 1) {
     chunk_sums(g + (d.g_per_head ? h : p.tok0 * d.Hv + h), d.g_per_head ? 0 : d.Hv, p.len, lane, hi, lo);
     __syncwarp();
 #pragma unroll
     for (int r = lane; r < kC; r += 32)
-      w[r] = ADJ ? factor * expf(hi[r] + lo[r]) : expf((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
-    if (lane == 0 && blk == 0) total[ch] = expf(hi[kC - 1] + lo[kC - 1]);
+      w[r] = m.adj ? m.factor * expf(hi[r] + lo[r]) : expf((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
+    if (lane == 0 && blk == 0 && blockIdx.y == 0) total[ch] = expf(hi[kC - 1] + lo[kC - 1]);
   }
   place<64, VD, kTerms<T>, N>(sm + M::V, ys, nullptr);
   tc_fence_before();
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(N, 2)
   tc_fence_after();
   const int qd = warp & 3, part = warp >> 2, row = 32 * qd + lane;
   if (good && row < VD) {
-    float* to = S + ((int64_t)ch * d.K + d0 + part * (KD / 2)) * d.V + e0 + row;
+    float* to = m.S + ((int64_t)ch * d.K + d0 + part * (KD / 2)) * d.V + e0 + row;
 #pragma unroll
     for (int b = 0; b < KD / 2; b += 16) {
       float v[16];
@@ -304,14 +304,14 @@ bool allow(F kern, uint32_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <typename T, int KD, int VD, bool ADJ>
-gdn_status states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g, const Pieces& pc,
-                  int most, float factor, float* S, float* total, int32_t* status, cudaStream_t s) {
-  auto kern = states_tc32_kernel<T, KD, VD, ADJ>;
+template <typename T, int KD, int VD>
+gdn_status states(const Shape& d, const Side<T>& first, const Side<T>& second, int sides, const float* g,
+                  const Pieces& pc, int most, float* total, int32_t* status, cudaStream_t s) {
+  auto kern = states_tc32_kernel<T, KD, VD>;
   constexpr uint32_t bytes = StateMap32<T, KD, VD>::Bytes;
   if (!allow(kern, bytes)) return GDN_ERR_CUDA;
   const int64_t grid = (int64_t)most * d.Hv * (d.K / KD) * (d.V / VD);
-  kern<<<(unsigned)grid, N, bytes, s>>>(x, ldx, y, ldy, d, g, pc, factor, S, total, status);
+  kern<<<dim3((unsigned)grid, sides), N, bytes, s>>>(first, second, d, g, pc, total, status);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -328,12 +328,11 @@ gdn_status outputs(const Shape& d, const float* q, const float* k, const float* 
 
 }  // namespace
 
-template <typename T, bool ADJ>
-gdn_status launch_states(const Shape& d, const T* x, int64_t ldx, const T* y, int64_t ldy, const float* g,
-                         const Pieces& pc, int most, float factor, float* S, float* total, int32_t* status,
-                         cudaStream_t s) {
+template <typename T>
+gdn_status launch_states(const Shape& d, const Side<T>& first, const Side<T>& second, int sides, const float* g,
+                         const Pieces& pc, int most, float* total, int32_t* status, cudaStream_t s) {
   if (most == 0) return GDN_OK;
-#define GDN_STATES(K, V) return states<T, K, V, ADJ>(d, x, ldx, y, ldy, g, pc, most, factor, S, total, status, s)
+#define GDN_STATES(K, V) return states<T, K, V>(d, first, second, sides, g, pc, most, total, status, s)
   if (d.K == 64 && d.V != 64) GDN_STATES(64, 128);
   if (d.K != 64 && d.V == 64) GDN_STATES(128, 64);
   if constexpr (sizeof(T) == 4) {   // bf16 comes here with a head dim of 256 alone
@@ -355,14 +354,10 @@ gdn_status launch_outputs(const Shape& d, const float* q, const float* k, const 
 #undef GDN_OUTPUTS
 }
 
-#define GDN_INSTANCE(T)                                                                                              \
-  template gdn_status launch_states<T, false>(const Shape&, const T*, int64_t, const T*, int64_t, const float*,      \
-                                              const Pieces&, int, float, float*, float*, int32_t*, cudaStream_t);    \
-  template gdn_status launch_states<T, true>(const Shape&, const T*, int64_t, const T*, int64_t, const float*,       \
-                                             const Pieces&, int, float, float*, float*, int32_t*, cudaStream_t)
-GDN_INSTANCE(float);
-GDN_INSTANCE(__nv_bfloat16);
-#undef GDN_INSTANCE
+template gdn_status launch_states<float>(const Shape&, const Side<float>&, const Side<float>&, int, const float*,
+                                         const Pieces&, int, float*, int32_t*, cudaStream_t);
+template gdn_status launch_states<__nv_bfloat16>(const Shape&, const Side<__nv_bfloat16>&, const Side<__nv_bfloat16>&,
+                                                 int, const float*, const Pieces&, int, float*, int32_t*, cudaStream_t);
 
 }  // namespace lin
 }  // namespace gdn

@@ -539,7 +539,8 @@ gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, con
     const bool cut = L.seg < p.T;
     if (st == GDN_OK && cut) {
       st = launch_walk(p, kOwn, false, nullptr, k, p.ld_k, v, p.ld_v, nullptr, prm, L.seg, s);
-      if (st == GDN_OK) st = launch_sums<false>(shape_of(p), segs, p.N, prm.total, h0, prm.own, nullptr, nullptr, 0, s);
+      if (st == GDN_OK)
+        st = launch_sums(shape_of(p), segs, p.N, prm.total, Sum{h0, prm.own, nullptr, nullptr, 0, false}, s);
     }
     TcParams walk = prm;
     walk.start = cut ? prm.own : nullptr;
@@ -548,7 +549,8 @@ gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, con
     if (st == GDN_OK) st = launch_walk(p, kEmit, false, nullptr, k, p.ld_k, v, p.ld_v, nullptr, walk, L.seg, s);
     if (st == GDN_OK && cut) {
       st = launch_walk(p, kOwn, true, nullptr, q, p.ld_q, dout, ldo, nullptr, prm, L.seg, s);
-      if (st == GDN_OK) st = launch_sums<true>(shape_of(p), segs, p.N, prm.total, dht, prm.own, nullptr, nullptr, 0, s);
+      if (st == GDN_OK)
+        st = launch_sums(shape_of(p), segs, p.N, prm.total, Sum{dht, prm.own, nullptr, nullptr, 0, true}, s);
     }
     walk.h0 = dht;
     walk.ht = dh0;

@@ -351,3 +351,57 @@ def test_large_values_keep_their_neighbours_bits(gdn, dtype, K, V):
     for e in range(0, V, 16):   # each band of columns against its own norm
         assert ref.rel(o[..., e:e + 16], wo[..., e:e + 16]) < O_TOL[dtype]
         assert ref.rel(ht[..., e:e + 16], wh[..., e:e + 16]) < S_TOL[dtype]
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 256)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_dh0_in_the_place_of_h0_or_dht(gdn, dtype, K, V):
+    """The C call's promise: dh0 may be h0 or dht, the same pointer; every output as with a buffer of its own."""
+    x = make(2, 2100, 1, 2, K, V, dtype)
+    want = gdn.gdn_linear_attn_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], scale=0.25, h0=x["h0"], dht=x["dht"])
+    p = gdn._linear_problem(x["q"], x["k"], x["v"], x["g"], None)
+    ws = torch.zeros(gdn.gdn_linear_attn_bwd_workspace_size(p), dtype=torch.uint8, device=DEV)
+    for place in ("h0", "dht"):
+        h0, dht = x["h0"].clone(), x["dht"].clone()
+        dh0 = h0 if place == "h0" else dht
+        out = [torch.empty_like(want[n]) for n in ("dq", "dk", "dv", "dg")] + [dh0]
+        st = gdn._call(0, gdn.load().gdn_linear_attn_bwd, p, *(x[n].data_ptr() for n in ("q", "k", "v", "g")), 0.25,
+                       h0.data_ptr(), 0, x["do"].data_ptr(), dht.data_ptr(), *(t.data_ptr() for t in out),
+                       ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        for n, t in zip(("dq", "dk", "dv", "dg", "dh0"), out):
+            assert torch.equal(t, want[n]), (place, n)
+
+
+@pytest.mark.parametrize("dtype,K,V", [(F32, 64, 128), (F32, 256, 256), (BF, 256, 128)])
+def test_two_calls_at_once_and_a_captured_one(gdn, dtype, K, V):
+    """Calls on two streams share the device's tensor memory; a captured call replays to the same bits."""
+    x = make(2, 700, 2, 4, K, V, dtype)
+    y = make(1, 0, 2, 4, K, V, dtype, lens=[300, 5, 900], seed=1)
+
+    def run(z):
+        o, ht = gdn.gdn_linear_attn_fwd(z["q"], z["k"], z["v"], z["g"], h0=z["h0"], cu_seqlens=z["cu"])
+        d = gdn.gdn_linear_attn_bwd(z["q"], z["k"], z["v"], z["g"], z["do"], h0=z["h0"], dht=z["dht"],
+                                    cu_seqlens=z["cu"])
+        return [o, ht] + [d[n] for n in ("dq", "dk", "dv", "dg", "dh0")]
+
+    want = run(x), run(y)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [None, None]
+    for _ in range(3):
+        for i, (s, z) in enumerate(zip(streams, (x, y))):
+            with torch.cuda.stream(s):
+                got[i] = run(z)
+    torch.cuda.synchronize()
+    for w, t in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, t))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(y)
+    for _ in range(2):
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[1], held))

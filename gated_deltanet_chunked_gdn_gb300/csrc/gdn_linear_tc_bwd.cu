@@ -46,7 +46,7 @@ template <int KD, int VD>
 struct GradMap {
   static constexpr uint32_t KQ = 0;                              // k rows 0..63, q rows 64..127
   static constexpr uint32_t VO = KQ + KD / 64 * 16384;           // v rows 0..63, do rows 64..127
-  static constexpr uint32_t S = VO + VD / 64 * 16384;            // S0^T [e][d] fp32, then its first two bf16 terms
+  static constexpr uint32_t S = VO + VD / 64 * 16384;            // S0 as it lies in memory, then S0^T's first two terms
   static constexpr uint32_t kTile = (uint32_t)KD * VD * 2;
   static constexpr uint32_t G = S + 2 * kTile;
   // the third terms of S0, then of G; then W^T rows 0..63, W rows 64..127 | P^T | sums, float[4][128] each.  (A 64-row

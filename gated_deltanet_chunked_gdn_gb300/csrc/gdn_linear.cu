@@ -121,7 +121,7 @@ namespace {
 // Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (rev: the adjoint of the
 // state behind it); four elements of a state a thread.  2 x 4096 tokens of 16 heads of 128 (64 chunks a sequence):
 // 55 us, 4.9 TB/s; with loads only after the sums before, 132.  blockIdx.y: the first or the second of two sums.
-__global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const float* __restrict__ total, Sum first,
+__global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const Two* __restrict__ total, Sum first,
                                                    Sum second) {
   const Sum m = blockIdx.y ? second : first;
   const float* __restrict__ init = m.init;
@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const flo
   // the next four chunks' loads are under way while these are added up
   constexpr int AHEAD = 4;
   float4 x[2][AHEAD];
-  float a[2][AHEAD];
+  Two a[2][AHEAD];
   auto chunk = [&](int i) { return m.rev ? c1 - 1 - i : c0 + i; };
-  auto fetch = [&](float4 (&y)[AHEAD], float (&f)[AHEAD], int base) {
+  auto fetch = [&](float4 (&y)[AHEAD], Two (&f)[AHEAD], int base) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
       if (base + i < c1 - c0) {
@@ -146,13 +146,14 @@ __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const flo
         f[i] = total[(int64_t)chunk(base + i) * d.Hv + h];
       }
   };
-  auto add = [&](const float4 (&y)[AHEAD], const float (&f)[AHEAD], int base) {
+  auto add = [&](const float4 (&y)[AHEAD], const Two (&f)[AHEAD], int base) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
       if (base + i < c1 - c0) {
         *reinterpret_cast<float4*>(S + ((int64_t)chunk(base + i) * d.Hv + h) * kv + at) = run;
-        run.x = fmaf(f[i], run.x, y[i].x), run.y = fmaf(f[i], run.y, y[i].y);
-        run.z = fmaf(f[i], run.z, y[i].z), run.w = fmaf(f[i], run.w, y[i].w);
+        const float h = f[i].h, l = f[i].l;
+        run.x = fmaf(h, run.x, fmaf(l, run.x, y[i].x)), run.y = fmaf(h, run.y, fmaf(l, run.y, y[i].y));
+        run.z = fmaf(h, run.z, fmaf(l, run.z, y[i].z)), run.w = fmaf(h, run.w, fmaf(l, run.w, y[i].w));
       }
   };
   fetch(x[0], a[0], 0);
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const flo
 
 }  // namespace
 
-gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const Sum& first, const Sum& second,
+gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const Two* total, const Sum& first, const Sum& second,
                        int sides, cudaStream_t s) {
   const int64_t grid = (int64_t)N * d.Hv * ((int64_t)d.K * d.V / 1024);
   sums_kernel<<<dim3((unsigned)grid, sides), 256, 0, s>>>(d, pc, total, first, second);
@@ -187,7 +188,8 @@ namespace {
 // One CTA per (sequence, value head, COLS columns of V): the state's slice lives in registers for all of the
 // sequence's tokens (COLS / 4 column groups of float4, the other threads' groups along K) and is read and written
 // once.  Bound by the state's traffic, 8 K V bytes a head; streaming hints, since a pool larger than L2 is touched
-// once a step.  512 sequences of 32 heads of 128 x 128: 309 us, 6.9 TB/s of their states; one sequence: 2.5 us.
+// once a step.  512 sequences of 32 heads of 128 x 128: 314 us, 6.8 TB/s of their states (309 with the decay in one float);
+// one sequence: 2.5 us.
 template <typename T, int K, int COLS>
 __global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, int64_t ldq, int64_t ldk, int64_t ldv,
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, 
   constexpr int CG = COLS / 4, RG = 256 / CG, RPG = K / RG;
   static_assert(RPG >= 1 && RPG * RG == K, "every thread holds rows");
   __shared__ float ks[K], qs[K];
-  __shared__ float part[8][COLS];
+  __shared__ __align__(16) float part[8][COLS];   // written as float4
   const int e0 = COLS * blockIdx.x, h = blockIdx.y % Hv;
   const int n = blockIdx.y / Hv;
   const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG, lane = tid & 31, warp = tid >> 5;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, 
     return;
   }
   float* S = state + (((int64_t)slot * Hv + h) * K) * (int64_t)V + e0 + 4 * cg;
+  float gt = g[g_per_head ? h : tok0 * Hv + h];
   float s[RPG][4];
 #pragma unroll
   for (int r = 0; r < RPG; ++r) {
@@ -226,7 +229,8 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, 
       ks[tid] = to_f(k[tok * ldk + hq * K + tid]);
       qs[tid] = to_f(q[tok * ldq + hq * K + tid]);
     }
-    const float a = expf(g_per_head ? g[h] : g[tok * Hv + h]);
+    const Two a = exp_two({gt, 0.f});
+    if (t + 1 < L && !g_per_head) gt = g[(tok + 1) * Hv + h];
     const float4 v4 = load4(v + tok * ldv + (int64_t)h * V + e0 + 4 * cg);
     const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
     __syncthreads();
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, 
       const float kd = ks[rg * RPG + r], qd = qs[rg * RPG + r];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[r][j] = fmaf(a, s[r][j], kd * vv[j]);
+        s[r][j] = fmaf(a.h, s[r][j], fmaf(a.l, s[r][j], kd * vv[j]));
         p[j] = fmaf(qd, s[r][j], p[j]);
       }
     }
@@ -316,10 +320,10 @@ gdn_status run_linear_step(const gdn_linear_problem& p, const void* q, const voi
 namespace lin {
 namespace {
 
-// [status][tables][total: chunks x Hv][states: chunks x Hv x K x V]
+// [status][tables][total: chunks x Hv, in two floats][states: chunks x Hv x K x V]
 size_t fwd32_bytes(const gdn_linear_problem& p) {
   const size_t cells = (size_t)pieces_max(p, kC) * p.Hv;
-  return kAlign + pieces_bytes(p, kC) + align_up(4 * cells) + 4 * cells * p.K * p.V;
+  return kAlign + pieces_bytes(p, kC) + align_up(sizeof(Two) * cells) + 4 * cells * p.K * p.V;
 }
 
 gdn_status fwd32(const gdn_linear_problem& p, const float* q, const float* k, const float* v, const float* g,
@@ -332,8 +336,8 @@ gdn_status fwd32(const gdn_linear_problem& p, const float* q, const float* k, co
   const Pieces pc = pieces_at(p, kC, tables);
   const Shape d = shape_of(p);
   const int most = pieces_max(p, kC);
-  float* total = reinterpret_cast<float*>(at + kAlign + pieces_bytes(p, kC));
-  float* states = total + align_up(4 * (size_t)most * p.Hv) / 4;
+  Two* total = reinterpret_cast<Two*>(at + kAlign + pieces_bytes(p, kC));
+  float* states = reinterpret_cast<float*>(total) + align_up(sizeof(Two) * (size_t)most * p.Hv) / 4;
   const Side<float> side{k, v, p.ld_k, p.ld_v, 1.f, states, false};
   gdn_status st = launch_states(d, side, side, 1, g, pc, most, total, status, s);
   if (st == GDN_OK) st = launch_sums(d, pc, p.N, total, Sum{h0, states, ht, idx, slots, false}, s);

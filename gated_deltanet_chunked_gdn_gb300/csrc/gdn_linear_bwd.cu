@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
     double past = 0.0;
 #pragma unroll
     for (int w = 0; w < N / 32; ++w) past += red[w];
-    past *= (double)expf(hi[kC - 1] + lo[kC - 1]);
+    const Two whole = exp_two({hi[kC - 1], lo[kC - 1]});
+    past *= (double)whole.h + whole.l;
     const int r = 2 * lane;
     double rw[2], ot[2];
 #pragma unroll
@@ -460,7 +461,7 @@ Layout layout_of(const gdn_linear_problem& p) {
   Layout L;
   L.tables = kAlign;
   L.total = L.tables + pieces_bytes(p, kC);
-  L.part = L.total + align_up(4 * cells);
+  L.part = L.total + align_up(sizeof(Two) * cells);
   L.states = L.part + (p.g_per_head ? align_up(4 * cells) : 0);
   L.adjoints = L.states + 4 * cells * p.K * p.V;
   L.dq = L.adjoints + 4 * cells * p.K * p.V;
@@ -477,7 +478,7 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
   const Shape d = shape_of(p);
   const int most = pieces_max(p, kC);
   int32_t* status = reinterpret_cast<int32_t*>(ws);
-  float* total = reinterpret_cast<float*>(ws + L.total);
+  Two* total = reinterpret_cast<Two*>(ws + L.total);
   float* S = reinterpret_cast<float*>(ws + L.states);
   float* G = reinterpret_cast<float*>(ws + L.adjoints);
   const Side<T> states{k, v, p.ld_k, p.ld_v, 1.f, S, false};

@@ -58,15 +58,15 @@ struct Side {
 // One launch for the states, or for them and the adjoint's (sides 1 or 2).
 template <typename T>
 gdn_status launch_states(const Shape& d, const Side<T>& first, const Side<T>& second, int sides, const float* g,
-                         const Pieces& pc, int most, float* total, int32_t* status, cudaStream_t s);
+                         const Pieces& pc, int most, Two* total, int32_t* status, cudaStream_t s);
 gdn_status launch_outputs(const Shape& d, const float* q, const float* k, const float* v, const float* g,
                           const Pieces& pc, int most, float scale, const float* S0, float* o, int32_t* status,
                           cudaStream_t s);
 
 // Final states (or a pool's rows by idx), or, with rev, the adjoints before the sequences, go to fin.
-gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const Sum& first, const Sum& second,
+gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const Two* total, const Sum& first, const Sum& second,
                        int sides, cudaStream_t s);
-inline gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const float* total, const Sum& one,
+inline gdn_status launch_sums(const Shape& d, const Pieces& pc, int N, const Two* total, const Sum& one,
                               cudaStream_t s) {
   return launch_sums(d, pc, N, total, one, one, 1, s);
 }

@@ -41,9 +41,10 @@ struct Map {
   // rows 64..127 of a 64-row A tile are read (and ignored): they stay inside
   static constexpr uint32_t kEnd = X + 32768 > OS + 16384 ? X + 32768 : OS + 16384;
   static constexpr uint32_t Misc = Tail < kEnd ? kEnd : Tail;
-  static constexpr uint32_t Gam = Misc;   // a chunk's decays, as they lie in memory: gam, down, up; two chunks'
-  static constexpr uint32_t Bar = Misc + 1536, Flags = Misc + 1600;
-  static constexpr uint32_t Used = Misc + 1664;
+  static constexpr uint32_t kGam = 4 * kWalkDecays;
+  static constexpr uint32_t Gam = Misc;   // a chunk's decays, as they lie in memory; two chunks'
+  static constexpr uint32_t Bar = Misc + 2 * kGam, Flags = Bar + 64;
+  static constexpr uint32_t Used = Flags + 64;
   static constexpr uint32_t Bytes = Used + 1024;
   static constexpr int Cols = KD + 128 <= 256 ? 256 : 512;        // TMEM: U^T, Q K^T / OP^T, OQ^T
   static constexpr int Ctas = KD == 256 ? 1 : 2;
@@ -85,10 +86,6 @@ __device__ __forceinline__ void weigh_values(uint8_t* sm, uint32_t v, uint32_t x
   }
 }
 
-// A sum of two floats that holds twice a float's bits.
-struct Two {
-  float h, l;
-};
 __device__ __forceinline__ Two add(Two a, float bh, float bl) {
   const float s = a.h + bh, v = s - a.h, e = ((a.h - (s - v)) + (bh - v)) + (a.l + bl);
   const float h = s + e;
@@ -100,8 +97,8 @@ __device__ __forceinline__ Two log2_units(Two a) {
   return {h, fmaf(a.h, kLog2e, -h) + fmaf(a.l, kLog2e, a.h * kLow)};
 }
 
-// Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i} and what the first lacks
-// to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
+// Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i}, e^{b_last} in two floats
+// and what the first lacks to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
 // differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads take 28 us, as
 // they are 8).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A
 // warp takes a chunk and head at a time.  (Within the
@@ -126,9 +123,13 @@ __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g
     }
     const float lh = __shfl_sync(0xffffffffu, s.h, 31), ll = __shfl_sync(0xffffffffu, s.l, 31);
     const Two s0 = add(s, -b, 0.f), x0 = log2_units(s0), x1 = log2_units(s);
-    float* to = out + ((chunk_slot(p) + i) * Hv + h) * 256 + r;
+    float* to = out + ((chunk_slot(p) + i) * Hv + h) * kDecays + r;
     *reinterpret_cast<float2*>(to) = make_float2(x0.h, x1.h);
-    *reinterpret_cast<float2*>(to + 192) = make_float2(x0.l, x1.l);
+    *reinterpret_cast<float2*>(to + kWalkDecays) = make_float2(x0.l, x1.l);
+    if (lane == 0) {
+      const Two whole = exp_two({lh, ll});
+      *reinterpret_cast<float4*>(to + 192) = make_float4(whole.h, whole.l, 0.f, 0.f);
+    }
     *reinterpret_cast<float2*>(to + 64) = make_float2(r < len ? expf((lh - s0.h) + (ll - s0.l)) : 0.f,
                                                       r + 1 < len ? expf((lh - s.h) + (ll - s.l)) : 0.f);
     *reinterpret_cast<float2*>(to + 128) = make_float2(scale * expf(s0.h + s0.l), scale * expf(s.h + s.l));
@@ -203,13 +204,13 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   auto v_tile = [&](int i) { return buffer(i) ? M::X : M::V; };     // the second in the place of the state's copy
   auto load_bar = [&](int which, int i) { return bars + which + 2 * buffer(i); };
   auto load_no = [&](int i) { return TWO ? i >> 1 : i; };
-  auto decays_of = [&](int i) { return reinterpret_cast<const float*>(sm + M::Gam + 768 * buffer(i)); };
+  auto decays_of = [&](int i) { return reinterpret_cast<const float*>(sm + M::Gam + M::kGam * buffer(i)); };
   auto issue_k = [&](int i) {
     const int at = chunk_at(i), t = (int)(p.tok0 + 64 * at);
     uint64_t* bar = load_bar(0, i);
     count[2 * buffer(i)] = load_no(i) + 1;
-    mbar_arrive_expect_tx(bar, KD / 64 * 8192 + 768);
-    bulk_load(sm + M::Gam + 768 * buffer(i), prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * 256, 768, bar);
+    mbar_arrive_expect_tx(bar, KD / 64 * 8192 + M::kGam);
+    bulk_load(sm + M::Gam + M::kGam * buffer(i), prm.decays + ((chunk_slot(p) + at) * prm.Hv + h) * kDecays, M::kGam, bar);
 #pragma unroll
     for (int a = 0; a < KD / 64; ++a) tma_load_3d(sm + k_tile(i) + a * 16384, &tm_k, bar, 64 * a, hq, t);
   };
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       for (int i = 0; i < KH; ++i) S[i] = 0.f;
     }
   }
-  float dec = 1.f, total = 1.f;
+  Two dec{1.f, 0.f}, total{1.f, 0.f};
 
 #pragma unroll 1
   for (int i = 0; i < nchunks; ++i) {
@@ -286,8 +287,9 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         tmem_ld32(R_U + lane_off + hf * KH + b, u);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float2 x = __ffma2_rn(make_float2(dec, dec), make_float2(S[b + j], S[b + j + 1]),
-                                      make_float2(u[j], u[j + 1]));
+          const float2 y = make_float2(S[b + j], S[b + j + 1]);
+          const float2 x = __ffma2_rn(make_float2(dec.h, dec.h), y,
+                                      __ffma2_rn(make_float2(dec.l, dec.l), y, make_float2(u[j], u[j + 1])));
           S[b + j] = x.x, S[b + j + 1] = x.y;
         }
       }
@@ -410,8 +412,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       weigh_values<VD>(sm, v_tile(i), v_tile(i), M::X + VD / 64 * 8192, M::OS, ADJ ? up : down, tid, 64 * (VD / 8),
                        kTcThreads);
     }
-    dec = ex2_fast(gam[63]);   // before the barrier behind which the next chunk's decays may come in
-    total *= dec;
+    dec = {gam[192], gam[193]};   // before the barrier behind which the next chunk's decays may come in
+    if (MODE == kOwn) total = times(total, dec);
     fence_proxy_async();
     tc_fence_before();
     if (__syncthreads_or(bad)) break;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       float u[32];
       tmem_ld32(R_U + lane_off + hf * KH + b, u);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) S[b + j] = fmaf(dec, S[b + j], u[j]);
+      for (int j = 0; j < 32; ++j) S[b + j] = fmaf(dec.h, S[b + j], fmaf(dec.l, S[b + j], u[j]));
     }
     float* to = nullptr;
     const int64_t kv = (int64_t)KD * prm.V;
@@ -603,7 +605,7 @@ int segment_tokens(const gdn_linear_problem& p) {
 }
 
 size_t decays_bytes(const gdn_linear_problem& p) {
-  return 1024 * (size_t)((int64_t)p.B * p.T / 64 + p.N + 1) * p.Hv;
+  return align_up(4 * kDecays * (size_t)((int64_t)p.B * p.T / 64 + p.N + 1) * p.Hv);
 }
 
 gdn_status launch_decays(const gdn_linear_problem& p, const Pieces& pc, int size, const float* g, float scale,
@@ -665,11 +667,11 @@ gdn_status launch_walk(const gdn_linear_problem& p, int mode, bool adj, const vo
   return launch_dims<256, 128>(mode, adj, grid, m, prm, s);
 }
 
-// [status][tables][decays][the segments' own: segments x Hv][states: segments x Hv x K x V]
+// [status][tables][decays][the segments' decays: segments x Hv][states: segments x Hv x K x V]
 size_t tc_fwd_bytes(const gdn_linear_problem& p) {
   const int seg = segment_tokens(p);
   const size_t cells = seg < p.T ? (size_t)pieces_max(p, seg) * p.Hv : 0;
-  return kAlign + pieces_bytes(p, seg) + decays_bytes(p) + align_up(4 * cells) + 4 * cells * p.K * p.V;
+  return kAlign + pieces_bytes(p, seg) + decays_bytes(p) + align_up(sizeof(Two) * cells) + 4 * cells * p.K * p.V;
 }
 
 gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
@@ -688,8 +690,8 @@ gdn_status tc_fwd(const gdn_linear_problem& p, const void* q, const void* k, con
   TcParams prm = tc_params(p, pc, cu, scale, decays, status);
   prm.h0 = h0;
   if (st == GDN_OK && seg < p.T) {
-    prm.total = decays + decays_bytes(p) / 4;
-    prm.own = prm.total + align_up(4 * (size_t)pieces_max(p, seg) * p.Hv) / 4;
+    prm.total = reinterpret_cast<Two*>(decays + decays_bytes(p) / 4);
+    prm.own = decays + (decays_bytes(p) + align_up(sizeof(Two) * (size_t)pieces_max(p, seg) * p.Hv)) / 4;
     st = launch_walk(p, kOwn, false, nullptr, k, p.ld_k, v, p.ld_v, nullptr, prm, seg, s);
     if (st == GDN_OK) st = launch_sums(shape_of(p), pc, p.N, prm.total, Sum{h0, prm.own, nullptr, nullptr, 0, false}, s);
     prm.start = prm.own;

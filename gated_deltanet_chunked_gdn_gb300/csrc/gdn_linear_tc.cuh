@@ -15,13 +15,13 @@ using namespace sm100;
 using solve64::dsw;
 
 struct TcParams {
-  const float* decays;   // [slots of chunks][Hv][4][64], decays_kernel
+  const float* decays;   // [slots of chunks][Hv][kDecays], decays_kernel
   const float* h0;       // [N][Hv][K][V]
   const float* start;    // [segments][Hv][K][V] states before the segments, or null (one segment a sequence)
   float* ht;             // final states (or a pool), or null
   const int32_t* idx;
   float* own;            // kOwn: the segments' own contributions
-  float* total;          // kOwn: their decays
+  Two* total;            // kOwn: their decays
   __nv_bfloat16* o;
   int32_t* status;
   Pieces pc;
@@ -78,12 +78,16 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int columns, uint32_t s
 // short, so that no two chunks share one.
 __device__ __forceinline__ int64_t chunk_slot(const Piece& p) { return p.tok0 / 64 + p.seq; }
 
+// A chunk's decays: log2(e) b_i, e^{b_last - b_j}, scale e^{b_i} (64 each); e^{b_last} in two floats, and two unused;
+// what the first 64 lack to 48 bits.  The walk reads all but the last.
+constexpr int kDecays = 260, kWalkDecays = 196;
+
 // What a launch of the walk does: the segments' own contributions and decays; outputs and final states; the state
 // before every chunk, for the backward pass.
 constexpr int kOwn = 0, kFull = 1, kEmit = 2;
 
 int segment_tokens(const gdn_linear_problem& p);
-size_t decays_bytes(const gdn_linear_problem& p);   // [slots of chunks][Hv][4][64] fp32
+size_t decays_bytes(const gdn_linear_problem& p);   // [slots of chunks][Hv][kDecays] fp32
 gdn_status launch_decays(const gdn_linear_problem& p, const Pieces& pc, int size, const float* g, float scale,
                          float* decays, cudaStream_t s);
 // One launch over the segments (size tokens each).  adj: the adjoint's walk, from the sequences' ends to their starts,

@@ -27,7 +27,7 @@ struct StateMap32 {
 template <typename T, int KD, int VD>
 __global__ void __launch_bounds__(N, 2)
     states_tc32_kernel(Side<T> first, Side<T> second, Shape d, const float* __restrict__ g, Pieces pc,
-                       float* __restrict__ total, int32_t* status) {
+                       Two* __restrict__ total, int32_t* status) {
   using M = StateMap32<T, KD, VD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int nv = d.V / VD, nb = d.K / KD * nv;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(N, 2)
 #pragma unroll
     for (int r = lane; r < kC; r += 32)
       w[r] = m.adj ? m.factor * expf(hi[r] + lo[r]) : expf((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
-    if (lane == 0 && blk == 0 && blockIdx.y == 0) total[ch] = expf(hi[kC - 1] + lo[kC - 1]);
+    if (lane == 0 && blk == 0 && blockIdx.y == 0) total[ch] = exp_two({hi[kC - 1], lo[kC - 1]});
   }
   place<64, VD, kTerms<T>, N>(sm + M::V, ys, nullptr);
   tc_fence_before();
@@ -306,7 +306,7 @@ bool allow(F kern, uint32_t bytes) {
 
 template <typename T, int KD, int VD>
 gdn_status states(const Shape& d, const Side<T>& first, const Side<T>& second, int sides, const float* g,
-                  const Pieces& pc, int most, float* total, int32_t* status, cudaStream_t s) {
+                  const Pieces& pc, int most, Two* total, int32_t* status, cudaStream_t s) {
   auto kern = states_tc32_kernel<T, KD, VD>;
   constexpr uint32_t bytes = StateMap32<T, KD, VD>::Bytes;
   if (!allow(kern, bytes)) return GDN_ERR_CUDA;
@@ -330,7 +330,7 @@ gdn_status outputs(const Shape& d, const float* q, const float* k, const float* 
 
 template <typename T>
 gdn_status launch_states(const Shape& d, const Side<T>& first, const Side<T>& second, int sides, const float* g,
-                         const Pieces& pc, int most, float* total, int32_t* status, cudaStream_t s) {
+                         const Pieces& pc, int most, Two* total, int32_t* status, cudaStream_t s) {
   if (most == 0) return GDN_OK;
 #define GDN_STATES(K, V) return states<T, K, V>(d, first, second, sides, g, pc, most, total, status, s)
   if (d.K == 64 && d.V != 64) GDN_STATES(64, 128);
@@ -355,9 +355,9 @@ gdn_status launch_outputs(const Shape& d, const float* q, const float* k, const 
 }
 
 template gdn_status launch_states<float>(const Shape&, const Side<float>&, const Side<float>&, int, const float*,
-                                         const Pieces&, int, float*, int32_t*, cudaStream_t);
+                                         const Pieces&, int, Two*, int32_t*, cudaStream_t);
 template gdn_status launch_states<__nv_bfloat16>(const Shape&, const Side<__nv_bfloat16>&, const Side<__nv_bfloat16>&,
-                                                 int, const float*, const Pieces&, int, float*, int32_t*, cudaStream_t);
+                                                 int, const float*, const Pieces&, int, Two*, int32_t*, cudaStream_t);
 
 }  // namespace lin
 }  // namespace gdn

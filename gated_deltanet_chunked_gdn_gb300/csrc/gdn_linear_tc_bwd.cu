@@ -28,7 +28,7 @@ namespace {
 constexpr int kGradThreads = 512;
 
 struct GradParams {
-  const float* decays;   // [slots][Hv][4][64]
+  const float* decays;   // [slots][Hv][kDecays]
   const float* states;   // [slots][Hv][K / 8][V][8]
   const float* adjoints;
   void* dq;              // bf16 [B, T, Hqk, K], or fp32 [B, T, Hv, K] (SHARED)
@@ -54,8 +54,9 @@ struct GradMap {
   static constexpr uint32_t X3 = G + 2 * kTile;
   static constexpr uint32_t W = X3, P = W + 16384, SumA = P + 8192, SumX = SumA + 2048;
   static constexpr uint32_t Misc = X3 + 32768;
-  static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512, Low = Misc + 768;
-  static constexpr uint32_t Red = Misc + 1024;   // float[16]
+  static constexpr uint32_t kGam = 4 * kDecays;
+  static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512, Whole = Misc + 768, Low = Whole + 16;
+  static constexpr uint32_t Red = Misc + kGam;   // float[16]
   static constexpr uint32_t Bar = Red + 64, Flags = Bar + 64;
   static constexpr uint32_t Bytes = Flags + 64 + 1024;
 };
@@ -133,8 +134,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const Piece p = piece_of(prm.pc, item / prm.Hv);
     const int t = (int)p.tok0;
     count[0] = n + 1;
-    mbar_arrive_expect_tx(bar_t, (KD + VD) / 64 * 16384 + 1024);
-    bulk_load(sm + M::Gam, prm.decays + cell(p, h) * 256, 1024, bar_t);
+    mbar_arrive_expect_tx(bar_t, (KD + VD) / 64 * 16384 + M::kGam);
+    bulk_load(sm + M::Gam, prm.decays + cell(p, h) * kDecays, M::kGam, bar_t);
 #pragma unroll
     for (int a = 0; a < KD / 64; ++a) {
       tma_load_3d(sm + M::KQ + a * 16384, &tm_k, bar_t, 64 * a, hq, t);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const int next = item + gridDim.x, h1 = next % prm.Hv, hq1 = h1 / (prm.Hv / prm.Hqk);
       const Piece p1 = piece_of(prm.pc, next / prm.Hv);
       const int t = (int)p1.tok0;
-      bulk_prefetch(prm.decays + cell(p1, h1) * 256, 1024);
+      bulk_prefetch(prm.decays + cell(p1, h1) * kDecays, M::kGam);
 #pragma unroll
       for (int a = 0; a < KD / 64; ++a) {
         tma_prefetch_3d(&tm_k, 64 * a, hq1, t);
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       float past = lane < 16 ? red[lane] : 0.f;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) past += __shfl_xor_sync(0xffffffffu, past, o);
-      past = __shfl_sync(0xffffffffu, past, 0) * ex2_fast(gam[63]);
+      past = __shfl_sync(0xffffffffu, past, 0) * *reinterpret_cast<const float*>(sm + M::Whole);
       const int r = 2 * lane;
       float rw[2], ot[2];
 #pragma unroll
@@ -486,7 +487,7 @@ Layout layout_of(const gdn_linear_problem& p) {
   L.chunk_tables = L.seg_tables + pieces_bytes(p, L.seg);
   L.decays = L.chunk_tables + pieces_bytes(p, 64);
   L.total = L.decays + decays_bytes(p);
-  L.own = L.total + align_up(4 * segs);
+  L.own = L.total + align_up(sizeof(Two) * segs);
   L.part = L.own + segs * tile;
   L.states = L.part + (p.g_per_head ? align_up(4 * (size_t)pieces_max(p, 64) * p.Hv) : 0);
   L.adjoints = L.states + slots * tile;
@@ -534,7 +535,7 @@ gdn_status tc_bwd(const gdn_linear_problem& p, const void* q, const void* k, con
     st = launch_decays(p, segs, L.seg, g, scale, decays, s);
     const int64_t ldo = (int64_t)p.Hv * p.V;
     TcParams prm = tc_params(p, segs, cu, scale, decays, status);
-    prm.total = reinterpret_cast<float*>(at + L.total);
+    prm.total = reinterpret_cast<Two*>(at + L.total);
     prm.own = reinterpret_cast<float*>(at + L.own);
     const bool cut = L.seg < p.T;
     if (st == GDN_OK && cut) {

@@ -4,7 +4,7 @@
 // transposed so that every tcgen05.mma has M = 128 (TMEM lane = value column e, or token):
 //
 //   [K;Q] K^T                -> lanes 64..127: Q K^T                              (M128 N64)
-//   OQ^T = S^T Q^T           S^T: bf16 copy of the state before the chunk         (M128 N64)
+//   OQ^T = S^T Q^T           S^T: copy of the state before the chunk, two bf16 terms (M128 N64)
 //   OP^T = V^T P^T           P = lower(scale e^{b_i - b_j} Q K^T), two bf16 terms (M128 N64)
 //   U^T  = V''^T K           V'' = diag(e^{b_last - b_j}) V in three bf16 terms   (M128 N K)
 //   o_i  = scale e^{b_i} OQ_i + OP_i,   S^T <- e^{b_last} S^T + U^T
@@ -12,7 +12,10 @@
 // The state itself stays in fp32 registers (a thread holds K / 2 columns of one row of S^T), and what a chunk adds to
 // it comes out of the tensor cores complete: V'' keeps all 24 bits of the weighted values (with two terms the final
 // state was off by 2.4e-6, with three by 1e-7), and no sum longer than a chunk is left to the tensor cores'
-// accumulation.  o reads a bf16 copy of the state: one rounding of its terms, like o's own.
+// accumulation.  o reads a copy of the state in two bf16 terms, as its weights P are (with one term of either o was off by
+// 2.3e-3 where that part made it up, with two by its own rounding, 1.7e-3).  The copy lies in tensor memory, where U^T was
+// before the registers took it and will be again: in shared memory its second term has no room beside two CTAs, or takes
+// that of P and o and makes their phases wait (4 x 8192 tokens of 32 heads: 499 us; so 470; one term 456).
 // Two CTAs share an SM: one's loads and SIMT phases run under the other's products.
 //
 // Chains that do not fill the device are cut into segments of whole chunks: a launch before forms every segment's own
@@ -28,26 +31,24 @@ namespace {
 
 constexpr int kTcThreads = 256;
 
-// Shared memory, byte offsets from a 1024-byte aligned base.
-template <int KD, int VD>
+// Shared memory, byte offsets from its start.
+template <int KD, int VD, bool FULL>
 struct Map {
   static constexpr uint32_t KQ = 0;                               // k rows 0..63, q rows 64..127; 64 columns an atom column
   static constexpr uint32_t V = KQ + KD / 64 * 16384;
-  static constexpr uint32_t P = V + VD / 64 * 8192;
-  static constexpr uint32_t X = P + 8192;                         // S^T bf16 [e][d], then the first two terms of V'' [j][e]
-  static constexpr uint32_t kS = (uint32_t)VD * KD * 2, kW = (uint32_t)VD * 64 * 2 * 2;
-  static constexpr uint32_t OS = X + (kS > kW ? kS : kW);         // the third term of V'', then o
+  static constexpr uint32_t P = V + VD / 64 * 8192;               // two terms
+  static constexpr uint32_t X = P + (FULL ? 16384 : 0);           // the first two terms of V'' [j][e]
+  static constexpr uint32_t OS = X + (uint32_t)VD * 64 * 2 * 2;   // the third, then o
   static constexpr uint32_t Tail = OS + VD / 64 * 8192;
   // rows 64..127 of a 64-row A tile are read (and ignored): they stay inside
-  static constexpr uint32_t kEnd = X + 32768 > OS + 16384 ? X + 32768 : OS + 16384;
-  static constexpr uint32_t Misc = Tail < kEnd ? kEnd : Tail;
+  static constexpr uint32_t Misc = Tail < OS + 16384 ? OS + 16384 : Tail;
   static constexpr uint32_t kGam = 4 * kWalkDecays;
-  static constexpr uint32_t Gam = Misc;   // a chunk's decays, as they lie in memory; two chunks'
-  static constexpr uint32_t Bar = Misc + 2 * kGam, Flags = Bar + 64;
-  static constexpr uint32_t Used = Flags + 64;
-  static constexpr uint32_t Bytes = Used + 1024;
-  static constexpr int Cols = KD + 128 <= 256 ? 256 : 512;        // TMEM: U^T, Q K^T / OP^T, OQ^T
+  static constexpr uint32_t Gam = Misc;   // a chunk's decays, as they lie in memory; without outputs two chunks'
+  static constexpr uint32_t Bar = Misc + (FULL ? 1 : 2) * kGam, Flags = Bar + 64;
+  static constexpr uint32_t Bytes = Flags + 64;
+  static constexpr int Cols = KD + 128 <= 256 ? 256 : 512;        // TMEM: U^T and S^T's copy, Q K^T / OP^T, OQ^T
   static constexpr int Ctas = KD == 256 ? 1 : 2;
+  static_assert(Ctas * (Bytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // A whole 32-byte sector a thread; a warp's lanes write 1 KB side by side.
@@ -100,8 +101,8 @@ __device__ __forceinline__ Two log2_units(Two a) {
 // Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i}, e^{b_last} in two floats
 // and what the first lacks to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
 // differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads take 28 us, as
-// they are 8).  o's weights, rounded to bf16, take the first 24 bits: a sum of 64 times the cut is off by 2^-11.  A
-// warp takes a chunk and head at a time.  (Within the
+// they are 8).  o's weights take the first 24 bits: behind 64 tokens at the cut the difference of two sums is off by 2^-11,
+// behind one by 2^-17, under the 2^-9 of o's own rounding.  A warp takes a chunk and head at a time.  (Within the
 // kernels below it was one warp's work for 2000 cycles a chunk, while the others waited.)  4 MB read, 17 MB written: the
 // 8 us are latency.
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
@@ -137,21 +138,20 @@ __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g
 }
 
 // The walk over a segment's chunks.  ADJ: backwards, x = q, y = do, weights scale e^{b_i}: the adjoint of the state.
-// 32 heads of 128: with outputs (kFull), 300 us for 4 x 8192 tokens and 82 for 8192 (3.6 TB/s of q, k, v and o); the
-// segments' own (kOwn) before it 117 and 37; states for the backward pass (kEmit), 139 us for 4 x 4096 tokens (5.8 TB/s,
+// 32 heads of 128: with outputs (kFull), 314 us for 4 x 8192 tokens and 86 for 8192 (3.4 TB/s of q, k, v and o); the
+// segments' own (kOwn) before it 122 and 39; states for the backward pass (kEmit), 137 us for 4 x 4096 tokens (5.9 TB/s,
 // 537 MB of them written: rows of S^T a lane took 152).  All but the last are bound by the chain of a chunk's phases:
 // tensor pipe 28 to 33 %, HBM 30 %, the schedulers issue a third of the time with two CTAs an SM.  A third CTA has no
 // room.
 template <int KD, int VD, int MODE, bool ADJ>
-__global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
+__global__ void __launch_bounds__(kTcThreads, (Map<KD, VD, MODE == kFull>::Ctas))
     lin_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const TcParams prm) {
-  using M = Map<KD, VD>;
   constexpr bool FULL = MODE == kFull;
+  using M = Map<KD, VD, FULL>;
   constexpr int KH = KD / 2;   // columns of S^T a thread holds
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t s4 = (smem_u32(sm) & 0x3FFFFu) >> 4;
   // Every barrier completes one phase a chunk, and every thread that waits for it does so once a chunk, in order.
   // Without outputs there is room for two chunks' loads, each with barriers of its own (bars 0, 1 and 2, 3).
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
   constexpr bool TWO = !FULL;
   auto buffer = [&](int i) { return TWO ? i & 1 : 0; };
   auto k_tile = [&](int i) { return M::KQ + 8192u * buffer(i); };   // the second in the place of Q
-  auto v_tile = [&](int i) { return buffer(i) ? M::X : M::V; };     // the second in the place of the state's copy
+  auto v_tile = [&](int i) { return buffer(i) ? M::X : M::V; };     // the second in the place of V'''s first term
   auto load_bar = [&](int which, int i) { return bars + which + 2 * buffer(i); };
   auto load_no = [&](int i) { return TWO ? i >> 1 : i; };
   auto decays_of = [&](int i) { return reinterpret_cast<const float*>(sm + M::Gam + M::kGam * buffer(i)); };
@@ -294,14 +294,19 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
         }
       }
     }
-    if (FULL && row < VD) {
+    if (FULL) {
+      // in the place of U^T, whose columns of this half this thread has just read: KH / 2 columns for the first terms,
+      // then as many for the second
+      if (tid == 0) bulk_wait_read();   // the o staging has been read: its place takes a term of V''
 #pragma unroll
-      for (int b = 0; b < KH; b += 8) {
-        const int d = hf * KH + b;
-        *reinterpret_cast<uint4*>(sm + M::X + (d >> 6) * (VD * 128) + sw128_chunk(row, (d & 63) >> 3)) =
-            make_uint4(pack_bf16(S[b], S[b + 1]), pack_bf16(S[b + 2], S[b + 3]), pack_bf16(S[b + 4], S[b + 5]),
-                       pack_bf16(S[b + 6], S[b + 7]));
+      for (int b = 0; b < KH; b += 32) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) split2(S[b + 2 * u], S[b + 2 * u + 1], hi[u], lo[u]);
+        tmem_st16(R_U + lane_off + hf * KH + b / 2, hi);
+        tmem_st16(R_U + lane_off + hf * KH + KH / 2 + b / 2, lo);
       }
+      tmem_wait_st();
     }
     if (MODE == kEmit && row < VD) {
       float* to = prm.emit + ((chunk_slot(p) + at) * prm.Hv + h) * (int64_t)(KD * VD) + hf * KH * VD + row * 8;
@@ -331,19 +336,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     }
     if (FULL) {
       if (tid == 0) {
-        bulk_wait_read();   // the o staging has been read
         const uint32_t id = idesc_bf16(128, 64, 0, 0, 0);
         wait(bar_q, i);
-        if (!bad) {
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < KD / 16; ++s) {
-            const uint32_t a = M::X + (s >> 2) * (VD * 128) + (s & 3) * 32;
-            const uint32_t b = M::KQ + 8192 + (s >> 2) * 16384 + (s & 3) * 32;
-            mma_bf16(R_b, dsw(s4, a, 16), dsw(s4, b, 16), id, s > 0);
-          }
-          commit(3, i);
-        }
         wait(bar_k, i);
         if (!bad) {
           tc_fence_after();
@@ -353,6 +347,13 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
             mma_bf16(R_a, dsw(s4, a, 16), dsw(s4, a, 16), id, s > 0);
           }
           commit(2, i);
+#pragma unroll
+          for (int s = 0; s < 2 * (KD / 16); ++s) {   // the second terms first
+            const int d = s % (KD / 16), half = 16 * d / KH;
+            const uint32_t a = R_U + half * KH + (16 * d - half * KH) / 2 + (s < KD / 16 ? KH / 2 : 0);
+            mma_bf16_ta(R_b, a, dsw(s4, M::KQ + 8192 + (d >> 2) * 16384 + (d & 3) * 32, 16), id, s > 0);
+          }
+          commit(3, i);
         }
       }
       __syncwarp();
@@ -382,7 +383,6 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
             }
           }
         }
-        // the second term in the place of Q, which both of its products have read
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t hi[4], lo[4];
@@ -390,14 +390,13 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
           for (int u = 0; u < 4; ++u) split2(v[8 * q + 2 * u], v[8 * q + 2 * u + 1], hi[u], lo[u]);
           const uint32_t off = sw128_chunk(i2, 4 * hf + q);
           *reinterpret_cast<uint4*>(sm + M::P + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(sm + M::KQ + 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(sm + M::P + 8192 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       // V'': the warps without weights begin with five eighths of it, the one whose weights are all zero takes as
       // much as the three others behind theirs
       wait(bar_k, i);
       wait(bar_v, i);
-      wait(bar_qs, i);   // the state's copy has been read: its place takes V''
       constexpr int n = 64 * (VD / 8);
       constexpr uint32_t x2 = M::X + VD / 64 * 8192;
       if (qd < 2) weigh_values<VD>(sm, M::V, M::X, x2, M::OS, down, 64 * hf + row, n * 5 / 8, 128);
@@ -418,7 +417,11 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
     tc_fence_before();
     if (__syncthreads_or(bad)) break;
     tc_fence_after();
-    if (tid == 0) {
+    if (FULL && tid == 0) {   // U^T takes the place of S^T's copy (products of different shapes need not end in order)
+      wait(bar_qs, i);
+      tc_fence_after();
+    }
+    if (tid == 0 && !bad) {
       const uint32_t idu = idesc_bf16(128, KD, 1, 1, 0);
       // the third term first: its place takes o, which is written once V^T P^T, issued behind it, is complete
 #pragma unroll
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
 #pragma unroll
         for (int s = 0; s < 8; ++s)
           mma_bf16(R_a, dsw(s4, M::V + (s & 3) * 2048, 8192),
-                   dsw(s4, (s >> 2 ? M::KQ + 8192 : M::P) + (s & 3) * 32, 16), id, s > 0);
+                   dsw(s4, M::P + (s >> 2) * 8192 + (s & 3) * 32, 16), id, s > 0);
         commit(4, i);
       }
 #pragma unroll
@@ -448,6 +451,8 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD>::Ctas))
       uint8_t* lbase = sm + M::OS + (row >> 6) * 8192 + (odd ? 128 : 0) + (ecol & 7) * 2;
       const uint32_t xsw = (static_cast<uint32_t>((ecol >> 3) ^ (odd ? 1 : 0))) << 4;
       float oq[32];
+      wait(bar_qs, i);
+      tc_fence_after();
       tmem_ld32(R_b + lane_off + 32 * hf, oq);
       wait(bar_pv, i);
       tc_fence_after();
@@ -562,9 +567,9 @@ struct Maps {
 template <int KD, int VD, int MODE, bool ADJ>
 gdn_status launch_one(unsigned grid, const Maps& m, const TcParams& prm, cudaStream_t s) {
   auto kern = lin_tc_kernel<KD, VD, MODE, ADJ>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Map<KD, VD>::Bytes) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  kern<<<grid, kTcThreads, Map<KD, VD>::Bytes, s>>>(m.q, m.x, m.y, m.o, prm);
+  constexpr int bytes = (int)Map<KD, VD, MODE == kFull>::Bytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return GDN_ERR_CUDA;
+  kern<<<grid, kTcThreads, bytes, s>>>(m.q, m.x, m.y, m.o, prm);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -6,16 +6,18 @@
 // terms each, all of their 24 bits: dg, an fp32 output, is a sum over products with them (with two terms it was off by
 // up to 1.2e-5 in sequences without decay).  Persistent CTAs, one an SM (the chunk's tiles, S0 and G fill its shared
 // memory), take chunks in turn; the next chunk's S0 comes in while this one's gradients are formed, its tiles and G are
-// prefetched to L2.  4 x 4096 tokens of 32 heads of 128: 570 us (3.5 TB/s of S0, G, the inputs and the gradients; HBM
-// 39 %, tensor pipe 25 %): a chunk takes 20k cycles, 5k of products, 5k of their operands' shared-memory reads, 2.5k of
-// splitting S0 and G, and barriers between.  Tiles released earlier (561 us) or a warp that only issues (678, registers)
-// did not help.
+// prefetched to L2.  4 x 4096 tokens of 32 heads of 128: 610 us (3.3 TB/s of S0, G, the inputs and the gradients; 570
+// with W and P in one term, at which HBM 39 %, tensor pipe 25 %, and a chunk 20k cycles, 5k of products, 5k of their
+// operands' shared-memory reads, 2.5k of splitting S0 and G, and barriers between).  Tiles released earlier (561 against
+// 570) or a warp that only issues (678, registers) did not help.
 // TMEM lane = token: rows 0..63 of every stacked product are keys' rows, 64..127 queries'.
 //
 //   D1 = [K;Q] [K;Q]^T, D2 = [V;dO] [V;dO]^T   (lanes 0..63: columns 64..127 are K Q^T, V dO^T; lanes 64..127: columns
 //                                              0..63 are Q K^T, dO V^T: both orientations in one product each)
 //   I1 = [V;dO] S0^T, I2 = [V;dO] G^T          (S0, G in three terms)    lanes 64..127: dO S0^T;  lanes 0..63: V G^T
-//   W = scale M (dO V^T), W^T, P^T             bf16, from D1, D2; row and column sums of A = W (Q K^T) in fp32
+//   W = scale M (dO V^T), W^T, P^T             from D1, D2, in two bf16 terms (with one dq, dk and dv were off by up to
+//                                              2.3e-3, with two by their own rounding, 1.7e-3); row and column sums of
+//                                              A = W (Q K^T) in fp32
 //   D1 <- [W^T;W] K, D2 <- [W^T;W] Q           lanes 64..127: W K;  lanes 0..63: W^T Q
 //   dq_i = scale e^{b_i} I1 + D1,  dk_j = e^{b_last - b_j} I2 + D2
 //   I1 <- dO^T P^T | G^T K^T                   lane = value column:  dv_j = I1a + e^{b_last - b_j} I1b
@@ -53,7 +55,12 @@ struct GradMap {
   // tile of G read as 128 rows, the upper half ignored, stays inside as well.)
   static constexpr uint32_t X3 = G + 2 * kTile;
   static constexpr uint32_t W = X3, P = W + 16384, SumA = P + 8192, SumX = SumA + 2048;
-  static constexpr uint32_t Misc = X3 + 32768;
+  // the second terms of W^T, W: where there is no room of their own, in the place of S0's front, which the next chunk's
+  // then takes last; of P^T: in the place of W^T, once that has been read
+  static constexpr bool kRoom = KD * VD < 128 * 128;
+  static constexpr uint32_t W2 = kRoom ? X3 + 32768 : S, P2 = W;
+  static constexpr uint32_t kFront = kRoom ? 0 : 16384;
+  static constexpr uint32_t Misc = X3 + 32768 + (kRoom ? 16384 : 0);
   static constexpr uint32_t kGam = 4 * kDecays;
   static constexpr uint32_t Gam = Misc, Down = Misc + 256, Up = Misc + 512, Whole = Misc + 768, Low = Whole + 16;
   static constexpr uint32_t Red = Misc + kGam;   // float[16]
@@ -151,7 +158,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const Piece p = piece_of(prm.pc, item / prm.Hv);
     count[1] = n + 1;
     mbar_arrive_expect_tx(bar_s, 2 * M::kTile);
-    bulk_load(sm + M::S, prm.states + cell(p, item % prm.Hv) * (KD * VD), 2 * M::kTile, bar_s);
+    bulk_load(sm + M::S + M::kFront, prm.states + cell(p, item % prm.Hv) * (KD * VD) + M::kFront / 4,
+              2 * M::kTile - M::kFront, bar_s);
+  };
+  auto issue_front = [&](int item) {   // the rest of it
+    if (M::kFront == 0) return;
+    const Piece p = piece_of(prm.pc, item / prm.Hv);
+    bulk_load(sm + M::S, prm.states + cell(p, item % prm.Hv) * (KD * VD), M::kFront, bar_s);
   };
   auto issue_adjoint = [&](int item, int n) {
     const Piece p = piece_of(prm.pc, item / prm.Hv);
@@ -162,6 +175,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   if (tid == 0) {
     issue_tiles(blockIdx.x, 0);
     issue_state(blockIdx.x, 0);
+    issue_front(blockIdx.x);
     issue_adjoint(blockIdx.x, 0);
   }
 
@@ -277,6 +291,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     // ---- W, W^T, P^T and the sums of A
     wait(bar_d, n);
     tc_fence_after();
+    uint32_t plow[2][4];   // P^T's second term
     {
       float qk[16], ov[16];
       const uint32_t at = (query ? 0 : 64) + 16 * part;
@@ -310,11 +325,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       __syncwarp();
       wait(bar_i, n);   // S0 and the third term of G have been read
       if (tid == 0 && more && !bad) issue_state(item + gridDim.x, n + 1);
-      solve64::store8_bf16(sm + M::W + sw128_chunk(row, 2 * part), w);
-      solve64::store8_bf16(sm + M::W + sw128_chunk(row, 2 * part + 1), w + 8);
-      if (!query) {
-        solve64::store8_bf16(sm + M::P + sw128_chunk(row, 2 * part), pt);
-        solve64::store8_bf16(sm + M::P + sw128_chunk(row, 2 * part + 1), pt + 8);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t off = sw128_chunk(row, 2 * part + u);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split2(w[8 * u + 2 * j], w[8 * u + 2 * j + 1], hi[j], lo[j]);
+        *reinterpret_cast<uint4*>(sm + M::W + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sm + M::W2 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split2(pt[8 * u + 2 * j], pt[8 * u + 2 * j + 1], hi[j], plow[u][j]);
+        if (!query) *reinterpret_cast<uint4*>(sm + M::P + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       }
       suma[part * 128 + row] = s;
     }
@@ -325,16 +346,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (tid == 0) {
       const uint32_t id = idesc_bf16(128, KD, 0, 1, 0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        mma_bf16(D1, dsw(s4, M::W + s * 32, 16), dsw(s4, M::KQ + s * 2048, 16384), id, s > 0);
+      for (int s = 0; s < 8; ++s)   // the second terms first
+        mma_bf16(D1, dsw(s4, (s >> 2 ? M::W : M::W2) + (s & 3) * 32, 16), dsw(s4, M::KQ + (s & 3) * 2048, 16384), id,
+                 s > 0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        mma_bf16(D2, dsw(s4, M::W + s * 32, 16), dsw(s4, M::KQ + 8192 + s * 2048, 16384), id, s > 0);
+      for (int s = 0; s < 8; ++s)
+        mma_bf16(D2, dsw(s4, (s >> 2 ? M::W : M::W2) + (s & 3) * 32, 16),
+                 dsw(s4, M::KQ + 8192 + (s & 3) * 2048, 16384), id, s > 0);
       commit(5, n);
     }
     __syncwarp();
     wait(bar_w, n);
     tc_fence_after();
+    if (tid == 0 && more && !bad) issue_front(item + gridDim.x);
+    if (!query) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<uint4*>(sm + M::P2 + sw128_chunk(row, 2 * part + u)) =
+            make_uint4(plow[u][0], plow[u][1], plow[u][2], plow[u][3]);
+    }
     // ---- dq (lanes 64..127), dk (lanes 0..63)
     {
       constexpr int COLS = KD / 4;   // of this thread
@@ -380,6 +410,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       sumx[part * 128 + row] = (x2.x + x2.y) * f;
     }
+    fence_proxy_async();
     tc_fence_before();
     if (__syncthreads_or(bad)) break;
     tc_fence_after();
@@ -387,8 +418,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (tid == 0) {
       const uint32_t ida = idesc_bf16(128, 64, 1, 0, 0), idb = idesc_bf16(128, 64, 0, 0, 0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        mma_bf16(I1, dsw(s4, M::VO + 8192 + s * 2048, 16384), dsw(s4, M::P + s * 32, 16), ida, s > 0);
+      for (int s = 0; s < 8; ++s)
+        mma_bf16(I1, dsw(s4, M::VO + 8192 + (s & 3) * 2048, 16384),
+                 dsw(s4, (s >> 2 ? M::P : M::P2) + (s & 3) * 32, 16), ida, s > 0);
 #pragma unroll
       for (int s = 0; s < 2 * (KD / 16); ++s) {   // two of G's terms
         const int k = s % (KD / 16);

@@ -574,7 +574,8 @@ gdn_status gdn_selective_scan_step(const gdn_scan_problem* p, const void* x, con
  *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
  * States and sums are fp32; o is rounded once to p->dt (bf16: products of bf16
  * operands, the weights between tokens and the copy of the state that o is
- * formed from as sums of two bf16 values each; final states keep fp32 accuracy).
+ * formed from as sums of two bf16 values each, and so for the gradients'
+ * weights; final states keep fp32 accuracy).
  *
  * Problem description.
  *   B, T, N, Hqk, Hv, K, V, varlen : as for gdn_problem (Hv at most 1024)

@@ -90,6 +90,9 @@ def test_gradients_of_slow_decays(gdn, g, dtype):
     want = ref.backward(x["q"], x["k"], x["v"], x["g"], do, 0.25, h0, h0)
     for n in ("dg", "dh0"):
         assert ref.rel(d[n], want[n]) <= 1e-6 + carried(64), n
+    if dtype is BF:
+        for n in ("dq", "dk", "dv"):
+            once(d[n], want[n])
 
 
 @pytest.mark.parametrize("g", [-1e-3, -1e-5])
@@ -117,6 +120,24 @@ def test_outputs_are_rounded_once(gdn, g, K, V):
         assert ref.rel(ht, wh) <= carried(6)
 
 
+@pytest.mark.parametrize("K,V", DIMS)
+@pytest.mark.parametrize("Hqk", [1, 2])
+@pytest.mark.parametrize("g", [0.0, -2.0 ** -8, -0.3])
+def test_gradients_are_rounded_once(gdn, g, Hqk, K, V):
+    x, do, h0 = slow(BF, 333, g, K=K, V=V, seed=K + V)
+    if Hqk == 2:   # heads of their own write dq and dk themselves
+        x["q"], x["k"] = (torch.cat((x[n], x[n].flip(1)), 2) for n in ("q", "k"))
+    for a, init in ((333, h0), (333, None), (70, h0)):
+        y = {n: t[:, :a].contiguous() for n, t in x.items()}
+        d = gdn.gdn_linear_attn_bwd(**y, dout=do[:, :a].contiguous(), scale=0.25, h0=init, dht=init, want_dh0=True)
+        want = ref.backward(y["q"], y["k"], y["v"], y["g"], do[:, :a], 0.25, init, init)
+        for n in ("dq", "dk", "dv"):
+            once(d[n], want[n])
+        # fp32 whatever the inputs' type
+        assert ref.rel(d["dh0"], want["dh0"]) <= carried(6)
+        assert ref.rel(d["dg"], want["dg"]) <= 1e-6
+
+
 def test_the_same_bits_with_the_device_full(gdn):
     """More CTAs than run at once, several of them an SM."""
     for K, V in ((128, 128), (64, 128), (128, 64), (64, 64)):
@@ -133,10 +154,14 @@ def test_the_same_bits_with_the_device_full(gdn):
 @pytest.mark.parametrize("lens", [[3, 0, 64, 100, 1], [700, 5]])
 def test_packed_outputs_are_rounded_once(gdn, lens):
     T = sum(lens)
-    x, _, _ = slow(BF, T, -2.0 ** -8, K=128, V=128)
+    x, do, _ = slow(BF, T, -2.0 ** -8, K=128, V=128)
     cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device=DEV)
     h0 = torch.randn(len(lens), 2, 128, 128, device=DEV)
     o, ht = gdn.gdn_linear_attn_fwd(**x, scale=0.25, h0=h0, cu_seqlens=cu)
     want, wh = ref.forward(x["q"], x["k"], x["v"], x["g"], 0.25, h0, cu)
     once(o, want)
     assert ref.rel(ht, wh) <= carried(11)
+    d = gdn.gdn_linear_attn_bwd(**x, dout=do, scale=0.25, h0=h0, dht=h0, cu_seqlens=cu)
+    want = ref.backward(x["q"], x["k"], x["v"], x["g"], do, 0.25, h0, h0, cu)
+    for n in ("dq", "dk", "dv"):
+        once(d[n], want[n])

@@ -102,7 +102,7 @@ __device__ __forceinline__ Two log2_units(Two a) {
 // and what the first lacks to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
 // differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads take 28 us, as
 // they are 8).  o's weights take the first 24 bits: behind 64 tokens at the cut the difference of two sums is off by 2^-11,
-// behind one by 2^-17, under the 2^-9 of o's own rounding.  A warp takes a chunk and head at a time.  (Within the
+// behind one by 2^-17, under the 2^-8 of o's own rounding.  A warp takes a chunk and head at a time.  (Within the
 // kernels below it was one warp's work for 2000 cycles a chunk, while the others waited.)  4 MB read, 17 MB written: the
 // 8 us are latency.
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,

@@ -103,9 +103,20 @@ __device__ __forceinline__ float row_sum(float v, float* sm, int& phase) {
   return v;
 }
 
-// 1 / (1 + e^-z) by the exponential and reciprocal units: within 2^-21 + |z| 2^-24 of it, relatively; far out it is 0
-// or 1.  (expf and a division take three times the instructions and would bound the gated norm.)
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + e^-z), and what it lacks to 1.  For bf16 rows by the exponential and reciprocal units: within 2^-21 + |z| 2^-24
+// of it, relatively (far out it is 0 or 1), which the outputs' rounding covers.  fp32 rows keep their bits, within 2^-22 of
+// each: e^-|z| by expf, whose argument is not rounded, and both values as quotients by 1 + e^-|z|.
+template <typename T>
+__device__ __forceinline__ float sigmoid_f(float z, float& rest) {
+  if constexpr (sizeof(T) == 4) {
+    const float e = expf(-fabsf(z)), r = __fdividef(1.f, 1.f + e), er = e * r;
+    rest = z >= 0.f ? er : r;
+    return z >= 0.f ? r : er;
+  }
+  const float s = __fdividef(1.f, 1.f + __expf(-z));
+  rest = 1.f - s;
+  return s;
+}
 
 // ------------------------------------------------------------- gated norm
 template <typename T, int VEC, int NV, int GROUP>
@@ -162,7 +173,8 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) gated_fwd_kernel(
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float u = a[i][j] * r * c[j];
-        a[i][j] = z ? u * (g[j] * sigmoid_f(g[j])) : u;
+        float rest;
+        a[i][j] = z ? u * (g[j] * sigmoid_f<T>(g[j], rest)) : u;
       }
       store_vec<T, VEC>(y + row * V + e, a[i]);
     }
@@ -236,8 +248,9 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) gated_bwd_kernel(
         xh[i][j] = h;
         float du = d[i][j];
         if (z) {
-          const float zv = zz[i][j], sg = sigmoid_f(zv);
-          zz[i][j] = du * h * wv[i][j] * (sg * fmaf(zv, 1.f - sg, 1.f));
+          float rest;
+          const float zv = zz[i][j], sg = sigmoid_f<T>(zv, rest);
+          zz[i][j] = du * h * wv[i][j] * (sg * fmaf(zv, rest, 1.f));
           du *= zv * sg;
         }
         dw[i][j] = fmaf(du, h, dw[i][j]);

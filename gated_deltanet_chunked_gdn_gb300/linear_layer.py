@@ -71,7 +71,10 @@ class ResidualNorm(torch.autograd.Function):
     @_first_order
     def backward(ctx, dh, dn):
         y, residual, post_weight, gate, weight, rstd = ctx.saved_tensors
-        dn = torch.zeros_like(y, memory_format=torch.contiguous_format) if dn is None else dn.contiguous()
+        if weight is None:
+            dn = None   # there was no n
+        else:
+            dn = torch.zeros_like(y, memory_format=torch.contiguous_format) if dn is None else dn.contiguous()
         d = gdn.gdn_residual_norm_bwd(y, residual, rstd, None if dh is None else dh.contiguous(), dn,
                                       post_weight=post_weight, gate=gate, residual_scale=ctx.scale, weight=weight)
         return d["dy"], d["dresidual"], d["dpost_weight"], d["dgate"], None, d["dweight"], None

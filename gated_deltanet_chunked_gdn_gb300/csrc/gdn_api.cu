@@ -547,6 +547,25 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_problem* pp, const void* q, cons
                         static_cast<cudaStream_t>(stream));
 }
 
+gdn_status gdn_selftest_linear_grads_timeout(const gdn_linear_problem* pp, const void* q, const void* k, const void* v,
+                                             const float* g, float scale, const void* dout, void* dq, void* dk, void* dv,
+                                             float* dg, void* workspace, size_t workspace_bytes, int batch,
+                                             unsigned warps, void* stream) {
+  gdn_linear_problem p;
+  const gdn_status st = linear_problem_ok(pp, &p);
+  if (st != GDN_OK) return st;
+  if (p.dt != GDN_F32 || p.varlen || p.g_per_head || p.Hqk != p.Hv || p.K < 128 || p.V < 128 || batch < 0 || !warps)
+    return GDN_ERR_UNSUPPORTED;
+  if (!linear_inputs_ok(p, q, k, v, g, nullptr) || !dout || !dq || !dk || !dv || !dg) return GDN_ERR_INVALID_ARG;
+  const void* a16[] = {dout, dq, dk, dv};
+  for (const void* x : a16)
+    if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(dg, 4) || !workspace || !aligned(workspace, kAlign) || workspace_bytes < linear_bwd_workspace_bytes(p))
+    return GDN_ERR_INVALID_ARG;
+  return run_linear_bwd_drop(p, q, k, v, g, scale, dout, dq, dk, dv, dg, workspace, batch, warps,
+                             static_cast<cudaStream_t>(stream));
+}
+
 gdn_status gdn_linear_attn_get_device_status(void* workspace, void* stream, int* dev_status) {
   if (!workspace || !dev_status) return GDN_ERR_INVALID_ARG;
   int32_t host = 0;

@@ -188,6 +188,9 @@ size_t linear_bwd_workspace_bytes(const gdn_linear_problem& p);
 gdn_status run_linear_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                           float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht,
                           void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s);
+gdn_status run_linear_bwd_drop(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                               float scale, const void* dout, void* dq, void* dk, void* dv, float* dg, void* ws,
+                               int batch, unsigned warps, cudaStream_t s);
 
 // Norms (gdn_norms.cu); gmode as gdn_gate.
 constexpr int kNormMaxWidth = 16384;

@@ -61,13 +61,15 @@ struct GradMap32 {
 // Gradients of one chunk of one value head.  TMEM lane = token (Q K^T, dO V^T) or column of K or V (all else, so that a
 // warp writes 32 neighbours of a row); one batch of products at a time, the next tiles' loads under it.  Bound by those
 // rounds of loading, splitting, products and a wait (seven for K = V = 128, 10k cycles each; tensor pipe 15 %, HBM 16 %,
-// issue 27 % with 16 warps).  2 x 4096 tokens of 16 heads: fp32 of 128 494 us (fp32 FMAs on 64 x 64 tiles: 950), bf16 of
-// 256 866 (3040).  Prefetching the states of the CTA behind to L2 changed nothing (498, 916).
-template <typename T, typename TG, int DB, int EB>
+// issue 27 % with 16 warps).  2 x 4096 tokens of 16 heads: fp32 of 128 500 us (fp32 FMAs on 64 x 64 tiles: 950), bf16 of
+// 256 877 (3040).  Prefetching the states of the CTA behind to L2 changed nothing (498 against 494, 916 against 866).
+// DROP (a test's): the waits for one batch of products run out in some warps of the first CTA.
+template <typename T, typename TG, int DB, int EB, bool DROP>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ dout, Shape d,
     const float* __restrict__ g, Pieces pc, float scale, const float* __restrict__ S0, const float* __restrict__ G,
-    TG* __restrict__ dq, TG* __restrict__ dk, T* __restrict__ dv, float* __restrict__ dg, int32_t* status) {
+    TG* __restrict__ dq, TG* __restrict__ dk, T* __restrict__ dv, float* __restrict__ dg, int32_t* status,
+    int drop_batch, uint32_t drop_warps) {
   using M = GradMap32<T, DB, EB>;
   constexpr int TERMS = M::TERMS, N = kGradThreads;
   constexpr uint32_t kT = M::kT;
@@ -116,10 +118,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
   const float* sp = S0 + ((int64_t)c * d.Hv + h) * d.K * d.V;
   const float* gp = G + ((int64_t)c * d.Hv + h) * d.K * d.V;
 
+  // A warp's waits can run out when another's do not.  `good` is the warp's own from drained() to the next ready(), which
+  // makes it the CTA's: no loop begins, ends or is left on it but behind ready(), or warps would meet different barriers.
   int n = 0;          // batches of products issued
   bool good = true;
   auto drained = [&] {   // they have been read and summed
     if (good && n > 0) good = warp_wait(bar, (n - 1) & 1, status);
+    if constexpr (DROP)
+      if (blockIdx.x == 0 && n - 1 == drop_batch && (drop_warps >> warp & 1)) {
+        good = false;
+        if (lane == 0) atomicExch(status, GDN_DEV_WAIT_TIMEOUT);
+      }
   };
   auto ready = [&] {     // tiles are in place, TMEM has been read
     fence_proxy_async();
@@ -145,7 +154,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
 
   // ---- Q K^T
 #pragma unroll 1
-  for (int kb = 0; kb < d.K / 64 && good; ++kb) {
+  for (int kb = 0; kb < d.K / 64; ++kb) {
     float4 xq[2], xk[2];
     fetch<64, 64, N>(xq, qp + 64 * kb, d.ldq, p.len);
     fetch<64, 64, N>(xk, kp + 64 * kb, d.ldk, p.len);
@@ -171,9 +180,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
   // ---- DB columns of dq, dk at a time
   float gs = 0.f;   // <G, S0>
 #pragma unroll 1
-  for (int db = 0; db < d.K / DB && good; ++db) {
+  for (int db = 0; db < d.K / DB; ++db) {
 #pragma unroll 1
-    for (int vb = 0; vb < d.V / 64 && good; ++vb) {
+    for (int vb = 0; vb < d.V / 64; ++vb) {
       float4 xo[2], xv[2], xs[DB / 32], xg[DB / 32];
       fetch<64, 64, N>(xo, op + 64 * vb, ldo, p.len);
       fetch<64, 64, N>(xv, vp + 64 * vb, d.ldv, p.len);
@@ -312,9 +321,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
   }
   // ---- EB columns of dv at a time
 #pragma unroll 1
-  for (int eb = 0; eb < d.V / EB && good; ++eb) {
+  for (int eb = 0; eb < d.V / EB; ++eb) {
 #pragma unroll 1
-    for (int kb = 0; kb < d.K / 64 && good; ++kb) {
+    for (int kb = 0; kb < d.K / 64; ++kb) {
       float4 xg[EB / 32], xk[2], xo[EB / 32];
       fetch<64, EB, N>(xg, gp + (int64_t)64 * kb * d.V + eb * EB, d.V, 64);
       fetch<64, 64, N>(xk, kp + 64 * kb, d.ldk, p.len);
@@ -346,6 +355,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
       ++n;
       __syncwarp();
     }
+    if (!good) break;
     drained();
     tc_fence_after();
     if (good) {
@@ -406,26 +416,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, typename TG, int DB, int EB>
+// What a test drops of the first CTA's waits (-1: nothing).
+struct Drop {
+  int batch;
+  uint32_t warps;
+};
+
+template <typename T, typename TG, int DB, int EB, bool DROP>
 gdn_status launch_grads(int most, const T* q, const T* k, const T* v, const T* dout, const Shape& d, const float* g,
                         const Pieces& pc, float scale, const float* S, const float* G, TG* dq, TG* dk, T* dv,
-                        float* dg, int32_t* status, cudaStream_t s) {
-  auto kern = grads_kernel<T, TG, DB, EB>;
+                        float* dg, int32_t* status, Drop drop, cudaStream_t s) {
+  auto kern = grads_kernel<T, TG, DB, EB, DROP>;
   constexpr int bytes = (int)GradMap32<T, DB, EB>::Bytes;
   static_assert(bytes <= 232448, "shared memory of one SM");
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GDN_ERR_CUDA;
   kern<<<(unsigned)((int64_t)most * d.Hv), kGradThreads, bytes, s>>>(q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv,
-                                                                     dg, status);
+                                                                     dg, status, drop.batch, drop.warps);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <typename T, typename TG>
 gdn_status run_grads(int most, const T* q, const T* k, const T* v, const T* dout, const Shape& d, const float* g,
                      const Pieces& pc, float scale, const float* S, const float* G, TG* dq, TG* dk, T* dv, float* dg,
-                     int32_t* status, cudaStream_t s) {
-#define GDN_GRADS(DB, EB) \
-  return launch_grads<T, TG, DB, EB>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dg, status, s)
+                     int32_t* status, Drop drop, cudaStream_t s) {
+#define GDN_GRADS_DROP(DB, EB, DROP) \
+  return launch_grads<T, TG, DB, EB, DROP>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dg, status, drop, s)
+#define GDN_GRADS(DB, EB) GDN_GRADS_DROP(DB, EB, false)
+  if constexpr (sizeof(T) == 4 && sizeof(TG) == 4) {
+    if (drop.batch >= 0) GDN_GRADS_DROP(128, 128, true);
+  }
   if (d.K == 64 && d.V != 64) GDN_GRADS(64, 128);
   if (d.K != 64 && d.V == 64) GDN_GRADS(128, 64);
   if constexpr (sizeof(T) == 4) {   // bf16 comes here with a head dim of 256 alone
@@ -433,6 +453,7 @@ gdn_status run_grads(int most, const T* q, const T* k, const T* v, const T* dout
   }
   GDN_GRADS(128, 128);
 #undef GDN_GRADS
+#undef GDN_GRADS_DROP
 }
 
 // dg of fixed decays: the chunks' sums of one head, in a fixed order
@@ -474,7 +495,7 @@ Layout layout_of(const gdn_linear_problem& p) {
 template <typename T>
 gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v, const float* g, float scale,
                  const float* h0, const T* dout, const float* dht, T* dq, T* dk, T* dv, float* dg, float* dh0,
-                 const Pieces& pc, const Layout& L, uint8_t* ws, cudaStream_t s) {
+                 const Pieces& pc, const Layout& L, uint8_t* ws, Drop drop, cudaStream_t s) {
   const Shape d = shape_of(p);
   const int most = pieces_max(p, kC);
   int32_t* status = reinterpret_cast<int32_t*>(ws);
@@ -498,9 +519,9 @@ gdn_status bwd_t(const gdn_linear_problem& p, const T* q, const T* k, const T* v
     float* dgp = p.g_per_head ? part : dg;
     if (shared)
       st = run_grads<T, float>(most, q, k, v, dout, d, g, pc, scale, S, G, reinterpret_cast<float*>(ws + L.dq),
-                               reinterpret_cast<float*>(ws + L.dk), dv, dgp, status, s);
+                               reinterpret_cast<float*>(ws + L.dk), dv, dgp, status, drop, s);
     else
-      st = run_grads<T, T>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dgp, status, s);
+      st = run_grads<T, T>(most, q, k, v, dout, d, g, pc, scale, S, G, dq, dk, dv, dgp, status, drop, s);
     if (st != GDN_OK) return st;
   }
   if (shared && (int64_t)p.B * p.T > 0) {
@@ -521,9 +542,9 @@ gdn_status launch_head_decays(const gdn_linear_problem& p, const float* part, co
 
 size_t bwd32_bytes(const gdn_linear_problem& p) { return layout_of(p).end; }
 
-gdn_status bwd32(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
-                    float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht, void* dq,
-                    void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s) {
+gdn_status bwd32(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g, float scale,
+                 const float* h0, const int32_t* cu, const void* dout, const float* dht, void* dq, void* dk, void* dv,
+                 float* dg, float* dh0, void* ws, Drop drop, cudaStream_t s) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   int32_t* status = reinterpret_cast<int32_t*>(at);
   const Layout L = layout_of(p);
@@ -531,10 +552,10 @@ gdn_status bwd32(const gdn_linear_problem& p, const void* q, const void* k, cons
   const Pieces pc = pieces_at(p, kC, at + L.tables);
   if (p.dt == GDN_F32)
     return bwd_t<float>(p, (const float*)q, (const float*)k, (const float*)v, g, scale, h0, (const float*)dout, dht,
-                        (float*)dq, (float*)dk, (float*)dv, dg, dh0, pc, L, at, s);
+                        (float*)dq, (float*)dk, (float*)dv, dg, dh0, pc, L, at, drop, s);
   using T = __nv_bfloat16;
   return bwd_t<T>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, h0, (const T*)dout, dht, (T*)dq, (T*)dk, (T*)dv,
-                  dg, dh0, pc, L, at, s);
+                  dg, dh0, pc, L, at, drop, s);
 }
 
 }  // namespace lin
@@ -546,7 +567,16 @@ size_t linear_bwd_workspace_bytes(const gdn_linear_problem& p) {
 gdn_status run_linear_bwd(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
                           float scale, const float* h0, const int32_t* cu, const void* dout, const float* dht,
                           void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, cudaStream_t s) {
-  return (lin::tc_bwd_supported(p) ? lin::tc_bwd : lin::bwd32)(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, s);
+  if (lin::tc_bwd_supported(p))
+    return lin::tc_bwd(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, s);
+  return lin::bwd32(p, q, k, v, g, scale, h0, cu, dout, dht, dq, dk, dv, dg, dh0, ws, lin::Drop{-1, 0}, s);
+}
+
+gdn_status run_linear_bwd_drop(const gdn_linear_problem& p, const void* q, const void* k, const void* v, const float* g,
+                               float scale, const void* dout, void* dq, void* dk, void* dv, float* dg, void* ws,
+                               int batch, unsigned warps, cudaStream_t s) {
+  return lin::bwd32(p, q, k, v, g, scale, nullptr, nullptr, dout, nullptr, dq, dk, dv, dg, nullptr, ws,
+                    lin::Drop{batch, warps}, s);
 }
 
 }  // namespace gdn

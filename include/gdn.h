@@ -641,6 +641,17 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_problem* p, const void* q, const
                                const float* g, float scale, const float* h0, const int32_t* cu_seqlens,
                                const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
                                float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * Test hook: the backward (fp32, equal lengths, decays for each token, Hqk ==
+ * Hv, K and V 128 or 256, no states) in which the first CTA's warps named by the
+ * bits of `warps` see their wait for product batch `batch` run out.  The launch
+ * ends, the status word says GDN_DEV_WAIT_TIMEOUT and the gradients of the first
+ * 64 tokens of the first head are unfinished; all others are right.
+ */
+gdn_status gdn_selftest_linear_grads_timeout(const gdn_linear_problem* p, const void* q, const void* k, const void* v,
+                                             const float* g, float scale, const void* dout, void* dq, void* dk, void* dv,
+                                             float* dg, void* workspace, size_t workspace_bytes, int batch,
+                                             unsigned warps, void* stream);
 /* Status word that the last call on `workspace` left (forward or backward;
  * synchronises `stream`, then clears the word). */
 gdn_status gdn_linear_attn_get_device_status(void* workspace, void* stream, int* dev_status);

@@ -869,6 +869,12 @@ def gdn_q4_matvec(x, qweight, scales, zeros=None, bias=None, y=None, stream=None
     return y
 
 
+def _check_ints(what: str, *sizes) -> None:
+    """Sizes that the C interface takes as ints (ctypes would pass their low 32 bits)."""
+    if any(n >> 31 for n in sizes):
+        raise GDNError(GDN_ERR_UNSUPPORTED, what)
+
+
 def _linear_problem(q, k, v, g, cu_seqlens, fp32=(), others=()):
     """Checks of a linear attention's tensors and its problem.  fp32: (name, tensor, shape) that must be contiguous
     float32; others: (name, tensor) that must be like v and contiguous."""
@@ -881,7 +887,7 @@ def _linear_problem(q, k, v, g, cu_seqlens, fp32=(), others=()):
         if (k.shape == qshape and b == B and t == T and q.dtype is dtype and k.dtype is dtype and g.dtype is f32
                 and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous()
                 and q.get_device() == dev and k.get_device() == dev and g.get_device() == dev
-                and (g.shape == (B, T, Hv) or g.shape == (Hv,))):
+                and (g.shape == (B, T, Hv) or g.shape == (Hv,)) and not (B | T | Hqk | Hv | K | V) >> 31):
             for _, x, want in fp32:
                 if x is not None and (x.dtype is not f32 or x.get_device() != dev or x.shape != want
                                       or not x.is_contiguous()):
@@ -899,6 +905,7 @@ def _linear_problem_checked(q, k, v, g, cu_seqlens, fp32, others):
     _, _, Hv, V = vshape = v.shape
     if k.shape != qshape or vshape[0] != B or vshape[1] != T:
         raise ValueError("q and k must have one shape, and v their batch and tokens")
+    _check_ints("gdn_linear_attn", B, T, Hqk, K, Hv, V)
     for name, t in (("q", q), ("k", k), *others):
         if t.dtype is not dtype or t.get_device() != dev:
             raise ValueError(f"{name} must have the dtype and device of v")
@@ -916,9 +923,10 @@ def _linear_problem_checked(q, k, v, g, cu_seqlens, fp32, others):
     N = B
     if cu_seqlens is not None:
         if (cu_seqlens.dtype is not torch.int32 or cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous()
-                or cu_seqlens.dim() != 1):
+                or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1):
             raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor [N + 1]")
         N = cu_seqlens.numel() - 1
+        _check_ints("gdn_linear_attn", N)
     return LinearProblem(B, T, N, Hqk, Hv, K, V, DTYPES[dtype], int(cu_seqlens is not None), int(per_head),
                          _row_stride("q", q, Hqk * K), _row_stride("k", k, Hqk * K), _row_stride("v", v, Hv * V))
 
@@ -1081,7 +1089,10 @@ def _gated_norm(x, z, weight, others=()):
             and weight.is_contiguous()
             and (z is None or (z.shape == shape and z.dtype is dtype and z.get_device() == dev and z.is_contiguous()))):
         H, V = shape[-2:]   # the usual call
-        return x.numel() // (H * V) if H * V else 0, H, V, 0, 0, DTYPES[dtype], dev
+        rows = x.numel() // (H * V) if H * V else 0
+        if (rows | H | V) >> 31:
+            _check_ints("gdn_gated_norm", rows, H, V)
+        return rows, H, V, 0, 0, DTYPES[dtype], dev
     if dtype not in DTYPES or dev < 0 or x.dim() < 2:
         raise ValueError("x must be a float32 or bfloat16 CUDA tensor [..., H, V]")
     H, V = x.shape[-2:]
@@ -1089,6 +1100,7 @@ def _gated_norm(x, z, weight, others=()):
         raise ValueError("z must have the shape, dtype and device of x")
     _check_like(dev, ("weight", weight, torch.float32, (V,)), *others)
     rows, ld_x = _norm_rows("x", x, 2, H * V)
+    _check_ints("gdn_gated_norm", rows, H, V)
     return rows, H, V, ld_x, _norm_rows("z", z, 2, H * V)[1] if z is not None else 0, DTYPES[dtype], dev
 
 
@@ -1159,7 +1171,10 @@ def _residual_norm(y, residual, post_weight, gate, weight, others):
                 break
         else:   # the usual call
             if kind < 2 or (gate.get_device() == dev and gate.is_contiguous()):
-                return y.numel() // D if D else 0, D, 0, kind, DTYPES[dtype], DTYPES[residual.dtype], dev
+                rows = y.numel() // D if D else 0
+                if (rows | D) >> 31:
+                    _check_ints("gdn_residual_norm", rows, D)
+                return rows, D, 0, kind, DTYPES[dtype], DTYPES[residual.dtype], dev
     if residual.dtype not in (dtype, torch.float32):
         raise ValueError("residual must have the dtype of y, or float32")
     kind = 0 if gate is None else 2 if gate.shape == shape and gate.dtype is dtype else 1
@@ -1167,6 +1182,7 @@ def _residual_norm(y, residual, post_weight, gate, weight, others):
                 ("gate", gate, *((f32, (D,)) if kind < 2 else (dtype, shape))), ("weight", weight, f32, (D,)),
                 *others)
     rows, ld = _norm_rows("y", y, 1, D)
+    _check_ints("gdn_residual_norm", rows, D)
     return rows, D, ld, kind, DTYPES[dtype], DTYPES[residual.dtype], dev
 
 

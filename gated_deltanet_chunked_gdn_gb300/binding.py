@@ -1084,6 +1084,8 @@ def _check_like(dev, *tensors):
 
 def _gated_norm(x, z, weight, others=()):
     dtype, dev, shape = x.dtype, x.get_device(), x.shape
+    if weight is None:
+        raise ValueError("weight must be a contiguous float32 tensor [V] (z alone may be None)")
     if (not others and dtype in DTYPES and dev >= 0 and len(shape) >= 2 and x.is_contiguous()
             and weight.dtype is torch.float32 and weight.shape == shape[-1:] and weight.get_device() == dev
             and weight.is_contiguous()
@@ -1132,6 +1134,8 @@ def gdn_gated_norm_bwd(x, z, weight, rstd, dy, workspace=None, stream=None) -> d
     z), dweight (fp32) and the workspace under "workspace"."""
     lib = _lib or load()
     _check_ws(workspace, x)
+    if rstd is None or dy is None:
+        raise ValueError("rstd, which the forward saves with save_rstd, and dy are needed")
     rows, H, V, ld_x, ld_z, dt, dev = _gated_norm(x, z, weight, (("dy", dy, x.dtype, x.shape),
                                                                  ("rstd", rstd, torch.float32, x.shape[:-1])))
     given = workspace
@@ -1226,6 +1230,8 @@ def gdn_residual_norm_bwd(y, residual, rstd, dh, dn=None, post_weight=None, gate
     lib = _lib or load()
     if workspace is not None and workspace.device != y.device:
         raise ValueError("workspace must be on the device of y")
+    if rstd is None:
+        raise ValueError("rstd, which the forward saves with save_rstd, is needed")
     rows, D, ld, kind, dt, rdt, dev = _residual_norm(
         y, residual, post_weight, gate, weight,
         (("rstd", rstd, torch.float32, (*y.shape[:-1], 2)), ("dh", dh, residual.dtype, y.shape),

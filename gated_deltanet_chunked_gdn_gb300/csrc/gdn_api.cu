@@ -572,7 +572,10 @@ gdn_status gdn_linear_attn_get_device_status(void* workspace, void* stream, int*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return GDN_ERR_CUDA;
   if (cudaMemcpy(&host, workspace, sizeof(host), cudaMemcpyDeviceToHost) != cudaSuccess) return GDN_ERR_CUDA;
-  if (cudaMemset(workspace, 0, sizeof(host)) != cudaSuccess) return GDN_ERR_CUDA;
+  // on the call's stream and waited for: cudaMemset may still be under way on the default stream, which non-blocking
+  // streams do not wait for, when the next call has left its word
+  if (cudaMemsetAsync(workspace, 0, sizeof(host), s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return GDN_ERR_CUDA;
   *dev_status = host;
   return GDN_OK;
 }

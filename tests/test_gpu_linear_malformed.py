@@ -37,3 +37,20 @@ def test_gradients_stay_as_they_were(gdn, bad, dtype, K, V, Hqk, per_head):
     assert st == 0 and gdn.gdn_linear_attn_get_device_status(ws) == gdn.DEV_BAD_CU_SEQLENS
     for n, t in zip(("dq", "dk", "dv", "dg", "dh0"), out):
         assert bool((t == 3.0).all()), n
+
+
+def test_each_call_leaves_its_own_word(gdn):
+    """Good and bad calls in turn on a stream that does not wait for the default one."""
+    q = torch.randn(1, 100, 1, 64, device=DEV)
+    g = -torch.rand(1, 100, 1, device=DEV)
+    good, bad = (torch.tensor(c, dtype=torch.int32, device=DEV) for c in ([0, 50, 100], [0, 50, 99]))
+    p = gdn._linear_problem(q, q, q, g, good)
+    ws = torch.zeros(gdn.gdn_linear_attn_fwd_workspace_size(p), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(50):
+            for cu, want in ((bad, gdn.DEV_BAD_CU_SEQLENS), (good, gdn.DEV_OK), (bad, gdn.DEV_BAD_CU_SEQLENS)):
+                gdn.gdn_linear_attn_fwd(q, q, q, g, cu_seqlens=cu, workspace=ws)
+                assert gdn.gdn_linear_attn_get_device_status(ws) == want
+            assert gdn.gdn_linear_attn_get_device_status(ws) == gdn.DEV_OK

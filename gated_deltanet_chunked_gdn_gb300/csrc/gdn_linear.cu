@@ -120,7 +120,7 @@ namespace {
 
 // Along every sequence, in place: S_c (what chunk c adds) becomes the state before chunk c (rev: the adjoint of the
 // state behind it); four elements of a state a thread.  2 x 4096 tokens of 16 heads of 128 (64 chunks a sequence):
-// 55 us, 4.9 TB/s; with loads only after the sums before, 132.  blockIdx.y: the first or the second of two sums.
+// 48 us, 5.7 TB/s; with loads only after the sums before, 132.  blockIdx.y: the first or the second of two sums.
 __global__ void __launch_bounds__(256) sums_kernel(Shape d, Pieces pc, const Two* __restrict__ total, Sum first,
                                                    Sum second) {
   const Sum m = blockIdx.y ? second : first;
@@ -189,7 +189,7 @@ namespace {
 // sequence's tokens (COLS / 4 column groups of float4, the other threads' groups along K) and is read and written
 // once.  Bound by the state's traffic, 8 K V bytes a head; streaming hints, since a pool larger than L2 is touched
 // once a step.  512 sequences of 32 heads of 128 x 128: 314 us, 6.8 TB/s of their states (309 with the decay in one float);
-// one sequence: 2.5 us.
+// one sequence: 2.7 us.
 template <typename T, int K, int COLS>
 __global__ void __launch_bounds__(256) lin_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, int64_t ldq, int64_t ldk, int64_t ldv,
@@ -299,7 +299,7 @@ gdn_status step_t(const gdn_linear_problem& p, const void* q, const void* k, con
                   float scale, float* state, const int32_t* idx, int slots, const int32_t* cu, void* o,
                   cudaStream_t s) {
   // few heads: narrower slices, so that every SM has some (32 heads of 128, slices of 16 and of 64 columns: 1 sequence
-  // 2.57 and 2.70 us, 4 sequences 4.87 and 3.61)
+  // 2.57 and 2.70 us, 4 sequences 4.87 and 3.61, before the decay took two floats, which adds 0.1 to each)
   if (2 * (int64_t)p.N * p.Hv * (p.V / 64) < sm_count())
     return launch_step<T, 16>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, state, idx, slots, cu, (T*)o, s);
   return launch_step<T, 64>(p, (const T*)q, (const T*)k, (const T*)v, g, scale, state, idx, slots, cu, (T*)o, s);

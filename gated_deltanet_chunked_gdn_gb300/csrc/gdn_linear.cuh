@@ -62,9 +62,9 @@ struct Two {
 // with slow decays by nearly the same one for as long as its memory lasts, so that an error of the factor adds up.  Final
 // states of 100000 tokens with decays of -1e-4 against 64 bits: 5.6e-6 with ex2.approx, 2.1e-6 with expf, 2.3e-7 with
 // this; 20000 single steps with -1e-5: 5.1e-4 with expf, 2.5e-6.
-// x = n ln 2 + r with n ln 2 in two parts, the first of 15 bits, so that its multiples are exact; e^r = 1 + r + r^2 / 2 +
-// ... + r^8 / 8! for |r| <= ln 2 / 2, where the rest, below 2e-10, meets factors that are forgotten after a few chunks, as
-// r's own rounding does; for small r all of it is exact to 2^-24 r^2.
+// x = n ln 2 + r with n ln 2 in two parts (Cody and Waite's reduction), the first of 15 bits, so that its multiples are
+// exact; e^r = 1 + r + r^2 / 2 + ... + r^8 / 8! for |r| <= ln 2 / 2, where the rest, below 2e-10, meets factors that are
+// forgotten after a few chunks, as r's own rounding does; for small r all of it is exact to 2^-24 r^2.
 __device__ __forceinline__ Two exp_two(Two x) {
   if (x.h < -150.f) return {0.f, 0.f};   // below fp32, above it (NaN goes on)
   if (x.h > 89.f) return {__int_as_float(0x7f800000), 0.f};

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g
 
 // The walk over a segment's chunks.  ADJ: backwards, x = q, y = do, weights scale e^{b_i}: the adjoint of the state.
 // 32 heads of 128: with outputs (kFull), 314 us for 4 x 8192 tokens and 86 for 8192 (3.4 TB/s of q, k, v and o); the
-// segments' own (kOwn) before it 122 and 39; states for the backward pass (kEmit), 137 us for 4 x 4096 tokens (5.9 TB/s,
+// segments' own (kOwn) before it 122 and 37; states for the backward pass (kEmit), 138 us for 4 x 4096 tokens (5.8 TB/s,
 // 537 MB of them written: rows of S^T a lane took 152).  All but the last are bound by the chain of a chunk's phases:
 // tensor pipe 28 to 33 %, HBM 30 %, the schedulers issue a third of the time with two CTAs an SM.  A third CTA has no
 // room.

@@ -13,7 +13,9 @@
 // fp32 columns of its own (registers or shared memory), and a second launch adds the CTAs' columns in a fixed order.
 // Measured, of the bytes that have to move: gated norm, 16384 x 32 rows of 128 in bf16: forward 71 us (5.7 TB/s),
 // backward 115 (5.8); residual norm, 8192 x 4096 in bf16: forward 57 us (4.7); 4099 x 2500 in fp32 with a gate of its own
-// for each element: forward 37 us (5.5), backward 99 (3.3).
+// for each element: forward 37 us (5.5), backward 100 (3.3).  Wide rows' backwards hold more than a thread's registers:
+// residual norm above 4096 bf16 elements (4096 x 8192 214 us, 1.9 TB/s; 2048 x 16384 473, 0.9), gated norm above 8192
+// (2048 x 16384 in bf16 618 us, 0.5 TB/s, in fp32 398, 1.7; 4096 x 8192 in bf16 87, 3.9).
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -389,9 +391,11 @@ __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512, NV * VEC <= 8 ? (
 // Column sums of dweight, dpost_weight and dgate: in registers for rows of up to 8 elements a thread, else in shared
 // memory ([RPB][3][D]; a thread adds to columns that no other thread of its row touches).  Where registers are left, the
 // next row's loads are in flight.  The furthest of these kernels from the bytes' time: registers for one CTA an SM, whose
-// 16 warps issue a third of the time (790 instructions a row and warp of 4096 fp32, and two sums over the CTA).  Slower
-// were, for 8192 x 4096 in bf16 (123 us), fewer threads a row (206), 64 registers and two CTAs (326, spills), the next
-// three rows in a ring in shared memory (135); for 4099 x 2500 in fp32 (99), that ring (105) and twice the threads (116).
+// 16 warps issue a third to half of the time (790 instructions a row and warp of 4096 fp32, and two sums over the CTA).
+// Some of those registers and instructions go to sums for weights and gates that a call does not have: the kinds are not
+// known where this is compiled, so all three are formed, and the second launch drops what nobody asked for.  Slower were,
+// for 8192 x 4096 in bf16 (122 us), fewer threads a row (206), 64 registers and two CTAs (326, spills), the next three
+// rows in a ring in shared memory (135); for 4099 x 2500 in fp32 (100), that ring (105) and twice the threads (116).
 template <typename T, typename R, int VEC, int NV, int GROUP>
 __global__ void __launch_bounds__(GROUP ? kGroupThreads : 512) residual_bwd_kernel(
     const T* __restrict__ y, int64_t ldy, const R* __restrict__ res, const float* __restrict__ rstd,

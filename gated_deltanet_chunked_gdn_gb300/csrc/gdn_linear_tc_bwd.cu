@@ -6,9 +6,9 @@
 // terms each, all of their 24 bits: dg, an fp32 output, is a sum over products with them (with two terms it was off by
 // up to 1.2e-5 in sequences without decay).  Persistent CTAs, one an SM (the chunk's tiles, S0 and G fill its shared
 // memory), take chunks in turn; the next chunk's S0 comes in while this one's gradients are formed, its tiles and G are
-// prefetched to L2.  4 x 4096 tokens of 32 heads of 128: 610 us (3.3 TB/s of S0, G, the inputs and the gradients; 570
-// with W and P in one term, at which HBM 39 %, tensor pipe 25 %, and a chunk 20k cycles, 5k of products, 5k of their
-// operands' shared-memory reads, 2.5k of splitting S0 and G, and barriers between).  Tiles released earlier (561 against
+// prefetched to L2.  4 x 4096 tokens of 32 heads of 128: 610 us (3.3 TB/s of S0, G, the inputs and the gradients; HBM
+// 36 %, tensor pipe 26 %; 570 with W and P in one term): a chunk takes 20k cycles and more, 5k of products, 5k of their
+// operands' shared-memory reads, 2.5k of splitting S0 and G, and barriers between.  Tiles released earlier (561 against
 // 570) or a warp that only issues (678, registers) did not help.
 // TMEM lane = token: rows 0..63 of every stacked product are keys' rows, 64..127 queries'.
 //

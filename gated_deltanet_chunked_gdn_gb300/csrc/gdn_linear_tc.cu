@@ -99,12 +99,12 @@ __device__ __forceinline__ Two log2_units(Two a) {
 }
 
 // Decays of every chunk and head: log2(e) b_i, e^{b_last - b_j} (0 past the end), scale e^{b_i}, e^{b_last} in two floats
-// and what the first lacks to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a strong decay, and
-// differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads take 28 us, as
-// they are 8).  o's weights take the first 24 bits: behind 64 tokens at the cut the difference of two sums is off by 2^-11,
-// behind one by 2^-17, under the 2^-8 of o's own rounding.  A warp takes a chunk and head at a time.  (Within the
-// kernels below it was one warp's work for 2000 cycles a chunk, while the others waited.)  4 MB read, 17 MB written: the
-// 8 us are latency.
+// and what the first lacks to 48 bits; the sums in pairs of floats (so that e^{b_last - b_j} keeps fp32 accuracy behind a
+// strong decay, and differences of the sums do; with sums in double, fp64 being scarce here, 4 x 8192 tokens of 32 heads
+// take 28 us, as they are 8).  o's weights take the first 24 bits: behind 64 tokens at the cut the difference of two sums
+// is off by 2^-11, behind one by 2^-17, under the 2^-8 of o's own rounding.  A warp takes a chunk and head at a time.
+// (Within the kernels below it was one warp's work for 2000 cycles a chunk, while the others waited.)  4 MB read, 17 MB
+// written: the 8 us are latency.
 __global__ void __launch_bounds__(256) decays_kernel(const float* __restrict__ g, int g_per_head, int Hv, Pieces pc,
                                                      float scale, float* __restrict__ out) {
   const Piece p = piece_of(pc, blockIdx.x);
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kTcThreads, (Map<KD, VD, MODE == kFull>::Ctas)
   constexpr bool TWO = !FULL;
   auto buffer = [&](int i) { return TWO ? i & 1 : 0; };
   auto k_tile = [&](int i) { return M::KQ + 8192u * buffer(i); };   // the second in the place of Q
-  auto v_tile = [&](int i) { return buffer(i) ? M::X : M::V; };     // the second in the place of V'''s first term
+  auto v_tile = [&](int i) { return buffer(i) ? M::X : M::V; };     // the second in the place of the first term of V''
   auto load_bar = [&](int which, int i) { return bars + which + 2 * buffer(i); };
   auto load_no = [&](int i) { return TWO ? i >> 1 : i; };
   auto decays_of = [&](int i) { return reinterpret_cast<const float*>(sm + M::Gam + M::kGam * buffer(i)); };
